@@ -10,6 +10,8 @@
  *   gradlev_decode_step                   deployment: token-by-token forward, costate, update
  *   gradlev_consistency_step              a training step from predicted costates
  *   gradlev_mlp2_recon                    the two-layer reconstruction of the synthetic test
+ *   gradlev_delta_fwd / _bwd / _step      the gated delta rule: chunked, its gradients, by token
+ *   gradlev_qk_norm_rope_fwd / _bwd       norms and rotation of queries and keys, per head
  *   gradlev_scan_bwd_noalloc              the reverse scan without a workspace argument
  *   gradlev_scan_bwd_noalloc_scratch_bytes  its scratch need
  *   gradlev_noalloc_device_status         its device status word
@@ -304,6 +306,140 @@ GRADLEV_API gradlev_status gradlev_mlp2_recon(int B, int H, int T, int d_x, int 
                                   int control, void* a, void* h, void* y, void* g2til,
                                   void* g1til, float* dW1, void* workspace, size_t ws_bytes,
                                   void* stream);
+
+/* The gated delta rule: a state that learns to return v_t for k_t.
+ *
+ * The scans above take the costates g_t as given. With the inner loss
+ * 0.5 ||S k_t - v_t||^2 the learner's own costate is known in closed form,
+ * S' k_t - v_t, and the serial learner becomes the gated delta rule. Per batch row b
+ * and value head h, with the key head h / (H / Hk), a_t = exp(log_alpha_t) and the
+ * state S [d_v, d_k]:
+ *
+ *     S'  = a_t S_{t-1}
+ *     S_t = S' + beta_t (v_t - S' k_t) k_t^T
+ *     y_t = scale S_t q_t
+ *
+ * The step is not affine in a scalar decay alone (it also projects along k_t), so the
+ * scans' segments do not apply; the chunked form solves a triangular system per chunk.
+ *
+ * Layouts: contiguous, row-major, device memory.
+ *     q, k, dq, dk           [B, Hk, T, d_k]   dtype
+ *     v, y, dy, dv           [B, H, T, d_v]    dtype
+ *     beta, log_alpha        [B, H, T]         float32 (all dtypes)
+ *     S0, ST (states)        [B, H, d_v, d_k]  float32 (all dtypes)
+ *     dbeta, dlog_alpha      [B, H, T]         dtype
+ *     dST, dS0               [B, H, d_v, d_k]  dtype
+ * Every gradient has the I/O dtype: the bf16 path forms gradients from bf16 operands.
+ * H must be a multiple of Hk; dq and dk add up over the value heads of a key head.
+ *
+ * log_alpha <= 0. log_alpha = -inf starts a new sequence at that token (the state
+ * before it has no influence, dlog_alpha = 0 there); a value below -87, whose
+ * exponential underflows float32, counts as -inf. beta_t = 0 leaves the state to its
+ * decay alone (padding), and dbeta is exact there too. Keys are expected with
+ * beta_t |k_t|^2 < 2, where the rule contracts (gradlev_qk_norm_rope_fwd with
+ * GRADLEV_NORM_L2 gives |k_t| = 1); beyond it states grow as the formula says. */
+
+/* Whether the shape is supported by gradlev_delta_fwd / _bwd: GRADLEV_OK, or
+ * GRADLEV_ERR_INVALID_ARG / GRADLEV_ERR_UNSUPPORTED without touching the GPU.
+ * Supported: H % Hk == 0, d_k and d_v multiples of 8 up to 256, B*H*T < 2^31 and
+ * B*H < 2^27. */
+GRADLEV_API gradlev_status gradlev_delta_supported(int B, int H, int Hk, int T, int d_k, int d_v,
+                                       gradlev_dtype dt);
+
+/* Bytes of device workspace of the forward (is_bwd = 0) or backward (is_bwd = 1)
+ * call; 0 if unsupported. Scratch: its contents on entry do not matter. Its first 16
+ * bytes hold the device status word on return (gradlev_device_status). Two calls
+ * that may overlap on the GPU need a workspace each. */
+GRADLEV_API size_t gradlev_delta_workspace_bytes(int B, int H, int Hk, int T, int d_k, int d_v,
+                                     gradlev_dtype dt, int is_bwd);
+
+/* Bytes of the optional checkpoint buffer that gradlev_delta_fwd fills and
+ * gradlev_delta_bwd of the same inputs consumes (chunk-start states, per-token errors
+ * and the chunks' triangular systems); 0 if unsupported. Contents
+ * implementation-defined. */
+GRADLEV_API size_t gradlev_delta_ckpt_bytes(int B, int H, int Hk, int T, int d_k, int d_v,
+                                gradlev_dtype dt);
+
+/* Chunked forward.
+ *   S0: NULL (zero), or the state before the first token, read only.
+ *   ST: NULL (not written), or the state after the last token. May not alias S0.
+ *   ckpt: NULL, or gradlev_delta_ckpt_bytes() bytes for a later gradlev_delta_bwd.
+ *   Alignment, else GRADLEV_ERR_INVALID_ARG: tensors with a d_k or d_v axis 16 bytes,
+ *   the [B,H,T] gates and their gradients 4 bytes, workspace and ckpt 256 bytes. Outputs may not alias inputs. */
+GRADLEV_API gradlev_status gradlev_delta_fwd(int B, int H, int Hk, int T, int d_k, int d_v,
+                                 gradlev_dtype dt, const void* q, const void* k, const void* v,
+                                 const float* beta, const float* log_alpha, float scale,
+                                 const float* S0, void* y, float* ST, void* ckpt, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+/* The gradients of L = sum_t <dy_t, y_t> + <dST, S_T>_F.
+ *   S0: as in the forward; read only when ckpt is NULL (the call then recomputes the
+ *       states from it).
+ *   dST: NULL (zero), or the gradient of the last state. When the sequence goes on in
+ *       a later part, it is the dS0 of that part's call.
+ *   dS0: NULL (not written), or the gradient of S0.
+ *   ckpt: NULL, or the buffer that gradlev_delta_fwd filled on the same inputs.
+ *   Alignment and aliasing as in the forward. No atomics: the same inputs give the
+ *   same bits. */
+GRADLEV_API gradlev_status gradlev_delta_bwd(int B, int H, int Hk, int T, int d_k, int d_v,
+                                 gradlev_dtype dt, const void* q, const void* k, const void* v,
+                                 const float* beta, const float* log_alpha, float scale,
+                                 const float* S0, const void* dy, const void* dST, void* dq,
+                                 void* dk, void* dv, void* dbeta, void* dlog_alpha, void* dS0,
+                                 const void* ckpt, void* workspace, size_t ws_bytes, void* stream);
+
+/* The recurrent form for serving: T tokens in order (usually 1) on states that stay in a
+ * pool S [pool, H, d_v, d_k] float32, read and overwritten.
+ *   slots: NULL (row b of the batch has state b; pool >= B), or [B] int32 device: the
+ *       pool row of each batch row. A batch row whose slot lies outside [0, pool)
+ *       (-1: padding), or is also the slot of an earlier batch row, has no state: its
+ *       y is zero and no state is written for it. Pool rows that no slot names keep
+ *       their values.
+ *   Constraints: d_k a multiple of 4 up to 256, any d_v >= 1, H % Hk == 0
+ *   (GRADLEV_ERR_UNSUPPORTED). Alignment, else GRADLEV_ERR_INVALID_ARG: q and k to 4
+ *   elements, v and y to one element, S to 16 bytes. One launch; no workspace. */
+GRADLEV_API gradlev_status gradlev_delta_step(int B, int H, int Hk, int T, int d_k, int d_v,
+                                  gradlev_dtype dt, const void* q, const void* k, const void* v,
+                                  const float* beta, const float* log_alpha, float scale,
+                                  const int* slots, int pool, float* S, void* y, void* stream);
+
+/* Norms of queries and keys per head, with the rotation by position in the same pass:
+ * what stands in front of the delta rule.
+ *
+ * Per (b, t, head) row x [d]: r = 1 / sqrt(ss + eps) with ss the sum of squares
+ * (GRADLEV_NORM_L2) or its mean over d (GRADLEV_NORM_RMS), u = w r x, and for
+ * i < rot / 2 with the angle th = pos[b][t] * inv_freq[i]:
+ *   y_i = u_i cos th - u_{i + rot/2} sin th,  y_{i + rot/2} = u_{i + rot/2} cos th + u_i sin th,
+ * and y_i = u_i for i >= rot. Angles are formed in double precision.
+ *   q, k: [B, T, H*, d] by strides in elements {b, t, head}, the columns contiguous, so
+ *     that a packed projection needs no copy. Strides are multiples of 16 bytes and not
+ *     negative, bases 16-byte aligned, else GRADLEV_ERR_INVALID_ARG.
+ *   yq [B,Hq,T,d], yk [B,Hk,T,d]: contiguous, the layout of gradlev_delta_fwd.
+ *   wq, wk: [d] float32, or NULL (1). pos: [B,T] int32, or NULL (t). inv_freq:
+ *     [rot / 2] float32 (NULL when rot = 0).
+ *   Constraints: d a multiple of 8 up to 256, rot a multiple of 16 up to d
+ *   (GRADLEV_ERR_UNSUPPORTED). A row of zeros with eps = 0 gives NaN, as the formula. */
+typedef enum { GRADLEV_NORM_L2 = 0, GRADLEV_NORM_RMS = 1 } gradlev_norm;
+
+GRADLEV_API gradlev_status gradlev_qk_norm_rope_fwd(
+    int B, int T, int Hq, int Hk, int d, int rot, gradlev_dtype dt, int norm, float eps,
+    const void* q, const long long* q_strides, const void* k, const long long* k_strides,
+    const float* wq, const float* wk, const int* pos, const float* inv_freq, void* yq, void* yk,
+    void* stream);
+
+/* Its gradients: dq and dk (by strides, like q and k; elements between the rows are not
+ * written) and dwq, dwk [d] float32, each present exactly when its weight is. Sums over
+ * rows run in a fixed order. workspace: gradlev_qk_norm_rope_workspace_bytes() bytes,
+ * 256-byte aligned; NULL when neither weight is given. dq and dk may be q and k. */
+GRADLEV_API size_t gradlev_qk_norm_rope_workspace_bytes(int B, int T, int Hq, int Hk, int d,
+                                            gradlev_dtype dt);
+GRADLEV_API gradlev_status gradlev_qk_norm_rope_bwd(
+    int B, int T, int Hq, int Hk, int d, int rot, gradlev_dtype dt, int norm, float eps,
+    const void* dyq, const void* dyk, const void* q, const long long* q_strides, const void* k,
+    const long long* k_strides, const float* wq, const float* wk, const int* pos,
+    const float* inv_freq, void* dq, const long long* dq_strides, void* dk,
+    const long long* dk_strides, float* dwq, float* dwk, void* workspace, size_t ws_bytes,
+    void* stream);
 
 /* Size of the static scratch array gradlev_scan_bwd_noalloc uses: 64 MiB,
  * held by every GPU that loads the library until the process exits. */

@@ -18,7 +18,11 @@ __all__ = [
     "gradlev_scan_workspace_bytes", "gradlev_scan_ckpt_bytes", "gradlev_scan_fwd",
     "gradlev_scan_bwd", "gradlev_scan_fwd_state", "gradlev_scan_bwd_state",
     "gradlev_decode_step", "gradlev_consistency_workspace_bytes", "gradlev_consistency_step",
-    "gradlev_mlp2_workspace_bytes", "gradlev_mlp2_recon", "gradlev_device_status", "gradlev_last_launch_count", "F32", "BF16", "LIB_PATH",
+    "gradlev_mlp2_workspace_bytes", "gradlev_mlp2_recon", "gradlev_delta_supported",
+    "gradlev_delta_workspace_bytes", "gradlev_delta_ckpt_bytes", "gradlev_delta_fwd",
+    "gradlev_delta_bwd", "gradlev_delta_step", "gradlev_qk_norm_rope_workspace_bytes",
+    "gradlev_qk_norm_rope_fwd", "gradlev_qk_norm_rope_bwd", "gradlev_device_status",
+    "gradlev_last_launch_count", "F32", "BF16", "LIB_PATH",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgradlev.so")
@@ -30,7 +34,10 @@ _ENTRY_POINTS = (
     "gradlev_scan_ckpt_bytes", "gradlev_scan_fwd", "gradlev_scan_bwd",
     "gradlev_scan_fwd_state", "gradlev_scan_bwd_state", "gradlev_decode_step",
     "gradlev_consistency_workspace_bytes", "gradlev_consistency_step",
-    "gradlev_mlp2_workspace_bytes", "gradlev_mlp2_recon", "gradlev_device_status",
+    "gradlev_mlp2_workspace_bytes", "gradlev_mlp2_recon", "gradlev_delta_supported",
+    "gradlev_delta_workspace_bytes", "gradlev_delta_ckpt_bytes", "gradlev_delta_fwd",
+    "gradlev_delta_bwd", "gradlev_delta_step", "gradlev_qk_norm_rope_workspace_bytes",
+    "gradlev_qk_norm_rope_fwd", "gradlev_qk_norm_rope_bwd", "gradlev_device_status",
     "gradlev_last_launch_count",
 )
 
@@ -86,6 +93,26 @@ def lib():
     L.gradlev_mlp2_workspace_bytes.restype = Z
     L.gradlev_mlp2_recon.argtypes = [I] * 7 + [P] * 8 + [I] + [P] * 7 + [Z, P]
     L.gradlev_mlp2_recon.restype = I
+    F, LL = ctypes.c_float, ctypes.POINTER(ctypes.c_longlong)
+    L.gradlev_delta_supported.argtypes = [I] * 7
+    L.gradlev_delta_supported.restype = I
+    L.gradlev_delta_workspace_bytes.argtypes = [I] * 8
+    L.gradlev_delta_workspace_bytes.restype = Z
+    L.gradlev_delta_ckpt_bytes.argtypes = [I] * 7
+    L.gradlev_delta_ckpt_bytes.restype = Z
+    L.gradlev_delta_fwd.argtypes = [I] * 7 + [P] * 5 + [F] + [P] * 5 + [Z, P]
+    L.gradlev_delta_fwd.restype = I
+    L.gradlev_delta_bwd.argtypes = [I] * 7 + [P] * 5 + [F] + [P] * 11 + [Z, P]
+    L.gradlev_delta_bwd.restype = I
+    L.gradlev_delta_step.argtypes = [I] * 7 + [P] * 5 + [F, P, I] + [P] * 3
+    L.gradlev_delta_step.restype = I
+    L.gradlev_qk_norm_rope_workspace_bytes.argtypes = [I] * 6
+    L.gradlev_qk_norm_rope_workspace_bytes.restype = Z
+    L.gradlev_qk_norm_rope_fwd.argtypes = [I] * 8 + [F, P, LL, P, LL] + [P] * 7
+    L.gradlev_qk_norm_rope_fwd.restype = I
+    L.gradlev_qk_norm_rope_bwd.argtypes = ([I] * 8 + [F, P, P, P, LL, P, LL] + [P] * 4 +
+                                           [P, LL, P, LL] + [P] * 3 + [Z, P])
+    L.gradlev_qk_norm_rope_bwd.restype = I
     L.gradlev_device_status.argtypes = [P, P]
     L.gradlev_device_status.restype = I
     L.gradlev_last_launch_count.argtypes = []
@@ -479,6 +506,231 @@ def gradlev_mlp2_recon(x, g1hat, g2hat, v, eta, alpha, W1, W2, control=False, *,
             _ptr(out["y"]), _ptr(out["g2til"]), _ptr(out["g1til"]), _ptr(out["dW1"]), _ptr(ws),
             ws.numel() * ws.element_size(), _stream_ptr(stream, dev))
     _check(st, "gradlev_mlp2_recon")
+    return out
+
+
+def gradlev_delta_supported(B, H, Hk, T, d_k, d_v, dt) -> int:
+    return int(lib().gradlev_delta_supported(B, H, Hk, T, d_k, d_v, dt))
+
+
+def gradlev_delta_workspace_bytes(B, H, Hk, T, d_k, d_v, dt, is_bwd) -> int:
+    return int(lib().gradlev_delta_workspace_bytes(B, H, Hk, T, d_k, d_v, dt, int(is_bwd)))
+
+
+def gradlev_delta_ckpt_bytes(B, H, Hk, T, d_k, d_v, dt) -> int:
+    return int(lib().gradlev_delta_ckpt_bytes(B, H, Hk, T, d_k, d_v, dt))
+
+
+def _delta_args(q, k, v, beta, log_alpha, scale):
+    """Checks shared by the delta calls. Returns the sizes, the dtype code and the scale."""
+    import torch
+    if q.dim() != 4 or v.dim() != 4:
+        raise GradlevError("q and v must be [B,H,T,d] tensors")
+    B, Hk, T, d_k = q.shape
+    H, d_v = v.shape[1], v.shape[3]
+    dev, dt = _cuda_device(q), q.dtype
+    code = _dt_code(dt)
+    _check_tensor("q", q, (B, Hk, T, d_k), dt, dev)
+    _check_tensor("k", k, (B, Hk, T, d_k), dt, dev)
+    _check_tensor("v", v, (B, H, T, d_v), dt, dev)
+    _check_tensor("beta", beta, (B, H, T), torch.float32, dev)
+    _check_tensor("log_alpha", log_alpha, (B, H, T), torch.float32, dev)
+    return (B, H, Hk, T, d_k, d_v, code), dev, dt, float(d_k ** -0.5 if scale is None else scale)
+
+
+def gradlev_delta_fwd(q, k, v, beta, log_alpha, S0=None, *, scale=None, y=None, ST=None,
+                      want_ST=True, ckpt=None, workspace=None, stream=None):
+    """Chunked gated delta rule (see include/gradlev.h): q, k [B,Hk,T,d_k], v [B,H,T,d_v],
+    beta and log_alpha [B,H,T] float32, S0 [B,H,d_v,d_k] float32 or None (zero). scale None:
+    d_k ** -0.5. Returns (y, ST), ST the float32 state after the last token (None when
+    want_ST is False and no buffer is given)."""
+    import torch
+    size, dev, dt, scale = _delta_args(q, k, v, beta, log_alpha, scale)
+    B, H, _, T, d_k, d_v, _ = size
+    f32 = torch.float32
+    _check(gradlev_delta_supported(*size), "gradlev_delta_fwd")
+    if S0 is not None:
+        _check_tensor("S0", S0, (B, H, d_v, d_k), f32, dev)
+    if y is None:
+        y = torch.empty((B, H, T, d_v), dtype=dt, device=dev)
+    _check_tensor("y", y, (B, H, T, d_v), dt, dev)
+    if ST is None and want_ST:
+        ST = torch.empty((B, H, d_v, d_k), dtype=f32, device=dev)
+    if ST is not None:
+        _check_tensor("ST", ST, (B, H, d_v, d_k), f32, dev)
+    if ckpt is not None:
+        _check_buffer("ckpt", ckpt, gradlev_delta_ckpt_bytes(*size), dev)
+    ws = _workspace(gradlev_delta_workspace_bytes(*size, 0), dev, workspace)
+    with torch.cuda.device(dev):  # launches go to the tensors' device
+        st = lib().gradlev_delta_fwd(*size, _ptr(q), _ptr(k), _ptr(v), _ptr(beta),
+                                     _ptr(log_alpha), scale, _ptr(S0), _ptr(y), _ptr(ST),
+                                     _ptr(ckpt), _ptr(ws), ws.numel() * ws.element_size(),
+                                     _stream_ptr(stream, dev))
+    _check(st, "gradlev_delta_fwd")
+    return y, ST
+
+
+def gradlev_delta_bwd(q, k, v, beta, log_alpha, dy, S0=None, dST=None, *, scale=None, ckpt=None,
+                      want_dS0=True, workspace=None, stream=None, out=None):
+    """Gradients of the gated delta rule, all in the I/O dtype: dict dq, dk, dv, dbeta,
+    dlog_alpha and dS0 (None when want_dS0 is False). dST [B,H,d_v,d_k] (I/O dtype, None = 0)
+    is the gradient of the last state; ckpt the buffer a forward call on the same inputs
+    filled (None: the states are recomputed from S0)."""
+    import torch
+    size, dev, dt, scale = _delta_args(q, k, v, beta, log_alpha, scale)
+    B, H, _, T, d_k, d_v, _ = size
+    _check(gradlev_delta_supported(*size), "gradlev_delta_bwd")
+    _check_tensor("dy", dy, (B, H, T, d_v), dt, dev)
+    if S0 is not None:
+        _check_tensor("S0", S0, (B, H, d_v, d_k), torch.float32, dev)
+    if dST is not None:
+        _check_tensor("dST", dST, (B, H, d_v, d_k), dt, dev)
+    if out is None:
+        out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+                   dbeta=torch.empty((B, H, T), dtype=dt, device=dev),
+                   dlog_alpha=torch.empty((B, H, T), dtype=dt, device=dev),
+                   dS0=torch.empty((B, H, d_v, d_k), dtype=dt, device=dev) if want_dS0 else None)
+    _check_out(out, dict(dq=(q.shape, dt), dk=(k.shape, dt), dv=(v.shape, dt),
+                         dbeta=((B, H, T), dt), dlog_alpha=((B, H, T), dt)), dev)
+    if out.get("dS0") is not None:
+        _check_tensor("out['dS0']", out["dS0"], (B, H, d_v, d_k), dt, dev)
+    if ckpt is not None:
+        _check_buffer("ckpt", ckpt, gradlev_delta_ckpt_bytes(*size), dev)
+    ws = _workspace(gradlev_delta_workspace_bytes(*size, 1), dev, workspace)
+    with torch.cuda.device(dev):  # launches go to the tensors' device
+        st = lib().gradlev_delta_bwd(
+            *size, _ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(log_alpha), scale, _ptr(S0),
+            _ptr(dy), _ptr(dST), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
+            _ptr(out["dbeta"]), _ptr(out["dlog_alpha"]), _ptr(out.get("dS0")), _ptr(ckpt),
+            _ptr(ws), ws.numel() * ws.element_size(), _stream_ptr(stream, dev))
+    _check(st, "gradlev_delta_bwd")
+    return out
+
+
+def gradlev_delta_step(q, k, v, beta, log_alpha, S, *, slots=None, scale=None, y=None,
+                       stream=None):
+    """The T tokens of q, k, v in order on the states S [pool,H,d_v,d_k] float32, updated in
+    place. slots [B] int32 picks each batch row's state (None: row b); a row without a state
+    of its own (slot outside the pool, or named by an earlier row) answers with zeros.
+    Returns y [B,H,T,d_v]."""
+    import torch
+    size, dev, dt, scale = _delta_args(q, k, v, beta, log_alpha, scale)
+    B, H, _, T, d_k, d_v, _ = size
+    if S.dim() != 4:
+        raise GradlevError("S must be a [pool,H,d_v,d_k] tensor")
+    _check_tensor("S", S, (S.shape[0], H, d_v, d_k), torch.float32, dev)
+    if slots is not None:
+        _check_tensor("slots", slots, (B,), torch.int32, dev)
+    if y is None:
+        y = torch.empty((B, H, T, d_v), dtype=dt, device=dev)
+    _check_tensor("y", y, (B, H, T, d_v), dt, dev)
+    with torch.cuda.device(dev):  # launches go to the tensors' device
+        st = lib().gradlev_delta_step(*size, _ptr(q), _ptr(k), _ptr(v), _ptr(beta),
+                                      _ptr(log_alpha), scale, _ptr(slots), S.shape[0], _ptr(S),
+                                      _ptr(y), _stream_ptr(stream, dev))
+    _check(st, "gradlev_delta_step")
+    return y
+
+
+_NORMS = {"l2": 0, "rms": 1}
+
+
+def gradlev_qk_norm_rope_workspace_bytes(B, T, Hq, Hk, d, dt) -> int:
+    return int(lib().gradlev_qk_norm_rope_workspace_bytes(B, T, Hq, Hk, d, dt))
+
+
+def _strided(name, t, shape, dtype, device):
+    """A [B,T,H,d] tensor whose columns are contiguous; its other strides as a C array."""
+    if t.shape != tuple(shape):
+        raise GradlevError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if t.dtype != dtype:
+        raise GradlevError(f"{name}: dtype {t.dtype} != {dtype}")
+    if t.device != device:
+        raise GradlevError(f"{name}: device {t.device} != {device}")
+    if t.stride(3) != 1 and t.shape[3] != 1:
+        raise GradlevError(f"{name}: columns must be contiguous")
+    # the stride of an axis of length 1 is never used
+    return (ctypes.c_longlong * 3)(*[t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)])
+
+
+def _norm_args(q, k, wq, wk, pos, inv_freq, norm):
+    import torch
+    if q.dim() != 4 or k.dim() != 4:
+        raise GradlevError("q and k must be [B,T,H,d] tensors")
+    if norm not in _NORMS:
+        raise GradlevError(f"norm: {norm!r} is not one of {sorted(_NORMS)}")
+    B, T, Hq, d = q.shape
+    Hk = k.shape[2]
+    dev, dt = _cuda_device(q), q.dtype
+    sq = _strided("q", q, (B, T, Hq, d), dt, dev)
+    sk = _strided("k", k, (B, T, Hk, d), dt, dev)
+    for n, w in (("wq", wq), ("wk", wk)):
+        if w is not None:
+            _check_tensor(n, w, (d,), torch.float32, dev)
+    if pos is not None:
+        _check_tensor("pos", pos, (B, T), torch.int32, dev)
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _check_tensor("inv_freq", inv_freq, (rot // 2,), torch.float32, dev)
+    return (B, T, Hq, Hk, d, rot, _dt_code(dt), _NORMS[norm]), dev, dt, sq, sk
+
+
+def gradlev_qk_norm_rope_fwd(q, k, wq=None, wk=None, pos=None, inv_freq=None, *, norm="l2",
+                             eps=1e-6, yq=None, yk=None, stream=None):
+    """Norm per head and rotation by position of q [B,T,Hq,d] and k [B,T,Hk,d] (any strides
+    with contiguous columns, e.g. views of one packed projection). Returns (yq [B,Hq,T,d],
+    yk [B,Hk,T,d]), contiguous. norm "l2" or "rms"; wq, wk [d] float32 or None; pos [B,T]
+    int32 or None (t); inv_freq [rot/2] float32 or None (no rotation)."""
+    import torch
+    a, dev, dt, sq, sk = _norm_args(q, k, wq, wk, pos, inv_freq, norm)
+    B, T, Hq, Hk, d = a[:5]
+    if yq is None:
+        yq = torch.empty((B, Hq, T, d), dtype=dt, device=dev)
+    if yk is None:
+        yk = torch.empty((B, Hk, T, d), dtype=dt, device=dev)
+    _check_tensor("yq", yq, (B, Hq, T, d), dt, dev)
+    _check_tensor("yk", yk, (B, Hk, T, d), dt, dev)
+    with torch.cuda.device(dev):  # launches go to the tensors' device
+        st = lib().gradlev_qk_norm_rope_fwd(*a, float(eps), _ptr(q), sq, _ptr(k), sk, _ptr(wq),
+                                            _ptr(wk), _ptr(pos), _ptr(inv_freq), _ptr(yq),
+                                            _ptr(yk), _stream_ptr(stream, dev))
+    _check(st, "gradlev_qk_norm_rope_fwd")
+    return yq, yk
+
+
+def gradlev_qk_norm_rope_bwd(dyq, dyk, q, k, wq=None, wk=None, pos=None, inv_freq=None, *,
+                             norm="l2", eps=1e-6, workspace=None, stream=None, out=None):
+    """Gradients of gradlev_qk_norm_rope_fwd from dyq [B,Hq,T,d] and dyk [B,Hk,T,d]. Returns
+    dict dq, dk (shaped like q and k; strided when given in `out`) and dwq, dwk for the
+    weights that are given."""
+    import torch
+    a, dev, dt, sq, sk = _norm_args(q, k, wq, wk, pos, inv_freq, norm)
+    B, T, Hq, Hk, d = a[:5]
+    _check_tensor("dyq", dyq, (B, Hq, T, d), dt, dev)
+    _check_tensor("dyk", dyk, (B, Hk, T, d), dt, dev)
+    f32 = torch.float32
+    if out is None:
+        out = dict(dq=torch.empty((B, T, Hq, d), dtype=dt, device=dev),
+                   dk=torch.empty((B, T, Hk, d), dtype=dt, device=dev))
+        for n, w in (("dwq", wq), ("dwk", wk)):
+            if w is not None:
+                out[n] = torch.empty((d,), dtype=f32, device=dev)
+    if out.get("dq") is None or out.get("dk") is None:
+        raise GradlevError("out needs 'dq' and 'dk'")
+    sdq = _strided("out['dq']", out["dq"], (B, T, Hq, d), dt, dev)
+    sdk = _strided("out['dk']", out["dk"], (B, T, Hk, d), dt, dev)
+    _check_out(out, {n: ((d,), f32) for n, w in (("dwq", wq), ("dwk", wk)) if w is not None}, dev)
+    nws = gradlev_qk_norm_rope_workspace_bytes(B, T, Hq, Hk, d, a[6])
+    ws = _workspace(nws, dev, workspace) if wq is not None or wk is not None else None
+    with torch.cuda.device(dev):  # launches go to the tensors' device
+        st = lib().gradlev_qk_norm_rope_bwd(
+            *a, float(eps), _ptr(dyq), _ptr(dyk), _ptr(q), sq, _ptr(k), sk, _ptr(wq), _ptr(wk),
+            _ptr(pos), _ptr(inv_freq), _ptr(out["dq"]), sdq, _ptr(out["dk"]), sdk,
+            _ptr(out["dwq"] if wq is not None else None),
+            _ptr(out["dwk"] if wk is not None else None), _ptr(ws),
+            ws.numel() * ws.element_size() if ws is not None else 0, _stream_ptr(stream, dev))
+    _check(st, "gradlev_qk_norm_rope_bwd")
     return out
 
 
