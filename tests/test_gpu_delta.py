@@ -101,8 +101,11 @@ def test_forward_and_gradients(case):
     args = [g[n] for n in NAMES]
     ck = torch.empty(tw.gradlev_delta_ckpt_bytes(B, H, Hk, T, dk, dv, code(dtype)),
                      dtype=torch.uint8, device="cuda")
-    y, ST = tw.gradlev_delta_fwd(*args, g["S0"], ckpt=ck)
+    y, ST = tw.gradlev_delta_fwd(*args, g["S0"])
     check(dict(y=y, ST=ST), dict(y=y64, ST=S64), dtype)
+    y, none = tw.gradlev_delta_fwd(*args, g["S0"], want_ST=False, ckpt=ck)
+    assert none is None
+    check(dict(y=y), dict(y=y64), dtype)
     out = tw.gradlev_delta_bwd(*args, g["dy"], g["S0"], dST.cuda(), ckpt=ck)
     if mask == "reset":  # every token starts anew: nothing flows through the gates
         assert not out["dlog_alpha"].any() and not out["dS0"].any()
@@ -113,10 +116,11 @@ def test_forward_and_gradients(case):
     again = tw.gradlev_delta_bwd(*args, g["dy"], g["S0"], dST.cuda())
     for n in out:
         assert torch.equal(out[n], again[n]), n
-    # and without the last state
-    y2, none = tw.gradlev_delta_fwd(*args, g["S0"], want_ST=False)
-    assert none is None
-    check(dict(y=y2), dict(y=y64), dtype)
+    # checkpoints of a forward that also gave the last state
+    y, ST = tw.gradlev_delta_fwd(*args, g["S0"], ckpt=ck)
+    check(dict(y=y, ST=ST), dict(y=y64, ST=S64), dtype)
+    out = tw.gradlev_delta_bwd(*args, g["dy"], g["S0"], dST.cuda(), ckpt=ck)
+    check(out, want, dtype, [n for n in want if mask != "reset" or n in ("dq", "dk", "dv", "dbeta")])
 
 
 @pytest.mark.parametrize("dtype,dv", [("f32", 32), ("bf16", 128), ("bf16", 256)])

@@ -5,6 +5,7 @@
 
 #include "common.cuh"
 #include "delta.h"
+#include "delta_tc.h"
 #include "dispatch.h"
 #include "gradlev.h"
 
@@ -28,19 +29,57 @@ Dims dims(int B, int H, int Hk, int T, int dk, int dv, gradlev_dtype dt) {
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-size_t ckpt_bytes(const Dims& d) { return ffma::saved_bytes(d, true); }
+constexpr uint64_t kWaitTimeoutNs = 2000000000ull;  // bound of device-side waits
+
+size_t ckpt_bytes(const Dims& d) {
+  return tc::shape_ok(d) ? tc::saved_bytes(d) : ffma::saved_bytes(d, true);
+}
+
+size_t fwd_scratch(const Dims& d) {
+  return tc::shape_ok(d) ? tc::fwd_scratch_bytes(d) : ffma::saved_bytes(d, false);
+}
 
 size_t bwd_scratch(const Dims& d) {  // E and the chunk-end gradients of the state
+  if (tc::shape_ok(d)) return tc::bwd_scratch_bytes(d);
   return up256(d.BH() * d.T * d.dv * sizeof(float)) +
          up256(d.BH() * ffma::chunks(d.T) * d.dv * d.dk * sizeof(float));
 }
 
+// The backward without checkpoints runs the forward into its own workspace. The forward's
+// scratch is dead by the time the backward's is written, so the two share their place.
 size_t ws_bytes_of(const Dims& d, int is_bwd) {
-  if (!is_bwd) return kStatusBytes + ffma::saved_bytes(d, false);
-  return kStatusBytes + bwd_scratch(d) + ckpt_bytes(d);
+  if (!is_bwd) return kStatusBytes + fwd_scratch(d);
+  const size_t f = fwd_scratch(d), b = bwd_scratch(d);
+  return kStatusBytes + (f > b ? f : b) + ckpt_bytes(d);
 }
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
+
+// The forward with its scratch behind the status word of `ws`; saved: the checkpoints, or
+// null; y: null for the checkpoints alone.
+cudaError_t fwd_run(const Dims& d, const void* q, const void* k, const void* v, const float* beta,
+                    const float* log_alpha, float scale, const float* S0, void* y, float* ST,
+                    char* saved, char* ws, cudaStream_t st) {
+  if (tc::shape_ok(d)) {
+    tc::Args a{d, q, k, v, beta, log_alpha, scale, reinterpret_cast<DeviceStatus*>(ws),
+               kWaitTimeoutNs, tc::mats_at(ws + kStatusBytes, d)};
+    if (saved) {
+      a.sv = tc::saved_at(saved, d);
+      a.m.Wb = a.sv.Wb;
+      a.m.PT = a.sv.PT;
+    }
+    a.S0 = S0;
+    a.y = y;
+    a.ST = ST;
+    return tc::run_fwd(a, st);
+  }
+  ffma::Args a{d, q, k, v, beta, log_alpha, scale,
+               saved ? ffma::saved_at(saved, d, true) : ffma::saved_at(ws + kStatusBytes, d, false)};
+  a.S0 = S0;
+  a.y = y;
+  a.ST = ST;
+  return ffma::run_fwd(a, st);
+}
 
 }  // namespace
 }  // namespace delta
@@ -85,13 +124,10 @@ gradlev_status gradlev_delta_fwd(int B, int H, int Hk, int T, int d_k, int d_v, 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
   if (cudaMemsetAsync(ws, 0, sizeof(DeviceStatus), st) != cudaSuccess) return GRADLEV_ERR_CUDA;
-  ffma::Args a{d, q, k, v, beta, log_alpha, scale,
-               ckpt ? ffma::saved_at(static_cast<char*>(ckpt), d, true)
-                    : ffma::saved_at(ws + kStatusBytes, d, false)};
-  a.S0 = S0;
-  a.y = y;
-  a.ST = ST;
-  return ffma::run_fwd(a, st) == cudaSuccess ? GRADLEV_OK : GRADLEV_ERR_CUDA;
+  return fwd_run(d, q, k, v, beta, log_alpha, scale, S0, y, ST, static_cast<char*>(ckpt), ws, st) ==
+                 cudaSuccess
+             ? GRADLEV_OK
+             : GRADLEV_ERR_CUDA;
 }
 
 gradlev_status gradlev_delta_bwd(int B, int H, int Hk, int T, int d_k, int d_v, gradlev_dtype dt,
@@ -117,13 +153,31 @@ gradlev_status gradlev_delta_bwd(int B, int H, int Hk, int T, int d_k, int d_v, 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
   if (cudaMemsetAsync(ws, 0, sizeof(DeviceStatus), st) != cudaSuccess) return GRADLEV_ERR_CUDA;
-  char* scratch = ws + kStatusBytes;
-  char* saved = ckpt ? static_cast<char*>(const_cast<void*>(ckpt)) : scratch + bwd_scratch(d);
-  ffma::Args a{d, q, k, v, beta, log_alpha, scale, ffma::saved_at(saved, d, true)};
+  char* saved = static_cast<char*>(const_cast<void*>(ckpt));
   if (!ckpt) {
-    a.S0 = S0;
-    if (ffma::run_fwd(a, st) != cudaSuccess) return GRADLEV_ERR_CUDA;
+    const size_t f = fwd_scratch(d), b = bwd_scratch(d);
+    saved = ws + kStatusBytes + (f > b ? f : b);
+    if (fwd_run(d, q, k, v, beta, log_alpha, scale, S0, nullptr, nullptr, saved, ws, st) != cudaSuccess)
+      return GRADLEV_ERR_CUDA;
   }
+  char* scratch = ws + kStatusBytes;
+  if (delta::tc::shape_ok(d)) {
+    delta::tc::Args a{d, q, k, v, beta, log_alpha, scale, reinterpret_cast<DeviceStatus*>(ws),
+               kWaitTimeoutNs};
+    a.sv = delta::tc::saved_at(saved, d);
+    a.dy = dy;
+    a.dST = dST;
+    a.E = reinterpret_cast<delta::tc::bf16*>(scratch);
+    a.dS = reinterpret_cast<delta::tc::bf16*>(scratch + up256(d.BH() * T * d_v * sizeof(delta::tc::bf16)));
+    a.dq = dq;
+    a.dk_ = dk;
+    a.dv_ = dv;
+    a.dbeta = dbeta;
+    a.dlog_alpha = dlog_alpha;
+    a.dS0 = dS0;
+    return delta::tc::run_bwd(a, st) == cudaSuccess ? GRADLEV_OK : GRADLEV_ERR_CUDA;
+  }
+  delta::ffma::Args a{d, q, k, v, beta, log_alpha, scale, delta::ffma::saved_at(saved, d, true)};
   a.dy = dy;
   a.dST = dST;
   a.E = reinterpret_cast<float*>(scratch);
@@ -134,7 +188,7 @@ gradlev_status gradlev_delta_bwd(int B, int H, int Hk, int T, int d_k, int d_v, 
   a.dbeta = dbeta;
   a.dlog_alpha = dlog_alpha;
   a.dS0 = dS0;
-  return ffma::run_bwd(a, st) == cudaSuccess ? GRADLEV_OK : GRADLEV_ERR_CUDA;
+  return delta::ffma::run_bwd(a, st) == cudaSuccess ? GRADLEV_OK : GRADLEV_ERR_CUDA;
 }
 
 }  // extern "C"

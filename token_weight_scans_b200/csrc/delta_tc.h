@@ -1,0 +1,148 @@
+// The gated delta rule on the tensor cores (tcgen05 / TMEM): bf16 I/O, d_k = 128,
+// d_v in {128, 256}, chunks of 64 tokens. Formulas in delta.h.
+//
+// Three kernels:
+//   prep  (delta_tc_prep.cu): per chunk, what does not depend on the state;
+//   walk  (delta_tc_walk.cu): the state recurrence, forward or backward;
+//   grad  (delta_tc_grad.cu): per chunk, the gradients of q, k and the gates.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "delta.h"
+
+namespace gradlev {
+namespace tc {
+bool make_map_bf16_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                      uint32_t box1);
+}
+
+namespace delta {
+namespace tc {
+
+constexpr int C = 64;            // tokens per chunk
+constexpr int TILE = C * 128;    // bytes of a [64 rows x 128 B] swizzled block
+constexpr int BIG = 128 * 128;   // bytes of a [128 rows x 128 B] swizzled block
+constexpr uint32_t LANE16 = 16u << 16;  // an M = 64 product in the upper 16 lanes of each 32
+
+__host__ __device__ inline int chunks(int T) { return (T + C - 1) / C; }
+
+inline bool shape_ok(const Dims& d) { return d.bf16 && d.dk == 128 && (d.dv == 128 || d.dv == 256); }
+
+using bf16 = __nv_bfloat16;
+
+// Chunk-local matrices that the walks read, all bf16 with N*64 rows per (b, h). With T0 =
+// I - Z diag(beta) and T = I - diag(beta) Z, the inverses of the two directions:
+//   W  [64][128] = -T0 diag(G) K      (D = T0 V + S W)
+//   T0 [64][64],  Pb [64][64] = P diag(beta)
+//   Wb [64][128] = T^T diag(w) K      (E = PT^T dY + dS Wb)
+//   PT [64][64]  = P T
+// lo parts: the remainders of W and T0, for a forward whose last state is asked for.
+struct Mats {
+  bf16 *W = nullptr, *Wlo = nullptr, *T0 = nullptr, *T0lo = nullptr, *Pb = nullptr;
+  bf16 *Wb = nullptr, *PT = nullptr;
+};
+
+// What the forward keeps for the backward: chunk-start states S [B*H][N][dv][128], D
+// [B*H][T][dv], Wb and PT.
+struct Saved {
+  bf16 *S = nullptr, *D = nullptr, *Wb = nullptr, *PT = nullptr;
+};
+size_t saved_bytes(const Dims& d);
+Saved saved_at(char* base, const Dims& d);
+size_t fwd_scratch_bytes(const Dims& d);  // W, Wlo, T0, T0lo, Pb
+Mats mats_at(char* base, const Dims& d);
+size_t bwd_scratch_bytes(const Dims& d);  // E and the chunk-end gradients of the state
+
+struct Args {
+  Dims d;
+  const void *q, *k, *v;
+  const float *beta, *log_alpha;
+  float scale;
+  DeviceStatus* status;
+  uint64_t timeout_ns;
+  Mats m;
+  Saved sv;                 // D, S null without checkpoints
+  const float* S0 = nullptr;
+  void* y = nullptr;
+  float* ST = nullptr;
+  const void* dy = nullptr;
+  const void* dST = nullptr;
+  bf16* E = nullptr;        // [B*H][T][dv]
+  bf16* dS = nullptr;       // [B*H][N][dv][128]: gradient of the chunk-end states
+  void *dq = nullptr, *dk_ = nullptr, *dv_ = nullptr, *dbeta = nullptr, *dlog_alpha = nullptr;
+  void* dS0 = nullptr;
+};
+
+cudaError_t launch_prep(const Args& a, bool split, cudaStream_t st);
+cudaError_t launch_walk(const Args& a, bool backward, bool split, cudaStream_t st);
+cudaError_t launch_grad(const Args& a, cudaStream_t st);
+
+cudaError_t run_fwd(const Args& a, cudaStream_t st);
+cudaError_t run_bwd(const Args& a, cudaStream_t st);
+
+// ---- gates of one chunk, one warp: lane l holds tokens l and l + 32.
+struct GatePair {
+  float be[2];        // beta
+  float Lh[2], Ll[2]; // running sum of log alpha without the resets, high and low part
+  int seg[2];         // resets up to and including the token
+  float Lend, Lend_lo;
+  int seg_end;
+};
+
+#ifdef __CUDACC__
+__device__ __forceinline__ GatePair chunk_gates(const float* beta, const float* log_alpha,
+                                                size_t row, int t0, int T) {
+  const int lane = threadIdx.x & 31;
+  GatePair g;
+  double L[2];
+  unsigned m[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int t = t0 + lane + 32 * k;
+    const float la = t < T ? log_alpha[row + t] : 0.f;
+    g.be[k] = t < T ? beta[row + t] : 0.f;
+    const bool reset = la < kResetLog;
+    L[k] = reset ? 0.0 : (double)la;
+    m[k] = __ballot_sync(0xffffffffu, reset);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double u = __shfl_up_sync(0xffffffffu, L[k], o);
+      if (lane >= o) L[k] += u;
+    }
+  }
+  L[1] += __shfl_sync(0xffffffffu, L[0], 31);
+  const unsigned below = 0xffffffffu >> (31 - lane);
+  g.seg[0] = __popc(m[0] & below);
+  g.seg[1] = __popc(m[0]) + __popc(m[1] & below);
+  g.seg_end = __popc(m[0]) + __popc(m[1]);
+  const double end = __shfl_sync(0xffffffffu, L[1], 31);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    g.Lh[k] = (float)L[k];
+    g.Ll[k] = (float)(L[k] - (double)g.Lh[k]);
+  }
+  g.Lend = (float)end;
+  g.Lend_lo = (float)(end - (double)g.Lend);
+  return g;
+}
+// G_i, w_i and G_C
+__device__ __forceinline__ float gate_G(const GatePair& g, int k) {
+  return g.seg[k] == 0 ? expf(g.Lh[k] + g.Ll[k]) : 0.f;
+}
+__device__ __forceinline__ float gate_w(const GatePair& g, int k) {
+  return g.seg[k] == g.seg_end ? expf((g.Lend - g.Lh[k]) + (g.Lend_lo - g.Ll[k])) : 0.f;
+}
+__device__ __forceinline__ float gate_GC(const GatePair& g) {
+  return g.seg_end == 0 ? expf(g.Lend + g.Lend_lo) : 0.f;
+}
+#endif
+
+}  // namespace tc
+}  // namespace delta
+}  // namespace gradlev

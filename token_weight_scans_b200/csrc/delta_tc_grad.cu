@@ -1,0 +1,465 @@
+// Tensor-core gated delta rule: the gradients of q, k and the gates of one chunk of 64
+// tokens and one key head, from the states at the chunk's start, their gradients at its
+// end, D and E (delta.h); two CTAs per SM. The value heads that share the key head are
+// taken in turn and add up in registers, so nothing is added through memory.
+//
+// Products of one value head (M = 64 tokens each; two share their TMEM columns, one in the
+// lower and one in the upper 16 lanes of each 32):
+//   F = dY D^T, H = E D^T (contracted over d_v)       t = dY S, u = E S, z = D dS
+//   X = scale M beta_j F,  Yn = -M beta_i beta_j H    (bf16, shared memory)
+//   xk = X K,  yk = Yn K,  ka = X^T Q + Yn^T K
+//   dQ += scale G t + xk,  dK += -beta G u + beta w z + ka + yk
+// The pairs' share of dlog_alpha needs only row and column sums of X q.k - Y k.k, which
+// are dot products of q and k with xk, yk and ka:
+//   row - column = q.xk + k.yk - k.ka.
+// Row and column sums come from the same bf16 X and Yn, so the parts that cancel over a
+// range of tokens do so to float32 rounding.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <atomic>
+
+#include "delta_tc.h"
+#include "sm100.cuh"
+
+namespace gradlev {
+namespace delta {
+namespace tc {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr uint32_t kCols = 256;
+constexpr uint32_t COL_A = 0;     // t | u, then . | yk
+constexpr uint32_t COL_B = 128;   // F, H (64 columns each) | z, then xk | ka
+
+struct GradSmem {
+  uint8_t Q[2 * TILE], K[2 * TILE];          // k-blocks; at the end dq and dk
+  uint8_t O[TILE], D[TILE], E[TILE];         // 64 tokens x 64 columns of d_v
+  uint8_t S[2 * TILE], dS[2 * TILE];         // 64 rows of d_v x 128
+  uint8_t X[TILE], Yn[TILE];
+  float Lh[C], Ll[C], be[C], cq[C], ck[C], cz[C];
+  int seg[C];
+  float xs[2][C], zs[2][C];                  // per column half
+  float red[8];
+  float GC;
+  uint64_t kq, full, mma;
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr size_t kSmem = sizeof(GradSmem) + 1024;
+static_assert(2 * kSmem <= 227 * 1024, "two CTAs per SM");
+
+enum : uint32_t { W_G_KQ = 0xa01, W_G_FULL, W_G_MMA };
+
+struct GradParams {
+  Dims d;
+  const float *beta, *log_alpha;
+  float scale;
+  DeviceStatus* status;
+  uint64_t timeout_ns;
+  bf16 *dbeta, *dlog_alpha;
+};
+
+// sum of v[e] * x over 32 columns of a swizzled row
+__device__ __forceinline__ float row_dot(const float (&v)[32], uint32_t tile, int r, int c8) {
+  float s = 0.f;
+#pragma unroll
+  for (int cc = 0; cc < 4; ++cc) {
+    const uint4 x = ld_shared_v4(tile + sw128_off(r, c8 + cc));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s = fmaf(v[8 * cc + 2 * e], bf16_lo(w[e]), s);
+      s = fmaf(v[8 * cc + 2 * e + 1], bf16_hi(w[e]), s);
+    }
+  }
+  return s;
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kThreads, 2)
+    grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmD,
+                const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmS,
+                const __grid_constant__ CUtensorMap tmdS, const __grid_constant__ CUtensorMap tmdq,
+                const __grid_constant__ CUtensorMap tmdk, GradParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  GradSmem& sm = *reinterpret_cast<GradSmem*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int q = warp & 3, hh = warp >> 2;          // TMEM quadrant, column half
+  const uint32_t lo = (uint32_t)(32 * q) << 16;
+  const int i = 16 * q + (lane & 15);              // token of this thread
+  const bool up = lane >= 16;                      // upper lanes: k's side, lower: q's
+  const int T = p.d.T, N = chunks(T), kh = blockIdx.x / N, n = blockIdx.x - kh * N, t0 = n * C;
+  const int b = kh / p.d.Hk, grp = p.d.H / p.d.Hk;
+  const WaitCtx wc{&sm.abort, p.status, p.timeout_ns};
+  if (tid == 0) {
+    sm.abort = 0;
+    mbar_init(&sm.kq, 1);
+    mbar_init(&sm.full, 1);
+    mbar_init(&sm.mma, 1);
+    fence_mbar_init();
+    mbar_arrive_expect_tx(&sm.kq, 4 * TILE);
+    for (int kb = 0; kb < 2; ++kb) {
+      tma_load_3d(sm.Q + kb * TILE, &tmQ, &sm.kq, 64 * kb, t0, kh);
+      tma_load_3d(sm.K + kb * TILE, &tmK, &sm.kq, 64 * kb, t0, kh);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(&sm.tmem_base, kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = sm.tmem_base;
+  const uint32_t sQ = smem_u32(sm.Q), sK = smem_u32(sm.K), sX = smem_u32(sm.X), sY = smem_u32(sm.Yn);
+  const uint32_t id_f = idesc_bf16(64, 64, false, false), id_t = idesc_bf16(64, 128, false, true);
+  const uint32_t id_m = idesc_bf16(64, 128, true, true);
+  uint32_t nfull = 0, nmma = 0;  // phases so far
+  const int nsl = p.d.dv / 64;
+
+  float acc[64];
+#pragma unroll
+  for (int e = 0; e < 64; ++e) acc[e] = 0.f;
+
+  for (int hv = 0; hv < grp; ++hv) {
+    const int bh = b * p.d.H + (kh - b * p.d.Hk) * grp + hv;
+    if (warp == 2) {
+      const GatePair g = chunk_gates(p.beta, p.log_alpha, (size_t)bh * T, t0, T);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int j = lane + 32 * k;
+        const float G = gate_G(g, k);
+        sm.Lh[j] = g.Lh[k];
+        sm.Ll[j] = g.Ll[k];
+        sm.seg[j] = g.seg[k];
+        sm.be[j] = g.be[k];
+        sm.cq[j] = p.scale * G;
+        sm.ck[j] = g.be[k] * G;
+        sm.cz[j] = g.be[k] * gate_w(g, k);
+      }
+      if (lane == 0) sm.GC = gate_GC(g);
+    }
+    float ss = 0.f;  // <dS, S>
+    for (int sl = 0; sl < nsl; ++sl) {
+      if (tid == 0) {
+        mbar_arrive_expect_tx(&sm.full, 7 * TILE);
+        tma_load_3d(sm.O, &tmO, &sm.full, 64 * sl, t0, bh);
+        tma_load_3d(sm.D, &tmD, &sm.full, 64 * sl, t0, bh);
+        tma_load_3d(sm.E, &tmE, &sm.full, 64 * sl, t0, bh);
+        for (int kb = 0; kb < 2; ++kb) {
+          tma_load_3d(sm.S + kb * TILE, &tmS, &sm.full, 64 * kb, 64 * sl, bh * N + n);
+          tma_load_3d(sm.dS + kb * TILE, &tmdS, &sm.full, 64 * kb, 64 * sl, bh * N + n);
+        }
+      }
+      mbar_wait(&sm.full, nfull++ & 1, wc, W_G_FULL);
+      __syncwarp();
+      if (tid == 0) {
+        const uint32_t sO = smem_u32(sm.O), sD = smem_u32(sm.D), sE = smem_u32(sm.E);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint32_t on = (sl > 0 || kk > 0) ? 1u : 0u;
+          const uint64_t ao = desc_at(sw128_desc(sO, 16, 1024), kk * 32);
+          const uint64_t ad = desc_at(sw128_desc(sD, 16, 1024), kk * 32);
+          const uint64_t ae = desc_at(sw128_desc(sE, 16, 1024), kk * 32);
+          const uint64_t bs = desc_at(sw128_desc(smem_u32(sm.S), TILE, 1024), kk * 2048);
+          const uint64_t bd = desc_at(sw128_desc(smem_u32(sm.dS), TILE, 1024), kk * 2048);
+          umma_bf16(tb + COL_B, ao, ad, id_f, on);                  // F
+          umma_bf16(tb + COL_B + 64, ae, ad, id_f, on);             // H
+          umma_bf16(tb + COL_A, ao, bs, id_t, on);                  // t
+          umma_bf16(tb + COL_A + LANE16, ae, bs, id_t, on);         // u
+          umma_bf16(tb + COL_B + LANE16, ad, bd, id_t, on);         // z
+        }
+        umma_commit(&sm.mma);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t off = (uint32_t)(tid + 256 * k) * 16;
+        const uint4 x = ld_shared_v4(smem_u32(sm.S) + off), y = ld_shared_v4(smem_u32(sm.dS) + off);
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          ss = fmaf(bf16_lo(xw[e]), bf16_lo(yw[e]), ss);
+          ss = fmaf(bf16_hi(xw[e]), bf16_hi(yw[e]), ss);
+        }
+      }
+      mbar_wait(&sm.mma, nmma++ & 1, wc, W_G_MMA);
+      __syncthreads();  // S and dS are read: the next slice may land (and the gates are there)
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (lane == 0) sm.red[warp] = ss;
+    tc_fence_after();
+    // ---- X and Yn: lower lanes, columns [32 hh, 32 hh + 32)
+    {
+      float f[32], g[32];
+      tmem_ld32(tb + COL_B + lo + 32 * hh, f);
+      tmem_ld32(tb + COL_B + 64 + lo + 32 * hh, g);
+      tmem_ld_wait();
+      if (!up) {
+        const float Lh = sm.Lh[i], Ll = sm.Ll[i], bi = sm.be[i];
+        const int seg = sm.seg[i];
+        float db = 0.f;
+        uint32_t xp[16], yp[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          float x[2], y[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int j = 32 * hh + e + u;
+            const bool on = j <= i && sm.seg[j] == seg;
+            const float m = on ? sm.be[j] * expf((Lh - sm.Lh[j]) + (Ll - sm.Ll[j])) : 0.f;
+            x[u] = on ? p.scale * m * f[e + u] : 0.f;
+            y[u] = on && j < i ? -bi * m * g[e + u] : 0.f;
+            if (j == i) db = g[e + u];
+          }
+          xp[e >> 1] = pack_bf16(x[0], x[1]);
+          yp[e >> 1] = pack_bf16(y[0], y[1]);
+        }
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          const uint32_t off = sw128_off(i, 4 * hh + cc);
+          st_shared_v4(sX + off, xp[4 * cc], xp[4 * cc + 1], xp[4 * cc + 2], xp[4 * cc + 3]);
+          st_shared_v4(sY + off, yp[4 * cc], yp[4 * cc + 1], yp[4 * cc + 2], yp[4 * cc + 3]);
+        }
+        if ((i >> 5) == hh && t0 + i < T) p.dbeta[(size_t)bh * T + t0 + i] = __float2bfloat16_rn(db);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+    }
+    if (hv == 0) mbar_wait(&sm.kq, 0, wc, W_G_KQ);
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)  // xk over F and H
+        umma_bf16(tb + COL_B, desc_at(sw128_desc(sX, 16, 1024), kk * 32),
+                  desc_at(sw128_desc(sK, TILE, 1024), kk * 2048), id_t, kk > 0);
+    }
+    __syncwarp();
+    // ---- t (lower) and u (upper); z (upper)
+    const uint32_t mine = up ? sK + hh * TILE : sQ + hh * TILE;
+    const float ca = up ? -sm.ck[i] : sm.cq[i], cz = up ? sm.cz[i] : 0.f;
+    float xs = 0.f, zs = 0.f;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      float v[32];
+      tmem_ld32(tb + COL_A + lo + 64 * hh + 32 * hf, v);
+      tmem_ld_wait();
+      xs = fmaf(ca, row_dot(v, mine, i, 4 * hf), xs);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) acc[32 * hf + e] = fmaf(ca, v[e], acc[32 * hf + e]);
+    }
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      float v[32];
+      tmem_ld32(tb + COL_B + lo + 64 * hh + 32 * hf, v);  // lower lanes: unused (xk in flight)
+      tmem_ld_wait();
+      if (up) {
+        zs = fmaf(cz, row_dot(v, mine, i, 4 * hf), zs);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[32 * hf + e] = fmaf(cz, v[e], acc[32 * hf + e]);
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const uint64_t bq = desc_at(sw128_desc(sQ, TILE, 1024), kk * 2048);
+        const uint64_t bk = desc_at(sw128_desc(sK, TILE, 1024), kk * 2048);
+        umma_bf16(tb + COL_B + LANE16, desc_at(sw128_desc(sX, TILE, 1024), kk * 2048), bq, id_m, kk > 0);
+        umma_bf16(tb + COL_B + LANE16, desc_at(sw128_desc(sY, TILE, 1024), kk * 2048), bk, id_m, 1);
+        umma_bf16(tb + COL_A + LANE16, desc_at(sw128_desc(sY, 16, 1024), kk * 32), bk, id_t, kk > 0);
+      }
+      umma_commit(&sm.mma);
+    }
+    __syncwarp();
+    mbar_wait(&sm.mma, nmma++ & 1, wc, W_G_MMA);
+    __syncwarp();
+    tc_fence_after();
+    // ---- xk (lower) and ka (upper); yk (upper)
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      float v[32];
+      tmem_ld32(tb + COL_B + lo + 64 * hh + 32 * hf, v);
+      tmem_ld_wait();
+      const float dot = row_dot(v, mine, i, 4 * hf);
+      xs += up ? -dot : dot;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) acc[32 * hf + e] += v[e];
+    }
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      float v[32];
+      tmem_ld32(tb + COL_A + lo + 64 * hh + 32 * hf, v);  // lower lanes: t, used above
+      tmem_ld_wait();
+      if (up) {
+        xs += row_dot(v, mine, i, 4 * hf);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[32 * hf + e] += v[e];
+      }
+      __syncwarp();
+    }
+    xs += __shfl_xor_sync(0xffffffffu, xs, 16);
+    zs += __shfl_xor_sync(0xffffffffu, zs, 16);
+    if (!up) {
+      sm.xs[hh][i] = xs;
+      sm.zs[hh][i] = zs;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {  // dlog_alpha: tokens 2 lane and 2 lane + 1
+      const int j = 2 * lane;
+      const float x0 = sm.xs[0][j] + sm.xs[1][j], x1 = sm.xs[0][j + 1] + sm.xs[1][j + 1];
+      const float z0 = sm.zs[0][j] + sm.zs[1][j], z1 = sm.zs[0][j + 1] + sm.zs[1][j + 1];
+      float sx = x0 + x1, sz = z0 + z1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float ux = __shfl_down_sync(0xffffffffu, sx, o), uz = __shfl_up_sync(0xffffffffu, sz, o);
+        if (lane + o < 32) sx += ux;
+        if (lane >= o) sz += uz;
+      }
+      float gg = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) gg += sm.red[w];
+      gg *= sm.GC;
+      const float before = __shfl_up_sync(0xffffffffu, sz, 1);
+      const float z_lt = lane == 0 ? 0.f : before;
+      const float after = __shfl_down_sync(0xffffffffu, sx, 1);
+      const float d1 = x1 + (lane == 31 ? 0.f : after);
+      const size_t row = (size_t)bh * T + t0;
+      if (t0 + j < T)
+        p.dlog_alpha[row + j] = __float2bfloat16_rn(
+            p.log_alpha[row + j] < kResetLog ? 0.f : sx + z_lt + gg);
+      if (t0 + j + 1 < T)
+        p.dlog_alpha[row + j + 1] = __float2bfloat16_rn(
+            p.log_alpha[row + j + 1] < kResetLog ? 0.f : d1 + z_lt + z0 + gg);
+    }
+    __syncthreads();  // the next head overwrites the gates and the sums
+  }
+  // ---- dq and dk over Q and K (every product has read them)
+#pragma unroll
+  for (int cc = 0; cc < 8; ++cc) {
+    const float* a = acc + 8 * cc;
+    st_shared_v4((up ? sK : sQ) + hh * TILE + sw128_off(i, cc), pack_bf16(a[0], a[1]),
+                 pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0) {
+    for (int kb = 0; kb < 2; ++kb) {
+      tma_store_3d(&tmdq, sm.Q + kb * TILE, 64 * kb, t0, kh);
+      tma_store_3d(&tmdk, sm.K + kb * TILE, 64 * kb, t0, kh);
+    }
+    tma_store_commit();
+    tma_store_wait_all();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tb, kCols);
+  }
+}
+
+cudaError_t launch_grad(const Args& a, cudaStream_t st) {
+  using gradlev::tc::make_map_bf16_3d;
+  const Dims& d = a.d;
+  const uint64_t N = chunks(d.T), kh = (uint64_t)d.B * d.Hk, bh = d.BH();
+  CUtensorMap mq, mk, mo, md, me, ms, mds, mdq, mdk;
+  if (!make_map_bf16_3d(&mq, a.q, 128, d.T, kh, C) || !make_map_bf16_3d(&mk, a.k, 128, d.T, kh, C) ||
+      !make_map_bf16_3d(&mo, a.dy, d.dv, d.T, bh, C) ||
+      !make_map_bf16_3d(&md, a.sv.D, d.dv, d.T, bh, C) ||
+      !make_map_bf16_3d(&me, a.E, d.dv, d.T, bh, C) ||
+      !make_map_bf16_3d(&ms, a.sv.S, 128, d.dv, bh * N, 64) ||
+      !make_map_bf16_3d(&mds, a.dS, 128, d.dv, bh * N, 64) ||
+      !make_map_bf16_3d(&mdq, a.dq, 128, d.T, kh, C) ||
+      !make_map_bf16_3d(&mdk, a.dk_, 128, d.T, kh, C))
+    return cudaErrorInvalidValue;
+  static std::atomic<uint64_t> set{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!bit || !(set.load() & bit)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit);
+  }
+  GradParams p{d, a.beta, a.log_alpha, a.scale, a.status, a.timeout_ns,
+               static_cast<bf16*>(a.dbeta), static_cast<bf16*>(a.dlog_alpha)};
+  grad_kernel<<<(unsigned)(N * kh), kThreads, kSmem, st>>>(mq, mk, mo, md, me, ms, mds, mdq, mdk, p);
+  count_launch();
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- buffers and order
+static size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+static bf16* take(char*& at, size_t elems) {
+  bf16* p = reinterpret_cast<bf16*>(at);
+  at += up256(elems * sizeof(bf16));
+  return p;
+}
+
+Saved saved_at(char* base, const Dims& d) {
+  const size_t rows = d.BH() * chunks(d.T);
+  char* at = base;
+  Saved s;
+  s.S = take(at, rows * d.dv * 128);
+  s.D = take(at, d.BH() * (size_t)d.T * d.dv);
+  s.Wb = take(at, rows * C * 128);
+  s.PT = take(at, rows * C * C);
+  return s;
+}
+
+size_t saved_bytes(const Dims& d) {
+  const size_t rows = d.BH() * chunks(d.T);
+  return up256(rows * d.dv * 256) + up256(d.BH() * (size_t)d.T * d.dv * 2) +
+         up256(rows * C * 256) + up256(rows * C * C * 2);
+}
+
+Mats mats_at(char* base, const Dims& d) {
+  const size_t rows = d.BH() * chunks(d.T);
+  char* at = base;
+  Mats m;
+  m.W = take(at, rows * C * 128);
+  m.Wlo = take(at, rows * C * 128);
+  m.T0 = take(at, rows * C * C);
+  m.T0lo = take(at, rows * C * C);
+  m.Pb = take(at, rows * C * C);
+  return m;
+}
+
+size_t fwd_scratch_bytes(const Dims& d) {
+  const size_t rows = d.BH() * chunks(d.T);
+  return 2 * up256(rows * C * 256) + 3 * up256(rows * C * C * 2);
+}
+
+size_t bwd_scratch_bytes(const Dims& d) {
+  return up256(d.BH() * (size_t)d.T * d.dv * 2) + up256(d.BH() * chunks(d.T) * d.dv * 256);
+}
+
+cudaError_t run_fwd(const Args& a, cudaStream_t st) {
+  const bool split = a.ST != nullptr;
+  const cudaError_t e = launch_prep(a, split, st);
+  return e != cudaSuccess ? e : launch_walk(a, false, split, st);
+}
+
+cudaError_t run_bwd(const Args& a, cudaStream_t st) {
+  const cudaError_t e = launch_walk(a, true, false, st);
+  return e != cudaSuccess ? e : launch_grad(a, st);
+}
+
+}  // namespace tc
+}  // namespace delta
+}  // namespace gradlev

@@ -1,0 +1,571 @@
+// Tensor-core gated delta rule: the state recurrence over the chunks of one scan, one CTA
+// per (b, h, 128 rows of d_v). Matrices of struct Mats in delta_tc.h; everything on the
+// state is transposed (rows of d_v in the 128 TMEM lanes, tokens or d_k in the columns),
+// so that the two operands made from the previous product stay in tensor memory:
+//
+//   forward                                backward (chunks in reverse, S is dS)
+//   D^T  = V^T T0^T + S W^T                E^T = dY^T PT + S Wb^T
+//   S    = G_C S + (beta w D)^T K          S   = G_C S + dY^T (scale G Q) + E^T (-beta G K)
+//   Y^T  = S (scale G Q)^T + D^T Pb^T      dV  = beta E
+//
+// The chain through a chunk is: S to bf16 (TMEM -> registers -> TMEM), the product with W,
+// its result to bf16, the product with K. All else (V^T T0^T, dY^T Q, the outputs, the
+// loads, the gates and the scaling of Q and K by them) runs beside it.
+//
+// SPLIT (a forward whose last state is asked for): every operand of the state that is not
+// exact in bf16 comes as a sum of two bf16 (S, W, T0, beta w D), three products in place of
+// one, so that S carries 16 bits through the chunks and the float32 state it ends with is
+// good to 1e-5. Training needs no such state and takes single products.
+//
+// Warp roles (16): 0 TMA producer, 1 MMA issuer (owns TMEM), 2 gates, 4-11 two chain
+// warpgroups (each half of the columns), 12-15 scaling of Q and K, and Y.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <atomic>
+
+#include "delta_tc.h"
+#include "sm100.cuh"
+
+namespace gradlev {
+namespace delta {
+namespace tc {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int NS = 2;             // TMA stages
+constexpr int GS = 4;             // gate slots
+constexpr int kThreads = 512;
+
+// TMEM columns
+constexpr uint32_t COL_S = 0;      // float32 state, 128
+constexpr uint32_t COL_SH = 128;   // bf16 state, 64
+constexpr uint32_t COL_D = 192;    // D^T (E^T) accumulator, 64
+constexpr uint32_t COL_DB = 256;   // bf16 D (E), 32
+constexpr uint32_t COL_U = 288;    // bf16 beta w D, 32
+constexpr uint32_t COL_Y = 320;    // Y^T, 64 per buffer
+constexpr uint32_t COL_SL = 384;   // remainder of the state, 64 (SPLIT: one Y buffer)
+constexpr uint32_t COL_UL = 448;   // remainder of beta w D, 32
+
+struct GateSlot {
+  float q[C];    // scale G
+  float u[C];    // forward: beta w; backward: -beta G
+  float be[C];   // beta
+  float GC;
+  float pad[3];
+};
+
+struct Bars {
+  GateSlot gates[GS];
+  uint64_t full[NS], empty[NS], scaled[NS];
+  uint64_t gfull[GS], gempty[GS];
+  uint64_t sready, dfull, uready, sfull, done;
+  uint64_t yfull[2], yfree[2];
+  uint32_t tmem_base;
+  int abort;
+};
+
+// Stage: Q, K, V (dY) tiles of 2 TILE; W (Wb) of 2 TILE; T0, Pb (or PT) of TILE; SPLIT adds
+// the remainders of W and T0.
+template <bool BWD, bool SPLIT>
+struct Layout {
+  static constexpr int q = 0, k = 2 * TILE, v = 4 * TILE, w = 6 * TILE, t = 8 * TILE;
+  static constexpr int p = 9 * TILE, wl = 10 * TILE, tl = 12 * TILE;
+  static constexpr int bytes = BWD ? 9 * TILE : (SPLIT ? 13 * TILE : 10 * TILE);
+  static constexpr bool staged = !SPLIT;   // bf16 states through shared memory and TMA
+  static constexpr int stage_s = NS * bytes;
+  static constexpr int bars = stage_s + (staged ? 2 * BIG : 0);
+  static constexpr size_t smem = bars + sizeof(Bars) + 1024;
+  static_assert(smem <= 227 * 1024, "over the shared memory of a CTA");
+};
+
+enum : uint32_t {
+  W_TMA = 0x901, W_TMA_DRAIN, W_FULL = 0x911, W_SCALED, W_SREADY, W_UREADY, W_YFREE, W_DONE,
+  W_GATE = 0x921, W_C_SFULL = 0x931, W_C_DFULL, W_C_GATE, W_C_Y, W_O_FULL = 0x941, W_O_GATE, W_O_Y,
+};
+
+struct WalkParams {
+  Dims d;
+  const float *beta, *log_alpha;
+  float scale;
+  DeviceStatus* status;
+  uint64_t timeout_ns;
+  const float* S0;       // forward start
+  const bf16* dST;       // backward start
+  float* ST;             // forward end
+  bf16* dS0;             // backward end
+  bf16* y;               // forward
+  bf16* D;               // forward: D, backward: E (null: not kept)
+  bf16* dv;              // backward
+  bf16* states;          // chunk-start (chunk-end) states, or null
+};
+
+__device__ __forceinline__ void st_tmem32(uint32_t col, const uint32_t (&r)[32]) {
+  float v[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+  tmem_st32(col, v);
+}
+__device__ __forceinline__ void st_tmem16(uint32_t col, const uint32_t (&r)[16]) {
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+  tmem_st16(col, v);
+}
+__device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
+  return pack_bf16(a - bf16_lo(hi), b - bf16_hi(hi));
+}
+
+// x *= factor[row] on a [64 tokens x 128] tile in place, by 128 threads.
+__device__ __forceinline__ void scale_tile(uint32_t tile, const float* factor, int t) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t off = (uint32_t)(t + 128 * k) * 16;
+    const int j = (off & (TILE - 1)) >> 7;
+    const float f = factor[j];
+    const uint4 v = ld_shared_v4(tile + off);
+    st_shared_v4(tile + off, pack_bf16(f * bf16_lo(v.x), f * bf16_hi(v.x)),
+                 pack_bf16(f * bf16_lo(v.y), f * bf16_hi(v.y)),
+                 pack_bf16(f * bf16_lo(v.z), f * bf16_hi(v.z)),
+                 pack_bf16(f * bf16_lo(v.w), f * bf16_hi(v.w)));
+  }
+}
+
+}  // namespace
+
+template <bool BWD, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
+    walk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmW,
+                const __grid_constant__ CUtensorMap tmWl, const __grid_constant__ CUtensorMap tmT,
+                const __grid_constant__ CUtensorMap tmTl, const __grid_constant__ CUtensorMap tmP,
+                const __grid_constant__ CUtensorMap tmS, WalkParams p) {
+  using L = Layout<BWD, SPLIT>;
+  constexpr int NY = SPLIT ? 1 : 2;   // Y buffers
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Bars& sm = *reinterpret_cast<Bars*>(base + L::bars);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ns = p.d.dv >> 7, bh = blockIdx.x / ns, n0 = (blockIdx.x - bh * ns) * 128;
+  const int b = bh / p.d.H, h = bh - b * p.d.H;
+  const int kh = b * p.d.Hk + h / (p.d.H / p.d.Hk);
+  const int T = p.d.T, N = chunks(T);
+  auto cg = [&](int c) { return BWD ? N - 1 - c : c; };  // the c-th chunk walked
+  const WaitCtx wc{&sm.abort, p.status, p.timeout_ns};
+
+  if (threadIdx.x == 0) {
+    sm.abort = 0;
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+      mbar_init(&sm.scaled[s], 4);
+    }
+    for (int g = 0; g < GS; ++g) {
+      mbar_init(&sm.gfull[g], 32);
+      mbar_init(&sm.gempty[g], 12);  // 8 chain warps, 4 scaling warps
+    }
+    mbar_init(&sm.sready, 8);
+    mbar_init(&sm.dfull, 1);
+    mbar_init(&sm.uready, 8);
+    mbar_init(&sm.sfull, 1);
+    mbar_init(&sm.done, 1);
+    for (int y = 0; y < 2; ++y) {
+      mbar_init(&sm.yfull[y], 1);
+      mbar_init(&sm.yfree[y], 4);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sm.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = sm.tmem_base;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      int issued = 0;
+      for (int c = 0; c < N; ++c) {
+        const int s = c % NS, n = cg(c), t0 = n * C;
+        if (!mbar_wait(&sm.empty[s], ((c / NS) & 1) ^ 1, wc, W_TMA)) break;
+        uint8_t* st = base + s * L::bytes;
+        mbar_arrive_expect_tx(&sm.full[s], L::bytes);
+        for (int kb = 0; kb < 2; ++kb) {
+          tma_load_3d(st + L::v + kb * TILE, &tmV, &sm.full[s], n0 + 64 * kb, t0, bh);
+          tma_load_3d(st + L::w + kb * TILE, &tmW, &sm.full[s], 64 * kb, t0, bh);
+          tma_load_3d(st + L::q + kb * TILE, &tmQ, &sm.full[s], 64 * kb, t0, kh);
+          tma_load_3d(st + L::k + kb * TILE, &tmK, &sm.full[s], 64 * kb, t0, kh);
+          if (SPLIT) tma_load_3d(st + L::wl + kb * TILE, &tmWl, &sm.full[s], 64 * kb, t0, bh);
+        }
+        tma_load_3d(st + L::t, &tmT, &sm.full[s], 0, t0, bh);
+        if (!BWD) tma_load_3d(st + L::p, &tmP, &sm.full[s], 0, t0, bh);
+        if (SPLIT) tma_load_3d(st + L::tl, &tmTl, &sm.full[s], 0, t0, bh);
+        issued = c + 1;
+      }
+      for (int c = issued > NS ? issued - NS : 0; c < issued; ++c)
+        mbar_drain(&sm.full[c % NS], (c / NS) & 1, wc, W_TMA_DRAIN);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t id_v = idesc_bf16(128, 64, true, BWD);       // V^T T0^T, dY^T PT
+      const uint32_t id_w = idesc_bf16(128, 64, false, false);    // S W^T, S Q^T, D^T Pb^T
+      const uint32_t id_u = idesc_bf16(128, 128, false, true);    // U^T K, E^T K
+      const uint32_t id_o = idesc_bf16(128, 128, true, true);     // dY^T Q
+      for (int c = 0; c < N; ++c) {
+        const int s = c % NS, yb = c % NY;
+        const uint32_t st = smem_u32(base + s * L::bytes);
+        if (!mbar_wait(&sm.full[s], (c / NS) & 1, wc, W_FULL)) break;
+        tc_fence_after();
+        // D^T = V^T T0^T: the chain warps have read D of chunk c - 1 (uready, waited below)
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t av = desc_at(sw128_desc(st + L::v, TILE, 1024), kk * 2048);
+          const uint32_t off = BWD ? kk * 2048 : kk * 32;
+          umma_bf16(tb + COL_D, av, desc_at(sw128_desc(st + L::t, BWD ? TILE : 16, 1024), off), id_v, kk > 0);
+          if (SPLIT) umma_bf16(tb + COL_D, av, desc_at(sw128_desc(st + L::tl, 16, 1024), off), id_v, 1);
+        }
+        if (!mbar_wait(&sm.sready, c & 1, wc, W_SREADY)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {  // += S W^T
+          const uint32_t off = (kk >> 2) * TILE + (kk & 3) * 32;
+          const uint64_t bw = desc_at(sw128_desc(st + L::w, 16, 1024), off);
+          umma_bf16_tmem_a(tb + COL_D, tb + COL_SH + 8 * kk, bw, id_w, 1);
+          if (SPLIT) {
+            umma_bf16_tmem_a(tb + COL_D, tb + COL_SL + 8 * kk, bw, id_w, 1);
+            umma_bf16_tmem_a(tb + COL_D, tb + COL_SH + 8 * kk,
+                             desc_at(sw128_desc(st + L::wl, 16, 1024), off), id_w, 1);
+          }
+        }
+        umma_commit(&sm.dfull);
+        if (!mbar_wait(&sm.scaled[s], (c / NS) & 1, wc, W_SCALED)) break;
+        tc_fence_after();
+        if (BWD) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // S += dY^T (scale G Q): S is scaled (sready)
+            umma_bf16(tb + COL_S, desc_at(sw128_desc(st + L::v, TILE, 1024), kk * 2048),
+                      desc_at(sw128_desc(st + L::q, TILE, 1024), kk * 2048), id_o, 1);
+        }
+        if (!mbar_wait(&sm.uready, c & 1, wc, W_UREADY)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {  // S += U^T K
+          const uint64_t bk = desc_at(sw128_desc(st + L::k, TILE, 1024), kk * 2048);
+          umma_bf16_tmem_a(tb + COL_S, tb + (BWD ? COL_DB : COL_U) + 8 * kk, bk, id_u, 1);
+          if (SPLIT) umma_bf16_tmem_a(tb + COL_S, tb + COL_UL + 8 * kk, bk, id_u, 1);
+        }
+        umma_commit(&sm.sfull);
+        if (!BWD) {
+          if (!mbar_wait(&sm.yfree[yb], ((c / NY) & 1) ^ 1, wc, W_YFREE)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {  // Y^T = S (scale G Q)^T
+            const uint32_t off = (kk >> 2) * TILE + (kk & 3) * 32;
+            umma_bf16_tmem_a(tb + COL_Y + 64 * yb, tb + COL_SH + 8 * kk,
+                             desc_at(sw128_desc(st + L::q, 16, 1024), off), id_w, kk > 0);
+          }
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // += D^T Pb^T
+            umma_bf16_tmem_a(tb + COL_Y + 64 * yb, tb + COL_DB + 8 * kk,
+                             desc_at(sw128_desc(st + L::p, 16, 1024), kk * 32), id_w, 1);
+          umma_commit(&sm.yfull[yb]);
+        }
+        umma_commit(&sm.empty[s]);
+      }
+      umma_commit(&sm.done);
+      mbar_drain(&sm.done, 0, wc, W_DONE);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ gates
+    for (int c = 0; c < N; ++c) {
+      const int g = c % GS;
+      const GatePair gp = chunk_gates(p.beta, p.log_alpha, (size_t)bh * T, cg(c) * C, T);
+      if (!mbar_wait_warp(&sm.gempty[g], ((c / GS) & 1) ^ 1, wc, W_GATE)) break;
+      GateSlot& gs = sm.gates[g];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int i = lane + 32 * k;
+        const float G = gate_G(gp, k);
+        gs.q[i] = p.scale * G;
+        gs.u[i] = BWD ? -gp.be[k] * G : gp.be[k] * gate_w(gp, k);
+        gs.be[i] = gp.be[k];
+      }
+      if (lane == 0) gs.GC = gate_GC(gp);
+      __syncwarp();
+      mbar_arrive(&sm.gfull[g]);
+    }
+  } else if (warp >= 4 && warp < 12) {
+    // ------------------------------------------------------------ the chain
+    const int q = warp & 3, hh = (warp - 4) >> 2;
+    const uint32_t lo = (uint32_t)(32 * q) << 16;
+    const int r = 32 * q + lane;           // row of the slice
+    const size_t row = (size_t)bh * p.d.dv + n0 + r;
+    // start state
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      float v[32];
+      const int col = 64 * hh + 32 * hf;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] = 0.f;
+      if (!BWD && p.S0) {
+        const float4* s = reinterpret_cast<const float4*>(p.S0 + row * 128 + col);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float4 u = s[e];
+          v[4 * e] = u.x;
+          v[4 * e + 1] = u.y;
+          v[4 * e + 2] = u.z;
+          v[4 * e + 3] = u.w;
+        }
+      }
+      if (BWD && p.dST) {
+        const uint4* s = reinterpret_cast<const uint4*>(p.dST + row * 128 + col);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint4 u = s[e];
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {
+            v[8 * e + 2 * f] = bf16_lo(w[f]);
+            v[8 * e + 2 * f + 1] = bf16_hi(w[f]);
+          }
+        }
+      }
+      tmem_st32(tb + COL_S + lo + col, v);
+    }
+    tmem_st_wait();
+    bool ok = true;
+    for (int c = 0; c < N && ok; ++c) {
+      const int g = c % GS, n = cg(c), t0 = n * C;
+      const GateSlot& gs = sm.gates[g];
+      ok = mbar_wait_warp(&sm.gfull[g], (c / GS) & 1, wc, W_C_GATE);
+      ok = ok && (c == 0 || mbar_wait_warp(&sm.sfull, (c - 1) & 1, wc, W_C_SFULL));
+      // the bf16 state is free once Y of chunk c - 1 has read it
+      ok = ok && (BWD || c == 0 ||
+                  mbar_wait_warp(&sm.yfull[(c - 1) % NY], ((c - 1) / NY) & 1, wc, W_C_Y));
+      if (!ok) break;
+      tc_fence_after();
+      const float GC = gs.GC;
+      uint32_t pk[32];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float v[32];
+        const uint32_t at = tb + COL_S + lo + 64 * hh + 32 * hf;
+        tmem_ld32(at, v);
+        tmem_ld_wait();
+        uint32_t rest[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          pk[16 * hf + e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+          if (SPLIT) rest[e] = pack_rest(v[2 * e], v[2 * e + 1], pk[16 * hf + e]);
+        }
+        if (SPLIT) st_tmem16(tb + COL_SL + lo + 32 * hh + 16 * hf, rest);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] *= GC;
+        tmem_st32(at, v);
+      }
+      st_tmem32(tb + COL_SH + lo + 32 * hh, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.sready);
+      if (p.states) {
+        if (L::staged) {
+          if (lane == 0) tma_store_wait_read_n<0>();  // the store of the chunk before
+          __syncwarp();
+          const uint32_t tile = smem_u32(base + L::stage_s + hh * BIG);
+#pragma unroll
+          for (int cc = 0; cc < 8; ++cc)
+            st_shared_v4(tile + sw128_off(r, cc), pk[4 * cc], pk[4 * cc + 1], pk[4 * cc + 2],
+                         pk[4 * cc + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tmS, base + L::stage_s + hh * BIG + 32 * q * 128, 64 * hh, n0 + 32 * q,
+                         bh * N + n);
+            tma_store_commit();
+          }
+        } else {
+          uint4* out = reinterpret_cast<uint4*>(
+              p.states + (((size_t)bh * N + n) * p.d.dv + n0 + r) * 128 + 64 * hh);
+#pragma unroll
+          for (int cc = 0; cc < 8; ++cc)
+            out[cc] = make_uint4(pk[4 * cc], pk[4 * cc + 1], pk[4 * cc + 2], pk[4 * cc + 3]);
+        }
+      }
+      ok = mbar_wait_warp(&sm.dfull, c & 1, wc, W_C_DFULL);
+      if (!ok) break;
+      tc_fence_after();
+      float v[32];
+      tmem_ld32(tb + COL_D + lo + 32 * hh, v);
+      tmem_ld_wait();
+      uint32_t db[16];
+      {
+        uint32_t ub[16], rest[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          db[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+          if (!BWD) {
+            const float u0 = v[2 * e] * gs.u[32 * hh + 2 * e];
+            const float u1 = v[2 * e + 1] * gs.u[32 * hh + 2 * e + 1];
+            ub[e] = pack_bf16(u0, u1);
+            if (SPLIT) rest[e] = pack_rest(u0, u1, ub[e]);
+          }
+        }
+        st_tmem16(tb + COL_DB + lo + 16 * hh, db);
+        if (!BWD) st_tmem16(tb + COL_U + lo + 16 * hh, ub);
+        if (SPLIT) st_tmem16(tb + COL_UL + lo + 16 * hh, rest);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.uready);
+      // D (E and dV) to memory: a warp's store covers 32 consecutive rows of one token
+      if (p.D) {
+        const size_t o = ((size_t)bh * T + t0 + 32 * hh) * p.d.dv + n0 + r;
+        const int left = T - t0 - 32 * hh;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          if (e >= left) break;
+          const uint32_t w = db[e >> 1];
+          reinterpret_cast<unsigned short*>(p.D)[o + (size_t)e * p.d.dv] =
+              (unsigned short)(e & 1 ? w >> 16 : w & 0xffff);
+          if (BWD) p.dv[o + (size_t)e * p.d.dv] = __float2bfloat16_rn(gs.be[32 * hh + e] * v[e]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.gempty[g]);
+    }
+    if (lane == 0 && L::staged) tma_store_wait_all();
+    if (ok && (BWD ? p.dS0 != nullptr : p.ST != nullptr) &&
+        mbar_wait_warp(&sm.sfull, (N - 1) & 1, wc, W_C_SFULL)) {
+      tc_fence_after();
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float v[32];
+        const int col = 64 * hh + 32 * hf;
+        tmem_ld32(tb + COL_S + lo + col, v);
+        tmem_ld_wait();
+        if (!BWD) {
+          float4* o = reinterpret_cast<float4*>(p.ST + row * 128 + col);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        } else {
+          uint4* o = reinterpret_cast<uint4*>(p.dS0 + row * 128 + col);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            o[e] = make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
+                              pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7]));
+        }
+      }
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ scaled Q (and K); Y
+    const int q = warp & 3, t = threadIdx.x - 384;
+    const uint32_t lo = (uint32_t)(32 * q) << 16;
+    auto scale_chunk = [&](int c) -> bool {
+      const int s = c % NS, g = c % GS;
+      if (!mbar_wait_warp(&sm.full[s], (c / NS) & 1, wc, W_O_FULL)) return false;
+      if (!mbar_wait_warp(&sm.gfull[g], (c / GS) & 1, wc, W_O_GATE)) return false;
+      const uint32_t st = smem_u32(base + s * L::bytes);
+      scale_tile(st + L::q, sm.gates[g].q, t);
+      if (BWD) scale_tile(st + L::k, sm.gates[g].u, t);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sm.scaled[s]);
+        mbar_arrive(&sm.gempty[g]);
+      }
+      return true;
+    };
+    bool ok = scale_chunk(0);
+    for (int c = 0; c < N && ok; ++c) {
+      if (c + 1 < N) ok = scale_chunk(c + 1);
+      if (BWD) continue;
+      const int yb = c % NY, t0 = c * C;
+      ok = ok && mbar_wait_warp(&sm.yfull[yb], (c / NY) & 1, wc, W_O_Y);
+      if (!ok) break;
+      tc_fence_after();
+      bf16* o = p.y + ((size_t)bh * T + t0) * p.d.dv + n0 + 32 * q + lane;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float v[32];
+        tmem_ld32(tb + COL_Y + 64 * yb + lo + 32 * hf, v);
+        tmem_ld_wait();
+        if (hf == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.yfree[yb]);
+        }
+        const int left = T - t0 - 32 * hf;
+        if (p.y) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (e < left) o[(size_t)(32 * hf + e) * p.d.dv] = __float2bfloat16_rn(v[e]);
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tb, 512);
+  }
+}
+
+template <bool BWD, bool SPLIT>
+static cudaError_t launch(const Args& a, cudaStream_t st) {
+  using L = Layout<BWD, SPLIT>;
+  using gradlev::tc::make_map_bf16_3d;
+  const Dims& d = a.d;
+  const uint64_t N = chunks(d.T), kh = (uint64_t)d.B * d.Hk, bh = d.BH();
+  const void* v = BWD ? a.dy : a.v;
+  bf16* states = BWD ? a.dS : a.sv.S;
+  const bf16* w = BWD ? a.sv.Wb : a.m.W;
+  const bf16* t = BWD ? a.sv.PT : a.m.T0;
+  CUtensorMap mq, mk, mv, mw, mwl, mt, mtl, mp, ms;
+  if (!make_map_bf16_3d(&mq, a.q, 128, d.T, kh, C) || !make_map_bf16_3d(&mk, a.k, 128, d.T, kh, C) ||
+      !make_map_bf16_3d(&mv, v, d.dv, d.T, bh, C) || !make_map_bf16_3d(&mw, w, 128, N * C, bh, C) ||
+      !make_map_bf16_3d(&mwl, SPLIT ? a.m.Wlo : w, 128, N * C, bh, C) ||
+      !make_map_bf16_3d(&mt, t, C, N * C, bh, C) ||
+      !make_map_bf16_3d(&mtl, SPLIT ? a.m.T0lo : t, C, N * C, bh, C) ||
+      !make_map_bf16_3d(&mp, BWD ? t : a.m.Pb, C, N * C, bh, C) ||
+      !make_map_bf16_3d(&ms, states ? (const void*)states : w, 128, states ? d.dv : N * C,
+                        states ? bh * N : bh, 32))
+    return cudaErrorInvalidValue;
+  static std::atomic<uint64_t> set{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!bit || !(set.load() & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        walk_kernel<BWD, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::smem);
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit);
+  }
+  WalkParams p{d, a.beta, a.log_alpha, a.scale, a.status, a.timeout_ns, a.S0,
+               static_cast<const bf16*>(a.dST), a.ST, static_cast<bf16*>(a.dS0),
+               static_cast<bf16*>(a.y), BWD ? a.E : a.sv.D, static_cast<bf16*>(a.dv_), states};
+  walk_kernel<BWD, SPLIT><<<(unsigned)(bh * (d.dv / 128)), kThreads, L::smem, st>>>(
+      mq, mk, mv, mw, mwl, mt, mtl, mp, ms, p);
+  count_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_walk(const Args& a, bool backward, bool split, cudaStream_t st) {
+  if (backward) return launch<true, false>(a, st);
+  return split ? launch<false, true>(a, st) : launch<false, false>(a, st);
+}
+
+}  // namespace tc
+}  // namespace delta
+}  // namespace gradlev
