@@ -10,7 +10,9 @@ If the shared library is missing or cannot be loaded, every call raises
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 
 __all__ = [
@@ -509,6 +511,37 @@ def gradlev_mlp2_recon(x, g1hat, g2hat, v, eta, alpha, W1, W2, control=False, *,
     return out
 
 
+# The calls below are launch-bound at a token per request, so their checks and pointers
+# avoid what torch's wrappers cost: the device is only switched when it is not current, the
+# stream is read as a raw handle, and addresses are passed as integers.
+_NO_SWITCH = contextlib.nullcontext()
+
+
+def _on(dev):
+    """Launches go to the tensors' device."""
+    import torch
+    return _NO_SWITCH if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_of(stream, dev):
+    """The raw cudaStream_t: the given stream, which must be on `dev`, or dev's current one."""
+    import torch
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    if stream.device != dev:
+        raise GradlevError(f"stream is on {stream.device}, the tensors on {dev}")
+    return stream.cuda_stream
+
+
+def _check_fast(name, t, shape, dtype, device):
+    if (t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous()):
+        _check_tensor(name, t, shape, dtype, device)
+
+
 def gradlev_delta_supported(B, H, Hk, T, d_k, d_v, dt) -> int:
     return int(lib().gradlev_delta_supported(B, H, Hk, T, d_k, d_v, dt))
 
@@ -530,11 +563,11 @@ def _delta_args(q, k, v, beta, log_alpha, scale):
     H, d_v = v.shape[1], v.shape[3]
     dev, dt = _cuda_device(q), q.dtype
     code = _dt_code(dt)
-    _check_tensor("q", q, (B, Hk, T, d_k), dt, dev)
-    _check_tensor("k", k, (B, Hk, T, d_k), dt, dev)
-    _check_tensor("v", v, (B, H, T, d_v), dt, dev)
-    _check_tensor("beta", beta, (B, H, T), torch.float32, dev)
-    _check_tensor("log_alpha", log_alpha, (B, H, T), torch.float32, dev)
+    _check_fast("q", q, (B, Hk, T, d_k), dt, dev)
+    _check_fast("k", k, (B, Hk, T, d_k), dt, dev)
+    _check_fast("v", v, (B, H, T, d_v), dt, dev)
+    _check_fast("beta", beta, (B, H, T), torch.float32, dev)
+    _check_fast("log_alpha", log_alpha, (B, H, T), torch.float32, dev)
     return (B, H, Hk, T, d_k, d_v, code), dev, dt, float(d_k ** -0.5 if scale is None else scale)
 
 
@@ -550,22 +583,22 @@ def gradlev_delta_fwd(q, k, v, beta, log_alpha, S0=None, *, scale=None, y=None, 
     f32 = torch.float32
     _check(gradlev_delta_supported(*size), "gradlev_delta_fwd")
     if S0 is not None:
-        _check_tensor("S0", S0, (B, H, d_v, d_k), f32, dev)
+        _check_fast("S0", S0, (B, H, d_v, d_k), f32, dev)
     if y is None:
         y = torch.empty((B, H, T, d_v), dtype=dt, device=dev)
-    _check_tensor("y", y, (B, H, T, d_v), dt, dev)
+    _check_fast("y", y, (B, H, T, d_v), dt, dev)
     if ST is None and want_ST:
         ST = torch.empty((B, H, d_v, d_k), dtype=f32, device=dev)
     if ST is not None:
-        _check_tensor("ST", ST, (B, H, d_v, d_k), f32, dev)
+        _check_fast("ST", ST, (B, H, d_v, d_k), f32, dev)
     if ckpt is not None:
         _check_buffer("ckpt", ckpt, gradlev_delta_ckpt_bytes(*size), dev)
     ws = _workspace(gradlev_delta_workspace_bytes(*size, 0), dev, workspace)
-    with torch.cuda.device(dev):  # launches go to the tensors' device
-        st = lib().gradlev_delta_fwd(*size, _ptr(q), _ptr(k), _ptr(v), _ptr(beta),
-                                     _ptr(log_alpha), scale, _ptr(S0), _ptr(y), _ptr(ST),
-                                     _ptr(ckpt), _ptr(ws), ws.numel() * ws.element_size(),
-                                     _stream_ptr(stream, dev))
+    with _on(dev):
+        st = lib().gradlev_delta_fwd(*size, _addr(q), _addr(k), _addr(v), _addr(beta),
+                                     _addr(log_alpha), scale, _addr(S0), _addr(y), _addr(ST),
+                                     _addr(ckpt), _addr(ws), ws.numel() * ws.element_size(),
+                                     _stream_of(stream, dev))
     _check(st, "gradlev_delta_fwd")
     return y, ST
 
@@ -580,11 +613,11 @@ def gradlev_delta_bwd(q, k, v, beta, log_alpha, dy, S0=None, dST=None, *, scale=
     size, dev, dt, scale = _delta_args(q, k, v, beta, log_alpha, scale)
     B, H, _, T, d_k, d_v, _ = size
     _check(gradlev_delta_supported(*size), "gradlev_delta_bwd")
-    _check_tensor("dy", dy, (B, H, T, d_v), dt, dev)
+    _check_fast("dy", dy, (B, H, T, d_v), dt, dev)
     if S0 is not None:
-        _check_tensor("S0", S0, (B, H, d_v, d_k), torch.float32, dev)
+        _check_fast("S0", S0, (B, H, d_v, d_k), torch.float32, dev)
     if dST is not None:
-        _check_tensor("dST", dST, (B, H, d_v, d_k), dt, dev)
+        _check_fast("dST", dST, (B, H, d_v, d_k), dt, dev)
     if out is None:
         out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
                    dbeta=torch.empty((B, H, T), dtype=dt, device=dev),
@@ -593,16 +626,16 @@ def gradlev_delta_bwd(q, k, v, beta, log_alpha, dy, S0=None, dST=None, *, scale=
     _check_out(out, dict(dq=(q.shape, dt), dk=(k.shape, dt), dv=(v.shape, dt),
                          dbeta=((B, H, T), dt), dlog_alpha=((B, H, T), dt)), dev)
     if out.get("dS0") is not None:
-        _check_tensor("out['dS0']", out["dS0"], (B, H, d_v, d_k), dt, dev)
+        _check_fast("out['dS0']", out["dS0"], (B, H, d_v, d_k), dt, dev)
     if ckpt is not None:
         _check_buffer("ckpt", ckpt, gradlev_delta_ckpt_bytes(*size), dev)
     ws = _workspace(gradlev_delta_workspace_bytes(*size, 1), dev, workspace)
-    with torch.cuda.device(dev):  # launches go to the tensors' device
+    with _on(dev):
         st = lib().gradlev_delta_bwd(
-            *size, _ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(log_alpha), scale, _ptr(S0),
-            _ptr(dy), _ptr(dST), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
-            _ptr(out["dbeta"]), _ptr(out["dlog_alpha"]), _ptr(out.get("dS0")), _ptr(ckpt),
-            _ptr(ws), ws.numel() * ws.element_size(), _stream_ptr(stream, dev))
+            *size, _addr(q), _addr(k), _addr(v), _addr(beta), _addr(log_alpha), scale, _addr(S0),
+            _addr(dy), _addr(dST), _addr(out["dq"]), _addr(out["dk"]), _addr(out["dv"]),
+            _addr(out["dbeta"]), _addr(out["dlog_alpha"]), _addr(out.get("dS0")), _addr(ckpt),
+            _addr(ws), ws.numel() * ws.element_size(), _stream_of(stream, dev))
     _check(st, "gradlev_delta_bwd")
     return out
 
@@ -618,16 +651,16 @@ def gradlev_delta_step(q, k, v, beta, log_alpha, S, *, slots=None, scale=None, y
     B, H, _, T, d_k, d_v, _ = size
     if S.dim() != 4:
         raise GradlevError("S must be a [pool,H,d_v,d_k] tensor")
-    _check_tensor("S", S, (S.shape[0], H, d_v, d_k), torch.float32, dev)
+    _check_fast("S", S, (S.shape[0], H, d_v, d_k), torch.float32, dev)
     if slots is not None:
-        _check_tensor("slots", slots, (B,), torch.int32, dev)
+        _check_fast("slots", slots, (B,), torch.int32, dev)
     if y is None:
         y = torch.empty((B, H, T, d_v), dtype=dt, device=dev)
-    _check_tensor("y", y, (B, H, T, d_v), dt, dev)
-    with torch.cuda.device(dev):  # launches go to the tensors' device
-        st = lib().gradlev_delta_step(*size, _ptr(q), _ptr(k), _ptr(v), _ptr(beta),
-                                      _ptr(log_alpha), scale, _ptr(slots), S.shape[0], _ptr(S),
-                                      _ptr(y), _stream_ptr(stream, dev))
+    _check_fast("y", y, (B, H, T, d_v), dt, dev)
+    with _on(dev):
+        st = lib().gradlev_delta_step(*size, _addr(q), _addr(k), _addr(v), _addr(beta),
+                                      _addr(log_alpha), scale, _addr(slots), S.shape[0], _addr(S),
+                                      _addr(y), _stream_of(stream, dev))
     _check(st, "gradlev_delta_step")
     return y
 
@@ -649,8 +682,13 @@ def _strided(name, t, shape, dtype, device):
         raise GradlevError(f"{name}: device {t.device} != {device}")
     if t.stride(3) != 1 and t.shape[3] != 1:
         raise GradlevError(f"{name}: columns must be contiguous")
-    # the stride of an axis of length 1 is never used
-    return (ctypes.c_longlong * 3)(*[t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)])
+    return _c_strides(t.stride(), t.shape)
+
+
+@functools.lru_cache(maxsize=256)
+def _c_strides(stride, shape):
+    """Strides of the first three axes as a C array; that of an axis of length 1 is unused."""
+    return (ctypes.c_longlong * 3)(*[stride[i] if shape[i] > 1 else 0 for i in range(3)])
 
 
 def _norm_args(q, k, wq, wk, pos, inv_freq, norm):
@@ -666,13 +704,13 @@ def _norm_args(q, k, wq, wk, pos, inv_freq, norm):
     sk = _strided("k", k, (B, T, Hk, d), dt, dev)
     for n, w in (("wq", wq), ("wk", wk)):
         if w is not None:
-            _check_tensor(n, w, (d,), torch.float32, dev)
+            _check_fast(n, w, (d,), torch.float32, dev)
     if pos is not None:
-        _check_tensor("pos", pos, (B, T), torch.int32, dev)
+        _check_fast("pos", pos, (B, T), torch.int32, dev)
     rot = 0
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
-        _check_tensor("inv_freq", inv_freq, (rot // 2,), torch.float32, dev)
+        _check_fast("inv_freq", inv_freq, (rot // 2,), torch.float32, dev)
     return (B, T, Hq, Hk, d, rot, _dt_code(dt), _NORMS[norm]), dev, dt, sq, sk
 
 
@@ -689,12 +727,12 @@ def gradlev_qk_norm_rope_fwd(q, k, wq=None, wk=None, pos=None, inv_freq=None, *,
         yq = torch.empty((B, Hq, T, d), dtype=dt, device=dev)
     if yk is None:
         yk = torch.empty((B, Hk, T, d), dtype=dt, device=dev)
-    _check_tensor("yq", yq, (B, Hq, T, d), dt, dev)
-    _check_tensor("yk", yk, (B, Hk, T, d), dt, dev)
-    with torch.cuda.device(dev):  # launches go to the tensors' device
-        st = lib().gradlev_qk_norm_rope_fwd(*a, float(eps), _ptr(q), sq, _ptr(k), sk, _ptr(wq),
-                                            _ptr(wk), _ptr(pos), _ptr(inv_freq), _ptr(yq),
-                                            _ptr(yk), _stream_ptr(stream, dev))
+    _check_fast("yq", yq, (B, Hq, T, d), dt, dev)
+    _check_fast("yk", yk, (B, Hk, T, d), dt, dev)
+    with _on(dev):
+        st = lib().gradlev_qk_norm_rope_fwd(*a, float(eps), _addr(q), sq, _addr(k), sk, _addr(wq),
+                                            _addr(wk), _addr(pos), _addr(inv_freq), _addr(yq),
+                                            _addr(yk), _stream_of(stream, dev))
     _check(st, "gradlev_qk_norm_rope_fwd")
     return yq, yk
 
@@ -707,8 +745,8 @@ def gradlev_qk_norm_rope_bwd(dyq, dyk, q, k, wq=None, wk=None, pos=None, inv_fre
     import torch
     a, dev, dt, sq, sk = _norm_args(q, k, wq, wk, pos, inv_freq, norm)
     B, T, Hq, Hk, d = a[:5]
-    _check_tensor("dyq", dyq, (B, Hq, T, d), dt, dev)
-    _check_tensor("dyk", dyk, (B, Hk, T, d), dt, dev)
+    _check_fast("dyq", dyq, (B, Hq, T, d), dt, dev)
+    _check_fast("dyk", dyk, (B, Hk, T, d), dt, dev)
     f32 = torch.float32
     if out is None:
         out = dict(dq=torch.empty((B, T, Hq, d), dtype=dt, device=dev),
@@ -723,13 +761,13 @@ def gradlev_qk_norm_rope_bwd(dyq, dyk, q, k, wq=None, wk=None, pos=None, inv_fre
     _check_out(out, {n: ((d,), f32) for n, w in (("dwq", wq), ("dwk", wk)) if w is not None}, dev)
     nws = gradlev_qk_norm_rope_workspace_bytes(B, T, Hq, Hk, d, a[6])
     ws = _workspace(nws, dev, workspace) if wq is not None or wk is not None else None
-    with torch.cuda.device(dev):  # launches go to the tensors' device
+    with _on(dev):
         st = lib().gradlev_qk_norm_rope_bwd(
-            *a, float(eps), _ptr(dyq), _ptr(dyk), _ptr(q), sq, _ptr(k), sk, _ptr(wq), _ptr(wk),
-            _ptr(pos), _ptr(inv_freq), _ptr(out["dq"]), sdq, _ptr(out["dk"]), sdk,
-            _ptr(out["dwq"] if wq is not None else None),
-            _ptr(out["dwk"] if wk is not None else None), _ptr(ws),
-            ws.numel() * ws.element_size() if ws is not None else 0, _stream_ptr(stream, dev))
+            *a, float(eps), _addr(dyq), _addr(dyk), _addr(q), sq, _addr(k), sk, _addr(wq), _addr(wk),
+            _addr(pos), _addr(inv_freq), _addr(out["dq"]), sdq, _addr(out["dk"]), sdk,
+            _addr(out["dwq"] if wq is not None else None),
+            _addr(out["dwk"] if wk is not None else None), _addr(ws),
+            ws.numel() * ws.element_size() if ws is not None else 0, _stream_of(stream, dev))
     _check(st, "gradlev_qk_norm_rope_bwd")
     return out
 

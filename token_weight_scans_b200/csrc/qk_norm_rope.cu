@@ -7,13 +7,20 @@
 // Backward, with g the turned-back gradient (the transpose of the turn):
 //   dw = sum over rows of g z,   dx = r (g w - z (sum g w z) / n).
 //
-// Bound by memory: x (and dy) read once, y (dx) written once. A lane holds 8 consecutive
-// columns (a 16-byte load of bf16), so a row of d columns takes the next power of two of
-// d / 8 lanes, and rot a multiple of 16 puts a pair's partner into the same place of
-// another lane of the row. The angles of a token are the same for all of its heads: a
-// warp takes one token's rows in turn and computes them once. They are formed in double
-// and reduced to a fraction of a turn there; a float32 product would be off by whole
-// radians at far positions.
+// Bound by memory: x (and dy) read once, y (dx) written once. A lane holds 8 columns of a
+// row, 4 in each of two places that the rotation pairs up (i and i + rot / 2; past the
+// rotated columns simply 8 in a row), so that the turn needs no exchange between lanes and
+// a lane only forms 4 angles. A row takes the next power of two of d / 8 lanes. The angles
+// of a token are the same for all of its heads: a warp takes one token's rows in turn and
+// computes them once.
+//
+// Angles: pos * inv_freq is off by whole radians in float32 at far positions. Only the
+// fraction of a turn matters, so inv_freq / 2 pi goes into a 64-bit binary fraction F once
+// per lane, and pos * F modulo 2^64 is that fraction, exact up to F's own rounding.
+//
+// What the bandwidth needs is loads in flight: 8 rows of bf16 per lane group (kept as
+// loaded) at 16 warps per SM move 537 MB (B8 T4096, 16 + 16 heads of 128) in 110 us;
+// 4 rows at 24 warps took 128 us, and 4 unpacked rows at 20 warps 218 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -28,8 +35,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int V = 8;           // columns per lane
-constexpr int U = 4;           // rows of a lane group in flight
-constexpr int kBwdCtas = 148 * 4;  // fixed: the weights' gradients add up in a fixed order
+constexpr int kFwdCtas = 148 * 8, kBwdCtas = 148 * 4;  // the latter fixed: the weights'
+                               // gradients add up in a fixed order
 
 struct Rows {                  // queries or keys
   const void* x;               // [B,T,H,d] by strides (elements)
@@ -51,35 +58,44 @@ struct NormArgs {
   float* part;                 // [kBwdCtas][2][d]: the weights' gradients, or null
 };
 
-struct F8 { float v[V]; };
+struct F8 { float v[V]; };   // columns [ca, ca + 4), [cb, cb + 4)
 
-__device__ __forceinline__ F8 load8(const __nv_bfloat16* p) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t a[4] = {u.x, u.y, u.z, u.w};
-  F8 f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f.v[2 * i] = __uint_as_float(a[i] << 16);
-    f.v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+// A lane's columns of a row as loaded: rows in flight cost half the registers that way.
+template <typename Tio> struct Raw;
+template <> struct Raw<__nv_bfloat16> {
+  uint2 a, b;
+  __device__ __forceinline__ void load(const __nv_bfloat16* pa, const __nv_bfloat16* pb) {
+    a = __ldg(reinterpret_cast<const uint2*>(pa));
+    b = __ldg(reinterpret_cast<const uint2*>(pb));
   }
-  return f;
-}
-__device__ __forceinline__ F8 load8(const float* p) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  return F8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const F8& f) {
-  uint32_t a[4];
+  __device__ __forceinline__ void zero() { a = b = make_uint2(0u, 0u); }
+  __device__ __forceinline__ F8 get() const {
+    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+    F8 f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f.v[2 * i], f.v[2 * i + 1]);
-    a[i] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int i = 0; i < 4; ++i) {
+      f.v[2 * i] = __uint_as_float(w[i] << 16);
+      f.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+    return f;
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(a[0], a[1], a[2], a[3]);
+};
+template <> struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* pa, const float* pb) {
+    a = __ldg(reinterpret_cast<const float4*>(pa));
+    b = __ldg(reinterpret_cast<const float4*>(pb));
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ F8 get() const { return F8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}}; }
+};
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                            *reinterpret_cast<const uint32_t*>(&b));
 }
-__device__ __forceinline__ void store8(float* p, const F8& f) {
-  *reinterpret_cast<float4*>(p) = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(f.v[4], f.v[5], f.v[6], f.v[7]);
+__device__ __forceinline__ void store4(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
 template <int G>
@@ -89,168 +105,213 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// The turn of this lane's 8 columns: out = c u + s u_partner (forward sign of s; the
-// transpose uses -s). c = 1 and s = 0 outside the rotated columns.
-struct Turn {
-  float c[V], s[V];
-  int partner;   // lane within the group
+// Where this lane's columns are, and the binary fractions of its 4 angles (zero outside the
+// rotated columns, which leaves them as they are).
+struct Lane {
+  int ca, cb;
+  bool in, turns;
+  unsigned long long F[4];
 };
 
-__device__ __forceinline__ Turn make_turn(const NormArgs& a, int gl, size_t bt, int t) {
-  Turn u;
-  const int c0 = V * gl;
-  u.partner = gl;
+__device__ __forceinline__ Lane make_lane(const NormArgs& a, int gl) {
+  Lane l;
+  l.in = V * gl < a.d;
+  l.turns = 4 * gl < a.half;
+  l.ca = l.turns ? 4 * gl : V * gl;
+  l.cb = l.turns ? a.half + 4 * gl : V * gl + 4;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    l.F[i] = 0;
+    if (l.turns) {
+      double f = (double)a.inv_freq[l.ca + i] * 0.15915494309189533577;  // / 2 pi
+      f -= floor(f);
+      l.F[i] = f < 1.0 ? (unsigned long long)(f * 18446744073709551616.0) : 0ull;
+    }
+  }
+  return l;
+}
+
+struct Turn { float c[4], s[4]; };
+
+__device__ __forceinline__ Turn make_turn(const NormArgs& a, const Lane& l, size_t bt, int t) {
+  Turn u;
+  const long long pos = a.pos ? a.pos[bt] : t;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // the top 32 bits, signed: half turns times 2^31
+    const int hi = (int)(((unsigned long long)pos * l.F[i]) >> 32);
     u.c[i] = 1.f;
     u.s[i] = 0.f;
-  }
-  if (c0 < 2 * a.half) {
-    const bool lo = c0 < a.half;
-    const int i0 = lo ? c0 : c0 - a.half;
-    u.partner = lo ? gl + a.half / V : gl - a.half / V;
-    const double pos = a.pos ? (double)a.pos[bt] : (double)t;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      double turns = pos * (double)a.inv_freq[i0 + i] * 0.15915494309189533577;  // / 2 pi
-      turns -= rint(turns);
-      float s, c;
-      sincospif((float)(2.0 * turns), &s, &c);
-      u.c[i] = c;
-      u.s[i] = lo ? -s : s;
-    }
+    if (l.turns) sincospif((float)hi * 0x1p-31f, &u.s[i], &u.c[i]);
   }
   return u;
 }
 
-template <int G>
-__device__ __forceinline__ F8 apply_turn(const Turn& u, const F8& x, int gbase, float sign) {
-  F8 y;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const float p = __shfl_sync(0xffffffffu, x.v[i], gbase + u.partner);
-    y.v[i] = fmaf(u.c[i], x.v[i], sign * u.s[i] * p);
-  }
-  return y;
-}
-
-__device__ __forceinline__ F8 weights(const float* w, int c0, int d) {
+__device__ __forceinline__ F8 weights(const float* w, const Lane& l) {
   F8 f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) f.v[i] = w && c0 < d ? w[c0 + i] : 1.f;
+  for (int i = 0; i < 4; ++i) {
+    f.v[i] = w && l.in ? w[l.ca + i] : 1.f;
+    f.v[4 + i] = w && l.in ? w[l.cb + i] : 1.f;
+  }
   return f;
 }
 
+template <typename Tio>
+__device__ __forceinline__ Raw<Tio> load_row(const Tio* p, const Lane& l, bool ok) {
+  Raw<Tio> x;
+  x.zero();
+  if (ok) x.load(p + l.ca, p + l.cb);
+  return x;
+}
+template <typename Tio>
+__device__ __forceinline__ void store_row(Tio* p, const Lane& l, const F8& x) {
+  store4(p + l.ca, x.v);
+  store4(p + l.cb, x.v + 4);
+}
+
 // ------------------------------------------------------------------ forward
-// A warp takes `items`-th parts of a token's rows (queries, then keys).
+// A warp takes `items`-th parts of a token's rows (queries, then keys), U rows of each lane
+// group in flight. The weights ride on the turn: 16 products per token and list instead of
+// 8 per row.
 template <typename Tio, int G>
-__global__ void __launch_bounds__(kThreads) fwd_kernel(NormArgs a) {
-  constexpr int R = 32 / G;  // rows a warp takes at a time
-  const int lane = threadIdx.x & 31, gl = lane % G, gbase = lane - gl, c0 = V * gl;
-  const size_t id = (size_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const size_t bt = id / a.items;
-  if (bt >= (size_t)a.B * a.T) return;
-  const int item = id - bt * a.items;
-  const int b = bt / a.T, t = bt - (size_t)b * a.T;
+__global__ void __launch_bounds__(kThreads, 4) fwd_kernel(NormArgs a) {
+  // rows a warp takes at a time, and how many of those are in flight
+  constexpr int R = 32 / G, U = sizeof(Tio) == 2 ? 8 : 4;
+  const int lane = threadIdx.x & 31;
+  const Lane l = make_lane(a, lane % G);
   const int rows = a.r[0].H + a.r[1].H;
   const int per = (rows + a.items - 1) / a.items;
-  const int lo = item * per, hi = min(rows, lo + per);
-  const Turn turn = make_turn(a, gl, bt, t);
-  const F8 w0 = weights(a.r[0].w, c0, a.d), w1 = weights(a.r[1].w, c0, a.d);
-  const bool in = c0 < a.d;
-  for (int base = lo; base < hi; base += R * U) {
-    F8 x[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int row = base + u * R + lane / G;
-      const int which = row >= a.r[0].H;
+  const size_t work = (size_t)a.B * a.T * a.items;
+  for (size_t id = (size_t)blockIdx.x * kWarps + (threadIdx.x >> 5); id < work;
+       id += (size_t)gridDim.x * kWarps) {
+    const size_t bt = id / a.items;
+    const int item = id - bt * a.items;
+    const int b = bt / a.T, t = bt - (size_t)b * a.T;
+    const Turn turn = make_turn(a, l, bt, t);
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
       const Rows& r = a.r[which];
-      const int h = row - (which ? a.r[0].H : 0);
-      if (in && row < hi)
-        x[u] = load8(static_cast<const Tio*>(r.x) + b * r.sb + t * r.st + h * r.sh + c0);
-      else
-        x[u] = F8{};
-    }
+      const int first = which ? a.r[0].H : 0;
+      const int lo = max(item * per - first, 0), hi = min((item + 1) * per - first, r.H);
+      if (lo >= hi) continue;
+      const F8 w = weights(r.w, l);
+      const Tio* x0 = static_cast<const Tio*>(r.x) + b * r.sb + t * r.st;
+      Tio* y0 = static_cast<Tio*>(r.y) + ((size_t)b * r.H * a.T + t) * a.d;
+      const size_t yh = (size_t)a.T * a.d;
+      for (int base = lo; base < hi; base += R * U) {
+        Raw<Tio> raw[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int row = base + u * R + lane / G;
-      const int which = row >= a.r[0].H;
-      const int h = row - (which ? a.r[0].H : 0);
-      float ss = 0.f;
+        for (int u = 0; u < U; ++u) {
+          const int h = base + u * R + lane / G;
+          raw[u] = load_row(x0 + h * r.sh, l, l.in && h < hi);
+        }
 #pragma unroll
-      for (int i = 0; i < V; ++i) ss = fmaf(x[u].v[i], x[u].v[i], ss);
-      const float rs = 1.f / sqrtf(fmaf(group_sum<G>(ss), a.inv_n, a.eps));
+        for (int u = 0; u < U; ++u) {
+          const int h = base + u * R + lane / G;
+          const F8 x = raw[u].get();
+          float ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) x[u].v[i] *= rs * (which ? w1.v[i] : w0.v[i]);
-      const F8 y = apply_turn<G>(turn, x[u], gbase, 1.f);
-      if (in && row < hi)
-        store8(static_cast<Tio*>(a.r[which].y) + (((size_t)b * a.r[which].H + h) * a.T + t) * a.d + c0, y);
+          for (int i = 0; i < V; ++i) ss = fmaf(x.v[i], x.v[i], ss);
+          const float rs = rsqrtf(fmaf(group_sum<G>(ss), a.inv_n, a.eps));
+          F8 y;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p = x.v[i] * rs, q = x.v[4 + i] * rs;
+            y.v[i] = fmaf(turn.c[i] * w.v[i], p, -(turn.s[i] * w.v[4 + i]) * q);
+            y.v[4 + i] = fmaf(turn.c[i] * w.v[4 + i], q, turn.s[i] * w.v[i] * p);
+          }
+          if (l.in && h < hi) store_row(y0 + h * yh, l, y);
+        }
+      }
     }
   }
 }
 
 // ------------------------------------------------------------------ backward
 // kBwdCtas CTAs walk the tokens with a fixed stride; each lane adds up the weights'
-// gradients of its columns and each CTA leaves one partial per weight.
+// gradients of its columns and each CTA leaves one partial per weight. Both sums of a row
+// are taken over x as it is, in one round of exchanges:
+//   sum g w z = r sum g w x.
 template <typename Tio, int G>
-__global__ void __launch_bounds__(kThreads) bwd_kernel(NormArgs a) {
-  constexpr int R = 32 / G;
-  __shared__ float acc[2][kWarps][32 / G][G * V];
+__global__ void __launch_bounds__(kThreads, 4) bwd_kernel(NormArgs a) {
+  constexpr int R = 32 / G, U = sizeof(Tio) == 2 ? 4 : 2;
+  __shared__ float acc[2][kWarps][R][G * V];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gl = lane % G, gbase = lane - gl, c0 = V * gl;
-  const bool in = c0 < a.d;
-  const int rows = a.r[0].H + a.r[1].H;
-  F8 dw0{}, dw1{};
+  const Lane l = make_lane(a, lane % G);
   const size_t tokens = (size_t)a.B * a.T;
-  for (size_t bt = (size_t)blockIdx.x * kWarps + warp; bt < tokens; bt += (size_t)gridDim.x * kWarps) {
-    const int b = bt / a.T, t = bt - (size_t)b * a.T;
-    const Turn turn = make_turn(a, gl, bt, t);
-    for (int base = 0; base < rows; base += R) {
-      const int row = base + lane / G;
-      const int which = row >= a.r[0].H;
-      const Rows& r = a.r[which];
-      const int h = row - (which ? a.r[0].H : 0);
-      const bool ok = in && row < rows;
-      F8 x{}, g{};
-      if (ok) {
-        x = load8(static_cast<const Tio*>(r.x) + b * r.sb + t * r.st + h * r.sh + c0);
-        g = load8(static_cast<const Tio*>(r.dy) + (((size_t)b * r.H + h) * a.T + t) * a.d + c0);
-      }
-      g = apply_turn<G>(turn, g, gbase, -1.f);
-      float ss = 0.f;
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const Rows& r = a.r[which];
+    const F8 w = weights(r.w, l);
+    F8 dw{};
+    for (size_t bt = (size_t)blockIdx.x * kWarps + warp; bt < tokens;
+         bt += (size_t)gridDim.x * kWarps) {
+      const int b = bt / a.T, t = bt - (size_t)b * a.T;
+      const Turn turn = make_turn(a, l, bt, t);
+      const Tio* x0 = static_cast<const Tio*>(r.x) + b * r.sb + t * r.st;
+      const Tio* g0 = static_cast<const Tio*>(r.dy) + ((size_t)b * r.H * a.T + t) * a.d;
+      Tio* d0 = static_cast<Tio*>(r.dx) + b * r.db + t * r.dt;
+      const size_t gh = (size_t)a.T * a.d;
+      for (int base = 0; base < r.H; base += R * U) {
+        Raw<Tio> xs[U], gs[U];
 #pragma unroll
-      for (int i = 0; i < V; ++i) ss = fmaf(x.v[i], x.v[i], ss);
-      const float rs = 1.f / sqrtf(fmaf(group_sum<G>(ss), a.inv_n, a.eps));
-      float dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        x.v[i] *= rs;  // z
-        const float gz = g.v[i] * x.v[i];
-        if (row < rows) {
-          dw0.v[i] += which ? 0.f : gz;
-          dw1.v[i] += which ? gz : 0.f;
+        for (int u = 0; u < U; ++u) {
+          const int h = base + u * R + lane / G;
+          const bool ok = l.in && h < r.H;
+          xs[u] = load_row(x0 + h * r.sh, l, ok);
+          gs[u] = load_row(g0 + h * gh, l, ok);
         }
-        if (r.w && ok) g.v[i] *= r.w[c0 + i];
-        dot = fmaf(g.v[i], x.v[i], dot);
-      }
-      dot = group_sum<G>(dot) * a.inv_n;
 #pragma unroll
-      for (int i = 0; i < V; ++i) g.v[i] = rs * fmaf(-dot, x.v[i], g.v[i]);
-      if (ok) store8(static_cast<Tio*>(r.dx) + b * r.db + t * r.dt + h * r.dh + c0, g);
+        for (int u = 0; u < U; ++u) {
+          const int h = base + u * R + lane / G;
+          const F8 x = xs[u].get(), gy = gs[u].get();
+          F8 g;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // turned back
+            g.v[i] = fmaf(turn.c[i], gy.v[i], turn.s[i] * gy.v[4 + i]);
+            g.v[4 + i] = fmaf(turn.c[i], gy.v[4 + i], -turn.s[i] * gy.v[i]);
+          }
+          float ss = 0.f, gx = 0.f;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            ss = fmaf(x.v[i], x.v[i], ss);
+            gx = fmaf(g.v[i] * w.v[i], x.v[i], gx);
+          }
+#pragma unroll
+          for (int o = G / 2; o > 0; o >>= 1) {
+            ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            gx += __shfl_xor_sync(0xffffffffu, gx, o);
+          }
+          const float rs = rsqrtf(fmaf(ss, a.inv_n, a.eps));
+          const bool ok = l.in && h < r.H;
+          const float m = -gx * rs * rs * a.inv_n;  // dx = r (g w + m x)
+          const float rz = ok ? rs : 0.f;           // a row past the end may have r = inf
+          F8 y;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            dw.v[i] = fmaf(g.v[i] * rz, x.v[i], dw.v[i]);
+            y.v[i] = rs * fmaf(m, x.v[i], g.v[i] * w.v[i]);
+          }
+          if (ok) store_row(d0 + h * r.dh, l, y);
+        }
+      }
+    }
+    if (a.part && l.in) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[which][warp][lane / G][l.ca + i] = dw.v[i];
+        acc[which][warp][lane / G][l.cb + i] = dw.v[4 + i];
+      }
     }
   }
   if (!a.part) return;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    acc[0][warp][lane / G][c0 + i] = dw0.v[i];
-    acc[1][warp][lane / G][c0 + i] = dw1.v[i];
-  }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * a.d; i += kThreads) {
     const int which = i / a.d, c = i - which * a.d;
     float s = 0.f;
     for (int w = 0; w < kWarps; ++w)
-      for (int g = 0; g < 32 / G; ++g) s += acc[which][w][g][c];
+      for (int g = 0; g < R; ++g) s += acc[which][w][g][c];
     a.part[(size_t)blockIdx.x * 2 * a.d + i] = s;
   }
 }
@@ -277,8 +338,8 @@ cudaError_t launch(NormArgs a, bool bwd, cudaStream_t st) {
     const int rows = a.r[0].H + a.r[1].H, most = (rows + 32 / G - 1) / (32 / G);
     a.items = 1;
     while (a.items < most && tokens * a.items < 148 * 4 * 8) a.items *= 2;
-    const size_t warps = tokens * a.items;
-    fwd_kernel<Tio, G><<<(unsigned)((warps + kWarps - 1) / kWarps), kThreads, 0, st>>>(a);
+    const size_t ctas = (tokens * a.items + kWarps - 1) / kWarps;
+    fwd_kernel<Tio, G><<<(unsigned)(ctas < kFwdCtas ? ctas : kFwdCtas), kThreads, 0, st>>>(a);
   } else {
     bwd_kernel<Tio, G><<<kBwdCtas, kThreads, 0, st>>>(a);
   }
