@@ -12,6 +12,9 @@
 // beta = 0 leaves T0's column zero, but T's column j needs A's: columns are computed with
 // beta at least 2^-60 in size, and T_ij = beta_i T0_ij / beta_j recovers them; T0 itself is
 // off by 2^-60.
+//
+// Waits: the in-flight TMA stores only read shared memory, so the CTA waits for that read
+// and not for their completion; the kernel boundary orders them for the walk.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -28,25 +31,34 @@ using namespace sm100;
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int LD = 68;        // row stride (floats) of the 64 x 64 float32 matrices: 16-byte rows
 constexpr int LT = 36;        // and of the 32 x 32 temporary
 constexpr uint32_t COL_KQ = 0, COL_W = 64, kCols = 256;  // K K^T | Q K^T, then PT; W | Wb
+constexpr float kTiny = 0x1p-60f;
 
 struct PrepSmem {
-  uint8_t K[2 * TILE], Q[2 * TILE];      // k-blocks: 64 token rows x 128 B
-  uint8_t Tg[TILE], Tgl[TILE];           // T0 diag(G): bf16, and its remainder
-  uint8_t Tw[TILE], Tt[TILE], P[TILE];   // diag(w) T, T, P
-  float X[C * LD], N[C * LD];            // T0; A diag(beta)
+  uint8_t K[2 * TILE];         // k-blocks: 64 token rows x 128 B; at the end Wb
+  uint8_t Q[2 * TILE];         // then Tw = diag(w) T and Tt = T; at the end W
+  union {
+    float N[C * LD];           // A diag(beta)
+    uint8_t Tg[2][TILE];       // then T0 diag(G) in bf16 and its remainder; at the end Wlo
+  };
+  uint8_t P[TILE];
+  float X[C * LD];             // T0
   float tmp[32 * LT];
-  float Lh[C], Ll[C], be[C], G[C], w[C];
+  // per token: with m in the middle of the chunk M_ij = ra_i ca_j where that stays in range
+  // (fac); cN = ca beta (at least kTiny), cP = scale ca
+  float ra[C], cN[C], cP[C];
+  float Lh[C], Ll[C], be[C], G[C], w[C], rb[C];
   int seg[C];
+  int fac;
   uint64_t full, mma;
   uint32_t tmem_base;
   int abort;
 };
 constexpr size_t kSmem = sizeof(PrepSmem) + 1024;
-static_assert(2 * kSmem <= 227 * 1024, "two CTAs per SM");
+static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
 
 enum : uint32_t { W_PREP_LOAD = 0x801, W_PREP_MMA };
 
@@ -57,39 +69,29 @@ struct PrepParams {
   DeviceStatus* status;
   uint64_t timeout_ns;
   Mats m;
-  int split, back;   // remainders; Wb and PT
 };
 
 __device__ __forceinline__ uint32_t pack_lo(float a, float b, uint32_t hi) {
   return pack_bf16(a - bf16_lo(hi), b - bf16_hi(hi));
 }
-
-// D[r][c..c+7] (r = tid / 4 rows, 8 columns) = sum_m A[r][m] B[m][c], m < n
-__device__ __forceinline__ void row8(float (&s)[8], const float* A, const float* B, int ldb, int n) {
-#pragma unroll 4
-  for (int m = 0; m < n; ++m) {
-    const float a = A[m];
-    const float4 b0 = *reinterpret_cast<const float4*>(B + m * ldb);
-    const float4 b1 = *reinterpret_cast<const float4*>(B + m * ldb + 4);
-    s[0] = fmaf(a, b0.x, s[0]);
-    s[1] = fmaf(a, b0.y, s[1]);
-    s[2] = fmaf(a, b0.z, s[2]);
-    s[3] = fmaf(a, b0.w, s[3]);
-    s[4] = fmaf(a, b1.x, s[4]);
-    s[5] = fmaf(a, b1.y, s[5]);
-    s[6] = fmaf(a, b1.z, s[6]);
-    s[7] = fmaf(a, b1.w, s[7]);
-  }
+__device__ __forceinline__ float4 at4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ void axpy4(float (&s)[4], float a, const float4& x) {
+  s[0] = fmaf(a, x.x, s[0]);
+  s[1] = fmaf(a, x.y, s[1]);
+  s[2] = fmaf(a, x.z, s[2]);
+  s[3] = fmaf(a, x.w, s[3]);
 }
 
 }  // namespace
 
-__global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ CUtensorMap tmK,
-                                                        const __grid_constant__ CUtensorMap tmQ,
-                                                        const __grid_constant__ CUtensorMap tmW,
-                                                        const __grid_constant__ CUtensorMap tmWlo,
-                                                        const __grid_constant__ CUtensorMap tmWb,
-                                                        PrepParams p) {
+// SPLIT: the remainders of T0 and W; BACK: Wb and PT for the backward.
+template <bool SPLIT, bool BACK>
+__global__ void __launch_bounds__(kThreads, 2) prep_kernel(const __grid_constant__ CUtensorMap tmK,
+                                                           const __grid_constant__ CUtensorMap tmQ,
+                                                           const __grid_constant__ CUtensorMap tmW,
+                                                           const __grid_constant__ CUtensorMap tmWlo,
+                                                           const __grid_constant__ CUtensorMap tmWb,
+                                                           PrepParams p) {
   extern __shared__ uint8_t smem_raw[];
   PrepSmem& sm = *reinterpret_cast<PrepSmem*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -116,24 +118,35 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
   }
   if (warp == 2) {
     const GatePair g = chunk_gates(p.beta, p.log_alpha, (size_t)bh * p.d.T, t0, p.d.T);
+    const float Lm = __shfl_sync(0xffffffffu, g.Lh[0], 31), Ll = __shfl_sync(0xffffffffu, g.Ll[0], 31);
+    const bool fac = g.seg_end == 0 && g.Lend > -80.f;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int i = lane + 32 * k;
+      const float be = g.be[k], bt = fabsf(be) < kTiny ? kTiny : be;
+      const float x = (g.Lh[k] - Lm) + (g.Ll[k] - Ll);
+      const float ca = fac ? expf(-x) : 1.f;
+      sm.ra[i] = fac ? expf(x) : 1.f;
+      sm.cN[i] = ca * bt;
+      sm.cP[i] = ca * p.scale;
       sm.Lh[i] = g.Lh[k];
       sm.Ll[i] = g.Ll[k];
       sm.seg[i] = g.seg[k];
-      sm.be[i] = g.be[k];
+      sm.be[i] = be;
+      sm.rb[i] = 1.f / bt;
       sm.G[i] = gate_G(g, k);
       sm.w[i] = gate_w(g, k);
     }
+    if (lane == 0) sm.fac = fac;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tb = sm.tmem_base;
-  const uint32_t sK = smem_u32(sm.K), sQ = smem_u32(sm.Q);
-  mbar_wait(&sm.full, 0, wc, W_PREP_LOAD);
+  const uint32_t sK = smem_u32(sm.K), sQ = smem_u32(sm.Q), sTg = smem_u32(sm.Tg[0]);
+  const uint32_t sTw = sQ, sTt = sQ + TILE;
   if (tid == 0) {
+    mbar_wait(&sm.full, 0, wc, W_PREP_LOAD);
     const uint32_t id = idesc_bf16(64, 64, false, false);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {
@@ -148,156 +161,185 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
   mbar_wait(&sm.mma, 0, wc, W_PREP_MMA);
   __syncwarp();
   tc_fence_after();
-  // Lane l < 16 of warp q holds row i = 16 q + l of K K^T, lane l + 16 that of Q K^T.
-  const int i = 16 * warp + (lane & 15);
+  // Lane l < 16 of quadrant q holds row i = 16 q + l of K K^T, lane l + 16 that of Q K^T;
+  // warps q and q + 4 take half of the columns each.
+  const int q = warp & 3, hh = warp >> 2;
+  const uint32_t lo = (uint32_t)(32 * q) << 16;
+  const int i = 16 * q + (lane & 15);
   const bool isP = lane >= 16;
   {
-    const float Lh = sm.Lh[i], Ll = sm.Ll[i];
-    const int seg = sm.seg[i];
-    bf16* Pg = p.m.Pb + (((size_t)bh * N + n) * C + i) * C;
+    float v[32];
+    tmem_ld32(tb + COL_KQ + lo + 32 * hh, v);
+    tmem_ld_wait();
+    // the entries below (P: and on) the diagonal
+    const int keep = i - 32 * hh + (isP ? 1 : 0);
+    if (sm.fac) {
+      const float ra = sm.ra[i];
+      const float* cv = (isP ? sm.cP : sm.cN) + 32 * hh;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float v[32];
-      tmem_ld32(tb + COL_KQ + ((uint32_t)(32 * warp) << 16) + 32 * half, v);
-      tmem_ld_wait();
-      uint32_t pp[16], pb[16];
-#pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        float x[2], xb[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int j = 32 * half + e + u;
-          const bool on = (isP ? j <= i : j < i) && sm.seg[j] == seg;
-          float be = sm.be[j];
-          x[u] = on ? v[e + u] * expf((Lh - sm.Lh[j]) + (Ll - sm.Ll[j])) : 0.f;
-          if (isP) {
-            x[u] *= p.scale;
-          } else {
-            be = fabsf(be) < 0x1p-60f ? 0x1p-60f : be;
-          }
-          xb[u] = x[u] * be;
-        }
-        if (!isP) {
-          *reinterpret_cast<float2*>(sm.N + i * LD + 32 * half + e) = make_float2(xb[0], xb[1]);
-        }
-        pp[e >> 1] = pack_bf16(x[0], x[1]);
-        pb[e >> 1] = pack_bf16(xb[0], xb[1]);
+      for (int e = 0; e < 32; e += 4) {
+        const float4 c = at4(cv + e);
+        v[e] = e < keep ? v[e] * (ra * c.x) : 0.f;
+        v[e + 1] = e + 1 < keep ? v[e + 1] * (ra * c.y) : 0.f;
+        v[e + 2] = e + 2 < keep ? v[e + 2] * (ra * c.z) : 0.f;
+        v[e + 3] = e + 3 < keep ? v[e + 3] * (ra * c.w) : 0.f;
       }
-      if (isP) {
+    } else {  // a reset, or decays whose factors leave float32
+      const float Lh = sm.Lh[i], Ll = sm.Ll[i];
+      const int seg = sm.seg[i];
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          reinterpret_cast<uint4*>(Pg)[4 * half + cc] =
-              make_uint4(pb[4 * cc], pb[4 * cc + 1], pb[4 * cc + 2], pb[4 * cc + 3]);
-          if (p.back)
-            st_shared_v4(smem_u32(sm.P) + sw128_off(i, 4 * half + cc), pp[4 * cc], pp[4 * cc + 1],
-                         pp[4 * cc + 2], pp[4 * cc + 3]);
-        }
+      for (int e = 0; e < 32; ++e) {
+        const int j = 32 * hh + e;
+        const float m = (isP ? sm.cP : sm.cN)[j] * expf(fminf((Lh - sm.Lh[j]) + (Ll - sm.Ll[j]), 0.f));
+        v[e] = e < keep && sm.seg[j] == seg ? v[e] * m : 0.f;
       }
-      __syncwarp();  // the next load is warp-collective
+    }
+    if (!isP) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 4)
+        *reinterpret_cast<float4*>(sm.N + i * LD + 32 * hh + e) =
+            make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+    } else {
+      uint4* Pg = reinterpret_cast<uint4*>(p.m.Pb + (((size_t)bh * N + n) * C + i) * C + 32 * hh);
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+        const float* x = v + 8 * cc;
+        if (BACK)
+          st_shared_v4(smem_u32(sm.P) + sw128_off(i, 4 * hh + cc), pack_bf16(x[0], x[1]),
+                       pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        const float4 b0 = at4(sm.be + 32 * hh + 8 * cc), b1 = at4(sm.be + 32 * hh + 8 * cc + 4);
+        Pg[cc] = make_uint4(pack_bf16(x[0] * b0.x, x[1] * b0.y), pack_bf16(x[2] * b0.z, x[3] * b0.w),
+                            pack_bf16(x[4] * b1.x, x[5] * b1.y), pack_bf16(x[6] * b1.z, x[7] * b1.w));
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
-  // ---- T0: 16 x 16 diagonal blocks, a lane per column
-  {
+  // ---- T0: 16 x 16 diagonal blocks, a lane per column; the other warps clear what is right
+  //      of them
+  if (warp < 4) {
     const int o = 16 * warp, c = lane & 15;
     float x[16];
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       float s = r == c ? 1.f : 0.f;
+      const float* Nr = sm.N + (o + r) * LD + o;
 #pragma unroll
-      for (int m = 0; m < r; ++m) s = fmaf(-sm.N[(o + r) * LD + o + m], x[m], s);
+      for (int m = 0; m < r; m += 4) {
+        const float4 a = at4(Nr + m);
+        s = fmaf(-a.x, x[m], s);
+        if (m + 1 < r) s = fmaf(-a.y, x[m + 1], s);
+        if (m + 2 < r) s = fmaf(-a.z, x[m + 2], s);
+        if (m + 3 < r) s = fmaf(-a.w, x[m + 3], s);
+      }
       x[r] = s;
     }
     if (lane < 16) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) sm.X[(o + r) * LD + o + c] = x[r];
-    } else {  // the blocks to the right of the diagonal
-      for (int r = 0; r < 16; ++r)
-        for (int cc = o + 16 + c; cc < C; cc += 16) sm.X[(o + r) * LD + cc] = 0.f;
     }
+  } else {
+    const int r = (tid - 128) >> 1, c1 = 32 * (tid & 1);  // row r, 32 columns
+    for (int c = max(c1, (r & ~15) + 16); c < c1 + 32; c += 4)
+      *reinterpret_cast<float4*>(sm.X + r * LD + c) = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   __syncthreads();
-  // ---- 16 -> 32: two pairs of blocks, 64 threads each: row r, 4 columns
+  // ---- 16 -> 32: two pairs of blocks, 128 threads each: row r, 2 columns
   {
-    const int pr = tid >> 6, r = (tid & 63) >> 2, c = 4 * (tid & 3), o = 32 * pr;
+    const int pr = tid >> 7, r = (tid & 127) >> 3, c = 2 * (tid & 7), o = 32 * pr;
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int m = 0; m < 16; m += 4) {
+      const float4 a = at4(sm.N + (o + 16 + r) * LD + o + m);
+      const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float2 x = *reinterpret_cast<const float2*>(sm.X + (o + m + u) * LD + o + c);
+        s0 = fmaf(av[u], x.x, s0);
+        s1 = fmaf(av[u], x.y, s1);
+      }
+    }
+    *reinterpret_cast<float2*>(sm.tmp + (16 * pr + r) * LT + c) = make_float2(s0, s1);
+    __syncthreads();
+    s0 = s1 = 0.f;
+#pragma unroll
+    for (int m = 0; m < 16; m += 4) {
+      const float4 a = at4(sm.X + (o + 16 + r) * LD + o + 16 + m);
+      const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float2 x = *reinterpret_cast<const float2*>(sm.tmp + (16 * pr + m + u) * LT + c);
+        s0 = fmaf(-av[u], x.x, s0);
+        s1 = fmaf(-av[u], x.y, s1);
+      }
+    }
+    *reinterpret_cast<float2*>(sm.X + (o + 16 + r) * LD + o + c) = make_float2(s0, s1);
+  }
+  __syncthreads();
+  // ---- 32 -> 64. N21 X1: a warp owns 4 columns, a lane a row; X1 is zero above its diagonal
+  {
+    const int c = 4 * warp;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int m = 0; m < 16; ++m) {
-      const float a = sm.N[(o + 16 + r) * LD + o + m];
-      const float4 x = *reinterpret_cast<const float4*>(sm.X + (o + m) * LD + o + c);
-      s[0] = fmaf(a, x.x, s[0]);
-      s[1] = fmaf(a, x.y, s[1]);
-      s[2] = fmaf(a, x.z, s[2]);
-      s[3] = fmaf(a, x.w, s[3]);
+    for (int m = c; m < 32; m += 4) {
+      const float4 a = at4(sm.N + (32 + lane) * LD + m);
+      axpy4(s, a.x, at4(sm.X + m * LD + c));
+      axpy4(s, a.y, at4(sm.X + (m + 1) * LD + c));
+      axpy4(s, a.z, at4(sm.X + (m + 2) * LD + c));
+      axpy4(s, a.w, at4(sm.X + (m + 3) * LD + c));
     }
-    *reinterpret_cast<float4*>(sm.tmp + (16 * pr + r) * LT + c) = make_float4(s[0], s[1], s[2], s[3]);
-    __syncthreads();
-    s[0] = s[1] = s[2] = s[3] = 0.f;
-#pragma unroll
-    for (int m = 0; m < 16; ++m) {
-      const float a = -sm.X[(o + 16 + r) * LD + o + 16 + m];
-      const float4 x = *reinterpret_cast<const float4*>(sm.tmp + (16 * pr + m) * LT + c);
-      s[0] = fmaf(a, x.x, s[0]);
-      s[1] = fmaf(a, x.y, s[1]);
-      s[2] = fmaf(a, x.z, s[2]);
-      s[3] = fmaf(a, x.w, s[3]);
-    }
-    *reinterpret_cast<float4*>(sm.X + (o + 16 + r) * LD + o + c) = make_float4(s[0], s[1], s[2], s[3]);
+    *reinterpret_cast<float4*>(sm.tmp + lane * LT + c) = make_float4(s[0], s[1], s[2], s[3]);
   }
   __syncthreads();
-  // ---- 32 -> 64: row r, 8 columns
-  {
-    const int r = tid >> 2, c = 8 * (tid & 3);
-    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    row8(s, sm.N + (32 + r) * LD, sm.X + c, LD, 32);
-    float* t = sm.tmp + r * LT + c;
-    *reinterpret_cast<float4*>(t) = make_float4(s[0], s[1], s[2], s[3]);
-    *reinterpret_cast<float4*>(t + 4) = make_float4(s[4], s[5], s[6], s[7]);
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] = 0.f;
-    row8(s, sm.X + (32 + r) * LD + 32, sm.tmp + c, LT, 32);
-    float* x = sm.X + (32 + r) * LD + c;
-    *reinterpret_cast<float4*>(x) = make_float4(-s[0], -s[1], -s[2], -s[3]);
-    *reinterpret_cast<float4*>(x + 4) = make_float4(-s[4], -s[5], -s[6], -s[7]);
+  {  // -X2 tmp: a warp owns 4 rows, X2 is zero right of its diagonal
+    const int r = 4 * warp + (lane >> 3), c = 4 * (lane & 7);
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int m = 0; m < 4 * warp + 4; m += 4) {
+      const float4 a = at4(sm.X + (32 + r) * LD + 32 + m);
+      axpy4(s, -a.x, at4(sm.tmp + m * LT + c));
+      axpy4(s, -a.y, at4(sm.tmp + (m + 1) * LT + c));
+      axpy4(s, -a.z, at4(sm.tmp + (m + 2) * LT + c));
+      axpy4(s, -a.w, at4(sm.tmp + (m + 3) * LT + c));
+    }
+    *reinterpret_cast<float4*>(sm.X + (32 + r) * LD + c) = make_float4(s[0], s[1], s[2], s[3]);
   }
   __syncthreads();
-  // ---- operands: thread (row r, 32 columns)
+  // ---- operands: thread (row r, 16 columns)
   {
-    const int r = tid >> 1, c0 = 32 * (tid & 1);
+    const int r = tid >> 2, c0 = 16 * (tid & 3);
     const size_t at = (((size_t)bh * N + n) * C + r) * C + c0;
     const float wr = sm.w[r], br = sm.be[r];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {  // 8 columns, one 16-byte piece
-      uint32_t hi[4], lo[4], gh[4], gl[4], tw[4], tt[4];
+    for (int g = 0; g < 2; ++g) {  // 8 columns, one 16-byte piece
+      uint32_t hi[4], low[4], gh[4], gl[4], tw[4], tt[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int c = c0 + 8 * g + 2 * e;
         const float2 x = *reinterpret_cast<const float2*>(sm.X + r * LD + c);
+        const float2 G = *reinterpret_cast<const float2*>(sm.G + c);
         hi[e] = pack_bf16(x.x, x.y);
-        lo[e] = pack_lo(x.x, x.y, hi[e]);
-        const float ga = -x.x * sm.G[c], gb = -x.y * sm.G[c + 1];
+        const float ga = -x.x * G.x, gb = -x.y * G.y;
         gh[e] = pack_bf16(ga, gb);
-        gl[e] = pack_lo(ga, gb, gh[e]);
-        if (p.back) {
-          const float b0 = sm.be[c], b1 = sm.be[c + 1];
-          const float ta = c < r ? br * x.x / (fabsf(b0) < 0x1p-60f ? 0x1p-60f : b0) : x.x;
-          const float tbv = c + 1 < r ? br * x.y / (fabsf(b1) < 0x1p-60f ? 0x1p-60f : b1) : x.y;
-          tw[e] = pack_bf16(wr * ta, wr * tbv);
-          tt[e] = pack_bf16(ta, tbv);
+        if (SPLIT) {
+          low[e] = pack_lo(x.x, x.y, hi[e]);
+          gl[e] = pack_lo(ga, gb, gh[e]);
+        }
+        if (BACK) {  // T_ij = beta_i T0_ij / beta_j below the diagonal
+          const float2 rb = *reinterpret_cast<const float2*>(sm.rb + c);
+          const float ta = c == r ? 1.f : br * x.x * rb.x, td = c + 1 == r ? 1.f : br * x.y * rb.y;
+          tw[e] = pack_bf16(wr * ta, wr * td);
+          tt[e] = pack_bf16(ta, td);
         }
       }
       const uint32_t off = sw128_off(r, (c0 >> 3) + g);
       *reinterpret_cast<uint4*>(p.m.T0 + at + 8 * g) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      st_shared_v4(smem_u32(sm.Tg) + off, gh[0], gh[1], gh[2], gh[3]);
-      if (p.split) {
-        *reinterpret_cast<uint4*>(p.m.T0lo + at + 8 * g) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        st_shared_v4(smem_u32(sm.Tgl) + off, gl[0], gl[1], gl[2], gl[3]);
+      st_shared_v4(sTg + off, gh[0], gh[1], gh[2], gh[3]);
+      if (SPLIT) {
+        *reinterpret_cast<uint4*>(p.m.T0lo + at + 8 * g) = make_uint4(low[0], low[1], low[2], low[3]);
+        st_shared_v4(sTg + TILE + off, gl[0], gl[1], gl[2], gl[3]);
       }
-      if (p.back) {
-        st_shared_v4(smem_u32(sm.Tw) + off, tw[0], tw[1], tw[2], tw[3]);
-        st_shared_v4(smem_u32(sm.Tt) + off, tt[0], tt[1], tt[2], tt[3]);
+      if (BACK) {
+        st_shared_v4(sTw + off, tw[0], tw[1], tw[2], tw[3]);
+        st_shared_v4(sTt + off, tt[0], tt[1], tt[2], tt[3]);
       }
     }
     fence_proxy_async_smem();
@@ -311,14 +353,14 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
       const uint64_t dk = desc_at(sw128_desc(sK, TILE, 1024), kk * 2048);  // K as [token][d_k]
-      umma_bf16(tb + COL_W, desc_at(sw128_desc(smem_u32(sm.Tg), 16, 1024), kk * 32), dk, id_w, kk > 0);
-      if (p.split)
-        umma_bf16(tb + COL_W, desc_at(sw128_desc(smem_u32(sm.Tgl), 16, 1024), kk * 32), dk, id_w, 1);
-      if (p.back) {
-        umma_bf16(tb + COL_W + LANE16, desc_at(sw128_desc(smem_u32(sm.Tw), TILE, 1024), kk * 2048),
-                  dk, id_wb, kk > 0);
+      umma_bf16(tb + COL_W, desc_at(sw128_desc(sTg, 16, 1024), kk * 32), dk, id_w, kk > 0);
+      if (SPLIT)
+        umma_bf16(tb + COL_W, desc_at(sw128_desc(sTg + TILE, 16, 1024), kk * 32), dk, id_w, 1);
+      if (BACK) {
+        umma_bf16(tb + COL_W + LANE16, desc_at(sw128_desc(sTw, TILE, 1024), kk * 2048), dk, id_wb,
+                  kk > 0);
         umma_bf16(tb + COL_KQ, desc_at(sw128_desc(smem_u32(sm.P), 16, 1024), kk * 32),
-                  desc_at(sw128_desc(smem_u32(sm.Tt), TILE, 1024), kk * 2048), id_pt, kk > 0);
+                  desc_at(sw128_desc(sTt, TILE, 1024), kk * 2048), id_pt, kk > 0);
       }
     }
     umma_commit(&sm.mma);
@@ -327,45 +369,27 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
   mbar_wait(&sm.mma, 1, wc, W_PREP_MMA);
   __syncwarp();
   tc_fence_after();
-  // W (lanes < 16) and Wb (lanes >= 16) to bf16; staged over Q (W), K (Wb) and the operand
-  // tiles Tg, Tgl (the remainder of W), which every product has read
+  // W (lanes < 16) and Wb (lanes >= 16) to bf16, columns [64 hh, 64 hh + 64); staged over Q
+  // (W), K (Wb) and Tg (the remainder of W), which every product has read
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {  // 32 columns
+  for (int g = 0; g < 2; ++g) {
     float v[32];
-    tmem_ld32(tb + COL_W + ((uint32_t)(32 * warp) << 16) + 32 * g, v);
+    tmem_ld32(tb + COL_W + lo + 64 * hh + 32 * g, v);
     tmem_ld_wait();
-    const bool on = !isP || p.back;
-    const uint32_t dst = smem_u32(isP ? sm.K : sm.Q) + (g >> 1) * TILE;
-    const uint32_t dlo = smem_u32(sm.Tg) + (g >> 1) * TILE;  // Tg and Tgl are adjacent
+    const uint32_t dst = (isP ? sK : sQ) + hh * TILE;
 #pragma unroll
     for (int cc = 0; cc < 4; ++cc) {
-      uint32_t hi[4], lo[4];
+      uint32_t hi[4], low[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         hi[e] = pack_bf16(v[8 * cc + 2 * e], v[8 * cc + 2 * e + 1]);
-        lo[e] = pack_lo(v[8 * cc + 2 * e], v[8 * cc + 2 * e + 1], hi[e]);
+        if (SPLIT) low[e] = pack_lo(v[8 * cc + 2 * e], v[8 * cc + 2 * e + 1], hi[e]);
       }
-      const uint32_t off = sw128_off(i, 4 * (g & 1) + cc);
-      if (on) st_shared_v4(dst + off, hi[0], hi[1], hi[2], hi[3]);
-      if (p.split && !isP) st_shared_v4(dlo + off, lo[0], lo[1], lo[2], lo[3]);
+      const uint32_t off = sw128_off(i, 4 * g + cc);
+      if (BACK || !isP) st_shared_v4(dst + off, hi[0], hi[1], hi[2], hi[3]);
+      if (SPLIT && !isP) st_shared_v4(sTg + hh * TILE + off, low[0], low[1], low[2], low[3]);
     }
     __syncwarp();
-  }
-  if (p.back) {
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float v[32];
-      tmem_ld32(tb + COL_KQ + ((uint32_t)(32 * warp) << 16) + 32 * half, v);
-      tmem_ld_wait();
-      if (!isP) {
-        uint4* out = reinterpret_cast<uint4*>(p.m.PT + (((size_t)bh * N + n) * C + i) * C + 32 * half);
-#pragma unroll
-        for (int cc = 0; cc < 4; ++cc)
-          out[cc] = make_uint4(pack_bf16(v[8 * cc], v[8 * cc + 1]), pack_bf16(v[8 * cc + 2], v[8 * cc + 3]),
-                               pack_bf16(v[8 * cc + 4], v[8 * cc + 5]), pack_bf16(v[8 * cc + 6], v[8 * cc + 7]));
-      }
-      __syncwarp();
-    }
   }
   fence_proxy_async_smem();
   tc_fence_before();
@@ -373,43 +397,68 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
   if (tid == 0) {
     for (int kb = 0; kb < 2; ++kb) {
       tma_store_3d(&tmW, sm.Q + kb * TILE, 64 * kb, t0, bh);
-      if (p.split) tma_store_3d(&tmWlo, sm.Tg + kb * TILE, 64 * kb, t0, bh);
-      if (p.back) tma_store_3d(&tmWb, sm.K + kb * TILE, 64 * kb, t0, bh);
+      if (SPLIT) tma_store_3d(&tmWlo, sm.Tg[kb], 64 * kb, t0, bh);
+      if (BACK) tma_store_3d(&tmWb, sm.K + kb * TILE, 64 * kb, t0, bh);
     }
     tma_store_commit();
-    tma_store_wait_all();
   }
+  __syncwarp();
+  if (BACK) {
+    tc_fence_after();
+    float v[32];
+    tmem_ld32(tb + COL_KQ + lo + 32 * hh, v);
+    tmem_ld_wait();
+    if (!isP) {
+      uint4* out = reinterpret_cast<uint4*>(p.m.PT + (((size_t)bh * N + n) * C + i) * C + 32 * hh);
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+        const float* x = v + 8 * cc;
+        out[cc] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                             pack_bf16(x[6], x[7]));
+      }
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
+  if (tid == 0) tma_store_wait_read();  // the CTA's shared memory may go once it has been read
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tb, kCols);
   }
 }
 
-cudaError_t launch_prep(const Args& a, bool split, cudaStream_t st) {
-  const Dims& d = a.d;
-  const uint64_t N = chunks(d.T), kh = (uint64_t)d.B * d.Hk, bh = d.BH();
-  const bool back = a.m.Wb != nullptr;
-  CUtensorMap mk, mq, mw, mwl, mwb;
-  using gradlev::tc::make_map_bf16_3d;
-  if (!make_map_bf16_3d(&mk, a.k, 128, d.T, kh, C) || !make_map_bf16_3d(&mq, a.q, 128, d.T, kh, C) ||
-      !make_map_bf16_3d(&mw, a.m.W, 128, N * C, bh, C) ||
-      !make_map_bf16_3d(&mwl, split ? a.m.Wlo : a.m.W, 128, N * C, bh, C) ||
-      !make_map_bf16_3d(&mwb, back ? a.m.Wb : a.m.W, 128, N * C, bh, C))
-    return cudaErrorInvalidValue;
-  static std::atomic<uint64_t> set{0};
+template <bool SPLIT, bool BACK>
+static cudaError_t launch(const CUtensorMap (&m)[5], const PrepParams& p, unsigned grid, cudaStream_t st) {
+  static std::atomic<uint64_t> set{0};  // devices whose opt-in is done
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (!bit || !(set.load() & bit)) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    const cudaError_t e = cudaFuncSetAttribute(prep_kernel<SPLIT, BACK>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     set.fetch_or(bit);
   }
-  PrepParams p{d, a.beta, a.log_alpha, a.scale, a.status, a.timeout_ns, a.m, split, back};
-  prep_kernel<<<(unsigned)(N * bh), kThreads, kSmem, st>>>(mk, mq, mw, mwl, mwb, p);
+  prep_kernel<SPLIT, BACK><<<grid, kThreads, kSmem, st>>>(m[0], m[1], m[2], m[3], m[4], p);
   count_launch();
   return cudaGetLastError();
+}
+
+cudaError_t launch_prep(const Args& a, bool split, cudaStream_t st) {
+  const Dims& d = a.d;
+  const uint64_t N = chunks(d.T), kh = (uint64_t)d.B * d.Hk, bh = d.BH();
+  const bool back = a.m.Wb != nullptr;
+  CUtensorMap m[5];
+  using gradlev::tc::make_map_bf16_3d;
+  if (!make_map_bf16_3d(&m[0], a.k, 128, d.T, kh, C) || !make_map_bf16_3d(&m[1], a.q, 128, d.T, kh, C) ||
+      !make_map_bf16_3d(&m[2], a.m.W, 128, N * C, bh, C) ||
+      !make_map_bf16_3d(&m[3], split ? a.m.Wlo : a.m.W, 128, N * C, bh, C) ||
+      !make_map_bf16_3d(&m[4], back ? a.m.Wb : a.m.W, 128, N * C, bh, C))
+    return cudaErrorInvalidValue;
+  const PrepParams p{d, a.beta, a.log_alpha, a.scale, a.status, a.timeout_ns, a.m};
+  const unsigned grid = (unsigned)(N * bh);
+  if (split) return back ? launch<true, true>(m, p, grid, st) : launch<true, false>(m, p, grid, st);
+  return back ? launch<false, true>(m, p, grid, st) : launch<false, false>(m, p, grid, st);
 }
 
 }  // namespace tc
