@@ -41,10 +41,12 @@ struct GradSmem {
   uint8_t S[2 * TILE], dS[2 * TILE];         // 64 rows of d_v x 128
   uint8_t X[TILE], Yn[TILE];
   float Lh[C], Ll[C], be[C], cq[C], ck[C], cz[C];
+  float ra[C], ca[C];                        // M_ij beta_j = ra_i ca_j (fac)
   int seg[C];
   float xs[2][C], zs[2][C];                  // per column half
   float red[8];
   float GC;
+  int fac;
   uint64_t kq, full, mma;
   uint32_t tmem_base;
   int abort;
@@ -63,11 +65,11 @@ struct GradParams {
   bf16 *dbeta, *dlog_alpha;
 };
 
-// sum of v[e] * x over 32 columns of a swizzled row
-__device__ __forceinline__ float row_dot(const float (&v)[32], uint32_t tile, int r, int c8) {
+// sum of v[e] * x over 16 columns of a swizzled row
+__device__ __forceinline__ float row_dot(const float (&v)[16], uint32_t tile, int r, int c8) {
   float s = 0.f;
 #pragma unroll
-  for (int cc = 0; cc < 4; ++cc) {
+  for (int cc = 0; cc < 2; ++cc) {
     const uint4 x = ld_shared_v4(tile + sw128_off(r, c8 + cc));
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -132,10 +134,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int bh = b * p.d.H + (kh - b * p.d.Hk) * grp + hv;
     if (warp == 2) {
       const GatePair g = chunk_gates(p.beta, p.log_alpha, (size_t)bh * T, t0, T);
+      const float Lm = __shfl_sync(0xffffffffu, g.Lh[0], 31), Ll = __shfl_sync(0xffffffffu, g.Ll[0], 31);
+      const bool fac = g.seg_end == 0 && g.Lend > -80.f;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int j = lane + 32 * k;
         const float G = gate_G(g, k);
+        const float x = (g.Lh[k] - Lm) + (g.Ll[k] - Ll);
+        sm.ra[j] = fac ? expf(x) : 1.f;
+        sm.ca[j] = fac ? expf(-x) * g.be[k] : g.be[k];
         sm.Lh[j] = g.Lh[k];
         sm.Ll[j] = g.Ll[k];
         sm.seg[j] = g.seg[k];
@@ -144,7 +151,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         sm.ck[j] = g.be[k] * G;
         sm.cz[j] = g.be[k] * gate_w(g, k);
       }
-      if (lane == 0) sm.GC = gate_GC(g);
+      if (lane == 0) {
+        sm.GC = gate_GC(g);
+        sm.fac = fac;
+      }
     }
     float ss = 0.f;  // <dS, S>
     for (int sl = 0; sl < nsl; ++sl) {
@@ -198,42 +208,57 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0) sm.red[warp] = ss;
     tc_fence_after();
     // ---- X and Yn: lower lanes, columns [32 hh, 32 hh + 32)
-    {
-      float f[32], g[32];
-      tmem_ld32(tb + COL_B + lo + 32 * hh, f);
-      tmem_ld32(tb + COL_B + 64 + lo + 32 * hh, g);
+    const float rx = p.scale * sm.ra[i], ry = -sm.be[i] * sm.ra[i];
+    float db = 0.f;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      float f[16], g[16];
+      const int j0 = 32 * hh + 16 * hf;
+      tmem_ld16(tb + COL_B + lo + j0, f);
+      tmem_ld16(tb + COL_B + 64 + lo + j0, g);
       tmem_ld_wait();
       if (!up) {
-        const float Lh = sm.Lh[i], Ll = sm.Ll[i], bi = sm.be[i];
-        const int seg = sm.seg[i];
-        float db = 0.f;
-        uint32_t xp[16], yp[16];
+        const int keep = i - j0;  // columns left of the diagonal
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          float x[2], y[2];
+        for (int e = 0; e < 16; ++e) db = e == keep ? g[e] : db;
+        if (sm.fac) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int j = 32 * hh + e + u;
-            const bool on = j <= i && sm.seg[j] == seg;
-            const float m = on ? sm.be[j] * expf((Lh - sm.Lh[j]) + (Ll - sm.Ll[j])) : 0.f;
-            x[u] = on ? p.scale * m * f[e + u] : 0.f;
-            y[u] = on && j < i ? -bi * m * g[e + u] : 0.f;
-            if (j == i) db = g[e + u];
+          for (int e = 0; e < 16; e += 4) {
+            const float4 c = *reinterpret_cast<const float4*>(sm.ca + j0 + e);
+            const float cv[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              f[e + u] = e + u <= keep ? f[e + u] * (rx * cv[u]) : 0.f;
+              g[e + u] = e + u < keep ? g[e + u] * (ry * cv[u]) : 0.f;
+            }
           }
-          xp[e >> 1] = pack_bf16(x[0], x[1]);
-          yp[e >> 1] = pack_bf16(y[0], y[1]);
+        } else {  // a reset, or decays whose factors leave float32
+          const float Lh = sm.Lh[i], Ll = sm.Ll[i];
+          const int seg = sm.seg[i];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int j = j0 + e;
+            const float m = sm.ca[j] * expf(fminf((Lh - sm.Lh[j]) + (Ll - sm.Ll[j]), 0.f));
+            const bool on = sm.seg[j] == seg;
+            f[e] = on && e <= keep ? f[e] * (rx * m) : 0.f;
+            g[e] = on && e < keep ? g[e] * (ry * m) : 0.f;
+          }
         }
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          const uint32_t off = sw128_off(i, 4 * hh + cc);
-          st_shared_v4(sX + off, xp[4 * cc], xp[4 * cc + 1], xp[4 * cc + 2], xp[4 * cc + 3]);
-          st_shared_v4(sY + off, yp[4 * cc], yp[4 * cc + 1], yp[4 * cc + 2], yp[4 * cc + 3]);
+        for (int cc = 0; cc < 2; ++cc) {
+          const uint32_t off = sw128_off(i, 4 * hh + 2 * hf + cc);
+          const float *x = f + 8 * cc, *y = g + 8 * cc;
+          st_shared_v4(sX + off, pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                       pack_bf16(x[6], x[7]));
+          st_shared_v4(sY + off, pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
+                       pack_bf16(y[6], y[7]));
         }
-        if ((i >> 5) == hh && t0 + i < T) p.dbeta[(size_t)bh * T + t0 + i] = __float2bfloat16_rn(db);
       }
-      fence_proxy_async_smem();
-      tc_fence_before();
+      __syncwarp();
     }
+    if (!up && (i >> 5) == hh && t0 + i < T) p.dbeta[(size_t)bh * T + t0 + i] = __float2bfloat16_rn(db);
+    fence_proxy_async_smem();
+    tc_fence_before();
     if (hv == 0) mbar_wait(&sm.kq, 0, wc, W_G_KQ);
     __syncthreads();
     if (tid == 0) {
@@ -249,23 +274,23 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float ca = up ? -sm.ck[i] : sm.cq[i], cz = up ? sm.cz[i] : 0.f;
     float xs = 0.f, zs = 0.f;
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      float v[32];
-      tmem_ld32(tb + COL_A + lo + 64 * hh + 32 * hf, v);
+    for (int hf = 0; hf < 4; ++hf) {
+      float v[16];
+      tmem_ld16(tb + COL_A + lo + 64 * hh + 16 * hf, v);
       tmem_ld_wait();
-      xs = fmaf(ca, row_dot(v, mine, i, 4 * hf), xs);
+      xs = fmaf(ca, row_dot(v, mine, i, 2 * hf), xs);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) acc[32 * hf + e] = fmaf(ca, v[e], acc[32 * hf + e]);
+      for (int e = 0; e < 16; ++e) acc[16 * hf + e] = fmaf(ca, v[e], acc[16 * hf + e]);
     }
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      float v[32];
-      tmem_ld32(tb + COL_B + lo + 64 * hh + 32 * hf, v);  // lower lanes: unused (xk in flight)
+    for (int hf = 0; hf < 4; ++hf) {
+      float v[16];
+      tmem_ld16(tb + COL_B + lo + 64 * hh + 16 * hf, v);  // lower lanes: unused (xk in flight)
       tmem_ld_wait();
       if (up) {
-        zs = fmaf(cz, row_dot(v, mine, i, 4 * hf), zs);
+        zs = fmaf(cz, row_dot(v, mine, i, 2 * hf), zs);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) acc[32 * hf + e] = fmaf(cz, v[e], acc[32 * hf + e]);
+        for (int e = 0; e < 16; ++e) acc[16 * hf + e] = fmaf(cz, v[e], acc[16 * hf + e]);
       }
       __syncwarp();
     }
@@ -289,24 +314,24 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     // ---- xk (lower) and ka (upper); yk (upper)
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      float v[32];
-      tmem_ld32(tb + COL_B + lo + 64 * hh + 32 * hf, v);
+    for (int hf = 0; hf < 4; ++hf) {
+      float v[16];
+      tmem_ld16(tb + COL_B + lo + 64 * hh + 16 * hf, v);
       tmem_ld_wait();
-      const float dot = row_dot(v, mine, i, 4 * hf);
+      const float dot = row_dot(v, mine, i, 2 * hf);
       xs += up ? -dot : dot;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) acc[32 * hf + e] += v[e];
+      for (int e = 0; e < 16; ++e) acc[16 * hf + e] += v[e];
     }
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      float v[32];
-      tmem_ld32(tb + COL_A + lo + 64 * hh + 32 * hf, v);  // lower lanes: t, used above
+    for (int hf = 0; hf < 4; ++hf) {
+      float v[16];
+      tmem_ld16(tb + COL_A + lo + 64 * hh + 16 * hf, v);  // lower lanes: t, used above
       tmem_ld_wait();
       if (up) {
-        xs += row_dot(v, mine, i, 4 * hf);
+        xs += row_dot(v, mine, i, 2 * hf);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) acc[32 * hf + e] += v[e];
+        for (int e = 0; e < 16; ++e) acc[16 * hf + e] += v[e];
       }
       __syncwarp();
     }
@@ -363,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       tma_store_3d(&tmdk, sm.K + kb * TILE, 64 * kb, t0, kh);
     }
     tma_store_commit();
-    tma_store_wait_all();
+    tma_store_wait_read();
   }
   if (warp == 1) {
     tc_fence_after();
