@@ -9,8 +9,10 @@
 //   Y^T  = S (scale G Q)^T + D^T Pb^T      dV  = beta E
 //
 // The chain through a chunk is: S to bf16 (TMEM -> registers -> TMEM), the product with W,
-// its result to bf16, the product with K. All else (V^T T0^T, dY^T Q, the outputs, the
-// loads, the gates and the scaling of Q and K by them) runs beside it.
+// its result to bf16, the product with K. All else runs beside it: V^T T0^T of the next
+// chunk and the outputs' products are issued into the gaps of the chain, and their results
+// leave through an output warpgroup. Without SPLIT one product of N = 128 takes S through W
+// and Q together.
 //
 // SPLIT (a forward whose last state is asked for): every operand of the state that is not
 // exact in bf16 comes as a sum of two bf16 (S, W, T0, beta w D), three products in place of
@@ -18,7 +20,9 @@
 // good to 1e-5. Training needs no such state and takes single products.
 //
 // Warp roles (16): 0 TMA producer, 1 MMA issuer (owns TMEM), 2 gates, 4-11 two chain
-// warpgroups (each half of the columns), 12-15 scaling of Q and K, and Y.
+// warpgroups (each half of the columns), 12-15 scaling of Q and K, and the outputs: 16-lane
+// TMEM loads in the layout of 8 x 8 fragments, transposed on the way to shared memory
+// (stmatrix) so that tokens become rows, and TMA stores.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -42,12 +46,11 @@ constexpr int kThreads = 512;
 // TMEM columns
 constexpr uint32_t COL_S = 0;      // float32 state, 128
 constexpr uint32_t COL_SH = 128;   // bf16 state, 64
-constexpr uint32_t COL_D = 192;    // D^T (E^T) accumulator, 64
-constexpr uint32_t COL_DB = 256;   // bf16 D (E), 32
-constexpr uint32_t COL_U = 288;    // bf16 beta w D, 32
-constexpr uint32_t COL_Y = 320;    // Y^T, 64 per buffer
-constexpr uint32_t COL_SL = 384;   // remainder of the state, 64 (SPLIT: one Y buffer)
-constexpr uint32_t COL_UL = 448;   // remainder of beta w D, 32
+constexpr uint32_t COL_DB = 192;   // bf16 D (E), 32
+constexpr uint32_t COL_U = 224;    // bf16 beta w D, 32
+constexpr uint32_t COL_D = 256;    // D^T (E^T) accumulator, 64, and Y^T, 64; two such pairs
+constexpr uint32_t COL_SL = 384;   // SPLIT (one pair): remainder of the state, 64,
+constexpr uint32_t COL_UL = 448;   // and of beta w D, 32
 
 struct GateSlot {
   float q[C];    // scale G
@@ -62,28 +65,30 @@ struct Bars {
   uint64_t full[NS], empty[NS], scaled[NS];
   uint64_t gfull[GS], gempty[GS];
   uint64_t sready, dfull, uready, sfull, done;
-  uint64_t yfull[2], yfree[2];
+  uint64_t yfull[2], yfree[2];   // per accumulator pair
   uint32_t tmem_base;
   int abort;
 };
 
-// Stage: Q, K, V (dY) tiles of 2 TILE; W (Wb) of 2 TILE; T0, Pb (or PT) of TILE; SPLIT adds
-// the remainders of W and T0.
+// Stage: per 64 columns of d_k the W (Wb) tile and the Q tile next to each other (128 rows of
+// one operand), then K and V (dY) tiles of 2 TILE, T0 (PT), Pb; SPLIT adds the remainders of W
+// and T0.
 template <bool BWD, bool SPLIT>
 struct Layout {
-  static constexpr int q = 0, k = 2 * TILE, v = 4 * TILE, w = 6 * TILE, t = 8 * TILE;
-  static constexpr int p = 9 * TILE, wl = 10 * TILE, tl = 12 * TILE;
+  static constexpr int w = 0, q = TILE, wq = 2 * TILE;   // wq: from one k-block to the next
+  static constexpr int k = 4 * TILE, v = 6 * TILE, t = 8 * TILE, p = 9 * TILE;
+  static constexpr int wl = 10 * TILE, tl = 12 * TILE;
   static constexpr int bytes = BWD ? 9 * TILE : (SPLIT ? 13 * TILE : 10 * TILE);
-  static constexpr bool staged = !SPLIT;   // bf16 states through shared memory and TMA
-  static constexpr int stage_s = NS * bytes;
-  static constexpr int bars = stage_s + (staged ? 2 * BIG : 0);
+  static constexpr bool staged = !SPLIT;   // states and outputs through shared memory and TMA
+  static constexpr int stage_s = NS * bytes, stage_o = stage_s + (staged ? 2 * BIG : 0);
+  static constexpr int bars = stage_o + (staged ? 2 * TILE : 0);
   static constexpr size_t smem = bars + sizeof(Bars) + 1024;
   static_assert(smem <= 227 * 1024, "over the shared memory of a CTA");
 };
 
 enum : uint32_t {
   W_TMA = 0x901, W_TMA_DRAIN, W_FULL = 0x911, W_SCALED, W_SREADY, W_UREADY, W_YFREE, W_DONE,
-  W_GATE = 0x921, W_C_SFULL = 0x931, W_C_DFULL, W_C_GATE, W_C_Y, W_O_FULL = 0x941, W_O_GATE, W_O_Y,
+  W_GATE = 0x921, W_C_SFULL = 0x931, W_C_DFULL, W_C_GATE, W_O_FULL = 0x941, W_O_GATE, W_O_Y,
 };
 
 struct WalkParams {
@@ -98,7 +103,6 @@ struct WalkParams {
   bf16* dS0;             // backward end
   bf16* y;               // forward
   bf16* D;               // forward: D, backward: E (null: not kept)
-  bf16* dv;              // backward
   bf16* states;          // chunk-start (chunk-end) states, or null
 };
 
@@ -118,19 +122,72 @@ __device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
   return pack_bf16(a - bf16_lo(hi), b - bf16_hi(hi));
 }
 
-// x *= factor[row] on a [64 tokens x 128] tile in place, by 128 threads.
-__device__ __forceinline__ void scale_tile(uint32_t tile, const float* factor, int t) {
+// Barrier `id` among `nthreads` threads; whether any of them brought `pred`.
+__device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t nthreads, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)pred), "r"(id), "r"(nthreads)
+      : "memory");
+  return r != 0;
+}
+
+// x *= factor[row] on a [64 tokens x 128] tile in place (its k-blocks `step` bytes apart), by
+// 128 threads.
+__device__ __forceinline__ void scale_tile(uint32_t tile, uint32_t step, const float* factor, int t) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const uint32_t off = (uint32_t)(t + 128 * k) * 16;
-    const int j = (off & (TILE - 1)) >> 7;
-    const float f = factor[j];
+    const uint32_t in = (uint32_t)(t + 128 * (k & 3)) * 16, off = (k >> 2) * step + in;
+    const float f = factor[in >> 7];
     const uint4 v = ld_shared_v4(tile + off);
     st_shared_v4(tile + off, pack_bf16(f * bf16_lo(v.x), f * bf16_hi(v.x)),
                  pack_bf16(f * bf16_lo(v.y), f * bf16_hi(v.y)),
                  pack_bf16(f * bf16_lo(v.z), f * bf16_hi(v.z)),
                  pack_bf16(f * bf16_lo(v.w), f * bf16_hi(v.w)));
   }
+}
+
+// 64 float32 columns of 16 TMEM lanes as 8 x 8 fragments: registers 4 g .. 4 g + 3 hold, of
+// columns 8 g + 2 (lane % 4) and the one after, rows lane / 4 (first two) and lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_frag64(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void stmatrix_trans4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                                uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// 16 state rows (fragments of 64 tokens) into the [64 tokens x 128] tile, tokens as rows; the
+// rows start at `row` (a multiple of 16).
+__device__ __forceinline__ void put_frag64(uint32_t tile, int row, const float (&v)[32]) {
+  const int lane = threadIdx.x & 31, m = lane >> 3;
+  const uint32_t block = tile + (row >> 6) * TILE;
+  const uint32_t c = ((row & 63) >> 3) + (m & 1);
+#pragma unroll
+  for (int g = 0; g < 8; g += 2)
+    stmatrix_trans4(block + sw128_off(8 * (g + (m >> 1)) + (lane & 7), c),
+                    pack_bf16(v[4 * g], v[4 * g + 1]), pack_bf16(v[4 * g + 2], v[4 * g + 3]),
+                    pack_bf16(v[4 * g + 4], v[4 * g + 5]), pack_bf16(v[4 * g + 6], v[4 * g + 7]));
 }
 
 }  // namespace
@@ -141,9 +198,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmW,
                 const __grid_constant__ CUtensorMap tmWl, const __grid_constant__ CUtensorMap tmT,
                 const __grid_constant__ CUtensorMap tmTl, const __grid_constant__ CUtensorMap tmP,
-                const __grid_constant__ CUtensorMap tmS, WalkParams p) {
+                const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmY,
+                const __grid_constant__ CUtensorMap tmD, WalkParams p) {
   using L = Layout<BWD, SPLIT>;
-  constexpr int NY = SPLIT ? 1 : 2;   // Y buffers
+  constexpr int NY = SPLIT ? 1 : 2;   // accumulator pairs
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -198,8 +256,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx(&sm.full[s], L::bytes);
         for (int kb = 0; kb < 2; ++kb) {
           tma_load_3d(st + L::v + kb * TILE, &tmV, &sm.full[s], n0 + 64 * kb, t0, bh);
-          tma_load_3d(st + L::w + kb * TILE, &tmW, &sm.full[s], 64 * kb, t0, bh);
-          tma_load_3d(st + L::q + kb * TILE, &tmQ, &sm.full[s], 64 * kb, t0, kh);
+          tma_load_3d(st + L::w + kb * L::wq, &tmW, &sm.full[s], 64 * kb, t0, bh);
+          tma_load_3d(st + L::q + kb * L::wq, &tmQ, &sm.full[s], 64 * kb, t0, kh);
           tma_load_3d(st + L::k + kb * TILE, &tmK, &sm.full[s], 64 * kb, t0, kh);
           if (SPLIT) tma_load_3d(st + L::wl + kb * TILE, &tmWl, &sm.full[s], 64 * kb, t0, bh);
         }
@@ -216,42 +274,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       const uint32_t id_v = idesc_bf16(128, 64, true, BWD);       // V^T T0^T, dY^T PT
       const uint32_t id_w = idesc_bf16(128, 64, false, false);    // S W^T, S Q^T, D^T Pb^T
+      const uint32_t id_wq = idesc_bf16(128, 128, false, false);  // S [W; Q]^T
       const uint32_t id_u = idesc_bf16(128, 128, false, true);    // U^T K, E^T K
       const uint32_t id_o = idesc_bf16(128, 128, true, true);     // dY^T Q
-      for (int c = 0; c < N; ++c) {
-        const int s = c % NS, yb = c % NY;
-        const uint32_t st = smem_u32(base + s * L::bytes);
-        if (!mbar_wait(&sm.full[s], (c / NS) & 1, wc, W_FULL)) break;
+      // D^T of chunk c = V^T T0^T. Its pair of accumulators is free once the chain has read D
+      // (uready, waited by then) and the outputs have been taken.
+      auto first = [&](int c) -> bool {
+        const int s = c % NS;
+        const uint32_t st = smem_u32(base + s * L::bytes), d = tb + COL_D + 128 * (c % NY);
+        if (!mbar_wait(&sm.full[s], (c / NS) & 1, wc, W_FULL)) return false;
+        if ((!SPLIT || p.D) && !mbar_wait(&sm.yfree[c % NY], ((c / NY) & 1) ^ 1, wc, W_YFREE)) return false;
         tc_fence_after();
-        // D^T = V^T T0^T: the chain warps have read D of chunk c - 1 (uready, waited below)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           const uint64_t av = desc_at(sw128_desc(st + L::v, TILE, 1024), kk * 2048);
           const uint32_t off = BWD ? kk * 2048 : kk * 32;
-          umma_bf16(tb + COL_D, av, desc_at(sw128_desc(st + L::t, BWD ? TILE : 16, 1024), off), id_v, kk > 0);
-          if (SPLIT) umma_bf16(tb + COL_D, av, desc_at(sw128_desc(st + L::tl, 16, 1024), off), id_v, 1);
+          umma_bf16(d, av, desc_at(sw128_desc(st + L::t, BWD ? TILE : 16, 1024), off), id_v, kk > 0);
+          if (SPLIT) umma_bf16(d, av, desc_at(sw128_desc(st + L::tl, 16, 1024), off), id_v, 1);
         }
+        return true;
+      };
+      bool ok = first(0);
+      for (int c = 0; c < N && ok; ++c) {
+        const int s = c % NS, yb = c % NY;
+        const uint32_t st = smem_u32(base + s * L::bytes);
+        const uint32_t d = tb + COL_D + 128 * yb, y = d + 64;
+        if (!mbar_wait(&sm.scaled[s], (c / NS) & 1, wc, W_SCALED)) break;
         if (!mbar_wait(&sm.sready, c & 1, wc, W_SREADY)) break;
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {  // += S W^T
-          const uint32_t off = (kk >> 2) * TILE + (kk & 3) * 32;
+        for (int kk = 0; kk < 8; ++kk) {  // D^T += S W^T (and Y^T = S Q^T)
+          const uint32_t off = (kk >> 2) * L::wq + (kk & 3) * 32;
           const uint64_t bw = desc_at(sw128_desc(st + L::w, 16, 1024), off);
-          umma_bf16_tmem_a(tb + COL_D, tb + COL_SH + 8 * kk, bw, id_w, 1);
+          const uint32_t a = tb + COL_SH + 8 * kk;
+          if (!BWD && !SPLIT && kk > 0) {
+            umma_bf16_tmem_a(d, a, bw, id_wq, 1);
+          } else {
+            umma_bf16_tmem_a(d, a, bw, id_w, 1);
+            if (!BWD && !SPLIT) umma_bf16_tmem_a(y, a, desc_at(sw128_desc(st + L::q, 16, 1024), off), id_w, 0);
+          }
           if (SPLIT) {
-            umma_bf16_tmem_a(tb + COL_D, tb + COL_SL + 8 * kk, bw, id_w, 1);
-            umma_bf16_tmem_a(tb + COL_D, tb + COL_SH + 8 * kk,
-                             desc_at(sw128_desc(st + L::wl, 16, 1024), off), id_w, 1);
+            umma_bf16_tmem_a(d, tb + COL_SL + 8 * kk, bw, id_w, 1);
+            umma_bf16_tmem_a(d, a, desc_at(sw128_desc(st + L::wl, 16, 1024),
+                                           (kk >> 2) * TILE + (kk & 3) * 32), id_w, 1);
           }
         }
         umma_commit(&sm.dfull);
-        if (!mbar_wait(&sm.scaled[s], (c / NS) & 1, wc, W_SCALED)) break;
-        tc_fence_after();
         if (BWD) {
+          umma_commit(&sm.yfull[yb]);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)  // S += dY^T (scale G Q): S is scaled (sready)
             umma_bf16(tb + COL_S, desc_at(sw128_desc(st + L::v, TILE, 1024), kk * 2048),
-                      desc_at(sw128_desc(st + L::q, TILE, 1024), kk * 2048), id_o, 1);
+                      desc_at(sw128_desc(st + L::q, L::wq, 1024), kk * 2048), id_o, 1);
+        } else if (SPLIT) {  // Y^T = S Q^T, which frees the bf16 state
+          if (!mbar_wait(&sm.yfree[0], (c & 1) ^ 1, wc, W_YFREE)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_bf16_tmem_a(y, tb + COL_SH + 8 * kk,
+                             desc_at(sw128_desc(st + L::q, 16, 1024), (kk >> 2) * L::wq + (kk & 3) * 32),
+                             id_w, kk > 0);
+        } else if (c + 1 < N && !first(c + 1)) {
+          break;
         }
         if (!mbar_wait(&sm.uready, c & 1, wc, W_UREADY)) break;
         tc_fence_after();
@@ -263,21 +347,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         umma_commit(&sm.sfull);
         if (!BWD) {
-          if (!mbar_wait(&sm.yfree[yb], ((c / NY) & 1) ^ 1, wc, W_YFREE)) break;
-          tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {  // Y^T = S (scale G Q)^T
-            const uint32_t off = (kk >> 2) * TILE + (kk & 3) * 32;
-            umma_bf16_tmem_a(tb + COL_Y + 64 * yb, tb + COL_SH + 8 * kk,
-                             desc_at(sw128_desc(st + L::q, 16, 1024), off), id_w, kk > 0);
-          }
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // += D^T Pb^T
-            umma_bf16_tmem_a(tb + COL_Y + 64 * yb, tb + COL_DB + 8 * kk,
-                             desc_at(sw128_desc(st + L::p, 16, 1024), kk * 32), id_w, 1);
+          for (int kk = 0; kk < 4; ++kk)  // Y^T += D^T Pb^T
+            umma_bf16_tmem_a(y, tb + COL_DB + 8 * kk, desc_at(sw128_desc(st + L::p, 16, 1024), kk * 32),
+                             id_w, 1);
           umma_commit(&sm.yfull[yb]);
         }
         umma_commit(&sm.empty[s]);
+        if ((BWD || SPLIT) && c + 1 < N) ok = first(c + 1);
       }
       umma_commit(&sm.done);
       mbar_drain(&sm.done, 0, wc, W_DONE);
@@ -346,10 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int g = c % GS, n = cg(c), t0 = n * C;
       const GateSlot& gs = sm.gates[g];
       ok = mbar_wait_warp(&sm.gfull[g], (c / GS) & 1, wc, W_C_GATE);
+      // every product of chunk c - 1 that reads the bf16 state was issued before this commit
       ok = ok && (c == 0 || mbar_wait_warp(&sm.sfull, (c - 1) & 1, wc, W_C_SFULL));
-      // the bf16 state is free once Y of chunk c - 1 has read it
-      ok = ok && (BWD || c == 0 ||
-                  mbar_wait_warp(&sm.yfull[(c - 1) % NY], ((c - 1) / NY) & 1, wc, W_C_Y));
       if (!ok) break;
       tc_fence_after();
       const float GC = gs.GC;
@@ -404,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       float v[32];
-      tmem_ld32(tb + COL_D + lo + 32 * hh, v);
+      tmem_ld32(tb + COL_D + 128 * (c % NY) + lo + 32 * hh, v);
       tmem_ld_wait();
       uint32_t db[16];
       {
@@ -427,19 +502,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.uready);
-      // D (E and dV) to memory: a warp's store covers 32 consecutive rows of one token
-      if (p.D) {
-        const size_t o = ((size_t)bh * T + t0 + 32 * hh) * p.d.dv + n0 + r;
-        const int left = T - t0 - 32 * hh;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          if (e >= left) break;
-          const uint32_t w = db[e >> 1];
-          reinterpret_cast<unsigned short*>(p.D)[o + (size_t)e * p.d.dv] =
-              (unsigned short)(e & 1 ? w >> 16 : w & 0xffff);
-          if (BWD) p.dv[o + (size_t)e * p.d.dv] = __float2bfloat16_rn(gs.be[32 * hh + e] * v[e]);
-        }
-      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.gempty[g]);
     }
@@ -467,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp >= 12) {
-    // ------------------------------------------------------------ scaled Q (and K); Y
+    // ------------------------------------------------------------ scaled Q (and K); outputs
     const int q = warp & 3, t = threadIdx.x - 384;
     const uint32_t lo = (uint32_t)(32 * q) << 16;
     auto scale_chunk = [&](int c) -> bool {
@@ -475,44 +537,96 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait_warp(&sm.full[s], (c / NS) & 1, wc, W_O_FULL)) return false;
       if (!mbar_wait_warp(&sm.gfull[g], (c / GS) & 1, wc, W_O_GATE)) return false;
       const uint32_t st = smem_u32(base + s * L::bytes);
-      scale_tile(st + L::q, sm.gates[g].q, t);
-      if (BWD) scale_tile(st + L::k, sm.gates[g].u, t);
+      scale_tile(st + L::q, L::wq, sm.gates[g].q, t);
+      if (BWD) scale_tile(st + L::k, TILE, sm.gates[g].u, t);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sm.scaled[s]);
-        mbar_arrive(&sm.gempty[g]);
-      }
+      if (lane == 0) mbar_arrive(&sm.scaled[s]);
       return true;
     };
-    bool ok = scale_chunk(0);
-    for (int c = 0; c < N && ok; ++c) {
-      if (c + 1 < N) ok = scale_chunk(c + 1);
-      if (BWD) continue;
-      const int yb = c % NY, t0 = c * C;
-      ok = ok && mbar_wait_warp(&sm.yfull[yb], (c / NY) & 1, wc, W_O_Y);
-      if (!ok) break;
-      tc_fence_after();
-      bf16* o = p.y + ((size_t)bh * T + t0) * p.d.dv + n0 + 32 * q + lane;
+    // 128 rows x 64 tokens at TMEM column `col` to a [64 tokens x 128] tile of `map`, times
+    // factor[token] if given
+    const uint32_t tile = smem_u32(base + L::stage_o);
+    auto emit = [&](uint32_t col, const CUtensorMap* map, const float* factor, int t0, uint64_t* after) {
+      if (t == 0) tma_store_wait_read_n<0>();  // the tile's last store
+      named_bar_sync(1, 128);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         float v[32];
-        tmem_ld32(tb + COL_Y + 64 * yb + lo + 32 * hf, v);
+        tmem_ld_frag64(tb + col + lo + hf * LANE16, v);
         tmem_ld_wait();
-        if (hf == 1) {
+        if (after && hf == 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.yfree[yb]);
+          if (lane == 0) mbar_arrive(after);
         }
-        const int left = T - t0 - 32 * hf;
-        if (p.y) {
+        if (factor) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (e < left) o[(size_t)(32 * hf + e) * p.d.dv] = __float2bfloat16_rn(v[e]);
+          for (int g = 0; g < 8; ++g) {
+            const float2 f = *reinterpret_cast<const float2*>(factor + 8 * g + 2 * (lane & 3));
+            v[4 * g] *= f.x;
+            v[4 * g + 1] *= f.y;
+            v[4 * g + 2] *= f.x;
+            v[4 * g + 3] *= f.y;
+          }
         }
-        __syncwarp();
+        put_frag64(tile, 32 * q + 16 * hf, v);
       }
+      fence_proxy_async_smem();
+      named_bar_sync(1, 128);
+      if (t == 0) {
+        tma_store_3d(map, base + L::stage_o, n0, t0, bh);
+        tma_store_3d(map, base + L::stage_o + TILE, n0 + 64, t0, bh);
+        tma_store_commit();
+      }
+    };
+    // the same straight from the registers (SPLIT has no shared memory left): a warp's store
+    // covers 32 consecutive rows of one token
+    auto emit_direct = [&](uint32_t col, bf16* out, int t0, uint64_t* after) {
+      bf16* o = out ? out + ((size_t)bh * T + t0) * p.d.dv + n0 + 32 * q + lane : nullptr;
+      float v[64];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float u[32];
+        tmem_ld32(tb + col + lo + 32 * hf, u);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[32 * hf + e] = u[e];
+      }
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (after && lane == 0) mbar_arrive(after);
+      const int left = T - t0;
+      if (o) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (e < left) o[(size_t)e * p.d.dv] = __float2bfloat16_rn(v[e]);
+      }
+      __syncwarp();
+    };
+    bool ok = scale_chunk(0);
+    for (int c = 0; c < N; ++c) {
+      const int g = c % GS, yb = c % NY, t0 = cg(c) * C;
+      if (ok && c + 1 < N) ok = scale_chunk(c + 1);
+      ok = ok && mbar_wait_warp(&sm.yfull[yb], (c / NY) & 1, wc, W_O_Y);
+      // the warps of emit() meet at barriers: all of them go on, or none does
+      if (L::staged) ok = !named_bar_or(2, 128, !ok);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = COL_D + 128 * yb;
+      if (BWD) {
+        emit(d, &tmD, nullptr, t0, nullptr);                          // E
+        emit(d, &tmY, sm.gates[g].be, t0, &sm.yfree[yb]);             // dV = beta E
+      } else if (L::staged) {
+        if (p.D) emit(d, &tmD, nullptr, t0, p.y ? nullptr : &sm.yfree[yb]);
+        if (p.y) emit(d + 64, &tmY, nullptr, t0, &sm.yfree[yb]);
+      } else {
+        if (p.D) emit_direct(d, p.D, t0, nullptr);
+        emit_direct(d + 64, p.y, t0, &sm.yfree[yb]);
+      }
+      if (lane == 0) mbar_arrive(&sm.gempty[g]);
     }
+    if (t == 0) tma_store_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -532,7 +646,9 @@ static cudaError_t launch(const Args& a, cudaStream_t st) {
   bf16* states = BWD ? a.dS : a.sv.S;
   const bf16* w = BWD ? a.sv.Wb : a.m.W;
   const bf16* t = BWD ? a.sv.PT : a.m.T0;
-  CUtensorMap mq, mk, mv, mw, mwl, mt, mtl, mp, ms;
+  bf16* dd = BWD ? a.E : a.sv.D;           // D or E
+  void* yy = BWD ? a.dv_ : a.y;
+  CUtensorMap mq, mk, mv, mw, mwl, mt, mtl, mp, ms, my, md;
   if (!make_map_bf16_3d(&mq, a.q, 128, d.T, kh, C) || !make_map_bf16_3d(&mk, a.k, 128, d.T, kh, C) ||
       !make_map_bf16_3d(&mv, v, d.dv, d.T, bh, C) || !make_map_bf16_3d(&mw, w, 128, N * C, bh, C) ||
       !make_map_bf16_3d(&mwl, SPLIT ? a.m.Wlo : w, 128, N * C, bh, C) ||
@@ -540,7 +656,9 @@ static cudaError_t launch(const Args& a, cudaStream_t st) {
       !make_map_bf16_3d(&mtl, SPLIT ? a.m.T0lo : t, C, N * C, bh, C) ||
       !make_map_bf16_3d(&mp, BWD ? t : a.m.Pb, C, N * C, bh, C) ||
       !make_map_bf16_3d(&ms, states ? (const void*)states : w, 128, states ? d.dv : N * C,
-                        states ? bh * N : bh, 32))
+                        states ? bh * N : bh, 32) ||
+      !make_map_bf16_3d(&my, yy ? yy : v, d.dv, d.T, bh, C) ||
+      !make_map_bf16_3d(&md, dd ? (const void*)dd : v, d.dv, d.T, bh, C))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> set{0};
   int dev = 0;
@@ -554,9 +672,9 @@ static cudaError_t launch(const Args& a, cudaStream_t st) {
   }
   WalkParams p{d, a.beta, a.log_alpha, a.scale, a.status, a.timeout_ns, a.S0,
                static_cast<const bf16*>(a.dST), a.ST, static_cast<bf16*>(a.dS0),
-               static_cast<bf16*>(a.y), BWD ? a.E : a.sv.D, static_cast<bf16*>(a.dv_), states};
+               static_cast<bf16*>(a.y), dd, states};
   walk_kernel<BWD, SPLIT><<<(unsigned)(bh * (d.dv / 128)), kThreads, L::smem, st>>>(
-      mq, mk, mv, mw, mwl, mt, mtl, mp, ms, p);
+      mq, mk, mv, mw, mwl, mt, mtl, mp, ms, my, md, p);
   count_launch();
   return cudaGetLastError();
 }
