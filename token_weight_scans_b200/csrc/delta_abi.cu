@@ -67,6 +67,7 @@ cudaError_t fwd_run(const Dims& d, const void* q, const void* k, const void* v, 
       a.sv = tc::saved_at(saved, d);
       a.m.Wb = a.sv.Wb;
       a.m.PT = a.sv.PT;
+      a.m.gates = a.sv.gates;
     }
     a.S0 = S0;
     a.y = y;
@@ -168,7 +169,7 @@ gradlev_status gradlev_delta_bwd(int B, int H, int Hk, int T, int d_k, int d_v, 
     a.dy = dy;
     a.dST = dST;
     a.E = reinterpret_cast<delta::tc::bf16*>(scratch);
-    a.dS = reinterpret_cast<delta::tc::bf16*>(scratch + up256(d.BH() * T * d_v * sizeof(delta::tc::bf16)));
+    a.dS = reinterpret_cast<delta::tc::bf16*>(scratch + delta::tc::token_rows_bytes(d));
     a.dq = dq;
     a.dk_ = dk;
     a.dv_ = dv;

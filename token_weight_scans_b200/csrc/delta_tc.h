@@ -20,6 +20,8 @@ namespace gradlev {
 namespace tc {
 bool make_map_bf16_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                       uint32_t box1);
+bool make_map_bf16_3d_box(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                          uint32_t box0, uint32_t box1);
 }
 
 namespace delta {
@@ -46,18 +48,32 @@ using bf16 = __nv_bfloat16;
 struct Mats {
   bf16 *W = nullptr, *Wlo = nullptr, *T0 = nullptr, *T0lo = nullptr, *Pb = nullptr;
   bf16 *Wb = nullptr, *PT = nullptr;
+  float* gates = nullptr;   // [B*H][N] GateBlock
 };
 
-// What the forward keeps for the backward: chunk-start states S [B*H][N][dv][128], D
-// [B*H][T][dv], Wb and PT.
+// The gates of a chunk as the kernels after prep read them (bulk copies of whole pieces).
+struct GateBlock {
+  float bw[C];        // beta w
+  float GC, fac;      // fac != 0: M_ij = ra_i ca_j
+  float pad[2];
+  float q[C];         // scale G
+  float bG[C];        // -beta G
+  float be[C];        // beta
+  float ra[C], cb[C]; // cb = ca beta
+};
+
+// What the forward keeps for the backward: chunk-start states S [B*H][N][dv][128], D^T
+// [B*H][N][dv][64] (the tokens of a chunk contiguous, as the walk has them), Wb, PT and gates.
 struct Saved {
   bf16 *S = nullptr, *D = nullptr, *Wb = nullptr, *PT = nullptr;
+  float* gates = nullptr;
 };
 size_t saved_bytes(const Dims& d);
 Saved saved_at(char* base, const Dims& d);
-size_t fwd_scratch_bytes(const Dims& d);  // W, Wlo, T0, T0lo, Pb
+size_t fwd_scratch_bytes(const Dims& d);  // W, Wlo, T0, T0lo, Pb, gates
 Mats mats_at(char* base, const Dims& d);
 size_t bwd_scratch_bytes(const Dims& d);  // E and the chunk-end gradients of the state
+size_t token_rows_bytes(const Dims& d);   // one of D^T, E^T
 
 struct Args {
   Dims d;
@@ -73,7 +89,7 @@ struct Args {
   float* ST = nullptr;
   const void* dy = nullptr;
   const void* dST = nullptr;
-  bf16* E = nullptr;        // [B*H][T][dv]
+  bf16* E = nullptr;        // E^T, like D^T
   bf16* dS = nullptr;       // [B*H][N][dv][128]: gradient of the chunk-end states
   void *dq = nullptr, *dk_ = nullptr, *dv_ = nullptr, *dbeta = nullptr, *dlog_alpha = nullptr;
   void* dS0 = nullptr;
@@ -100,7 +116,10 @@ __device__ __forceinline__ GatePair chunk_gates(const float* beta, const float* 
                                                 size_t row, int t0, int T) {
   const int lane = threadIdx.x & 31;
   GatePair g;
-  double L[2];
+  // The running sum in 64-bit integers of 2^-40: exact, and no matter how strong the decays
+  // are (a float32 sum would leave 1e-4 in the differences at L = -64 * 87). The two halves
+  // of the chunk go side by side.
+  long long L[2];
   unsigned m[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
@@ -108,12 +127,16 @@ __device__ __forceinline__ GatePair chunk_gates(const float* beta, const float* 
     const float la = t < T ? log_alpha[row + t] : 0.f;
     g.be[k] = t < T ? beta[row + t] : 0.f;
     const bool reset = la < kResetLog;
-    L[k] = reset ? 0.0 : (double)la;
+    L[k] = reset ? 0 : __float2ll_rn(la * 0x1p40f);
     m[k] = __ballot_sync(0xffffffffu, reset);
+  }
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double u = __shfl_up_sync(0xffffffffu, L[k], o);
-      if (lane >= o) L[k] += u;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u0 = __shfl_up_sync(0xffffffffu, L[0], o);
+    const long long u1 = __shfl_up_sync(0xffffffffu, L[1], o);
+    if (lane >= o) {
+      L[0] += u0;
+      L[1] += u1;
     }
   }
   L[1] += __shfl_sync(0xffffffffu, L[0], 31);
@@ -121,14 +144,15 @@ __device__ __forceinline__ GatePair chunk_gates(const float* beta, const float* 
   g.seg[0] = __popc(m[0] & below);
   g.seg[1] = __popc(m[0]) + __popc(m[1] & below);
   g.seg_end = __popc(m[0]) + __popc(m[1]);
-  const double end = __shfl_sync(0xffffffffu, L[1], 31);
+  const long long end = __shfl_sync(0xffffffffu, L[1], 31);
+  auto split = [](long long v, float& hi, float& lo) {
+    hi = __ll2float_rn(v);
+    lo = __ll2float_rn(v - __float2ll_rn(hi)) * 0x1p-40f;
+    hi *= 0x1p-40f;
+  };
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    g.Lh[k] = (float)L[k];
-    g.Ll[k] = (float)(L[k] - (double)g.Lh[k]);
-  }
-  g.Lend = (float)end;
-  g.Lend_lo = (float)(end - (double)g.Lend);
+  for (int k = 0; k < 2; ++k) split(L[k], g.Lh[k], g.Ll[k]);
+  split(end, g.Lend, g.Lend_lo);
   return g;
 }
 // G_i, w_i and G_C

@@ -37,7 +37,8 @@ constexpr uint32_t COL_B = 128;   // F, H (64 columns each) | z, then xk | ka
 
 struct GradSmem {
   uint8_t Q[2 * TILE], K[2 * TILE];          // k-blocks; at the end dq and dk
-  uint8_t O[TILE], D[TILE], E[TILE];         // 64 tokens x 64 columns of d_v
+  uint8_t O[TILE];                           // dY: 64 tokens x 64 columns of d_v
+  uint8_t D[TILE], E[TILE];                  // D^T, E^T: 64 rows of d_v x 64 tokens
   uint8_t S[2 * TILE], dS[2 * TILE];         // 64 rows of d_v x 128
   uint8_t X[TILE], Yn[TILE];
   float Lh[C], Ll[C], be[C], cq[C], ck[C], cz[C];
@@ -58,7 +59,7 @@ enum : uint32_t { W_G_KQ = 0xa01, W_G_FULL, W_G_MMA };
 
 struct GradParams {
   Dims d;
-  const float *beta, *log_alpha;
+  const float *beta, *log_alpha, *gates;
   float scale;
   DeviceStatus* status;
   uint64_t timeout_ns;
@@ -121,7 +122,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_after();
   const uint32_t tb = sm.tmem_base;
   const uint32_t sQ = smem_u32(sm.Q), sK = smem_u32(sm.K), sX = smem_u32(sm.X), sY = smem_u32(sm.Yn);
-  const uint32_t id_f = idesc_bf16(64, 64, false, false), id_t = idesc_bf16(64, 128, false, true);
+  const uint32_t id_f = idesc_bf16(64, 64, false, true), id_h = idesc_bf16(64, 64, true, true);
+  const uint32_t id_t = idesc_bf16(64, 128, false, true);
   const uint32_t id_m = idesc_bf16(64, 128, true, true);
   uint32_t nfull = 0, nmma = 0;  // phases so far
   const int nsl = p.d.dv / 64;
@@ -133,27 +135,30 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int hv = 0; hv < grp; ++hv) {
     const int bh = b * p.d.H + (kh - b * p.d.Hk) * grp + hv;
     if (warp == 2) {
-      const GatePair g = chunk_gates(p.beta, p.log_alpha, (size_t)bh * T, t0, T);
-      const float Lm = __shfl_sync(0xffffffffu, g.Lh[0], 31), Ll = __shfl_sync(0xffffffffu, g.Ll[0], 31);
-      const bool fac = g.seg_end == 0 && g.Lend > -80.f;
+      const GateBlock* gb = reinterpret_cast<const GateBlock*>(p.gates) + (size_t)bh * N + n;
+      const bool fac = gb->fac != 0.f;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int j = lane + 32 * k;
-        const float G = gate_G(g, k);
-        const float x = (g.Lh[k] - Lm) + (g.Ll[k] - Ll);
-        sm.ra[j] = fac ? expf(x) : 1.f;
-        sm.ca[j] = fac ? expf(-x) * g.be[k] : g.be[k];
-        sm.Lh[j] = g.Lh[k];
-        sm.Ll[j] = g.Ll[k];
-        sm.seg[j] = g.seg[k];
-        sm.be[j] = g.be[k];
-        sm.cq[j] = p.scale * G;
-        sm.ck[j] = g.be[k] * G;
-        sm.cz[j] = g.be[k] * gate_w(g, k);
+        sm.be[j] = gb->be[j];
+        sm.cq[j] = gb->q[j];
+        sm.ck[j] = gb->bG[j];
+        sm.cz[j] = gb->bw[j];
+        sm.ra[j] = gb->ra[j];
+        sm.ca[j] = gb->cb[j];
       }
       if (lane == 0) {
-        sm.GC = gate_GC(g);
+        sm.GC = gb->GC;
         sm.fac = fac;
+      }
+      if (!fac) {
+        const GatePair g = chunk_gates(p.beta, p.log_alpha, (size_t)bh * T, t0, T);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          sm.Lh[lane + 32 * k] = g.Lh[k];
+          sm.Ll[lane + 32 * k] = g.Ll[k];
+          sm.seg[lane + 32 * k] = g.seg[k];
+        }
       }
     }
     float ss = 0.f;  // <dS, S>
@@ -161,8 +166,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (tid == 0) {
         mbar_arrive_expect_tx(&sm.full, 7 * TILE);
         tma_load_3d(sm.O, &tmO, &sm.full, 64 * sl, t0, bh);
-        tma_load_3d(sm.D, &tmD, &sm.full, 64 * sl, t0, bh);
-        tma_load_3d(sm.E, &tmE, &sm.full, 64 * sl, t0, bh);
+        tma_load_3d(sm.D, &tmD, &sm.full, 0, 64 * sl, bh * N + n);
+        tma_load_3d(sm.E, &tmE, &sm.full, 0, 64 * sl, bh * N + n);
         for (int kb = 0; kb < 2; ++kb) {
           tma_load_3d(sm.S + kb * TILE, &tmS, &sm.full, 64 * kb, 64 * sl, bh * N + n);
           tma_load_3d(sm.dS + kb * TILE, &tmdS, &sm.full, 64 * kb, 64 * sl, bh * N + n);
@@ -176,15 +181,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int kk = 0; kk < 4; ++kk) {
           const uint32_t on = (sl > 0 || kk > 0) ? 1u : 0u;
           const uint64_t ao = desc_at(sw128_desc(sO, 16, 1024), kk * 32);
-          const uint64_t ad = desc_at(sw128_desc(sD, 16, 1024), kk * 32);
-          const uint64_t ae = desc_at(sw128_desc(sE, 16, 1024), kk * 32);
+          const uint64_t ad = desc_at(sw128_desc(sD, TILE, 1024), kk * 2048);
+          const uint64_t ae = desc_at(sw128_desc(sE, TILE, 1024), kk * 2048);
           const uint64_t bs = desc_at(sw128_desc(smem_u32(sm.S), TILE, 1024), kk * 2048);
           const uint64_t bd = desc_at(sw128_desc(smem_u32(sm.dS), TILE, 1024), kk * 2048);
           umma_bf16(tb + COL_B, ao, ad, id_f, on);                  // F
-          umma_bf16(tb + COL_B + 64, ae, ad, id_f, on);             // H
+          umma_bf16(tb + COL_B + 64, ae, ad, id_h, on);             // H
           umma_bf16(tb + COL_A, ao, bs, id_t, on);                  // t
-          umma_bf16(tb + COL_A + LANE16, ae, bs, id_t, on);         // u
-          umma_bf16(tb + COL_B + LANE16, ad, bd, id_t, on);         // z
+          umma_bf16(tb + COL_A + LANE16, ae, bs, id_m, on);         // u
+          umma_bf16(tb + COL_B + LANE16, ad, bd, id_m, on);         // z
         }
         umma_commit(&sm.mma);
       }
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
     // ---- t (lower) and u (upper); z (upper)
     const uint32_t mine = up ? sK + hh * TILE : sQ + hh * TILE;
-    const float ca = up ? -sm.ck[i] : sm.cq[i], cz = up ? sm.cz[i] : 0.f;
+    const float ca = up ? sm.ck[i] : sm.cq[i], cz = up ? sm.cz[i] : 0.f;
     float xs = 0.f, zs = 0.f;
 #pragma unroll
     for (int hf = 0; hf < 4; ++hf) {
@@ -403,8 +408,8 @@ cudaError_t launch_grad(const Args& a, cudaStream_t st) {
   CUtensorMap mq, mk, mo, md, me, ms, mds, mdq, mdk;
   if (!make_map_bf16_3d(&mq, a.q, 128, d.T, kh, C) || !make_map_bf16_3d(&mk, a.k, 128, d.T, kh, C) ||
       !make_map_bf16_3d(&mo, a.dy, d.dv, d.T, bh, C) ||
-      !make_map_bf16_3d(&md, a.sv.D, d.dv, d.T, bh, C) ||
-      !make_map_bf16_3d(&me, a.E, d.dv, d.T, bh, C) ||
+      !make_map_bf16_3d(&md, a.sv.D, C, d.dv, bh * N, 64) ||
+      !make_map_bf16_3d(&me, a.E, C, d.dv, bh * N, 64) ||
       !make_map_bf16_3d(&ms, a.sv.S, 128, d.dv, bh * N, 64) ||
       !make_map_bf16_3d(&mds, a.dS, 128, d.dv, bh * N, 64) ||
       !make_map_bf16_3d(&mdq, a.dq, 128, d.T, kh, C) ||
@@ -420,7 +425,7 @@ cudaError_t launch_grad(const Args& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     set.fetch_or(bit);
   }
-  GradParams p{d, a.beta, a.log_alpha, a.scale, a.status, a.timeout_ns,
+  GradParams p{d, a.beta, a.log_alpha, a.sv.gates, a.scale, a.status, a.timeout_ns,
                static_cast<bf16*>(a.dbeta), static_cast<bf16*>(a.dlog_alpha)};
   grad_kernel<<<(unsigned)(N * kh), kThreads, kSmem, st>>>(mq, mk, mo, md, me, ms, mds, mdq, mdk, p);
   count_launch();
@@ -435,22 +440,27 @@ static bf16* take(char*& at, size_t elems) {
   at += up256(elems * sizeof(bf16));
   return p;
 }
+static size_t gate_bytes(const Dims& d) {
+  return up256(d.BH() * chunks(d.T) * sizeof(GateBlock));
+}
+size_t token_rows_bytes(const Dims& d) { return up256(d.BH() * chunks(d.T) * d.dv * C * sizeof(bf16)); }
 
 Saved saved_at(char* base, const Dims& d) {
   const size_t rows = d.BH() * chunks(d.T);
   char* at = base;
   Saved s;
   s.S = take(at, rows * d.dv * 128);
-  s.D = take(at, d.BH() * (size_t)d.T * d.dv);
+  s.D = take(at, rows * d.dv * C);
   s.Wb = take(at, rows * C * 128);
   s.PT = take(at, rows * C * C);
+  s.gates = reinterpret_cast<float*>(at);
   return s;
 }
 
 size_t saved_bytes(const Dims& d) {
   const size_t rows = d.BH() * chunks(d.T);
-  return up256(rows * d.dv * 256) + up256(d.BH() * (size_t)d.T * d.dv * 2) +
-         up256(rows * C * 256) + up256(rows * C * C * 2);
+  return up256(rows * d.dv * 256) + token_rows_bytes(d) + up256(rows * C * 256) +
+         up256(rows * C * C * 2) + gate_bytes(d);
 }
 
 Mats mats_at(char* base, const Dims& d) {
@@ -462,16 +472,17 @@ Mats mats_at(char* base, const Dims& d) {
   m.T0 = take(at, rows * C * C);
   m.T0lo = take(at, rows * C * C);
   m.Pb = take(at, rows * C * C);
+  m.gates = reinterpret_cast<float*>(at);
   return m;
 }
 
 size_t fwd_scratch_bytes(const Dims& d) {
   const size_t rows = d.BH() * chunks(d.T);
-  return 2 * up256(rows * C * 256) + 3 * up256(rows * C * C * 2);
+  return 2 * up256(rows * C * 256) + 3 * up256(rows * C * C * 2) + gate_bytes(d);
 }
 
 size_t bwd_scratch_bytes(const Dims& d) {
-  return up256(d.BH() * (size_t)d.T * d.dv * 2) + up256(d.BH() * chunks(d.T) * d.dv * 256);
+  return token_rows_bytes(d) + up256(d.BH() * chunks(d.T) * d.dv * 256);
 }
 
 cudaError_t run_fwd(const Args& a, cudaStream_t st) {

@@ -120,6 +120,11 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const __grid_constant
     const GatePair g = chunk_gates(p.beta, p.log_alpha, (size_t)bh * p.d.T, t0, p.d.T);
     const float Lm = __shfl_sync(0xffffffffu, g.Lh[0], 31), Ll = __shfl_sync(0xffffffffu, g.Ll[0], 31);
     const bool fac = g.seg_end == 0 && g.Lend > -80.f;
+    GateBlock* gb = reinterpret_cast<GateBlock*>(p.m.gates) + (size_t)bh * N + n;
+    if (lane == 0) {
+      gb->GC = gate_GC(g);
+      gb->fac = fac ? 1.f : 0.f;
+    }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int i = lane + 32 * k;
@@ -134,8 +139,15 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const __grid_constant
       sm.seg[i] = g.seg[k];
       sm.be[i] = be;
       sm.rb[i] = 1.f / bt;
-      sm.G[i] = gate_G(g, k);
-      sm.w[i] = gate_w(g, k);
+      const float G = gate_G(g, k), w = gate_w(g, k);
+      sm.G[i] = G;
+      sm.w[i] = w;
+      gb->bw[i] = be * w;
+      gb->q[i] = p.scale * G;
+      gb->bG[i] = -be * G;
+      gb->be[i] = be;
+      gb->ra[i] = sm.ra[i];
+      gb->cb[i] = ca * be;
     }
     if (lane == 0) sm.fac = fac;
   }

@@ -19,10 +19,14 @@
 // one, so that S carries 16 bits through the chunks and the float32 state it ends with is
 // good to 1e-5. Training needs no such state and takes single products.
 //
-// Warp roles (16): 0 TMA producer, 1 MMA issuer (owns TMEM), 2 gates, 4-11 two chain
-// warpgroups (each half of the columns), 12-15 scaling of Q and K, and the outputs: 16-lane
-// TMEM loads in the layout of 8 x 8 fragments, transposed on the way to shared memory
-// (stmatrix) so that tokens become rows, and TMA stores.
+// Warp roles (16): 0 and 3 TMA producers, 1 MMA issuer (owns TMEM), 2 copies the gates in,
+// 4-11 two chain warpgroups (each half of the columns), which also leave S and D^T (E^T) for
+// the kernels after, 12-15 scaling of Q by scale G, and Y (dV): 16-lane TMEM loads in the
+// layout of 8 x 8 fragments, transposed on the way to shared memory (stmatrix) so that tokens
+// become rows, and TMA stores. D^T and E^T stay as they are, a chunk's tokens contiguous.
+//
+// Each chunk's tiles come in three groups with a two-deep ring of their own, since they are
+// done with at different times: V (dY) with T0 (PT), W with Q, K with Pb.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -40,7 +44,7 @@ using namespace sm100;
 namespace {
 
 constexpr int NS = 2;             // TMA stages
-constexpr int GS = 4;             // gate slots
+constexpr int GS = 3;             // gate slots
 constexpr int kThreads = 512;
 
 // TMEM columns
@@ -52,38 +56,53 @@ constexpr uint32_t COL_D = 256;    // D^T (E^T) accumulator, 64, and Y^T, 64; tw
 constexpr uint32_t COL_SL = 384;   // SPLIT (one pair): remainder of the state, 64,
 constexpr uint32_t COL_UL = 448;   // and of beta w D, 32
 
-struct GateSlot {
-  float q[C];    // scale G
-  float u[C];    // forward: beta w; backward: -beta G
-  float be[C];   // beta
-  float GC;
-  float pad[3];
+// A chunk's gates: the piece of GateBlock that the direction needs, as it lies there.
+template <bool BWD> struct GateSlot;
+template <> struct GateSlot<false> {
+  float u[C], GC, pad[3], q[C];         // bw .. q
+  static constexpr int offset = 0;
 };
+template <> struct GateSlot<true> {
+  float GC, pad[3], q[C], u[C], be[C];  // GC .. be
+  static constexpr int offset = C * sizeof(float);
+};
+static_assert(sizeof(GateSlot<false>) % 16 == 0 && sizeof(GateSlot<true>) % 16 == 0 &&
+              sizeof(GateBlock) % 16 == 0, "bulk copies");
 
+template <bool BWD>
 struct Bars {
-  GateSlot gates[GS];
-  uint64_t full[NS], empty[NS], scaled[NS];
+  GateSlot<BWD> gates[GS];
+  uint64_t full[3][NS], empty[3][NS];   // per group of tiles
+  uint64_t scaled[NS];
   uint64_t gfull[GS], gempty[GS];
   uint64_t sready, dfull, uready, sfull, done;
-  uint64_t yfull[2], yfree[2];   // per accumulator pair
+  uint64_t yfull[2], yfree[2];          // per accumulator pair
   uint32_t tmem_base;
   int abort;
 };
+enum { VT = 0, WQ = 1, KP = 2 };
 
-// Stage: per 64 columns of d_k the W (Wb) tile and the Q tile next to each other (128 rows of
-// one operand), then K and V (dY) tiles of 2 TILE, T0 (PT), Pb; SPLIT adds the remainders of W
-// and T0.
+// The rings. VT: V (dY), T0 (PT), SPLIT also the remainder of T0. WQ: per 64 columns of d_k the
+// W (Wb) tile and the Q tile next to each other (128 rows of one operand), SPLIT also the
+// remainder of W. KP: K, forward also Pb.
 template <bool BWD, bool SPLIT>
 struct Layout {
-  static constexpr int w = 0, q = TILE, wq = 2 * TILE;   // wq: from one k-block to the next
-  static constexpr int k = 4 * TILE, v = 6 * TILE, t = 8 * TILE, p = 9 * TILE;
-  static constexpr int wl = 10 * TILE, tl = 12 * TILE;
-  static constexpr int bytes = BWD ? 9 * TILE : (SPLIT ? 13 * TILE : 10 * TILE);
-  static constexpr bool staged = !SPLIT;   // states and outputs through shared memory and TMA
-  static constexpr int stage_s = NS * bytes, stage_o = stage_s + (staged ? 2 * BIG : 0);
-  static constexpr int bars = stage_o + (staged ? 2 * TILE : 0);
-  static constexpr size_t smem = bars + sizeof(Bars) + 1024;
+  static constexpr int v = 0, t = 2 * TILE, tl = 3 * TILE;
+  static constexpr int w = 0, q = TILE, wq = 2 * TILE, wl = 4 * TILE;  // wq: between k-blocks
+  static constexpr int k = 0, p = 2 * TILE;
+  static constexpr int vt_bytes = SPLIT ? 4 * TILE : 3 * TILE;
+  static constexpr int wq_bytes = SPLIT ? 6 * TILE : 4 * TILE;
+  static constexpr int kp_bytes = BWD ? 2 * TILE : 3 * TILE;
+  static constexpr int wq0 = NS * vt_bytes, kp0 = wq0 + NS * wq_bytes;
+  static constexpr bool staged = !SPLIT;   // S and D^T through shared memory and TMA
+  static constexpr int stage_s = kp0 + NS * kp_bytes, stage_o = stage_s + (staged ? 2 * BIG : 0);
+  static constexpr int stage_d = stage_o + 2 * TILE;
+  static constexpr int bars = stage_d + (staged ? 2 * TILE : 0);  // (SPLIT: Y alone is staged)
+  static constexpr size_t smem = bars + sizeof(Bars<BWD>) + 1024;
   static_assert(smem <= 227 * 1024, "over the shared memory of a CTA");
+  static constexpr int vt(int s) { return s * vt_bytes; }
+  static constexpr int wq_at(int s) { return wq0 + s * wq_bytes; }
+  static constexpr int kp(int s) { return kp0 + s * kp_bytes; }
 };
 
 enum : uint32_t {
@@ -93,8 +112,7 @@ enum : uint32_t {
 
 struct WalkParams {
   Dims d;
-  const float *beta, *log_alpha;
-  float scale;
+  const float* gates;
   DeviceStatus* status;
   uint64_t timeout_ns;
   const float* S0;       // forward start
@@ -102,9 +120,18 @@ struct WalkParams {
   float* ST;             // forward end
   bf16* dS0;             // backward end
   bf16* y;               // forward
-  bf16* D;               // forward: D, backward: E (null: not kept)
+  bf16* D;               // forward: D^T, backward: E^T (null: not kept)
   bf16* states;          // chunk-start (chunk-end) states, or null
 };
+
+// Untiled bulk copy global -> shared (addresses and size multiples of 16 bytes).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
 
 __device__ __forceinline__ void st_tmem32(uint32_t col, const uint32_t (&r)[32]) {
   float v[32];
@@ -137,17 +164,19 @@ __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t nthreads, boo
 }
 
 // x *= factor[row] on a [64 tokens x 128] tile in place (its k-blocks `step` bytes apart), by
-// 128 threads.
+// 128 threads; the loads go out together.
 __device__ __forceinline__ void scale_tile(uint32_t tile, uint32_t step, const float* factor, int t) {
+  uint4 v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = ld_shared_v4(tile + (k >> 2) * step + (t + 128 * (k & 3)) * 16);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const uint32_t in = (uint32_t)(t + 128 * (k & 3)) * 16, off = (k >> 2) * step + in;
+    const uint32_t in = (uint32_t)(t + 128 * (k & 3)) * 16;
     const float f = factor[in >> 7];
-    const uint4 v = ld_shared_v4(tile + off);
-    st_shared_v4(tile + off, pack_bf16(f * bf16_lo(v.x), f * bf16_hi(v.x)),
-                 pack_bf16(f * bf16_lo(v.y), f * bf16_hi(v.y)),
-                 pack_bf16(f * bf16_lo(v.z), f * bf16_hi(v.z)),
-                 pack_bf16(f * bf16_lo(v.w), f * bf16_hi(v.w)));
+    st_shared_v4(tile + (k >> 2) * step + in, pack_bf16(f * bf16_lo(v[k].x), f * bf16_hi(v[k].x)),
+                 pack_bf16(f * bf16_lo(v[k].y), f * bf16_hi(v[k].y)),
+                 pack_bf16(f * bf16_lo(v[k].z), f * bf16_hi(v[k].z)),
+                 pack_bf16(f * bf16_lo(v[k].w), f * bf16_hi(v[k].w)));
   }
 }
 
@@ -205,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  Bars& sm = *reinterpret_cast<Bars*>(base + L::bars);
+  Bars<BWD>& sm = *reinterpret_cast<Bars<BWD>*>(base + L::bars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ns = p.d.dv >> 7, bh = blockIdx.x / ns, n0 = (blockIdx.x - bh * ns) * 128;
   const int b = bh / p.d.H, h = bh - b * p.d.H;
@@ -217,13 +246,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     sm.abort = 0;
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], 1);
+      for (int r = 0; r < 3; ++r) {
+        mbar_init(&sm.full[r][s], 1);
+        mbar_init(&sm.empty[r][s], 1);
+      }
       mbar_init(&sm.scaled[s], 4);
     }
     for (int g = 0; g < GS; ++g) {
-      mbar_init(&sm.gfull[g], 32);
-      mbar_init(&sm.gempty[g], 12);  // 8 chain warps, 4 scaling warps
+      mbar_init(&sm.gfull[g], 1);
+      mbar_init(&sm.gempty[g], 12);  // the chain's 8 warps, 4 that scale Q
     }
     mbar_init(&sm.sready, 8);
     mbar_init(&sm.dfull, 1);
@@ -245,29 +276,48 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tb = sm.tmem_base;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
+  if (warp == 0 || warp == 3) {
+    // ------------------------------------------------------------ TMA producers
+    // warp 0: V with T0, and K with Pb; warp 3: W with Q
     if (lane == 0) {
-      int issued = 0;
+      int issued[3] = {0, 0, 0};
+      auto open = [&](int r, int c, int bytes) -> bool {
+        if (!mbar_wait(&sm.empty[r][c % NS], ((c / NS) & 1) ^ 1, wc, W_TMA)) return false;
+        mbar_arrive_expect_tx(&sm.full[r][c % NS], bytes);
+        issued[r] = c + 1;
+        return true;
+      };
       for (int c = 0; c < N; ++c) {
-        const int s = c % NS, n = cg(c), t0 = n * C;
-        if (!mbar_wait(&sm.empty[s], ((c / NS) & 1) ^ 1, wc, W_TMA)) break;
-        uint8_t* st = base + s * L::bytes;
-        mbar_arrive_expect_tx(&sm.full[s], L::bytes);
-        for (int kb = 0; kb < 2; ++kb) {
-          tma_load_3d(st + L::v + kb * TILE, &tmV, &sm.full[s], n0 + 64 * kb, t0, bh);
-          tma_load_3d(st + L::w + kb * L::wq, &tmW, &sm.full[s], 64 * kb, t0, bh);
-          tma_load_3d(st + L::q + kb * L::wq, &tmQ, &sm.full[s], 64 * kb, t0, kh);
-          tma_load_3d(st + L::k + kb * TILE, &tmK, &sm.full[s], 64 * kb, t0, kh);
-          if (SPLIT) tma_load_3d(st + L::wl + kb * TILE, &tmWl, &sm.full[s], 64 * kb, t0, bh);
+        const int s = c % NS, t0 = cg(c) * C;
+        if (warp == 0) {
+          uint8_t* a = base + L::vt(s);
+          uint64_t* f = &sm.full[VT][s];
+          if (!open(VT, c, L::vt_bytes)) break;
+          tma_load_3d(a + L::v, &tmV, f, n0, t0, bh);
+          tma_load_3d(a + L::v + TILE, &tmV, f, n0 + 64, t0, bh);
+          tma_load_3d(a + L::t, &tmT, f, 0, t0, bh);
+          if (SPLIT) tma_load_3d(a + L::tl, &tmTl, f, 0, t0, bh);
+          a = base + L::kp(s);
+          f = &sm.full[KP][s];
+          if (!open(KP, c, L::kp_bytes)) break;
+          tma_load_3d(a + L::k, &tmK, f, 0, t0, kh);
+          tma_load_3d(a + L::k + TILE, &tmK, f, 64, t0, kh);
+          if (!BWD) tma_load_3d(a + L::p, &tmP, f, 0, t0, bh);
+        } else {
+          uint8_t* a = base + L::wq_at(s);
+          uint64_t* f = &sm.full[WQ][s];
+          if (!open(WQ, c, L::wq_bytes)) break;
+          for (int kb = 0; kb < 2; ++kb) {
+            tma_load_3d(a + L::q + kb * L::wq, &tmQ, f, 64 * kb, t0, kh);
+            tma_load_3d(a + L::w + kb * L::wq, &tmW, f, 64 * kb, t0, bh);
+            if (SPLIT) tma_load_3d(a + L::wl + kb * TILE, &tmWl, f, 64 * kb, t0, bh);
+          }
         }
-        tma_load_3d(st + L::t, &tmT, &sm.full[s], 0, t0, bh);
-        if (!BWD) tma_load_3d(st + L::p, &tmP, &sm.full[s], 0, t0, bh);
-        if (SPLIT) tma_load_3d(st + L::tl, &tmTl, &sm.full[s], 0, t0, bh);
-        issued = c + 1;
       }
-      for (int c = issued > NS ? issued - NS : 0; c < issued; ++c)
-        mbar_drain(&sm.full[c % NS], (c / NS) & 1, wc, W_TMA_DRAIN);
+      // teardown: every load issued has landed
+      for (int r = 0; r < 3; ++r)
+        for (int c = issued[r] > NS ? issued[r] - NS : 0; c < issued[r]; ++c)
+          mbar_drain(&sm.full[r][c % NS], (c / NS) & 1, wc, W_TMA_DRAIN);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -281,9 +331,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (uready, waited by then) and the outputs have been taken.
       auto first = [&](int c) -> bool {
         const int s = c % NS;
-        const uint32_t st = smem_u32(base + s * L::bytes), d = tb + COL_D + 128 * (c % NY);
-        if (!mbar_wait(&sm.full[s], (c / NS) & 1, wc, W_FULL)) return false;
-        if ((!SPLIT || p.D) && !mbar_wait(&sm.yfree[c % NY], ((c / NY) & 1) ^ 1, wc, W_YFREE)) return false;
+        const uint32_t st = smem_u32(base + L::vt(s)), d = tb + COL_D + 128 * (c % NY);
+        if (!mbar_wait(&sm.full[VT][s], (c / NS) & 1, wc, W_FULL)) return false;
+        if (!SPLIT && !mbar_wait(&sm.yfree[c % NY], ((c / NY) & 1) ^ 1, wc, W_YFREE)) return false;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
@@ -292,12 +342,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_bf16(d, av, desc_at(sw128_desc(st + L::t, BWD ? TILE : 16, 1024), off), id_v, kk > 0);
           if (SPLIT) umma_bf16(d, av, desc_at(sw128_desc(st + L::tl, 16, 1024), off), id_v, 1);
         }
+        if (!BWD) umma_commit(&sm.empty[VT][s]);
         return true;
       };
       bool ok = first(0);
       for (int c = 0; c < N && ok; ++c) {
         const int s = c % NS, yb = c % NY;
-        const uint32_t st = smem_u32(base + s * L::bytes);
+        const uint32_t st = smem_u32(base + L::wq_at(s)), sv = smem_u32(base + L::vt(s));
+        const uint32_t sk = smem_u32(base + L::kp(s));
         const uint32_t d = tb + COL_D + 128 * yb, y = d + 64;
         if (!mbar_wait(&sm.scaled[s], (c / NS) & 1, wc, W_SCALED)) break;
         if (!mbar_wait(&sm.sready, c & 1, wc, W_SREADY)) break;
@@ -324,8 +376,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit(&sm.yfull[yb]);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)  // S += dY^T (scale G Q): S is scaled (sready)
-            umma_bf16(tb + COL_S, desc_at(sw128_desc(st + L::v, TILE, 1024), kk * 2048),
+            umma_bf16(tb + COL_S, desc_at(sw128_desc(sv + L::v, TILE, 1024), kk * 2048),
                       desc_at(sw128_desc(st + L::q, L::wq, 1024), kk * 2048), id_o, 1);
+          umma_commit(&sm.empty[VT][s]);
+          umma_commit(&sm.empty[WQ][s]);
         } else if (SPLIT) {  // Y^T = S Q^T, which frees the bf16 state
           if (!mbar_wait(&sm.yfree[0], (c & 1) ^ 1, wc, W_YFREE)) break;
           tc_fence_after();
@@ -334,26 +388,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_bf16_tmem_a(y, tb + COL_SH + 8 * kk,
                              desc_at(sw128_desc(st + L::q, 16, 1024), (kk >> 2) * L::wq + (kk & 3) * 32),
                              id_w, kk > 0);
-        } else if (c + 1 < N && !first(c + 1)) {
-          break;
+          umma_commit(&sm.empty[WQ][s]);
+        } else {
+          umma_commit(&sm.empty[WQ][s]);
+          if (c + 1 < N && !first(c + 1)) break;
         }
+        if (!mbar_wait(&sm.full[KP][s], (c / NS) & 1, wc, W_FULL)) break;
         if (!mbar_wait(&sm.uready, c & 1, wc, W_UREADY)) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {  // S += U^T K
-          const uint64_t bk = desc_at(sw128_desc(st + L::k, TILE, 1024), kk * 2048);
-          umma_bf16_tmem_a(tb + COL_S, tb + (BWD ? COL_DB : COL_U) + 8 * kk, bk, id_u, 1);
+          const uint64_t bk = desc_at(sw128_desc(sk + L::k, TILE, 1024), kk * 2048);
+          umma_bf16_tmem_a(tb + COL_S, tb + COL_U + 8 * kk, bk, id_u, 1);
           if (SPLIT) umma_bf16_tmem_a(tb + COL_S, tb + COL_UL + 8 * kk, bk, id_u, 1);
         }
         umma_commit(&sm.sfull);
         if (!BWD) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)  // Y^T += D^T Pb^T
-            umma_bf16_tmem_a(y, tb + COL_DB + 8 * kk, desc_at(sw128_desc(st + L::p, 16, 1024), kk * 32),
+            umma_bf16_tmem_a(y, tb + COL_DB + 8 * kk, desc_at(sw128_desc(sk + L::p, 16, 1024), kk * 32),
                              id_w, 1);
           umma_commit(&sm.yfull[yb]);
         }
-        umma_commit(&sm.empty[s]);
+        umma_commit(&sm.empty[KP][s]);
         if ((BWD || SPLIT) && c + 1 < N) ok = first(c + 1);
       }
       umma_commit(&sm.done);
@@ -361,22 +418,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ gates
-    for (int c = 0; c < N; ++c) {
-      const int g = c % GS;
-      const GatePair gp = chunk_gates(p.beta, p.log_alpha, (size_t)bh * T, cg(c) * C, T);
-      if (!mbar_wait_warp(&sm.gempty[g], ((c / GS) & 1) ^ 1, wc, W_GATE)) break;
-      GateSlot& gs = sm.gates[g];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int i = lane + 32 * k;
-        const float G = gate_G(gp, k);
-        gs.q[i] = p.scale * G;
-        gs.u[i] = BWD ? -gp.be[k] * G : gp.be[k] * gate_w(gp, k);
-        gs.be[i] = gp.be[k];
+    if (lane == 0) {
+      const char* src = reinterpret_cast<const char*>(p.gates) + GateSlot<BWD>::offset;
+      int issued = 0;
+      for (int c = 0; c < N; ++c) {
+        const int g = c % GS;
+        if (!mbar_wait(&sm.gempty[g], ((c / GS) & 1) ^ 1, wc, W_GATE)) break;
+        mbar_arrive_expect_tx(&sm.gfull[g], sizeof(GateSlot<BWD>));
+        bulk_load(&sm.gates[g], src + ((size_t)bh * N + cg(c)) * sizeof(GateBlock),
+                  sizeof(GateSlot<BWD>), &sm.gfull[g]);
+        issued = c + 1;
       }
-      if (lane == 0) gs.GC = gate_GC(gp);
-      __syncwarp();
-      mbar_arrive(&sm.gfull[g]);
+      for (int c = issued > GS ? issued - GS : 0; c < issued; ++c)
+        mbar_drain(&sm.gfull[c % GS], (c / GS) & 1, wc, W_TMA_DRAIN);
     }
   } else if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------ the chain
@@ -420,8 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_st_wait();
     bool ok = true;
     for (int c = 0; c < N && ok; ++c) {
-      const int g = c % GS, n = cg(c), t0 = n * C;
-      const GateSlot& gs = sm.gates[g];
+      const int g = c % GS, n = cg(c);
+      const GateSlot<BWD>& gs = sm.gates[g];
       ok = mbar_wait_warp(&sm.gfull[g], (c / GS) & 1, wc, W_C_GATE);
       // every product of chunk c - 1 that reads the bf16 state was issued before this commit
       ok = ok && (c == 0 || mbar_wait_warp(&sm.sfull, (c - 1) & 1, wc, W_C_SFULL));
@@ -481,27 +535,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       float v[32];
       tmem_ld32(tb + COL_D + 128 * (c % NY) + lo + 32 * hh, v);
       tmem_ld_wait();
-      uint32_t db[16];
+      uint32_t db[16];  // D (E) in bf16: 32 tokens of this row
       {
         uint32_t ub[16], rest[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
+          const float2 f = *reinterpret_cast<const float2*>(gs.u + 32 * hh + 2 * e);
+          const float u0 = v[2 * e] * f.x, u1 = v[2 * e + 1] * f.y;
+          ub[e] = pack_bf16(u0, u1);
           db[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-          if (!BWD) {
-            const float u0 = v[2 * e] * gs.u[32 * hh + 2 * e];
-            const float u1 = v[2 * e + 1] * gs.u[32 * hh + 2 * e + 1];
-            ub[e] = pack_bf16(u0, u1);
-            if (SPLIT) rest[e] = pack_rest(u0, u1, ub[e]);
-          }
+          if (SPLIT) rest[e] = pack_rest(u0, u1, ub[e]);
         }
-        st_tmem16(tb + COL_DB + lo + 16 * hh, db);
-        if (!BWD) st_tmem16(tb + COL_U + lo + 16 * hh, ub);
+        st_tmem16(tb + COL_U + lo + 16 * hh, ub);
+        if (!BWD) st_tmem16(tb + COL_DB + lo + 16 * hh, db);
         if (SPLIT) st_tmem16(tb + COL_UL + lo + 16 * hh, rest);
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.uready);
+      if (p.D) {
+        if (L::staged) {  // a warp stores its own 32 rows x 32 tokens (64-byte rows and swizzle)
+          if (lane == 0) tma_store_wait_read_n<1>();  // all but S of this chunk
+          __syncwarp();
+          uint8_t* const part = base + L::stage_d + (warp - 4) * 2048;
+          const uint32_t at = smem_u32(part) + lane * 64;
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc)
+            st_shared_v4(at + ((cc ^ ((lane >> 1) & 3)) << 4), db[4 * cc], db[4 * cc + 1],
+                         db[4 * cc + 2], db[4 * cc + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tmD, part, 32 * hh, n0 + 32 * q, bh * N + n);
+            tma_store_commit();
+          }
+        } else {
+          uint4* out = reinterpret_cast<uint4*>(
+              p.D + (((size_t)bh * N + n) * p.d.dv + n0 + r) * C + 32 * hh);
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc)
+            out[cc] = make_uint4(db[4 * cc], db[4 * cc + 1], db[4 * cc + 2], db[4 * cc + 3]);
+        }
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.gempty[g]);
     }
@@ -529,16 +605,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp >= 12) {
-    // ------------------------------------------------------------ scaled Q (and K); outputs
-    const int q = warp & 3, t = threadIdx.x - 384;
+    // ------------------------------------------------------------ scaled Q; outputs
+    const int q = warp & 3, t = threadIdx.x & 127;
     const uint32_t lo = (uint32_t)(32 * q) << 16;
     auto scale_chunk = [&](int c) -> bool {
       const int s = c % NS, g = c % GS;
-      if (!mbar_wait_warp(&sm.full[s], (c / NS) & 1, wc, W_O_FULL)) return false;
+      if (!mbar_wait_warp(&sm.full[WQ][s], (c / NS) & 1, wc, W_O_FULL)) return false;
       if (!mbar_wait_warp(&sm.gfull[g], (c / GS) & 1, wc, W_O_GATE)) return false;
-      const uint32_t st = smem_u32(base + s * L::bytes);
-      scale_tile(st + L::q, L::wq, sm.gates[g].q, t);
-      if (BWD) scale_tile(st + L::k, TILE, sm.gates[g].u, t);
+      scale_tile(smem_u32(base + L::wq_at(s)) + L::q, L::wq, sm.gates[g].q, t);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.scaled[s]);
@@ -546,7 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // 128 rows x 64 tokens at TMEM column `col` to a [64 tokens x 128] tile of `map`, times
     // factor[token] if given
-    const uint32_t tile = smem_u32(base + L::stage_o);
+    uint8_t* const stage = base + L::stage_o;
+    const uint32_t tile = smem_u32(stage);
     auto emit = [&](uint32_t col, const CUtensorMap* map, const float* factor, int t0, uint64_t* after) {
       if (t == 0) tma_store_wait_read_n<0>();  // the tile's last store
       named_bar_sync(1, 128);
@@ -575,34 +650,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       named_bar_sync(1, 128);
       if (t == 0) {
-        tma_store_3d(map, base + L::stage_o, n0, t0, bh);
-        tma_store_3d(map, base + L::stage_o + TILE, n0 + 64, t0, bh);
+        tma_store_3d(map, stage, n0, t0, bh);
+        tma_store_3d(map, stage + TILE, n0 + 64, t0, bh);
         tma_store_commit();
       }
-    };
-    // the same straight from the registers (SPLIT has no shared memory left): a warp's store
-    // covers 32 consecutive rows of one token
-    auto emit_direct = [&](uint32_t col, bf16* out, int t0, uint64_t* after) {
-      bf16* o = out ? out + ((size_t)bh * T + t0) * p.d.dv + n0 + 32 * q + lane : nullptr;
-      float v[64];
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        float u[32];
-        tmem_ld32(tb + col + lo + 32 * hf, u);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[32 * hf + e] = u[e];
-      }
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (after && lane == 0) mbar_arrive(after);
-      const int left = T - t0;
-      if (o) {
-#pragma unroll
-        for (int e = 0; e < 64; ++e)
-          if (e < left) o[(size_t)e * p.d.dv] = __float2bfloat16_rn(v[e]);
-      }
-      __syncwarp();
     };
     bool ok = scale_chunk(0);
     for (int c = 0; c < N; ++c) {
@@ -610,19 +661,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && c + 1 < N) ok = scale_chunk(c + 1);
       ok = ok && mbar_wait_warp(&sm.yfull[yb], (c / NY) & 1, wc, W_O_Y);
       // the warps of emit() meet at barriers: all of them go on, or none does
-      if (L::staged) ok = !named_bar_or(2, 128, !ok);
+      ok = !named_bar_or(2, 128, !ok);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = COL_D + 128 * yb;
-      if (BWD) {
-        emit(d, &tmD, nullptr, t0, nullptr);                          // E
-        emit(d, &tmY, sm.gates[g].be, t0, &sm.yfree[yb]);             // dV = beta E
-      } else if (L::staged) {
-        if (p.D) emit(d, &tmD, nullptr, t0, p.y ? nullptr : &sm.yfree[yb]);
-        if (p.y) emit(d + 64, &tmY, nullptr, t0, &sm.yfree[yb]);
-      } else {
-        if (p.D) emit_direct(d, p.D, t0, nullptr);
-        emit_direct(d + 64, p.y, t0, &sm.yfree[yb]);
+      if constexpr (BWD) {
+        emit(d, &tmY, sm.gates[g].be, t0, &sm.yfree[yb]);  // dV = beta E
+      } else if (p.y) {
+        emit(d + 64, &tmY, nullptr, t0, &sm.yfree[yb]);
+      } else if (lane == 0) {
+        mbar_arrive(&sm.yfree[yb]);
       }
       if (lane == 0) mbar_arrive(&sm.gempty[g]);
     }
@@ -658,7 +706,8 @@ static cudaError_t launch(const Args& a, cudaStream_t st) {
       !make_map_bf16_3d(&ms, states ? (const void*)states : w, 128, states ? d.dv : N * C,
                         states ? bh * N : bh, 32) ||
       !make_map_bf16_3d(&my, yy ? yy : v, d.dv, d.T, bh, C) ||
-      !make_map_bf16_3d(&md, dd ? (const void*)dd : v, d.dv, d.T, bh, C))
+      !gradlev::tc::make_map_bf16_3d_box(&md, dd ? (const void*)dd : w, dd ? C : 128,
+                                         dd ? d.dv : N * C, dd ? bh * N : bh, 32, 32))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> set{0};
   int dev = 0;
@@ -670,7 +719,7 @@ static cudaError_t launch(const Args& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     set.fetch_or(bit);
   }
-  WalkParams p{d, a.beta, a.log_alpha, a.scale, a.status, a.timeout_ns, a.S0,
+  WalkParams p{d, BWD ? a.sv.gates : a.m.gates, a.status, a.timeout_ns, a.S0,
                static_cast<const bf16*>(a.dST), a.ST, static_cast<bf16*>(a.dS0),
                static_cast<bf16*>(a.y), dd, states};
   walk_kernel<BWD, SPLIT><<<(unsigned)(bh * (d.dv / 128)), kThreads, L::smem, st>>>(
