@@ -56,12 +56,18 @@ namespace ffma {
 constexpr int C = 32;
 
 // What the forward leaves for the backward, all float32:
-//   S [B*H][N][dv][dk] chunk-start states, D [B*H][T][dv], Z and P [B*H][N][C][C].
+//   S [B*H][N][dv][dk] chunk-start states, D [B*H][T][dv], Z and P [B*H][N][C][C], gates
+//   [B*H][N] WalkGates.
 struct Saved {
-  float *S, *D, *Z, *P;
+  float *S, *D, *Z, *P, *gates;
+};
+// A chunk's gates as the walks copy them in.
+struct WalkGates {
+  float beta[C], G[C], w[C];
+  float GC, pad[3];
 };
 __host__ __device__ inline int chunks(int T) { return (T + C - 1) / C; }
-size_t saved_bytes(const Dims& d, bool states);  // states = false: Z and P alone
+size_t saved_bytes(const Dims& d, bool states);  // states = false: Z, P and gates alone
 Saved saved_at(char* base, const Dims& d, bool states);
 
 struct Args {

@@ -64,16 +64,6 @@ __device__ __forceinline__ float decay(const Gates& g, int i, int j) {  // M_ij,
   return g.seg[i] == g.seg[j] ? expf((float)(g.L[i] - g.L[j])) : 0.f;
 }
 
-// Rows [t0, t0 + C) x columns [c0, c0 + n) of a [T][ld] matrix into dst[C][ldd], zero past T.
-template <typename Tio>
-__device__ void load_tile(float* dst, int ldd, const Tio* src, size_t ld, int t0, int T, int c0,
-                          int n) {
-  for (int i = threadIdx.x; i < C * n; i += kThreads) {
-    const int r = i / n, c = i - r * n;
-    dst[r * ldd + c] = t0 + r < T ? to_f32(src[(size_t)(t0 + r) * ld + c0 + c]) : 0.f;
-  }
-}
-
 __device__ __forceinline__ float dot4(const float4& a, const float4& b, float s) {
   s = fmaf(a.x, b.x, s);
   s = fmaf(a.y, b.y, s);
@@ -81,6 +71,23 @@ __device__ __forceinline__ float dot4(const float4& a, const float4& b, float s)
   return fmaf(a.w, b.w, s);
 }
 __device__ __forceinline__ float4 at4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
+__device__ __forceinline__ float4 at4(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+
+// Rows [t0, t0 + C) of a [T][n] matrix into dst[C][ldd], zero past T. n a multiple of 8.
+template <typename Tio>
+__device__ void load_tile(float* dst, int ldd, const Tio* src, int t0, int T, int n) {
+  const int n4 = n >> 2;
+  for (int i = threadIdx.x; i < C * n4; i += kThreads) {
+    const int r = i / n4, c = 4 * (i - r * n4);
+    *reinterpret_cast<float4*>(dst + r * ldd + c) =
+        t0 + r < T ? at4(src + (size_t)(t0 + r) * n + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -104,8 +111,8 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(Args a) {
   float *K = sm, *Q = sm + C * ld;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) load_gates(g, a.beta, a.log_alpha, (size_t)bh * d.T, t0, d.T);
-  load_tile(K, ld, static_cast<const Tio*>(a.k) + kh * d.T * d.dk, d.dk, t0, d.T, 0, d.dk);
-  load_tile(Q, ld, static_cast<const Tio*>(a.q) + kh * d.T * d.dk, d.dk, t0, d.T, 0, d.dk);
+  load_tile(K, ld, static_cast<const Tio*>(a.k) + kh * d.T * d.dk, t0, d.T, d.dk);
+  load_tile(Q, ld, static_cast<const Tio*>(a.q) + kh * d.T * d.dk, t0, d.T, d.dk);
   __syncthreads();
   const size_t cc = ((size_t)bh * N + n) * C * C;
   for (int i = warp; i < C; i += kWarps) {
@@ -118,6 +125,13 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(Args a) {
     const float m = lane <= i ? decay(g, i, lane) : 0.f;
     A[i * LD + lane] = lane < i ? m * kk : 0.f;
     a.sv.P[cc + i * C + lane] = lane <= i ? a.scale * m * qk : 0.f;
+  }
+  if (warp == kWarps - 1) {
+    WalkGates* wg = reinterpret_cast<WalkGates*>(a.sv.gates) + (size_t)bh * N + n;
+    wg->beta[lane] = g.beta[lane];
+    wg->G[lane] = g.G[lane];
+    wg->w[lane] = g.w[lane];
+    if (lane == 0) wg->GC = g.GC;
   }
   __syncthreads();
   // Z_ij = A_ij - sum_{j<m<i} A_im beta_m Z_mj: lane j owns column j, row by row. A lane
@@ -132,227 +146,256 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(Args a) {
   }
 }
 
-// ------------------------------------------------------------------ forward walk
+// ------------------------------------------------------------------ the walks
+// One chunk's inputs in shared memory, two stages: the next chunk's copies (cp.async, in the
+// I/O dtype) run while this one is worked on.
+constexpr int LZ = C + 4;     // row stride of Z and P: 16-byte rows, no bank conflicts
+constexpr int LV = kRows + 8; // of V: 16-byte pieces in both types
+
 template <typename Tio>
-__global__ void __launch_bounds__(kThreads) fwd_kernel(Args a) {
-  extern __shared__ __align__(16) float sm[];
-  __shared__ Gates g;
-  __shared__ float Z[C * LD], P[C * LD];
-  __shared__ __align__(16) float R[C * kRows], D[C * kRows];  // read as float4
+struct Stage {
+  WalkGates* g;
+  float *Z, *P;               // [C][LZ]
+  Tio *K, *Q;                 // [C][padded dk]
+  Tio* V;                     // [C][LV]: V or dY
+};
+// row stride of K and Q: whole 16-byte pieces, and an odd number of them
+template <typename Tio>
+__host__ __device__ constexpr int pad_row(int dk) { return dk + 16 / (int)sizeof(Tio); }
+template <typename Tio>
+__host__ __device__ constexpr size_t stage_bytes(int dk) {
+  return sizeof(WalkGates) + 2 * C * LZ * sizeof(float) + (2 * C * pad_row<Tio>(dk) + C * LV) * sizeof(Tio);
+}
+template <typename Tio>
+__device__ __forceinline__ Stage<Tio> stage_at(char* base, int s, int dk) {
+  char* p = base + s * stage_bytes<Tio>(dk);
+  Stage<Tio> g;
+  g.g = reinterpret_cast<WalkGates*>(p);
+  g.Z = reinterpret_cast<float*>(g.g + 1);
+  g.P = g.Z + C * LZ;
+  g.K = reinterpret_cast<Tio*>(g.P + C * LZ);
+  g.Q = g.K + C * pad_row<Tio>(dk);
+  g.V = g.Q + C * pad_row<Tio>(dk);
+  return g;
+}
+
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool ok) {
+  const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
+  const int n = ok ? 16 : 0;  // 0: filled with zeros
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+}
+
+// Asynchronous copies of chunk n (its 16-byte pieces over the CTA's threads).
+template <typename Tio>
+__device__ void fetch(const Stage<Tio>& g, const Args& a, const Tio* v, size_t bh, size_t kh, int n,
+                      int n0, int rows) {
+  constexpr int E = 16 / sizeof(Tio);
+  const Dims& d = a.d;
+  const int N = chunks(d.T), t0 = n * C, kc = d.dk / E;
+  const Tio* K = static_cast<const Tio*>(a.k) + kh * d.T * d.dk;
+  const Tio* Q = static_cast<const Tio*>(a.q) + kh * d.T * d.dk;
+  for (int i = threadIdx.x; i < C * kc; i += kThreads) {
+    const int t = i / kc, c = (i - t * kc) * E;
+    const bool ok = t0 + t < d.T;
+    const size_t at = (size_t)(ok ? t0 + t : 0) * d.dk + c;
+    copy16(g.K + t * pad_row<Tio>(d.dk) + c, K + at, ok);
+    copy16(g.Q + t * pad_row<Tio>(d.dk) + c, Q + at, ok);
+  }
+  constexpr int vc = kRows / E;
+  for (int i = threadIdx.x; i < C * vc; i += kThreads) {
+    const int t = i / vc, c = (i - t * vc) * E;
+    const bool ok = t0 + t < d.T && c < rows;
+    copy16(g.V + t * LV + c, ok ? v + (bh * d.T + t0 + t) * d.dv + n0 + c : v, ok);
+  }
+  const float* Z = a.sv.Z + (bh * N + n) * C * C;
+  const float* P = a.sv.P + (bh * N + n) * C * C;
+  const float* wg = a.sv.gates + (bh * N + n) * (sizeof(WalkGates) / sizeof(float));
+  static_assert(sizeof(WalkGates) % 16 == 0 && sizeof(WalkGates) / 16 <= kThreads, "");
+  if (threadIdx.x < sizeof(WalkGates) / 16)
+    copy16(reinterpret_cast<float*>(g.g) + 4 * threadIdx.x, wg + 4 * threadIdx.x, true);
+  static_assert(C * C / 4 == kThreads, "one piece of Z and P per thread");
+  const int t = threadIdx.x / (C / 4), c = 4 * (threadIdx.x % (C / 4));
+  copy16(g.Z + t * LZ + c, Z + t * C + c, true);
+  copy16(g.P + t * LZ + c, P + t * C + c, true);
+}
+
+// Threads: token `lane` and state rows 2 warp, 2 warp + 1 for the products that end in tokens;
+// four rows and one column of d_k for the update of S.
+template <typename Tio, bool BWD>
+__global__ void __launch_bounds__(kThreads) walk_kernel(Args a) {
+  extern __shared__ __align__(16) char smc[];
+  // [row][token]: a lane's stores and a warp's reads of a row are free of bank conflicts
+  __shared__ __align__(16) float X[kRows * LZ], Y[kRows * LZ], U[kRows * LZ], W[kRows * LZ];
   const Dims& d = a.d;
   const int N = chunks(d.T), ns = slices(d.dv), bh = blockIdx.x / ns;
   const int n0 = (blockIdx.x - bh * ns) * kRows;
   const int rows = min(kRows, d.dv - n0);
   const int b = bh / d.H, h = bh - b * d.H;
   const size_t kh = (size_t)b * d.Hk + h / (d.H / d.Hk);
-  const int ld = pad4(d.dk);
-  float *K = sm, *Q = K + C * ld, *S = Q + C * ld;  // S [kRows][ld]
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int r0 = 2 * warp;  // this thread: token `lane`, rows r0 and r0 + 1
+  const int ld = pad4(d.dk), lk = pad_row<Tio>(d.dk);
+  float* S = reinterpret_cast<float*>(smc + 2 * stage_bytes<Tio>(d.dk));  // [kRows][ld]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r0 = 2 * warp;
+  const Tio* v = static_cast<const Tio*>(BWD ? a.dy : a.v);
   for (int i = tid; i < kRows * d.dk; i += kThreads) {
     const int r = i / d.dk, c = i - r * d.dk;
-    S[r * ld + c] = a.S0 && r < rows ? a.S0[((size_t)bh * d.dv + n0 + r) * d.dk + c] : 0.f;
+    const size_t at = ((size_t)bh * d.dv + n0 + r) * d.dk + c;
+    float s = 0.f;
+    if (r < rows) {
+      if (BWD)
+        s = a.dST ? to_f32(static_cast<const Tio*>(a.dST)[at]) : 0.f;
+      else
+        s = a.S0 ? a.S0[at] : 0.f;
+    }
+    S[r * ld + c] = s;
   }
-  for (int n = 0; n < N; ++n) {
-    const int t0 = n * C;
+  auto at_chunk = [&](int c) { return BWD ? N - 1 - c : c; };
+  fetch(stage_at<Tio>(smc, 0, d.dk), a, v, (size_t)bh, kh, at_chunk(0), n0, rows);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  float* states = BWD ? a.dS : a.sv.S;
+  for (int ci = 0; ci < N; ++ci) {
+    const int n = at_chunk(ci), t0 = n * C;
+    const Stage<Tio> st = stage_at<Tio>(smc, ci & 1, d.dk);
+    const WalkGates& g = *st.g;
+    if (ci + 1 < N)  // the other stage was last read before the barrier that ended chunk ci - 1
+      fetch(stage_at<Tio>(smc, (ci + 1) & 1, d.dk), a, v, (size_t)bh, kh, at_chunk(ci + 1), n0, rows);
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 1;" ::: "memory");
     __syncthreads();
-    if (warp == 0) load_gates(g, a.beta, a.log_alpha, (size_t)bh * d.T, t0, d.T);
-    load_tile(K, ld, static_cast<const Tio*>(a.k) + kh * d.T * d.dk, d.dk, t0, d.T, 0, d.dk);
-    load_tile(Q, ld, static_cast<const Tio*>(a.q) + kh * d.T * d.dk, d.dk, t0, d.T, 0, d.dk);
-    for (int i = tid; i < C * kRows; i += kThreads) {
-      const int t = i / kRows, r = i - t * kRows;
-      R[i] = t0 + t < d.T && r < rows
-                 ? to_f32(static_cast<const Tio*>(a.v)[((size_t)bh * d.T + t0 + t) * d.dv + n0 + r])
-                 : 0.f;
+    if (states) {
+      float* out = states + (((size_t)bh * N + n) * d.dv + n0) * d.dk;
+      for (int i = 4 * tid; i < rows * d.dk; i += 4 * kThreads)
+        *reinterpret_cast<float4*>(out + i) = at4(S + (i / d.dk) * ld + i % d.dk);
     }
-    const size_t cc = ((size_t)bh * N + n) * C * C;
-    for (int i = tid; i < C * C; i += kThreads) {
-      Z[(i / C) * LD + i % C] = a.sv.Z[cc + i];
-      P[(i / C) * LD + i % C] = a.sv.P[cc + i];
-    }
-    if (a.sv.S) {
-      float* out = a.sv.S + (((size_t)bh * N + n) * d.dv + n0) * d.dk;
-      for (int i = tid; i < rows * d.dk; i += kThreads) out[i] = S[(i / d.dk) * ld + i % d.dk];
-    }
-    __syncthreads();
-    // K S^T and Q S^T
     float x0 = 0.f, x1 = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll 4
     for (int c = 0; c < d.dk; c += 4) {
-      const float4 kv = at4(K + lane * ld + c), qv = at4(Q + lane * ld + c);
+      const float4 kv = at4(st.K + lane * lk + c);
       const float4 s0 = at4(S + r0 * ld + c), s1 = at4(S + (r0 + 1) * ld + c);
       x0 = dot4(kv, s0, x0);
       x1 = dot4(kv, s1, x1);
-      y0 = dot4(qv, s0, y0);
-      y1 = dot4(qv, s1, y1);
-    }
-    const float Gi = g.G[lane];
-    x0 = R[lane * kRows + r0] - Gi * x0;
-    x1 = R[lane * kRows + r0 + 1] - Gi * x1;
-    __syncwarp();  // a warp's rows of R are its own
-    R[lane * kRows + r0] = x0;
-    R[lane * kRows + r0 + 1] = x1;
-    __syncwarp();
-    for (int m = 0; m < C; ++m) {
-      const float z = -Z[lane * LD + m] * g.beta[m];
-      x0 = fmaf(z, R[m * kRows + r0], x0);
-      x1 = fmaf(z, R[m * kRows + r0 + 1], x1);
-    }
-    D[lane * kRows + r0] = x0;
-    D[lane * kRows + r0 + 1] = x1;
-    __syncwarp();
-    y0 *= a.scale * Gi;
-    y1 *= a.scale * Gi;
-    for (int m = 0; m < C; ++m) {
-      const float p = P[lane * LD + m] * g.beta[m];
-      y0 = fmaf(p, D[m * kRows + r0], y0);
-      y1 = fmaf(p, D[m * kRows + r0 + 1], y1);
-    }
-    __syncwarp();
-    R[lane * kRows + r0] = y0;
-    R[lane * kRows + r0 + 1] = y1;
-    __syncthreads();
-    for (int i = tid; i < C * kRows; i += kThreads) {
-      const int t = i / kRows, r = i - t * kRows;
-      if (t0 + t < d.T && r < rows) {
-        const size_t at = ((size_t)bh * d.T + t0 + t) * d.dv + n0 + r;
-        if (a.y) static_cast<Tio*>(a.y)[at] = from_f32<Tio>(R[i]);
-        if (a.sv.D) a.sv.D[at] = D[i];
+      if (!BWD) {
+        const float4 qv = at4(st.Q + lane * lk + c);
+        y0 = dot4(qv, s0, y0);
+        y1 = dot4(qv, s1, y1);
       }
     }
-    // S <- G_C S + D^T diag(beta w) K
+    const float be = g.beta[lane], G = g.G[lane], w = g.w[lane];
+    if (!BWD) {
+      x0 = to_f32(st.V[lane * LV + r0]) - G * x0;  // R
+      x1 = to_f32(st.V[lane * LV + r0 + 1]) - G * x1;
+    } else {
+      x0 *= w;  // F = diag(w) K dS^T + P^T dY
+      x1 *= w;
+#pragma unroll 8
+      for (int m = 0; m < C; ++m) {
+        const float p = st.P[m * LZ + lane];
+        x0 = fmaf(p, to_f32(st.V[m * LV + r0]), x0);
+        x1 = fmaf(p, to_f32(st.V[m * LV + r0 + 1]), x1);
+      }
+    }
+    X[r0 * LZ + lane] = -be * x0;  // a warp's rows of X and Y are its own
+    X[(r0 + 1) * LZ + lane] = -be * x1;
+    __syncwarp();
+    if (!BWD) {  // D = R - Z diag(beta) R
+#pragma unroll
+      for (int m = 0; m < C; m += 4) {
+        const float4 z = at4(st.Z + lane * LZ + m);
+        x0 = dot4(z, at4(X + r0 * LZ + m), x0);
+        x1 = dot4(z, at4(X + (r0 + 1) * LZ + m), x1);
+      }
+    } else {     // E = F - Z^T diag(beta) F
+#pragma unroll 8
+      for (int m = 0; m < C; m += 4) {
+        const float4 z = make_float4(st.Z[m * LZ + lane], st.Z[(m + 1) * LZ + lane],
+                                     st.Z[(m + 2) * LZ + lane], st.Z[(m + 3) * LZ + lane]);
+        x0 = dot4(z, at4(X + r0 * LZ + m), x0);
+        x1 = dot4(z, at4(X + (r0 + 1) * LZ + m), x1);
+      }
+    }
+    // W: what leaves (D, E); U: what updates S (beta w D, -beta G E)
+    const float cu = BWD ? -be * G : be * w;
+    W[r0 * LZ + lane] = x0;
+    W[(r0 + 1) * LZ + lane] = x1;
+    U[r0 * LZ + lane] = cu * x0;
+    U[(r0 + 1) * LZ + lane] = cu * x1;
+    if (!BWD) {
+      Y[r0 * LZ + lane] = be * x0;
+      Y[(r0 + 1) * LZ + lane] = be * x1;
+      __syncwarp();
+      y0 *= a.scale * G;
+      y1 *= a.scale * G;
+#pragma unroll
+      for (int m = 0; m < C; m += 4) {
+        const float4 p = at4(st.P + lane * LZ + m);
+        y0 = dot4(p, at4(Y + r0 * LZ + m), y0);
+        y1 = dot4(p, at4(Y + (r0 + 1) * LZ + m), y1);
+      }
+      __syncwarp();
+    } else {  // dV, and dY scaled for the update
+      y0 = be * x0;
+      y1 = be * x1;
+      X[r0 * LZ + lane] = a.scale * G * to_f32(st.V[lane * LV + r0]);
+      X[(r0 + 1) * LZ + lane] = a.scale * G * to_f32(st.V[lane * LV + r0 + 1]);
+    }
+    Y[r0 * LZ + lane] = y0;
+    Y[(r0 + 1) * LZ + lane] = y1;
+    __syncthreads();
+    {
+      Tio* yo = static_cast<Tio*>(BWD ? a.dv_ : a.y);
+      float* wo = BWD ? a.E : a.sv.D;
+      for (int i = tid; i < C * kRows; i += kThreads) {
+        const int t = i / kRows, r = i - t * kRows;
+        if (t0 + t < d.T && r < rows) {
+          const size_t at = ((size_t)bh * d.T + t0 + t) * d.dv + n0 + r;
+          if (yo) yo[at] = from_f32<Tio>(Y[r * LZ + t]);
+          if (wo) wo[at] = W[r * LZ + t];
+        }
+      }
+    }
+    // S <- G_C S + U^T K (+ (scale G dY)^T Q)
     const float GC = g.GC;
     for (int i = tid; i < kRows / 4 * d.dk; i += kThreads) {
       const int rq = i / d.dk, c = i - rq * d.dk;
       float s[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[e] = GC * S[(4 * rq + e) * ld + c];
-      for (int m = 0; m < C; ++m) {
-        const float kv = K[m * ld + c] * (g.beta[m] * g.w[m]);
-        const float4 dd = at4(D + m * kRows + 4 * rq);
-        s[0] = fmaf(dd.x, kv, s[0]);
-        s[1] = fmaf(dd.y, kv, s[1]);
-        s[2] = fmaf(dd.z, kv, s[2]);
-        s[3] = fmaf(dd.w, kv, s[3]);
+#pragma unroll 2
+      for (int m = 0; m < C; m += 4) {
+        const float4 kv = make_float4(to_f32(st.K[m * lk + c]), to_f32(st.K[(m + 1) * lk + c]),
+                                      to_f32(st.K[(m + 2) * lk + c]), to_f32(st.K[(m + 3) * lk + c]));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = dot4(at4(U + (4 * rq + e) * LZ + m), kv, s[e]);
+        if (BWD) {
+          const float4 qv = make_float4(to_f32(st.Q[m * lk + c]), to_f32(st.Q[(m + 1) * lk + c]),
+                                        to_f32(st.Q[(m + 2) * lk + c]), to_f32(st.Q[(m + 3) * lk + c]));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[e] = dot4(at4(X + (4 * rq + e) * LZ + m), qv, s[e]);
+        }
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) S[(4 * rq + e) * ld + c] = s[e];
     }
+    __syncthreads();
   }
-  __syncthreads();
-  if (a.ST)
-    for (int i = tid; i < rows * d.dk; i += kThreads)
-      a.ST[((size_t)bh * d.dv + n0) * d.dk + i] = S[(i / d.dk) * ld + i % d.dk];
+  if (BWD ? a.dS0 != nullptr : a.ST != nullptr)
+    for (int i = tid; i < rows * d.dk; i += kThreads) {
+      const size_t at = ((size_t)bh * d.dv + n0) * d.dk + i;
+      const float s = S[(i / d.dk) * ld + i % d.dk];
+      if (BWD)
+        static_cast<Tio*>(a.dS0)[at] = from_f32<Tio>(s);
+      else
+        a.ST[at] = s;
+    }
 }
 
-// ------------------------------------------------------------------ backward walk
 template <typename Tio>
-__global__ void __launch_bounds__(kThreads) bwd_kernel(Args a) {
-  extern __shared__ __align__(16) float sm[];
-  __shared__ Gates g;
-  __shared__ float Z[C * LD], P[C * LD];
-  __shared__ __align__(16) float R[C * kRows], F[C * kRows];  // read as float4
-  const Dims& d = a.d;
-  const int N = chunks(d.T), ns = slices(d.dv), bh = blockIdx.x / ns;
-  const int n0 = (blockIdx.x - bh * ns) * kRows;
-  const int rows = min(kRows, d.dv - n0);
-  const int b = bh / d.H, h = bh - b * d.H;
-  const size_t kh = (size_t)b * d.Hk + h / (d.H / d.Hk);
-  const int ld = pad4(d.dk);
-  float *K = sm, *Q = K + C * ld, *S = Q + C * ld;  // S [kRows][ld]: dS
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int r0 = 2 * warp;
-  for (int i = tid; i < kRows * d.dk; i += kThreads) {
-    const int r = i / d.dk, c = i - r * d.dk;
-    S[r * ld + c] =
-        a.dST && r < rows
-            ? to_f32(static_cast<const Tio*>(a.dST)[((size_t)bh * d.dv + n0 + r) * d.dk + c])
-            : 0.f;
-  }
-  for (int n = N - 1; n >= 0; --n) {
-    const int t0 = n * C;
-    __syncthreads();
-    if (warp == 0) load_gates(g, a.beta, a.log_alpha, (size_t)bh * d.T, t0, d.T);
-    load_tile(K, ld, static_cast<const Tio*>(a.k) + kh * d.T * d.dk, d.dk, t0, d.T, 0, d.dk);
-    load_tile(Q, ld, static_cast<const Tio*>(a.q) + kh * d.T * d.dk, d.dk, t0, d.T, 0, d.dk);
-    for (int i = tid; i < C * kRows; i += kThreads) {
-      const int t = i / kRows, r = i - t * kRows;
-      R[i] = t0 + t < d.T && r < rows
-                 ? to_f32(static_cast<const Tio*>(a.dy)[((size_t)bh * d.T + t0 + t) * d.dv + n0 + r])
-                 : 0.f;
-    }
-    const size_t cc = ((size_t)bh * N + n) * C * C;
-    for (int i = tid; i < C * C; i += kThreads) {
-      Z[(i / C) * LD + i % C] = a.sv.Z[cc + i];
-      P[(i / C) * LD + i % C] = a.sv.P[cc + i];
-    }
-    {
-      float* out = a.dS + (((size_t)bh * N + n) * d.dv + n0) * d.dk;
-      for (int i = tid; i < rows * d.dk; i += kThreads) out[i] = S[(i / d.dk) * ld + i % d.dk];
-    }
-    __syncthreads();
-    float x0 = 0.f, x1 = 0.f;
-    for (int c = 0; c < d.dk; c += 4) {
-      const float4 kv = at4(K + lane * ld + c);
-      x0 = dot4(kv, at4(S + r0 * ld + c), x0);
-      x1 = dot4(kv, at4(S + (r0 + 1) * ld + c), x1);
-    }
-    x0 *= g.w[lane];
-    x1 *= g.w[lane];
-    for (int m = 0; m < C; ++m) {  // P^T dY
-      const float p = P[m * LD + lane];
-      x0 = fmaf(p, R[m * kRows + r0], x0);
-      x1 = fmaf(p, R[m * kRows + r0 + 1], x1);
-    }
-    F[lane * kRows + r0] = x0;
-    F[lane * kRows + r0 + 1] = x1;
-    __syncwarp();
-    for (int m = 0; m < C; ++m) {  // - Z^T diag(beta) F
-      const float z = -Z[m * LD + lane] * g.beta[m];
-      x0 = fmaf(z, F[m * kRows + r0], x0);
-      x1 = fmaf(z, F[m * kRows + r0 + 1], x1);
-    }
-    __syncwarp();
-    F[lane * kRows + r0] = x0;  // E
-    F[lane * kRows + r0 + 1] = x1;
-    __syncthreads();
-    for (int i = tid; i < C * kRows; i += kThreads) {
-      const int t = i / kRows, r = i - t * kRows;
-      if (t0 + t < d.T && r < rows) {
-        const size_t at = ((size_t)bh * d.T + t0 + t) * d.dv + n0 + r;
-        a.E[at] = F[i];
-        static_cast<Tio*>(a.dv_)[at] = from_f32<Tio>(g.beta[t] * F[i]);
-      }
-    }
-    const float GC = g.GC;
-    for (int i = tid; i < kRows / 4 * d.dk; i += kThreads) {
-      const int rq = i / d.dk, c = i - rq * d.dk;
-      float s[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] = GC * S[(4 * rq + e) * ld + c];
-      for (int m = 0; m < C; ++m) {
-        const float qv = Q[m * ld + c] * (a.scale * g.G[m]);
-        const float kv = -K[m * ld + c] * (g.beta[m] * g.G[m]);
-        const float4 oo = at4(R + m * kRows + 4 * rq), ee = at4(F + m * kRows + 4 * rq);
-        s[0] = fmaf(ee.x, kv, fmaf(oo.x, qv, s[0]));
-        s[1] = fmaf(ee.y, kv, fmaf(oo.y, qv, s[1]));
-        s[2] = fmaf(ee.z, kv, fmaf(oo.z, qv, s[2]));
-        s[3] = fmaf(ee.w, kv, fmaf(oo.w, qv, s[3]));
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S[(4 * rq + e) * ld + c] = s[e];
-    }
-  }
-  __syncthreads();
-  if (a.dS0)
-    for (int i = tid; i < rows * d.dk; i += kThreads)
-      static_cast<Tio*>(a.dS0)[((size_t)bh * d.dv + n0) * d.dk + i] =
-          from_f32<Tio>(S[(i / d.dk) * ld + i % d.dk]);
-}
+size_t walk_smem(int dk) { return 2 * stage_bytes<Tio>(dk) + kRows * pad4(dk) * sizeof(float); }
 
 // ------------------------------------------------------------------ gradients of q, k, gates
 // One CTA per (chunk, key head). A warp owns 4 tokens and every column, so a token's dot
 // products end in a warp sum; the value heads that share the key head are walked in order
 // and add up in registers.
+constexpr int kVB = 16;       // rows of the states in shared memory at a time
+
 template <typename Tio, int NJ>  // NJ: 32-column groups that cover dk
 __global__ void __launch_bounds__(kThreads) grad_kernel(Args a) {
   extern __shared__ __align__(16) float sm[];
@@ -365,10 +408,11 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(Args a) {
   const int b = kh / d.Hk, hk = kh - (size_t)b * d.Hk, grp = d.H / d.Hk;
   const int ld = pad4(d.dk), lv = pad4(d.dv);
   float *K = sm, *Q = K + C * ld, *O = Q + C * ld, *D = O + C * lv, *E = D + C * lv;
+  float *Sv = E + C * lv, *dSv = Sv + kVB * d.dk;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, i0 = 4 * warp;
   static_assert(4 * kWarps == C, "a warp owns 4 tokens");
-  load_tile(K, ld, static_cast<const Tio*>(a.k) + kh * d.T * d.dk, d.dk, t0, d.T, 0, d.dk);
-  load_tile(Q, ld, static_cast<const Tio*>(a.q) + kh * d.T * d.dk, d.dk, t0, d.T, 0, d.dk);
+  load_tile(K, ld, static_cast<const Tio*>(a.k) + kh * d.T * d.dk, t0, d.T, d.dk);
+  load_tile(Q, ld, static_cast<const Tio*>(a.q) + kh * d.T * d.dk, t0, d.T, d.dk);
   __syncthreads();
   float kk[4], qk[4];  // k_i.k_j, q_i.k_j of this warp's tokens i, j = lane
 #pragma unroll
@@ -391,9 +435,9 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(Args a) {
     const size_t bh = (size_t)b * d.H + hk * grp + hh;
     __syncthreads();
     if (warp == 0) load_gates(g, a.beta, a.log_alpha, bh * d.T, t0, d.T);
-    load_tile(O, lv, static_cast<const Tio*>(a.dy) + bh * d.T * d.dv, d.dv, t0, d.T, 0, d.dv);
-    load_tile(D, lv, a.sv.D + bh * d.T * d.dv, d.dv, t0, d.T, 0, d.dv);
-    load_tile(E, lv, a.E + bh * d.T * d.dv, d.dv, t0, d.T, 0, d.dv);
+    load_tile(O, lv, static_cast<const Tio*>(a.dy) + bh * d.T * d.dv, t0, d.T, d.dv);
+    load_tile(D, lv, a.sv.D + bh * d.T * d.dv, t0, d.T, d.dv);
+    load_tile(E, lv, a.E + bh * d.T * d.dv, t0, d.T, d.dv);
     __syncthreads();
     const float* S = a.sv.S + (bh * N + n) * d.dv * d.dk;
     const float* dS = a.dS + (bh * N + n) * d.dv * d.dk;
@@ -429,25 +473,37 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(Args a) {
 #pragma unroll
       for (int j = 0; j < NJ; ++j) t[e][j] = u[e][j] = z[e][j] = 0.f;
     float ss = 0.f;
-    for (int v = 0; v < d.dv; ++v) {
-      float o[4], ee[4], dd[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        o[e] = O[(i0 + e) * lv + v];
-        ee[e] = E[(i0 + e) * lv + v];
-        dd[e] = D[(i0 + e) * lv + v];
+    for (int v0 = 0; v0 < d.dv; v0 += kVB) {  // kVB rows of S and dS at a time (dv may end inside)
+      const int nv = min(kVB, d.dv - v0), n4 = nv * d.dk / 4;
+      __syncthreads();
+      for (int i = tid; i < n4; i += kThreads) {
+        reinterpret_cast<float4*>(Sv)[i] = at4(S + (size_t)v0 * d.dk + 4 * i);
+        reinterpret_cast<float4*>(dSv)[i] = at4(dS + (size_t)v0 * d.dk + 4 * i);
       }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int c = lane + 32 * j;
-        const float s = c < d.dk ? S[(size_t)v * d.dk + c] : 0.f;
-        const float ds = c < d.dk ? dS[(size_t)v * d.dk + c] : 0.f;
-        if ((v & (kWarps - 1)) == warp) ss = fmaf(s, ds, ss);
+      __syncthreads();
+      for (int i = tid; i < n4; i += kThreads) ss = dot4(at4(Sv + 4 * i), at4(dSv + 4 * i), ss);
+      for (int v = 0; v < nv; v += 4) {
+        float4 o[4], ee[4], dd[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          t[e][j] = fmaf(o[e], s, t[e][j]);
-          u[e][j] = fmaf(ee[e], s, u[e][j]);
-          z[e][j] = fmaf(dd[e], ds, z[e][j]);
+          o[e] = at4(O + (i0 + e) * lv + v0 + v);
+          ee[e] = at4(E + (i0 + e) * lv + v0 + v);
+          dd[e] = at4(D + (i0 + e) * lv + v0 + v);
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const int c = lane + 32 * j;
+          if (32 * j + 32 > d.dk && c >= d.dk) continue;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float s = Sv[(v + x) * d.dk + c], ds = dSv[(v + x) * d.dk + c];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              t[e][j] = fmaf(x == 0 ? o[e].x : x == 1 ? o[e].y : x == 2 ? o[e].z : o[e].w, s, t[e][j]);
+              u[e][j] = fmaf(x == 0 ? ee[e].x : x == 1 ? ee[e].y : x == 2 ? ee[e].z : ee[e].w, s, u[e][j]);
+              z[e][j] = fmaf(x == 0 ? dd[e].x : x == 1 ? dd[e].y : x == 2 ? dd[e].z : dd[e].w, ds, z[e][j]);
+            }
+          }
         }
       }
     }
@@ -543,7 +599,7 @@ cudaError_t set_smem(F f, size_t bytes) {
 template <typename Tio, int NJ>
 cudaError_t launch_grad(const Args& a, cudaStream_t st) {
   const size_t smem =
-      (size_t)C * (2 * pad4(a.d.dk) + 3 * pad4(a.d.dv)) * sizeof(float);
+      ((size_t)C * (2 * pad4(a.d.dk) + 3 * pad4(a.d.dv)) + 2 * kVB * a.d.dk) * sizeof(float);
   const cudaError_t e = set_smem(grad_kernel<Tio, NJ>, smem);
   if (e != cudaSuccess) return e;
   grad_kernel<Tio, NJ><<<chunks(a.d.T) * a.d.B * a.d.Hk, kThreads, smem, st>>>(a);
@@ -560,9 +616,9 @@ cudaError_t fwd_t(const Args& a, cudaStream_t st) {
   prep_kernel<Tio><<<chunks(d.T) * d.B * d.H, kThreads, sp, st>>>(a);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const size_t sf = (size_t)(2 * C + kRows) * pad4(d.dk) * sizeof(float);
-  if ((e = set_smem(fwd_kernel<Tio>, sf)) != cudaSuccess) return e;
-  fwd_kernel<Tio><<<slices(d.dv) * d.B * d.H, kThreads, sf, st>>>(a);
+  const size_t sf = walk_smem<Tio>(d.dk);
+  if ((e = set_smem(walk_kernel<Tio, false>, sf)) != cudaSuccess) return e;
+  walk_kernel<Tio, false><<<slices(d.dv) * d.B * d.H, kThreads, sf, st>>>(a);
   count_launch();
   return cudaGetLastError();
 }
@@ -570,10 +626,10 @@ cudaError_t fwd_t(const Args& a, cudaStream_t st) {
 template <typename Tio>
 cudaError_t bwd_t(const Args& a, cudaStream_t st) {
   const Dims& d = a.d;
-  const size_t sf = (size_t)(2 * C + kRows) * pad4(d.dk) * sizeof(float);
-  cudaError_t e = set_smem(bwd_kernel<Tio>, sf);
+  const size_t sf = walk_smem<Tio>(d.dk);
+  cudaError_t e = set_smem(walk_kernel<Tio, true>, sf);
   if (e != cudaSuccess) return e;
-  bwd_kernel<Tio><<<slices(d.dv) * d.B * d.H, kThreads, sf, st>>>(a);
+  walk_kernel<Tio, true><<<slices(d.dv) * d.B * d.H, kThreads, sf, st>>>(a);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (d.dk <= 64) return launch_grad<Tio, 2>(a, st);
@@ -585,7 +641,7 @@ cudaError_t bwd_t(const Args& a, cudaStream_t st) {
 
 size_t saved_bytes(const Dims& d, bool states) {
   const size_t N = chunks(d.T), cc = up256(d.BH() * N * C * C * sizeof(float));
-  size_t n = 2 * cc;
+  size_t n = 2 * cc + up256(d.BH() * N * sizeof(WalkGates));
   if (states)
     n += up256(d.BH() * N * d.dv * d.dk * sizeof(float)) +
          up256(d.BH() * (size_t)d.T * d.dv * sizeof(float));
@@ -597,10 +653,11 @@ Saved saved_at(char* base, const Dims& d, bool states) {
   Saved s{};
   s.Z = reinterpret_cast<float*>(base);
   s.P = reinterpret_cast<float*>(base + cc);
+  s.gates = reinterpret_cast<float*>(base + 2 * cc);
   if (states) {
-    s.S = reinterpret_cast<float*>(base + 2 * cc);
-    s.D = reinterpret_cast<float*>(base + 2 * cc +
-                                   up256(d.BH() * N * d.dv * d.dk * sizeof(float)));
+    base += 2 * cc + up256(d.BH() * N * sizeof(WalkGates));
+    s.S = reinterpret_cast<float*>(base);
+    s.D = reinterpret_cast<float*>(base + up256(d.BH() * N * d.dv * d.dk * sizeof(float)));
   }
   return s;
 }
