@@ -41,13 +41,11 @@ struct GradSmem {
   uint8_t D[TILE], E[TILE];                  // D^T, E^T: 64 rows of d_v x 64 tokens
   uint8_t S[2 * TILE], dS[2 * TILE];         // 64 rows of d_v x 128
   uint8_t X[TILE], Yn[TILE];
-  float Lh[C], Ll[C], be[C], cq[C], ck[C], cz[C];
-  float ra[C], ca[C];                        // M_ij beta_j = ra_i ca_j (fac)
+  GateBlock g;
+  float Lh[C], Ll[C];                        // where a reset or strong decays rule out g.fac
   int seg[C];
   float xs[2][C], zs[2][C];                  // per column half
   float red[8];
-  float GC;
-  int fac;
   uint64_t kq, full, mma;
   uint32_t tmem_base;
   int abort;
@@ -66,20 +64,18 @@ struct GradParams {
   bf16 *dbeta, *dlog_alpha;
 };
 
-// sum of v[e] * x over 16 columns of a swizzled row
-__device__ __forceinline__ float row_dot(const float (&v)[16], uint32_t tile, int r, int c8) {
-  float s = 0.f;
+// 16 columns of a swizzled bf16 row
+__device__ __forceinline__ void row16(float (&x)[16], const uint8_t* tile, int r, int c8) {
 #pragma unroll
   for (int cc = 0; cc < 2; ++cc) {
-    const uint4 x = ld_shared_v4(tile + sw128_off(r, c8 + cc));
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const uint4 u = *reinterpret_cast<const uint4*>(tile + sw128_off(r, c8 + cc));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      s = fmaf(v[8 * cc + 2 * e], bf16_lo(w[e]), s);
-      s = fmaf(v[8 * cc + 2 * e + 1], bf16_hi(w[e]), s);
+      x[8 * cc + 2 * e] = bf16_lo(w[e]);
+      x[8 * cc + 2 * e + 1] = bf16_hi(w[e]);
     }
   }
-  return s;
 }
 
 }  // namespace
@@ -101,18 +97,36 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int T = p.d.T, N = chunks(T), kh = blockIdx.x / N, n = blockIdx.x - kh * N, t0 = n * C;
   const int b = kh / p.d.Hk, grp = p.d.H / p.d.Hk;
   const WaitCtx wc{&sm.abort, p.status, p.timeout_ns};
+  // tiles of 64 columns of d_v (and, with the first, the gates); the first slice goes out
+  // before anything else
+  auto load_slice = [&](int bh, int sl) {
+    mbar_arrive_expect_tx(&sm.full, 7 * TILE + (sl == 0 ? (uint32_t)sizeof(GateBlock) : 0u));
+    if (sl == 0)
+      bulk_load(&sm.g, p.gates + ((size_t)bh * N + n) * (sizeof(GateBlock) / sizeof(float)),
+                sizeof(GateBlock), &sm.full);
+    tma_load_3d(sm.O, &tmO, &sm.full, 64 * sl, t0, bh);
+    tma_load_3d(sm.D, &tmD, &sm.full, 0, 64 * sl, bh * N + n);
+    tma_load_3d(sm.E, &tmE, &sm.full, 0, 64 * sl, bh * N + n);
+    for (int kb = 0; kb < 2; ++kb) {
+      tma_load_3d(sm.S + kb * TILE, &tmS, &sm.full, 64 * kb, 64 * sl, bh * N + n);
+      tma_load_3d(sm.dS + kb * TILE, &tmdS, &sm.full, 64 * kb, 64 * sl, bh * N + n);
+    }
+  };
+  const int bh0 = b * p.d.H + (kh - b * p.d.Hk) * grp;
   if (tid == 0) {
     sm.abort = 0;
     mbar_init(&sm.kq, 1);
     mbar_init(&sm.full, 1);
     mbar_init(&sm.mma, 1);
     fence_mbar_init();
+    load_slice(bh0, 0);
     mbar_arrive_expect_tx(&sm.kq, 4 * TILE);
     for (int kb = 0; kb < 2; ++kb) {
       tma_load_3d(sm.Q + kb * TILE, &tmQ, &sm.kq, 64 * kb, t0, kh);
       tma_load_3d(sm.K + kb * TILE, &tmK, &sm.kq, 64 * kb, t0, kh);
     }
   }
+  const int nsl = p.d.dv / 64;
   if (warp == 1) {
     tmem_alloc(&sm.tmem_base, kCols);
     tmem_relinquish();
@@ -126,53 +140,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t id_t = idesc_bf16(64, 128, false, true);
   const uint32_t id_m = idesc_bf16(64, 128, true, true);
   uint32_t nfull = 0, nmma = 0;  // phases so far
-  const int nsl = p.d.dv / 64;
 
   float acc[64];
 #pragma unroll
   for (int e = 0; e < 64; ++e) acc[e] = 0.f;
 
   for (int hv = 0; hv < grp; ++hv) {
-    const int bh = b * p.d.H + (kh - b * p.d.Hk) * grp + hv;
-    if (warp == 2) {
-      const GateBlock* gb = reinterpret_cast<const GateBlock*>(p.gates) + (size_t)bh * N + n;
-      const bool fac = gb->fac != 0.f;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int j = lane + 32 * k;
-        sm.be[j] = gb->be[j];
-        sm.cq[j] = gb->q[j];
-        sm.ck[j] = gb->bG[j];
-        sm.cz[j] = gb->bw[j];
-        sm.ra[j] = gb->ra[j];
-        sm.ca[j] = gb->cb[j];
-      }
-      if (lane == 0) {
-        sm.GC = gb->GC;
-        sm.fac = fac;
-      }
-      if (!fac) {
-        const GatePair g = chunk_gates(p.beta, p.log_alpha, (size_t)bh * T, t0, T);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          sm.Lh[lane + 32 * k] = g.Lh[k];
-          sm.Ll[lane + 32 * k] = g.Ll[k];
-          sm.seg[lane + 32 * k] = g.seg[k];
-        }
-      }
-    }
+    const int bh = bh0 + hv;
     float ss = 0.f;  // <dS, S>
     for (int sl = 0; sl < nsl; ++sl) {
-      if (tid == 0) {
-        mbar_arrive_expect_tx(&sm.full, 7 * TILE);
-        tma_load_3d(sm.O, &tmO, &sm.full, 64 * sl, t0, bh);
-        tma_load_3d(sm.D, &tmD, &sm.full, 0, 64 * sl, bh * N + n);
-        tma_load_3d(sm.E, &tmE, &sm.full, 0, 64 * sl, bh * N + n);
-        for (int kb = 0; kb < 2; ++kb) {
-          tma_load_3d(sm.S + kb * TILE, &tmS, &sm.full, 64 * kb, 64 * sl, bh * N + n);
-          tma_load_3d(sm.dS + kb * TILE, &tmdS, &sm.full, 64 * kb, 64 * sl, bh * N + n);
-        }
-      }
+      if (tid == 0 && (hv > 0 || sl > 0)) load_slice(bh, sl);
       mbar_wait(&sm.full, nfull++ & 1, wc, W_G_FULL);
       __syncwarp();
       if (tid == 0) {
@@ -197,7 +174,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t off = (uint32_t)(tid + 256 * k) * 16;
-        const uint4 x = ld_shared_v4(smem_u32(sm.S) + off), y = ld_shared_v4(smem_u32(sm.dS) + off);
+        const uint4 x = *reinterpret_cast<const uint4*>(sm.S + off);
+        const uint4 y = *reinterpret_cast<const uint4*>(sm.dS + off);
         const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -205,15 +183,24 @@ __global__ void __launch_bounds__(kThreads, 2)
           ss = fmaf(bf16_hi(xw[e]), bf16_hi(yw[e]), ss);
         }
       }
+      if (sl == 0 && warp == 2 && sm.g.fac == 0.f) {
+        const GatePair g = chunk_gates(p.beta, p.log_alpha, (size_t)bh * T, t0, T);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          sm.Lh[lane + 32 * k] = g.Lh[k];
+          sm.Ll[lane + 32 * k] = g.Ll[k];
+          sm.seg[lane + 32 * k] = g.seg[k];
+        }
+      }
       mbar_wait(&sm.mma, nmma++ & 1, wc, W_G_MMA);
-      __syncthreads();  // S and dS are read: the next slice may land (and the gates are there)
+      __syncthreads();  // S and dS are read: the next slice may land
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     if (lane == 0) sm.red[warp] = ss;
     tc_fence_after();
     // ---- X and Yn: lower lanes, columns [32 hh, 32 hh + 32)
-    const float rx = p.scale * sm.ra[i], ry = -sm.be[i] * sm.ra[i];
+    const float rx = p.scale * sm.g.ra[i], ry = -sm.g.be[i] * sm.g.ra[i];
     float db = 0.f;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
@@ -226,10 +213,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int keep = i - j0;  // columns left of the diagonal
 #pragma unroll
         for (int e = 0; e < 16; ++e) db = e == keep ? g[e] : db;
-        if (sm.fac) {
+        if (sm.g.fac != 0.f) {
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
-            const float4 c = *reinterpret_cast<const float4*>(sm.ca + j0 + e);
+            const float4 c = *reinterpret_cast<const float4*>(sm.g.cb + j0 + e);
             const float cv[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -243,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int j = j0 + e;
-            const float m = sm.ca[j] * expf(fminf((Lh - sm.Lh[j]) + (Ll - sm.Ll[j]), 0.f));
+            const float m = sm.g.cb[j] * expf(fminf((Lh - sm.Lh[j]) + (Ll - sm.Ll[j]), 0.f));
             const bool on = sm.seg[j] == seg;
             f[e] = on && e <= keep ? f[e] * (rx * m) : 0.f;
             g[e] = on && e < keep ? g[e] * (ry * m) : 0.f;
@@ -275,29 +262,26 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncwarp();
     // ---- t (lower) and u (upper); z (upper)
-    const uint32_t mine = up ? sK + hh * TILE : sQ + hh * TILE;
-    const float ca = up ? sm.ck[i] : sm.cq[i], cz = up ? sm.cz[i] : 0.f;
+    const uint8_t* mine = (up ? sm.K : sm.Q) + hh * TILE;
+    const float ca = up ? sm.g.bG[i] : sm.g.q[i], cz = up ? sm.g.bw[i] : 0.f;
     float xs = 0.f, zs = 0.f;
 #pragma unroll
     for (int hf = 0; hf < 4; ++hf) {
-      float v[16];
+      float v[16], z[16], x[16];
       tmem_ld16(tb + COL_A + lo + 64 * hh + 16 * hf, v);
+      tmem_ld16(tb + COL_B + lo + 64 * hh + 16 * hf, z);  // lower lanes: unused (xk in flight)
+      row16(x, mine, i, 2 * hf);
       tmem_ld_wait();
-      xs = fmaf(ca, row_dot(v, mine, i, 2 * hf), xs);
+      float dv = 0.f, dz = 0.f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[16 * hf + e] = fmaf(ca, v[e], acc[16 * hf + e]);
-    }
-#pragma unroll
-    for (int hf = 0; hf < 4; ++hf) {
-      float v[16];
-      tmem_ld16(tb + COL_B + lo + 64 * hh + 16 * hf, v);  // lower lanes: unused (xk in flight)
-      tmem_ld_wait();
-      if (up) {
-        zs = fmaf(cz, row_dot(v, mine, i, 2 * hf), zs);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[16 * hf + e] = fmaf(cz, v[e], acc[16 * hf + e]);
+      for (int e = 0; e < 16; ++e) {
+        const float ze = up ? z[e] : 0.f;
+        dv = fmaf(v[e], x[e], dv);
+        dz = fmaf(ze, x[e], dz);
+        acc[16 * hf + e] = fmaf(ca, v[e], fmaf(cz, ze, acc[16 * hf + e]));
       }
-      __syncwarp();
+      xs = fmaf(ca, dv, xs);
+      zs = fmaf(cz, dz, zs);
     }
     tc_fence_before();
     __syncthreads();
@@ -320,25 +304,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ---- xk (lower) and ka (upper); yk (upper)
 #pragma unroll
     for (int hf = 0; hf < 4; ++hf) {
-      float v[16];
+      float v[16], z[16], x[16];
       tmem_ld16(tb + COL_B + lo + 64 * hh + 16 * hf, v);
+      tmem_ld16(tb + COL_A + lo + 64 * hh + 16 * hf, z);  // lower lanes: t, used above
+      row16(x, mine, i, 2 * hf);
       tmem_ld_wait();
-      const float dot = row_dot(v, mine, i, 2 * hf);
-      xs += up ? -dot : dot;
+      float dot = 0.f;  // q.xk, or k.(yk - ka)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[16 * hf + e] += v[e];
-    }
-#pragma unroll
-    for (int hf = 0; hf < 4; ++hf) {
-      float v[16];
-      tmem_ld16(tb + COL_A + lo + 64 * hh + 16 * hf, v);  // lower lanes: t, used above
-      tmem_ld_wait();
-      if (up) {
-        xs += row_dot(v, mine, i, 2 * hf);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[16 * hf + e] += v[e];
+      for (int e = 0; e < 16; ++e) {
+        const float ye = up ? z[e] : 0.f;
+        dot = fmaf(up ? ye - v[e] : v[e], x[e], dot);
+        acc[16 * hf + e] += v[e] + ye;
       }
-      __syncwarp();
+      xs += dot;
     }
     xs += __shfl_xor_sync(0xffffffffu, xs, 16);
     zs += __shfl_xor_sync(0xffffffffu, zs, 16);
@@ -362,18 +340,21 @@ __global__ void __launch_bounds__(kThreads, 2)
       float gg = 0.f;
 #pragma unroll
       for (int w = 0; w < 8; ++w) gg += sm.red[w];
-      gg *= sm.GC;
+      gg *= sm.g.GC;
       const float before = __shfl_up_sync(0xffffffffu, sz, 1);
       const float z_lt = lane == 0 ? 0.f : before;
       const float after = __shfl_down_sync(0xffffffffu, sx, 1);
       const float d1 = x1 + (lane == 31 ? 0.f : after);
       const size_t row = (size_t)bh * T + t0;
+      const bool plain = sm.g.fac != 0.f;  // no reset in the chunk
+      const bool r0 = !plain && sm.seg[j] != (j > 0 ? sm.seg[j - 1] : 0);
+      const bool r1 = !plain && sm.seg[j + 1] != sm.seg[j];
       if (t0 + j < T)
         p.dlog_alpha[row + j] = __float2bfloat16_rn(
-            p.log_alpha[row + j] < kResetLog ? 0.f : sx + z_lt + gg);
+            r0 ? 0.f : sx + z_lt + gg);
       if (t0 + j + 1 < T)
         p.dlog_alpha[row + j + 1] = __float2bfloat16_rn(
-            p.log_alpha[row + j + 1] < kResetLog ? 0.f : d1 + z_lt + z0 + gg);
+            r1 ? 0.f : d1 + z_lt + z0 + gg);
     }
     __syncthreads();  // the next head overwrites the gates and the sums
   }

@@ -124,15 +124,6 @@ struct WalkParams {
   bf16* states;          // chunk-start (chunk-end) states, or null
 };
 
-// Untiled bulk copy global -> shared (addresses and size multiples of 16 bytes).
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-
 __device__ __forceinline__ void st_tmem32(uint32_t col, const uint32_t (&r)[32]) {
   float v[32];
 #pragma unroll
