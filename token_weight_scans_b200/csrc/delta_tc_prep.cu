@@ -1,5 +1,5 @@
 // Tensor-core gated delta rule: the chunk-local matrices (delta_tc.h, struct Mats), one
-// CTA per (chunk, value head), two CTAs per SM.
+// CTA per (chunk, value head), three CTAs per SM (two where both SPLIT and BACK).
 //
 // K K^T and Q K^T go through the tensor core; the unit lower triangular inverse
 // T0 = (I + A diag(beta))^-1 is formed in float32 by halves: 16 x 16 diagonal blocks by
@@ -33,20 +33,22 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int LD = 68;        // row stride (floats) of the 64 x 64 float32 matrices: 16-byte rows
-constexpr int LT = 36;        // and of the 32 x 32 temporary
-constexpr uint32_t COL_KQ = 0, COL_W = 64, kCols = 256;  // K K^T | Q K^T, then PT; W | Wb
+constexpr uint32_t kCols = 128;  // K K^T | Q K^T (64), then PT (64), then W | Wb
 constexpr float kTiny = 0x1p-60f;
 
+// Tiles live where something dead was: P and diag(w) T over Q, T over the remainder of T0 diag(G)
+// (with both, SPLIT and BACK, P has a place of its own), at the end W over Q, Wb over K, the
+// remainder of W over T0 diag(G).
+template <bool OWN_P>
 struct PrepSmem {
-  uint8_t K[2 * TILE];         // k-blocks: 64 token rows x 128 B; at the end Wb
-  uint8_t Q[2 * TILE];         // then Tw = diag(w) T and Tt = T; at the end W
+  uint8_t K[2 * TILE];         // k-blocks: 64 token rows x 128 B
+  uint8_t Q[2 * TILE];
   union {
-    float N[C * LD];           // A diag(beta)
-    uint8_t Tg[2][TILE];       // then T0 diag(G) in bf16 and its remainder; at the end Wlo
+    float N[C * LD];           // A diag(beta); parts that are done with hold the products' halves
+    uint8_t Tg[2][TILE];       // T0 diag(G) in bf16 and its remainder
   };
-  uint8_t P[TILE];
+  uint8_t P[OWN_P ? TILE : 16];
   float X[C * LD];             // T0
-  float tmp[32 * LT];
   // per token: with m in the middle of the chunk M_ij = ra_i ca_j where that stays in range
   // (fac); cN = ca beta (at least kTiny), cP = scale ca
   float ra[C], cN[C], cP[C];
@@ -57,8 +59,9 @@ struct PrepSmem {
   uint32_t tmem_base;
   int abort;
 };
-constexpr size_t kSmem = sizeof(PrepSmem) + 1024;
-static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+template <bool OWN_P> constexpr size_t smem_bytes() { return sizeof(PrepSmem<OWN_P>) + 1024; }
+static_assert(3 * (smem_bytes<false>() + 1024) <= 228 * 1024, "three CTAs per SM");
+static_assert(2 * (smem_bytes<true>() + 1024) <= 228 * 1024, "two CTAs per SM");
 
 enum : uint32_t { W_PREP_LOAD = 0x801, W_PREP_MMA };
 
@@ -86,14 +89,16 @@ __device__ __forceinline__ void axpy4(float (&s)[4], float a, const float4& x) {
 
 // SPLIT: the remainders of T0 and W; BACK: Wb and PT for the backward.
 template <bool SPLIT, bool BACK>
-__global__ void __launch_bounds__(kThreads, 2) prep_kernel(const __grid_constant__ CUtensorMap tmK,
+__global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(const __grid_constant__ CUtensorMap tmK,
                                                            const __grid_constant__ CUtensorMap tmQ,
                                                            const __grid_constant__ CUtensorMap tmW,
                                                            const __grid_constant__ CUtensorMap tmWlo,
                                                            const __grid_constant__ CUtensorMap tmWb,
                                                            PrepParams p) {
   extern __shared__ uint8_t smem_raw[];
-  PrepSmem& sm = *reinterpret_cast<PrepSmem*>(
+  constexpr bool own_p = SPLIT && BACK;
+  using Smem = PrepSmem<own_p>;
+  Smem& sm = *reinterpret_cast<Smem*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int N = chunks(p.d.T), bh = blockIdx.x / N, n = blockIdx.x - bh * N;
@@ -116,6 +121,26 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const __grid_constant
     tmem_alloc(&sm.tmem_base, kCols);
     tmem_relinquish();
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = sm.tmem_base;
+  const uint32_t sK = smem_u32(sm.K), sQ = smem_u32(sm.Q), sTg = smem_u32(sm.Tg[0]);
+  const uint32_t sP = own_p ? smem_u32(sm.P) : sQ;
+  const uint32_t sTw = sQ + TILE, sTt = own_p ? sQ : sTg + TILE;
+  if (tid == 0) {
+    mbar_wait(&sm.full, 0, wc, W_PREP_LOAD);
+    const uint32_t id = idesc_bf16(64, 64, false, false);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      const uint32_t off = (kk >> 2) * TILE + (kk & 3) * 32;
+      const uint64_t dk = desc_at(sw128_desc(sK, 16, 1024), off);
+      umma_bf16(tb, dk, dk, id, kk > 0);
+      umma_bf16(tb + LANE16, desc_at(sw128_desc(sQ, 16, 1024), off), dk, id, kk > 0);
+    }
+    umma_commit(&sm.mma);
+  }
+  __syncwarp();
   if (warp == 2) {
     const GatePair g = chunk_gates(p.beta, p.log_alpha, (size_t)bh * p.d.T, t0, p.d.T);
     const float Lm = __shfl_sync(0xffffffffu, g.Lh[0], 31), Ll = __shfl_sync(0xffffffffu, g.Ll[0], 31);
@@ -151,27 +176,8 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const __grid_constant
     }
     if (lane == 0) sm.fac = fac;
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tb = sm.tmem_base;
-  const uint32_t sK = smem_u32(sm.K), sQ = smem_u32(sm.Q), sTg = smem_u32(sm.Tg[0]);
-  const uint32_t sTw = sQ, sTt = sQ + TILE;
-  if (tid == 0) {
-    mbar_wait(&sm.full, 0, wc, W_PREP_LOAD);
-    const uint32_t id = idesc_bf16(64, 64, false, false);
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {
-      const uint32_t off = (kk >> 2) * TILE + (kk & 3) * 32;
-      const uint64_t dk = desc_at(sw128_desc(sK, 16, 1024), off);
-      umma_bf16(tb + COL_KQ, dk, dk, id, kk > 0);
-      umma_bf16(tb + COL_KQ + LANE16, desc_at(sw128_desc(sQ, 16, 1024), off), dk, id, kk > 0);
-    }
-    umma_commit(&sm.mma);
-  }
-  __syncwarp();
   mbar_wait(&sm.mma, 0, wc, W_PREP_MMA);
-  __syncwarp();
+  __syncthreads();  // the gates are there
   tc_fence_after();
   // Lane l < 16 of quadrant q holds row i = 16 q + l of K K^T, lane l + 16 that of Q K^T;
   // warps q and q + 4 take half of the columns each.
@@ -181,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const __grid_constant
   const bool isP = lane >= 16;
   {
     float v[32];
-    tmem_ld32(tb + COL_KQ + lo + 32 * hh, v);
+    tmem_ld32(tb + lo + 32 * hh, v);
     tmem_ld_wait();
     // the entries below (P: and on) the diagonal
     const int keep = i - 32 * hh + (isP ? 1 : 0);
@@ -217,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const __grid_constant
       for (int cc = 0; cc < 4; ++cc) {
         const float* x = v + 8 * cc;
         if (BACK)
-          st_shared_v4(smem_u32(sm.P) + sw128_off(i, 4 * hh + cc), pack_bf16(x[0], x[1]),
+          st_shared_v4(sP + sw128_off(i, 4 * hh + cc), pack_bf16(x[0], x[1]),
                        pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
         const float4 b0 = at4(sm.be + 32 * hh + 8 * cc), b1 = at4(sm.be + 32 * hh + 8 * cc + 4);
         Pg[cc] = make_uint4(pack_bf16(x[0] * b0.x, x[1] * b0.y), pack_bf16(x[2] * b0.z, x[3] * b0.w),
@@ -271,7 +277,8 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const __grid_constant
         s1 = fmaf(av[u], x.y, s1);
       }
     }
-    *reinterpret_cast<float2*>(sm.tmp + (16 * pr + r) * LT + c) = make_float2(s0, s1);
+    float* tmp = sm.N + o * LD + o;  // the first diagonal block of the pair, done with
+    *reinterpret_cast<float2*>(tmp + r * LD + c) = make_float2(s0, s1);
     __syncthreads();
     s0 = s1 = 0.f;
 #pragma unroll
@@ -280,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const __grid_constant
       const float av[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float2 x = *reinterpret_cast<const float2*>(sm.tmp + (16 * pr + m + u) * LT + c);
+        const float2 x = *reinterpret_cast<const float2*>(tmp + (m + u) * LD + c);
         s0 = fmaf(-av[u], x.x, s0);
         s1 = fmaf(-av[u], x.y, s1);
       }
@@ -288,7 +295,8 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const __grid_constant
     *reinterpret_cast<float2*>(sm.X + (o + 16 + r) * LD + o + c) = make_float2(s0, s1);
   }
   __syncthreads();
-  // ---- 32 -> 64. N21 X1: a warp owns 4 columns, a lane a row; X1 is zero above its diagonal
+  // ---- 32 -> 64. N21 X1 (into the first 32 x 32 of N, done with): a warp owns 4 columns, a
+  //      lane a row; X1 is zero above its diagonal
   {
     const int c = 4 * warp;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -299,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const __grid_constant
       axpy4(s, a.z, at4(sm.X + (m + 2) * LD + c));
       axpy4(s, a.w, at4(sm.X + (m + 3) * LD + c));
     }
-    *reinterpret_cast<float4*>(sm.tmp + lane * LT + c) = make_float4(s[0], s[1], s[2], s[3]);
+    *reinterpret_cast<float4*>(sm.N + lane * LD + c) = make_float4(s[0], s[1], s[2], s[3]);
   }
   __syncthreads();
   {  // -X2 tmp: a warp owns 4 rows, X2 is zero right of its diagonal
@@ -307,10 +315,10 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const __grid_constant
     float s[4] = {0.f, 0.f, 0.f, 0.f};
     for (int m = 0; m < 4 * warp + 4; m += 4) {
       const float4 a = at4(sm.X + (32 + r) * LD + 32 + m);
-      axpy4(s, -a.x, at4(sm.tmp + m * LT + c));
-      axpy4(s, -a.y, at4(sm.tmp + (m + 1) * LT + c));
-      axpy4(s, -a.z, at4(sm.tmp + (m + 2) * LT + c));
-      axpy4(s, -a.w, at4(sm.tmp + (m + 3) * LT + c));
+      axpy4(s, -a.x, at4(sm.N + m * LD + c));
+      axpy4(s, -a.y, at4(sm.N + (m + 1) * LD + c));
+      axpy4(s, -a.z, at4(sm.N + (m + 2) * LD + c));
+      axpy4(s, -a.w, at4(sm.N + (m + 3) * LD + c));
     }
     *reinterpret_cast<float4*>(sm.X + (32 + r) * LD + c) = make_float4(s[0], s[1], s[2], s[3]);
   }
@@ -358,27 +366,52 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const __grid_constant
   }
   tc_fence_before();
   __syncthreads();
+  uint32_t phase = 1;
+  if (BACK) {  // PT = P T
+    if (tid == 0) {
+      tc_fence_after();
+      const uint32_t id_pt = idesc_bf16(64, 64, false, true);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        umma_bf16(tb, desc_at(sw128_desc(sP, 16, 1024), kk * 32),
+                  desc_at(sw128_desc(sTt, TILE, 1024), kk * 2048), id_pt, kk > 0);
+      umma_commit(&sm.mma);
+    }
+    __syncwarp();
+    mbar_wait(&sm.mma, phase, wc, W_PREP_MMA);
+    phase ^= 1;
+    __syncwarp();
+    tc_fence_after();
+    float v[32];
+    tmem_ld32(tb + lo + 32 * hh, v);
+    tmem_ld_wait();
+    if (!isP) {
+      uint4* out = reinterpret_cast<uint4*>(p.m.PT + (((size_t)bh * N + n) * C + i) * C + 32 * hh);
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+        const float* x = v + 8 * cc;
+        out[cc] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                             pack_bf16(x[6], x[7]));
+      }
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
   if (tid == 0) {
     tc_fence_after();
     const uint32_t id_w = idesc_bf16(64, 128, false, true), id_wb = idesc_bf16(64, 128, true, true);
-    const uint32_t id_pt = idesc_bf16(64, 64, false, true);
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
       const uint64_t dk = desc_at(sw128_desc(sK, TILE, 1024), kk * 2048);  // K as [token][d_k]
-      umma_bf16(tb + COL_W, desc_at(sw128_desc(sTg, 16, 1024), kk * 32), dk, id_w, kk > 0);
-      if (SPLIT)
-        umma_bf16(tb + COL_W, desc_at(sw128_desc(sTg + TILE, 16, 1024), kk * 32), dk, id_w, 1);
-      if (BACK) {
-        umma_bf16(tb + COL_W + LANE16, desc_at(sw128_desc(sTw, TILE, 1024), kk * 2048), dk, id_wb,
-                  kk > 0);
-        umma_bf16(tb + COL_KQ, desc_at(sw128_desc(smem_u32(sm.P), 16, 1024), kk * 32),
-                  desc_at(sw128_desc(sTt, TILE, 1024), kk * 2048), id_pt, kk > 0);
-      }
+      umma_bf16(tb, desc_at(sw128_desc(sTg, 16, 1024), kk * 32), dk, id_w, kk > 0);
+      if (SPLIT) umma_bf16(tb, desc_at(sw128_desc(sTg + TILE, 16, 1024), kk * 32), dk, id_w, 1);
+      if (BACK)
+        umma_bf16(tb + LANE16, desc_at(sw128_desc(sTw, TILE, 1024), kk * 2048), dk, id_wb, kk > 0);
     }
     umma_commit(&sm.mma);
   }
   __syncwarp();
-  mbar_wait(&sm.mma, 1, wc, W_PREP_MMA);
+  mbar_wait(&sm.mma, phase, wc, W_PREP_MMA);
   __syncwarp();
   tc_fence_after();
   // W (lanes < 16) and Wb (lanes >= 16) to bf16, columns [64 hh, 64 hh + 64); staged over Q
@@ -386,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const __grid_constant
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     float v[32];
-    tmem_ld32(tb + COL_W + lo + 64 * hh + 32 * g, v);
+    tmem_ld32(tb + lo + 64 * hh + 32 * g, v);
     tmem_ld_wait();
     const uint32_t dst = (isP ? sK : sQ) + hh * TILE;
 #pragma unroll
@@ -414,24 +447,6 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const __grid_constant
     }
     tma_store_commit();
   }
-  __syncwarp();
-  if (BACK) {
-    tc_fence_after();
-    float v[32];
-    tmem_ld32(tb + COL_KQ + lo + 32 * hh, v);
-    tmem_ld_wait();
-    if (!isP) {
-      uint4* out = reinterpret_cast<uint4*>(p.m.PT + (((size_t)bh * N + n) * C + i) * C + 32 * hh);
-#pragma unroll
-      for (int cc = 0; cc < 4; ++cc) {
-        const float* x = v + 8 * cc;
-        out[cc] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                             pack_bf16(x[6], x[7]));
-      }
-    }
-    tc_fence_before();
-    __syncthreads();
-  }
   if (tid == 0) tma_store_wait_read();  // the CTA's shared memory may go once it has been read
   if (warp == 1) {
     tc_fence_after();
@@ -447,11 +462,12 @@ static cudaError_t launch(const CUtensorMap (&m)[5], const PrepParams& p, unsign
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (!bit || !(set.load() & bit)) {
     const cudaError_t e = cudaFuncSetAttribute(prep_kernel<SPLIT, BACK>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem_bytes<SPLIT && BACK>());
     if (e != cudaSuccess) return e;
     set.fetch_or(bit);
   }
-  prep_kernel<SPLIT, BACK><<<grid, kThreads, kSmem, st>>>(m[0], m[1], m[2], m[3], m[4], p);
+  prep_kernel<SPLIT, BACK><<<grid, kThreads, smem_bytes<SPLIT && BACK>(), st>>>(m[0], m[1], m[2], m[3], m[4], p);
   count_launch();
   return cudaGetLastError();
 }
