@@ -85,6 +85,11 @@ CASES = [
     (2, 2, 2, 130, 128, 128, "bf16", True, "empty"),
     (1, 2, 2, 130, 128, 128, "bf16", True, "reset"),
     (1, 2, 2, 1100, 128, 128, "bf16", True, "none"),
+    # few long scans, walked in segments
+    (1, 2, 1, 1283, 128, 256, "bf16", True, "none"),
+    (1, 2, 1, 1283, 128, 256, "bf16", False, "docs"),
+    (1, 1, 1, 2049, 128, 128, "bf16", True, "docs"),
+    (2, 3, 3, 770, 128, 128, "bf16", False, "empty"),
 ]
 
 

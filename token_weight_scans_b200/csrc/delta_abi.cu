@@ -72,6 +72,7 @@ cudaError_t fwd_run(const Dims& d, const void* q, const void* k, const void* v, 
     a.S0 = S0;
     a.y = y;
     a.ST = ST;
+    tc::set_segments(a, ws + kStatusBytes + tc::fwd_scratch_bytes(d) - tc::seg_bytes(d, true), a.sv.M);
     return tc::run_fwd(a, st);
   }
   ffma::Args a{d, q, k, v, beta, log_alpha, scale,
@@ -176,6 +177,8 @@ gradlev_status gradlev_delta_bwd(int B, int H, int Hk, int T, int d_k, int d_v, 
     a.dbeta = dbeta;
     a.dlog_alpha = dlog_alpha;
     a.dS0 = dS0;
+    delta::tc::set_segments(a, scratch + delta::tc::bwd_scratch_bytes(d) - delta::tc::seg_bytes(d, false),
+                            a.sv.M);
     return delta::tc::run_bwd(a, st) == cudaSuccess ? GRADLEV_OK : GRADLEV_ERR_CUDA;
   }
   delta::ffma::Args a{d, q, k, v, beta, log_alpha, scale, delta::ffma::saved_at(saved, d, true)};

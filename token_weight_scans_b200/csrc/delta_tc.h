@@ -5,6 +5,7 @@
 //   prep  (delta_tc_prep.cu): per chunk, what does not depend on the state;
 //   walk  (delta_tc_walk.cu): the state recurrence, forward or backward;
 //   grad  (delta_tc_grad.cu): per chunk, the gradients of q, k and the gates.
+// Few long scans are cut into segments that are walked at the same time (delta_tc_seg.cu).
 #pragma once
 
 #include <cuda.h>
@@ -66,8 +67,14 @@ struct GateBlock {
 // [B*H][N][dv][64] (the tokens of a chunk contiguous, as the walk has them), Wb, PT and gates.
 struct Saved {
   bf16 *S = nullptr, *D = nullptr, *Wb = nullptr, *PT = nullptr;
-  float* gates = nullptr;
+  float *gates = nullptr, *M = nullptr;  // M: the segments' maps, with segments
 };
+
+// Segments of `chunks` chunks each (the last may be shorter).
+struct SegPlan {
+  int nseg, chunks;
+};
+SegPlan seg_plan(const Dims& d);
 size_t saved_bytes(const Dims& d);
 Saved saved_at(char* base, const Dims& d);
 size_t fwd_scratch_bytes(const Dims& d);  // W, Wlo, T0, T0lo, Pb, gates
@@ -93,10 +100,17 @@ struct Args {
   bf16* dS = nullptr;       // [B*H][N][dv][128]: gradient of the chunk-end states
   void *dq = nullptr, *dk_ = nullptr, *dv_ = nullptr, *dbeta = nullptr, *dlog_alpha = nullptr;
   void* dS0 = nullptr;
+  SegPlan seg{1, 1 << 30};
+  float *loc = nullptr, *init = nullptr, *M = nullptr;  // with segments (WalkParams)
 };
 
+// Lays the segments' buffers out behind `at` (seg_bytes(d, own_M) bytes) and sets a.seg.
+void set_segments(Args& a, char* at, float* M);
+size_t seg_bytes(const Dims& d, bool own_M);
+
 cudaError_t launch_prep(const Args& a, bool split, cudaStream_t st);
-cudaError_t launch_walk(const Args& a, bool backward, bool split, cudaStream_t st);
+cudaError_t launch_walk(const Args& a, bool backward, bool split, bool sum, cudaStream_t st);
+cudaError_t launch_combine(const Args& a, bool backward, cudaStream_t st);
 cudaError_t launch_grad(const Args& a, cudaStream_t st);
 
 cudaError_t run_fwd(const Args& a, cudaStream_t st);

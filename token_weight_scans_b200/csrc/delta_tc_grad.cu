@@ -413,70 +413,6 @@ cudaError_t launch_grad(const Args& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// ---------------------------------------------------------------- buffers and order
-static size_t up256(size_t v) { return (v + 255) / 256 * 256; }
-
-static bf16* take(char*& at, size_t elems) {
-  bf16* p = reinterpret_cast<bf16*>(at);
-  at += up256(elems * sizeof(bf16));
-  return p;
-}
-static size_t gate_bytes(const Dims& d) {
-  return up256(d.BH() * chunks(d.T) * sizeof(GateBlock));
-}
-size_t token_rows_bytes(const Dims& d) { return up256(d.BH() * chunks(d.T) * d.dv * C * sizeof(bf16)); }
-
-Saved saved_at(char* base, const Dims& d) {
-  const size_t rows = d.BH() * chunks(d.T);
-  char* at = base;
-  Saved s;
-  s.S = take(at, rows * d.dv * 128);
-  s.D = take(at, rows * d.dv * C);
-  s.Wb = take(at, rows * C * 128);
-  s.PT = take(at, rows * C * C);
-  s.gates = reinterpret_cast<float*>(at);
-  return s;
-}
-
-size_t saved_bytes(const Dims& d) {
-  const size_t rows = d.BH() * chunks(d.T);
-  return up256(rows * d.dv * 256) + token_rows_bytes(d) + up256(rows * C * 256) +
-         up256(rows * C * C * 2) + gate_bytes(d);
-}
-
-Mats mats_at(char* base, const Dims& d) {
-  const size_t rows = d.BH() * chunks(d.T);
-  char* at = base;
-  Mats m;
-  m.W = take(at, rows * C * 128);
-  m.Wlo = take(at, rows * C * 128);
-  m.T0 = take(at, rows * C * C);
-  m.T0lo = take(at, rows * C * C);
-  m.Pb = take(at, rows * C * C);
-  m.gates = reinterpret_cast<float*>(at);
-  return m;
-}
-
-size_t fwd_scratch_bytes(const Dims& d) {
-  const size_t rows = d.BH() * chunks(d.T);
-  return 2 * up256(rows * C * 256) + 3 * up256(rows * C * C * 2) + gate_bytes(d);
-}
-
-size_t bwd_scratch_bytes(const Dims& d) {
-  return token_rows_bytes(d) + up256(d.BH() * chunks(d.T) * d.dv * 256);
-}
-
-cudaError_t run_fwd(const Args& a, cudaStream_t st) {
-  const bool split = a.ST != nullptr;
-  const cudaError_t e = launch_prep(a, split, st);
-  return e != cudaSuccess ? e : launch_walk(a, false, split, st);
-}
-
-cudaError_t run_bwd(const Args& a, cudaStream_t st) {
-  const cudaError_t e = launch_walk(a, true, false, st);
-  return e != cudaSuccess ? e : launch_grad(a, st);
-}
-
 }  // namespace tc
 }  // namespace delta
 }  // namespace gradlev

@@ -1,0 +1,201 @@
+// Tensor-core gated delta rule: few long scans in segments, and the order of the kernels.
+//
+// Within a segment the state after is affine in the state before, S_end = S_start M + L, with
+// one 128 x 128 matrix M per (b, h, segment) that every row of S shares: the products of the
+// chunks' maps. A first walk over all segments at once carries zero (which gives L) and, as
+// one more slice of rows, the identity (which gives M); launch_combine runs the short serial
+// recursion over the segments; the walk proper then starts every segment from its own state.
+// Backward the same with dS_start = dS_end M^T + L', with the M of the forward.
+//
+// The first walk costs about as much again, so segments pay where the scans leave the GPU
+// idle: B1 H16 T32768 d_v 256 has 32 CTAs of 512 chunks without them, and with four segments
+// 144 and then 144 of 128 chunks.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "delta_tc.h"
+
+namespace gradlev {
+namespace delta {
+namespace tc {
+
+namespace {
+
+constexpr int kSMs = 148;
+constexpr int kMinChunks = 4;    // per segment
+constexpr int kMaxSeg = 16;
+constexpr int kRows = 16, kThreads = 256;
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+size_t state_bytes(const Dims& d, int nseg) {
+  return up256(d.BH() * nseg * d.dv * 128 * sizeof(float));
+}
+
+// kRows rows of one scan through its segments: out[s] = out[s -+ 1] M (M^T) + L. Thread: column
+// c, kRows / 2 rows. BWD: from the last segment.
+template <bool BWD>
+__global__ void __launch_bounds__(kThreads) combine_kernel(int dv, int nseg, const float* L,
+                                                           const float* M, const float* S0,
+                                                           const bf16* dST, float* out) {
+  __shared__ __align__(16) float S[kRows][132];
+  const int nb = dv / kRows, bh = blockIdx.x / nb, r0 = (blockIdx.x - bh * nb) * kRows;
+  const int c = threadIdx.x & 127, h = (threadIdx.x >> 7) * (kRows / 2);
+  float s[kRows / 2];
+#pragma unroll
+  for (int e = 0; e < kRows / 2; ++e) {
+    const size_t at = ((size_t)bh * dv + r0 + h + e) * 128 + c;
+    s[e] = BWD ? (dST ? __bfloat162float(dST[at]) : 0.f) : (S0 ? S0[at] : 0.f);
+  }
+  for (int i = 0; i < nseg; ++i) {
+    const int seg = BWD ? nseg - 1 - i : i;
+    const size_t sg = (size_t)bh * nseg + seg;
+#pragma unroll
+    for (int e = 0; e < kRows / 2; ++e) {
+      out[(sg * dv + r0 + h + e) * 128 + c] = s[e];
+      S[h + e][c] = s[e];
+    }
+    if (i + 1 == nseg) break;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kRows / 2; ++e) s[e] = L[(sg * dv + r0 + h + e) * 128 + c];
+    const float* m = M + sg * 128 * 128;
+#pragma unroll 4
+    for (int k = 0; k < 128; k += 4) {
+      const float4 mv = BWD ? *reinterpret_cast<const float4*>(m + c * 128 + k)
+                            : make_float4(m[k * 128 + c], m[(k + 1) * 128 + c],
+                                          m[(k + 2) * 128 + c], m[(k + 3) * 128 + c]);
+#pragma unroll
+      for (int e = 0; e < kRows / 2; ++e) {
+        const float4 v = *reinterpret_cast<const float4*>(&S[h + e][k]);
+        s[e] = fmaf(v.x, mv.x, s[e]);
+        s[e] = fmaf(v.y, mv.y, s[e]);
+        s[e] = fmaf(v.z, mv.z, s[e]);
+        s[e] = fmaf(v.w, mv.w, s[e]);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+// The most segments whose CTAs still run at once, both in the first walk (the slices and the
+// identity, all segments but one) and in the walk proper (and the last segment's identity).
+SegPlan seg_plan(const Dims& d) {
+  const long long BH = (long long)d.B * d.H, ns = d.dv / 128;
+  const int N = chunks(d.T);
+  for (int s = kMaxSeg; s >= 3; --s) {
+    const int per = (N + s - 1) / s, nseg = (N + per - 1) / per;
+    if (nseg >= 3 && per >= kMinChunks && BH * (ns + 1) * (nseg - 1) <= kSMs &&
+        BH * (ns * nseg + 1) <= kSMs)
+      return SegPlan{nseg, per};
+  }
+  return SegPlan{1, N};
+}
+
+size_t seg_bytes(const Dims& d, bool own_M) {
+  const SegPlan s = seg_plan(d);
+  if (s.nseg == 1) return 0;
+  return 2 * state_bytes(d, s.nseg) + (own_M ? d.BH() * s.nseg * 128 * 128 * sizeof(float) : 0);
+}
+
+void set_segments(Args& a, char* at, float* M) {
+  a.seg = seg_plan(a.d);
+  if (a.seg.nseg == 1) return;
+  a.loc = reinterpret_cast<float*>(at);
+  a.init = reinterpret_cast<float*>(at + state_bytes(a.d, a.seg.nseg));
+  a.M = M ? M : reinterpret_cast<float*>(at + 2 * state_bytes(a.d, a.seg.nseg));
+}
+
+cudaError_t launch_combine(const Args& a, bool backward, cudaStream_t st) {
+  const unsigned grid = (unsigned)(a.d.BH() * (a.d.dv / kRows));
+  if (backward)
+    combine_kernel<true><<<grid, kThreads, 0, st>>>(a.d.dv, a.seg.nseg, a.loc, a.M, nullptr,
+                                                    static_cast<const bf16*>(a.dST), a.init);
+  else
+    combine_kernel<false><<<grid, kThreads, 0, st>>>(a.d.dv, a.seg.nseg, a.loc, a.M, a.S0, nullptr,
+                                                     a.init);
+  count_launch();
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- the kernels in order
+static cudaError_t walk(const Args& a, bool backward, bool split, cudaStream_t st) {
+  if (a.seg.nseg > 1) {
+    cudaError_t e = launch_walk(a, backward, split, true, st);
+    if (e == cudaSuccess) e = launch_combine(a, backward, st);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_walk(a, backward, split, false, st);
+}
+
+cudaError_t run_fwd(const Args& a, cudaStream_t st) {
+  const bool split = a.ST != nullptr;
+  const cudaError_t e = launch_prep(a, split, st);
+  return e != cudaSuccess ? e : walk(a, false, split, st);
+}
+
+cudaError_t run_bwd(const Args& a, cudaStream_t st) {
+  const cudaError_t e = walk(a, true, false, st);
+  return e != cudaSuccess ? e : launch_grad(a, st);
+}
+
+// ---------------------------------------------------------------- buffers
+static bf16* take(char*& at, size_t elems) {
+  bf16* p = reinterpret_cast<bf16*>(at);
+  at += up256(elems * sizeof(bf16));
+  return p;
+}
+static size_t gate_bytes(const Dims& d) {
+  return up256(d.BH() * chunks(d.T) * sizeof(GateBlock));
+}
+size_t token_rows_bytes(const Dims& d) { return up256(d.BH() * chunks(d.T) * d.dv * C * sizeof(bf16)); }
+
+Saved saved_at(char* base, const Dims& d) {
+  const size_t rows = d.BH() * chunks(d.T);
+  char* at = base;
+  Saved s;
+  s.S = take(at, rows * d.dv * 128);
+  s.D = take(at, rows * d.dv * C);
+  s.Wb = take(at, rows * C * 128);
+  s.PT = take(at, rows * C * C);
+  s.gates = reinterpret_cast<float*>(at);
+  s.M = reinterpret_cast<float*>(at + gate_bytes(d));
+  return s;
+}
+
+size_t saved_bytes(const Dims& d) {
+  const size_t rows = d.BH() * chunks(d.T);
+  const int nseg = seg_plan(d).nseg;
+  return up256(rows * d.dv * 256) + token_rows_bytes(d) + up256(rows * C * 256) +
+         up256(rows * C * C * 2) + gate_bytes(d) +
+         (nseg > 1 ? d.BH() * nseg * 128 * 128 * sizeof(float) : 0);
+}
+
+Mats mats_at(char* base, const Dims& d) {
+  const size_t rows = d.BH() * chunks(d.T);
+  char* at = base;
+  Mats m;
+  m.W = take(at, rows * C * 128);
+  m.Wlo = take(at, rows * C * 128);
+  m.T0 = take(at, rows * C * C);
+  m.T0lo = take(at, rows * C * C);
+  m.Pb = take(at, rows * C * C);
+  m.gates = reinterpret_cast<float*>(at);
+  return m;
+}
+
+size_t fwd_scratch_bytes(const Dims& d) {  // the segments' buffers come last
+  const size_t rows = d.BH() * chunks(d.T);
+  return 2 * up256(rows * C * 256) + 3 * up256(rows * C * C * 2) + gate_bytes(d) +
+         seg_bytes(d, true);
+}
+
+size_t bwd_scratch_bytes(const Dims& d) {  // E, dS, the segments' buffers
+  return token_rows_bytes(d) + up256(d.BH() * chunks(d.T) * d.dv * 256) + seg_bytes(d, false);
+}
+
+}  // namespace tc
+}  // namespace delta
+}  // namespace gradlev

@@ -122,6 +122,13 @@ struct WalkParams {
   bf16* y;               // forward
   bf16* D;               // forward: D^T, backward: E^T (null: not kept)
   bf16* states;          // chunk-start (chunk-end) states, or null
+  // Segments (delta_tc_seg.cu): CTA u < nsl B H segs walks segment seg0 + u / (nsl B H); the
+  // slice past the last one carries the identity. CTAs past those carry it through the last
+  // segment.
+  int nseg, seg_chunks, seg0, segs, nsl;
+  int sum;               // states alone: nothing is left for other kernels but loc and M
+  const float* init;     // [B*H][nseg][dv][128] states the segments start from, or null
+  float *loc, *M;        // [B*H][nseg][dv][128], [B*H][nseg][128][128]
 };
 
 __device__ __forceinline__ void st_tmem32(uint32_t col, const uint32_t (&r)[32]) {
@@ -227,11 +234,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   Bars<BWD>& sm = *reinterpret_cast<Bars<BWD>*>(base + L::bars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ns = p.d.dv >> 7, bh = blockIdx.x / ns, n0 = (blockIdx.x - bh * ns) * 128;
+  const int BH = p.d.B * p.d.H, per_seg = p.nsl * BH;
+  const bool extra = (int)blockIdx.x >= per_seg * p.segs;
+  const int in_seg = extra ? blockIdx.x - per_seg * p.segs : blockIdx.x % per_seg;
+  const int seg = extra ? p.nseg - 1 : p.seg0 + blockIdx.x / per_seg;
+  const int bh = extra ? in_seg : in_seg / p.nsl, slice = extra ? 0 : in_seg - bh * p.nsl;
+  const bool ident = extra || slice == p.d.dv >> 7;  // carries the identity: the segment's map
+  const int n0 = ident ? 0 : slice * 128;
+  const bool carry = p.sum || ident;                 // the end state is all that is wanted
+  const bool outputs = !BWD && !carry;               // the forward's products for Y
+  const size_t sg = (size_t)bh * p.nseg + seg;
   const int b = bh / p.d.H, h = bh - b * p.d.H;
   const int kh = b * p.d.Hk + h / (p.d.H / p.d.Hk);
   const int T = p.d.T, N = chunks(T);
-  auto cg = [&](int c) { return BWD ? N - 1 - c : c; };  // the c-th chunk walked
+  const int c0 = seg * p.seg_chunks, NC = min(N - c0, p.seg_chunks);  // the chunks walked
+  auto cg = [&](int c) { return BWD ? c0 + NC - 1 - c : c0 + c; };
   const WaitCtx wc{&sm.abort, p.status, p.timeout_ns};
 
   if (threadIdx.x == 0) {
@@ -278,28 +295,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         issued[r] = c + 1;
         return true;
       };
-      for (int c = 0; c < N; ++c) {
+      for (int c = 0; c < NC; ++c) {
         const int s = c % NS, t0 = cg(c) * C;
         if (warp == 0) {
           uint8_t* a = base + L::vt(s);
           uint64_t* f = &sm.full[VT][s];
           if (!open(VT, c, L::vt_bytes)) break;
-          tma_load_3d(a + L::v, &tmV, f, n0, t0, bh);
-          tma_load_3d(a + L::v + TILE, &tmV, f, n0 + 64, t0, bh);
+          const int tv = ident ? N * C : t0;  // past the last token: zeros
+          tma_load_3d(a + L::v, &tmV, f, n0, tv, bh);
+          tma_load_3d(a + L::v + TILE, &tmV, f, n0 + 64, tv, bh);
           tma_load_3d(a + L::t, &tmT, f, 0, t0, bh);
           if (SPLIT) tma_load_3d(a + L::tl, &tmTl, f, 0, t0, bh);
           a = base + L::kp(s);
           f = &sm.full[KP][s];
-          if (!open(KP, c, L::kp_bytes)) break;
+          if (!open(KP, c, L::kp_bytes - (!BWD && carry ? TILE : 0))) break;
           tma_load_3d(a + L::k, &tmK, f, 0, t0, kh);
           tma_load_3d(a + L::k + TILE, &tmK, f, 64, t0, kh);
-          if (!BWD) tma_load_3d(a + L::p, &tmP, f, 0, t0, bh);
+          if (outputs) tma_load_3d(a + L::p, &tmP, f, 0, t0, bh);
         } else {
           uint8_t* a = base + L::wq_at(s);
           uint64_t* f = &sm.full[WQ][s];
-          if (!open(WQ, c, L::wq_bytes)) break;
+          if (!open(WQ, c, L::wq_bytes - (!BWD && carry ? 2 * TILE : 0))) break;
           for (int kb = 0; kb < 2; ++kb) {
-            tma_load_3d(a + L::q + kb * L::wq, &tmQ, f, 64 * kb, t0, kh);
+            if (BWD || outputs) tma_load_3d(a + L::q + kb * L::wq, &tmQ, f, 64 * kb, t0, kh);
             tma_load_3d(a + L::w + kb * L::wq, &tmW, f, 64 * kb, t0, bh);
             if (SPLIT) tma_load_3d(a + L::wl + kb * TILE, &tmWl, f, 64 * kb, t0, bh);
           }
@@ -337,12 +355,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       bool ok = first(0);
-      for (int c = 0; c < N && ok; ++c) {
+      for (int c = 0; c < NC && ok; ++c) {
         const int s = c % NS, yb = c % NY;
         const uint32_t st = smem_u32(base + L::wq_at(s)), sv = smem_u32(base + L::vt(s));
         const uint32_t sk = smem_u32(base + L::kp(s));
         const uint32_t d = tb + COL_D + 128 * yb, y = d + 64;
-        if (!mbar_wait(&sm.scaled[s], (c / NS) & 1, wc, W_SCALED)) break;
+        if (!mbar_wait(carry && !BWD ? &sm.full[WQ][s] : &sm.scaled[s], (c / NS) & 1, wc, W_SCALED)) break;
         if (!mbar_wait(&sm.sready, c & 1, wc, W_SREADY)) break;
         tc_fence_after();
 #pragma unroll
@@ -350,11 +368,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t off = (kk >> 2) * L::wq + (kk & 3) * 32;
           const uint64_t bw = desc_at(sw128_desc(st + L::w, 16, 1024), off);
           const uint32_t a = tb + COL_SH + 8 * kk;
-          if (!BWD && !SPLIT && kk > 0) {
+          if (!SPLIT && outputs && kk > 0) {
             umma_bf16_tmem_a(d, a, bw, id_wq, 1);
           } else {
             umma_bf16_tmem_a(d, a, bw, id_w, 1);
-            if (!BWD && !SPLIT) umma_bf16_tmem_a(y, a, desc_at(sw128_desc(st + L::q, 16, 1024), off), id_w, 0);
+            if (!SPLIT && outputs)
+              umma_bf16_tmem_a(y, a, desc_at(sw128_desc(st + L::q, 16, 1024), off), id_w, 0);
           }
           if (SPLIT) {
             umma_bf16_tmem_a(d, tb + COL_SL + 8 * kk, bw, id_w, 1);
@@ -374,15 +393,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (SPLIT) {  // Y^T = S Q^T, which frees the bf16 state
           if (!mbar_wait(&sm.yfree[0], (c & 1) ^ 1, wc, W_YFREE)) break;
           tc_fence_after();
+          if (outputs) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_bf16_tmem_a(y, tb + COL_SH + 8 * kk,
-                             desc_at(sw128_desc(st + L::q, 16, 1024), (kk >> 2) * L::wq + (kk & 3) * 32),
-                             id_w, kk > 0);
+            for (int kk = 0; kk < 8; ++kk)
+              umma_bf16_tmem_a(y, tb + COL_SH + 8 * kk,
+                               desc_at(sw128_desc(st + L::q, 16, 1024),
+                                       (kk >> 2) * L::wq + (kk & 3) * 32), id_w, kk > 0);
+          }
           umma_commit(&sm.empty[WQ][s]);
         } else {
           umma_commit(&sm.empty[WQ][s]);
-          if (c + 1 < N && !first(c + 1)) break;
+          if (c + 1 < NC && !first(c + 1)) break;
         }
         if (!mbar_wait(&sm.full[KP][s], (c / NS) & 1, wc, W_FULL)) break;
         if (!mbar_wait(&sm.uready, c & 1, wc, W_UREADY)) break;
@@ -395,14 +416,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         umma_commit(&sm.sfull);
         if (!BWD) {
+          if (outputs) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // Y^T += D^T Pb^T
-            umma_bf16_tmem_a(y, tb + COL_DB + 8 * kk, desc_at(sw128_desc(sk + L::p, 16, 1024), kk * 32),
-                             id_w, 1);
+            for (int kk = 0; kk < 4; ++kk)  // Y^T += D^T Pb^T
+              umma_bf16_tmem_a(y, tb + COL_DB + 8 * kk,
+                               desc_at(sw128_desc(sk + L::p, 16, 1024), kk * 32), id_w, 1);
+          }
           umma_commit(&sm.yfull[yb]);
         }
         umma_commit(&sm.empty[KP][s]);
-        if ((BWD || SPLIT) && c + 1 < N) ok = first(c + 1);
+        if ((BWD || SPLIT) && c + 1 < NC) ok = first(c + 1);
       }
       umma_commit(&sm.done);
       mbar_drain(&sm.done, 0, wc, W_DONE);
@@ -412,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       const char* src = reinterpret_cast<const char*>(p.gates) + GateSlot<BWD>::offset;
       int issued = 0;
-      for (int c = 0; c < N; ++c) {
+      for (int c = 0; c < NC; ++c) {
         const int g = c % GS;
         if (!mbar_wait(&sm.gempty[g], ((c / GS) & 1) ^ 1, wc, W_GATE)) break;
         mbar_arrive_expect_tx(&sm.gfull[g], sizeof(GateSlot<BWD>));
@@ -435,9 +458,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       float v[32];
       const int col = 64 * hh + 32 * hf;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] = 0.f;
-      if (!BWD && p.S0) {
-        const float4* s = reinterpret_cast<const float4*>(p.S0 + row * 128 + col);
+      for (int e = 0; e < 32; ++e) v[e] = ident && col + e == r ? 1.f : 0.f;
+      const float* from = p.init ? p.init + (sg * p.d.dv + n0 + r) * 128
+                                 : (!BWD && p.S0 ? p.S0 + row * 128 : nullptr);
+      if (!carry && from) {
+        const float4* s = reinterpret_cast<const float4*>(from + col);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float4 u = s[e];
@@ -447,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           v[4 * e + 3] = u.w;
         }
       }
-      if (BWD && p.dST) {
+      if (BWD && !carry && !p.init && p.dST) {
         const uint4* s = reinterpret_cast<const uint4*>(p.dST + row * 128 + col);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -464,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tmem_st_wait();
     bool ok = true;
-    for (int c = 0; c < N && ok; ++c) {
+    for (int c = 0; c < NC && ok; ++c) {
       const int g = c % GS, n = cg(c);
       const GateSlot<BWD>& gs = sm.gates[g];
       ok = mbar_wait_warp(&sm.gfull[g], (c / GS) & 1, wc, W_C_GATE);
@@ -496,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.sready);
-      if (p.states) {
+      if (p.states && !carry) {
         if (L::staged) {
           if (lane == 0) tma_store_wait_read_n<0>();  // the store of the chunk before
           __syncwarp();
@@ -545,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.uready);
-      if (p.D) {
+      if (p.D && !carry) {
         if (L::staged) {  // a warp stores its own 32 rows x 32 tokens (64-byte rows and swizzle)
           if (lane == 0) tma_store_wait_read_n<1>();  // all but S of this chunk
           __syncwarp();
@@ -573,8 +598,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&sm.gempty[g]);
     }
     if (lane == 0 && L::staged) tma_store_wait_all();
-    if (ok && (BWD ? p.dS0 != nullptr : p.ST != nullptr) &&
-        mbar_wait_warp(&sm.sfull, (N - 1) & 1, wc, W_C_SFULL)) {
+    float* end = ident ? p.M + (sg * 128 + r) * 128
+                       : carry ? p.loc + (sg * p.d.dv + n0 + r) * 128
+                               : !BWD && p.ST && seg == p.nseg - 1 ? p.ST + row * 128 : nullptr;
+    bf16* end16 = BWD && !carry && p.dS0 && seg == 0 ? p.dS0 + row * 128 : nullptr;
+    if (ok && (end || end16) && mbar_wait_warp(&sm.sfull, (NC - 1) & 1, wc, W_C_SFULL)) {
       tc_fence_after();
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
@@ -582,12 +610,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int col = 64 * hh + 32 * hf;
         tmem_ld32(tb + COL_S + lo + col, v);
         tmem_ld_wait();
-        if (!BWD) {
-          float4* o = reinterpret_cast<float4*>(p.ST + row * 128 + col);
+        if (end) {
+          float4* o = reinterpret_cast<float4*>(end + col);
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         } else {
-          uint4* o = reinterpret_cast<uint4*>(p.dS0 + row * 128 + col);
+          uint4* o = reinterpret_cast<uint4*>(end16 + col);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             o[e] = make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
@@ -601,6 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lo = (uint32_t)(32 * q) << 16;
     auto scale_chunk = [&](int c) -> bool {
       const int s = c % NS, g = c % GS;
+      if (!BWD && carry) return true;
       if (!mbar_wait_warp(&sm.full[WQ][s], (c / NS) & 1, wc, W_O_FULL)) return false;
       if (!mbar_wait_warp(&sm.gfull[g], (c / GS) & 1, wc, W_O_GATE)) return false;
       scale_tile(smem_u32(base + L::wq_at(s)) + L::q, L::wq, sm.gates[g].q, t);
@@ -647,21 +676,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     bool ok = scale_chunk(0);
-    for (int c = 0; c < N; ++c) {
+    for (int c = 0; c < NC; ++c) {
       const int g = c % GS, yb = c % NY, t0 = cg(c) * C;
-      if (ok && c + 1 < N) ok = scale_chunk(c + 1);
+      if (ok && c + 1 < NC) ok = scale_chunk(c + 1);
       ok = ok && mbar_wait_warp(&sm.yfull[yb], (c / NY) & 1, wc, W_O_Y);
       // the warps of emit() meet at barriers: all of them go on, or none does
       ok = !named_bar_or(2, 128, !ok);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = COL_D + 128 * yb;
-      if constexpr (BWD) {
+      if (carry || (!BWD && !p.y)) {
+        if (lane == 0) mbar_arrive(&sm.yfree[yb]);
+      } else if constexpr (BWD) {
         emit(d, &tmY, sm.gates[g].be, t0, &sm.yfree[yb]);  // dV = beta E
-      } else if (p.y) {
+      } else {
         emit(d + 64, &tmY, nullptr, t0, &sm.yfree[yb]);
-      } else if (lane == 0) {
-        mbar_arrive(&sm.yfree[yb]);
       }
       if (lane == 0) mbar_arrive(&sm.gempty[g]);
     }
@@ -676,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool BWD, bool SPLIT>
-static cudaError_t launch(const Args& a, cudaStream_t st) {
+static cudaError_t launch(const Args& a, bool sum, cudaStream_t st) {
   using L = Layout<BWD, SPLIT>;
   using gradlev::tc::make_map_bf16_3d;
   const Dims& d = a.d;
@@ -710,18 +739,29 @@ static cudaError_t launch(const Args& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     set.fetch_or(bit);
   }
+  const int ns = d.dv / 128, nseg = a.seg.nseg;
   WalkParams p{d, BWD ? a.sv.gates : a.m.gates, a.status, a.timeout_ns, a.S0,
                static_cast<const bf16*>(a.dST), a.ST, static_cast<bf16*>(a.dS0),
-               static_cast<bf16*>(a.y), dd, states};
-  walk_kernel<BWD, SPLIT><<<(unsigned)(bh * (d.dv / 128)), kThreads, L::smem, st>>>(
+               static_cast<bf16*>(a.y), dd, states, nseg, a.seg.chunks, 0, nseg, ns, sum,
+               nseg > 1 ? a.init : nullptr, a.loc, a.M};
+  unsigned grid = (unsigned)(bh * ns * nseg);
+  if (sum) {  // forward: all segments but the last, with the identity; backward: all but the first
+    p.seg0 = BWD ? 1 : 0;
+    p.segs = nseg - 1;
+    p.nsl = BWD ? ns : ns + 1;
+    grid = (unsigned)(bh * p.nsl * p.segs);
+  } else if (!BWD && nseg > 1 && a.sv.S) {
+    grid += (unsigned)bh;  // the last segment's map, for the backward
+  }
+  walk_kernel<BWD, SPLIT><<<grid, kThreads, L::smem, st>>>(
       mq, mk, mv, mw, mwl, mt, mtl, mp, ms, my, md, p);
   count_launch();
   return cudaGetLastError();
 }
 
-cudaError_t launch_walk(const Args& a, bool backward, bool split, cudaStream_t st) {
-  if (backward) return launch<true, false>(a, st);
-  return split ? launch<false, true>(a, st) : launch<false, false>(a, st);
+cudaError_t launch_walk(const Args& a, bool backward, bool split, bool sum, cudaStream_t st) {
+  if (backward) return launch<true, false>(a, sum, st);
+  return split ? launch<false, true>(a, sum, st) : launch<false, false>(a, sum, st);
 }
 
 }  // namespace tc
