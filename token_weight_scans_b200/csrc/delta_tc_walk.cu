@@ -363,22 +363,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait(carry && !BWD ? &sm.full[WQ][s] : &sm.scaled[s], (c / NS) & 1, wc, W_SCALED)) break;
         if (!mbar_wait(&sm.sready, c & 1, wc, W_SREADY)) break;
         tc_fence_after();
+        // D^T += S W^T, and without SPLIT Y^T = S Q^T in the same products
+        if (!SPLIT && outputs) {
+          umma_bf16_tmem_a(d, tb + COL_SH, sw128_desc(st + L::w, 16, 1024), id_w, 1);
+          umma_bf16_tmem_a(y, tb + COL_SH, sw128_desc(st + L::q, 16, 1024), id_w, 0);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {  // D^T += S W^T (and Y^T = S Q^T)
-          const uint32_t off = (kk >> 2) * L::wq + (kk & 3) * 32;
-          const uint64_t bw = desc_at(sw128_desc(st + L::w, 16, 1024), off);
-          const uint32_t a = tb + COL_SH + 8 * kk;
-          if (!SPLIT && outputs && kk > 0) {
-            umma_bf16_tmem_a(d, a, bw, id_wq, 1);
-          } else {
-            umma_bf16_tmem_a(d, a, bw, id_w, 1);
-            if (!SPLIT && outputs)
-              umma_bf16_tmem_a(y, a, desc_at(sw128_desc(st + L::q, 16, 1024), off), id_w, 0);
-          }
-          if (SPLIT) {
-            umma_bf16_tmem_a(d, tb + COL_SL + 8 * kk, bw, id_w, 1);
-            umma_bf16_tmem_a(d, a, desc_at(sw128_desc(st + L::wl, 16, 1024),
-                                           (kk >> 2) * TILE + (kk & 3) * 32), id_w, 1);
+          for (int kk = 1; kk < 8; ++kk)
+            umma_bf16_tmem_a(d, tb + COL_SH + 8 * kk,
+                             desc_at(sw128_desc(st + L::w, 16, 1024), (kk >> 2) * L::wq + (kk & 3) * 32),
+                             id_wq, 1);
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint64_t bw =
+                desc_at(sw128_desc(st + L::w, 16, 1024), (kk >> 2) * L::wq + (kk & 3) * 32);
+            umma_bf16_tmem_a(d, tb + COL_SH + 8 * kk, bw, id_w, 1);
+            if (SPLIT) {
+              umma_bf16_tmem_a(d, tb + COL_SL + 8 * kk, bw, id_w, 1);
+              umma_bf16_tmem_a(d, tb + COL_SH + 8 * kk,
+                               desc_at(sw128_desc(st + L::wl, 16, 1024),
+                                       (kk >> 2) * TILE + (kk & 3) * 32), id_w, 1);
+            }
           }
         }
         umma_commit(&sm.dfull);
@@ -545,6 +550,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             out[cc] = make_uint4(pk[4 * cc], pk[4 * cc + 1], pk[4 * cc + 2], pk[4 * cc + 3]);
         }
       }
+      // this warp's 32 factors, before the wait: shared memory is busy with operands after it
+      float uf[32];
+#pragma unroll
+      for (int e = 0; e < 32; e += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(gs.u + 32 * hh + e);
+        uf[e] = f.x;
+        uf[e + 1] = f.y;
+        uf[e + 2] = f.z;
+        uf[e + 3] = f.w;
+      }
       ok = mbar_wait_warp(&sm.dfull, c & 1, wc, W_C_DFULL);
       if (!ok) break;
       tc_fence_after();
@@ -556,8 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t ub[16], rest[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float2 f = *reinterpret_cast<const float2*>(gs.u + 32 * hh + 2 * e);
-          const float u0 = v[2 * e] * f.x, u1 = v[2 * e + 1] * f.y;
+          const float u0 = v[2 * e] * uf[2 * e], u1 = v[2 * e + 1] * uf[2 * e + 1];
           ub[e] = pack_bf16(u0, u1);
           db[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
           if (SPLIT) rest[e] = pack_rest(u0, u1, ub[e]);
