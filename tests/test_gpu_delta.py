@@ -128,6 +128,14 @@ def test_forward_and_gradients(case):
     check(out, want, dtype, [n for n in want if mask != "reset" or n in ("dq", "dk", "dv", "dbeta")])
 
 
+@pytest.mark.parametrize("B,H,dtype,d", [(1, 2, "f32", 32), (1, 2, "bf16", 128), (40, 8, "bf16", 128)])
+def test_first_token_of_an_empty_state_has_no_gate_gradient(B, H, dtype, d):
+    """One token and no start state: log_alpha multiplies zero, so its gradient is zero itself."""
+    g = dev(ref.draw(B, H, H, 1, d, d, dtype, False, seed=3))
+    out = tw.gradlev_delta_bwd(*[g[n] for n in NAMES], g["dy"])
+    assert not out["dlog_alpha"].any()
+
+
 @pytest.mark.parametrize("dtype,dv", [("f32", 32), ("bf16", 128), ("bf16", 256)])
 def test_split_sequence_carries_the_state(dtype, dv):
     B, H, Hk, T, dk, cut = 1, 2, 1, 150, 128 if dtype == "bf16" else 32, 77

@@ -31,16 +31,28 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;  // bound of device-side waits
 
-size_t ckpt_bytes(const Dims& d) {
-  return tc::shape_ok(d) ? tc::saved_bytes(d) : ffma::saved_bytes(d, true);
+// A gate's gradient is one dot product of two bf16-rounded rows: 4e-3 off over many gates (in
+// the 2-norm), but any single one that happens to be small may be much further off. Calls whose
+// gradients have at most kFewGates of them take the float32 kernels (90 us in place of 41 us
+// for B1 H4 T32 d128, forward and gradients); without gradients there is no such value.
+constexpr size_t kFewGates = 128;
+bool use_tc(const Dims& d, bool gradients) {
+  return tc::shape_ok(d) && !(gradients && d.BH() * d.T <= kFewGates);
 }
 
-size_t fwd_scratch(const Dims& d) {
-  return tc::shape_ok(d) ? tc::fwd_scratch_bytes(d) : ffma::saved_bytes(d, false);
+size_t ckpt_bytes(const Dims& d) {
+  return use_tc(d, true) ? tc::saved_bytes(d) : ffma::saved_bytes(d, true);
+}
+
+size_t fwd_scratch(const Dims& d) {  // whichever family the call takes
+  const size_t f = ffma::saved_bytes(d, false);
+  if (!tc::shape_ok(d)) return f;
+  const size_t t = tc::fwd_scratch_bytes(d);
+  return use_tc(d, true) || t > f ? t : f;
 }
 
 size_t bwd_scratch(const Dims& d) {  // E and the chunk-end gradients of the state
-  if (tc::shape_ok(d)) return tc::bwd_scratch_bytes(d);
+  if (use_tc(d, true)) return tc::bwd_scratch_bytes(d);
   return up256(d.BH() * d.T * d.dv * sizeof(float)) +
          up256(d.BH() * ffma::chunks(d.T) * d.dv * d.dk * sizeof(float));
 }
@@ -60,7 +72,7 @@ bool aligned(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
 cudaError_t fwd_run(const Dims& d, const void* q, const void* k, const void* v, const float* beta,
                     const float* log_alpha, float scale, const float* S0, void* y, float* ST,
                     char* saved, char* ws, cudaStream_t st) {
-  if (tc::shape_ok(d)) {
+  if (use_tc(d, saved != nullptr)) {
     tc::Args a{d, q, k, v, beta, log_alpha, scale, reinterpret_cast<DeviceStatus*>(ws),
                kWaitTimeoutNs, tc::mats_at(ws + kStatusBytes, d)};
     if (saved) {
@@ -163,7 +175,7 @@ gradlev_status gradlev_delta_bwd(int B, int H, int Hk, int T, int d_k, int d_v, 
       return GRADLEV_ERR_CUDA;
   }
   char* scratch = ws + kStatusBytes;
-  if (delta::tc::shape_ok(d)) {
+  if (use_tc(d, true)) {
     delta::tc::Args a{d, q, k, v, beta, log_alpha, scale, reinterpret_cast<DeviceStatus*>(ws),
                kWaitTimeoutNs};
     a.sv = delta::tc::saved_at(saved, d);

@@ -44,7 +44,7 @@ struct GradSmem {
   GateBlock g;
   float Lh[C], Ll[C];                        // where a reset or strong decays rule out g.fac
   int seg[C];
-  float xs[2][C], zs[2][C];                  // per column half
+  float xs[2][C], ps[2][C], zs[2][C];        // per column half
   float red[8];
   uint64_t kq, full, mma;
   uint32_t tmem_base;
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ---- t (lower) and u (upper); z (upper)
     const uint8_t* mine = (up ? sm.K : sm.Q) + hh * TILE;
     const float ca = up ? sm.g.bG[i] : sm.g.q[i], cz = up ? sm.g.bw[i] : 0.f;
-    float xs = 0.f, zs = 0.f;
+    float xs = 0.f, ps = 0.f, zs = 0.f;
 #pragma unroll
     for (int hf = 0; hf < 4; ++hf) {
       float v[16], z[16], x[16];
@@ -316,12 +316,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         dot = fmaf(up ? ye - v[e] : v[e], x[e], dot);
         acc[16 * hf + e] += v[e] + ye;
       }
-      xs += dot;
+      ps += dot;
     }
     xs += __shfl_xor_sync(0xffffffffu, xs, 16);
+    ps += __shfl_xor_sync(0xffffffffu, ps, 16);
     zs += __shfl_xor_sync(0xffffffffu, zs, 16);
     if (!up) {
       sm.xs[hh][i] = xs;
+      sm.ps[hh][i] = ps;
       sm.zs[hh][i] = zs;
     }
     tc_fence_before();
@@ -329,12 +331,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp == 0) {  // dlog_alpha: tokens 2 lane and 2 lane + 1
       const int j = 2 * lane;
       const float x0 = sm.xs[0][j] + sm.xs[1][j], x1 = sm.xs[0][j + 1] + sm.xs[1][j + 1];
+      const float p0 = sm.ps[0][j] + sm.ps[1][j], p1 = sm.ps[0][j + 1] + sm.ps[1][j + 1];
       const float z0 = sm.zs[0][j] + sm.zs[1][j], z1 = sm.zs[0][j + 1] + sm.zs[1][j + 1];
-      float sx = x0 + x1, sz = z0 + z1;
+      float sx = x0 + x1, sp = p0 + p1, sz = z0 + z1;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const float ux = __shfl_down_sync(0xffffffffu, sx, o), uz = __shfl_up_sync(0xffffffffu, sz, o);
-        if (lane + o < 32) sx += ux;
+        const float ux = __shfl_down_sync(0xffffffffu, sx, o), up_ = __shfl_down_sync(0xffffffffu, sp, o);
+        const float uz = __shfl_up_sync(0xffffffffu, sz, o);
+        if (lane + o < 32) {
+          sx += ux;
+          sp += up_;
+        }
         if (lane >= o) sz += uz;
       }
       float gg = 0.f;
@@ -343,15 +350,17 @@ __global__ void __launch_bounds__(kThreads, 2)
       gg *= sm.g.GC;
       const float before = __shfl_up_sync(0xffffffffu, sz, 1);
       const float z_lt = lane == 0 ? 0.f : before;
-      const float after = __shfl_down_sync(0xffffffffu, sx, 1);
-      const float d1 = x1 + (lane == 31 ? 0.f : after);
+      // no pair reaches across the chunk's first token: its sum is zero, not what rounding left
+      const float pair0 = lane == 0 ? 0.f : sp;
+      const float after = __shfl_down_sync(0xffffffffu, sx + sp, 1);
+      const float d0 = sx + pair0, d1 = (x1 + p1) + (lane == 31 ? 0.f : after);
       const size_t row = (size_t)bh * T + t0;
       const bool plain = sm.g.fac != 0.f;  // no reset in the chunk
       const bool r0 = !plain && sm.seg[j] != (j > 0 ? sm.seg[j - 1] : 0);
       const bool r1 = !plain && sm.seg[j + 1] != sm.seg[j];
       if (t0 + j < T)
         p.dlog_alpha[row + j] = __float2bfloat16_rn(
-            r0 ? 0.f : sx + z_lt + gg);
+            r0 ? 0.f : d0 + z_lt + gg);
       if (t0 + j + 1 < T)
         p.dlog_alpha[row + j + 1] = __float2bfloat16_rn(
             r1 ? 0.f : d1 + z_lt + z0 + gg);
