@@ -127,7 +127,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
   const uint32_t tb = sm.tmem_base;
   const uint32_t sK = smem_u32(sm.K), sQ = smem_u32(sm.Q), sTg = smem_u32(sm.Tg[0]);
   const uint32_t sP = own_p ? smem_u32(sm.P) : sQ;
-  const uint32_t sTw = sQ + TILE, sTt = own_p ? sQ : sTg + TILE;
+  uint8_t *const pTw = sm.Q + TILE, *const pTt = own_p ? sm.Q : sm.Tg[1];
+  const uint32_t sTw = smem_u32(pTw), sTt = smem_u32(pTt);
   if (tid == 0) {
     mbar_wait(&sm.full, 0, wc, W_PREP_LOAD);
     const uint32_t id = idesc_bf16(64, 64, false, false);
@@ -323,47 +324,41 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
     *reinterpret_cast<float4*>(sm.X + (32 + r) * LD + c) = make_float4(s[0], s[1], s[2], s[3]);
   }
   __syncthreads();
-  // ---- operands: thread (row r, 16 columns)
-  {
-    const int r = tid >> 2, c0 = 16 * (tid & 3);
-    const size_t at = (((size_t)bh * N + n) * C + r) * C + c0;
-    const float wr = sm.w[r], br = sm.be[r];
+  // ---- operands: a lane takes 4 columns, 8 lanes half a row (float4 loads free of bank
+  //      conflicts, 8-byte stores)
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {  // 8 columns, one 16-byte piece
-      uint32_t hi[4], low[4], gh[4], gl[4], tw[4], tt[4];
+  for (int k = 0; k < 2; ++k) {
+    const int c = 32 * k + 4 * (tid & 7);
+    const float4 G = at4(sm.G + c);
+    const float4 rb = BACK ? at4(sm.rb + c) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int c = c0 + 8 * g + 2 * e;
-        const float2 x = *reinterpret_cast<const float2*>(sm.X + r * LD + c);
-        const float2 G = *reinterpret_cast<const float2*>(sm.G + c);
-        hi[e] = pack_bf16(x.x, x.y);
-        const float ga = -x.x * G.x, gb = -x.y * G.y;
-        gh[e] = pack_bf16(ga, gb);
-        if (SPLIT) {
-          low[e] = pack_lo(x.x, x.y, hi[e]);
-          gl[e] = pack_lo(ga, gb, gh[e]);
-        }
-        if (BACK) {  // T_ij = beta_i T0_ij / beta_j below the diagonal
-          const float2 rb = *reinterpret_cast<const float2*>(sm.rb + c);
-          const float ta = c == r ? 1.f : br * x.x * rb.x, td = c + 1 == r ? 1.f : br * x.y * rb.y;
-          tw[e] = pack_bf16(wr * ta, wr * td);
-          tt[e] = pack_bf16(ta, td);
-        }
-      }
-      const uint32_t off = sw128_off(r, (c0 >> 3) + g);
-      *reinterpret_cast<uint4*>(p.m.T0 + at + 8 * g) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      st_shared_v4(sTg + off, gh[0], gh[1], gh[2], gh[3]);
+    for (int rr = 0; rr < 2; ++rr) {
+      const int r = (tid >> 3) + 32 * rr;
+      const float4 x = at4(sm.X + r * LD + c);
+      const uint32_t off = sw128_off(r, c >> 3) + (c & 4) * 2;
+      const size_t at = (((size_t)bh * N + n) * C + r) * C + c;
+      const uint2 hi = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+      const float4 g = make_float4(-x.x * G.x, -x.y * G.y, -x.z * G.z, -x.w * G.w);
+      const uint2 gh = make_uint2(pack_bf16(g.x, g.y), pack_bf16(g.z, g.w));
+      *reinterpret_cast<uint2*>(p.m.T0 + at) = hi;
+      *reinterpret_cast<uint2*>(sm.Tg[0] + off) = gh;
       if (SPLIT) {
-        *reinterpret_cast<uint4*>(p.m.T0lo + at + 8 * g) = make_uint4(low[0], low[1], low[2], low[3]);
-        st_shared_v4(sTg + TILE + off, gl[0], gl[1], gl[2], gl[3]);
+        *reinterpret_cast<uint2*>(p.m.T0lo + at) =
+            make_uint2(pack_lo(x.x, x.y, hi.x), pack_lo(x.z, x.w, hi.y));
+        *reinterpret_cast<uint2*>(sm.Tg[1] + off) =
+            make_uint2(pack_lo(g.x, g.y, gh.x), pack_lo(g.z, g.w, gh.y));
       }
-      if (BACK) {
-        st_shared_v4(sTw + off, tw[0], tw[1], tw[2], tw[3]);
-        st_shared_v4(sTt + off, tt[0], tt[1], tt[2], tt[3]);
+      if (BACK) {  // T_ij = beta_i T0_ij / beta_j below the diagonal
+        const float wr = sm.w[r], br = sm.be[r];
+        const float4 t = make_float4(c == r ? 1.f : br * x.x * rb.x, c + 1 == r ? 1.f : br * x.y * rb.y,
+                                     c + 2 == r ? 1.f : br * x.z * rb.z, c + 3 == r ? 1.f : br * x.w * rb.w);
+        *reinterpret_cast<uint2*>(pTw + off) =
+            make_uint2(pack_bf16(wr * t.x, wr * t.y), pack_bf16(wr * t.z, wr * t.w));
+        *reinterpret_cast<uint2*>(pTt + off) = make_uint2(pack_bf16(t.x, t.y), pack_bf16(t.z, t.w));
       }
     }
-    fence_proxy_async_smem();
   }
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   uint32_t phase = 1;
