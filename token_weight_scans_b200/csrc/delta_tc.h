@@ -126,8 +126,19 @@ struct GatePair {
 };
 
 #ifdef __CUDACC__
-__device__ __forceinline__ GatePair chunk_gates(const float* beta, const float* log_alpha,
-                                                size_t row, int t0, int T) {
+struct RawGates { float la[2], be[2]; };
+__device__ __forceinline__ RawGates load_gates(const float* beta, const float* log_alpha, size_t row,
+                                               int t0, int T) {
+  RawGates r;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int t = t0 + (threadIdx.x & 31) + 32 * k;
+    r.la[k] = t < T ? log_alpha[row + t] : 0.f;
+    r.be[k] = t < T ? beta[row + t] : 0.f;
+  }
+  return r;
+}
+__device__ __forceinline__ GatePair chunk_gates(const RawGates& raw) {
   const int lane = threadIdx.x & 31;
   GatePair g;
   // The running sum in 64-bit integers of 2^-40: exact, and no matter how strong the decays
@@ -137,9 +148,8 @@ __device__ __forceinline__ GatePair chunk_gates(const float* beta, const float* 
   unsigned m[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const int t = t0 + lane + 32 * k;
-    const float la = t < T ? log_alpha[row + t] : 0.f;
-    g.be[k] = t < T ? beta[row + t] : 0.f;
+    const float la = raw.la[k];
+    g.be[k] = raw.be[k];
     const bool reset = la < kResetLog;
     L[k] = reset ? 0 : __float2ll_rn(la * 0x1p40f);
     m[k] = __ballot_sync(0xffffffffu, reset);

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       if (sl == 0 && warp == 2 && sm.g.fac == 0.f) {
-        const GatePair g = chunk_gates(p.beta, p.log_alpha, (size_t)bh * T, t0, T);
+        const GatePair g = chunk_gates(load_gates(p.beta, p.log_alpha, (size_t)bh * T, t0, T));
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           sm.Lh[lane + 32 * k] = g.Lh[k];

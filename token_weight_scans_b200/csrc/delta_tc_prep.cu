@@ -106,6 +106,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
   const int kh = b * p.d.Hk + h / (p.d.H / p.d.Hk);
   const int t0 = n * C;
   const WaitCtx wc{&sm.abort, p.status, p.timeout_ns};
+  RawGates raw{};
+  if (warp == 2) raw = load_gates(p.beta, p.log_alpha, (size_t)bh * p.d.T, t0, p.d.T);
   if (tid == 0) {
     sm.abort = 0;
     mbar_init(&sm.full, 1);
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
   }
   __syncwarp();
   if (warp == 2) {
-    const GatePair g = chunk_gates(p.beta, p.log_alpha, (size_t)bh * p.d.T, t0, p.d.T);
+    const GatePair g = chunk_gates(raw);
     const float Lm = __shfl_sync(0xffffffffu, g.Lh[0], 31), Ll = __shfl_sync(0xffffffffu, g.Ll[0], 31);
     const bool fac = g.seg_end == 0 && g.Lend > -80.f;
     GateBlock* gb = reinterpret_cast<GateBlock*>(p.m.gates) + (size_t)bh * N + n;
@@ -301,6 +303,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
   {
     const int c = 4 * warp;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
     for (int m = c; m < 32; m += 4) {
       const float4 a = at4(sm.N + (32 + lane) * LD + m);
       axpy4(s, a.x, at4(sm.X + m * LD + c));
@@ -314,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
   {  // -X2 tmp: a warp owns 4 rows, X2 is zero right of its diagonal
     const int r = 4 * warp + (lane >> 3), c = 4 * (lane & 7);
     float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
     for (int m = 0; m < 4 * warp + 4; m += 4) {
       const float4 a = at4(sm.X + (32 + r) * LD + 32 + m);
       axpy4(s, -a.x, at4(sm.N + m * LD + c));
