@@ -557,17 +557,24 @@ def gradlev_delta_ckpt_bytes(B, H, Hk, T, d_k, d_v, dt) -> int:
 def _delta_args(q, k, v, beta, log_alpha, scale):
     """Checks shared by the delta calls. Returns the sizes, the dtype code and the scale."""
     import torch
-    if q.dim() != 4 or v.dim() != 4:
+    qs, vs, dt = q.shape, v.shape, q.dtype
+    if len(qs) != 4 or len(vs) != 4:
         raise GradlevError("q and v must be [B,H,T,d] tensors")
-    B, Hk, T, d_k = q.shape
-    H, d_v = v.shape[1], v.shape[3]
-    dev, dt = _cuda_device(q), q.dtype
+    B, Hk, T, d_k = qs
+    H, d_v = vs[1], vs[3]
+    dev, f32, gate = _cuda_device(q), torch.float32, (B, H, T)
     code = _dt_code(dt)
-    _check_fast("q", q, (B, Hk, T, d_k), dt, dev)
-    _check_fast("k", k, (B, Hk, T, d_k), dt, dev)
-    _check_fast("v", v, (B, H, T, d_v), dt, dev)
-    _check_fast("beta", beta, (B, H, T), torch.float32, dev)
-    _check_fast("log_alpha", log_alpha, (B, H, T), torch.float32, dev)
+    # one expression for the usual case; the loop names what is wrong
+    if not (k.shape == qs and vs == (B, H, T, d_v) and beta.shape == gate and
+            log_alpha.shape == gate and k.dtype == dt and v.dtype == dt and beta.dtype == f32 and
+            log_alpha.dtype == f32 and k.device == dev and v.device == dev and
+            beta.device == dev and log_alpha.device == dev and q.is_contiguous() and
+            k.is_contiguous() and v.is_contiguous() and beta.is_contiguous() and
+            log_alpha.is_contiguous()):
+        for name, t, shape, dtype in (("q", q, qs, dt), ("k", k, qs, dt),
+                                      ("v", v, (B, H, T, d_v), dt), ("beta", beta, gate, f32),
+                                      ("log_alpha", log_alpha, gate, f32)):
+            _check_tensor(name, t, shape, dtype, dev)
     return (B, H, Hk, T, d_k, d_v, code), dev, dt, float(d_k ** -0.5 if scale is None else scale)
 
 
@@ -585,8 +592,9 @@ def gradlev_delta_fwd(q, k, v, beta, log_alpha, S0=None, *, scale=None, y=None, 
     if S0 is not None:
         _check_fast("S0", S0, (B, H, d_v, d_k), f32, dev)
     if y is None:
-        y = torch.empty((B, H, T, d_v), dtype=dt, device=dev)
-    _check_fast("y", y, (B, H, T, d_v), dt, dev)
+        y = torch.empty_like(v)
+    else:
+        _check_tensor("y", y, (B, H, T, d_v), dt, dev)
     if ST is None and want_ST:
         ST = torch.empty((B, H, d_v, d_k), dtype=f32, device=dev)
     if ST is not None:
@@ -655,8 +663,9 @@ def gradlev_delta_step(q, k, v, beta, log_alpha, S, *, slots=None, scale=None, y
     if slots is not None:
         _check_fast("slots", slots, (B,), torch.int32, dev)
     if y is None:
-        y = torch.empty((B, H, T, d_v), dtype=dt, device=dev)
-    _check_fast("y", y, (B, H, T, d_v), dt, dev)
+        y = torch.empty_like(v)
+    else:
+        _check_tensor("y", y, (B, H, T, d_v), dt, dev)
     with _on(dev):
         st = lib().gradlev_delta_step(*size, _addr(q), _addr(k), _addr(v), _addr(beta),
                                       _addr(log_alpha), scale, _addr(slots), S.shape[0], _addr(S),
@@ -724,11 +733,13 @@ def gradlev_qk_norm_rope_fwd(q, k, wq=None, wk=None, pos=None, inv_freq=None, *,
     a, dev, dt, sq, sk = _norm_args(q, k, wq, wk, pos, inv_freq, norm)
     B, T, Hq, Hk, d = a[:5]
     if yq is None:
-        yq = torch.empty((B, Hq, T, d), dtype=dt, device=dev)
+        yq = q.new_empty((B, Hq, T, d))
+    else:
+        _check_tensor("yq", yq, (B, Hq, T, d), dt, dev)
     if yk is None:
-        yk = torch.empty((B, Hk, T, d), dtype=dt, device=dev)
-    _check_fast("yq", yq, (B, Hq, T, d), dt, dev)
-    _check_fast("yk", yk, (B, Hk, T, d), dt, dev)
+        yk = q.new_empty((B, Hk, T, d))
+    else:
+        _check_tensor("yk", yk, (B, Hk, T, d), dt, dev)
     with _on(dev):
         st = lib().gradlev_qk_norm_rope_fwd(*a, float(eps), _addr(q), sq, _addr(k), sk, _addr(wq),
                                             _addr(wk), _addr(pos), _addr(inv_freq), _addr(yq),
