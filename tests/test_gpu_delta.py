@@ -85,6 +85,13 @@ CASES = [
     (2, 2, 2, 130, 128, 128, "bf16", True, "empty"),
     (1, 2, 2, 130, 128, 128, "bf16", True, "reset"),
     (1, 2, 2, 1100, 128, 128, "bf16", True, "none"),
+    # heads narrower than the tensor-core tiles
+    (2, 2, 1, 150, 64, 64, "bf16", True, "docs"),
+    (1, 3, 3, 257, 8, 8, "bf16", True, "none"),
+    (2, 2, 2, 130, 72, 200, "bf16", True, "none"),
+    (1, 2, 1, 1000, 120, 136, "bf16", True, "docs"),
+    (1, 2, 1, 257, 128, 40, "bf16", False, "none"),
+    (2, 2, 1, 100, 136, 64, "bf16", True, "none"),
     # few long scans, walked in segments
     (1, 2, 1, 1283, 128, 256, "bf16", True, "none"),
     (1, 2, 1, 1283, 128, 256, "bf16", False, "docs"),
@@ -193,7 +200,8 @@ def test_step_slots():
     assert torch.equal(S[[1, 2, 4]].cpu(), first[[1, 2, 4]])
 
 
-@pytest.mark.parametrize("dtype,dk,dv", [("f32", 24, 40), ("bf16", 128, 128), ("bf16", 128, 256)])
+@pytest.mark.parametrize("dtype,dk,dv", [("f32", 24, 40), ("bf16", 128, 128), ("bf16", 128, 256),
+                                         ("bf16", 40, 72), ("bf16", 72, 136)])
 def test_outputs_stay_inside_their_buffers(dtype, dk, dv):
     B, H, Hk, T = 1, 2, 2, 70
     d = dev(ref.draw(B, H, Hk, T, dk, dv, dtype, True, seed=6))

@@ -1,5 +1,5 @@
-// The gated delta rule on the tensor cores (tcgen05 / TMEM): bf16 I/O, d_k = 128,
-// d_v in {128, 256}, chunks of 64 tokens. Formulas in delta.h.
+// The gated delta rule on the tensor cores (tcgen05 / TMEM): bf16 I/O, d_k up to 128, d_v up
+// to 256 (multiples of 8), chunks of 64 tokens. Formulas in delta.h.
 //
 // Three kernels:
 //   prep  (delta_tc_prep.cu): per chunk, what does not depend on the state;
@@ -35,7 +35,12 @@ constexpr uint32_t LANE16 = 16u << 16;  // an M = 64 product in the upper 16 lan
 
 __host__ __device__ inline int chunks(int T) { return (T + C - 1) / C; }
 
-inline bool shape_ok(const Dims& d) { return d.bf16 && d.dk == 128 && (d.dv == 128 || d.dv == 256); }
+inline bool shape_ok(const Dims& d) { return d.bf16 && d.dk <= 128 && d.dv <= 256; }
+
+// The kernels work on 128 columns of d_k and whole slices of 128 rows of d_v. Narrower heads
+// are padded with zeros by the TMA loads' bounds and cut off by those of the stores; only the
+// buffers between the kernels hold the padded sizes.
+__host__ __device__ inline int dvp(const Dims& d) { return d.dv <= 128 ? 128 : 256; }
 
 using bf16 = __nv_bfloat16;
 
@@ -63,8 +68,8 @@ struct GateBlock {
   float ra[C], cb[C]; // cb = ca beta
 };
 
-// What the forward keeps for the backward: chunk-start states S [B*H][N][dv][128], D^T
-// [B*H][N][dv][64] (the tokens of a chunk contiguous, as the walk has them), Wb, PT and gates.
+// What the forward keeps for the backward: chunk-start states S [B*H][N][dvp][128], D^T
+// [B*H][N][dvp][64] (the tokens of a chunk contiguous, as the walk has them), Wb, PT and gates.
 struct Saved {
   bf16 *S = nullptr, *D = nullptr, *Wb = nullptr, *PT = nullptr;
   float *gates = nullptr, *M = nullptr;  // M: the segments' maps, with segments
@@ -97,7 +102,7 @@ struct Args {
   const void* dy = nullptr;
   const void* dST = nullptr;
   bf16* E = nullptr;        // E^T, like D^T
-  bf16* dS = nullptr;       // [B*H][N][dv][128]: gradient of the chunk-end states
+  bf16* dS = nullptr;       // [B*H][N][dvp][128]: gradient of the chunk-end states
   void *dq = nullptr, *dk_ = nullptr, *dv_ = nullptr, *dbeta = nullptr, *dlog_alpha = nullptr;
   void* dS0 = nullptr;
   SegPlan seg{1, 1 << 30};

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       tma_load_3d(sm.K + kb * TILE, &tmK, &sm.kq, 64 * kb, t0, kh);
     }
   }
-  const int nsl = p.d.dv / 64;
+  const int nsl = (p.d.dv + 63) / 64;
   if (warp == 1) {
     tmem_alloc(&sm.tmem_base, kCols);
     tmem_relinquish();
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_before();
   __syncthreads();
   if (tid == 0) {
-    for (int kb = 0; kb < 2; ++kb) {
+    for (int kb = 0; kb < (p.d.dk > 64 ? 2 : 1); ++kb) {
       tma_store_3d(&tmdq, sm.Q + kb * TILE, 64 * kb, t0, kh);
       tma_store_3d(&tmdk, sm.K + kb * TILE, 64 * kb, t0, kh);
     }
@@ -396,14 +396,14 @@ cudaError_t launch_grad(const Args& a, cudaStream_t st) {
   const Dims& d = a.d;
   const uint64_t N = chunks(d.T), kh = (uint64_t)d.B * d.Hk, bh = d.BH();
   CUtensorMap mq, mk, mo, md, me, ms, mds, mdq, mdk;
-  if (!make_map_bf16_3d(&mq, a.q, 128, d.T, kh, C) || !make_map_bf16_3d(&mk, a.k, 128, d.T, kh, C) ||
+  if (!make_map_bf16_3d(&mq, a.q, d.dk, d.T, kh, C) || !make_map_bf16_3d(&mk, a.k, d.dk, d.T, kh, C) ||
       !make_map_bf16_3d(&mo, a.dy, d.dv, d.T, bh, C) ||
-      !make_map_bf16_3d(&md, a.sv.D, C, d.dv, bh * N, 64) ||
-      !make_map_bf16_3d(&me, a.E, C, d.dv, bh * N, 64) ||
-      !make_map_bf16_3d(&ms, a.sv.S, 128, d.dv, bh * N, 64) ||
-      !make_map_bf16_3d(&mds, a.dS, 128, d.dv, bh * N, 64) ||
-      !make_map_bf16_3d(&mdq, a.dq, 128, d.T, kh, C) ||
-      !make_map_bf16_3d(&mdk, a.dk_, 128, d.T, kh, C))
+      !make_map_bf16_3d(&md, a.sv.D, C, dvp(d), bh * N, 64) ||
+      !make_map_bf16_3d(&me, a.E, C, dvp(d), bh * N, 64) ||
+      !make_map_bf16_3d(&ms, a.sv.S, 128, dvp(d), bh * N, 64) ||
+      !make_map_bf16_3d(&mds, a.dS, 128, dvp(d), bh * N, 64) ||
+      !make_map_bf16_3d(&mdq, a.dq, d.dk, d.T, kh, C) ||
+      !make_map_bf16_3d(&mdk, a.dk_, d.dk, d.T, kh, C))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> set{0};
   int dev = 0;

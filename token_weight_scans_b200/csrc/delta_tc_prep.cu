@@ -477,7 +477,7 @@ cudaError_t launch_prep(const Args& a, bool split, cudaStream_t st) {
   const bool back = a.m.Wb != nullptr;
   CUtensorMap m[5];
   using gradlev::tc::make_map_bf16_3d;
-  if (!make_map_bf16_3d(&m[0], a.k, 128, d.T, kh, C) || !make_map_bf16_3d(&m[1], a.q, 128, d.T, kh, C) ||
+  if (!make_map_bf16_3d(&m[0], a.k, d.dk, d.T, kh, C) || !make_map_bf16_3d(&m[1], a.q, d.dk, d.T, kh, C) ||
       !make_map_bf16_3d(&m[2], a.m.W, 128, N * C, bh, C) ||
       !make_map_bf16_3d(&m[3], split ? a.m.Wlo : a.m.W, 128, N * C, bh, C) ||
       !make_map_bf16_3d(&m[4], back ? a.m.Wb : a.m.W, 128, N * C, bh, C))

@@ -30,7 +30,7 @@ constexpr int kThreads = 256;
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 size_t state_bytes(const Dims& d, int nseg) {
-  return up256(d.BH() * nseg * d.dv * 128 * sizeof(float));
+  return up256(d.BH() * nseg * dvp(d) * 128 * sizeof(float));
 }
 
 constexpr int kLd = 132;         // row stride of M in shared memory: 16-byte rows, no bank conflicts
@@ -47,12 +47,12 @@ __device__ __forceinline__ void copy16(void* dst, const void* src) {
 // c, kRows / 2 rows. BWD: from the last segment. The next segment's M lands while this one's is
 // used: read straight from memory a step took 12 us.
 template <bool BWD, int kRows>
-__global__ void __launch_bounds__(kThreads) combine_kernel(int dv, int nseg, const float* L,
+__global__ void __launch_bounds__(kThreads) combine_kernel(Dims d, int nseg, const float* L,
                                                            const float* M, const float* S0,
                                                            const bf16* dST, float* out) {
   extern __shared__ __align__(16) float sm[];
   float* S = sm + 2 * 128 * kLd;  // [kRows][kLd]
-  const int nb = dv / kRows, bh = blockIdx.x / nb, r0 = (blockIdx.x - bh * nb) * kRows;
+  const int dv = dvp(d), nb = dv / kRows, bh = blockIdx.x / nb, r0 = (blockIdx.x - bh * nb) * kRows;
   const int c = threadIdx.x & 127, h = (threadIdx.x >> 7) * (kRows / 2);
   auto seg_at = [&](int i) { return (size_t)bh * nseg + (BWD ? nseg - 1 - i : i); };
   auto fetch = [&](int i) {
@@ -67,8 +67,10 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(int dv, int nseg, con
   float s[kRows / 2];
 #pragma unroll
   for (int e = 0; e < kRows / 2; ++e) {
-    const size_t at = ((size_t)bh * dv + r0 + h + e) * 128 + c;
-    s[e] = BWD ? (dST ? __bfloat162float(dST[at]) : 0.f) : (S0 ? S0[at] : 0.f);
+    const int r = r0 + h + e;  // the caller's states have no padding
+    const bool ok = r < d.dv && c < d.dk;
+    const size_t at = ((size_t)bh * d.dv + r) * d.dk + c;
+    s[e] = !ok ? 0.f : BWD ? (dST ? __bfloat162float(dST[at]) : 0.f) : (S0 ? S0[at] : 0.f);
   }
   fetch(0);
   for (int i = 0; i < nseg; ++i) {
@@ -116,9 +118,9 @@ cudaError_t combine(const Args& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     set.fetch_or(bit);
   }
-  combine_kernel<BWD, kRows><<<(unsigned)(a.d.BH() * (a.d.dv / kRows)), kThreads,
+  combine_kernel<BWD, kRows><<<(unsigned)(a.d.BH() * (dvp(a.d) / kRows)), kThreads,
                                combine_smem<kRows>(), st>>>(
-      a.d.dv, a.seg.nseg, a.loc, a.M, a.S0, static_cast<const bf16*>(a.dST), a.init);
+      a.d, a.seg.nseg, a.loc, a.M, a.S0, static_cast<const bf16*>(a.dST), a.init);
   count_launch();
   return cudaGetLastError();
 }
@@ -128,7 +130,7 @@ cudaError_t combine(const Args& a, cudaStream_t st) {
 // The most segments whose CTAs still run at once, both in the first walk (the slices and the
 // identity, all segments but one) and in the walk proper (and the last segment's identity).
 SegPlan seg_plan(const Dims& d) {
-  const long long BH = (long long)d.B * d.H, ns = d.dv / 128;
+  const long long BH = (long long)d.B * d.H, ns = dvp(d) / 128;
   const int N = chunks(d.T);
   for (int s = kMaxSeg; s >= 3; --s) {
     const int per = (N + s - 1) / s, nseg = (N + per - 1) / per;
@@ -156,7 +158,7 @@ void set_segments(Args& a, char* at, float* M) {
 cudaError_t launch_combine(const Args& a, bool backward, cudaStream_t st) {
   // One CTA per SM (two M tiles): 16 rows each (5 us a step) while those run at once, 32 (7 us)
   // beyond.
-  if (a.d.BH() * (a.d.dv / 16) <= kSMs)
+  if (a.d.BH() * (dvp(a.d) / 16) <= kSMs)
     return backward ? combine<true, 16>(a, st) : combine<false, 16>(a, st);
   return backward ? combine<true, 32>(a, st) : combine<false, 32>(a, st);
 }
@@ -191,14 +193,14 @@ static bf16* take(char*& at, size_t elems) {
 static size_t gate_bytes(const Dims& d) {
   return up256(d.BH() * chunks(d.T) * sizeof(GateBlock));
 }
-size_t token_rows_bytes(const Dims& d) { return up256(d.BH() * chunks(d.T) * d.dv * C * sizeof(bf16)); }
+size_t token_rows_bytes(const Dims& d) { return up256(d.BH() * chunks(d.T) * dvp(d) * C * sizeof(bf16)); }
 
 Saved saved_at(char* base, const Dims& d) {
   const size_t rows = d.BH() * chunks(d.T);
   char* at = base;
   Saved s;
-  s.S = take(at, rows * d.dv * 128);
-  s.D = take(at, rows * d.dv * C);
+  s.S = take(at, rows * dvp(d) * 128);
+  s.D = take(at, rows * dvp(d) * C);
   s.Wb = take(at, rows * C * 128);
   s.PT = take(at, rows * C * C);
   s.gates = reinterpret_cast<float*>(at);
@@ -209,7 +211,7 @@ Saved saved_at(char* base, const Dims& d) {
 size_t saved_bytes(const Dims& d) {
   const size_t rows = d.BH() * chunks(d.T);
   const int nseg = seg_plan(d).nseg;
-  return up256(rows * d.dv * 256) + token_rows_bytes(d) + up256(rows * C * 256) +
+  return up256(rows * dvp(d) * 256) + token_rows_bytes(d) + up256(rows * C * 256) +
          up256(rows * C * C * 2) + gate_bytes(d) +
          (nseg > 1 ? d.BH() * nseg * 128 * 128 * sizeof(float) : 0);
 }
@@ -234,7 +236,7 @@ size_t fwd_scratch_bytes(const Dims& d) {  // the segments' buffers come last
 }
 
 size_t bwd_scratch_bytes(const Dims& d) {  // E, dS, the segments' buffers
-  return token_rows_bytes(d) + up256(d.BH() * chunks(d.T) * d.dv * 256) + seg_bytes(d, false);
+  return token_rows_bytes(d) + up256(d.BH() * chunks(d.T) * dvp(d) * 256) + seg_bytes(d, false);
 }
 
 }  // namespace tc

@@ -127,8 +127,8 @@ struct WalkParams {
   // segment.
   int nseg, seg_chunks, seg0, segs, nsl;
   int sum;               // states alone: nothing is left for other kernels but loc and M
-  const float* init;     // [B*H][nseg][dv][128] states the segments start from, or null
-  float *loc, *M;        // [B*H][nseg][dv][128], [B*H][nseg][128][128]
+  const float* init;     // [B*H][nseg][dvp][128] states the segments start from, or null
+  float *loc, *M;        // [B*H][nseg][dvp][128], [B*H][nseg][128][128]
 };
 
 __device__ __forceinline__ void st_tmem32(uint32_t col, const uint32_t (&r)[32]) {
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int in_seg = extra ? blockIdx.x - per_seg * p.segs : blockIdx.x % per_seg;
   const int seg = extra ? p.nseg - 1 : p.seg0 + blockIdx.x / per_seg;
   const int bh = extra ? in_seg : in_seg / p.nsl, slice = extra ? 0 : in_seg - bh * p.nsl;
-  const bool ident = extra || slice == p.d.dv >> 7;  // carries the identity: the segment's map
+  const bool ident = extra || slice == dvp(p.d) >> 7;  // carries the identity: the segment's map
   const int n0 = ident ? 0 : slice * 128;
   const bool carry = p.sum || ident;                 // the end state is all that is wanted
   const bool outputs = !BWD && !carry;               // the forward's products for Y
@@ -456,7 +456,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3, hh = (warp - 4) >> 2;
     const uint32_t lo = (uint32_t)(32 * q) << 16;
     const int r = 32 * q + lane;           // row of the slice
-    const size_t row = (size_t)bh * p.d.dv + n0 + r;
+    // rows and columns of the caller's states (S0, ST, dST, dS0 have no padding)
+    const bool rok = n0 + r < p.d.dv;
+    const size_t row = ((size_t)bh * p.d.dv + n0 + r) * p.d.dk;
+    auto cok = [&](int col) { return rok && col < p.d.dk; };
+    const int rows = dvp(p.d);
     // start state
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
@@ -464,13 +468,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int col = 64 * hh + 32 * hf;
 #pragma unroll
       for (int e = 0; e < 32; ++e) v[e] = ident && col + e == r ? 1.f : 0.f;
-      const float* from = p.init ? p.init + (sg * p.d.dv + n0 + r) * 128
-                                 : (!BWD && p.S0 ? p.S0 + row * 128 : nullptr);
+      const float* from = p.init ? p.init + (sg * rows + n0 + r) * 128 : !BWD && p.S0 ? p.S0 + row : nullptr;
       if (!carry && from) {
-        const float4* s = reinterpret_cast<const float4*>(from + col);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float4 u = s[e];
+          if (!p.init && !cok(col + 4 * e)) continue;
+          const float4 u = *reinterpret_cast<const float4*>(from + col + 4 * e);
           v[4 * e] = u.x;
           v[4 * e + 1] = u.y;
           v[4 * e + 2] = u.z;
@@ -478,10 +481,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (BWD && !carry && !p.init && p.dST) {
-        const uint4* s = reinterpret_cast<const uint4*>(p.dST + row * 128 + col);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint4 u = s[e];
+          if (!cok(col + 8 * e)) continue;
+          const uint4 u = *reinterpret_cast<const uint4*>(p.dST + row + col + 8 * e);
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
@@ -490,6 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      __syncwarp();
       tmem_st32(tb + COL_S + lo + col, v);
     }
     tmem_st_wait();
@@ -544,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           uint4* out = reinterpret_cast<uint4*>(
-              p.states + (((size_t)bh * N + n) * p.d.dv + n0 + r) * 128 + 64 * hh);
+              p.states + (((size_t)bh * N + n) * rows + n0 + r) * 128 + 64 * hh);
 #pragma unroll
           for (int cc = 0; cc < 8; ++cc)
             out[cc] = make_uint4(pk[4 * cc], pk[4 * cc + 1], pk[4 * cc + 2], pk[4 * cc + 3]);
@@ -602,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           uint4* out = reinterpret_cast<uint4*>(
-              p.D + (((size_t)bh * N + n) * p.d.dv + n0 + r) * C + 32 * hh);
+              p.D + (((size_t)bh * N + n) * rows + n0 + r) * C + 32 * hh);
 #pragma unroll
           for (int cc = 0; cc < 4; ++cc)
             out[cc] = make_uint4(db[4 * cc], db[4 * cc + 1], db[4 * cc + 2], db[4 * cc + 3]);
@@ -612,11 +616,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&sm.gempty[g]);
     }
     if (lane == 0 && L::staged) tma_store_wait_all();
-    float* end = ident ? p.M + (sg * 128 + r) * 128
-                       : carry ? p.loc + (sg * p.d.dv + n0 + r) * 128
-                               : !BWD && p.ST && seg == p.nseg - 1 ? p.ST + row * 128 : nullptr;
-    bf16* end16 = BWD && !carry && p.dS0 && seg == 0 ? p.dS0 + row * 128 : nullptr;
-    if (ok && (end || end16) && mbar_wait_warp(&sm.sfull, (NC - 1) & 1, wc, W_C_SFULL)) {
+    float* inner = ident ? p.M + (sg * 128 + r) * 128 : carry ? p.loc + (sg * rows + n0 + r) * 128 : nullptr;
+    float* end = !BWD && !carry && seg == p.nseg - 1 ? p.ST : nullptr;
+    bf16* end16 = BWD && !carry && seg == 0 ? p.dS0 : nullptr;
+    if (ok && (inner || end || end16) && mbar_wait_warp(&sm.sfull, (NC - 1) & 1, wc, W_C_SFULL)) {
       tc_fence_after();
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
@@ -624,17 +627,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int col = 64 * hh + 32 * hf;
         tmem_ld32(tb + COL_S + lo + col, v);
         tmem_ld_wait();
-        if (end) {
-          float4* o = reinterpret_cast<float4*>(end + col);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-        } else {
-          uint4* o = reinterpret_cast<uint4*>(end16 + col);
+        if (end16) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            o[e] = make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
-                              pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7]));
+            if (cok(col + 8 * e))
+              *reinterpret_cast<uint4*>(end16 + row + col + 8 * e) =
+                  make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
+                             pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7]));
+        } else {
+          float* o = inner ? inner + col : end + row + col;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (inner || cok(col + 4 * e))
+              *reinterpret_cast<float4*>(o + 4 * e) =
+                  make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
+        __syncwarp();
       }
     }
   } else if (warp >= 12) {
@@ -685,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_bar_sync(1, 128);
       if (t == 0) {
         tma_store_3d(map, stage, n0, t0, bh);
-        tma_store_3d(map, stage + TILE, n0 + 64, t0, bh);
+        if (n0 + 64 < p.d.dv) tma_store_3d(map, stage + TILE, n0 + 64, t0, bh);
         tma_store_commit();
       }
     };
@@ -731,17 +739,17 @@ static cudaError_t launch(const Args& a, bool sum, cudaStream_t st) {
   bf16* dd = BWD ? a.E : a.sv.D;           // D or E
   void* yy = BWD ? a.dv_ : a.y;
   CUtensorMap mq, mk, mv, mw, mwl, mt, mtl, mp, ms, my, md;
-  if (!make_map_bf16_3d(&mq, a.q, 128, d.T, kh, C) || !make_map_bf16_3d(&mk, a.k, 128, d.T, kh, C) ||
+  if (!make_map_bf16_3d(&mq, a.q, d.dk, d.T, kh, C) || !make_map_bf16_3d(&mk, a.k, d.dk, d.T, kh, C) ||
       !make_map_bf16_3d(&mv, v, d.dv, d.T, bh, C) || !make_map_bf16_3d(&mw, w, 128, N * C, bh, C) ||
       !make_map_bf16_3d(&mwl, SPLIT ? a.m.Wlo : w, 128, N * C, bh, C) ||
       !make_map_bf16_3d(&mt, t, C, N * C, bh, C) ||
       !make_map_bf16_3d(&mtl, SPLIT ? a.m.T0lo : t, C, N * C, bh, C) ||
       !make_map_bf16_3d(&mp, BWD ? t : a.m.Pb, C, N * C, bh, C) ||
-      !make_map_bf16_3d(&ms, states ? (const void*)states : w, 128, states ? d.dv : N * C,
+      !make_map_bf16_3d(&ms, states ? (const void*)states : w, 128, states ? dvp(d) : N * C,
                         states ? bh * N : bh, 32) ||
       !make_map_bf16_3d(&my, yy ? yy : v, d.dv, d.T, bh, C) ||
       !gradlev::tc::make_map_bf16_3d_box(&md, dd ? (const void*)dd : w, dd ? C : 128,
-                                         dd ? d.dv : N * C, dd ? bh * N : bh, 32, 32))
+                                         dd ? dvp(d) : N * C, dd ? bh * N : bh, 32, 32))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> set{0};
   int dev = 0;
@@ -753,7 +761,7 @@ static cudaError_t launch(const Args& a, bool sum, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     set.fetch_or(bit);
   }
-  const int ns = d.dv / 128, nseg = a.seg.nseg;
+  const int ns = dvp(d) / 128, nseg = a.seg.nseg;
   WalkParams p{d, BWD ? a.sv.gates : a.m.gates, a.status, a.timeout_ns, a.S0,
                static_cast<const bf16*>(a.dST), a.ST, static_cast<bf16*>(a.dS0),
                static_cast<bf16*>(a.y), dd, states, nseg, a.seg.chunks, 0, nseg, ns, sum,
