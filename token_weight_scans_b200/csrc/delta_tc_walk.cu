@@ -75,7 +75,7 @@ struct Bars {
   uint64_t full[3][NS], empty[3][NS];   // per group of tiles
   uint64_t scaled[NS];
   uint64_t gfull[GS], gempty[GS];
-  uint64_t sready, dfull, uready, sfull, done;
+  uint64_t sready, sscaled, dfull, uready, sfull, done;
   uint64_t yfull[2], yfree[2];          // per accumulator pair
   uint32_t tmem_base;
   int abort;
@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.gempty[g], 12);  // the chain's 8 warps, 4 that scale Q
     }
     mbar_init(&sm.sready, 8);
+    mbar_init(&sm.sscaled, 8);
     mbar_init(&sm.dfull, 1);
     mbar_init(&sm.uready, 8);
     mbar_init(&sm.sfull, 1);
@@ -389,8 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit(&sm.dfull);
         if (BWD) {
           umma_commit(&sm.yfull[yb]);
+          if (!mbar_wait(&sm.sscaled, c & 1, wc, W_SREADY)) break;
+          tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // S += dY^T (scale G Q): S is scaled (sready)
+          for (int kk = 0; kk < 4; ++kk)  // S += dY^T (scale G Q)
             umma_bf16(tb + COL_S, desc_at(sw128_desc(sv + L::v, TILE, 1024), kk * 2048),
                       desc_at(sw128_desc(st + L::q, L::wq, 1024), kk * 2048), id_o, 1);
           umma_commit(&sm.empty[VT][s]);
@@ -508,28 +511,60 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const float GC = gs.GC;
       uint32_t pk[32];
+      const uint32_t at = tb + COL_S + lo + 64 * hh;
+      if constexpr (SPLIT) {  // 32 columns at a time: registers
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        float v[32];
-        const uint32_t at = tb + COL_S + lo + 64 * hh + 32 * hf;
-        tmem_ld32(at, v);
+        for (int hf = 0; hf < 2; ++hf) {
+          float v[32];
+          tmem_ld32(at + 32 * hf, v);
+          tmem_ld_wait();
+          uint32_t rest[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            pk[16 * hf + e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+            rest[e] = pack_rest(v[2 * e], v[2 * e + 1], pk[16 * hf + e]);
+          }
+          st_tmem16(tb + COL_SL + lo + 32 * hh + 16 * hf, rest);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] *= GC;
+          tmem_st32(at + 32 * hf, v);
+        }
+        st_tmem32(tb + COL_SH + lo + 32 * hh, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.sready);
+      } else {
+        // the bf16 copy first; the decayed state is only needed by the update (backward: by
+        // dY^T Q)
+        float v0[32], v1[32];
+        tmem_ld32(at, v0);
+        tmem_ld32(at + 32, v1);
         tmem_ld_wait();
-        uint32_t rest[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          pk[16 * hf + e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-          if (SPLIT) rest[e] = pack_rest(v[2 * e], v[2 * e + 1], pk[16 * hf + e]);
+          pk[e] = pack_bf16(v0[2 * e], v0[2 * e + 1]);
+          pk[16 + e] = pack_bf16(v1[2 * e], v1[2 * e + 1]);
         }
-        if (SPLIT) st_tmem16(tb + COL_SL + lo + 32 * hh + 16 * hf, rest);
+        st_tmem32(tb + COL_SH + lo + 32 * hh, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.sready);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] *= GC;
-        tmem_st32(at, v);
+        for (int e = 0; e < 32; ++e) {
+          v0[e] *= GC;
+          v1[e] *= GC;
+        }
+        tmem_st32(at, v0);
+        tmem_st32(at + 32, v1);
+        if (BWD) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.sscaled);
+        }
       }
-      st_tmem32(tb + COL_SH + lo + 32 * hh, pk);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.sready);
       if (p.states && !carry) {
         if (L::staged) {
           if (lane == 0) tma_store_wait_read_n<0>();  // the store of the chunk before
