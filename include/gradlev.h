@@ -513,6 +513,8 @@ GRADLEV_API int gradlev_last_launch_count(void);
  *   2  the reverse scan's main kernel
  *   3  the forward's segment-summary pass (few long scans, cut into segments)
  *   4  the reverse scan's segment-summary pass
+ *   5  the gated delta rule's forward walk (gradlev_delta_fwd; needs two chunks of 64)
+ *   6  its backward walk (gradlev_delta_bwd)
  *   0  off
  * Host-global, one-shot, not thread-safe; for tests only. */
 GRADLEV_API void gradlev_debug_inject_timeout(int site, int timeout_ms);

@@ -332,6 +332,50 @@ def test_the_layer_end_to_end():
     assert ref.rel2(S, ST.cpu()) <= 2 * F32_TOL
 
 
+@pytest.mark.parametrize("site,want_ST", [(5, False), (5, True), (6, False)])
+def test_a_wait_that_runs_out_is_reported_and_leaves_the_device_usable(site, want_ST):
+    B, H, T, d = 1, 2, 300, 128
+    g = dev(ref.draw(B, H, H, T, d, d, "bf16", True, seed=5))
+    args = [g[n] for n in NAMES]
+    size = (B, H, H, T, d, d, tw.BF16)
+    ws = [torch.empty(tw.gradlev_delta_workspace_bytes(*size, b), dtype=torch.uint8, device="cuda")
+          for b in (0, 1)]
+    ck = torch.empty(tw.gradlev_delta_ckpt_bytes(*size), dtype=torch.uint8, device="cuda")
+
+    def run():
+        y, ST = tw.gradlev_delta_fwd(*args, g["S0"], want_ST=want_ST, ckpt=ck, workspace=ws[0])
+        out = tw.gradlev_delta_bwd(*args, g["dy"], ckpt=ck, workspace=ws[1])
+        return dict(out, y=y, ST=ST), [tw.gradlev_device_status(w) for w in ws]
+
+    good, status = run()
+    assert status == [0, 0]
+    tw.lib().gradlev_debug_inject_timeout(site, 20)
+    _, status = run()
+    assert status[site - 5] == 5  # GRADLEV_ERR_TIMEOUT
+    again, status = run()
+    assert status == [0, 0]
+    for n in good:
+        assert good[n] is None or torch.equal(good[n], again[n]), n
+
+
+def test_calls_on_a_stream_of_their_own():
+    """stream=: the work goes to that stream, with buffers the call allocates itself."""
+    d = dev(ref.draw(1, 4, 2, 200, 128, 128, "bf16", True, seed=6))
+    args = [d[n] for n in NAMES]
+    y0, S0 = tw.gradlev_delta_fwd(*args, d["S0"])
+    g0 = tw.gradlev_delta_bwd(*args, d["dy"], d["S0"])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        y, S = tw.gradlev_delta_fwd(*args, d["S0"], stream=side)
+        g = tw.gradlev_delta_bwd(*args, d["dy"], d["S0"], stream=side)
+        torch.empty(1 << 22, device="cuda").fill_(1.0)  # would reuse what the calls let go
+    side.synchronize()
+    assert torch.equal(y, y0) and torch.equal(S, S0)
+    for n in g0:
+        assert torch.equal(g[n], g0[n]), n
+
+
 def test_binding_refusals():
     d = dev(ref.draw(1, 2, 1, 8, 16, 16, S0=True))
     args = [d[n] for n in NAMES]

@@ -537,6 +537,15 @@ def _stream_of(stream, dev):
     return stream.cuda_stream
 
 
+def _lend(stream, *tensors):
+    """Tensors that a call allocated on the current stream and works on in another: their memory
+    must not be handed out again before that stream is done with it."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _check_fast(name, t, shape, dtype, device):
     if (t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous()):
         _check_tensor(name, t, shape, dtype, device)
@@ -607,6 +616,7 @@ def gradlev_delta_fwd(q, k, v, beta, log_alpha, S0=None, *, scale=None, y=None, 
                                      _addr(log_alpha), scale, _addr(S0), _addr(y), _addr(ST),
                                      _addr(ckpt), _addr(ws), ws.numel() * ws.element_size(),
                                      _stream_of(stream, dev))
+    _lend(stream, y, ST, ws)
     _check(st, "gradlev_delta_fwd")
     return y, ST
 
@@ -644,6 +654,7 @@ def gradlev_delta_bwd(q, k, v, beta, log_alpha, dy, S0=None, dST=None, *, scale=
             _addr(dy), _addr(dST), _addr(out["dq"]), _addr(out["dk"]), _addr(out["dv"]),
             _addr(out["dbeta"]), _addr(out["dlog_alpha"]), _addr(out.get("dS0")), _addr(ckpt),
             _addr(ws), ws.numel() * ws.element_size(), _stream_of(stream, dev))
+    _lend(stream, ws, *out.values())
     _check(st, "gradlev_delta_bwd")
     return out
 
@@ -670,6 +681,7 @@ def gradlev_delta_step(q, k, v, beta, log_alpha, S, *, slots=None, scale=None, y
         st = lib().gradlev_delta_step(*size, _addr(q), _addr(k), _addr(v), _addr(beta),
                                       _addr(log_alpha), scale, _addr(slots), S.shape[0], _addr(S),
                                       _addr(y), _stream_of(stream, dev))
+    _lend(stream, y)
     _check(st, "gradlev_delta_step")
     return y
 
@@ -744,6 +756,7 @@ def gradlev_qk_norm_rope_fwd(q, k, wq=None, wk=None, pos=None, inv_freq=None, *,
         st = lib().gradlev_qk_norm_rope_fwd(*a, float(eps), _addr(q), sq, _addr(k), sk, _addr(wq),
                                             _addr(wk), _addr(pos), _addr(inv_freq), _addr(yq),
                                             _addr(yk), _stream_of(stream, dev))
+    _lend(stream, yq, yk)
     _check(st, "gradlev_qk_norm_rope_fwd")
     return yq, yk
 
@@ -779,6 +792,7 @@ def gradlev_qk_norm_rope_bwd(dyq, dyk, q, k, wq=None, wk=None, pos=None, inv_fre
             _addr(out["dwq"] if wq is not None else None),
             _addr(out["dwk"] if wk is not None else None), _addr(ws),
             ws.numel() * ws.element_size() if ws is not None else 0, _stream_of(stream, dev))
+    _lend(stream, ws, *out.values())
     _check(st, "gradlev_qk_norm_rope_bwd")
     return out
 

@@ -29,8 +29,6 @@ Dims dims(int B, int H, int Hk, int T, int dk, int dv, gradlev_dtype dt) {
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-constexpr uint64_t kWaitTimeoutNs = 2000000000ull;  // bound of device-side waits
-
 // A gate's gradient is one dot product of two bf16-rounded rows: 4e-3 off over many gates (in
 // the 2-norm), but any single one that happens to be small may be much further off. Calls whose
 // gradients have at most kFewGates of them take the float32 kernels (90 us in place of 41 us
@@ -84,6 +82,7 @@ cudaError_t fwd_run(const Dims& d, const void* q, const void* k, const void* v, 
     a.S0 = S0;
     a.y = y;
     a.ST = ST;
+    a.inject = take_inject(INJ_DELTA_FWD, 1, &a.timeout_ns);
     tc::set_segments(a, ws + kStatusBytes + tc::fwd_scratch_bytes(d) - tc::seg_bytes(d, true), a.sv.M);
     return tc::run_fwd(a, st);
   }
@@ -189,6 +188,7 @@ gradlev_status gradlev_delta_bwd(int B, int H, int Hk, int T, int d_k, int d_v, 
     a.dbeta = dbeta;
     a.dlog_alpha = dlog_alpha;
     a.dS0 = dS0;
+    a.inject = take_inject(INJ_DELTA_BWD, 1, &a.timeout_ns);
     delta::tc::set_segments(a, scratch + delta::tc::bwd_scratch_bytes(d) - delta::tc::seg_bytes(d, false),
                             a.sv.M);
     return delta::tc::run_bwd(a, st) == cudaSuccess ? GRADLEV_OK : GRADLEV_ERR_CUDA;

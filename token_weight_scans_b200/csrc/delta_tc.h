@@ -105,6 +105,7 @@ struct Args {
   bf16* dS = nullptr;       // [B*H][N][dvp][128]: gradient of the chunk-end states
   void *dq = nullptr, *dk_ = nullptr, *dv_ = nullptr, *dbeta = nullptr, *dlog_alpha = nullptr;
   void* dS0 = nullptr;
+  int inject = 0;           // test hook: the walk proper withholds one completion signal
   SegPlan seg{1, 1 << 30};
   float *loc = nullptr, *init = nullptr, *M = nullptr;  // with segments (WalkParams)
 };

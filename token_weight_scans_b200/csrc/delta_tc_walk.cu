@@ -126,6 +126,7 @@ struct WalkParams {
   // slice past the last one carries the identity. CTAs past those carry it through the last
   // segment.
   int nseg, seg_chunks, seg0, segs, nsl;
+  int inject;            // test hook
   int sum;               // states alone: nothing is left for other kernels but loc and M
   const float* init;     // [B*H][nseg][dvp][128] states the segments start from, or null
   float *loc, *M;        // [B*H][nseg][dvp][128], [B*H][nseg][128][128]
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        umma_commit(&sm.dfull);
+        if (!(p.inject && c == 1)) umma_commit(&sm.dfull);
         if (BWD) {
           umma_commit(&sm.yfull[yb]);
           if (!mbar_wait(&sm.sscaled, c & 1, wc, W_SREADY)) break;
@@ -799,7 +800,7 @@ static cudaError_t launch(const Args& a, bool sum, cudaStream_t st) {
   const int ns = dvp(d) / 128, nseg = a.seg.nseg;
   WalkParams p{d, BWD ? a.sv.gates : a.m.gates, a.status, a.timeout_ns, a.S0,
                static_cast<const bf16*>(a.dST), a.ST, static_cast<bf16*>(a.dS0),
-               static_cast<bf16*>(a.y), dd, states, nseg, a.seg.chunks, 0, nseg, ns, sum,
+               static_cast<bf16*>(a.y), dd, states, nseg, a.seg.chunks, 0, nseg, ns, sum ? 0 : a.inject, sum,
                nseg > 1 ? a.init : nullptr, a.loc, a.M};
   unsigned grid = (unsigned)(bh * ns * nseg);
   if (sum) {  // forward: all segments but the last, with the identity; backward: all but the first

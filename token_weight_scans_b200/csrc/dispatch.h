@@ -3,12 +3,22 @@
 
 #include <cuda_runtime.h>
 #include <stddef.h>
+#include <stdint.h>
 
 #include "gradlev.h"
 
 namespace gradlev {
 
 constexpr size_t kStatusBytes = 256;  // device status word + alignment pad
+constexpr uint64_t kWaitTimeoutNs = 2000000000ull;  // bound of device-side waits
+
+// Test hook (gradlev_debug_inject_timeout): the kernel's inject code and wait bound for a
+// launch at `site` (one-shot; 0 and kWaitTimeoutNs where that site is not armed).
+enum InjectSite {
+  INJ_NONE = 0, INJ_FWD = 1, INJ_BWD = 2, INJ_FWD_SUMMARY = 3, INJ_BWD_SUMMARY = 4,
+  INJ_DELTA_FWD = 5, INJ_DELTA_BWD = 6
+};
+int take_inject(int site, int code, uint64_t* timeout_ns);
 
 // Which kernel family serves a shape: the tcgen05 kernels for bf16 with
 // d_in = d_out = 128, the CUDA-core kernels otherwise.

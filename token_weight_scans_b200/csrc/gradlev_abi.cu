@@ -24,7 +24,6 @@
 
 namespace gradlev {
 
-static constexpr uint64_t kWaitTimeoutNs = 2000000000ull;  // bound of device-side waits
 
 static thread_local int t_launches = 0;
 void count_launch() { ++t_launches; }
@@ -32,14 +31,13 @@ void reset_launch_count() { t_launches = 0; }
 
 // Test hook state (gradlev_debug_inject_timeout): the site of the next launch that
 // withholds one completion signal (0 = none), consumed by that launch.
-enum InjectSite { INJ_NONE = 0, INJ_FWD = 1, INJ_BWD = 2, INJ_FWD_SUMMARY = 3, INJ_BWD_SUMMARY = 4 };
 static int g_inject = INJ_NONE;
 static uint64_t g_inject_timeout_ns = 0;
 // Test hook state (gradlev_debug_summary_rescale): bound of the summary passes' deferred decay
 static float g_rescale_log2 = tc::kSummaryRescaleLog2;
 
 // The kernel's inject code and wait bound for a launch at `site` (one-shot).
-static int take_inject(int site, int code, uint64_t* timeout_ns) {
+int take_inject(int site, int code, uint64_t* timeout_ns) {
   if (g_inject != site) {
     *timeout_ns = kWaitTimeoutNs;
     return 0;
@@ -648,7 +646,7 @@ gradlev_status gradlev_device_status(const void* workspace, void* stream) {
 int gradlev_last_launch_count(void) { return t_launches; }
 
 void gradlev_debug_inject_timeout(int site, int timeout_ms) {
-  g_inject = (site >= INJ_FWD && site <= INJ_BWD_SUMMARY) ? site : INJ_NONE;
+  g_inject = (site >= INJ_FWD && site <= INJ_DELTA_BWD) ? site : INJ_NONE;
   g_inject_timeout_ns = (uint64_t)(timeout_ms > 0 ? timeout_ms : 1) * 1000000ull;
 }
 
