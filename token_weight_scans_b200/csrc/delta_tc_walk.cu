@@ -75,7 +75,8 @@ struct Bars {
   uint64_t full[3][NS], empty[3][NS];   // per group of tiles
   uint64_t scaled[NS];
   uint64_t gfull[GS], gempty[GS];
-  uint64_t sready, sscaled, dfull, uready, sfull, done;
+  uint64_t sready[2];                   // (SPLIT: in two halves of each warp's columns)
+  uint64_t sscaled, dfull, uready, sfull, done;
   uint64_t yfull[2], yfree[2];          // per accumulator pair
   uint32_t tmem_base;
   int abort;
@@ -265,7 +266,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.gfull[g], 1);
       mbar_init(&sm.gempty[g], 12);  // the chain's 8 warps, 4 that scale Q
     }
-    mbar_init(&sm.sready, 8);
+    mbar_init(&sm.sready[0], 8);
+    mbar_init(&sm.sready[1], 8);
     mbar_init(&sm.sscaled, 8);
     mbar_init(&sm.dfull, 1);
     mbar_init(&sm.uready, 8);
@@ -363,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sk = smem_u32(base + L::kp(s));
         const uint32_t d = tb + COL_D + 128 * yb, y = d + 64;
         if (!mbar_wait(carry && !BWD ? &sm.full[WQ][s] : &sm.scaled[s], (c / NS) & 1, wc, W_SCALED)) break;
-        if (!mbar_wait(&sm.sready, c & 1, wc, W_SREADY)) break;
+        if (!mbar_wait(&sm.sready[0], c & 1, wc, W_SREADY)) break;
         tc_fence_after();
         // D^T += S W^T, and without SPLIT Y^T = S Q^T in the same products
         if (!SPLIT && outputs) {
@@ -374,19 +376,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_bf16_tmem_a(d, tb + COL_SH + 8 * kk,
                              desc_at(sw128_desc(st + L::w, 16, 1024), (kk >> 2) * L::wq + (kk & 3) * 32),
                              id_wq, 1);
-        } else {
+        } else if (!SPLIT) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint64_t bw =
-                desc_at(sw128_desc(st + L::w, 16, 1024), (kk >> 2) * L::wq + (kk & 3) * 32);
-            umma_bf16_tmem_a(d, tb + COL_SH + 8 * kk, bw, id_w, 1);
-            if (SPLIT) {
+          for (int kk = 0; kk < 8; ++kk)
+            umma_bf16_tmem_a(d, tb + COL_SH + 8 * kk,
+                             desc_at(sw128_desc(st + L::w, 16, 1024), (kk >> 2) * L::wq + (kk & 3) * 32),
+                             id_w, 1);
+        } else {
+          // the K steps in the order in which the two warpgroups convert S, so that the products
+          // of the first half run while the second is converted
+          bool got = true;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (half == 1) {
+              got = mbar_wait(&sm.sready[1], c & 1, wc, W_SREADY);
+              if (!got) break;
+              tc_fence_after();
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int kk = 4 * (j >> 1) + 2 * half + (j & 1);
+              const uint64_t bw =
+                  desc_at(sw128_desc(st + L::w, 16, 1024), (kk >> 2) * L::wq + (kk & 3) * 32);
+              umma_bf16_tmem_a(d, tb + COL_SH + 8 * kk, bw, id_w, 1);
               umma_bf16_tmem_a(d, tb + COL_SL + 8 * kk, bw, id_w, 1);
               umma_bf16_tmem_a(d, tb + COL_SH + 8 * kk,
                                desc_at(sw128_desc(st + L::wl, 16, 1024),
                                        (kk >> 2) * TILE + (kk & 3) * 32), id_w, 1);
             }
           }
+          if (!got) break;
         }
         if (!(p.inject && c == 1)) umma_commit(&sm.dfull);
         if (BWD) {
@@ -513,28 +532,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float GC = gs.GC;
       uint32_t pk[32];
       const uint32_t at = tb + COL_S + lo + 64 * hh;
-      if constexpr (SPLIT) {  // 32 columns at a time: registers
+      if constexpr (SPLIT) {  // 32 columns at a time (registers), each half as it is ready
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           float v[32];
           tmem_ld32(at + 32 * hf, v);
           tmem_ld_wait();
-          uint32_t rest[16];
+          uint32_t hi[16], rest[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            pk[16 * hf + e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-            rest[e] = pack_rest(v[2 * e], v[2 * e + 1], pk[16 * hf + e]);
+            hi[e] = pk[16 * hf + e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+            rest[e] = pack_rest(v[2 * e], v[2 * e + 1], hi[e]);
           }
+          st_tmem16(tb + COL_SH + lo + 32 * hh + 16 * hf, hi);
           st_tmem16(tb + COL_SL + lo + 32 * hh + 16 * hf, rest);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.sready[hf]);
+        }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {  // the decay, read again: not before the update
+          float v[32];
+          tmem_ld32(at + 32 * hf, v);
+          tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] *= GC;
           tmem_st32(at + 32 * hf, v);
         }
-        st_tmem32(tb + COL_SH + lo + 32 * hh, pk);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.sready);
       } else {
         // the bf16 copy first; the decayed state is only needed by the update (backward: by
         // dY^T Q)
@@ -551,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.sready);
+        if (lane == 0) mbar_arrive(&sm.sready[0]);
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           v0[e] *= GC;
