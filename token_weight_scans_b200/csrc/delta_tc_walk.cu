@@ -53,8 +53,11 @@ constexpr uint32_t COL_SH = 128;   // bf16 state, 64
 constexpr uint32_t COL_DB = 192;   // bf16 D (E), 32
 constexpr uint32_t COL_U = 224;    // bf16 beta w D, 32
 constexpr uint32_t COL_D = 256;    // D^T (E^T) accumulator, 64, and Y^T, 64; two such pairs
-constexpr uint32_t COL_SL = 384;   // SPLIT (one pair): remainder of the state, 64,
-constexpr uint32_t COL_UL = 448;   // and of beta w D, 32
+// SPLIT has one set: D^T in two parts that the chain adds (the products with T0 and W, and with
+// their remainders), then Y^T: the three take one product of N = 192
+constexpr uint32_t COL_YS = 384;   // SPLIT: Y^T
+constexpr uint32_t COL_SL = 448;   // SPLIT: remainder of the state, 64; once the products with W
+constexpr uint32_t COL_UL = 448;   // have read it, that of beta w D, 32
 
 // A chunk's gates: the piece of GateBlock that the direction needs, as it lies there.
 template <bool BWD> struct GateSlot;
@@ -84,12 +87,13 @@ struct Bars {
 enum { VT = 0, WQ = 1, KP = 2 };
 
 // The rings. VT: V (dY), T0 (PT), SPLIT also the remainder of T0. WQ: per 64 columns of d_k the
-// W (Wb) tile and the Q tile next to each other (128 rows of one operand), SPLIT also the
-// remainder of W. KP: K, forward also Pb.
+// W (Wb) tile, SPLIT the remainder of W, and the Q tile next to each other (128 or 192 rows of
+// one operand). KP: K, forward also Pb.
 template <bool BWD, bool SPLIT>
 struct Layout {
   static constexpr int v = 0, t = 2 * TILE, tl = 3 * TILE;
-  static constexpr int w = 0, q = TILE, wq = 2 * TILE, wl = 4 * TILE;  // wq: between k-blocks
+  static constexpr int w = 0, wl = TILE, q = SPLIT ? 2 * TILE : TILE;
+  static constexpr int wq = q + TILE;    // from one k-block to the next
   static constexpr int k = 0, p = 2 * TILE;
   static constexpr int vt_bytes = SPLIT ? 4 * TILE : 3 * TILE;
   static constexpr int wq_bytes = SPLIT ? 6 * TILE : 4 * TILE;
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kb = 0; kb < 2; ++kb) {
             if (BWD || outputs) tma_load_3d(a + L::q + kb * L::wq, &tmQ, f, 64 * kb, t0, kh);
             tma_load_3d(a + L::w + kb * L::wq, &tmW, f, 64 * kb, t0, bh);
-            if (SPLIT) tma_load_3d(a + L::wl + kb * TILE, &tmWl, f, 64 * kb, t0, bh);
+            if (SPLIT) tma_load_3d(a + L::wl + kb * L::wq, &tmWl, f, 64 * kb, t0, bh);
           }
         }
       }
@@ -335,9 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      const uint32_t id_v = idesc_bf16(128, 64, true, BWD);       // V^T T0^T, dY^T PT
+      const uint32_t id_v = idesc_bf16(128, SPLIT ? 128 : 64, true, BWD);  // V^T T0^T, dY^T PT
       const uint32_t id_w = idesc_bf16(128, 64, false, false);    // S W^T, S Q^T, D^T Pb^T
-      const uint32_t id_wq = idesc_bf16(128, 128, false, false);  // S [W; Q]^T
+      const uint32_t id_wq = idesc_bf16(128, 128, false, false);  // S [W; Q]^T, S [W; Wlo]^T
+      const uint32_t id_wwq = idesc_bf16(128, 192, false, false); // S [W; Wlo; Q]^T
       const uint32_t id_u = idesc_bf16(128, 128, false, true);    // U^T K, E^T K
       const uint32_t id_o = idesc_bf16(128, 128, true, true);     // dY^T Q
       // D^T of chunk c = V^T T0^T. Its pair of accumulators is free once the chain has read D
@@ -353,7 +358,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t av = desc_at(sw128_desc(st + L::v, TILE, 1024), kk * 2048);
           const uint32_t off = BWD ? kk * 2048 : kk * 32;
           umma_bf16(d, av, desc_at(sw128_desc(st + L::t, BWD ? TILE : 16, 1024), off), id_v, kk > 0);
-          if (SPLIT) umma_bf16(d, av, desc_at(sw128_desc(st + L::tl, 16, 1024), off), id_v, 1);
         }
         if (!BWD) umma_commit(&sm.empty[VT][s]);
         return true;
@@ -363,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = c % NS, yb = c % NY;
         const uint32_t st = smem_u32(base + L::wq_at(s)), sv = smem_u32(base + L::vt(s));
         const uint32_t sk = smem_u32(base + L::kp(s));
-        const uint32_t d = tb + COL_D + 128 * yb, y = d + 64;
+        const uint32_t d = tb + COL_D + 128 * yb, y = SPLIT ? tb + COL_YS : d + 64;
         if (!mbar_wait(carry && !BWD ? &sm.full[WQ][s] : &sm.scaled[s], (c / NS) & 1, wc, W_SCALED)) break;
         if (!mbar_wait(&sm.sready[0], c & 1, wc, W_SREADY)) break;
         tc_fence_after();
@@ -385,24 +389,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           // the K steps in the order in which the two warpgroups convert S, so that the products
           // of the first half run while the second is converted
-          bool got = true;
+          bool got = !outputs || mbar_wait(&sm.yfree[0], (c & 1) ^ 1, wc, W_YFREE);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            if (half == 1) {
-              got = mbar_wait(&sm.sready[1], c & 1, wc, W_SREADY);
-              if (!got) break;
-              tc_fence_after();
-            }
+            if (half == 1) got = got && mbar_wait(&sm.sready[1], c & 1, wc, W_SREADY);
+            if (!got) break;
+            tc_fence_after();
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int kk = 4 * (j >> 1) + 2 * half + (j & 1);
-              const uint64_t bw =
-                  desc_at(sw128_desc(st + L::w, 16, 1024), (kk >> 2) * L::wq + (kk & 3) * 32);
-              umma_bf16_tmem_a(d, tb + COL_SH + 8 * kk, bw, id_w, 1);
+              const uint32_t off = (kk >> 2) * L::wq + (kk & 3) * 32;
+              const uint64_t bw = desc_at(sw128_desc(st + L::w, 16, 1024), off);
+              if (outputs && kk > 0) {
+                umma_bf16_tmem_a(d, tb + COL_SH + 8 * kk, bw, id_wwq, 1);
+              } else {
+                umma_bf16_tmem_a(d, tb + COL_SH + 8 * kk, bw, id_wq, 1);
+                if (outputs)
+                  umma_bf16_tmem_a(y, tb + COL_SH, desc_at(sw128_desc(st + L::q, 16, 1024), off), id_w, 0);
+              }
               umma_bf16_tmem_a(d, tb + COL_SL + 8 * kk, bw, id_w, 1);
-              umma_bf16_tmem_a(d, tb + COL_SH + 8 * kk,
-                               desc_at(sw128_desc(st + L::wl, 16, 1024),
-                                       (kk >> 2) * TILE + (kk & 3) * 32), id_w, 1);
             }
           }
           if (!got) break;
@@ -418,20 +423,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                       desc_at(sw128_desc(st + L::q, L::wq, 1024), kk * 2048), id_o, 1);
           umma_commit(&sm.empty[VT][s]);
           umma_commit(&sm.empty[WQ][s]);
-        } else if (SPLIT) {  // Y^T = S Q^T, which frees the bf16 state
-          if (!mbar_wait(&sm.yfree[0], (c & 1) ^ 1, wc, W_YFREE)) break;
-          tc_fence_after();
-          if (outputs) {
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma_bf16_tmem_a(y, tb + COL_SH + 8 * kk,
-                               desc_at(sw128_desc(st + L::q, 16, 1024),
-                                       (kk >> 2) * L::wq + (kk & 3) * 32), id_w, kk > 0);
-          }
-          umma_commit(&sm.empty[WQ][s]);
         } else {
           umma_commit(&sm.empty[WQ][s]);
-          if (c + 1 < NC && !first(c + 1)) break;
+          if (!SPLIT && c + 1 < NC && !first(c + 1)) break;
         }
         if (!mbar_wait(&sm.full[KP][s], (c / NS) & 1, wc, W_FULL)) break;
         if (!mbar_wait(&sm.uready, c & 1, wc, W_UREADY)) break;
@@ -630,7 +624,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       float v[32];
       tmem_ld32(tb + COL_D + 128 * (c % NY) + lo + 32 * hh, v);
-      tmem_ld_wait();
+      if constexpr (SPLIT) {
+        float w[32];
+        tmem_ld32(tb + COL_D + 64 + lo + 32 * hh, w);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] += w[e];
+      } else {
+        tmem_ld_wait();
+      }
       uint32_t db[16];  // D (E) in bf16: 32 tokens of this row
       {
         uint32_t ub[16], rest[16];
@@ -767,13 +769,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = !named_bar_or(2, 128, !ok);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t d = COL_D + 128 * yb;
+      const uint32_t d = COL_D + 128 * yb;  // D^T (E^T)
       if (carry || (!BWD && !p.y)) {
         if (lane == 0) mbar_arrive(&sm.yfree[yb]);
       } else if constexpr (BWD) {
         emit(d, &tmY, sm.gates[g].be, t0, &sm.yfree[yb]);  // dV = beta E
       } else {
-        emit(d + 64, &tmY, nullptr, t0, &sm.yfree[yb]);
+        emit(SPLIT ? COL_YS : d + 64, &tmY, nullptr, t0, &sm.yfree[yb]);
       }
       if (lane == 0) mbar_arrive(&sm.gempty[g]);
     }
