@@ -337,7 +337,11 @@ GRADLEV_API gradlev_status gradlev_mlp2_recon(int B, int H, int T, int d_x, int 
  * exponential underflows float32, counts as -inf. beta_t = 0 leaves the state to its
  * decay alone (padding), and dbeta is exact there too. Keys are expected with
  * beta_t |k_t|^2 < 2, where the rule contracts (gradlev_qk_norm_rope_fwd with
- * GRADLEV_NORM_L2 gives |k_t| = 1); beyond it states grow as the formula says. */
+ * GRADLEV_NORM_L2 gives |k_t| = 1); beyond it states grow as the formula says.
+ * A state that a call starts from is not used where the first token is a reset and may
+ * hold anything there (a slot of an earlier request, fresh memory). Everything else must
+ * be finite, padding and the tokens before a reset too: the chunks multiply what a gate
+ * masks by zero. */
 
 /* Whether the shape is supported by gradlev_delta_fwd / _bwd: GRADLEV_OK, or
  * GRADLEV_ERR_INVALID_ARG / GRADLEV_ERR_UNSUPPORTED without touching the GPU.

@@ -200,6 +200,32 @@ def test_step_slots():
     assert torch.equal(S[[1, 2, 4]].cpu(), first[[1, 2, 4]])
 
 
+@pytest.mark.parametrize("B,H,T,dk,dv,dtype", [
+    (1, 2, 40, 32, 32, "f32"), (2, 2, 100, 136, 64, "bf16"), (2, 4, 100, 128, 128, "bf16"),
+    (1, 2, 1283, 128, 256, "bf16"), (2, 2, 3, 64, 64, "bf16")])
+def test_a_reset_first_token_forgets_any_state(B, H, T, dk, dv, dtype):
+    """What S0 or the pool holds, NaN and infinities among it, does not matter to a scan whose
+    first token is a reset; the other scans of the call keep theirs."""
+    d = ref.draw(B, H, H, T, dk, dv, dtype, True, seed=8)
+    d["log_alpha"][:, 0, 0] = float("-inf")
+    d["S0"][:, 0] = 0.0
+    g = dev(d)
+    args, zero = [g[n] for n in NAMES], g["S0"]
+    junk = zero.clone()
+    junk[:, 0] = float("nan")
+    junk[:, 0, ::2] = float("inf")
+    for want_ST in (False, True):
+        got, want = (tw.gradlev_delta_fwd(*args, s, want_ST=want_ST) for s in (junk, zero))
+        assert torch.equal(got[0], want[0]) and torch.isfinite(got[0].float()).all()
+        assert not want_ST or torch.equal(got[1], want[1])
+    got, want = (tw.gradlev_delta_bwd(*args, g["dy"], s) for s in (junk, zero))
+    for n in want:
+        assert torch.equal(got[n], want[n]) and torch.isfinite(got[n].float()).all(), n
+    a, b = junk.clone(), zero.clone()
+    ya, yb = (tw.gradlev_delta_step(*args, s) for s in (a, b))
+    assert torch.equal(ya, yb) and torch.equal(a, b) and torch.isfinite(a).all()
+
+
 @pytest.mark.parametrize("dtype,dk,dv", [("f32", 24, 40), ("bf16", 128, 128), ("bf16", 128, 256),
                                          ("bf16", 40, 72), ("bf16", 72, 136)])
 def test_outputs_stay_inside_their_buffers(dtype, dk, dv):

@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(Args a) {
   float* S = reinterpret_cast<float*>(smc + 2 * stage_bytes<Tio>(d.dk));  // [kRows][ld]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r0 = 2 * warp;
   const Tio* v = static_cast<const Tio*>(BWD ? a.dy : a.v);
+  const bool fresh = a.log_alpha[(size_t)bh * d.T] < kResetLog;  // S0 may hold anything then
   for (int i = tid; i < kRows * d.dk; i += kThreads) {
     const int r = i / d.dk, c = i - r * d.dk;
     const size_t at = ((size_t)bh * d.dv + n0 + r) * d.dk + c;
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(Args a) {
       if (BWD)
         s = a.dST ? to_f32(static_cast<const Tio*>(a.dST)[at]) : 0.f;
       else
-        s = a.S0 ? a.S0[at] : 0.f;
+        s = a.S0 && !fresh ? a.S0[at] : 0.f;
     }
     S[r * ld + c] = s;
   }

@@ -11,6 +11,7 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "delta.h"
 #include "gradlev.h"
 
 namespace gradlev {
@@ -96,7 +97,9 @@ __global__ void __launch_bounds__(kWarps * 32) step_kernel(StepArgs a) {
       kv[i] = kok[i] ? load4(kg + (size_t)t * dk + 4 * (gl + LPR * i)) : zero;
       kq += qv[i].x * kv[i].x + qv[i].y * kv[i].y + qv[i].z * kv[i].z + qv[i].w * kv[i].w;
     }
-    const float be = a.beta[(size_t)bh * a.T + t], al = expf(a.log_alpha[(size_t)bh * a.T + t]);
+    const float be = a.beta[(size_t)bh * a.T + t], la = a.log_alpha[(size_t)bh * a.T + t];
+    const bool reset = la < kResetLog;  // whatever the state held, NaN among it, is gone
+    const float al = expf(la);
     float vv[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
@@ -107,7 +110,8 @@ __global__ void __launch_bounds__(kWarps * 32) step_kernel(StepArgs a) {
       float pk = 0.f, pq = 0.f;
 #pragma unroll
       for (int i = 0; i < NK4; ++i) {
-        s[r][i] = make_float4(al * s[r][i].x, al * s[r][i].y, al * s[r][i].z, al * s[r][i].w);
+        s[r][i] = reset ? zero
+                        : make_float4(al * s[r][i].x, al * s[r][i].y, al * s[r][i].z, al * s[r][i].w);
         pk = fmaf(s[r][i].x, kv[i].x, pk);
         pq = fmaf(s[r][i].x, qv[i].x, pq);
         pk = fmaf(s[r][i].y, kv[i].y, pk);

@@ -49,7 +49,8 @@ __device__ __forceinline__ void copy16(void* dst, const void* src) {
 template <bool BWD, int kRows>
 __global__ void __launch_bounds__(kThreads) combine_kernel(Dims d, int nseg, const float* L,
                                                            const float* M, const float* S0,
-                                                           const bf16* dST, float* out) {
+                                                           const float* log_alpha, const bf16* dST,
+                                                           float* out) {
   extern __shared__ __align__(16) float sm[];
   float* S = sm + 2 * 128 * kLd;  // [kRows][kLd]
   const int dv = dvp(d), nb = dv / kRows, bh = blockIdx.x / nb, r0 = (blockIdx.x - bh * nb) * kRows;
@@ -64,13 +65,14 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(Dims d, int nseg, con
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  const bool use_S0 = S0 && !(log_alpha[(size_t)bh * d.T] < kResetLog);
   float s[kRows / 2];
 #pragma unroll
   for (int e = 0; e < kRows / 2; ++e) {
     const int r = r0 + h + e;  // the caller's states have no padding
     const bool ok = r < d.dv && c < d.dk;
     const size_t at = ((size_t)bh * d.dv + r) * d.dk + c;
-    s[e] = !ok ? 0.f : BWD ? (dST ? __bfloat162float(dST[at]) : 0.f) : (S0 ? S0[at] : 0.f);
+    s[e] = !ok ? 0.f : BWD ? (dST ? __bfloat162float(dST[at]) : 0.f) : (use_S0 ? S0[at] : 0.f);
   }
   fetch(0);
   for (int i = 0; i < nseg; ++i) {
@@ -120,7 +122,7 @@ cudaError_t combine(const Args& a, cudaStream_t st) {
   }
   combine_kernel<BWD, kRows><<<(unsigned)(a.d.BH() * (dvp(a.d) / kRows)), kThreads,
                                combine_smem<kRows>(), st>>>(
-      a.d, a.seg.nseg, a.loc, a.M, a.S0, static_cast<const bf16*>(a.dST), a.init);
+      a.d, a.seg.nseg, a.loc, a.M, a.S0, a.log_alpha, static_cast<const bf16*>(a.dST), a.init);
   count_launch();
   return cudaGetLastError();
 }

@@ -121,6 +121,7 @@ struct WalkParams {
   DeviceStatus* status;
   uint64_t timeout_ns;
   const float* S0;       // forward start
+  const float* log_alpha;
   const bf16* dST;       // backward start
   float* ST;             // forward end
   bf16* dS0;             // backward end
@@ -478,14 +479,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const size_t row = ((size_t)bh * p.d.dv + n0 + r) * p.d.dk;
     auto cok = [&](int col) { return rok && col < p.d.dk; };
     const int rows = dvp(p.d);
-    // start state
+    // start state; S0 may hold anything where the first token is a reset
+    const bool use_S0 = !BWD && p.S0 && !(p.log_alpha[(size_t)bh * p.d.T] < kResetLog);
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       float v[32];
       const int col = 64 * hh + 32 * hf;
 #pragma unroll
       for (int e = 0; e < 32; ++e) v[e] = ident && col + e == r ? 1.f : 0.f;
-      const float* from = p.init ? p.init + (sg * rows + n0 + r) * 128 : !BWD && p.S0 ? p.S0 + row : nullptr;
+      const float* from = p.init ? p.init + (sg * rows + n0 + r) * 128 : use_S0 ? p.S0 + row : nullptr;
       if (!carry && from) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -825,7 +827,7 @@ static cudaError_t launch(const Args& a, bool sum, cudaStream_t st) {
     set.fetch_or(bit);
   }
   const int ns = dvp(d) / 128, nseg = a.seg.nseg;
-  WalkParams p{d, BWD ? a.sv.gates : a.m.gates, a.status, a.timeout_ns, a.S0,
+  WalkParams p{d, BWD ? a.sv.gates : a.m.gates, a.status, a.timeout_ns, a.S0, a.log_alpha,
                static_cast<const bf16*>(a.dST), a.ST, static_cast<bf16*>(a.dS0),
                static_cast<bf16*>(a.y), dd, states, nseg, a.seg.chunks, 0, nseg, ns, sum ? 0 : a.inject, sum,
                nseg > 1 ? a.init : nullptr, a.loc, a.M};
