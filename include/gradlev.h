@@ -399,8 +399,8 @@ GRADLEV_API gradlev_status gradlev_delta_bwd(int B, int H, int Hk, int T, int d_
  *       (-1: padding), or is also the slot of an earlier batch row, has no state: its
  *       y is zero and no state is written for it. Pool rows that no slot names keep
  *       their values.
- *   Constraints: d_k a multiple of 4 up to 256, any d_v >= 1, H % Hk == 0
- *   (GRADLEV_ERR_UNSUPPORTED). Alignment, else GRADLEV_ERR_INVALID_ARG: q and k to 4
+ *   Constraints: d_k a multiple of 4 up to 256, any d_v >= 1, H % Hk == 0,
+ *   B*H*T < 2^31, B*H*d_v < 2^30 (GRADLEV_ERR_UNSUPPORTED). Alignment, else GRADLEV_ERR_INVALID_ARG: q and k to 4
  *   elements, v and y to one element, S to 16 bytes. One launch; no workspace. */
 GRADLEV_API gradlev_status gradlev_delta_step(int B, int H, int Hk, int T, int d_k, int d_v,
                                   gradlev_dtype dt, const void* q, const void* k, const void* v,
@@ -421,8 +421,8 @@ GRADLEV_API gradlev_status gradlev_delta_step(int B, int H, int Hk, int T, int d
  *   yq [B,Hq,T,d], yk [B,Hk,T,d]: contiguous, the layout of gradlev_delta_fwd.
  *   wq, wk: [d] float32, or NULL (1). pos: [B,T] int32, or NULL (t). inv_freq:
  *     [rot / 2] float32 (NULL when rot = 0).
- *   Constraints: d a multiple of 8 up to 256, rot a multiple of 16 up to d
- *   (GRADLEV_ERR_UNSUPPORTED). A row of zeros with eps = 0 gives NaN, as the formula. */
+ *   Constraints: d a multiple of 8 up to 256, rot a multiple of 16 up to d,
+ *   B*T*(Hq+Hk) < 2^31 (GRADLEV_ERR_UNSUPPORTED). A row of zeros with eps = 0 gives NaN, as the formula. */
 typedef enum { GRADLEV_NORM_L2 = 0, GRADLEV_NORM_RMS = 1 } gradlev_norm;
 
 GRADLEV_API gradlev_status gradlev_qk_norm_rope_fwd(
@@ -431,8 +431,9 @@ GRADLEV_API gradlev_status gradlev_qk_norm_rope_fwd(
     const float* wq, const float* wk, const int* pos, const float* inv_freq, void* yq, void* yk,
     void* stream);
 
-/* Its gradients: dq and dk (by strides, like q and k; elements between the rows are not
- * written) and dwq, dwk [d] float32, each present exactly when its weight is. Sums over
+/* Its gradients: dq and dk (by strides, like q and k, but no two rows in one place: a
+ * stride of 0 over an axis longer than 1 is GRADLEV_ERR_INVALID_ARG; elements between the
+ * rows are not written) and dwq, dwk [d] float32, each present exactly when its weight is. Sums over
  * rows run in a fixed order. workspace: gradlev_qk_norm_rope_workspace_bytes() bytes,
  * 256-byte aligned; NULL when neither weight is given. dq and dk may be q and k. */
 GRADLEV_API size_t gradlev_qk_norm_rope_workspace_bytes(int B, int T, int Hq, int Hk, int d,

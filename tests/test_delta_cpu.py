@@ -181,3 +181,23 @@ def test_the_binding_refuses_before_any_call():
         tw.gradlev_qk_norm_rope_fwd(x, x)
     with pytest.raises(tw.GradlevError, match="not one of"):
         tw.gradlev_qk_norm_rope_fwd(x, x, norm="max")
+
+
+@pytest.mark.parametrize("call", [fwd, bwd, step])
+def test_products_of_sizes_past_64_bits_are_refused(L, call):
+    big = 1 << 30
+    assert call(L, B=big, H=big, Hk=1, T=1 << 10) == 2  # 2^70: 0 modulo 2^64
+    assert call(L, B=big, H=big, Hk=1, T=1) == 2
+    assert call(L, B=1, H=1, T=1, dv=2 ** 31 - 8) == 2
+    if call is not step:
+        for shape in ((big, big, 1, 1 << 10, 16, 16, 0), (big, big, 1, 1, 16, 16, 1)):
+            assert L.gradlev_delta_supported(*shape) == 2
+            assert L.gradlev_delta_workspace_bytes(*shape, 1) == 0
+    for b in (False, True):
+        assert norm(L, bwd=b, B=big, T=big, Hq=1 << 9, Hk=1 << 9) == 2
+
+
+def test_outputs_over_their_inputs_or_themselves_are_refused(L):
+    assert fwd(L, S0=P(8192), ST=P(8192)) == 1
+    for qs in ((0, 64, 32), (128, 0, 32), (128, 64, 0)):  # gradients of many rows in one place
+        assert norm(L, bwd=True, B=2, qs=qs) == 1

@@ -66,7 +66,7 @@ struct WalkGates {
   float beta[C], G[C], w[C];
   float GC, pad[3];
 };
-__host__ __device__ inline int chunks(int T) { return (T + C - 1) / C; }
+__host__ __device__ inline int chunks(int T) { return (T - 1) / C + 1; }
 size_t saved_bytes(const Dims& d, bool states);  // states = false: Z, P and gates alone
 Saved saved_at(char* base, const Dims& d, bool states);
 

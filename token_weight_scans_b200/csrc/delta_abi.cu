@@ -18,8 +18,8 @@ gradlev_status check_shape(int B, int H, int Hk, int T, int dk, int dv, gradlev_
   if (dt != GRADLEV_F32 && dt != GRADLEV_BF16) return GRADLEV_ERR_INVALID_ARG;
   if (H % Hk != 0) return GRADLEV_ERR_UNSUPPORTED;
   if (dk % 8 != 0 || dv % 8 != 0 || dk > 256 || dv > 256) return GRADLEV_ERR_UNSUPPORTED;
-  if ((long long)B * H * T >= (1LL << 31) || (long long)B * H * 16 >= (1LL << 31))
-    return GRADLEV_ERR_UNSUPPORTED;
+  const long long BH = (long long)B * H;  // B*H*T itself may pass 64 bits
+  if (BH >= 1LL << 27 || BH * T >= 1LL << 31) return GRADLEV_ERR_UNSUPPORTED;
   return GRADLEV_OK;
 }
 
@@ -130,7 +130,7 @@ gradlev_status gradlev_delta_fwd(int B, int H, int Hk, int T, int d_k, int d_v, 
   if (!q || !k || !v || !beta || !log_alpha || !y || !workspace) return GRADLEV_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(y, 16) ||
       !aligned(beta, 4) || !aligned(log_alpha, 4) || !aligned(S0, 16) || !aligned(ST, 16) ||
-      !aligned(ckpt, 256) || !aligned(workspace, 256))
+      !aligned(ckpt, 256) || !aligned(workspace, 256) || (ST && ST == S0))
     return GRADLEV_ERR_INVALID_ARG;
   const Dims d = dims(B, H, Hk, T, d_k, d_v, dt);
   if (ws_bytes < ws_bytes_of(d, 0)) return GRADLEV_ERR_WORKSPACE;

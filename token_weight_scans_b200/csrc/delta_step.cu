@@ -180,8 +180,8 @@ extern "C" gradlev_status gradlev_delta_step(int B, int H, int Hk, int T, int d_
     return GRADLEV_ERR_INVALID_ARG;
   if (dt != GRADLEV_F32 && dt != GRADLEV_BF16) return GRADLEV_ERR_INVALID_ARG;
   if (H % Hk != 0 || d_k % 4 != 0 || d_k > kMaxDk) return GRADLEV_ERR_UNSUPPORTED;
-  if ((long long)B * H * T >= (1LL << 31) || (long long)B * H * ((d_v + 15) / 16) >= (1LL << 31))
-    return GRADLEV_ERR_UNSUPPORTED;
+  const long long BH = (long long)B * H;  // the products of three may pass 64 bits
+  if (BH >= 1LL << 31 || BH * T >= 1LL << 31 || BH * d_v >= 1LL << 30) return GRADLEV_ERR_UNSUPPORTED;
   if (!q || !k || !v || !beta || !log_alpha || !S || !y) return GRADLEV_ERR_INVALID_ARG;
   if (!slots && pool < B) return GRADLEV_ERR_INVALID_ARG;
   const size_t es = dt == GRADLEV_BF16 ? 2 : 4;

@@ -33,7 +33,7 @@ constexpr int TILE = C * 128;    // bytes of a [64 rows x 128 B] swizzled block
 constexpr int BIG = 128 * 128;   // bytes of a [128 rows x 128 B] swizzled block
 constexpr uint32_t LANE16 = 16u << 16;  // an M = 64 product in the upper 16 lanes of each 32
 
-__host__ __device__ inline int chunks(int T) { return (T + C - 1) / C; }
+__host__ __device__ inline int chunks(int T) { return (T - 1) / C + 1; }
 
 inline bool shape_ok(const Dims& d) { return d.bf16 && d.dk <= 128 && d.dv <= 256; }
 

@@ -363,7 +363,8 @@ gradlev_status check(int B, int T, int Hq, int Hk, int d, int rot, gradlev_dtype
   if (dt != GRADLEV_F32 && dt != GRADLEV_BF16) return GRADLEV_ERR_INVALID_ARG;
   if (norm != GRADLEV_NORM_L2 && norm != GRADLEV_NORM_RMS) return GRADLEV_ERR_INVALID_ARG;
   if (d % V != 0 || d > 32 * V || rot % (2 * V) != 0 || rot > d) return GRADLEV_ERR_UNSUPPORTED;
-  if ((long long)B * T * ((long long)Hq + Hk) >= (1LL << 31)) return GRADLEV_ERR_UNSUPPORTED;
+  const long long BT = (long long)B * T, heads = (long long)Hq + Hk;
+  if (BT >= 1LL << 31 || BT * heads >= 1LL << 31) return GRADLEV_ERR_UNSUPPORTED;
   return GRADLEV_OK;
 }
 
@@ -373,6 +374,11 @@ bool strides_ok(const long long* s, size_t es) {
   for (int i = 0; i < 3; ++i)
     if (s[i] < 0 || (s[i] * (long long)es) % 16 != 0) return false;
   return true;
+}
+
+// Rows that are written: none of them twice by a stride of zero.
+bool rows_apart(const long long* s, int B, int T, int H) {
+  return (s[0] != 0 || B == 1) && (s[1] != 0 || T == 1) && (s[2] != 0 || H == 1);
 }
 
 Rows rows_of(const void* x, const long long* s, const float* w, int H) {
@@ -449,6 +455,8 @@ gradlev_status gradlev_qk_norm_rope_bwd(
     if (!aligned(p, 4)) return GRADLEV_ERR_INVALID_ARG;
   for (const long long* t : {q_strides, k_strides, dq_strides, dk_strides})
     if (!strides_ok(t, es)) return GRADLEV_ERR_INVALID_ARG;
+  if (!rows_apart(dq_strides, B, T, Hq) || !rows_apart(dk_strides, B, T, Hk))
+    return GRADLEV_ERR_INVALID_ARG;
   const bool dw = dwq || dwk;
   if (dw && (!workspace || !aligned(workspace, 256))) return GRADLEV_ERR_INVALID_ARG;
   if (dw && ws_bytes < gradlev_qk_norm_rope_workspace_bytes(B, T, Hq, Hk, d, dt))
