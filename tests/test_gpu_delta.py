@@ -429,3 +429,52 @@ def test_binding_refusals():
         tw.gradlev_delta_step(*args, d["S0"], slots=torch.zeros(1, dtype=torch.int64, device="cuda"))
     with pytest.raises(tw.GradlevError):
         tw.gradlev_delta_bwd(*args, d["dy"], dST=d["S0"].bfloat16())
+
+
+def _room(gb):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gb * 2 ** 30:
+        pytest.skip(f"needs {gb} GB")
+
+
+@pytest.mark.parametrize("dtype,T,gb", [("bf16", 1 << 20, 110), ("f32", 1 << 19, 125)])
+def test_offsets_past_32_bits(dtype, T, gb):
+    """Tensors of more than 2^31 elements and states of more than 2^32: the first 1024 tokens
+    and the last (behind a reset) have the bits of a call on them alone."""
+    _room(gb)
+    H, d, tail = 18, 128, 1024
+    size = (1, H, H, T, d, d, code(dtype))
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    gen = torch.Generator("cuda").manual_seed(1)
+    q, k, v, dy = (torch.randn(1, H, T, d, generator=gen, dtype=dt, device="cuda") for _ in range(4))
+    k *= d ** -0.5 / 1.5  # |k|^2 below 1
+    beta = torch.rand(1, H, T, generator=gen, device="cuda")
+    la = -0.1 * torch.rand(1, H, T, generator=gen, device="cuda")
+    la[:, :, T - tail] = float("-inf")
+    full = (q, k, v, beta, la, dy)
+    first, last = ([x[:, :, s].contiguous() for x in full] for s in (slice(tail), slice(T - tail, T)))
+
+    def run(a):
+        n = a[0].shape[2]
+        ck = torch.empty(tw.gradlev_delta_ckpt_bytes(1, H, H, n, d, d, size[-1]), dtype=torch.uint8,
+                         device="cuda")
+        y, ST = tw.gradlev_delta_fwd(*a[:5], ckpt=ck)
+        return dict(tw.gradlev_delta_bwd(*a, ckpt=ck), y=y, ST=ST)
+
+    got, front, back = run(full), run(first), run(last)
+    assert torch.equal(got["y"][:, :, :tail], front["y"])
+    assert torch.equal(got["ST"], back["ST"])
+    for n in ("y", "dq", "dk", "dv", "dbeta", "dlog_alpha"):
+        assert torch.equal(got[n][:, :, T - tail:], back[n]), n
+
+
+def test_step_in_a_pool_past_32_bits():
+    _room(25)
+    pool, H, d = 8300, 32, 128  # 4.35e9 elements
+    g = dev(ref.draw(2, H, H, 1, d, d, "f32", True, seed=12))
+    args, S = [g[n] for n in NAMES], torch.zeros(pool, H, d, d, device="cuda")
+    at = torch.tensor([pool - 1, 0], device="cuda")
+    S[at] = g["S0"]
+    y = tw.gradlev_delta_step(*args, S, slots=at.int())
+    want = tw.gradlev_delta_step(*args, g["S0"])
+    assert torch.equal(y, want) and torch.equal(S[at], g["S0"]) and not S[1:pool - 1].any()
