@@ -5,7 +5,9 @@
 // T0 = (I + A diag(beta))^-1 is formed in float32 by halves: 16 x 16 diagonal blocks by
 // forward substitution (a lane per column, in registers), then twice
 //   [[X1, 0], [-X2 N21 X1, X2]]
-// which is as stable as substitution and needs only two products per level. The scaled
+// which is as stable as substitution and needs only two products per level (warp-wide tf32
+// products of split operands: 247 -> 222 us for B8 H16 T4096 against float32 FMAs, whose
+// shared-memory reads held the kernel up; tiles this small leave tcgen05.mma idle). The scaled
 // matrices T0 diag(G), diag(w) T and P then multiply K (or T) on the tensor core; K is
 // exact in bf16, so the gates ride on the other operand.
 //
@@ -78,11 +80,47 @@ __device__ __forceinline__ uint32_t pack_lo(float a, float b, uint32_t hi) {
   return pack_bf16(a - bf16_lo(hi), b - bf16_hi(hi));
 }
 __device__ __forceinline__ float4 at4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ void axpy4(float (&s)[4], float a, const float4& x) {
-  s[0] = fmaf(a, x.x, s[0]);
-  s[1] = fmaf(a, x.y, s[1]);
-  s[2] = fmaf(a, x.z, s[2]);
-  s[3] = fmaf(a, x.w, s[3]);
+
+// 16 x 8 of a product of float32 matrices in shared memory (row stride LD), k0 <= k < k1 (whole
+// eights), with both operands split into two tf32 parts: off by 2^-21, where one part would be
+// off by 2^-11. One warp; out[0..1] in row lane / 4, out[2..3] eight rows below, at columns
+// 2 (lane % 4) and the next.
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+               "{%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ void product16x8(float (&out)[4], const float* A, const float* B, int k0,
+                                            int k1) {
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  float small[4] = {0.f, 0.f, 0.f, 0.f};
+  out[0] = out[1] = out[2] = out[3] = 0.f;
+  for (int k = k0; k < k1; k += 8) {
+    const float* a = A + g * LD + k + t;
+    const float* b = B + (k + t) * LD + g;
+    uint32_t ah[4], al[4], bh[2], bl[2];
+    split_tf32(a[0], ah[0], al[0]);
+    split_tf32(a[8 * LD], ah[1], al[1]);
+    split_tf32(a[4], ah[2], al[2]);
+    split_tf32(a[8 * LD + 4], ah[3], al[3]);
+    split_tf32(b[0], bh[0], bl[0]);
+    split_tf32(b[4 * LD], bh[1], bl[1]);
+    mma_tf32(out, ah, bh);
+    mma_tf32(small, ah, bl);
+    mma_tf32(small, al, bh);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) out[e] += small[e];
+}
+__device__ __forceinline__ void store16x8(float* at, const float (&v)[4], float sign) {
+  float* p = at + ((threadIdx.x & 31) >> 2) * LD + 2 * (threadIdx.x & 3);
+  *reinterpret_cast<float2*>(p) = make_float2(sign * v[0], sign * v[1]);
+  *reinterpret_cast<float2*>(p + 8 * LD) = make_float2(sign * v[2], sign * v[3]);
 }
 
 }  // namespace
@@ -265,67 +303,27 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
       *reinterpret_cast<float4*>(sm.X + r * LD + c) = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   __syncthreads();
-  // ---- 16 -> 32: two pairs of blocks, 128 threads each: row r, 2 columns
-  {
-    const int pr = tid >> 7, r = (tid & 127) >> 3, c = 2 * (tid & 7), o = 32 * pr;
-    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-    for (int m = 0; m < 16; m += 4) {
-      const float4 a = at4(sm.N + (o + 16 + r) * LD + o + m);
-      const float av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float2 x = *reinterpret_cast<const float2*>(sm.X + (o + m + u) * LD + o + c);
-        s0 = fmaf(av[u], x.x, s0);
-        s1 = fmaf(av[u], x.y, s1);
-      }
-    }
-    float* tmp = sm.N + o * LD + o;  // the first diagonal block of the pair, done with
-    *reinterpret_cast<float2*>(tmp + r * LD + c) = make_float2(s0, s1);
-    __syncthreads();
-    s0 = s1 = 0.f;
-#pragma unroll
-    for (int m = 0; m < 16; m += 4) {
-      const float4 a = at4(sm.X + (o + 16 + r) * LD + o + 16 + m);
-      const float av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float2 x = *reinterpret_cast<const float2*>(tmp + (m + u) * LD + c);
-        s0 = fmaf(-av[u], x.x, s0);
-        s1 = fmaf(-av[u], x.y, s1);
-      }
-    }
-    *reinterpret_cast<float2*>(sm.X + (o + 16 + r) * LD + o + c) = make_float2(s0, s1);
+  // ---- 16 -> 32: two pairs of blocks, a warp for 8 columns of one. N21 X1 goes into the first
+  //      diagonal block of N, done with; X1 is zero above its diagonal
+  float s4[4];
+  if (warp < 4) {
+    const int o = 32 * (warp >> 1), c = 8 * (warp & 1);
+    float* tmp = sm.N + o * LD + o + c;
+    product16x8(s4, sm.N + (o + 16) * LD + o, sm.X + o * LD + o + c, c, 16);
+    store16x8(tmp, s4, 1.f);
+    __syncwarp();
+    product16x8(s4, sm.X + (o + 16) * LD + o + 16, tmp, 0, 16);
+    store16x8(sm.X + (o + 16) * LD + o + c, s4, -1.f);
   }
   __syncthreads();
-  // ---- 32 -> 64. N21 X1 (into the first 32 x 32 of N, done with): a warp owns 4 columns, a
-  //      lane a row; X1 is zero above its diagonal
+  // ---- 32 -> 64, the same with two warps, of 16 rows each, for 8 columns
   {
-    const int c = 4 * warp;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-    for (int m = c; m < 32; m += 4) {
-      const float4 a = at4(sm.N + (32 + lane) * LD + m);
-      axpy4(s, a.x, at4(sm.X + m * LD + c));
-      axpy4(s, a.y, at4(sm.X + (m + 1) * LD + c));
-      axpy4(s, a.z, at4(sm.X + (m + 2) * LD + c));
-      axpy4(s, a.w, at4(sm.X + (m + 3) * LD + c));
-    }
-    *reinterpret_cast<float4*>(sm.N + lane * LD + c) = make_float4(s[0], s[1], s[2], s[3]);
-  }
-  __syncthreads();
-  {  // -X2 tmp: a warp owns 4 rows, X2 is zero right of its diagonal
-    const int r = 4 * warp + (lane >> 3), c = 4 * (lane & 7);
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-    for (int m = 0; m < 4 * warp + 4; m += 4) {
-      const float4 a = at4(sm.X + (32 + r) * LD + 32 + m);
-      axpy4(s, -a.x, at4(sm.N + m * LD + c));
-      axpy4(s, -a.y, at4(sm.N + (m + 1) * LD + c));
-      axpy4(s, -a.z, at4(sm.N + (m + 2) * LD + c));
-      axpy4(s, -a.w, at4(sm.N + (m + 3) * LD + c));
-    }
-    *reinterpret_cast<float4*>(sm.X + (32 + r) * LD + c) = make_float4(s[0], s[1], s[2], s[3]);
+    const int c = 8 * (warp >> 1), r = 16 * (warp & 1);
+    product16x8(s4, sm.N + (32 + r) * LD, sm.X + c, c, 32);
+    store16x8(sm.N + r * LD + c, s4, 1.f);
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
+    product16x8(s4, sm.X + (32 + r) * LD + 32, sm.N + c, 0, r + 16);
+    store16x8(sm.X + (32 + r) * LD + c, s4, -1.f);
   }
   __syncthreads();
   // ---- operands: a lane takes 4 columns, 8 lanes half a row (float4 loads free of bank
