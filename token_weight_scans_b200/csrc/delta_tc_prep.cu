@@ -11,9 +11,10 @@
 // matrices T0 diag(G), diag(w) T and P then multiply K (or T) on the tensor core; K is
 // exact in bf16, so the gates ride on the other operand.
 //
-// beta = 0 leaves T0's column zero, but T's column j needs A's: columns are computed with
-// beta at least 2^-60 in size, and T_ij = beta_i T0_ij / beta_j recovers them; T0 itself is
-// off by 2^-60.
+// The backward's T follows from T0 as T_ij = beta_i T0_ij / beta_j, so
+//   Wb_j = (1 / beta_j) sum_i T0_ij beta_i w_i k_i,   PT = (P diag(beta)) (T0 diag(1 / beta)).
+// beta = 0 would leave T0's column zero where T's column j needs A's: beta is taken at least
+// 2^-60 in size here, which puts T0, Pb and W off by no more than that.
 //
 // Waits: the in-flight TMA stores only read shared memory, so the CTA waits for that read
 // and not for their completion; the kernel boundary orders them for the walk.
@@ -38,7 +39,8 @@ constexpr int LD = 68;        // row stride (floats) of the 64 x 64 float32 matr
 constexpr uint32_t kCols = 128;  // K K^T | Q K^T (64), then PT (64), then W | Wb
 constexpr float kTiny = 0x1p-60f;
 
-// Tiles live where something dead was: P and diag(w) T over Q, T over the remainder of T0 diag(G)
+// Tiles live where something dead was: P diag(beta) and diag(beta w) T0 over Q, T0 diag(1 / beta)
+// over the remainder of T0 diag(G)
 // (with both, SPLIT and BACK, P has a place of its own), at the end W over Q, Wb over K, the
 // remainder of W over T0 diag(G).
 template <bool OWN_P>
@@ -52,9 +54,9 @@ struct PrepSmem {
   uint8_t P[OWN_P ? TILE : 16];
   float X[C * LD];             // T0
   // per token: with m in the middle of the chunk M_ij = ra_i ca_j where that stays in range
-  // (fac); cN = ca beta (at least kTiny), cP = scale ca
+  // (fac); bt is beta, at least kTiny in size: cN = ca bt, cP = scale ca bt, wb = w bt, rb = 1 / bt
   float ra[C], cN[C], cP[C];
-  float Lh[C], Ll[C], be[C], G[C], w[C], rb[C];
+  float Lh[C], Ll[C], G[C], wb[C], rb[C];
   int seg[C];
   int fac;
   uint64_t full, mma;
@@ -132,6 +134,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
                                                            const __grid_constant__ CUtensorMap tmW,
                                                            const __grid_constant__ CUtensorMap tmWlo,
                                                            const __grid_constant__ CUtensorMap tmWb,
+                                                           const __grid_constant__ CUtensorMap tmPb,
+                                                           const __grid_constant__ CUtensorMap tmPT,
                                                            PrepParams p) {
   extern __shared__ uint8_t smem_raw[];
   constexpr bool own_p = SPLIT && BACK;
@@ -169,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
   const uint32_t sP = own_p ? smem_u32(sm.P) : sQ;
   uint8_t *const pTw = sm.Q + TILE, *const pTt = own_p ? sm.Q : sm.Tg[1];
   const uint32_t sTw = smem_u32(pTw), sTt = smem_u32(pTt);
+  const uint32_t sPT = own_p ? sP : sTt;  // PT over an operand of its own product
   if (tid == 0) {
     mbar_wait(&sm.full, 0, wc, W_PREP_LOAD);
     const uint32_t id = idesc_bf16(64, 64, false, false);
@@ -199,15 +204,14 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
       const float ca = fac ? expf(-x) : 1.f;
       sm.ra[i] = fac ? expf(x) : 1.f;
       sm.cN[i] = ca * bt;
-      sm.cP[i] = ca * p.scale;
+      sm.cP[i] = ca * bt * p.scale;
       sm.Lh[i] = g.Lh[k];
       sm.Ll[i] = g.Ll[k];
       sm.seg[i] = g.seg[k];
-      sm.be[i] = be;
       sm.rb[i] = 1.f / bt;
       const float G = gate_G(g, k), w = gate_w(g, k);
       sm.G[i] = G;
-      sm.w[i] = w;
+      sm.wb[i] = w * bt;
       gb->bw[i] = be * w;
       gb->q[i] = p.scale * G;
       gb->bG[i] = -be * G;
@@ -259,25 +263,27 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
         *reinterpret_cast<float4*>(sm.N + i * LD + 32 * hh + e) =
             make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
     } else {
-      uint4* Pg = reinterpret_cast<uint4*>(p.m.Pb + (((size_t)bh * N + n) * C + i) * C + 32 * hh);
 #pragma unroll
       for (int cc = 0; cc < 4; ++cc) {
         const float* x = v + 8 * cc;
-        if (BACK)
-          st_shared_v4(sP + sw128_off(i, 4 * hh + cc), pack_bf16(x[0], x[1]),
-                       pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-        const float4 b0 = at4(sm.be + 32 * hh + 8 * cc), b1 = at4(sm.be + 32 * hh + 8 * cc + 4);
-        Pg[cc] = make_uint4(pack_bf16(x[0] * b0.x, x[1] * b0.y), pack_bf16(x[2] * b0.z, x[3] * b0.w),
-                            pack_bf16(x[4] * b1.x, x[5] * b1.y), pack_bf16(x[6] * b1.z, x[7] * b1.w));
+        st_shared_v4(sP + sw128_off(i, 4 * hh + cc), pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                     pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
       }
     }
   }
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
-  // ---- T0: 16 x 16 diagonal blocks, a lane per column; the other warps clear what is right
-  //      of them
-  if (warp < 4) {
-    const int o = 16 * warp, c = lane & 15;
+  if (tid == 128) {  // a warp with little to do next
+    tma_store_3d(&tmPb, own_p ? sm.P : sm.Q, 0, t0, bh);
+    tma_store_commit();
+    tma_store_wait_read();
+  }
+  __syncwarp();
+  // ---- T0: 16 x 16 diagonal blocks, two per warp, a lane per column; other warps clear what
+  //      is right of them
+  if (warp < 2) {
+    const int o = 32 * warp + (lane & 16), c = lane & 15;
     float x[16];
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
@@ -293,11 +299,9 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
       }
       x[r] = s;
     }
-    if (lane < 16) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) sm.X[(o + r) * LD + o + c] = x[r];
-    }
-  } else {
+    for (int r = 0; r < 16; ++r) sm.X[(o + r) * LD + o + c] = x[r];
+  } else if (warp >= 4) {
     const int r = (tid - 128) >> 1, c1 = 32 * (tid & 1);  // row r, 32 columns
     for (int c = max(c1, (r & ~15) + 16); c < c1 + 32; c += 4)
       *reinterpret_cast<float4*>(sm.X + r * LD + c) = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -350,13 +354,12 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
         *reinterpret_cast<uint2*>(sm.Tg[1] + off) =
             make_uint2(pack_lo(g.x, g.y, gh.x), pack_lo(g.z, g.w, gh.y));
       }
-      if (BACK) {  // T_ij = beta_i T0_ij / beta_j below the diagonal
-        const float wr = sm.w[r], br = sm.be[r];
-        const float4 t = make_float4(c == r ? 1.f : br * x.x * rb.x, c + 1 == r ? 1.f : br * x.y * rb.y,
-                                     c + 2 == r ? 1.f : br * x.z * rb.z, c + 3 == r ? 1.f : br * x.w * rb.w);
+      if (BACK) {
+        const float wr = sm.wb[r];
         *reinterpret_cast<uint2*>(pTw + off) =
-            make_uint2(pack_bf16(wr * t.x, wr * t.y), pack_bf16(wr * t.z, wr * t.w));
-        *reinterpret_cast<uint2*>(pTt + off) = make_uint2(pack_bf16(t.x, t.y), pack_bf16(t.z, t.w));
+            make_uint2(pack_bf16(wr * x.x, wr * x.y), pack_bf16(wr * x.z, wr * x.w));
+        *reinterpret_cast<uint2*>(pTt + off) =
+            make_uint2(pack_bf16(x.x * rb.x, x.y * rb.y), pack_bf16(x.z * rb.z, x.w * rb.w));
       }
     }
   }
@@ -364,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
   tc_fence_before();
   __syncthreads();
   uint32_t phase = 1;
-  if (BACK) {  // PT = P T
+  if (BACK) {  // PT = (P diag(bt)) (T0 diag(1 / bt))
     if (tid == 0) {
       tc_fence_after();
       const uint32_t id_pt = idesc_bf16(64, 64, false, true);
@@ -383,16 +386,20 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
     tmem_ld32(tb + lo + 32 * hh, v);
     tmem_ld_wait();
     if (!isP) {
-      uint4* out = reinterpret_cast<uint4*>(p.m.PT + (((size_t)bh * N + n) * C + i) * C + 32 * hh);
 #pragma unroll
       for (int cc = 0; cc < 4; ++cc) {
         const float* x = v + 8 * cc;
-        out[cc] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                             pack_bf16(x[6], x[7]));
+        st_shared_v4(sPT + sw128_off(i, 4 * hh + cc), pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                     pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
       }
     }
+    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
+    if (tid == 128) {
+      tma_store_3d(&tmPT, own_p ? sm.P : sm.Tg[1], 0, t0, bh);
+      tma_store_commit();
+    }
   }
   if (tid == 0) {
     tc_fence_after();
@@ -418,6 +425,11 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
     float v[32];
     tmem_ld32(tb + lo + 64 * hh + 32 * g, v);
     tmem_ld_wait();
+    if (BACK && isP) {
+      const float rb = sm.rb[i];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] *= rb;
+    }
     const uint32_t dst = (isP ? sK : sQ) + hh * TILE;
 #pragma unroll
     for (int cc = 0; cc < 4; ++cc) {
@@ -444,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
     }
     tma_store_commit();
   }
-  if (tid == 0) tma_store_wait_read();  // the CTA's shared memory may go once it has been read
+  if (tid == 0 || tid == 128) tma_store_wait_read();  // the CTA's shared memory may go once it has been read
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tb, kCols);
@@ -452,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
 }
 
 template <bool SPLIT, bool BACK>
-static cudaError_t launch(const CUtensorMap (&m)[5], const PrepParams& p, unsigned grid, cudaStream_t st) {
+static cudaError_t launch(const CUtensorMap (&m)[7], const PrepParams& p, unsigned grid, cudaStream_t st) {
   static std::atomic<uint64_t> set{0};  // devices whose opt-in is done
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
@@ -464,7 +476,8 @@ static cudaError_t launch(const CUtensorMap (&m)[5], const PrepParams& p, unsign
     if (e != cudaSuccess) return e;
     set.fetch_or(bit);
   }
-  prep_kernel<SPLIT, BACK><<<grid, kThreads, smem_bytes<SPLIT && BACK>(), st>>>(m[0], m[1], m[2], m[3], m[4], p);
+  prep_kernel<SPLIT, BACK><<<grid, kThreads, smem_bytes<SPLIT && BACK>(), st>>>(m[0], m[1], m[2], m[3], m[4], m[5],
+                                                                              m[6], p);
   count_launch();
   return cudaGetLastError();
 }
@@ -473,12 +486,14 @@ cudaError_t launch_prep(const Args& a, bool split, cudaStream_t st) {
   const Dims& d = a.d;
   const uint64_t N = chunks(d.T), kh = (uint64_t)d.B * d.Hk, bh = d.BH();
   const bool back = a.m.Wb != nullptr;
-  CUtensorMap m[5];
+  CUtensorMap m[7];
   using gradlev::tc::make_map_bf16_3d;
   if (!make_map_bf16_3d(&m[0], a.k, d.dk, d.T, kh, C) || !make_map_bf16_3d(&m[1], a.q, d.dk, d.T, kh, C) ||
       !make_map_bf16_3d(&m[2], a.m.W, 128, N * C, bh, C) ||
       !make_map_bf16_3d(&m[3], split ? a.m.Wlo : a.m.W, 128, N * C, bh, C) ||
-      !make_map_bf16_3d(&m[4], back ? a.m.Wb : a.m.W, 128, N * C, bh, C))
+      !make_map_bf16_3d(&m[4], back ? a.m.Wb : a.m.W, 128, N * C, bh, C) ||
+      !make_map_bf16_3d(&m[5], a.m.Pb, C, N * C, bh, C) ||
+      !make_map_bf16_3d(&m[6], back ? a.m.PT : a.m.Pb, C, N * C, bh, C))
     return cudaErrorInvalidValue;
   const PrepParams p{d, a.beta, a.log_alpha, a.scale, a.status, a.timeout_ns, a.m};
   const unsigned grid = (unsigned)(N * bh);
