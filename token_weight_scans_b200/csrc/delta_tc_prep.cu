@@ -38,11 +38,12 @@ constexpr int kThreads = 256;
 constexpr int LD = 68;        // row stride (floats) of the 64 x 64 float32 matrices: 16-byte rows
 constexpr uint32_t kCols = 128;  // K K^T | Q K^T (64), then PT (64), then W | Wb
 constexpr float kTiny = 0x1p-60f;
+constexpr int kLoader = 128;  // the thread that loads K and Q, and stores P and PT
 
 // Tiles live where something dead was: P diag(beta) and diag(beta w) T0 over Q, T0 diag(1 / beta)
-// over the remainder of T0 diag(G)
-// (with both, SPLIT and BACK, P has a place of its own), at the end W over Q, Wb over K, the
-// remainder of W over T0 diag(G).
+// over the remainder of T0 diag(G) (with both, SPLIT and BACK, P has a place of its own), PT over
+// its operand in Q. At the end W, Wb and the remainder of W go over T0, T0 diag(G) and P, so that
+// K and Q are free for the next chunk's loads as soon as the last product is done.
 template <bool OWN_P>
 struct PrepSmem {
   uint8_t K[2 * TILE];         // k-blocks: 64 token rows x 128 B
@@ -51,8 +52,8 @@ struct PrepSmem {
     float N[C * LD];           // A diag(beta); parts that are done with hold the products' halves
     uint8_t Tg[2][TILE];       // T0 diag(G) in bf16 and its remainder
   };
-  uint8_t P[OWN_P ? TILE : 16];
   float X[C * LD];             // T0
+  uint8_t P[OWN_P ? 2 * TILE : 16];
   // per token: with m in the middle of the chunk M_ij = ra_i ca_j where that stays in range
   // (fac); bt is beta, at least kTiny in size: cN = ca bt, cP = scale ca bt, wb = w bt, rb = 1 / bt
   float ra[C], cN[C], cP[C];
@@ -67,7 +68,7 @@ template <bool OWN_P> constexpr size_t smem_bytes() { return sizeof(PrepSmem<OWN
 static_assert(3 * (smem_bytes<false>() + 1024) <= 228 * 1024, "three CTAs per SM");
 static_assert(2 * (smem_bytes<true>() + 1024) <= 228 * 1024, "two CTAs per SM");
 
-enum : uint32_t { W_PREP_LOAD = 0x801, W_PREP_MMA };
+enum : uint32_t { W_PREP_LOAD = 0x801, W_PREP_MMA, W_PREP_DRAIN };
 
 struct PrepParams {
   Dims d;
@@ -143,23 +144,30 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
   Smem& sm = *reinterpret_cast<Smem*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int N = chunks(p.d.T), bh = blockIdx.x / N, n = blockIdx.x - bh * N;
-  const int b = bh / p.d.H, h = bh - b * p.d.H;
-  const int kh = b * p.d.Hk + h / (p.d.H / p.d.Hk);
-  const int t0 = n * C;
+  const int N = chunks(p.d.T);
   const WaitCtx wc{&sm.abort, p.status, p.timeout_ns};
-  RawGates raw{};
-  if (warp == 2) raw = load_gates(p.beta, p.log_alpha, (size_t)bh * p.d.T, t0, p.d.T);
-  if (tid == 0) {
-    sm.abort = 0;
-    mbar_init(&sm.full, 1);
-    mbar_init(&sm.mma, 1);
-    fence_mbar_init();
+  const unsigned total = (unsigned)((size_t)p.d.B * p.d.H * N);
+  auto load_kq = [&](unsigned id) {  // one thread
+    const int bh = id / N, t0 = (id - bh * N) * C, b = bh / p.d.H, h = bh - b * p.d.H;
+    const int kh = b * p.d.Hk + h / (p.d.H / p.d.Hk);
     mbar_arrive_expect_tx(&sm.full, 4 * TILE);
     tma_load_3d(sm.K, &tmK, &sm.full, 0, t0, kh);
     tma_load_3d(sm.K + TILE, &tmK, &sm.full, 64, t0, kh);
     tma_load_3d(sm.Q, &tmQ, &sm.full, 0, t0, kh);
     tma_load_3d(sm.Q + TILE, &tmQ, &sm.full, 64, t0, kh);
+  };
+  RawGates raw{};
+  auto load_raw = [&](unsigned id) {  // warp 2
+    const int bh = id / N;
+    raw = load_gates(p.beta, p.log_alpha, (size_t)bh * p.d.T, (id - bh * N) * C, p.d.T);
+  };
+  if (warp == 2) load_raw(blockIdx.x);
+  if (tid == kLoader) {
+    sm.abort = 0;
+    mbar_init(&sm.full, 1);
+    mbar_init(&sm.mma, 1);
+    fence_mbar_init();
+    load_kq(blockIdx.x);
   }
   if (warp == 1) {
     tmem_alloc(&sm.tmem_base, kCols);
@@ -173,9 +181,16 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
   const uint32_t sP = own_p ? smem_u32(sm.P) : sQ;
   uint8_t *const pTw = sm.Q + TILE, *const pTt = own_p ? sm.Q : sm.Tg[1];
   const uint32_t sTw = smem_u32(pTw), sTt = smem_u32(pTt);
-  const uint32_t sPT = own_p ? sP : sTt;  // PT over an operand of its own product
+  // places of the results (all 16 KB)
+  uint8_t *const oX = reinterpret_cast<uint8_t*>(sm.X), *const oW = own_p ? sm.P : BACK ? sm.Tg[0] : oX;
+  uint8_t *const oWb = oX, *const oWlo = sm.Tg[0];
+  uint32_t phase = 0, full = 0, loads = 0;  // loads: after the first, of the loading thread
+  for (unsigned id = blockIdx.x; id < total; id += gridDim.x, full ^= 1) {
+  const int bh = id / N, n = id - bh * N, t0 = n * C;
   if (tid == 0) {
-    mbar_wait(&sm.full, 0, wc, W_PREP_LOAD);
+    tma_store_wait_read();  // the last chunk's results
+    mbar_wait(&sm.full, full, wc, W_PREP_LOAD);
+    tc_fence_after();
     const uint32_t id = idesc_bf16(64, 64, false, false);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {
@@ -189,6 +204,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
   __syncwarp();
   if (warp == 2) {
     const GatePair g = chunk_gates(raw);
+    if (id + gridDim.x < total) load_raw(id + gridDim.x);
     const float Lm = __shfl_sync(0xffffffffu, g.Lh[0], 31), Ll = __shfl_sync(0xffffffffu, g.Ll[0], 31);
     const bool fac = g.seg_end == 0 && g.Lend > -80.f;
     GateBlock* gb = reinterpret_cast<GateBlock*>(p.m.gates) + (size_t)bh * N + n;
@@ -221,7 +237,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
     }
     if (lane == 0) sm.fac = fac;
   }
-  mbar_wait(&sm.mma, 0, wc, W_PREP_MMA);
+  mbar_wait(&sm.mma, phase, wc, W_PREP_MMA);
+  phase ^= 1;
   __syncthreads();  // the gates are there
   tc_fence_after();
   // Lane l < 16 of quadrant q holds row i = 16 q + l of K K^T, lane l + 16 that of Q K^T;
@@ -274,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
-  if (tid == 128) {  // a warp with little to do next
+  if (tid == kLoader) {  // in a warp with little to do next
     tma_store_3d(&tmPb, own_p ? sm.P : sm.Q, 0, t0, bh);
     tma_store_commit();
     tma_store_wait_read();
@@ -366,7 +383,6 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
-  uint32_t phase = 1;
   if (BACK) {  // PT = (P diag(bt)) (T0 diag(1 / bt))
     if (tid == 0) {
       tc_fence_after();
@@ -389,15 +405,15 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
 #pragma unroll
       for (int cc = 0; cc < 4; ++cc) {
         const float* x = v + 8 * cc;
-        st_shared_v4(sPT + sw128_off(i, 4 * hh + cc), pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+        st_shared_v4(sQ + sw128_off(i, 4 * hh + cc), pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
                      pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
       }
     }
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
-    if (tid == 128) {
-      tma_store_3d(&tmPT, own_p ? sm.P : sm.Tg[1], 0, t0, bh);
+    if (tid == kLoader) {
+      tma_store_3d(&tmPT, sm.Q, 0, t0, bh);
       tma_store_commit();
     }
   }
@@ -415,11 +431,16 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
     umma_commit(&sm.mma);
   }
   __syncwarp();
-  mbar_wait(&sm.mma, phase, wc, W_PREP_MMA);
+  const bool done = mbar_wait(&sm.mma, phase, wc, W_PREP_MMA);
+  phase ^= 1;
+  if (tid == kLoader && done && id + gridDim.x < total) {
+    tma_store_wait_read();  // PT
+    load_kq(id + gridDim.x);
+    ++loads;
+  }
   __syncwarp();
   tc_fence_after();
-  // W (lanes < 16) and Wb (lanes >= 16) to bf16, columns [64 hh, 64 hh + 64); staged over Q
-  // (W), K (Wb) and Tg (the remainder of W), which every product has read
+  // W (lanes < 16) and Wb (lanes >= 16) to bf16, columns [64 hh, 64 hh + 64)
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     float v[32];
@@ -430,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
 #pragma unroll
       for (int e = 0; e < 32; ++e) v[e] *= rb;
     }
-    const uint32_t dst = (isP ? sK : sQ) + hh * TILE;
+    const uint32_t dst = smem_u32(isP ? oWb : oW) + hh * TILE;
 #pragma unroll
     for (int cc = 0; cc < 4; ++cc) {
       uint32_t hi[4], low[4];
@@ -441,22 +462,26 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
       }
       const uint32_t off = sw128_off(i, 4 * g + cc);
       if (BACK || !isP) st_shared_v4(dst + off, hi[0], hi[1], hi[2], hi[3]);
-      if (SPLIT && !isP) st_shared_v4(sTg + hh * TILE + off, low[0], low[1], low[2], low[3]);
+      if (SPLIT && !isP) st_shared_v4(smem_u32(oWlo) + hh * TILE + off, low[0], low[1], low[2], low[3]);
     }
     __syncwarp();
   }
   fence_proxy_async_smem();
   tc_fence_before();
-  __syncthreads();
+  const bool stop = __syncthreads_or(*reinterpret_cast<volatile int*>(&sm.abort));
   if (tid == 0) {
     for (int kb = 0; kb < 2; ++kb) {
-      tma_store_3d(&tmW, sm.Q + kb * TILE, 64 * kb, t0, bh);
-      if (SPLIT) tma_store_3d(&tmWlo, sm.Tg[kb], 64 * kb, t0, bh);
-      if (BACK) tma_store_3d(&tmWb, sm.K + kb * TILE, 64 * kb, t0, bh);
+      tma_store_3d(&tmW, oW + kb * TILE, 64 * kb, t0, bh);
+      if (SPLIT) tma_store_3d(&tmWlo, oWlo + kb * TILE, 64 * kb, t0, bh);
+      if (BACK) tma_store_3d(&tmWb, oWb + kb * TILE, 64 * kb, t0, bh);
     }
     tma_store_commit();
   }
-  if (tid == 0 || tid == 128) tma_store_wait_read();  // the CTA's shared memory may go once it has been read
+  if (stop) break;
+  }
+  if (tid == kLoader) mbar_drain(&sm.full, loads & 1, wc, W_PREP_DRAIN);
+  if (tid == 0 || tid == kLoader) tma_store_wait_read();  // shared memory may go once it is read
+  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tb, kCols);
@@ -476,7 +501,8 @@ static cudaError_t launch(const CUtensorMap (&m)[7], const PrepParams& p, unsign
     if (e != cudaSuccess) return e;
     set.fetch_or(bit);
   }
-  prep_kernel<SPLIT, BACK><<<grid, kThreads, smem_bytes<SPLIT && BACK>(), st>>>(m[0], m[1], m[2], m[3], m[4], m[5],
+  const unsigned most = 148 * (SPLIT && BACK ? 2 : 3);
+  prep_kernel<SPLIT, BACK><<<grid < most ? grid : most, kThreads, smem_bytes<SPLIT && BACK>(), st>>>(m[0], m[1], m[2], m[3], m[4], m[5],
                                                                               m[6], p);
   count_launch();
   return cudaGetLastError();
