@@ -179,8 +179,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
   const uint32_t tb = sm.tmem_base;
   const uint32_t sK = smem_u32(sm.K), sQ = smem_u32(sm.Q), sTg = smem_u32(sm.Tg[0]);
   const uint32_t sP = own_p ? smem_u32(sm.P) : sQ;
-  uint8_t *const pTw = sm.Q + TILE, *const pTt = own_p ? sm.Q : sm.Tg[1];
-  const uint32_t sTw = smem_u32(pTw), sTt = smem_u32(pTt);
+  const uint32_t sTw = sQ + TILE, sTt = own_p ? sQ : sTg + TILE;
   // places of the results (all 16 KB)
   uint8_t *const oX = reinterpret_cast<uint8_t*>(sm.X), *const oW = own_p ? sm.P : BACK ? sm.Tg[0] : oX;
   uint8_t *const oWb = oX, *const oWlo = sm.Tg[0];
@@ -294,7 +293,6 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
   if (tid == kLoader) {  // in a warp with little to do next
     tma_store_3d(&tmPb, own_p ? sm.P : sm.Q, 0, t0, bh);
     tma_store_commit();
-    tma_store_wait_read();
   }
   __syncwarp();
   // ---- T0: 16 x 16 diagonal blocks, two per warp, a lane per column; other warps clear what
@@ -347,39 +345,55 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
     store16x8(sm.X + (32 + r) * LD + c, s4, -1.f);
   }
   __syncthreads();
-  // ---- operands: a lane takes 4 columns, 8 lanes half a row (float4 loads free of bank
-  //      conflicts, 8-byte stores)
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int c = 32 * k + 4 * (tid & 7);
-    const float4 G = at4(sm.G + c);
-    const float4 rb = BACK ? at4(sm.rb + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+  // ---- operands: a lane takes 8 columns of two rows, 8 lanes a row. Lanes 4 to 7 load their
+  //      second half first, so that the loads have no bank conflicts.
+  {
+    const int c = 8 * (tid & 7), sw = tid & 4;
+    auto at8 = [&](const float* p, float (&x)[8]) {
+      const float4 a = at4(p + sw), b = at4(p + (4 - sw));
+      x[0] = sw ? b.x : a.x, x[1] = sw ? b.y : a.y, x[2] = sw ? b.z : a.z, x[3] = sw ? b.w : a.w;
+      x[4] = sw ? a.x : b.x, x[5] = sw ? a.y : b.y, x[6] = sw ? a.z : b.z, x[7] = sw ? a.w : b.w;
+    };
+    auto pack8 = [&](const float (&x)[8]) {
+      return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                        pack_bf16(x[6], x[7]));
+    };
+    auto rest8 = [&](const float (&x)[8], const uint4& h) {
+      return make_uint4(pack_lo(x[0], x[1], h.x), pack_lo(x[2], x[3], h.y), pack_lo(x[4], x[5], h.z),
+                        pack_lo(x[6], x[7], h.w));
+    };
+    auto put = [&](uint32_t dst, const uint4& v) { st_shared_v4(dst, v.x, v.y, v.z, v.w); };
+    float G[8], rb[8];
+    at8(sm.G + c, G);
+    if (BACK) at8(sm.rb + c, rb);
 #pragma unroll
     for (int rr = 0; rr < 2; ++rr) {
       const int r = (tid >> 3) + 32 * rr;
-      const float4 x = at4(sm.X + r * LD + c);
-      const uint32_t off = sw128_off(r, c >> 3) + (c & 4) * 2;
+      float x[8], y[8];
+      at8(sm.X + r * LD + c, x);
+      const uint32_t off = sw128_off(r, c >> 3);
       const size_t at = (((size_t)bh * N + n) * C + r) * C + c;
-      const uint2 hi = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
-      const float4 g = make_float4(-x.x * G.x, -x.y * G.y, -x.z * G.z, -x.w * G.w);
-      const uint2 gh = make_uint2(pack_bf16(g.x, g.y), pack_bf16(g.z, g.w));
-      *reinterpret_cast<uint2*>(p.m.T0 + at) = hi;
-      *reinterpret_cast<uint2*>(sm.Tg[0] + off) = gh;
-      if (SPLIT) {
-        *reinterpret_cast<uint2*>(p.m.T0lo + at) =
-            make_uint2(pack_lo(x.x, x.y, hi.x), pack_lo(x.z, x.w, hi.y));
-        *reinterpret_cast<uint2*>(sm.Tg[1] + off) =
-            make_uint2(pack_lo(g.x, g.y, gh.x), pack_lo(g.z, g.w, gh.y));
-      }
+      const uint4 hi = pack8(x);
+      *reinterpret_cast<uint4*>(p.m.T0 + at) = hi;
+      if (SPLIT) *reinterpret_cast<uint4*>(p.m.T0lo + at) = rest8(x, hi);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = -x[e] * G[e];
+      const uint4 gh = pack8(y);
+      put(sTg + off, gh);
+      if (SPLIT) put(sTg + TILE + off, rest8(y, gh));
       if (BACK) {
         const float wr = sm.wb[r];
-        *reinterpret_cast<uint2*>(pTw + off) =
-            make_uint2(pack_bf16(wr * x.x, wr * x.y), pack_bf16(wr * x.z, wr * x.w));
-        *reinterpret_cast<uint2*>(pTt + off) =
-            make_uint2(pack_bf16(x.x * rb.x, x.y * rb.y), pack_bf16(x.z * rb.z, x.w * rb.w));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = wr * x[e];
+        put(sTw + off, pack8(y));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = x[e] * rb[e];
+        put(sTt + off, pack8(y));
       }
     }
   }
+  if (tid == kLoader) tma_store_wait_read();  // P
+  __syncwarp();
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
