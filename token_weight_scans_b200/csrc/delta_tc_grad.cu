@@ -1,6 +1,6 @@
 // Tensor-core gated delta rule: the gradients of q, k and the gates of one chunk of 64
 // tokens and one key head, from the states at the chunk's start, their gradients at its
-// end, D and E (delta.h); two CTAs per SM. The value heads that share the key head are
+// end, D and E (delta.h); two persistent CTAs per SM. The value heads that share the key head are
 // taken in turn and add up in registers, so nothing is added through memory.
 //
 // Products of one value head (M = 64 tokens each; two share their TMEM columns, one in the
@@ -41,7 +41,7 @@ struct GradSmem {
   uint8_t D[TILE], E[TILE];                  // D^T, E^T: 64 rows of d_v x 64 tokens
   uint8_t S[2 * TILE], dS[2 * TILE];         // 64 rows of d_v x 128
   uint8_t X[TILE], Yn[TILE];
-  GateBlock g;
+  GateBlock gates[2];                        // this head's and the next one's
   float Lh[C], Ll[C];                        // where a reset or strong decays rule out g.fac
   int seg[C];
   float xs[2][C], ps[2][C], zs[2][C];        // per column half
@@ -53,7 +53,7 @@ struct GradSmem {
 constexpr size_t kSmem = sizeof(GradSmem) + 1024;
 static_assert(2 * kSmem <= 227 * 1024, "two CTAs per SM");
 
-enum : uint32_t { W_G_KQ = 0xa01, W_G_FULL, W_G_MMA };
+enum : uint32_t { W_G_KQ = 0xa01, W_G_FULL, W_G_MMA, W_G_DRAIN };
 
 struct GradParams {
   Dims d;
@@ -64,22 +64,22 @@ struct GradParams {
   bf16 *dbeta, *dlog_alpha;
 };
 
-// 16 columns of a swizzled bf16 row
-__device__ __forceinline__ void row16(float (&x)[16], const uint8_t* tile, int r, int c8) {
+// 8 columns of a swizzled bf16 row
+__device__ __forceinline__ void row8(float (&x)[8], const uint8_t* tile, int r, int c8) {
+  const uint4 u = *reinterpret_cast<const uint4*>(tile + sw128_off(r, c8));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int cc = 0; cc < 2; ++cc) {
-    const uint4 u = *reinterpret_cast<const uint4*>(tile + sw128_off(r, c8 + cc));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[8 * cc + 2 * e] = bf16_lo(w[e]);
-      x[8 * cc + 2 * e + 1] = bf16_hi(w[e]);
-    }
+  for (int e = 0; e < 4; ++e) {
+    x[2 * e] = bf16_lo(w[e]);
+    x[2 * e + 1] = bf16_hi(w[e]);
   }
 }
 
 }  // namespace
 
+// GROUP: several value heads share a key head, and the sums in acc live across their products;
+// without, they begin after the state's products, which spares the registers until then.
+template <bool GROUP>
 __global__ void __launch_bounds__(kThreads, 2)
     grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmD,
@@ -94,37 +94,52 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t lo = (uint32_t)(32 * q) << 16;
   const int i = 16 * q + (lane & 15);              // token of this thread
   const bool up = lane >= 16;                      // upper lanes: k's side, lower: q's
-  const int T = p.d.T, N = chunks(T), kh = blockIdx.x / N, n = blockIdx.x - kh * N, t0 = n * C;
-  const int b = kh / p.d.Hk, grp = p.d.H / p.d.Hk;
+  const int T = p.d.T, N = chunks(T), grp = GROUP ? p.d.H / p.d.Hk : 1;
+  const unsigned total = (unsigned)((size_t)p.d.B * p.d.Hk * N);
   const WaitCtx wc{&sm.abort, p.status, p.timeout_ns};
-  // tiles of 64 columns of d_v (and, with the first, the gates); the first slice goes out
-  // before anything else
-  auto load_slice = [&](int bh, int sl) {
-    mbar_arrive_expect_tx(&sm.full, 7 * TILE + (sl == 0 ? (uint32_t)sizeof(GateBlock) : 0u));
-    if (sl == 0)
-      bulk_load(&sm.g, p.gates + ((size_t)bh * N + n) * (sizeof(GateBlock) / sizeof(float)),
-                sizeof(GateBlock), &sm.full);
-    tma_load_3d(sm.O, &tmO, &sm.full, 64 * sl, t0, bh);
-    tma_load_3d(sm.D, &tmD, &sm.full, 0, 64 * sl, bh * N + n);
-    tma_load_3d(sm.E, &tmE, &sm.full, 0, 64 * sl, bh * N + n);
-    for (int kb = 0; kb < 2; ++kb) {
-      tma_load_3d(sm.S + kb * TILE, &tmS, &sm.full, 64 * kb, 64 * sl, bh * N + n);
-      tma_load_3d(sm.dS + kb * TILE, &tmdS, &sm.full, 64 * kb, 64 * sl, bh * N + n);
+  uint32_t lfull = 0, lkq = 0;  // loads so far
+  auto first_head = [&](unsigned id) {
+    const int kh = id / N, b = kh / p.d.Hk;
+    return b * p.d.H + (kh - b * p.d.Hk) * grp;
+  };
+  // Tiles of 64 columns of d_v and, with the first, the gates: one copy for the first lane of each
+  // warp (issuing one takes about 100 cycles). A copy may land before thread 0 has announced it.
+  auto load_slice = [&](int bh, int n, int sl, GateBlock* gates) {
+    ++lfull;
+    if (lane != 0) return;
+    const int w = warp & 1;
+    if (warp == 0) {
+      mbar_arrive_expect_tx(&sm.full, 7 * TILE + (sl == 0 ? (uint32_t)sizeof(GateBlock) : 0u));
+      tma_load_3d(sm.O, &tmO, &sm.full, 64 * sl, n * C, bh);
+    } else if (warp == 1) {
+      tma_load_3d(sm.D, &tmD, &sm.full, 0, 64 * sl, bh * N + n);
+    } else if (warp == 2) {
+      tma_load_3d(sm.E, &tmE, &sm.full, 0, 64 * sl, bh * N + n);
+    } else if (warp == 3) {
+      if (sl == 0)
+        bulk_load(gates, p.gates + ((size_t)bh * N + n) * (sizeof(GateBlock) / sizeof(float)),
+                  sizeof(GateBlock), &sm.full);
+    } else if (warp < 6) {
+      tma_load_3d(sm.S + w * TILE, &tmS, &sm.full, 64 * w, 64 * sl, bh * N + n);
+    } else {
+      tma_load_3d(sm.dS + w * TILE, &tmdS, &sm.full, 64 * w, 64 * sl, bh * N + n);
     }
   };
-  const int bh0 = b * p.d.H + (kh - b * p.d.Hk) * grp;
+  // Tiles of Q (warps 4 and 5) and K (6 and 7)
+  uint8_t* const kq_tile = (warp < 6 ? sm.Q : sm.K) + (warp & 1) * TILE;
+  auto load_kq = [&](unsigned id) {
+    const int kh = id / N, t0 = (id - kh * N) * C;
+    ++lkq;
+    if (warp < 4 || lane != 0) return;
+    mbar_arrive_expect_tx(&sm.kq, TILE);
+    tma_load_3d(kq_tile, warp < 6 ? &tmQ : &tmK, &sm.kq, 64 * (warp & 1), t0, kh);
+  };
   if (tid == 0) {
     sm.abort = 0;
-    mbar_init(&sm.kq, 1);
+    mbar_init(&sm.kq, 4);
     mbar_init(&sm.full, 1);
     mbar_init(&sm.mma, 1);
     fence_mbar_init();
-    load_slice(bh0, 0);
-    mbar_arrive_expect_tx(&sm.kq, 4 * TILE);
-    for (int kb = 0; kb < 2; ++kb) {
-      tma_load_3d(sm.Q + kb * TILE, &tmQ, &sm.kq, 64 * kb, t0, kh);
-      tma_load_3d(sm.K + kb * TILE, &tmK, &sm.kq, 64 * kb, t0, kh);
-    }
   }
   const int nsl = (p.d.dv + 63) / 64;
   if (warp == 1) {
@@ -134,25 +149,34 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  load_slice(first_head(blockIdx.x), blockIdx.x % N, 0, &sm.gates[0]);
+  load_kq(blockIdx.x);
+  __syncwarp();
   const uint32_t tb = sm.tmem_base;
   const uint32_t sQ = smem_u32(sm.Q), sK = smem_u32(sm.K), sX = smem_u32(sm.X), sY = smem_u32(sm.Yn);
   const uint32_t id_f = idesc_bf16(64, 64, false, true), id_h = idesc_bf16(64, 64, true, true);
   const uint32_t id_t = idesc_bf16(64, 128, false, true);
   const uint32_t id_m = idesc_bf16(64, 128, true, true);
-  uint32_t nfull = 0, nmma = 0;  // phases so far
+  uint32_t nfull = 0, nmma = 0, nkq = 0, nhead = 0;  // phases and heads so far
 
+  bool stop = false;
+  for (unsigned id = blockIdx.x; id < total; id += gridDim.x) {
+  const int kh = id / N, n = id - kh * N, t0 = n * C, bh0 = first_head(id);
   float acc[64];
 #pragma unroll
   for (int e = 0; e < 64; ++e) acc[e] = 0.f;
 
-  for (int hv = 0; hv < grp; ++hv) {
+  for (int hv = 0; hv < grp; ++hv, ++nhead) {
     const int bh = bh0 + hv;
+    const GateBlock& g = sm.gates[nhead & 1];
     float ss = 0.f;  // <dS, S>
     for (int sl = 0; sl < nsl; ++sl) {
-      if (tid == 0 && (hv > 0 || sl > 0)) load_slice(bh, sl);
+      if (sl > 0) load_slice(bh, n, sl, nullptr);
+      __syncwarp();
       mbar_wait(&sm.full, nfull++ & 1, wc, W_G_FULL);
       __syncwarp();
       if (tid == 0) {
+        tc_fence_after();
         const uint32_t sO = smem_u32(sm.O), sD = smem_u32(sm.D), sE = smem_u32(sm.E);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
@@ -183,45 +207,54 @@ __global__ void __launch_bounds__(kThreads, 2)
           ss = fmaf(bf16_hi(xw[e]), bf16_hi(yw[e]), ss);
         }
       }
-      if (sl == 0 && warp == 2 && sm.g.fac == 0.f) {
-        const GatePair g = chunk_gates(load_gates(p.beta, p.log_alpha, (size_t)bh * T, t0, T));
+      if (sl == 0 && warp == 2 && g.fac == 0.f) {
+        const GatePair gp = chunk_gates(load_gates(p.beta, p.log_alpha, (size_t)bh * T, t0, T));
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          sm.Lh[lane + 32 * k] = g.Lh[k];
-          sm.Ll[lane + 32 * k] = g.Ll[k];
-          sm.seg[lane + 32 * k] = g.seg[k];
+          sm.Lh[lane + 32 * k] = gp.Lh[k];
+          sm.Ll[lane + 32 * k] = gp.Ll[k];
+          sm.seg[lane + 32 * k] = gp.seg[k];
         }
       }
       mbar_wait(&sm.mma, nmma++ & 1, wc, W_G_MMA);
-      __syncthreads();  // S and dS are read: the next slice may land
+      // S and dS are read: the next slice may land
+      stop = __syncthreads_or(*reinterpret_cast<volatile int*>(&sm.abort));
+      if (stop) break;
     }
+    if (stop) break;
+    // the first slice of the next head or chunk lands behind what follows
+    if (hv + 1 < grp)
+      load_slice(bh + 1, n, 0, &sm.gates[(nhead + 1) & 1]);
+    else if (id + gridDim.x < total)
+      load_slice(first_head(id + gridDim.x), (id + gridDim.x) % N, 0, &sm.gates[(nhead + 1) & 1]);
+    __syncwarp();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     if (lane == 0) sm.red[warp] = ss;
     tc_fence_after();
     // ---- X and Yn: lower lanes, columns [32 hh, 32 hh + 32)
-    const float rx = p.scale * sm.g.ra[i], ry = -sm.g.be[i] * sm.g.ra[i];
+    const float rx = p.scale * g.ra[i], ry = -g.be[i] * g.ra[i];
     float db = 0.f;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      float f[16], g[16];
+      float f[16], y[16];
       const int j0 = 32 * hh + 16 * hf;
       tmem_ld16(tb + COL_B + lo + j0, f);
-      tmem_ld16(tb + COL_B + 64 + lo + j0, g);
+      tmem_ld16(tb + COL_B + 64 + lo + j0, y);
       tmem_ld_wait();
       if (!up) {
         const int keep = i - j0;  // columns left of the diagonal
 #pragma unroll
-        for (int e = 0; e < 16; ++e) db = e == keep ? g[e] : db;
-        if (sm.g.fac != 0.f) {
+        for (int e = 0; e < 16; ++e) db = e == keep ? y[e] : db;
+        if (g.fac != 0.f) {
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
-            const float4 c = *reinterpret_cast<const float4*>(sm.g.cb + j0 + e);
+            const float4 c = *reinterpret_cast<const float4*>(g.cb + j0 + e);
             const float cv[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               f[e + u] = e + u <= keep ? f[e + u] * (rx * cv[u]) : 0.f;
-              g[e + u] = e + u < keep ? g[e + u] * (ry * cv[u]) : 0.f;
+              y[e + u] = e + u < keep ? y[e + u] * (ry * cv[u]) : 0.f;
             }
           }
         } else {  // a reset, or decays whose factors leave float32
@@ -230,20 +263,20 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int j = j0 + e;
-            const float m = sm.g.cb[j] * expf(fminf((Lh - sm.Lh[j]) + (Ll - sm.Ll[j]), 0.f));
+            const float m = g.cb[j] * expf(fminf((Lh - sm.Lh[j]) + (Ll - sm.Ll[j]), 0.f));
             const bool on = sm.seg[j] == seg;
             f[e] = on && e <= keep ? f[e] * (rx * m) : 0.f;
-            g[e] = on && e < keep ? g[e] * (ry * m) : 0.f;
+            y[e] = on && e < keep ? y[e] * (ry * m) : 0.f;
           }
         }
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           const uint32_t off = sw128_off(i, 4 * hh + 2 * hf + cc);
-          const float *x = f + 8 * cc, *y = g + 8 * cc;
+          const float *x = f + 8 * cc, *h = y + 8 * cc;
           st_shared_v4(sX + off, pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
                        pack_bf16(x[6], x[7]));
-          st_shared_v4(sY + off, pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
-                       pack_bf16(y[6], y[7]));
+          st_shared_v4(sY + off, pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]), pack_bf16(h[4], h[5]),
+                       pack_bf16(h[6], h[7]));
         }
       }
       __syncwarp();
@@ -251,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (!up && (i >> 5) == hh && t0 + i < T) p.dbeta[(size_t)bh * T + t0 + i] = __float2bfloat16_rn(db);
     fence_proxy_async_smem();
     tc_fence_before();
-    if (hv == 0) mbar_wait(&sm.kq, 0, wc, W_G_KQ);
+    if (hv == 0) mbar_wait(&sm.kq, nkq++ & 1, wc, W_G_KQ);
     __syncthreads();
     if (tid == 0) {
       tc_fence_after();
@@ -263,22 +296,22 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
     // ---- t (lower) and u (upper); z (upper)
     const uint8_t* mine = (up ? sm.K : sm.Q) + hh * TILE;
-    const float ca = up ? sm.g.bG[i] : sm.g.q[i], cz = up ? sm.g.bw[i] : 0.f;
+    const float ca = up ? g.bG[i] : g.q[i], cz = up ? g.bw[i] : 0.f;
     float xs = 0.f, ps = 0.f, zs = 0.f;
 #pragma unroll
-    for (int hf = 0; hf < 4; ++hf) {
-      float v[16], z[16], x[16];
-      tmem_ld16(tb + COL_A + lo + 64 * hh + 16 * hf, v);
-      tmem_ld16(tb + COL_B + lo + 64 * hh + 16 * hf, z);  // lower lanes: unused (xk in flight)
-      row16(x, mine, i, 2 * hf);
+    for (int cc = 0; cc < 8; ++cc) {
+      float v[8], z[8], x[8];
+      tmem_ld8(tb + COL_A + lo + 64 * hh + 8 * cc, v);
+      tmem_ld8(tb + COL_B + lo + 64 * hh + 8 * cc, z);  // lower lanes: unused (xk in flight)
+      row8(x, mine, i, cc);
       tmem_ld_wait();
       float dv = 0.f, dz = 0.f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
+      for (int e = 0; e < 8; ++e) {
         const float ze = up ? z[e] : 0.f;
         dv = fmaf(v[e], x[e], dv);
         dz = fmaf(ze, x[e], dz);
-        acc[16 * hf + e] = fmaf(ca, v[e], fmaf(cz, ze, acc[16 * hf + e]));
+        acc[8 * cc + e] = fmaf(ca, v[e], GROUP ? fmaf(cz, ze, acc[8 * cc + e]) : cz * ze);
       }
       xs = fmaf(ca, dv, xs);
       zs = fmaf(cz, dz, zs);
@@ -303,18 +336,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     // ---- xk (lower) and ka (upper); yk (upper)
 #pragma unroll
-    for (int hf = 0; hf < 4; ++hf) {
-      float v[16], z[16], x[16];
-      tmem_ld16(tb + COL_B + lo + 64 * hh + 16 * hf, v);
-      tmem_ld16(tb + COL_A + lo + 64 * hh + 16 * hf, z);  // lower lanes: t, used above
-      row16(x, mine, i, 2 * hf);
+    for (int cc = 0; cc < 8; ++cc) {
+      float v[8], z[8], x[8];
+      tmem_ld8(tb + COL_B + lo + 64 * hh + 8 * cc, v);
+      tmem_ld8(tb + COL_A + lo + 64 * hh + 8 * cc, z);  // lower lanes: t, used above
+      row8(x, mine, i, cc);
       tmem_ld_wait();
       float dot = 0.f;  // q.xk, or k.(yk - ka)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
+      for (int e = 0; e < 8; ++e) {
         const float ye = up ? z[e] : 0.f;
         dot = fmaf(up ? ye - v[e] : v[e], x[e], dot);
-        acc[16 * hf + e] += v[e] + ye;
+        acc[8 * cc + e] += v[e] + ye;
       }
       ps += dot;
     }
@@ -347,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       float gg = 0.f;
 #pragma unroll
       for (int w = 0; w < 8; ++w) gg += sm.red[w];
-      gg *= sm.g.GC;
+      gg *= g.GC;
       const float before = __shfl_up_sync(0xffffffffu, sz, 1);
       const float z_lt = lane == 0 ? 0.f : before;
       // no pair reaches across the chunk's first token: its sum is zero, not what rounding left
@@ -355,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const float after = __shfl_down_sync(0xffffffffu, sx + sp, 1);
       const float d0 = sx + pair0, d1 = (x1 + p1) + (lane == 31 ? 0.f : after);
       const size_t row = (size_t)bh * T + t0;
-      const bool plain = sm.g.fac != 0.f;  // no reset in the chunk
+      const bool plain = g.fac != 0.f;  // no reset in the chunk
       const bool r0 = !plain && sm.seg[j] != (j > 0 ? sm.seg[j - 1] : 0);
       const bool r1 = !plain && sm.seg[j + 1] != sm.seg[j];
       if (t0 + j < T)
@@ -367,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncthreads();  // the next head overwrites the gates and the sums
   }
+  if (stop) break;
   // ---- dq and dk over Q and K (every product has read them)
 #pragma unroll
   for (int cc = 0; cc < 8; ++cc) {
@@ -376,50 +410,65 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   fence_proxy_async_smem();
   tc_fence_before();
-  __syncthreads();
-  if (tid == 0) {
-    for (int kb = 0; kb < (p.d.dk > 64 ? 2 : 1); ++kb) {
-      tma_store_3d(&tmdq, sm.Q + kb * TILE, 64 * kb, t0, kh);
-      tma_store_3d(&tmdk, sm.K + kb * TILE, 64 * kb, t0, kh);
+  stop = __syncthreads_or(*reinterpret_cast<volatile int*>(&sm.abort));
+  if (warp >= 4 && lane == 0) {  // a tile each, whose place the next chunk's takes
+    if (64 * (warp & 1) < p.d.dk) {
+      tma_store_3d(warp < 6 ? &tmdq : &tmdk, kq_tile, 64 * (warp & 1), t0, kh);
+      tma_store_commit();
+      tma_store_wait_read();
     }
-    tma_store_commit();
-    tma_store_wait_read();
   }
+  if (stop) break;
+  if (id + gridDim.x < total) load_kq(id + gridDim.x);
+  __syncwarp();
+  }
+  if (tid == 0) {  // every load has landed
+    mbar_drain(&sm.full, (lfull - 1) & 1, wc, W_G_DRAIN);
+    mbar_drain(&sm.kq, (lkq - 1) & 1, wc, W_G_DRAIN);
+  }
+  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tb, kCols);
   }
 }
 
-cudaError_t launch_grad(const Args& a, cudaStream_t st) {
-  using gradlev::tc::make_map_bf16_3d;
-  const Dims& d = a.d;
-  const uint64_t N = chunks(d.T), kh = (uint64_t)d.B * d.Hk, bh = d.BH();
-  CUtensorMap mq, mk, mo, md, me, ms, mds, mdq, mdk;
-  if (!make_map_bf16_3d(&mq, a.q, d.dk, d.T, kh, C) || !make_map_bf16_3d(&mk, a.k, d.dk, d.T, kh, C) ||
-      !make_map_bf16_3d(&mo, a.dy, d.dv, d.T, bh, C) ||
-      !make_map_bf16_3d(&md, a.sv.D, C, dvp(d), bh * N, 64) ||
-      !make_map_bf16_3d(&me, a.E, C, dvp(d), bh * N, 64) ||
-      !make_map_bf16_3d(&ms, a.sv.S, 128, dvp(d), bh * N, 64) ||
-      !make_map_bf16_3d(&mds, a.dS, 128, dvp(d), bh * N, 64) ||
-      !make_map_bf16_3d(&mdq, a.dq, d.dk, d.T, kh, C) ||
-      !make_map_bf16_3d(&mdk, a.dk_, d.dk, d.T, kh, C))
-    return cudaErrorInvalidValue;
+template <bool GROUP>
+static cudaError_t launch(const CUtensorMap (&m)[9], const GradParams& p, unsigned work, cudaStream_t st) {
   static std::atomic<uint64_t> set{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (!bit || !(set.load() & bit)) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    const cudaError_t e = cudaFuncSetAttribute(
+        grad_kernel<GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     set.fetch_or(bit);
   }
-  GradParams p{d, a.beta, a.log_alpha, a.sv.gates, a.scale, a.status, a.timeout_ns,
-               static_cast<bf16*>(a.dbeta), static_cast<bf16*>(a.dlog_alpha)};
-  grad_kernel<<<(unsigned)(N * kh), kThreads, kSmem, st>>>(mq, mk, mo, md, me, ms, mds, mdq, mdk, p);
+  const unsigned most = 2 * 148;
+  grad_kernel<GROUP><<<work < most ? work : most, kThreads, kSmem, st>>>(m[0], m[1], m[2], m[3], m[4],
+                                                                        m[5], m[6], m[7], m[8], p);
   count_launch();
   return cudaGetLastError();
+}
+
+cudaError_t launch_grad(const Args& a, cudaStream_t st) {
+  using gradlev::tc::make_map_bf16_3d;
+  const Dims& d = a.d;
+  const uint64_t N = chunks(d.T), kh = (uint64_t)d.B * d.Hk, bh = d.BH();
+  CUtensorMap m[9];
+  if (!make_map_bf16_3d(&m[0], a.q, d.dk, d.T, kh, C) || !make_map_bf16_3d(&m[1], a.k, d.dk, d.T, kh, C) ||
+      !make_map_bf16_3d(&m[2], a.dy, d.dv, d.T, bh, C) ||
+      !make_map_bf16_3d(&m[3], a.sv.D, C, dvp(d), bh * N, 64) ||
+      !make_map_bf16_3d(&m[4], a.E, C, dvp(d), bh * N, 64) ||
+      !make_map_bf16_3d(&m[5], a.sv.S, 128, dvp(d), bh * N, 64) ||
+      !make_map_bf16_3d(&m[6], a.dS, 128, dvp(d), bh * N, 64) ||
+      !make_map_bf16_3d(&m[7], a.dq, d.dk, d.T, kh, C) ||
+      !make_map_bf16_3d(&m[8], a.dk_, d.dk, d.T, kh, C))
+    return cudaErrorInvalidValue;
+  GradParams p{d, a.beta, a.log_alpha, a.sv.gates, a.scale, a.status, a.timeout_ns,
+               static_cast<bf16*>(a.dbeta), static_cast<bf16*>(a.dlog_alpha)};
+  return d.H > d.Hk ? launch<true>(m, p, (unsigned)(N * kh), st) : launch<false>(m, p, (unsigned)(N * kh), st);
 }
 
 }  // namespace tc
