@@ -75,6 +75,9 @@ __device__ __forceinline__ void row8(float (&x)[8], const uint8_t* tile, int r, 
   }
 }
 
+__device__ __forceinline__ void tmem_ld(uint32_t at, float (&v)[8]) { tmem_ld8(at, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t at, float (&v)[16]) { tmem_ld16(at, v); }
+
 }  // namespace
 
 // GROUP: several value heads share a key head, and the sums in acc live across their products;
@@ -157,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t id_f = idesc_bf16(64, 64, false, true), id_h = idesc_bf16(64, 64, true, true);
   const uint32_t id_t = idesc_bf16(64, 128, false, true);
   const uint32_t id_m = idesc_bf16(64, 128, true, true);
+  constexpr int XW = GROUP ? 8 : 16;  // columns of X and Yn at a time, as the registers allow
   uint32_t nfull = 0, nmma = 0, nkq = 0, nhead = 0;  // phases and heads so far
 
   bool stop = false;
@@ -236,19 +240,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float rx = p.scale * g.ra[i], ry = -g.be[i] * g.ra[i];
     float db = 0.f;
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      float f[16], y[16];
-      const int j0 = 32 * hh + 16 * hf;
-      tmem_ld16(tb + COL_B + lo + j0, f);
-      tmem_ld16(tb + COL_B + 64 + lo + j0, y);
+    for (int hf = 0; hf < 32 / XW; ++hf) {
+      float f[XW], y[XW];
+      const int j0 = 32 * hh + XW * hf;
+      tmem_ld(tb + COL_B + lo + j0, f);
+      tmem_ld(tb + COL_B + 64 + lo + j0, y);
       tmem_ld_wait();
       if (!up) {
         const int keep = i - j0;  // columns left of the diagonal
 #pragma unroll
-        for (int e = 0; e < 16; ++e) db = e == keep ? y[e] : db;
+        for (int e = 0; e < XW; ++e) db = e == keep ? y[e] : db;
         if (g.fac != 0.f) {
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) {
+          for (int e = 0; e < XW; e += 4) {
             const float4 c = *reinterpret_cast<const float4*>(g.cb + j0 + e);
             const float cv[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
@@ -261,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const float Lh = sm.Lh[i], Ll = sm.Ll[i];
           const int seg = sm.seg[i];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < XW; ++e) {
             const int j = j0 + e;
             const float m = g.cb[j] * expf(fminf((Lh - sm.Lh[j]) + (Ll - sm.Ll[j]), 0.f));
             const bool on = sm.seg[j] == seg;
@@ -270,8 +274,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
 #pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-          const uint32_t off = sw128_off(i, 4 * hh + 2 * hf + cc);
+        for (int cc = 0; cc < XW / 8; ++cc) {
+          const uint32_t off = sw128_off(i, 4 * hh + XW / 8 * hf + cc);
           const float *x = f + 8 * cc, *h = y + 8 * cc;
           st_shared_v4(sX + off, pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
                        pack_bf16(x[6], x[7]));
