@@ -64,6 +64,27 @@ struct GradParams {
   bf16 *dbeta, *dlog_alpha;
 };
 
+// Two float32 products at once.
+struct F2 { unsigned long long v; };
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void get2(const F2& x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
+}
+__device__ __forceinline__ F2 fma2(const F2& a, const F2& b, const F2& c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(const F2& a, const F2& b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
 // 8 columns of a swizzled bf16 row
 __device__ __forceinline__ void row8(float (&x)[8], const uint8_t* tile, int r, int c8) {
   const uint4 u = *reinterpret_cast<const uint4*>(tile + sw128_off(r, c8));
@@ -166,17 +187,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   bool stop = false;
   for (unsigned id = blockIdx.x; id < total; id += gridDim.x) {
   const int kh = id / N, n = id - kh * N, t0 = n * C, bh0 = first_head(id);
-  float acc[64];
+  F2 acc[32];
 #pragma unroll
-  for (int e = 0; e < 64; ++e) acc[e] = 0.f;
+  for (int e = 0; e < 32; ++e) acc[e] = f2(0.f, 0.f);
 
   for (int hv = 0; hv < grp; ++hv, ++nhead) {
     const int bh = bh0 + hv;
     const GateBlock& g = sm.gates[nhead & 1];
-    float ss = 0.f;  // <dS, S>
+    F2 ss = f2(0.f, 0.f);  // <dS, S>
     for (int sl = 0; sl < nsl; ++sl) {
-      if (sl > 0) load_slice(bh, n, sl, nullptr);
-      __syncwarp();
       mbar_wait(&sm.full, nfull++ & 1, wc, W_G_FULL);
       __syncwarp();
       if (tid == 0) {
@@ -206,10 +225,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint4 y = *reinterpret_cast<const uint4*>(sm.dS + off);
         const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          ss = fmaf(bf16_lo(xw[e]), bf16_lo(yw[e]), ss);
-          ss = fmaf(bf16_hi(xw[e]), bf16_hi(yw[e]), ss);
-        }
+        for (int e = 0; e < 4; ++e)
+          ss = fma2(f2(bf16_lo(xw[e]), bf16_hi(xw[e])), f2(bf16_lo(yw[e]), bf16_hi(yw[e])), ss);
       }
       if (sl == 0 && warp == 2 && g.fac == 0.f) {
         const GatePair gp = chunk_gates(load_gates(p.beta, p.log_alpha, (size_t)bh * T, t0, T));
@@ -221,20 +238,27 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       mbar_wait(&sm.mma, nmma++ & 1, wc, W_G_MMA);
-      // S and dS are read: the next slice may land
+      // S and dS are read
       stop = __syncthreads_or(*reinterpret_cast<volatile int*>(&sm.abort));
       if (stop) break;
+      // the next slice, of this head or the next one or (behind what follows here) the next chunk
+      int bh1 = bh, n1 = n, sl1 = sl + 1;
+      if (sl1 == nsl) {
+        const unsigned id1 = id + (hv + 1 < grp ? 0u : gridDim.x);
+        bh1 = hv + 1 < grp ? bh + 1 : first_head(id1);
+        n1 = id1 % N;
+        sl1 = id1 < total ? 0 : -1;
+      }
+      if (sl1 >= 0) load_slice(bh1, n1, sl1, &sm.gates[(nhead + 1) & 1]);
+      __syncwarp();
     }
     if (stop) break;
-    // the first slice of the next head or chunk lands behind what follows
-    if (hv + 1 < grp)
-      load_slice(bh + 1, n, 0, &sm.gates[(nhead + 1) & 1]);
-    else if (id + gridDim.x < total)
-      load_slice(first_head(id + gridDim.x), (id + gridDim.x) % N, 0, &sm.gates[(nhead + 1) & 1]);
-    __syncwarp();
+    float s0, s1;
+    get2(ss, s0, s1);
+    s0 += s1;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (lane == 0) sm.red[warp] = ss;
+    for (int o = 16; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+    if (lane == 0) sm.red[warp] = s0;
     tc_fence_after();
     // ---- X and Yn: lower lanes, columns [32 hh, 32 hh + 32)
     const float rx = p.scale * g.ra[i], ry = -g.be[i] * g.ra[i];
@@ -301,7 +325,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ---- t (lower) and u (upper); z (upper)
     const uint8_t* mine = (up ? sm.K : sm.Q) + hh * TILE;
     const float ca = up ? g.bG[i] : g.q[i], cz = up ? g.bw[i] : 0.f;
-    float xs = 0.f, ps = 0.f, zs = 0.f;
+    float xs, ps, zs;
+    const F2 ca2 = f2(ca, ca), cz2 = f2(cz, cz);
+    F2 dv = f2(0.f, 0.f), dz = dv;
+    if (!GROUP) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) acc[e] = dv;
+    }
 #pragma unroll
     for (int cc = 0; cc < 8; ++cc) {
       float v[8], z[8], x[8];
@@ -309,16 +339,22 @@ __global__ void __launch_bounds__(kThreads, 2)
       tmem_ld8(tb + COL_B + lo + 64 * hh + 8 * cc, z);  // lower lanes: unused (xk in flight)
       row8(x, mine, i, cc);
       tmem_ld_wait();
-      float dv = 0.f, dz = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float ze = up ? z[e] : 0.f;
-        dv = fmaf(v[e], x[e], dv);
-        dz = fmaf(ze, x[e], dz);
-        acc[8 * cc + e] = fmaf(ca, v[e], GROUP ? fmaf(cz, ze, acc[8 * cc + e]) : cz * ze);
+      for (int e = 0; e < 8; e += 2) {
+        const F2 ve = f2(v[e], v[e + 1]), ze = up ? f2(z[e], z[e + 1]) : f2(0.f, 0.f);
+        const F2 xe = f2(x[e], x[e + 1]);
+        F2& s = acc[4 * cc + e / 2];
+        dv = fma2(ve, xe, dv);
+        dz = fma2(ze, xe, dz);
+        s = fma2(ca2, ve, fma2(cz2, ze, s));
       }
-      xs = fmaf(ca, dv, xs);
-      zs = fmaf(cz, dz, zs);
+    }
+    {
+      float a, c;
+      get2(dv, a, c);
+      xs = ca * (a + c);
+      get2(dz, a, c);
+      zs = cz * (a + c);
     }
     tc_fence_before();
     __syncthreads();
@@ -339,6 +375,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
     tc_fence_after();
     // ---- xk (lower) and ka (upper); yk (upper)
+    dv = dz = f2(0.f, 0.f);
 #pragma unroll
     for (int cc = 0; cc < 8; ++cc) {
       float v[8], z[8], x[8];
@@ -346,14 +383,21 @@ __global__ void __launch_bounds__(kThreads, 2)
       tmem_ld8(tb + COL_A + lo + 64 * hh + 8 * cc, z);  // lower lanes: t, used above
       row8(x, mine, i, cc);
       tmem_ld_wait();
-      float dot = 0.f;  // q.xk, or k.(yk - ka)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float ye = up ? z[e] : 0.f;
-        dot = fmaf(up ? ye - v[e] : v[e], x[e], dot);
-        acc[8 * cc + e] += v[e] + ye;
+      for (int e = 0; e < 8; e += 2) {
+        const F2 ve = f2(v[e], v[e + 1]), ye = up ? f2(z[e], z[e + 1]) : f2(0.f, 0.f);
+        const F2 xe = f2(x[e], x[e + 1]);
+        F2& s = acc[4 * cc + e / 2];
+        dv = fma2(ve, xe, dv);
+        dz = fma2(ye, xe, dz);
+        s = add2(s, add2(ve, ye));
       }
-      ps += dot;
+    }
+    {  // q.xk, or k.(yk - ka)
+      float a, c, y0, y1;
+      get2(dv, a, c);
+      get2(dz, y0, y1);
+      ps = up ? (y0 + y1) - (a + c) : a + c;
     }
     xs += __shfl_xor_sync(0xffffffffu, xs, 16);
     ps += __shfl_xor_sync(0xffffffffu, ps, 16);
@@ -408,7 +452,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   // ---- dq and dk over Q and K (every product has read them)
 #pragma unroll
   for (int cc = 0; cc < 8; ++cc) {
-    const float* a = acc + 8 * cc;
+    float a[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) get2(acc[4 * cc + e], a[2 * e], a[2 * e + 1]);
     st_shared_v4((up ? sK : sQ) + hh * TILE + sw128_off(i, cc), pack_bf16(a[0], a[1]),
                  pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
   }
