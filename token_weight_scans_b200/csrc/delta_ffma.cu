@@ -12,6 +12,7 @@
 
 #include "common.cuh"
 #include "delta.h"
+#include "tf32.cuh"
 
 namespace gradlev {
 namespace delta {
@@ -185,6 +186,9 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool ok) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
 }
 
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
 // Asynchronous copies of chunk n (its 16-byte pieces over the CTA's threads).
 template <typename Tio>
 __device__ void fetch(const Stage<Tio>& g, const Args& a, const Tio* v, size_t bh, size_t kh, int n,
@@ -219,13 +223,13 @@ __device__ void fetch(const Stage<Tio>& g, const Args& a, const Tio* v, size_t b
   copy16(g.P + t * LZ + c, P + t * C + c, true);
 }
 
-// Threads: token `lane` and state rows 2 warp, 2 warp + 1 for the products that end in tokens;
-// four rows and one column of d_k for the update of S.
+// Every product has the slice's 16 rows on one side, which is the height of a warp's tf32 tile
+// (tf32.cuh). Warps 0 to 3 own 8 tokens each of S K^T, D and E, warps 4 to 7 the same tokens of
+// S Q^T and y (backward: of dY P^T); for the update of S a warp owns every eighth 8 columns.
 template <typename Tio, bool BWD>
 __global__ void __launch_bounds__(kThreads) walk_kernel(Args a) {
   extern __shared__ __align__(16) char smc[];
-  // [row][token]: a lane's stores and a warp's reads of a row are free of bank conflicts
-  __shared__ __align__(16) float X[kRows * LZ], Y[kRows * LZ], U[kRows * LZ], W[kRows * LZ];
+  __shared__ float X[kRows * LZ], Y[kRows * LZ], U[kRows * LZ], W[kRows * LZ];  // [row][token]
   const Dims& d = a.d;
   const int N = chunks(d.T), ns = slices(d.dv), bh = blockIdx.x / ns;
   const int n0 = (blockIdx.x - bh * ns) * kRows;
@@ -234,7 +238,10 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(Args a) {
   const size_t kh = (size_t)b * d.Hk + h / (d.H / d.Hk);
   const int ld = pad4(d.dk), lk = pad_row<Tio>(d.dk);
   float* S = reinterpret_cast<float*>(smc + 2 * stage_bytes<Tio>(d.dk));  // [kRows][ld]
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r0 = 2 * warp;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tr = (tid & 31) >> 2, tt = 8 * (warp & 3) + 2 * (tid & 3);  // this thread's part of a tile
+  const bool second = warp >= 4;
+  constexpr bool kExact = sizeof(Tio) == 2;
   const Tio* v = static_cast<const Tio*>(BWD ? a.dy : a.v);
   const bool fresh = a.log_alpha[(size_t)bh * d.T] < kResetLog;  // S0 may hold anything then
   for (int i = tid; i < kRows * d.dk; i += kThreads) {
@@ -266,114 +273,78 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(Args a) {
       for (int i = 4 * tid; i < rows * d.dk; i += 4 * kThreads)
         *reinterpret_cast<float4*>(out + i) = at4(S + (i / d.dk) * ld + i % d.dk);
     }
-    float x0 = 0.f, x1 = 0.f, y0 = 0.f, y1 = 0.f;
-#pragma unroll 4
-    for (int c = 0; c < d.dk; c += 4) {
-      const float4 kv = at4(st.K + lane * lk + c);
-      const float4 s0 = at4(S + r0 * ld + c), s1 = at4(S + (r0 + 1) * ld + c);
-      x0 = dot4(kv, s0, x0);
-      x1 = dot4(kv, s1, x1);
-      if (!BWD) {
-        const float4 qv = at4(st.Q + lane * lk + c);
-        y0 = dot4(qv, s0, y0);
-        y1 = dot4(qv, s1, y1);
-      }
-    }
-    const float be = g.beta[lane], G = g.G[lane], w = g.w[lane];
-    if (!BWD) {
-      x0 = to_f32(st.V[lane * LV + r0]) - G * x0;  // R
-      x1 = to_f32(st.V[lane * LV + r0 + 1]) - G * x1;
-    } else {
-      x0 *= w;  // F = diag(w) K dS^T + P^T dY
-      x1 *= w;
-#pragma unroll 8
-      for (int m = 0; m < C; ++m) {
-        const float p = st.P[m * LZ + lane];
-        x0 = fmaf(p, to_f32(st.V[m * LV + r0]), x0);
-        x1 = fmaf(p, to_f32(st.V[m * LV + r0 + 1]), x1);
-      }
-    }
-    X[r0 * LZ + lane] = -be * x0;  // a warp's rows of X and Y are its own
-    X[(r0 + 1) * LZ + lane] = -be * x1;
-    __syncwarp();
-    if (!BWD) {  // D = R - Z diag(beta) R
+    const int n8 = 8 * (warp & 3);
+    auto V = [&](int r, int t) { return to_f32(st.V[t * LV + r]); };
+    auto store = [&](auto* out, const float (&x)[4]) {  // a tile of [row][token] to [t][d_v]
 #pragma unroll
-      for (int m = 0; m < C; m += 4) {
-        const float4 z = at4(st.Z + lane * LZ + m);
-        x0 = dot4(z, at4(X + r0 * LZ + m), x0);
-        x1 = dot4(z, at4(X + (r0 + 1) * LZ + m), x1);
+      for (int e = 0; e < 4; ++e) {
+        const int r = tr + 8 * (e >> 1), t = tt + (e & 1);
+        if (t0 + t < d.T && r < rows) put(out + ((size_t)bh * d.T + t0 + t) * d.dv + n0 + r, x[e]);
       }
-    } else {     // E = F - Z^T diag(beta) F
-#pragma unroll 8
-      for (int m = 0; m < C; m += 4) {
-        const float4 z = make_float4(st.Z[m * LZ + lane], st.Z[(m + 1) * LZ + lane],
-                                     st.Z[(m + 2) * LZ + lane], st.Z[(m + 3) * LZ + lane]);
-        x0 = dot4(z, at4(X + r0 * LZ + m), x0);
-        x1 = dot4(z, at4(X + (r0 + 1) * LZ + m), x1);
-      }
-    }
-    // W: what leaves (D, E); U: what updates S (beta w D, -beta G E)
-    const float cu = BWD ? -be * G : be * w;
-    W[r0 * LZ + lane] = x0;
-    W[(r0 + 1) * LZ + lane] = x1;
-    U[r0 * LZ + lane] = cu * x0;
-    U[(r0 + 1) * LZ + lane] = cu * x1;
-    if (!BWD) {
-      Y[r0 * LZ + lane] = be * x0;
-      Y[(r0 + 1) * LZ + lane] = be * x1;
-      __syncwarp();
-      y0 *= a.scale * G;
-      y1 *= a.scale * G;
+    };
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (!BWD || !second) {
+      const Tio* B = !BWD && second ? st.Q : st.K;
+      tf32::tile<kExact>(x, 0, d.dk, [&](int r, int k) { return S[r * ld + k]; },
+                         [&](int k, int t) { return to_f32(B[(n8 + t) * lk + k]); });
+    } else {  // P^T dY, and dY scaled for the update
+      tf32::tile<false>(x, 0, C, [&](int r, int m) { return V(r, m); },
+                        [&](int m, int t) { return st.P[m * LZ + n8 + t]; });
 #pragma unroll
-      for (int m = 0; m < C; m += 4) {
-        const float4 p = at4(st.P + lane * LZ + m);
-        y0 = dot4(p, at4(Y + r0 * LZ + m), y0);
-        y1 = dot4(p, at4(Y + (r0 + 1) * LZ + m), y1);
+      for (int e = 0; e < 4; ++e) {
+        const int r = tr + 8 * (e >> 1), t = tt + (e & 1);
+        Y[r * LZ + t] = x[e];
+        W[r * LZ + t] = a.scale * g.G[t] * V(r, t);
       }
-      __syncwarp();
-    } else {  // dV, and dY scaled for the update
-      y0 = be * x0;
-      y1 = be * x1;
-      X[r0 * LZ + lane] = a.scale * G * to_f32(st.V[lane * LV + r0]);
-      X[(r0 + 1) * LZ + lane] = a.scale * G * to_f32(st.V[lane * LV + r0 + 1]);
     }
-    Y[r0 * LZ + lane] = y0;
-    Y[(r0 + 1) * LZ + lane] = y1;
-    __syncthreads();
-    {
-      Tio* yo = static_cast<Tio*>(BWD ? a.dv_ : a.y);
+    if (BWD) __syncthreads();
+    if (!second) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = tr + 8 * (e >> 1), t = tt + (e & 1);
+        // R = V - G S K; backward F = w dS K + P^T dY
+        x[e] = BWD ? fmaf(g.w[t], x[e], Y[r * LZ + t]) : V(r, t) - g.G[t] * x[e];
+        X[r * LZ + t] = -g.beta[t] * x[e];
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      // D = R - Z diag(beta) R; backward E = F - Z^T diag(beta) F
+      tf32::tile<false>(x, 0, C, [&](int r, int m) { return X[r * LZ + m]; },
+                        [&](int m, int t) { return BWD ? st.Z[m * LZ + n8 + t] : st.Z[(n8 + t) * LZ + m]; });
       float* wo = BWD ? a.E : a.sv.D;
-      for (int i = tid; i < C * kRows; i += kThreads) {
-        const int t = i / kRows, r = i - t * kRows;
-        if (t0 + t < d.T && r < rows) {
-          const size_t at = ((size_t)bh * d.T + t0 + t) * d.dv + n0 + r;
-          if (yo) yo[at] = from_f32<Tio>(Y[r * LZ + t]);
-          if (wo) wo[at] = W[r * LZ + t];
-        }
+      if (wo) store(wo, x);
+      // U: what updates S (beta w D, -beta G E)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = tr + 8 * (e >> 1), t = tt + (e & 1);
+        const float be = g.beta[t];
+        U[r * LZ + t] = (BWD ? -be * g.G[t] : be * g.w[t]) * x[e];
+        x[e] *= be;
+        if (!BWD) Y[r * LZ + t] = x[e];
       }
+      if (BWD) store(static_cast<Tio*>(a.dv_), x);
     }
-    // S <- G_C S + U^T K (+ (scale G dY)^T Q)
+    __syncthreads();
+    if (!BWD && second) {  // y = scale G S Q^T + P diag(beta) D
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] *= a.scale * g.G[tt + (e & 1)];
+      tf32::tile<false>(x, 0, C, [&](int r, int m) { return Y[r * LZ + m]; },
+                        [&](int m, int t) { return st.P[(n8 + t) * LZ + m]; });
+      if (a.y) store(static_cast<Tio*>(a.y), x);
+    }
+    // S <- G_C S + U K (+ scale G dY Q)
     const float GC = g.GC;
-    for (int i = tid; i < kRows / 4 * d.dk; i += kThreads) {
-      const int rq = i / d.dk, c = i - rq * d.dk;
-      float s[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] = GC * S[(4 * rq + e) * ld + c];
-#pragma unroll 2
-      for (int m = 0; m < C; m += 4) {
-        const float4 kv = make_float4(to_f32(st.K[m * lk + c]), to_f32(st.K[(m + 1) * lk + c]),
-                                      to_f32(st.K[(m + 2) * lk + c]), to_f32(st.K[(m + 3) * lk + c]));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] = dot4(at4(U + (4 * rq + e) * LZ + m), kv, s[e]);
-        if (BWD) {
-          const float4 qv = make_float4(to_f32(st.Q[m * lk + c]), to_f32(st.Q[(m + 1) * lk + c]),
-                                        to_f32(st.Q[(m + 2) * lk + c]), to_f32(st.Q[(m + 3) * lk + c]));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[e] = dot4(at4(X + (4 * rq + e) * LZ + m), qv, s[e]);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S[(4 * rq + e) * ld + c] = s[e];
+    for (int c0 = 8 * warp; c0 < d.dk; c0 += 8 * kWarps) {
+      float* at = S + tr * ld + c0 + 2 * (tid & 3);
+      float s[4] = {GC * at[0], GC * at[1], GC * at[8 * ld], GC * at[8 * ld + 1]};
+      tf32::tile<kExact>(s, 0, C, [&](int r, int m) { return U[r * LZ + m]; },
+                         [&](int m, int c) { return to_f32(st.K[m * lk + c0 + c]); });
+      if (BWD)
+        tf32::tile<kExact>(s, 0, C, [&](int r, int m) { return W[r * LZ + m]; },
+                           [&](int m, int c) { return to_f32(st.Q[m * lk + c0 + c]); });
+      at[0] = s[0];
+      at[1] = s[1];
+      at[8 * ld] = s[2];
+      at[8 * ld + 1] = s[3];
     }
     __syncthreads();
   }

@@ -25,6 +25,7 @@
 
 #include "delta_tc.h"
 #include "sm100.cuh"
+#include "tf32.cuh"
 
 namespace gradlev {
 namespace delta {
@@ -85,40 +86,13 @@ __device__ __forceinline__ uint32_t pack_lo(float a, float b, uint32_t hi) {
 __device__ __forceinline__ float4 at4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 // 16 x 8 of a product of float32 matrices in shared memory (row stride LD), k0 <= k < k1 (whole
-// eights), with both operands split into two tf32 parts: off by 2^-21, where one part would be
-// off by 2^-11. One warp; out[0..1] in row lane / 4, out[2..3] eight rows below, at columns
-// 2 (lane % 4) and the next.
-__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
-  lo = __float_as_uint(x - __uint_as_float(hi));
-}
-__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-               "{%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
+// eights): out[0..1] in row lane / 4, out[2..3] eight rows below, at columns 2 (lane % 4) and the
+// next.
 __device__ __forceinline__ void product16x8(float (&out)[4], const float* A, const float* B, int k0,
                                             int k1) {
-  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
-  float small[4] = {0.f, 0.f, 0.f, 0.f};
   out[0] = out[1] = out[2] = out[3] = 0.f;
-  for (int k = k0; k < k1; k += 8) {
-    const float* a = A + g * LD + k + t;
-    const float* b = B + (k + t) * LD + g;
-    uint32_t ah[4], al[4], bh[2], bl[2];
-    split_tf32(a[0], ah[0], al[0]);
-    split_tf32(a[8 * LD], ah[1], al[1]);
-    split_tf32(a[4], ah[2], al[2]);
-    split_tf32(a[8 * LD + 4], ah[3], al[3]);
-    split_tf32(b[0], bh[0], bl[0]);
-    split_tf32(b[4 * LD], bh[1], bl[1]);
-    mma_tf32(out, ah, bh);
-    mma_tf32(small, ah, bl);
-    mma_tf32(small, al, bh);
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) out[e] += small[e];
+  tf32::tile<false>(out, k0, k1, [&](int r, int k) { return A[r * LD + k]; },
+                    [&](int k, int c) { return B[k * LD + c]; });
 }
 __device__ __forceinline__ void store16x8(float* at, const float (&v)[4], float sign) {
   float* p = at + ((threadIdx.x & 31) >> 2) * LD + 2 * (threadIdx.x & 3);
