@@ -189,22 +189,43 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool ok) {
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+// The pieces tid, tid + kThreads, .. of a matrix with `per` pieces in a row, without a division
+// for each of them.
+struct Pieces {
+  int row, col, drow, dcol, per;
+  __device__ Pieces(int per_row) : per(per_row) {
+    row = threadIdx.x / per;
+    col = threadIdx.x - row * per;
+    drow = kThreads / per;
+    dcol = kThreads - drow * per;
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(int rows, F f) const {
+    for (int r = row, c = col; r < rows;) {
+      f(r, c);
+      r += drow;
+      c += dcol;
+      if (c >= per) c -= per, ++r;
+    }
+  }
+};
+
 // Asynchronous copies of chunk n (its 16-byte pieces over the CTA's threads).
 template <typename Tio>
-__device__ void fetch(const Stage<Tio>& g, const Args& a, const Tio* v, size_t bh, size_t kh, int n,
-                      int n0, int rows) {
+__device__ __forceinline__ void fetch(const Stage<Tio>& g, const Args& a, const Tio* v, size_t bh,
+                                      size_t kh, int n, int n0, int rows, const Pieces& kp) {
   constexpr int E = 16 / sizeof(Tio);
   const Dims& d = a.d;
-  const int N = chunks(d.T), t0 = n * C, kc = d.dk / E;
+  const int N = chunks(d.T), t0 = n * C;
   const Tio* K = static_cast<const Tio*>(a.k) + kh * d.T * d.dk;
   const Tio* Q = static_cast<const Tio*>(a.q) + kh * d.T * d.dk;
-  for (int i = threadIdx.x; i < C * kc; i += kThreads) {
-    const int t = i / kc, c = (i - t * kc) * E;
+  kp.each(C, [&](int t, int piece) {
+    const int c = piece * E;
     const bool ok = t0 + t < d.T;
     const size_t at = (size_t)(ok ? t0 + t : 0) * d.dk + c;
     copy16(g.K + t * pad_row<Tio>(d.dk) + c, K + at, ok);
     copy16(g.Q + t * pad_row<Tio>(d.dk) + c, Q + at, ok);
-  }
+  });
   constexpr int vc = kRows / E;
   for (int i = threadIdx.x; i < C * vc; i += kThreads) {
     const int t = i / vc, c = (i - t * vc) * E;
@@ -256,8 +277,9 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(Args a) {
     }
     S[r * ld + c] = s;
   }
+  const Pieces kp(d.dk * (int)sizeof(Tio) / 16), sp(d.dk / 4);  // of rows of K and Q, of S
   auto at_chunk = [&](int c) { return BWD ? N - 1 - c : c; };
-  fetch(stage_at<Tio>(smc, 0, d.dk), a, v, (size_t)bh, kh, at_chunk(0), n0, rows);
+  fetch(stage_at<Tio>(smc, 0, d.dk), a, v, (size_t)bh, kh, at_chunk(0), n0, rows, kp);
   asm volatile("cp.async.commit_group;" ::: "memory");
   float* states = BWD ? a.dS : a.sv.S;
   for (int ci = 0; ci < N; ++ci) {
@@ -265,13 +287,14 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(Args a) {
     const Stage<Tio> st = stage_at<Tio>(smc, ci & 1, d.dk);
     const WalkGates& g = *st.g;
     if (ci + 1 < N)  // the other stage was last read before the barrier that ended chunk ci - 1
-      fetch(stage_at<Tio>(smc, (ci + 1) & 1, d.dk), a, v, (size_t)bh, kh, at_chunk(ci + 1), n0, rows);
+      fetch(stage_at<Tio>(smc, (ci + 1) & 1, d.dk), a, v, (size_t)bh, kh, at_chunk(ci + 1), n0, rows, kp);
     asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 1;" ::: "memory");
     __syncthreads();
     if (states) {
       float* out = states + (((size_t)bh * N + n) * d.dv + n0) * d.dk;
-      for (int i = 4 * tid; i < rows * d.dk; i += 4 * kThreads)
-        *reinterpret_cast<float4*>(out + i) = at4(S + (i / d.dk) * ld + i % d.dk);
+      sp.each(rows, [&](int r, int c) {
+        *reinterpret_cast<float4*>(out + r * d.dk + 4 * c) = at4(S + r * ld + 4 * c);
+      });
     }
     const int n8 = 8 * (warp & 3);
     auto V = [&](int r, int t) { return to_f32(st.V[t * LV + r]); };
