@@ -386,45 +386,45 @@ template <typename Tio>
 size_t walk_smem(int dk) { return 2 * stage_bytes<Tio>(dk) + kRows * pad4(dk) * sizeof(float); }
 
 // ------------------------------------------------------------------ gradients of q, k, gates
-// One CTA per (chunk, key head). A warp owns 4 tokens and every column, so a token's dot
-// products end in a warp sum; the value heads that share the key head are walked in order
-// and add up in registers.
+// One CTA per (chunk, key head). All products are warp tiles of 16 tokens and 8 columns (tf32.cuh):
+// a warp has one of the tokens x tokens matrices and, of tokens x d_k, every fourth 8 columns, so
+// sums over columns end in four lanes and four warps. The value heads that share the key head
+// are walked in order and add up in registers.
 constexpr int kVB = 16;       // rows of the states in shared memory at a time
 
 template <typename Tio, int NJ>  // NJ: 32-column groups that cover dk
 __global__ void __launch_bounds__(kThreads) grad_kernel(Args a) {
   extern __shared__ __align__(16) float sm[];
   __shared__ Gates g;
-  __shared__ float X[C * LD], Y[C * LD], W[C * LD];  // W: X q.k - Y k.k
-  __shared__ float dLx[C], dLz[C], red[kWarps];
+  __shared__ float X[C * LZ], Y[C * LZ], W[C * LD];  // W: X q.k - Y k.k
+  __shared__ float dLx[4][C], dLz[4][C], red[kWarps];
   const Dims& d = a.d;
   const int N = chunks(d.T), n = blockIdx.x % N, t0 = n * C;
   const size_t kh = blockIdx.x / N;
   const int b = kh / d.Hk, hk = kh - (size_t)b * d.Hk, grp = d.H / d.Hk;
   const int ld = pad4(d.dk), lv = pad4(d.dv);
   float *K = sm, *Q = K + C * ld, *O = Q + C * ld, *D = O + C * lv, *E = D + C * lv;
-  float *Sv = E + C * lv, *dSv = Sv + kVB * d.dk;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, i0 = 4 * warp;
-  static_assert(4 * kWarps == C, "a warp owns 4 tokens");
+  float *Sv = E + C * lv, *dSv = Sv + kVB * (d.dk + 8);
+  const Pieces sp(d.dk / 4);  // of rows of S
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // this warp's tokens and columns, this thread's first of either
+  const int m0 = 16 * (warp & 1), n0 = 8 * (warp >> 1);
+  const int i0 = m0 + (lane >> 2), j0 = n0 + 2 * (lane & 3), lds = d.dk + 8;
+  static_assert(2 * 16 == C && 8 * kWarps / 2 == C, "a tile of tokens x tokens per warp");
   load_tile(K, ld, static_cast<const Tio*>(a.k) + kh * d.T * d.dk, t0, d.T, d.dk);
   load_tile(Q, ld, static_cast<const Tio*>(a.q) + kh * d.T * d.dk, t0, d.T, d.dk);
   __syncthreads();
-  float kk[4], qk[4];  // k_i.k_j, q_i.k_j of this warp's tokens i, j = lane
-#pragma unroll
-  for (int e = 0; e < 4; ++e) kk[e] = qk[e] = 0.f;
-  for (int c = 0; c < d.dk; c += 4) {
-    const float4 kj = at4(K + lane * ld + c);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      kk[e] = dot4(at4(K + (i0 + e) * ld + c), kj, kk[e]);
-      qk[e] = dot4(at4(Q + (i0 + e) * ld + c), kj, qk[e]);
-    }
+  float kk[4] = {0.f, 0.f, 0.f, 0.f}, qk[4] = {0.f, 0.f, 0.f, 0.f};  // k_i.k_j, q_i.k_j
+  for (int c = 0; c < d.dk; c += 8) {
+    const tf32::B8 kj = tf32::load_b<false>([&](int x, int j) { return K[(n0 + j) * ld + c + x]; });
+    tf32::mma3<false>(kk, tf32::load_a([&](int i, int x) { return K[(m0 + i) * ld + c + x]; }), kj);
+    tf32::mma3<false>(qk, tf32::load_a([&](int i, int x) { return Q[(m0 + i) * ld + c + x]; }), kj);
   }
-  float aq[4][NJ], ak[4][NJ];
+  float aq[NJ][4], ak[NJ][4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
+  for (int j = 0; j < NJ; ++j)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) aq[e][j] = ak[e][j] = 0.f;
+    for (int e = 0; e < 4; ++e) aq[j][e] = ak[j][e] = 0.f;
 
   for (int hh = 0; hh < grp; ++hh) {
     const size_t bh = (size_t)b * d.H + hk * grp + hh;
@@ -437,119 +437,114 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(Args a) {
     const float* S = a.sv.S + (bh * N + n) * d.dv * d.dk;
     const float* dS = a.dS + (bh * N + n) * d.dv * d.dk;
     {  // X, Y, their part of dlog_alpha, dbeta
-      float f[4], ed[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f[e] = ed[e] = 0.f;
-      for (int c = 0; c < d.dv; c += 4) {
-        const float4 dj = at4(D + lane * lv + c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          f[e] = dot4(at4(O + (i0 + e) * lv + c), dj, f[e]);
-          ed[e] = dot4(at4(E + (i0 + e) * lv + c), dj, ed[e]);
-        }
+      float f[4] = {0.f, 0.f, 0.f, 0.f}, ed[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int c = 0; c < d.dv; c += 8) {
+        const tf32::B8 dj = tf32::load_b<false>([&](int x, int j) { return D[(n0 + j) * lv + c + x]; });
+        tf32::mma3<false>(f, tf32::load_a([&](int i, int x) { return O[(m0 + i) * lv + c + x]; }), dj);
+        tf32::mma3<false>(ed, tf32::load_a([&](int i, int x) { return E[(m0 + i) * lv + c + x]; }), dj);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int i = i0 + e;
-        const float m = lane <= i ? decay(g, i, lane) * g.beta[lane] : 0.f;
-        const float x = a.scale * m * f[e], y = lane < i ? m * g.beta[i] * ed[e] : 0.f;
-        X[i * LD + lane] = x;
-        Y[i * LD + lane] = y;
-        W[i * LD + lane] = lane < i ? x * qk[e] - y * kk[e] : 0.f;
-        const float db = __shfl_sync(0xffffffffu, ed[e], i);
-        if (lane == 0 && t0 + i < d.T)
-          static_cast<Tio*>(a.dbeta)[bh * d.T + t0 + i] = from_f32<Tio>(db);
+        const int i = i0 + 8 * (e >> 1), j = j0 + (e & 1);
+        const float m = j <= i ? decay(g, i, j) * g.beta[j] : 0.f;
+        const float x = a.scale * m * f[e], y = j < i ? m * g.beta[i] * ed[e] : 0.f;
+        X[i * LZ + j] = x;
+        Y[i * LZ + j] = y;
+        W[i * LD + j] = j < i ? x * qk[e] - y * kk[e] : 0.f;
+        if (i == j && t0 + i < d.T) static_cast<Tio*>(a.dbeta)[bh * d.T + t0 + i] = from_f32<Tio>(ed[e]);
       }
     }
-    // dY S, E S, D dS: columns lane + 32 j
-    float t[4][NJ], u[4][NJ], z[4][NJ];
+    // dY S, E S, D dS
+    float t[NJ][4], u[NJ][4], z[NJ][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) t[e][j] = u[e][j] = z[e][j] = 0.f;
+      for (int e = 0; e < 4; ++e) t[j][e] = u[j][e] = z[j][e] = 0.f;
     float ss = 0.f;
     for (int v0 = 0; v0 < d.dv; v0 += kVB) {  // kVB rows of S and dS at a time (dv may end inside)
-      const int nv = min(kVB, d.dv - v0), n4 = nv * d.dk / 4;
+      const int nv = min(kVB, d.dv - v0);
       __syncthreads();
-      for (int i = tid; i < n4; i += kThreads) {
-        reinterpret_cast<float4*>(Sv)[i] = at4(S + (size_t)v0 * d.dk + 4 * i);
-        reinterpret_cast<float4*>(dSv)[i] = at4(dS + (size_t)v0 * d.dk + 4 * i);
-      }
+      sp.each(nv, [&](int v, int c4) {
+        const float4 s = at4(S + (size_t)(v0 + v) * d.dk + 4 * c4), ds = at4(dS + (size_t)(v0 + v) * d.dk + 4 * c4);
+        *reinterpret_cast<float4*>(Sv + v * lds + 4 * c4) = s;
+        *reinterpret_cast<float4*>(dSv + v * lds + 4 * c4) = ds;
+        ss = dot4(s, ds, ss);
+      });
       __syncthreads();
-      for (int i = tid; i < n4; i += kThreads) ss = dot4(at4(Sv + 4 * i), at4(dSv + 4 * i), ss);
-      for (int v = 0; v < nv; v += 4) {
-        float4 o[4], ee[4], dd[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          o[e] = at4(O + (i0 + e) * lv + v0 + v);
-          ee[e] = at4(E + (i0 + e) * lv + v0 + v);
-          dd[e] = at4(D + (i0 + e) * lv + v0 + v);
-        }
+      for (int v = 0; v < nv; v += 8) {
+        const tf32::A16 o = tf32::load_a([&](int i, int x) { return O[(m0 + i) * lv + v0 + v + x]; });
+        const tf32::A16 ee = tf32::load_a([&](int i, int x) { return E[(m0 + i) * lv + v0 + v + x]; });
+        const tf32::A16 dd = tf32::load_a([&](int i, int x) { return D[(m0 + i) * lv + v0 + v + x]; });
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-          const int c = lane + 32 * j;
-          if (32 * j + 32 > d.dk && c >= d.dk) continue;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float s = Sv[(v + x) * d.dk + c], ds = dSv[(v + x) * d.dk + c];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              t[e][j] = fmaf(x == 0 ? o[e].x : x == 1 ? o[e].y : x == 2 ? o[e].z : o[e].w, s, t[e][j]);
-              u[e][j] = fmaf(x == 0 ? ee[e].x : x == 1 ? ee[e].y : x == 2 ? ee[e].z : ee[e].w, s, u[e][j]);
-              z[e][j] = fmaf(x == 0 ? dd[e].x : x == 1 ? dd[e].y : x == 2 ? dd[e].z : dd[e].w, ds, z[e][j]);
-            }
-          }
+          const int c0 = n0 + 32 * j;
+          if (c0 >= d.dk) continue;
+          const tf32::B8 s = tf32::load_b<false>([&](int x, int c) { return Sv[(v + x) * lds + c0 + c]; });
+          const tf32::B8 ds = tf32::load_b<false>([&](int x, int c) { return dSv[(v + x) * lds + c0 + c]; });
+          tf32::mma3<false>(t[j], o, s);
+          tf32::mma3<false>(u[j], ee, s);
+          tf32::mma3<false>(z[j], dd, ds);
         }
       }
     }
     ss = warp_sum(ss);
     if (lane == 0) red[warp] = ss;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = i0 + e;
+    for (int h = 0; h < 2; ++h) {  // tokens i0 and i0 + 8
+      const int i = i0 + 8 * h;
       const float cq = a.scale * g.G[i], ck = g.beta[i] * g.G[i], cz = g.beta[i] * g.w[i];
       float x = 0.f, zz = 0.f;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const int c = lane + 32 * j;
-        const float qv = c < d.dk ? Q[i * ld + c] : 0.f, kv = c < d.dk ? K[i * ld + c] : 0.f;
-        x += cq * t[e][j] * qv - ck * u[e][j] * kv;
-        zz += cz * z[e][j] * kv;
-        aq[e][j] += cq * t[e][j];
-        ak[e][j] += cz * z[e][j] - ck * u[e][j];
+        if (n0 + 32 * j >= d.dk) continue;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int e = 2 * h + y, c = j0 + 32 * j + y;
+          const float qv = Q[i * ld + c], kv = K[i * ld + c];
+          x += cq * t[j][e] * qv - ck * u[j][e] * kv;
+          zz += cz * z[j][e] * kv;
+          aq[j][e] += cq * t[j][e];
+          ak[j][e] += cz * z[j][e] - ck * u[j][e];
+        }
       }
-      x = warp_sum(x);
-      zz = warp_sum(zz);
-      if (lane == 0) {
-        dLx[i] = x;
-        dLz[i] = zz;
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+        zz += __shfl_xor_sync(0xffffffffu, zz, o);
+      }
+      if ((lane & 3) == 0) {
+        dLx[warp >> 1][i] = x;
+        dLz[warp >> 1][i] = zz;
       }
     }
     __syncthreads();
-    for (int m = 0; m < C; ++m) {
-      float x[4], xt[4], yy[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[e] = X[(i0 + e) * LD + m];
-        xt[e] = X[m * LD + i0 + e];
-        yy[e] = Y[(i0 + e) * LD + m] + Y[m * LD + i0 + e];
-      }
+    for (int m = 0; m < C; m += 8) {  // dq += X K, dk += X^T Q - (Y + Y^T) K
+      const tf32::A16 x = tf32::load_a([&](int i, int y) { return X[(m0 + i) * LZ + m + y]; });
+      const tf32::A16 xt = tf32::load_a([&](int i, int y) { return X[(m + y) * LZ + m0 + i]; });
+      const tf32::A16 yy = tf32::load_a([&](int i, int y) {
+        return -(Y[(m0 + i) * LZ + m + y] + Y[(m + y) * LZ + m0 + i]);
+      });
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const int c = lane + 32 * j;
-        const float qv = c < d.dk ? Q[m * ld + c] : 0.f, kv = c < d.dk ? K[m * ld + c] : 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          aq[e][j] = fmaf(x[e], kv, aq[e][j]);
-          ak[e][j] = fmaf(xt[e], qv, fmaf(-yy[e], kv, ak[e][j]));
-        }
+        const int c0 = n0 + 32 * j;
+        if (c0 >= d.dk) continue;
+        const tf32::B8 kv = tf32::load_b<false>([&](int y, int c) { return K[(m + y) * ld + c0 + c]; });
+        const tf32::B8 qv = tf32::load_b<false>([&](int y, int c) { return Q[(m + y) * ld + c0 + c]; });
+        tf32::mma3<false>(aq[j], x, kv);
+        tf32::mma3<false>(ak[j], xt, qv);
+        tf32::mma3<false>(ak[j], yy, kv);
       }
     }
     if (warp == 0) {
       // token `lane`: the pairs (i >= t > j) by the running sum of column sums - row sums
       float rc = 0.f;
       for (int m = 0; m < C; ++m) rc += W[lane * LD + m] - W[m * LD + lane];
-      float x = dLx[lane] + rc, zz = dLz[lane];
+      float x = rc, zz = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        x += dLx[w][lane];
+        zz += dLz[w][lane];
+      }
       float acc = zz;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {  // suffix sum of x, prefix sum of z
@@ -570,15 +565,15 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(Args a) {
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    if (t0 + i0 + e >= d.T) break;
-    const size_t row = (kh * d.T + t0 + i0 + e) * d.dk;
+    const int i = i0 + 8 * (e >> 1);
+    const size_t row = (kh * d.T + t0 + i) * d.dk;
+    if (t0 + i >= d.T) continue;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int c = lane + 32 * j;
-      if (c < d.dk) {
-        static_cast<Tio*>(a.dq)[row + c] = from_f32<Tio>(aq[e][j]);
-        static_cast<Tio*>(a.dk_)[row + c] = from_f32<Tio>(ak[e][j]);
-      }
+      if (n0 + 32 * j >= d.dk) continue;
+      const int c = j0 + 32 * j + (e & 1);
+      static_cast<Tio*>(a.dq)[row + c] = from_f32<Tio>(aq[j][e]);
+      static_cast<Tio*>(a.dk_)[row + c] = from_f32<Tio>(ak[j][e]);
     }
   }
 }
@@ -594,7 +589,7 @@ cudaError_t set_smem(F f, size_t bytes) {
 template <typename Tio, int NJ>
 cudaError_t launch_grad(const Args& a, cudaStream_t st) {
   const size_t smem =
-      ((size_t)C * (2 * pad4(a.d.dk) + 3 * pad4(a.d.dv)) + 2 * kVB * a.d.dk) * sizeof(float);
+      ((size_t)C * (2 * pad4(a.d.dk) + 3 * pad4(a.d.dv)) + 2 * kVB * (a.d.dk + 8)) * sizeof(float);
   const cudaError_t e = set_smem(grad_kernel<Tio, NJ>, smem);
   if (e != cudaSuccess) return e;
   grad_kernel<Tio, NJ><<<chunks(a.d.T) * a.d.B * a.d.Hk, kThreads, smem, st>>>(a);

@@ -24,31 +24,54 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], const
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-// One warp: c += A B over k0 <= k < k1 (whole eights), A(row, k) for 16 rows, B(k, column) for 8
-// columns. c[0], c[1] are in row lane / 4 at columns 2 (lane % 4) and the next, c[2], c[3] eight
-// rows below. kExactB: B is exact in tf32 (bf16 values).
+// Operand fragments of one warp: 16 rows x 8 of A(row, k), 8 of B(k, column) x 8 columns. kExact:
+// the values are exact in tf32 (bf16 ones).
+struct A16 { uint32_t hi[4], lo[4]; };
+struct B8 { uint32_t hi[2], lo[2]; };
+template <typename F>
+__device__ __forceinline__ A16 load_a(F A) {
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  A16 a;
+  split(A(g, t), a.hi[0], a.lo[0]);
+  split(A(g + 8, t), a.hi[1], a.lo[1]);
+  split(A(g, t + 4), a.hi[2], a.lo[2]);
+  split(A(g + 8, t + 4), a.hi[3], a.lo[3]);
+  return a;
+}
+template <bool kExact, typename F>
+__device__ __forceinline__ B8 load_b(F B) {
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  B8 b;
+  if (kExact) {
+    b.hi[0] = __float_as_uint(B(t, g));
+    b.hi[1] = __float_as_uint(B(t + 4, g));
+  } else {
+    split(B(t, g), b.hi[0], b.lo[0]);
+    split(B(t + 4, g), b.hi[1], b.lo[1]);
+  }
+  return b;
+}
+// c += a b. c[0], c[1] are in row lane / 4 at columns 2 (lane % 4) and the next, c[2], c[3] eight
+// rows below.
+template <bool kExactB>
+__device__ __forceinline__ void mma3(float (&c)[4], const A16& a, const B8& b) {
+  if (!kExactB) mma(c, a.hi, b.lo);
+  mma(c, a.lo, b.hi);
+  mma(c, a.hi, b.hi);
+}
+
+// One warp: c += A B over k0 <= k < k1 (whole eights).
 template <bool kExactB, typename FA, typename FB>
 __device__ __forceinline__ void tile(float (&c)[4], int k0, int k1, FA A, FB B) {
-  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
   float big[4] = {0.f, 0.f, 0.f, 0.f}, s0[4] = {0.f, 0.f, 0.f, 0.f};
   float s1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (int k = k0; k < k1; k += 8) {
-    uint32_t ah[4], al[4], bh[2], bl[2];
-    split(A(g, k + t), ah[0], al[0]);
-    split(A(g + 8, k + t), ah[1], al[1]);
-    split(A(g, k + t + 4), ah[2], al[2]);
-    split(A(g + 8, k + t + 4), ah[3], al[3]);
-    if (kExactB) {
-      bh[0] = __float_as_uint(B(k + t, g));
-      bh[1] = __float_as_uint(B(k + t + 4, g));
-    } else {
-      split(B(k + t, g), bh[0], bl[0]);
-      split(B(k + t + 4, g), bh[1], bl[1]);
-    }
-    mma(big, ah, bh);
-    if (!kExactB) mma(s0, ah, bl);
-    mma(s1, al, bh);
+    const A16 a = load_a([&](int r, int kk) { return A(r, k + kk); });
+    const B8 b = load_b<kExactB>([&](int kk, int n) { return B(k + kk, n); });
+    mma(big, a.hi, b.hi);
+    if (!kExactB) mma(s0, a.hi, b.lo);
+    mma(s1, a.lo, b.hi);
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) c[e] += big[e] + (s0[e] + s1[e]);
