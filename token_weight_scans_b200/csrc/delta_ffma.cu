@@ -3,7 +3,8 @@
 //
 // Four kernels. The chunk-local part (Z, P) and the gradients of q, k and the gates
 // need no order among the chunks and run one CTA per chunk; only the two state
-// recurrences walk the chunks in order. The rows of S (and of dS) evolve
+// recurrences walk the chunks in order. All products are warp tiles of split tf32 operands
+// (tf32.cuh): float32 FMAs waited for shared memory. The rows of S (and of dS) evolve
 // independently given K, so a walk is cut into slices of kRows rows, one CTA each.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -24,7 +25,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 16;     // state rows per CTA of a walk
 __host__ __device__ constexpr int slices(int dv) { return (dv + kRows - 1) / kRows; }
-constexpr int LD = C + 1;     // row stride of a C x C matrix in shared memory
+// row strides of a C x C matrix in shared memory: read by columns; by rows and in tiles
+constexpr int LD = C + 1, LZ = C + 4;
 
 // Gates of one chunk. The running sum is kept in double: over a chunk of strong decays L
 // reaches -32 * 87, where a float32 sum would leave 1e-4 in the differences.
@@ -103,7 +105,7 @@ template <typename Tio>
 __global__ void __launch_bounds__(kThreads) prep_kernel(Args a) {
   extern __shared__ __align__(16) float sm[];
   __shared__ Gates g;
-  __shared__ float A[C * LD], Zs[C * LD];
+  __shared__ __align__(16) float A[C * LZ], Ab[C * LZ];
   const Dims& d = a.d;
   const int N = chunks(d.T), bh = blockIdx.x / N, n = blockIdx.x - bh * N;
   const int b = bh / d.H, h = bh - b * d.H;
@@ -116,16 +118,22 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(Args a) {
   load_tile(Q, ld, static_cast<const Tio*>(a.q) + kh * d.T * d.dk, t0, d.T, d.dk);
   __syncthreads();
   const size_t cc = ((size_t)bh * N + n) * C * C;
-  for (int i = warp; i < C; i += kWarps) {
-    float kk = 0.f, qk = 0.f;
-    for (int c = 0; c < d.dk; c += 4) {
-      const float4 kj = at4(K + lane * ld + c);
-      kk = dot4(at4(K + i * ld + c), kj, kk);
-      qk = dot4(at4(Q + i * ld + c), kj, qk);
+  {  // a tile of 16 x 8 of K K^T and Q K^T per warp
+    const int m0 = 16 * (warp & 1), n0 = 8 * (warp >> 1);
+    float kk[4] = {0.f, 0.f, 0.f, 0.f}, qk[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < d.dk; c += 8) {
+      const tf32::B8 kj = tf32::load_b<false>([&](int x, int j) { return K[(n0 + j) * ld + c + x]; });
+      tf32::mma3<false>(kk, tf32::load_a([&](int i, int x) { return K[(m0 + i) * ld + c + x]; }), kj);
+      tf32::mma3<false>(qk, tf32::load_a([&](int i, int x) { return Q[(m0 + i) * ld + c + x]; }), kj);
     }
-    const float m = lane <= i ? decay(g, i, lane) : 0.f;
-    A[i * LD + lane] = lane < i ? m * kk : 0.f;
-    a.sv.P[cc + i * C + lane] = lane <= i ? a.scale * m * qk : 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = m0 + (lane >> 2) + 8 * (e >> 1), j = n0 + 2 * (lane & 3) + (e & 1);
+      const float m = j <= i ? decay(g, i, j) : 0.f, x = j < i ? m * kk[e] : 0.f;
+      A[i * LZ + j] = x;
+      Ab[i * LZ + j] = -x * g.beta[j];
+      a.sv.P[cc + i * C + j] = a.scale * m * qk[e];
+    }
   }
   if (warp == kWarps - 1) {
     WalkGates* wg = reinterpret_cast<WalkGates*>(a.sv.gates) + (size_t)bh * N + n;
@@ -135,14 +143,22 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(Args a) {
     if (lane == 0) wg->GC = g.GC;
   }
   __syncthreads();
-  // Z_ij = A_ij - sum_{j<m<i} A_im beta_m Z_mj: lane j owns column j, row by row. A lane
-  // reads back only what it wrote itself.
+  // Z_ij = A_ij - sum_{j<m<i} A_im beta_m Z_mj: lane j owns column j (zero down to row j)
   if (warp == 0) {
+    float z[C];
+#pragma unroll
     for (int i = 0; i < C; ++i) {
-      float z = A[i * LD + lane];
-      for (int m = 0; m < i; ++m) z = fmaf(-A[i * LD + m] * g.beta[m], m > lane ? Zs[m * LD + lane] : 0.f, z);
-      Zs[i * LD + lane] = z;
-      a.sv.Z[cc + i * C + lane] = z;
+      float s0 = A[i * LZ + lane], s1 = 0.f;
+#pragma unroll
+      for (int m = 0; m < i; m += 4) {
+        const float4 b = at4(Ab + i * LZ + m);
+        s0 = fmaf(b.x, z[m], s0);
+        if (m + 1 < i) s1 = fmaf(b.y, z[m + 1], s1);
+        if (m + 2 < i) s0 = fmaf(b.z, z[m + 2], s0);
+        if (m + 3 < i) s1 = fmaf(b.w, z[m + 3], s1);
+      }
+      z[i] = s0 + s1;
+      a.sv.Z[cc + i * C + lane] = z[i];
     }
   }
 }
@@ -150,7 +166,6 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(Args a) {
 // ------------------------------------------------------------------ the walks
 // One chunk's inputs in shared memory, two stages: the next chunk's copies (cp.async, in the
 // I/O dtype) run while this one is worked on.
-constexpr int LZ = C + 4;     // row stride of Z and P: 16-byte rows, no bank conflicts
 constexpr int LV = kRows + 8; // of V: 16-byte pieces in both types
 
 template <typename Tio>
