@@ -92,6 +92,20 @@ CASES = [
     (1, 2, 1, 1000, 120, 136, "bf16", True, "docs"),
     (1, 2, 1, 257, 128, 40, "bf16", False, "none"),
     (2, 2, 1, 100, 136, 64, "bf16", True, "none"),
+    # the same with gates enough for the tensor-core gradients (few gates, or narrow heads with
+    # fewer than 8192, take the float32 kernels)
+    (20, 64, 32, 1, 128, 128, "bf16", True, "none"),
+    (9, 2, 2, 63, 128, 128, "bf16", True, "none"),
+    (9, 2, 2, 64, 128, 128, "bf16", False, "none"),
+    (9, 2, 1, 65, 128, 256, "bf16", True, "none"),
+    (3, 3, 1, 200, 128, 256, "bf16", True, "docs"),
+    (5, 2, 2, 130, 128, 128, "bf16", True, "empty"),
+    (5, 2, 2, 130, 128, 128, "bf16", True, "reset"),
+    (4, 2, 1, 150, 64, 64, "bf16", True, "docs"),
+    (5, 2, 2, 130, 72, 200, "bf16", True, "none"),
+    (3, 2, 1, 257, 128, 40, "bf16", False, "none"),
+    (8, 4, 2, 257, 40, 72, "bf16", True, "docs"),
+    (4, 8, 8, 257, 24, 136, "bf16", True, "none"),
     # few long scans, walked in segments
     (1, 2, 1, 1283, 128, 256, "bf16", True, "none"),
     (1, 2, 1, 1283, 128, 256, "bf16", False, "docs"),
@@ -145,7 +159,7 @@ def test_first_token_of_an_empty_state_has_no_gate_gradient(B, H, dtype, d):
 
 @pytest.mark.parametrize("dtype,dv", [("f32", 32), ("bf16", 128), ("bf16", 256)])
 def test_split_sequence_carries_the_state(dtype, dv):
-    B, H, Hk, T, dk, cut = 1, 2, 1, 150, 128 if dtype == "bf16" else 32, 77
+    B, H, Hk, T, dk, cut = 8 if dtype == "bf16" else 1, 2, 1, 150, 128 if dtype == "bf16" else 32, 77
     d = ref.draw(B, H, Hk, T, dk, dv, dtype, True, seed=4)
     g = dev(d)
     x = ref.f64(d)
@@ -202,6 +216,7 @@ def test_step_slots():
 
 @pytest.mark.parametrize("B,H,T,dk,dv,dtype", [
     (1, 2, 40, 32, 32, "f32"), (2, 2, 100, 136, 64, "bf16"), (2, 4, 100, 128, 128, "bf16"),
+    (4, 4, 100, 128, 128, "bf16"),
     (1, 2, 1283, 128, 256, "bf16"), (2, 2, 3, 64, 64, "bf16")])
 def test_a_reset_first_token_forgets_any_state(B, H, T, dk, dv, dtype):
     """What S0 or the pool holds, NaN and infinities among it, does not matter to a scan whose
@@ -229,7 +244,7 @@ def test_a_reset_first_token_forgets_any_state(B, H, T, dk, dv, dtype):
 @pytest.mark.parametrize("dtype,dk,dv", [("f32", 24, 40), ("bf16", 128, 128), ("bf16", 128, 256),
                                          ("bf16", 40, 72), ("bf16", 72, 136)])
 def test_outputs_stay_inside_their_buffers(dtype, dk, dv):
-    B, H, Hk, T = 1, 2, 2, 70
+    B, H, Hk, T = 8, 2, 2, 70
     d = dev(ref.draw(B, H, Hk, T, dk, dv, dtype, True, seed=6))
     args = [d[n] for n in NAMES]
     size = (B, H, Hk, T, dk, dv, code(dtype))
@@ -261,7 +276,7 @@ def test_outputs_stay_inside_their_buffers(dtype, dk, dv):
 def test_graph_replay_and_streams(dtype, dk, dv):
     """A captured pass replayed on new inputs, and a pass on another stream, give the bits of
     an eager pass; two graphs with their own workspaces do not disturb each other."""
-    B, H, Hk, T = 1, 4, 2, 200
+    B, H, Hk, T = 2, 4, 2, 200
     size = (B, H, Hk, T, dk, dv, code(dtype))
     sets = [dev(ref.draw(B, H, Hk, T, dk, dv, dtype, True, seed=s)) for s in (1, 2, 3)]
 
@@ -360,7 +375,7 @@ def test_the_layer_end_to_end():
 
 @pytest.mark.parametrize("site,want_ST", [(5, False), (5, True), (6, False)])
 def test_a_wait_that_runs_out_is_reported_and_leaves_the_device_usable(site, want_ST):
-    B, H, T, d = 1, 2, 300, 128
+    B, H, T, d = 1, 2, 600, 128
     g = dev(ref.draw(B, H, H, T, d, d, "bf16", True, seed=5))
     args = [g[n] for n in NAMES]
     size = (B, H, H, T, d, d, tw.BF16)
@@ -386,7 +401,7 @@ def test_a_wait_that_runs_out_is_reported_and_leaves_the_device_usable(site, wan
 
 def test_calls_on_a_stream_of_their_own():
     """stream=: the work goes to that stream, with buffers the call allocates itself."""
-    d = dev(ref.draw(1, 4, 2, 200, 128, 128, "bf16", True, seed=6))
+    d = dev(ref.draw(2, 4, 2, 200, 128, 128, "bf16", True, seed=6))
     args = [d[n] for n in NAMES]
     y0, S0 = tw.gradlev_delta_fwd(*args, d["S0"])
     g0 = tw.gradlev_delta_bwd(*args, d["dy"], d["S0"])

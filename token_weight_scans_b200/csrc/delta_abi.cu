@@ -29,13 +29,18 @@ Dims dims(int B, int H, int Hk, int T, int dk, int dv, gradlev_dtype dt) {
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// A gate's gradient is one dot product of two bf16-rounded rows: 4e-3 off over many gates (in
-// the 2-norm), but any single one that happens to be small may be much further off. Calls whose
-// gradients have at most kFewGates of them take the float32 kernels (90 us in place of 41 us
-// for B1 H4 T32 d128, forward and gradients); without gradients there is no such value.
-constexpr size_t kFewGates = 128;
+// The tensor-core kernels round their operands to bf16, the float32 kernels nothing but the
+// outputs. A gate's gradient is one dot product of two rounded rows: 4 to 4.8e-3 off over many
+// gates (in the 2-norm; the float32 kernels 1.7e-3), but any single one that happens to be small
+// may be much further off, so that calls of few gates, or of heads so narrow that the chunk's
+// triangular systems amplify, passed 5e-3 (6e-3 at 300 gates; 7.6e-3 at d_k 8). Calls with
+// gradients take the tensor cores from there on: kernels of forward and gradients at 1024 gates
+// of d_k 128 31 against 62 us (H16 T64) and 83 against 213 us (H1 T1024), at 8192 gates of
+// d_k 48 about 80 against 100 us. Without gradients only the narrowest heads leave them
+// (tc::shape_ok).
 bool use_tc(const Dims& d, bool gradients) {
-  return tc::shape_ok(d) && !(gradients && d.BH() * d.T <= kFewGates);
+  if (!tc::shape_ok(d)) return false;
+  return !gradients || d.BH() * d.T > (d.dk >= 64 ? 1024 : 8192);
 }
 
 size_t ckpt_bytes(const Dims& d) {
