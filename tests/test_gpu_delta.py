@@ -181,6 +181,7 @@ def test_split_sequence_carries_the_state(dtype, dv):
     (1, 2, 2, 1, 128, 128, "bf16"), (3, 4, 2, 1, 128, 256, "bf16"), (2, 2, 1, 9, 64, 64, "f32"),
     (2, 2, 1, 3, 32, 40, "f32"), (2, 2, 2, 2, 256, 33, "bf16"), (1, 1, 1, 4, 4, 1, "f32"),
     (9, 2, 2, 2, 100, 128, "bf16"),
+    (40, 32, 16, 2, 128, 100, "bf16"), (75, 32, 32, 1, 24, 130, "f32"),  # 8 rows per lane group
 ])
 def test_step(B, H, Hk, T, dk, dv, dtype):
     d = ref.draw(B, H, Hk, T, dk, dv, dtype, True, "docs" if T == 9 else "none", seed=dk + T)
