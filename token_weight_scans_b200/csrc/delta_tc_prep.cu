@@ -1,5 +1,6 @@
-// Tensor-core gated delta rule: the chunk-local matrices (delta_tc.h, struct Mats), one
-// CTA per (chunk, value head), three CTAs per SM (two where both SPLIT and BACK).
+// Tensor-core gated delta rule: the chunk-local matrices (delta_tc.h, struct Mats) of one
+// (chunk, value head) after the other, three persistent CTAs per SM (two where both SPLIT and
+// BACK).
 //
 // K K^T and Q K^T go through the tensor core; the unit lower triangular inverse
 // T0 = (I + A diag(beta))^-1 is formed in float32 by halves: 16 x 16 diagonal blocks by
@@ -15,6 +16,13 @@
 //   Wb_j = (1 / beta_j) sum_i T0_ij beta_i w_i k_i,   PT = (P diag(beta)) (T0 diag(1 / beta)).
 // beta = 0 would leave T0's column zero where T's column j needs A's: beta is taken at least
 // 2^-60 in size here, which puts T0, Pb and W off by no more than that.
+//
+// Measured (B8 H16 T4096 d 128, 8192 chunks): 195 us with the backward's matrices, 1408 bytes per
+// token or 3.8 TB/s; 190 us with the remainders in their place (B1 H16 T32768). What bounds it is
+// the chain of short steps through a chunk at 24 warps per SM: 46 % of the issue slots, 44 % of
+// the shared-memory pipe, 26 % of the tensor pipe, 30 % of the DRAM. Without the triangular
+// inverse's products it would take 162 us. Registers decide: products unrolled over their
+// terms spill and take 236 us in all.
 //
 // Waits: the in-flight TMA stores only read shared memory, so the CTA waits for that read
 // and not for their completion; the kernel boundary orders them for the walk.

@@ -9,7 +9,9 @@
 //
 // The first walk costs about as much again, so segments pay where the scans leave the GPU
 // idle: B1 H16 T32768 d_v 256 has 32 CTAs of 512 chunks without them, and with four segments
-// 144 and then 144 of 128 chunks.
+// 144 and then 144 of 128 chunks. Measured there: forward with the last state 344 us for the
+// first walk, 23 for the combination and 377 for the walk proper, of about 1480 in one piece;
+// backward 215, 23 and 286.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <atomic>
@@ -45,7 +47,7 @@ __device__ __forceinline__ void copy16(void* dst, const void* src) {
 
 // kRows rows of one scan through its segments: out[s] = out[s -+ 1] M (M^T) + L. Thread: column
 // c, kRows / 2 rows. BWD: from the last segment. The next segment's M lands while this one's is
-// used: read straight from memory a step took 12 us.
+// used (5 us a step; 12 us when it was read straight from memory).
 template <bool BWD, int kRows>
 __global__ void __launch_bounds__(kThreads) combine_kernel(Dims d, int nseg, const float* L,
                                                            const float* M, const float* S0,

@@ -25,6 +25,11 @@
 // layout of 8 x 8 fragments, transposed on the way to shared memory (stmatrix) so that tokens
 // become rows, and TMA stores. D^T and E^T stay as they are, a chunk's tokens contiguous.
 //
+// Measured (B8 H16 T4096 d 128, 128 CTAs of 64 chunks): forward 190 us, backward 180 us, of
+// 2304 and 2176 bytes per token: 6.3 TB/s, the measured copy bandwidth (6.47). Where HBM does
+// not bound it, a chunk takes 2.3 us (forward), 2.9 us with SPLIT: the chain, two products and
+// two passes of the state or D through registers.
+//
 // Each chunk's tiles come in three groups with a two-deep ring of their own, since they are
 // done with at different times: V (dY) with T0 (PT), W with Q, K with Pb.
 #include <cuda.h>

@@ -18,6 +18,8 @@
 // fraction of a turn matters, so inv_freq / 2 pi goes into a 64-bit binary fraction F once
 // per lane, and pos * F modulo 2^64 is that fraction, exact up to F's own rounding.
 //
+// Measured with 16 + 16 heads of 128, bf16: forward 110 us for B8 T4096 (537 MB, 4.9 TB/s),
+// backward 173 + 7 us (806 MB, 4.6 TB/s).
 // What the bandwidth needs is loads in flight: 8 rows of bf16 per lane group (kept as
 // loaded) at 16 warps per SM move 537 MB (B8 T4096, 16 + 16 heads of 128) in 110 us;
 // 4 rows at 24 warps took 128 us, and 4 unpacked rows at 20 warps 218 us.
