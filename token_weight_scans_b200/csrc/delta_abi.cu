@@ -35,8 +35,8 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // may be much further off, so that calls of few gates, or of heads so narrow that the chunk's
 // triangular systems amplify, passed 5e-3 (6e-3 at 300 gates; 7.6e-3 at d_k 8). Calls with
 // gradients take the tensor cores from there on: kernels of forward and gradients at 1024 gates
-// of d_k 128 31 against 62 us (H16 T64) and 83 against 213 us (H1 T1024), at 8192 gates of
-// d_k 48 about 80 against 100 us. Without gradients only the narrowest heads leave them
+// of d_k 128 31 against 62 us (H16 T64) and 83 against 213 us (H1 T1024); a call at 6888 gates
+// of d_k 48 83 against 93 us (H14 T492). Without gradients only the narrowest heads leave them
 // (tc::shape_ok).
 bool use_tc(const Dims& d, bool gradients) {
   if (!tc::shape_ok(d)) return false;
