@@ -587,6 +587,15 @@ def _delta_args(q, k, v, beta, log_alpha, scale):
     return (B, H, Hk, T, d_k, d_v, code), dev, dt, float(d_k ** -0.5 if scale is None else scale)
 
 
+@functools.lru_cache(maxsize=256)
+def _delta_need(size):
+    """For sizes and a dtype: the status of gradlev_delta_supported, the workspace bytes of the
+    forward and the backward, and the checkpoint bytes."""
+    L = lib()
+    return (int(L.gradlev_delta_supported(*size)), L.gradlev_delta_workspace_bytes(*size, 0),
+            L.gradlev_delta_workspace_bytes(*size, 1), L.gradlev_delta_ckpt_bytes(*size))
+
+
 def gradlev_delta_fwd(q, k, v, beta, log_alpha, S0=None, *, scale=None, y=None, ST=None,
                       want_ST=True, ckpt=None, workspace=None, stream=None):
     """Chunked gated delta rule (see include/gradlev.h): q, k [B,Hk,T,d_k], v [B,H,T,d_v],
@@ -597,7 +606,8 @@ def gradlev_delta_fwd(q, k, v, beta, log_alpha, S0=None, *, scale=None, y=None, 
     size, dev, dt, scale = _delta_args(q, k, v, beta, log_alpha, scale)
     B, H, _, T, d_k, d_v, _ = size
     f32 = torch.float32
-    _check(gradlev_delta_supported(*size), "gradlev_delta_fwd")
+    supported, need, _, need_ckpt = _delta_need(size)
+    _check(supported, "gradlev_delta_fwd")
     if S0 is not None:
         _check_fast("S0", S0, (B, H, d_v, d_k), f32, dev)
     if y is None:
@@ -609,8 +619,8 @@ def gradlev_delta_fwd(q, k, v, beta, log_alpha, S0=None, *, scale=None, y=None, 
     if ST is not None:
         _check_fast("ST", ST, (B, H, d_v, d_k), f32, dev)
     if ckpt is not None:
-        _check_buffer("ckpt", ckpt, gradlev_delta_ckpt_bytes(*size), dev)
-    ws = _workspace(gradlev_delta_workspace_bytes(*size, 0), dev, workspace)
+        _check_buffer("ckpt", ckpt, need_ckpt, dev)
+    ws = _workspace(need, dev, workspace)
     with _on(dev):
         st = lib().gradlev_delta_fwd(*size, _addr(q), _addr(k), _addr(v), _addr(beta),
                                      _addr(log_alpha), scale, _addr(S0), _addr(y), _addr(ST),
@@ -630,7 +640,8 @@ def gradlev_delta_bwd(q, k, v, beta, log_alpha, dy, S0=None, dST=None, *, scale=
     import torch
     size, dev, dt, scale = _delta_args(q, k, v, beta, log_alpha, scale)
     B, H, _, T, d_k, d_v, _ = size
-    _check(gradlev_delta_supported(*size), "gradlev_delta_bwd")
+    supported, _, need, need_ckpt = _delta_need(size)
+    _check(supported, "gradlev_delta_bwd")
     _check_fast("dy", dy, (B, H, T, d_v), dt, dev)
     if S0 is not None:
         _check_fast("S0", S0, (B, H, d_v, d_k), torch.float32, dev)
@@ -641,13 +652,14 @@ def gradlev_delta_bwd(q, k, v, beta, log_alpha, dy, S0=None, dST=None, *, scale=
                    dbeta=torch.empty((B, H, T), dtype=dt, device=dev),
                    dlog_alpha=torch.empty((B, H, T), dtype=dt, device=dev),
                    dS0=torch.empty((B, H, d_v, d_k), dtype=dt, device=dev) if want_dS0 else None)
-    _check_out(out, dict(dq=(q.shape, dt), dk=(k.shape, dt), dv=(v.shape, dt),
-                         dbeta=((B, H, T), dt), dlog_alpha=((B, H, T), dt)), dev)
-    if out.get("dS0") is not None:
-        _check_fast("out['dS0']", out["dS0"], (B, H, d_v, d_k), dt, dev)
+    else:
+        _check_out(out, dict(dq=(q.shape, dt), dk=(k.shape, dt), dv=(v.shape, dt),
+                             dbeta=((B, H, T), dt), dlog_alpha=((B, H, T), dt)), dev)
+        if out.get("dS0") is not None:
+            _check_fast("out['dS0']", out["dS0"], (B, H, d_v, d_k), dt, dev)
     if ckpt is not None:
-        _check_buffer("ckpt", ckpt, gradlev_delta_ckpt_bytes(*size), dev)
-    ws = _workspace(gradlev_delta_workspace_bytes(*size, 1), dev, workspace)
+        _check_buffer("ckpt", ckpt, need_ckpt, dev)
+    ws = _workspace(need, dev, workspace)
     with _on(dev):
         st = lib().gradlev_delta_bwd(
             *size, _addr(q), _addr(k), _addr(v), _addr(beta), _addr(log_alpha), scale, _addr(S0),
@@ -718,11 +730,17 @@ def _norm_args(q, k, wq, wk, pos, inv_freq, norm):
         raise GradlevError("q and k must be [B,T,H,d] tensors")
     if norm not in _NORMS:
         raise GradlevError(f"norm: {norm!r} is not one of {sorted(_NORMS)}")
-    B, T, Hq, d = q.shape
-    Hk = k.shape[2]
+    qs, ks = q.shape, k.shape
+    B, T, Hq, d = qs
+    Hk = ks[2]
     dev, dt = _cuda_device(q), q.dtype
-    sq = _strided("q", q, (B, T, Hq, d), dt, dev)
-    sk = _strided("k", k, (B, T, Hk, d), dt, dev)
+    qt, kt = q.stride(), k.stride()
+    # one expression for the usual case; _strided names what is wrong
+    if not (ks == (B, T, Hk, d) and k.dtype == dt and k.device == dev and
+            (d == 1 or (qt[3] == 1 and kt[3] == 1))):
+        _strided("q", q, (B, T, Hq, d), dt, dev)
+        _strided("k", k, (B, T, Hk, d), dt, dev)
+    sq, sk = _c_strides(qt, qs), _c_strides(kt, ks)
     for n, w in (("wq", wq), ("wk", wk)):
         if w is not None:
             _check_fast(n, w, (d,), torch.float32, dev)
