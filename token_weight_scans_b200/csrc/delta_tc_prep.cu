@@ -169,7 +169,6 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
   for (unsigned id = blockIdx.x; id < total; id += gridDim.x, full ^= 1) {
   const int bh = id / N, n = id - bh * N, t0 = n * C;
   if (tid == 0) {
-    tma_store_wait_read();  // the last chunk's results
     mbar_wait(&sm.full, full, wc, W_PREP_LOAD);
     tc_fence_after();
     const uint32_t id = idesc_bf16(64, 64, false, false);
@@ -181,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
       umma_bf16(tb + LANE16, desc_at(sw128_desc(sQ, 16, 1024), off), dk, id, kk > 0);
     }
     umma_commit(&sm.mma);
+    tma_store_wait_read();  // the last chunk's results, whose places are written from here on
   }
   __syncwarp();
   if (warp == 2) {
