@@ -494,3 +494,24 @@ def test_step_in_a_pool_past_32_bits():
     y = tw.gradlev_delta_step(*args, S, slots=at.int())
     want = tw.gradlev_delta_step(*args, g["S0"])
     assert torch.equal(y, want) and torch.equal(S[at], g["S0"]) and not S[1:pool - 1].any()
+
+
+def test_calls_at_once_on_two_streams():
+    """Passes that overlap on the GPU, a workspace each (their own allocations): the bits of passes
+    one after the other."""
+    sets = [dev(ref.draw(2, 4, h, 700, 128, d, "bf16", True, seed=20 + h)) for h, d in ((4, 128), (2, 256))]
+
+    def one(d, stream=None):
+        args = [d[n] for n in NAMES]
+        y, ST = tw.gradlev_delta_fwd(*args, d["S0"], stream=stream)
+        return dict(tw.gradlev_delta_bwd(*args, d["dy"], d["S0"], stream=stream), y=y, ST=ST)
+
+    alone = [one(d) for d in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        got = [one(d, st) for d, st in zip(sets, streams)]
+    torch.cuda.synchronize()
+    for g, a in zip(got, alone):
+        for n in a:
+            assert torch.equal(g[n], a[n]), n
