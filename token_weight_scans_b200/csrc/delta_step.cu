@@ -67,18 +67,21 @@ __global__ void __launch_bounds__(kWarps * 32) step_kernel(StepArgs a) {
   const Tio* qg = static_cast<const Tio*>(a.q) + kt * dk;
   const Tio* kg = static_cast<const Tio*>(a.k) + kt * dk;
   const Tio* vg = static_cast<const Tio*>(a.v) + (size_t)bh * a.T * a.dv;
+  // The sums over a group's lanes go by halves: an exchange leaves each lane with half of the values
+  // (those of S'k in the lower lanes, of S'q in the upper ones), until each has one row's.
+  constexpr int kHalf = LPR / 2, kSpread = kHalf / kRows;  // lanes per row in either half
+  static_assert(kSpread >= 1 && kSpread * kRows == kHalf, "a lane ends with one value");
+  const int own = nb + (gl & (kHalf - 1)) / kSpread;
   // a token's vectors, loaded one token ahead (the first while the slot is looked up)
   float4 qn[NK4], kn[NK4];
-  float vn[kRows], bn, ln;
+  float vn, bn, ln;  // v of this lane's own row (below)
   auto load_token = [&](int t) {
 #pragma unroll
     for (int i = 0; i < NK4; ++i) {
       qn[i] = kok[i] ? load4(qg + (size_t)t * dk + 4 * (gl + LPR * i)) : zero;
       kn[i] = kok[i] ? load4(kg + (size_t)t * dk + 4 * (gl + LPR * i)) : zero;
     }
-#pragma unroll
-    for (int r = 0; r < kRows; ++r)
-      vn[r] = nb + r < a.dv ? to_f32(vg[(size_t)t * a.dv + nb + r]) : 0.f;
+    vn = own < a.dv ? to_f32(vg[(size_t)t * a.dv + own]) : 0.f;
     bn = a.beta[(size_t)bh * a.T + t];
     ln = a.log_alpha[(size_t)bh * a.T + t];
   };
@@ -119,11 +122,10 @@ __global__ void __launch_bounds__(kWarps * 32) step_kernel(StepArgs a) {
     const float be = bn, la = ln;
     const bool reset = la < kResetLog;  // whatever the state held, NaN among it, is gone
     const float al = expf(la);
-    float vv[kRows];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) vv[r] = vn[r];
+    const float vv = vn;
     if (t + 1 < a.T) load_token(t + 1);
     kq = group_sum<LPR>(kq);
+    float p[2 * kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       float pk = 0.f, pq = 0.f;
@@ -140,9 +142,27 @@ __global__ void __launch_bounds__(kWarps * 32) step_kernel(StepArgs a) {
         pk = fmaf(s[r][i].w, kv[i].w, pk);
         pq = fmaf(s[r][i].w, qv[i].w, pq);
       }
-      const float c = be * (vv[r] - group_sum<LPR>(pk));
-      const float y = a.scale * fmaf(c, kq, group_sum<LPR>(pq));
-      if (gl == r && nb + r < a.dv) yg[(size_t)t * a.dv + nb + r] = from_f32<Tio>(y);
+      p[r] = pk;
+      p[kRows + r] = pq;
+    }
+#pragma unroll
+    for (int m = kRows, o = kHalf; m >= 1; m >>= 1, o >>= 1) {
+      const bool up = gl & o;
+#pragma unroll
+      for (int e = 0; e < m; ++e) {
+        const float give = up ? p[e] : p[m + e];
+        p[e] = (up ? p[m + e] : p[e]) + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+    }
+#pragma unroll
+    for (int o = kSpread / 2; o > 0; o >>= 1) p[0] += __shfl_xor_sync(0xffffffffu, p[0], o);
+    // lower lanes: c = beta (v - S'k); upper lanes: y = scale (S'q + c k.q)
+    const float own_c = be * (vv - p[0]), c_low = __shfl_xor_sync(0xffffffffu, own_c, kHalf);
+    if (gl >= kHalf && gl % kSpread == 0 && own < a.dv)
+      yg[(size_t)t * a.dv + own] = from_f32<Tio>(a.scale * fmaf(c_low, kq, p[0]));
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const float c = __shfl_sync(0xffffffffu, own_c, r * kSpread, LPR);
 #pragma unroll
       for (int i = 0; i < NK4; ++i) {
         s[r][i].x = fmaf(c, kv[i].x, s[r][i].x);
@@ -172,9 +192,10 @@ template <typename Tio, int LPR, int NK4>
 void launch(const StepArgs& a, cudaStream_t st) {
   constexpr int rows = kWarps * (32 / LPR);  // per row of a lane group
   const int c4 = a.B * a.H * ((a.dv + 4 * rows - 1) / (4 * rows));
-  const int c8 = a.B * a.H * ((a.dv + 8 * rows - 1) / (8 * rows));
+  constexpr int big = LPR >= 16 ? 8 : 4;
+  const int c8 = a.B * a.H * ((a.dv + big * rows - 1) / (big * rows));
   if (c8 >= 148 * 16)
-    launch_rows<Tio, LPR, NK4, 8>(a, c8, st);
+    launch_rows<Tio, LPR, NK4, big>(a, c8, st);
   else
     launch_rows<Tio, LPR, NK4, 4>(a, c4, st);
 }
