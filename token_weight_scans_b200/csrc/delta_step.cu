@@ -3,12 +3,12 @@
 // owns kRows rows and keeps them in float32 registers across the T tokens of the call.
 // y needs no second pass over the updated row:
 //   S' = a S,  e = v - S' k,  y = scale (S' q + beta e (k.q)),  S <- S' + beta e k^T,
-// so a token costs one round of butterfly sums (S'k, S'q and k.q together).
+// so a token costs one round of sums over the lanes (S'k, S'q and k.q together).
 //
-// Bound by memory: S is read once and written once per call, everything else is small: 134 MB
-// for 64 x 16 heads of 128 x 128, 30 us or 4.4 TB/s (a lane group's chain of loads, sums and
-// stores has 16 warps per SM to hide it). A single request's 16 heads take 3.2 us, the latency of
-// that chain.
+// Bound by memory: S is read once and written once per call, everything else is small: 118 MB
+// for 56 requests (and 8 padding rows) of 16 heads of 128 x 128, 24.2 us or 4.9 TB/s (30 us with
+// a butterfly for every row, which costs 80 exchanges where the halves take 25). A single
+// request's 16 heads take 3.2 us, the latency of loads, sums and stores.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -186,8 +186,8 @@ void launch_rows(const StepArgs& a, int ctas, cudaStream_t st) {
   count_launch();
 }
 // 8 rows per lane group keep more loads in flight, once there are CTAs enough all the same: with
-// 64 x 16 heads of 128 x 128 34.8 us against 37.9 us with 4, but 14.3 us against 10.2 us with
-// 4 x 8 heads of 64 x 64 (5 tokens; both between events, caches flushed).
+// 64 x 16 heads of 128 x 128 24.2 us against 24.8 us with 4 (float32, 3 tokens: 36.0 against
+// 37.8 us), but 6.1 us against 5.6 us with 4 x 8 heads of 64 x 64 (5 tokens; caches flushed).
 template <typename Tio, int LPR, int NK4>
 void launch(const StepArgs& a, cudaStream_t st) {
   constexpr int rows = kWarps * (32 / LPR);  // per row of a lane group
