@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dep_wait();
   load_slice(first_head(blockIdx.x), blockIdx.x % N, 0, &sm.gates[0]);
   load_kq(blockIdx.x);
   __syncwarp();
@@ -503,8 +504,10 @@ static cudaError_t launch(const CUtensorMap (&m)[9], const GradParams& p, unsign
     set.fetch_or(bit);
   }
   const unsigned most = 2 * 148;
-  grad_kernel<GROUP><<<work < most ? work : most, kThreads, kSmem, st>>>(m[0], m[1], m[2], m[3], m[4],
-                                                                        m[5], m[6], m[7], m[8], p);
+  const cudaError_t e =
+      launch_after(p.d, grad_kernel<GROUP>, work < most ? work : most, kThreads, kSmem, st, m[0], m[1], m[2],
+                   m[3], m[4], m[5], m[6], m[7], m[8], p);
+  if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
 }

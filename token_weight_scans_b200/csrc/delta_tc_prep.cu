@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
     tma_load_3d(sm.Q, &tmQ, &sm.full, 0, t0, kh);
     tma_load_3d(sm.Q + TILE, &tmQ, &sm.full, 64, t0, kh);
   };
+  grid_dep_launch();
   RawGates raw{};
   auto load_raw = [&](unsigned id) {  // warp 2
     const int bh = id / N;

@@ -17,6 +17,7 @@
 #include <atomic>
 
 #include "delta_tc.h"
+#include "sm100.cuh"
 
 namespace gradlev {
 namespace delta {
@@ -67,6 +68,8 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(Dims d, int nseg, con
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  sm100::grid_dep_wait();
+  sm100::grid_dep_launch();
   const bool use_S0 = S0 && !(log_alpha[(size_t)bh * d.T] < kResetLog);
   float s[kRows / 2];
 #pragma unroll
@@ -122,9 +125,11 @@ cudaError_t combine(const Args& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     set.fetch_or(bit);
   }
-  combine_kernel<BWD, kRows><<<(unsigned)(a.d.BH() * (dvp(a.d) / kRows)), kThreads,
-                               combine_smem<kRows>(), st>>>(
-      a.d, a.seg.nseg, a.loc, a.M, a.S0, a.log_alpha, static_cast<const bf16*>(a.dST), a.init);
+  const cudaError_t e = launch_after(
+      a.d, combine_kernel<BWD, kRows>, (unsigned)(a.d.BH() * (dvp(a.d) / kRows)), kThreads,
+      combine_smem<kRows>(), st, a.d, a.seg.nseg, (const float*)a.loc, (const float*)a.M, a.S0,
+      a.log_alpha, static_cast<const bf16*>(a.dST), a.init);
+  if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
 }
@@ -170,11 +175,11 @@ cudaError_t launch_combine(const Args& a, bool backward, cudaStream_t st) {
 // ---------------------------------------------------------------- the kernels in order
 static cudaError_t walk(const Args& a, bool backward, bool split, cudaStream_t st) {
   if (a.seg.nseg > 1) {
-    cudaError_t e = launch_walk(a, backward, split, true, st);
+    cudaError_t e = launch_walk(a, backward, split, true, !backward, st);
     if (e == cudaSuccess) e = launch_combine(a, backward, st);
     if (e != cudaSuccess) return e;
   }
-  return launch_walk(a, backward, split, false, st);
+  return launch_walk(a, backward, split, false, !backward || a.seg.nseg > 1, st);
 }
 
 cudaError_t run_fwd(const Args& a, cudaStream_t st) {

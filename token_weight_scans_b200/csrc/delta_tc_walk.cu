@@ -296,6 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dep_wait();  // nothing before this line reads or writes global memory
+  grid_dep_launch();
   const uint32_t tb = sm.tmem_base;
 
   if (warp == 0 || warp == 3) {
@@ -797,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool BWD, bool SPLIT>
-static cudaError_t launch(const Args& a, bool sum, cudaStream_t st) {
+static cudaError_t launch(const Args& a, bool sum, bool after, cudaStream_t st) {
   using L = Layout<BWD, SPLIT>;
   using gradlev::tc::make_map_bf16_3d;
   const Dims& d = a.d;
@@ -845,15 +847,22 @@ static cudaError_t launch(const Args& a, bool sum, cudaStream_t st) {
   } else if (!BWD && nseg > 1 && a.sv.S) {
     grid += (unsigned)bh;  // the last segment's map, for the backward
   }
-  walk_kernel<BWD, SPLIT><<<grid, kThreads, L::smem, st>>>(
-      mq, mk, mv, mw, mwl, mt, mtl, mp, ms, my, md, p);
+  if (after) {
+    const cudaError_t e = launch_after(d, walk_kernel<BWD, SPLIT>, grid, kThreads, L::smem, st, mq, mk, mv,
+                                       mw, mwl, mt, mtl, mp, ms, my, md, p);
+    if (e != cudaSuccess) return e;
+  } else {
+    walk_kernel<BWD, SPLIT><<<grid, kThreads, L::smem, st>>>(mq, mk, mv, mw, mwl, mt, mtl, mp, ms, my,
+                                                             md, p);
+  }
   count_launch();
   return cudaGetLastError();
 }
 
-cudaError_t launch_walk(const Args& a, bool backward, bool split, bool sum, cudaStream_t st) {
-  if (backward) return launch<true, false>(a, sum, st);
-  return split ? launch<false, true>(a, sum, st) : launch<false, false>(a, sum, st);
+cudaError_t launch_walk(const Args& a, bool backward, bool split, bool sum, bool after,
+                        cudaStream_t st) {
+  if (backward) return launch<true, false>(a, sum, after, st);
+  return split ? launch<false, true>(a, sum, after, st) : launch<false, false>(a, sum, after, st);
 }
 
 }  // namespace tc
