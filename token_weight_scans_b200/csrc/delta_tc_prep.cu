@@ -17,15 +17,15 @@
 // beta = 0 would leave T0's column zero where T's column j needs A's: beta is taken at least
 // 2^-60 in size here, which puts T0, Pb and W off by no more than that.
 //
-// Measured (B8 H16 T4096 d 128, 8192 chunks): 195 us with the backward's matrices, 1408 bytes per
-// token or 3.8 TB/s; 190 us with the remainders in their place (B1 H16 T32768). What bounds it is
+// Measured (B8 H16 T4096 d 128, 8192 chunks): 185 us with the backward's matrices, 1408 bytes per
+// token or 4.0 TB/s; 190 us with the remainders in their place (B1 H16 T32768). What bounds it is
 // the chain of short steps through a chunk at 24 warps per SM: 46 % of the issue slots, 44 % of
 // the shared-memory pipe, 26 % of the tensor pipe, 30 % of the DRAM. Without the triangular
-// inverse's products it would take 162 us. Registers decide: products unrolled over their
-// terms spill and take 236 us in all.
+// inverse's products it would take 30 us less. Registers decide: products unrolled over their
+// terms spill and take 40 us more.
 //
 // Waits: the in-flight TMA stores only read shared memory, so the CTA waits for that read
-// and not for their completion; the kernel boundary orders them for the walk.
+// and not for their completion; the end of the kernel, which the walk waits for, orders them.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
