@@ -63,9 +63,11 @@ struct PrepSmem {
   };
   float X[C * LD];             // T0
   uint8_t P[OWN_P ? 2 * TILE : 16];
-  // per token: with m in the middle of the chunk M_ij = ra_i ca_j where that stays in range
-  // (fac); bt is beta, at least kTiny in size: cN = ca bt, cP = scale ca bt, wb = w bt, rb = 1 / bt
-  float ra[C], cN[C], cP[C];
+  // per token: M_ij = ra_i ca_j with both factors within e^40 (fac: all decays of the chunk within
+  // e^80, and the factors taken from the middle of that range, so that ca kTiny stays a normal
+  // number: a factor taken from a token, e^-80 kTiny, would underflow and take dbeta with it where
+  // beta = 0); bt is beta, at least kTiny in size: cb = ca bt, wb = w bt, rb = 1 / bt
+  float ra[C], cb[C];
   float Lh[C], Ll[C], G[C], wb[C], rb[C];
   int seg[C];
   int fac;
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
   if (warp == 2) {
     const GatePair g = chunk_gates(raw);
     if (id + gridDim.x < total) load_raw(id + gridDim.x);
-    const float Lm = __shfl_sync(0xffffffffu, g.Lh[0], 31), Ll = __shfl_sync(0xffffffffu, g.Ll[0], 31);
+    const float Lm = 0.5f * g.Lend, Ll = 0.5f * g.Lend_lo;
     const bool fac = g.seg_end == 0 && g.Lend > -80.f;
     GateBlock* gb = reinterpret_cast<GateBlock*>(p.m.gates) + (size_t)bh * N + n;
     if (lane == 0) {
@@ -201,8 +203,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
       const float x = (g.Lh[k] - Lm) + (g.Ll[k] - Ll);
       const float ca = fac ? expf(-x) : 1.f;
       sm.ra[i] = fac ? expf(x) : 1.f;
-      sm.cN[i] = ca * bt;
-      sm.cP[i] = ca * bt * p.scale;
+      sm.cb[i] = ca * bt;
       sm.Lh[i] = g.Lh[k];
       sm.Ll[i] = g.Ll[k];
       sm.seg[i] = g.seg[k];
@@ -235,9 +236,10 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
     tmem_ld_wait();
     // the entries below (P: and on) the diagonal
     const int keep = i - 32 * hh + (isP ? 1 : 0);
+    const float sc = isP ? p.scale : 1.f;
     if (sm.fac) {
-      const float ra = sm.ra[i];
-      const float* cv = (isP ? sm.cP : sm.cN) + 32 * hh;
+      const float ra = sc * sm.ra[i];
+      const float* cv = sm.cb + 32 * hh;
 #pragma unroll
       for (int e = 0; e < 32; e += 4) {
         const float4 c = at4(cv + e);
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
         const int j = 32 * hh + e;
-        const float m = (isP ? sm.cP : sm.cN)[j] * expf(fminf((Lh - sm.Lh[j]) + (Ll - sm.Ll[j]), 0.f));
+        const float m = sc * sm.cb[j] * expf(fminf((Lh - sm.Lh[j]) + (Ll - sm.Ll[j]), 0.f));
         v[e] = e < keep && sm.seg[j] == seg ? v[e] * m : 0.f;
       }
     }
