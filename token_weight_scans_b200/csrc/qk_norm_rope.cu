@@ -62,13 +62,14 @@ struct NormArgs {
 
 struct F8 { float v[V]; };   // columns [ca, ca + 4), [cb, cb + 4)
 
-// A lane's columns of a row as loaded: rows in flight cost half the registers that way.
+// A lane's columns of a row as loaded: rows in flight cost half the registers that way. Plain
+// loads: the gradients may be written over the rows they are formed from.
 template <typename Tio> struct Raw;
 template <> struct Raw<__nv_bfloat16> {
   uint2 a, b;
   __device__ __forceinline__ void load(const __nv_bfloat16* pa, const __nv_bfloat16* pb) {
-    a = __ldg(reinterpret_cast<const uint2*>(pa));
-    b = __ldg(reinterpret_cast<const uint2*>(pb));
+    a = *reinterpret_cast<const uint2*>(pa);
+    b = *reinterpret_cast<const uint2*>(pb);
   }
   __device__ __forceinline__ void zero() { a = b = make_uint2(0u, 0u); }
   __device__ __forceinline__ F8 get() const {
@@ -85,8 +86,8 @@ template <> struct Raw<__nv_bfloat16> {
 template <> struct Raw<float> {
   float4 a, b;
   __device__ __forceinline__ void load(const float* pa, const float* pb) {
-    a = __ldg(reinterpret_cast<const float4*>(pa));
-    b = __ldg(reinterpret_cast<const float4*>(pb));
+    a = *reinterpret_cast<const float4*>(pa);
+    b = *reinterpret_cast<const float4*>(pb);
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ F8 get() const { return F8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}}; }
