@@ -176,6 +176,27 @@ def _stream_ptr(stream, device=None):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _on_stream(call, stream, *args, **named):
+    """`call` with the given stream current, so that what it allocates comes from that stream's
+    memory: a block of the current stream's may still be in use by kernels queued there, which the
+    given stream does not wait for. The tensors that come back are used by the caller's stream as
+    well, and what the caller lent by the given one, so both hold their memory until they are done
+    with it."""
+    import torch
+    dev = _cuda_device(args[0])
+    if stream.device != dev:
+        raise GradlevError(f"stream is on {stream.device}, the tensors on {dev}")
+    with torch.cuda.stream(stream):
+        result = call(*args, **named)
+    held = result.values() if isinstance(result, dict) else \
+        result if isinstance(result, tuple) else (result,)
+    for t in (*held, named.get("ckpt"), named.get("workspace")):
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
+            t.record_stream(torch.cuda.current_stream(dev))
+    return result
+
+
 def _cuda_device(x):
     """The device of x, which must be a CUDA device: the library's kernels dereference
     every pointer on the GPU, so host memory is refused here, before any call."""
@@ -241,6 +262,9 @@ def _dims(x, g):
 
 def gradlev_scan_fwd(x, g, eta, alpha, W0, *, y=None, ckpt=None, workspace=None, stream=None):
     """Forward scan on the GPU. Returns y [B,H,T,d_out] (dtype of x)."""
+    if stream is not None:
+        return _on_stream(gradlev_scan_fwd, stream, x, g, eta, alpha, W0, y=y, ckpt=ckpt,
+                          workspace=workspace)
     import torch
     B, H, T, d_in, d_out = _dims(x, g)
     dev, dt = _cuda_device(x), x.dtype
@@ -261,7 +285,7 @@ def gradlev_scan_fwd(x, g, eta, alpha, W0, *, y=None, ckpt=None, workspace=None,
     with torch.cuda.device(dev):  # launches go to the tensors' device
         st = lib().gradlev_scan_fwd(B, H, T, d_in, d_out, code, _ptr(x), _ptr(g), _ptr(eta),
                                     _ptr(alpha), _ptr(W0), _ptr(y), _ptr(ckpt), _ptr(ws),
-                                    ws.numel() * ws.element_size(), _stream_ptr(stream, dev))
+                                    ws.numel() * ws.element_size(), _stream_ptr(None, dev))
     _check(st, "gradlev_scan_fwd")
     return y
 
@@ -269,6 +293,9 @@ def gradlev_scan_fwd(x, g, eta, alpha, W0, *, y=None, ckpt=None, workspace=None,
 def gradlev_scan_bwd(x, g, eta, alpha, W0, dy, *, ckpt=None, workspace=None, stream=None,
                      out=None):
     """Reverse scan on the GPU. Returns dict dx, dg, deta, dalpha, dW0."""
+    if stream is not None:
+        return _on_stream(gradlev_scan_bwd, stream, x, g, eta, alpha, W0, dy, ckpt=ckpt,
+                          workspace=workspace, out=out)
     import torch
     B, H, T, d_in, d_out = _dims(x, g)
     dev, dt = _cuda_device(x), x.dtype
@@ -297,7 +324,7 @@ def gradlev_scan_bwd(x, g, eta, alpha, W0, dy, *, ckpt=None, workspace=None, str
                                     _ptr(alpha), _ptr(W0), _ptr(dy), _ptr(out["dx"]),
                                     _ptr(out["dg"]), _ptr(out["deta"]), _ptr(out["dalpha"]),
                                     _ptr(out["dW0"]), _ptr(ckpt), _ptr(ws),
-                                    ws.numel() * ws.element_size(), _stream_ptr(stream, dev))
+                                    ws.numel() * ws.element_size(), _stream_ptr(None, dev))
     _check(st, "gradlev_scan_bwd")
     return out
 
@@ -313,6 +340,9 @@ def gradlev_scan_fwd_state(x, g, eta, alpha, W0, S0=None, *, y=None, ST=None, ck
                            workspace=None, stream=None):
     """Forward scan continuing from the carried deviation S0 ([B,H,d_out,d_in] float32,
     None = 0). Returns (y, ST), ST the deviation after the last token."""
+    if stream is not None:
+        return _on_stream(gradlev_scan_fwd_state, stream, x, g, eta, alpha, W0, S0, y=y, ST=ST,
+                          ckpt=ckpt, workspace=workspace)
     import torch
     B, H, T, d_in, d_out = _dims(x, g)
     dev, dt = _cuda_device(x), x.dtype
@@ -338,7 +368,7 @@ def gradlev_scan_fwd_state(x, g, eta, alpha, W0, S0=None, *, y=None, ST=None, ck
         st = lib().gradlev_scan_fwd_state(B, H, T, d_in, d_out, code, _ptr(x), _ptr(g), _ptr(eta),
                                           _ptr(alpha), _ptr(W0), _ptr(S0), _ptr(y), _ptr(ST),
                                           _ptr(ckpt), _ptr(ws), ws.numel() * ws.element_size(),
-                                          _stream_ptr(stream, dev))
+                                          _stream_ptr(None, dev))
     _check(st, "gradlev_scan_fwd_state")
     return y, ST
 
@@ -348,6 +378,9 @@ def gradlev_scan_bwd_state(x, g, eta, alpha, W0, dy, S0=None, LamT=None, *, ckpt
     """Reverse scan with the carried state: S0 the start deviation of the forward (read only
     without ckpt), LamT the adjoint flowing in after the last token (both [B,H,d_out,d_in]
     float32, None = 0). Returns dict dx, dg, deta, dalpha, dW0, dS0."""
+    if stream is not None:
+        return _on_stream(gradlev_scan_bwd_state, stream, x, g, eta, alpha, W0, dy, S0, LamT,
+                          ckpt=ckpt, workspace=workspace, out=out)
     import torch
     B, H, T, d_in, d_out = _dims(x, g)
     dev, dt = _cuda_device(x), x.dtype
@@ -380,7 +413,7 @@ def gradlev_scan_bwd_state(x, g, eta, alpha, W0, dy, S0=None, LamT=None, *, ckpt
                                           _ptr(out["dx"]), _ptr(out["dg"]), _ptr(out["deta"]),
                                           _ptr(out["dalpha"]), _ptr(out["dW0"]), _ptr(out["dS0"]),
                                           _ptr(ckpt), _ptr(ws), ws.numel() * ws.element_size(),
-                                          _stream_ptr(stream, dev))
+                                          _stream_ptr(None, dev))
     _check(st, "gradlev_scan_bwd_state")
     return out
 
@@ -389,6 +422,9 @@ def gradlev_decode_step(x, v, eta, alpha, W0, S, *, y=None, g=None, want_g=True,
     """Deployment decode of the T tokens of x in order, from the carried deviation S
     ([B,H,d_out,d_in] float32, updated in place). Returns (y, g): outputs and costates
     [B,H,T,d_out] (g is None when want_g is False and no buffer is given)."""
+    if stream is not None:
+        return _on_stream(gradlev_decode_step, stream, x, v, eta, alpha, W0, S, y=y, g=g,
+                          want_g=want_g)
     import torch
     B, H, T, d_in, d_out = _dims(x, v)
     dev, dt = _cuda_device(x), x.dtype
@@ -409,7 +445,7 @@ def gradlev_decode_step(x, v, eta, alpha, W0, S, *, y=None, g=None, want_g=True,
     with torch.cuda.device(dev):  # launches go to the tensors' device
         st = lib().gradlev_decode_step(B, H, T, d_in, d_out, _dt_code(dt), _ptr(x), _ptr(v),
                                        _ptr(eta), _ptr(alpha), _ptr(W0), _ptr(S), _ptr(y), _ptr(g),
-                                       _stream_ptr(stream, dev))
+                                       _stream_ptr(None, dev))
     _check(st, "gradlev_decode_step")
     return y, g
 
@@ -423,6 +459,9 @@ def gradlev_consistency_step(x, ghat, eta, alpha, W0, v, lam=1.0, *, want_dv=Tru
     """One training step of the adapted layer from predicted costates ghat (see
     include/gradlev.h). Returns dict y, gtil, loss_tok, loss_c, dx, dghat, deta, dalpha, dW0
     and dv (None when want_dv is False)."""
+    if stream is not None:
+        return _on_stream(gradlev_consistency_step, stream, x, ghat, eta, alpha, W0, v, lam,
+                          want_dv=want_dv, workspace=workspace, out=out)
     import torch
     B, H, T, d_in, d_out = _dims(x, ghat)
     dev, dt = _cuda_device(x), x.dtype
@@ -460,7 +499,7 @@ def gradlev_consistency_step(x, ghat, eta, alpha, W0, v, lam=1.0, *, want_dv=Tru
             _ptr(v), float(lam), _ptr(out["y"]), _ptr(out["gtil"]), _ptr(out["loss_tok"]),
             _ptr(out["loss_c"]), _ptr(out["dx"]), _ptr(out["dghat"]), _ptr(out["deta"]),
             _ptr(out["dalpha"]), _ptr(out["dW0"]), _ptr(out.get("dv")), _ptr(ws),
-            ws.numel() * ws.element_size(), _stream_ptr(stream, dev))
+            ws.numel() * ws.element_size(), _stream_ptr(None, dev))
     _check(st, "gradlev_consistency_step")
     return out
 
@@ -473,6 +512,9 @@ def gradlev_mlp2_recon(x, g1hat, g2hat, v, eta, alpha, W1, W2, control=False, *,
                        workspace=None, stream=None, out=None):
     """Parallel reconstruction of the two-layer adapted MLP from given costates (see
     include/gradlev.h). Returns dict a, h, y, g2til, g1til, dW1."""
+    if stream is not None:
+        return _on_stream(gradlev_mlp2_recon, stream, x, g1hat, g2hat, v, eta, alpha, W1, W2,
+                          control, workspace=workspace, out=out)
     import torch
     if x.dim() != 4 or v.dim() != 4 or W1.dim() != 3:
         raise GradlevError("x, v must be [B,H,T,d] and W1 [H,d_h,d_x]")
@@ -506,7 +548,7 @@ def gradlev_mlp2_recon(x, g1hat, g2hat, v, eta, alpha, W1, W2, control=False, *,
             B, H, T, d_x, d_h, d_y, code, _ptr(x), _ptr(g1hat), _ptr(g2hat), _ptr(v), _ptr(eta),
             _ptr(alpha), _ptr(W1), _ptr(W2), 1 if control else 0, _ptr(out["a"]), _ptr(out["h"]),
             _ptr(out["y"]), _ptr(out["g2til"]), _ptr(out["g1til"]), _ptr(out["dW1"]), _ptr(ws),
-            ws.numel() * ws.element_size(), _stream_ptr(stream, dev))
+            ws.numel() * ws.element_size(), _stream_ptr(None, dev))
     _check(st, "gradlev_mlp2_recon")
     return out
 
@@ -527,23 +569,10 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream_of(stream, dev):
-    """The raw cudaStream_t: the given stream, which must be on `dev`, or dev's current one."""
+def _stream_of(dev):
+    """dev's current stream as a raw cudaStream_t."""
     import torch
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index)
-    if stream.device != dev:
-        raise GradlevError(f"stream is on {stream.device}, the tensors on {dev}")
-    return stream.cuda_stream
-
-
-def _lend(stream, *tensors):
-    """Tensors that a call allocated on the current stream and works on in another: their memory
-    must not be handed out again before that stream is done with it."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _check_fast(name, t, shape, dtype, device):
@@ -602,6 +631,9 @@ def gradlev_delta_fwd(q, k, v, beta, log_alpha, S0=None, *, scale=None, y=None, 
     beta and log_alpha [B,H,T] float32, S0 [B,H,d_v,d_k] float32 or None (zero). scale None:
     d_k ** -0.5. Returns (y, ST), ST the float32 state after the last token (None when
     want_ST is False and no buffer is given)."""
+    if stream is not None:
+        return _on_stream(gradlev_delta_fwd, stream, q, k, v, beta, log_alpha, S0, scale=scale,
+                          y=y, ST=ST, want_ST=want_ST, ckpt=ckpt, workspace=workspace)
     import torch
     size, dev, dt, scale = _delta_args(q, k, v, beta, log_alpha, scale)
     B, H, _, T, d_k, d_v, _ = size
@@ -625,8 +657,7 @@ def gradlev_delta_fwd(q, k, v, beta, log_alpha, S0=None, *, scale=None, y=None, 
         st = lib().gradlev_delta_fwd(*size, _addr(q), _addr(k), _addr(v), _addr(beta),
                                      _addr(log_alpha), scale, _addr(S0), _addr(y), _addr(ST),
                                      _addr(ckpt), _addr(ws), ws.numel() * ws.element_size(),
-                                     _stream_of(stream, dev))
-    _lend(stream, y, ST, ws)
+                                     _stream_of(dev))
     _check(st, "gradlev_delta_fwd")
     return y, ST
 
@@ -637,6 +668,9 @@ def gradlev_delta_bwd(q, k, v, beta, log_alpha, dy, S0=None, dST=None, *, scale=
     dlog_alpha and dS0 (None when want_dS0 is False). dST [B,H,d_v,d_k] (I/O dtype, None = 0)
     is the gradient of the last state; ckpt the buffer a forward call on the same inputs
     filled (None: the states are recomputed from S0)."""
+    if stream is not None:
+        return _on_stream(gradlev_delta_bwd, stream, q, k, v, beta, log_alpha, dy, S0, dST,
+                          scale=scale, ckpt=ckpt, want_dS0=want_dS0, workspace=workspace, out=out)
     import torch
     size, dev, dt, scale = _delta_args(q, k, v, beta, log_alpha, scale)
     B, H, _, T, d_k, d_v, _ = size
@@ -665,8 +699,7 @@ def gradlev_delta_bwd(q, k, v, beta, log_alpha, dy, S0=None, dST=None, *, scale=
             *size, _addr(q), _addr(k), _addr(v), _addr(beta), _addr(log_alpha), scale, _addr(S0),
             _addr(dy), _addr(dST), _addr(out["dq"]), _addr(out["dk"]), _addr(out["dv"]),
             _addr(out["dbeta"]), _addr(out["dlog_alpha"]), _addr(out.get("dS0")), _addr(ckpt),
-            _addr(ws), ws.numel() * ws.element_size(), _stream_of(stream, dev))
-    _lend(stream, ws, *out.values())
+            _addr(ws), ws.numel() * ws.element_size(), _stream_of(dev))
     _check(st, "gradlev_delta_bwd")
     return out
 
@@ -677,6 +710,9 @@ def gradlev_delta_step(q, k, v, beta, log_alpha, S, *, slots=None, scale=None, y
     place. slots [B] int32 picks each batch row's state (None: row b); a row without a state
     of its own (slot outside the pool, or named by an earlier row) answers with zeros.
     Returns y [B,H,T,d_v]."""
+    if stream is not None:
+        return _on_stream(gradlev_delta_step, stream, q, k, v, beta, log_alpha, S, slots=slots,
+                          scale=scale, y=y)
     import torch
     size, dev, dt, scale = _delta_args(q, k, v, beta, log_alpha, scale)
     B, H, _, T, d_k, d_v, _ = size
@@ -692,8 +728,7 @@ def gradlev_delta_step(q, k, v, beta, log_alpha, S, *, slots=None, scale=None, y
     with _on(dev):
         st = lib().gradlev_delta_step(*size, _addr(q), _addr(k), _addr(v), _addr(beta),
                                       _addr(log_alpha), scale, _addr(slots), S.shape[0], _addr(S),
-                                      _addr(y), _stream_of(stream, dev))
-    _lend(stream, y)
+                                      _addr(y), _stream_of(dev))
     _check(st, "gradlev_delta_step")
     return y
 
@@ -759,6 +794,9 @@ def gradlev_qk_norm_rope_fwd(q, k, wq=None, wk=None, pos=None, inv_freq=None, *,
     with contiguous columns, e.g. views of one packed projection). Returns (yq [B,Hq,T,d],
     yk [B,Hk,T,d]), contiguous. norm "l2" or "rms"; wq, wk [d] float32 or None; pos [B,T]
     int32 or None (t); inv_freq [rot/2] float32 or None (no rotation)."""
+    if stream is not None:
+        return _on_stream(gradlev_qk_norm_rope_fwd, stream, q, k, wq, wk, pos, inv_freq,
+                          norm=norm, eps=eps, yq=yq, yk=yk)
     import torch
     a, dev, dt, sq, sk = _norm_args(q, k, wq, wk, pos, inv_freq, norm)
     B, T, Hq, Hk, d = a[:5]
@@ -773,8 +811,7 @@ def gradlev_qk_norm_rope_fwd(q, k, wq=None, wk=None, pos=None, inv_freq=None, *,
     with _on(dev):
         st = lib().gradlev_qk_norm_rope_fwd(*a, float(eps), _addr(q), sq, _addr(k), sk, _addr(wq),
                                             _addr(wk), _addr(pos), _addr(inv_freq), _addr(yq),
-                                            _addr(yk), _stream_of(stream, dev))
-    _lend(stream, yq, yk)
+                                            _addr(yk), _stream_of(dev))
     _check(st, "gradlev_qk_norm_rope_fwd")
     return yq, yk
 
@@ -784,6 +821,9 @@ def gradlev_qk_norm_rope_bwd(dyq, dyk, q, k, wq=None, wk=None, pos=None, inv_fre
     """Gradients of gradlev_qk_norm_rope_fwd from dyq [B,Hq,T,d] and dyk [B,Hk,T,d]. Returns
     dict dq, dk (shaped like q and k; strided when given in `out`) and dwq, dwk for the
     weights that are given."""
+    if stream is not None:
+        return _on_stream(gradlev_qk_norm_rope_bwd, stream, dyq, dyk, q, k, wq, wk, pos, inv_freq,
+                          norm=norm, eps=eps, workspace=workspace, out=out)
     import torch
     a, dev, dt, sq, sk = _norm_args(q, k, wq, wk, pos, inv_freq, norm)
     B, T, Hq, Hk, d = a[:5]
@@ -809,8 +849,7 @@ def gradlev_qk_norm_rope_bwd(dyq, dyk, q, k, wq=None, wk=None, pos=None, inv_fre
             _addr(pos), _addr(inv_freq), _addr(out["dq"]), sdq, _addr(out["dk"]), sdk,
             _addr(out["dwq"] if wq is not None else None),
             _addr(out["dwk"] if wk is not None else None), _addr(ws),
-            ws.numel() * ws.element_size() if ws is not None else 0, _stream_of(stream, dev))
-    _lend(stream, ws, *out.values())
+            ws.numel() * ws.element_size() if ws is not None else 0, _stream_of(dev))
     _check(st, "gradlev_qk_norm_rope_bwd")
     return out
 
