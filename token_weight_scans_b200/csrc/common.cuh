@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <atomic>
 
 #include "gradlev.h"
 
@@ -30,5 +31,24 @@ struct DeviceStatus {
 // count, every kernel launch adds one.
 void count_launch();
 void reset_launch_count();
+
+// Opts a kernel whose dynamic shared memory depends on the call's sizes into all that the device
+// has, once per device (`done`: one bit each, a static of that kernel). The limit belongs to the
+// kernel, not to the call: set to a call's own size, another host thread's narrower call could
+// lower it again between this call's setting and its launch, which then fails.
+inline cudaError_t allow_smem(const void* kernel, std::atomic<uint64_t>& done) {
+  int dev = 0, most = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (done.load() & bit)) return cudaSuccess;
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             most - (int)fa.sharedSizeBytes);
+  if (e == cudaSuccess) done.fetch_or(bit);
+  return e;
+}
 
 }  // namespace gradlev

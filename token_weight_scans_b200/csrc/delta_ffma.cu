@@ -600,17 +600,18 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(Args a) {
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// The 48 KB that need no opt-in hold the static arrays too.
-template <typename F>
-cudaError_t set_smem(F f, size_t bytes) {
-  return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+// The shared memory of these kernels depends on d_k and d_v, so the opt-in is to all there is.
+template <auto kKernel>
+cudaError_t allow() {
+  static std::atomic<uint64_t> done{0};
+  return allow_smem(reinterpret_cast<const void*>(kKernel), done);
 }
 
 template <typename Tio, int NJ>
 cudaError_t launch_grad(const Args& a, cudaStream_t st) {
   const size_t smem =
       ((size_t)C * (2 * pad4(a.d.dk) + 3 * pad4(a.d.dv)) + 2 * kVB * (a.d.dk + 8)) * sizeof(float);
-  const cudaError_t e = set_smem(grad_kernel<Tio, NJ>, smem);
+  const cudaError_t e = allow<grad_kernel<Tio, NJ>>();
   if (e != cudaSuccess) return e;
   grad_kernel<Tio, NJ><<<chunks(a.d.T) * a.d.B * a.d.Hk, kThreads, smem, st>>>(a);
   count_launch();
@@ -621,13 +622,13 @@ template <typename Tio>
 cudaError_t fwd_t(const Args& a, cudaStream_t st) {
   const Dims& d = a.d;
   const size_t sp = (size_t)2 * C * pad4(d.dk) * sizeof(float);
-  cudaError_t e = set_smem(prep_kernel<Tio>, sp);
+  cudaError_t e = allow<prep_kernel<Tio>>();
   if (e != cudaSuccess) return e;
   prep_kernel<Tio><<<chunks(d.T) * d.B * d.H, kThreads, sp, st>>>(a);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const size_t sf = walk_smem<Tio>(d.dk);
-  if ((e = set_smem(walk_kernel<Tio, false>, sf)) != cudaSuccess) return e;
+  if ((e = allow<walk_kernel<Tio, false>>()) != cudaSuccess) return e;
   walk_kernel<Tio, false><<<slices(d.dv) * d.B * d.H, kThreads, sf, st>>>(a);
   count_launch();
   return cudaGetLastError();
@@ -637,7 +638,7 @@ template <typename Tio>
 cudaError_t bwd_t(const Args& a, cudaStream_t st) {
   const Dims& d = a.d;
   const size_t sf = walk_smem<Tio>(d.dk);
-  cudaError_t e = set_smem(walk_kernel<Tio, true>, sf);
+  cudaError_t e = allow<walk_kernel<Tio, true>>();
   if (e != cudaSuccess) return e;
   walk_kernel<Tio, true><<<slices(d.dv) * d.B * d.H, kThreads, sf, st>>>(a);
   count_launch();
