@@ -435,8 +435,8 @@ template <typename Tio>
 static cudaError_t launch_outer_sum_t(const void* g1, const void* x, float* dW1, int BH, int T,
                                       int dh, int dx, cudaStream_t st) {
   const size_t smem = sizeof(float) * (size_t)FC * ((dh + 4) + (dx + 4));
-  cudaError_t e = cudaFuncSetAttribute(outer_sum_kernel<Tio>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(outer_sum_kernel<Tio>), done);
   if (e != cudaSuccess) return e;
   outer_sum_kernel<Tio><<<BH, FT, smem, st>>>(static_cast<const Tio*>(g1),
                                               static_cast<const Tio*>(x), dW1, T, dh, dx);
@@ -453,8 +453,8 @@ cudaError_t launch_outer_sum(const void* g1, const void* x, float* dW1, int BH, 
 template <typename Tio>
 static cudaError_t launch_tquery_t(const TqueryArgs& a, cudaStream_t st) {
   const size_t smem = layout(a.dx, a.dh, a.dy).total * sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(tquery_kernel<Tio>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(tquery_kernel<Tio>), done);
   if (e != cudaSuccess) return e;
   tquery_kernel<Tio><<<a.B * a.H, FT, smem, st>>>(a);
   count_launch();
