@@ -77,11 +77,12 @@ cudaError_t fwd_run(const Dims& d, const void* q, const void* k, const void* v, 
                     char* saved, char* ws, cudaStream_t st) {
   if (use_tc(d, saved != nullptr)) {
     tc::Args a{d, q, k, v, beta, log_alpha, scale, reinterpret_cast<DeviceStatus*>(ws),
-               kWaitTimeoutNs, tc::mats_at(ws + kStatusBytes, d)};
+               kWaitTimeoutNs, tc::mats_at(ws + kStatusBytes, d, saved != nullptr)};
     if (saved) {
       a.sv = tc::saved_at(saved, d);
-      a.m.Wb = a.sv.Wb;
-      a.m.PT = a.sv.PT;
+      a.m.Kw = a.sv.Kw;
+      a.m.Wq = a.sv.Wq;
+      a.m.Pv = a.sv.Pv;
       a.m.gates = a.sv.gates;
     }
     a.S0 = S0;
@@ -183,6 +184,10 @@ gradlev_status gradlev_delta_bwd(int B, int H, int Hk, int T, int d_k, int d_v, 
     delta::tc::Args a{d, q, k, v, beta, log_alpha, scale, reinterpret_cast<DeviceStatus*>(ws),
                kWaitTimeoutNs};
     a.sv = delta::tc::saved_at(saved, d);
+    a.m.Kw = a.sv.Kw;
+    a.m.Wq = a.sv.Wq;
+    a.m.Pv = a.sv.Pv;
+    a.m.gates = a.sv.gates;
     a.dy = dy;
     a.dST = dST;
     a.E = reinterpret_cast<delta::tc::bf16*>(scratch);

@@ -21,8 +21,6 @@ namespace gradlev {
 namespace tc {
 bool make_map_bf16_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                       uint32_t box1);
-bool make_map_bf16_3d_box(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
-                          uint32_t box0, uint32_t box1);
 }
 
 namespace delta {
@@ -46,34 +44,56 @@ __host__ __device__ inline int dvp(const Dims& d) { return d.dv <= 128 ? 128 : 2
 
 using bf16 = __nv_bfloat16;
 
-// Chunk-local matrices that the walks read, all bf16 with N*64 rows per (b, h). With T0 =
-// I - Z diag(beta) and T = I - diag(beta) Z, the inverses of the two directions:
-//   W  [64][128] = -T0 diag(G) K      (D = T0 V + S W)
-//   T0 [64][64],  Pb [64][64] = P diag(beta)
-//   Wb [64][128] = T^T diag(w) K      (E = PT^T dY + dS Wb)
-//   PT [64][64]  = P T
-// lo parts: the remainders of W and T0, for a forward whose last state is asked for.
+// Where keys are alike, the errors D of a chunk nearly cancel in P diag(beta) D and D^T K: each
+// token takes back what the one before it wrote. A rounding of D, P, T0 or -T0 diag(G) K would be
+// summed up over the chunk, unlike the values it sits on (y 1 to 5 %, dlog_alpha 20 % and more off
+// where keys have a mean cosine of 0.9). So the triangular system is folded into the matrices that
+// follow it, before anything is rounded. With R = V - diag(G) K S^T, the errors against the state
+// at the chunk's start,
+//   Kw = T0^T diag(beta w) K,   Pv = P diag(beta) T0,   Wq = scale diag(G) Q - Pv diag(G) K,
+//   S <- G_C S + R^T Kw,        Y = Pv V + Wq S^T,      D = T0 R,
+// and backwards
+//   diag(beta) E = Pv^T dY + Kw dS^T,
+//   dS <- G_C dS + dY^T Wq - (Kw dS^T)^T diag(G) K.
+// A row of Kw, Pv or Wq is what is left of a token after all the ones that follow (precede) it, no
+// longer than beta (scale) times a key, and its rounding counts like one of v itself: 2^-9 once.
+// Only the gradients' per-token sums over a chunk (the grad kernel) need D and E apart, there as
+// two bf16 each.
+// beta is taken at least 2^-60 in size (bt): row j of Kw and column j of Pv carry it as a factor,
+// and E_j is that of beta E divided by bt.
+//
+// Chunk-local matrices that the walks read, all bf16 with N*64 rows per (b, h):
+//   Kw, Wq [64][128]; Kwlo, the remainder of Kw, for a forward whose last state is asked for;
+//   Pv [64][64 | 64], its remainder behind it (written for the backward alone);
+//   T0 [64][64 | 64] likewise, for the D that the backward needs.
 struct Mats {
-  bf16 *W = nullptr, *Wlo = nullptr, *T0 = nullptr, *T0lo = nullptr, *Pb = nullptr;
-  bf16 *Wb = nullptr, *PT = nullptr;
+  bf16 *Kw = nullptr, *Kwlo = nullptr, *Wq = nullptr, *Pv = nullptr, *T0 = nullptr;
   float* gates = nullptr;   // [B*H][N] GateBlock
 };
 
-// The gates of a chunk as the kernels after prep read them (bulk copies of whole pieces).
+// The gates of a chunk as the kernels after prep read them (bulk copies of whole pieces: forward
+// walk nG .. GC, gradients GC .. cb, backward walk GCb .. zb).
 struct GateBlock {
-  float bw[C];        // beta w
+  float nG[C];        // -G
+  float z[C];         // beta / bt: 1, but 0 where beta = 0
   float GC, fac;      // fac != 0: M_ij = ra_i ca_j
   float pad[2];
+  float bw[C];        // beta w
   float q[C];         // scale G
   float bG[C];        // -beta G
   float be[C];        // beta
   float ra[C], cb[C]; // cb = ca beta
+  float GCb, padb[3];
+  float zG[C];        // -G beta / bt
+  float rb[C];        // 1 / bt
+  float zb[C];        // beta / bt
 };
 
 // What the forward keeps for the backward: chunk-start states S [B*H][N][dvp][128], D^T
-// [B*H][N][dvp][64] (the tokens of a chunk contiguous, as the walk has them), Wb, PT and gates.
+// [B*H][N][2][dvp][64] (bf16 and remainder, the tokens of a chunk contiguous, as the walk has
+// them), Kw, Wq, Pv and gates.
 struct Saved {
-  bf16 *S = nullptr, *D = nullptr, *Wb = nullptr, *PT = nullptr;
+  bf16 *S = nullptr, *D = nullptr, *Kw = nullptr, *Wq = nullptr, *Pv = nullptr;
   float *gates = nullptr, *M = nullptr;  // M: the segments' maps, with segments
 };
 
@@ -84,10 +104,10 @@ struct SegPlan {
 SegPlan seg_plan(const Dims& d);
 size_t saved_bytes(const Dims& d);
 Saved saved_at(char* base, const Dims& d);
-size_t fwd_scratch_bytes(const Dims& d);  // W, Wlo, T0, T0lo, Pb, gates
-Mats mats_at(char* base, const Dims& d);
+size_t fwd_scratch_bytes(const Dims& d);  // Mats
+Mats mats_at(char* base, const Dims& d, bool saved);  // saved: what is not part of Saved
 size_t bwd_scratch_bytes(const Dims& d);  // E and the chunk-end gradients of the state
-size_t token_rows_bytes(const Dims& d);   // one of D^T, E^T
+size_t token_rows_bytes(const Dims& d);   // D^T or E^T, both parts
 
 struct Args {
   Dims d;

@@ -6,14 +6,16 @@
 // Products of one value head (M = 64 tokens each; two share their TMEM columns, one in the
 // lower and one in the upper 16 lanes of each 32):
 //   F = dY D^T, H = E D^T (contracted over d_v)       t = dY S, u = E S, z = D dS
-//   X = scale M beta_j F,  Yn = -M beta_i beta_j H    (bf16, shared memory)
+//   X = scale M beta_j F,  Yn = -M beta_i beta_j H
 //   xk = X K,  yk = Yn K,  ka = X^T Q + Yn^T K
 //   dQ += scale G t + xk,  dK += -beta G u + beta w z + ka + yk
 // The pairs' share of dlog_alpha needs only row and column sums of X q.k - Y k.k, which
 // are dot products of q and k with xk, yk and ka:
 //   row - column = q.xk + k.yk - k.ka.
-// Row and column sums come from the same bf16 X and Yn, so the parts that cancel over a
+// Row and column sums come from the same X and Yn, so the parts that cancel over a
 // range of tokens do so to float32 rounding.
+// D, E, X and Yn are two bf16 each: their terms cancel in all of these sums where keys are alike.
+// With one bf16 in their place dq and dk are 1 %, dlog_alpha 4 to 90 % off there.
 //
 // Measured: 295 us for B8 H16 T4096 d 128 (2816 bytes per token: 5.0 TB/s), 440 us for B1 H16
 // T32768 d_v 256 (4608 bytes: 5.5 TB/s), 293 us where four heads share a key head. 43 % of the
@@ -42,25 +44,33 @@ constexpr uint32_t kCols = 256;
 constexpr uint32_t COL_A = 0;     // t | u, then . | yk
 constexpr uint32_t COL_B = 128;   // F, H (64 columns each) | z, then xk | ka
 
+struct GradGates {                           // GC .. cb of GateBlock
+  float GC, fac, pad[2], bw[C], q[C], bG[C], be[C], ra[C], cb[C];
+  static constexpr size_t offset = offsetof(GateBlock, GC);
+};
+static_assert(sizeof(GradGates) % 16 == 0 && GradGates::offset % 16 == 0 &&
+              GradGates::offset + sizeof(GradGates) == offsetof(GateBlock, GCb), "a bulk copy");
+
 struct GradSmem {
   uint8_t Q[2 * TILE], K[2 * TILE];          // k-blocks; at the end dq and dk
   uint8_t O[TILE];                           // dY: 64 tokens x 64 columns of d_v
-  uint8_t D[TILE], E[TILE];                  // D^T, E^T: 64 rows of d_v x 64 tokens
   uint8_t S[2 * TILE], dS[2 * TILE];         // 64 rows of d_v x 128
-  uint8_t X[TILE], Yn[TILE];
-  GateBlock gates[2];                        // this head's and the next one's
+  // D^T, E^T: 64 rows of d_v x 64 tokens, with their remainders; once the products of the last
+  // slice have read them, X and Yn
+  uint8_t D[2 * TILE], E[2 * TILE];
+  GradGates gates[2];                        // this head's and the next one's
   float Lh[C], Ll[C];                        // where a reset or strong decays rule out g.fac
   int seg[C];
   float xs[2][C], ps[2][C], zs[2][C];        // per column half
   float red[8];
-  uint64_t kq, full, mma;
+  uint64_t kq, full, de, mma;
   uint32_t tmem_base;
   int abort;
 };
 constexpr size_t kSmem = sizeof(GradSmem) + 1024;
 static_assert(2 * kSmem <= 227 * 1024, "two CTAs per SM");
 
-enum : uint32_t { W_G_KQ = 0xa01, W_G_FULL, W_G_MMA, W_G_DRAIN };
+enum : uint32_t { W_G_KQ = 0xa01, W_G_FULL, W_G_DE, W_G_MMA, W_G_DRAIN };
 
 struct GradParams {
   Dims d;
@@ -103,6 +113,18 @@ __device__ __forceinline__ void row8(float (&x)[8], const uint8_t* tile, int r, 
   }
 }
 
+// 8 values as two bf16 each, into a pair of tiles
+__device__ __forceinline__ void put_split8(uint32_t at, const float* x) {
+  uint32_t hi[4], rest[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    hi[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+    rest[e] = pack_bf16(x[2 * e] - bf16_lo(hi[e]), x[2 * e + 1] - bf16_hi(hi[e]));
+  }
+  st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
+  st_shared_v4(at + TILE, rest[0], rest[1], rest[2], rest[3]);
+}
+
 __device__ __forceinline__ void tmem_ld(uint32_t at, float (&v)[8]) { tmem_ld8(at, v); }
 __device__ __forceinline__ void tmem_ld(uint32_t at, float (&v)[16]) { tmem_ld16(at, v); }
 
@@ -128,33 +150,41 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int T = p.d.T, N = chunks(T), grp = GROUP ? p.d.H / p.d.Hk : 1;
   const unsigned total = (unsigned)((size_t)p.d.B * p.d.Hk * N);
   const WaitCtx wc{&sm.abort, p.status, p.timeout_ns};
-  uint32_t lfull = 0, lkq = 0;  // loads so far
+  uint32_t lfull = 0, lde = 0, lkq = 0;  // loads so far
   auto first_head = [&](unsigned id) {
     const int kh = id / N, b = kh / p.d.Hk;
     return b * p.d.H + (kh - b * p.d.Hk) * grp;
   };
-  // Tiles of 64 columns of d_v and, with the first, the gates: one copy for the first lane of each
-  // warp (issuing one takes about 100 cycles). A copy may land before thread 0 has announced it.
-  auto load_slice = [&](int bh, int n, int sl, GateBlock* gates) {
+  // Tiles of 64 columns of d_v: dY, S and dS and, with the first, the gates; and D and E, whose place
+  // is free later. One copy for the first lane of a warp (issuing one takes about 100 cycles). A
+  // copy may land before its barrier has been told.
+  auto load_slice = [&](int bh, int n, int sl, GradGates* gates) {
     ++lfull;
     if (lane != 0) return;
     const int w = warp & 1;
     if (warp == 0) {
-      mbar_arrive_expect_tx(&sm.full, 7 * TILE + (sl == 0 ? (uint32_t)sizeof(GateBlock) : 0u));
+      mbar_arrive_expect_tx(&sm.full, 5 * TILE + (sl == 0 ? (uint32_t)sizeof(GradGates) : 0u));
       tma_load_3d(sm.O, &tmO, &sm.full, 64 * sl, n * C, bh);
     } else if (warp == 1) {
-      tma_load_3d(sm.D, &tmD, &sm.full, 0, 64 * sl, bh * N + n);
-    } else if (warp == 2) {
-      tma_load_3d(sm.E, &tmE, &sm.full, 0, 64 * sl, bh * N + n);
-    } else if (warp == 3) {
       if (sl == 0)
-        bulk_load(gates, p.gates + ((size_t)bh * N + n) * (sizeof(GateBlock) / sizeof(float)),
-                  sizeof(GateBlock), &sm.full);
-    } else if (warp < 6) {
+        bulk_load(gates,
+                  reinterpret_cast<const char*>(p.gates) + ((size_t)bh * N + n) * sizeof(GateBlock) +
+                      GradGates::offset,
+                  sizeof(GradGates), &sm.full);
+    } else if (warp >= 4 && warp < 6) {
       tma_load_3d(sm.S + w * TILE, &tmS, &sm.full, 64 * w, 64 * sl, bh * N + n);
-    } else {
+    } else if (warp >= 6) {
       tma_load_3d(sm.dS + w * TILE, &tmdS, &sm.full, 64 * w, 64 * sl, bh * N + n);
     }
+  };
+  const int rows = dvp(p.d);
+  auto load_de = [&](int bh, int n, int sl) {
+    ++lde;
+    if (lane != 0 || warp >= 4) return;
+    const int w = warp & 1;
+    if (warp == 0) mbar_arrive_expect_tx(&sm.de, 4 * TILE);
+    tma_load_3d((warp < 2 ? sm.D : sm.E) + w * TILE, warp < 2 ? &tmD : &tmE, &sm.de, 0,
+                w * rows + 64 * sl, bh * N + n);
   };
   // Tiles of Q (warps 4 and 5) and K (6 and 7)
   uint8_t* const kq_tile = (warp < 6 ? sm.Q : sm.K) + (warp & 1) * TILE;
@@ -169,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     sm.abort = 0;
     mbar_init(&sm.kq, 4);
     mbar_init(&sm.full, 1);
+    mbar_init(&sm.de, 1);
     mbar_init(&sm.mma, 1);
     fence_mbar_init();
   }
@@ -182,15 +213,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_after();
   grid_dep_wait();
   load_slice(first_head(blockIdx.x), blockIdx.x % N, 0, &sm.gates[0]);
+  load_de(first_head(blockIdx.x), blockIdx.x % N, 0);
   load_kq(blockIdx.x);
   __syncwarp();
   const uint32_t tb = sm.tmem_base;
-  const uint32_t sQ = smem_u32(sm.Q), sK = smem_u32(sm.K), sX = smem_u32(sm.X), sY = smem_u32(sm.Yn);
+  const uint32_t sQ = smem_u32(sm.Q), sK = smem_u32(sm.K), sX = smem_u32(sm.D), sY = smem_u32(sm.E);
   const uint32_t id_f = idesc_bf16(64, 64, false, true), id_h = idesc_bf16(64, 64, true, true);
   const uint32_t id_t = idesc_bf16(64, 128, false, true);
   const uint32_t id_m = idesc_bf16(64, 128, true, true);
   constexpr int XW = GROUP ? 8 : 16;  // columns of X and Yn at a time, as the registers allow
-  uint32_t nfull = 0, nmma = 0, nkq = 0, nhead = 0;  // phases and heads so far
+  uint32_t nfull = 0, nde = 0, nmma = 0, nkq = 0, nhead = 0;  // phases and heads so far
 
   bool stop = false;
   for (unsigned id = blockIdx.x; id < total; id += gridDim.x) {
@@ -201,10 +233,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   for (int hv = 0; hv < grp; ++hv, ++nhead) {
     const int bh = bh0 + hv;
-    const GateBlock& g = sm.gates[nhead & 1];
+    const GradGates& g = sm.gates[nhead & 1];
+    int bh1 = bh, n1 = n, sl1 = 0;  // the next slice
     F2 ss = f2(0.f, 0.f);  // <dS, S>
     for (int sl = 0; sl < nsl; ++sl) {
       mbar_wait(&sm.full, nfull++ & 1, wc, W_G_FULL);
+      mbar_wait(&sm.de, nde++ & 1, wc, W_G_DE);
       __syncwarp();
       if (tid == 0) {
         tc_fence_after();
@@ -215,13 +249,19 @@ __global__ void __launch_bounds__(kThreads, 2)
           const uint64_t ao = desc_at(sw128_desc(sO, 16, 1024), kk * 32);
           const uint64_t ad = desc_at(sw128_desc(sD, TILE, 1024), kk * 2048);
           const uint64_t ae = desc_at(sw128_desc(sE, TILE, 1024), kk * 2048);
+          const uint64_t adl = desc_at(ad, TILE), ael = desc_at(ae, TILE);  // the remainders
           const uint64_t bs = desc_at(sw128_desc(smem_u32(sm.S), TILE, 1024), kk * 2048);
           const uint64_t bd = desc_at(sw128_desc(smem_u32(sm.dS), TILE, 1024), kk * 2048);
           umma_bf16(tb + COL_B, ao, ad, id_f, on);                  // F
+          umma_bf16(tb + COL_B, ao, adl, id_f, 1);
           umma_bf16(tb + COL_B + 64, ae, ad, id_h, on);             // H
+          umma_bf16(tb + COL_B + 64, ae, adl, id_h, 1);
+          umma_bf16(tb + COL_B + 64, ael, ad, id_h, 1);
           umma_bf16(tb + COL_A, ao, bs, id_t, on);                  // t
           umma_bf16(tb + COL_A + LANE16, ae, bs, id_m, on);         // u
+          umma_bf16(tb + COL_A + LANE16, ael, bs, id_m, 1);
           umma_bf16(tb + COL_B + LANE16, ad, bd, id_m, on);         // z
+          umma_bf16(tb + COL_B + LANE16, adl, bd, id_m, 1);
         }
         umma_commit(&sm.mma);
       }
@@ -249,8 +289,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       // S and dS are read
       stop = __syncthreads_or(*reinterpret_cast<volatile int*>(&sm.abort));
       if (stop) break;
-      // the next slice, of this head or the next one or (behind what follows here) the next chunk
-      int bh1 = bh, n1 = n, sl1 = sl + 1;
+      // the next slice, of this head or the next one or (behind what follows here) the next chunk;
+      // X and Yn come before its D and E
+      bh1 = bh, n1 = n, sl1 = sl + 1;
       if (sl1 == nsl) {
         const unsigned id1 = id + (hv + 1 < grp ? 0u : gridDim.x);
         bh1 = hv + 1 < grp ? bh + 1 : first_head(id1);
@@ -258,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         sl1 = id1 < total ? 0 : -1;
       }
       if (sl1 >= 0) load_slice(bh1, n1, sl1, &sm.gates[(nhead + 1) & 1]);
+      if (sl1 > 0) load_de(bh1, n1, sl1);
       __syncwarp();
     }
     if (stop) break;
@@ -308,11 +350,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int cc = 0; cc < XW / 8; ++cc) {
           const uint32_t off = sw128_off(i, 4 * hh + XW / 8 * hf + cc);
-          const float *x = f + 8 * cc, *h = y + 8 * cc;
-          st_shared_v4(sX + off, pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                       pack_bf16(x[6], x[7]));
-          st_shared_v4(sY + off, pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3]), pack_bf16(h[4], h[5]),
-                       pack_bf16(h[6], h[7]));
+          put_split8(sX + off, f + 8 * cc);
+          put_split8(sY + off, y + 8 * cc);
         }
       }
       __syncwarp();
@@ -325,9 +364,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (tid == 0) {
       tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)  // xk over F and H
-        umma_bf16(tb + COL_B, desc_at(sw128_desc(sX, 16, 1024), kk * 32),
-                  desc_at(sw128_desc(sK, TILE, 1024), kk * 2048), id_t, kk > 0);
+      for (int kk = 0; kk < 4; ++kk) {  // xk over F and H
+        const uint64_t ax = desc_at(sw128_desc(sX, 16, 1024), kk * 32);
+        const uint64_t bk = desc_at(sw128_desc(sK, TILE, 1024), kk * 2048);
+        umma_bf16(tb + COL_B, ax, bk, id_t, kk > 0);
+        umma_bf16(tb + COL_B, desc_at(ax, TILE), bk, id_t, 1);
+      }
     }
     __syncwarp();
     // ---- t (lower) and u (upper); z (upper)
@@ -372,9 +414,15 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int kk = 0; kk < 4; ++kk) {
         const uint64_t bq = desc_at(sw128_desc(sQ, TILE, 1024), kk * 2048);
         const uint64_t bk = desc_at(sw128_desc(sK, TILE, 1024), kk * 2048);
-        umma_bf16(tb + COL_B + LANE16, desc_at(sw128_desc(sX, TILE, 1024), kk * 2048), bq, id_m, kk > 0);
-        umma_bf16(tb + COL_B + LANE16, desc_at(sw128_desc(sY, TILE, 1024), kk * 2048), bk, id_m, 1);
-        umma_bf16(tb + COL_A + LANE16, desc_at(sw128_desc(sY, 16, 1024), kk * 32), bk, id_t, kk > 0);
+        const uint64_t xt = desc_at(sw128_desc(sX, TILE, 1024), kk * 2048);
+        const uint64_t yt = desc_at(sw128_desc(sY, TILE, 1024), kk * 2048);
+        const uint64_t ay = desc_at(sw128_desc(sY, 16, 1024), kk * 32);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          umma_bf16(tb + COL_B + LANE16, desc_at(xt, part * TILE), bq, id_m, kk + part > 0);
+          umma_bf16(tb + COL_B + LANE16, desc_at(yt, part * TILE), bk, id_m, 1);
+          umma_bf16(tb + COL_A + LANE16, desc_at(ay, part * TILE), bk, id_t, kk + part > 0);
+        }
       }
       umma_commit(&sm.mma);
     }
@@ -382,6 +430,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     mbar_wait(&sm.mma, nmma++ & 1, wc, W_G_MMA);
     __syncwarp();
     tc_fence_after();
+    if (sl1 >= 0) load_de(bh1, n1, 0);  // X and Yn are read
+    __syncwarp();
     // ---- xk (lower) and ka (upper); yk (upper)
     dv = dz = f2(0.f, 0.f);
 #pragma unroll
@@ -482,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   if (tid == 0) {  // every load has landed
     mbar_drain(&sm.full, (lfull - 1) & 1, wc, W_G_DRAIN);
+    mbar_drain(&sm.de, (lde - 1) & 1, wc, W_G_DRAIN);
     mbar_drain(&sm.kq, (lkq - 1) & 1, wc, W_G_DRAIN);
   }
   __syncthreads();
@@ -519,8 +570,8 @@ cudaError_t launch_grad(const Args& a, cudaStream_t st) {
   CUtensorMap m[9];
   if (!make_map_bf16_3d(&m[0], a.q, d.dk, d.T, kh, C) || !make_map_bf16_3d(&m[1], a.k, d.dk, d.T, kh, C) ||
       !make_map_bf16_3d(&m[2], a.dy, d.dv, d.T, bh, C) ||
-      !make_map_bf16_3d(&m[3], a.sv.D, C, dvp(d), bh * N, 64) ||
-      !make_map_bf16_3d(&m[4], a.E, C, dvp(d), bh * N, 64) ||
+      !make_map_bf16_3d(&m[3], a.sv.D, C, 2 * dvp(d), bh * N, 64) ||
+      !make_map_bf16_3d(&m[4], a.E, C, 2 * dvp(d), bh * N, 64) ||
       !make_map_bf16_3d(&m[5], a.sv.S, 128, dvp(d), bh * N, 64) ||
       !make_map_bf16_3d(&m[6], a.dS, 128, dvp(d), bh * N, 64) ||
       !make_map_bf16_3d(&m[7], a.dq, d.dk, d.T, kh, C) ||

@@ -1,6 +1,5 @@
 // Tensor-core gated delta rule: the chunk-local matrices (delta_tc.h, struct Mats) of one
-// (chunk, value head) after the other, three persistent CTAs per SM (two where both SPLIT and
-// BACK).
+// (chunk, value head) after the other, three persistent CTAs per SM.
 //
 // K K^T and Q K^T go through the tensor core; the unit lower triangular inverse
 // T0 = (I + A diag(beta))^-1 is formed in float32 by halves: 16 x 16 diagonal blocks by
@@ -8,14 +7,15 @@
 //   [[X1, 0], [-X2 N21 X1, X2]]
 // which is as stable as substitution and needs only two products per level (warp-wide tf32
 // products of split operands: 247 -> 222 us for B8 H16 T4096 against float32 FMAs, whose
-// shared-memory reads held the kernel up; tiles this small leave tcgen05.mma idle). The scaled
-// matrices T0 diag(G), diag(w) T and P then multiply K (or T) on the tensor core; K is
-// exact in bf16, so the gates ride on the other operand.
+// shared-memory reads held the kernel up; tiles this small leave tcgen05.mma idle).
 //
-// The backward's T follows from T0 as T_ij = beta_i T0_ij / beta_j, so
-//   Wb_j = (1 / beta_j) sum_i T0_ij beta_i w_i k_i,   PT = (P diag(beta)) (T0 diag(1 / beta)).
-// beta = 0 would leave T0's column zero where T's column j needs A's: beta is taken at least
-// 2^-60 in size here, which puts T0, Pb and W off by no more than that.
+// Kw = T0^T diag(beta w) K, Pv = P diag(beta) T0 and Wq = scale diag(G) Q - Pv diag(G) K then go
+// through the tensor core again. Their terms cancel where keys are alike, so T0, P and Pv diag(G)
+// enter as two bf16 each (K is exact in bf16): the results are good to 2^-16 before they are
+// rounded.
+//
+// beta = 0 would leave T0's column zero where E's row needs it: beta is taken at least 2^-60 in
+// size here (bt), which puts T0, Pv and Kw off by no more than that.
 //
 // Measured (B8 H16 T4096 d 128, 8192 chunks): 185 us with the backward's matrices, 1408 bytes per
 // token or 4.0 TB/s; 190 us with the remainders in their place (B1 H16 T32768). What bounds it is
@@ -45,39 +45,40 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int LD = 68;        // row stride (floats) of the 64 x 64 float32 matrices: 16-byte rows
-constexpr uint32_t kCols = 128;  // K K^T | Q K^T (64), then PT (64), then W | Wb
+// TMEM, in the lower and the upper 16 lanes of each 32: K K^T | Q K^T in columns 0 to 63; Kw | Pv
+// (columns 64 to 127); Kw | Wq
+constexpr uint32_t kCols = 128;
 constexpr float kTiny = 0x1p-60f;
 constexpr int kLoader = 128;  // the thread that loads K and Q, and stores P and PT
 
-// Tiles live where something dead was: P diag(beta) and diag(beta w) T0 over Q, T0 diag(1 / beta)
-// over the remainder of T0 diag(G) (with both, SPLIT and BACK, P has a place of its own), PT over
-// its operand in Q. At the end W, Wb and the remainder of W go over T0, T0 diag(G) and P, so that
-// K and Q are free for the next chunk's loads as soon as the last product is done.
-template <bool OWN_P>
+// Tiles live where something dead was. Over N: diag(beta w) T0, then P diag(beta), then Pv diag(G)
+// (two bf16 each), at the end Kw. Over X: T0, then Pv, at the end the remainder of Kw. Wq goes over
+// Q, row by row as it is formed.
 struct PrepSmem {
   uint8_t K[2 * TILE];         // k-blocks: 64 token rows x 128 B
   uint8_t Q[2 * TILE];
   union {
     float N[C * LD];           // A diag(beta); parts that are done with hold the products' halves
-    uint8_t Tg[2][TILE];       // T0 diag(G) in bf16 and its remainder
+    uint8_t A[2][TILE];
   };
-  float X[C * LD];             // T0
-  uint8_t P[OWN_P ? 2 * TILE : 16];
+  union {
+    float X[C * LD];           // T0
+    uint8_t B[2][TILE];
+  };
   // per token: M_ij = ra_i ca_j with both factors within e^40 (fac: all decays of the chunk within
   // e^80, and the factors taken from the middle of that range, so that ca kTiny stays a normal
   // number: a factor taken from a token, e^-80 kTiny, would underflow and take dbeta with it where
-  // beta = 0); bt is beta, at least kTiny in size: cb = ca bt, wb = w bt, rb = 1 / bt
+  // beta = 0); bt is beta, at least kTiny in size: cb = ca bt, wb = w bt, sG = scale G
   float ra[C], cb[C];
-  float Lh[C], Ll[C], G[C], wb[C], rb[C];
+  float Lh[C], Ll[C], G[C], wb[C], sG[C];
   int seg[C];
   int fac;
   uint64_t full, mma;
   uint32_t tmem_base;
   int abort;
 };
-template <bool OWN_P> constexpr size_t smem_bytes() { return sizeof(PrepSmem<OWN_P>) + 1024; }
-static_assert(3 * (smem_bytes<false>() + 1024) <= 228 * 1024, "three CTAs per SM");
-static_assert(2 * (smem_bytes<true>() + 1024) <= 228 * 1024, "two CTAs per SM");
+constexpr size_t kSmem = sizeof(PrepSmem) + 1024;
+static_assert(3 * (kSmem + 1024) <= 228 * 1024, "three CTAs per SM");
 
 enum : uint32_t { W_PREP_LOAD = 0x801, W_PREP_MMA, W_PREP_DRAIN };
 
@@ -112,33 +113,27 @@ __device__ __forceinline__ void store16x8(float* at, const float (&v)[4], float 
 
 }  // namespace
 
-// SPLIT: the remainders of T0 and W; BACK: Wb and PT for the backward.
+// SPLIT: the remainder of Kw; BACK: that of Pv, and T0, for the backward.
 template <bool SPLIT, bool BACK>
-__global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(const __grid_constant__ CUtensorMap tmK,
-                                                           const __grid_constant__ CUtensorMap tmQ,
-                                                           const __grid_constant__ CUtensorMap tmW,
-                                                           const __grid_constant__ CUtensorMap tmWlo,
-                                                           const __grid_constant__ CUtensorMap tmWb,
-                                                           const __grid_constant__ CUtensorMap tmPb,
-                                                           const __grid_constant__ CUtensorMap tmPT,
-                                                           PrepParams p) {
+__global__ void __launch_bounds__(kThreads, 3)
+    prep_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ,
+                const __grid_constant__ CUtensorMap tmKw, const __grid_constant__ CUtensorMap tmKwlo,
+                const __grid_constant__ CUtensorMap tmWq, const __grid_constant__ CUtensorMap tmPv,
+                PrepParams p) {
   extern __shared__ uint8_t smem_raw[];
-  constexpr bool own_p = SPLIT && BACK;
-  using Smem = PrepSmem<own_p>;
-  Smem& sm = *reinterpret_cast<Smem*>(
+  PrepSmem& sm = *reinterpret_cast<PrepSmem*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int N = chunks(p.d.T);
   const WaitCtx wc{&sm.abort, p.status, p.timeout_ns};
   const unsigned total = (unsigned)((size_t)p.d.B * p.d.H * N);
-  auto load_kq = [&](unsigned id) {  // one thread
+  // one thread; K, which announces both, before Q
+  auto load_kq = [&](unsigned id, bool q) {
     const int bh = id / N, t0 = (id - bh * N) * C, b = bh / p.d.H, h = bh - b * p.d.H;
     const int kh = b * p.d.Hk + h / (p.d.H / p.d.Hk);
-    mbar_arrive_expect_tx(&sm.full, 4 * TILE);
-    tma_load_3d(sm.K, &tmK, &sm.full, 0, t0, kh);
-    tma_load_3d(sm.K + TILE, &tmK, &sm.full, 64, t0, kh);
-    tma_load_3d(sm.Q, &tmQ, &sm.full, 0, t0, kh);
-    tma_load_3d(sm.Q + TILE, &tmQ, &sm.full, 64, t0, kh);
+    if (!q) mbar_arrive_expect_tx(&sm.full, 4 * TILE);
+    tma_load_3d(q ? sm.Q : sm.K, q ? &tmQ : &tmK, &sm.full, 0, t0, kh);
+    tma_load_3d((q ? sm.Q : sm.K) + TILE, q ? &tmQ : &tmK, &sm.full, 64, t0, kh);
   };
   grid_dep_launch();
   RawGates raw{};
@@ -152,7 +147,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
     mbar_init(&sm.full, 1);
     mbar_init(&sm.mma, 1);
     fence_mbar_init();
-    load_kq(blockIdx.x);
+    load_kq(blockIdx.x, false);
+    load_kq(blockIdx.x, true);
   }
   if (warp == 1) {
     tmem_alloc(&sm.tmem_base, kCols);
@@ -162,12 +158,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
   __syncthreads();
   tc_fence_after();
   const uint32_t tb = sm.tmem_base;
-  const uint32_t sK = smem_u32(sm.K), sQ = smem_u32(sm.Q), sTg = smem_u32(sm.Tg[0]);
-  const uint32_t sP = own_p ? smem_u32(sm.P) : sQ;
-  const uint32_t sTw = sQ + TILE, sTt = own_p ? sQ : sTg + TILE;
-  // places of the results (all 16 KB)
-  uint8_t *const oX = reinterpret_cast<uint8_t*>(sm.X), *const oW = own_p ? sm.P : BACK ? sm.Tg[0] : oX;
-  uint8_t *const oWb = oX, *const oWlo = sm.Tg[0];
+  const uint32_t sK = smem_u32(sm.K), sQ = smem_u32(sm.Q), sA = smem_u32(sm.A[0]), sB = smem_u32(sm.B[0]);
   uint32_t phase = 0, full = 0, loads = 0;  // loads: after the first, of the loading thread
   for (unsigned id = blockIdx.x; id < total; id += gridDim.x, full ^= 1) {
   const int bh = id / N, n = id - bh * N, t0 = n * C;
@@ -183,7 +174,6 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
       umma_bf16(tb + LANE16, desc_at(sw128_desc(sQ, 16, 1024), off), dk, id, kk > 0);
     }
     umma_commit(&sm.mma);
-    tma_store_wait_read();  // the last chunk's results, whose places are written from here on
   }
   __syncwarp();
   if (warp == 2) {
@@ -193,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
     const bool fac = g.seg_end == 0 && g.Lend > -80.f;
     GateBlock* gb = reinterpret_cast<GateBlock*>(p.m.gates) + (size_t)bh * N + n;
     if (lane == 0) {
-      gb->GC = gate_GC(g);
+      gb->GC = gb->GCb = gate_GC(g);
       gb->fac = fac ? 1.f : 0.f;
     }
 #pragma unroll
@@ -207,10 +197,14 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
       sm.Lh[i] = g.Lh[k];
       sm.Ll[i] = g.Ll[k];
       sm.seg[i] = g.seg[k];
-      sm.rb[i] = 1.f / bt;
-      const float G = gate_G(g, k), w = gate_w(g, k);
+      const float G = gate_G(g, k), w = gate_w(g, k), z = fabsf(be) < kTiny ? be / bt : 1.f;
       sm.G[i] = G;
+      sm.sG[i] = p.scale * G;
       sm.wb[i] = w * bt;
+      gb->nG[i] = -G;
+      gb->z[i] = gb->zb[i] = z;
+      gb->zG[i] = -G * z;
+      gb->rb[i] = 1.f / bt;
       gb->bw[i] = be * w;
       gb->q[i] = p.scale * G;
       gb->bG[i] = -be * G;
@@ -230,8 +224,8 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
   const uint32_t lo = (uint32_t)(32 * q) << 16;
   const int i = 16 * q + (lane & 15);
   const bool isP = lane >= 16;
-  {
-    float v[32];
+  // this thread's half row of K K^T or Q K^T, times M and bt (and scale), on and below the diagonal
+  auto scaled = [&](float (&v)[32]) {
     tmem_ld32(tb + lo + 32 * hh, v);
     tmem_ld_wait();
     // the entries below (P: and on) the diagonal
@@ -258,28 +252,33 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
         v[e] = e < keep && sm.seg[j] == seg ? v[e] * m : 0.f;
       }
     }
+  };
+  // 32 columns of row i as two bf16 into a pair of tiles
+  auto put_split = [&](uint32_t at, const float (&v)[32]) {
+#pragma unroll
+    for (int cc = 0; cc < 4; ++cc) {
+      uint32_t hi[4], low[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        hi[e] = pack_bf16(v[8 * cc + 2 * e], v[8 * cc + 2 * e + 1]);
+        low[e] = pack_lo(v[8 * cc + 2 * e], v[8 * cc + 2 * e + 1], hi[e]);
+      }
+      const uint32_t off = sw128_off(i, 4 * hh + cc);
+      st_shared_v4(at + off, hi[0], hi[1], hi[2], hi[3]);
+      st_shared_v4(at + TILE + off, low[0], low[1], low[2], low[3]);
+    }
+  };
+  {
+    float v[32];
+    scaled(v);
     if (!isP) {
 #pragma unroll
       for (int e = 0; e < 32; e += 4)
         *reinterpret_cast<float4*>(sm.N + i * LD + 32 * hh + e) =
             make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-    } else {
-#pragma unroll
-      for (int cc = 0; cc < 4; ++cc) {
-        const float* x = v + 8 * cc;
-        st_shared_v4(sP + sw128_off(i, 4 * hh + cc), pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                     pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-      }
     }
   }
-  fence_proxy_async_smem();
-  tc_fence_before();
   __syncthreads();
-  if (tid == kLoader) {  // in a warp with little to do next
-    tma_store_3d(&tmPb, own_p ? sm.P : sm.Q, 0, t0, bh);
-    tma_store_commit();
-  }
-  __syncwarp();
   // ---- T0: 16 x 16 diagonal blocks, two per warp, a lane per column; other warps clear what
   //      is right of them
   if (warp < 2) {
@@ -348,138 +347,174 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
                         pack_lo(x[6], x[7], h.w));
     };
     auto put = [&](uint32_t dst, const uint4& v) { st_shared_v4(dst, v.x, v.y, v.z, v.w); };
-    float G[8], rb[8];
-    at8(sm.G + c, G);
-    if (BACK) at8(sm.rb + c, rb);
+    uint4 hi[2], rest[2];
 #pragma unroll
     for (int rr = 0; rr < 2; ++rr) {
       const int r = (tid >> 3) + 32 * rr;
-      float x[8], y[8];
+      float x[8];
       at8(sm.X + r * LD + c, x);
+      hi[rr] = pack8(x);
+      rest[rr] = rest8(x, hi[rr]);
+      const float wr = sm.wb[r];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= wr;
       const uint32_t off = sw128_off(r, c >> 3);
-      const size_t at = (((size_t)bh * N + n) * C + r) * C + c;
-      const uint4 hi = pack8(x);
-      *reinterpret_cast<uint4*>(p.m.T0 + at) = hi;
-      if (SPLIT) *reinterpret_cast<uint4*>(p.m.T0lo + at) = rest8(x, hi);
+      const uint4 h = pack8(x);
+      put(sA + off, h);
+      put(sA + TILE + off, rest8(x, h));
+    }
+    __syncthreads();  // X is read, and T0 goes over it
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = -x[e] * G[e];
-      const uint4 gh = pack8(y);
-      put(sTg + off, gh);
-      if (SPLIT) put(sTg + TILE + off, rest8(y, gh));
+    for (int rr = 0; rr < 2; ++rr) {
+      const int r = (tid >> 3) + 32 * rr;
+      const uint32_t off = sw128_off(r, c >> 3);
+      put(sB + off, hi[rr]);
+      put(sB + TILE + off, rest[rr]);
       if (BACK) {
-        const float wr = sm.wb[r];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = wr * x[e];
-        put(sTw + off, pack8(y));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[e] * rb[e];
-        put(sTt + off, pack8(y));
+        bf16* const at = p.m.T0 + (((size_t)bh * N + n) * C + r) * 128 + c;
+        *reinterpret_cast<uint4*>(at) = hi[rr];
+        *reinterpret_cast<uint4*>(at + 64) = rest[rr];
       }
     }
   }
-  if (tid == kLoader) tma_store_wait_read();  // P
-  __syncwarp();
+  // One group of products of M = 64: d (+)= a b over the 64 tokens, from thread 0
+  auto product = [&](uint32_t d, uint32_t a, bool a_mn, uint32_t b, int cols, bool first) {
+    const uint32_t what = idesc_bf16(64, cols, a_mn, true);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+      umma_bf16(d, a_mn ? desc_at(sw128_desc(a, TILE, 1024), kk * 2048)
+                        : desc_at(sw128_desc(a, 16, 1024), kk * 32),
+                desc_at(sw128_desc(b, TILE, 1024), kk * 2048), what, !first || kk > 0);
+  };
+  const uint32_t tU = tb + LANE16;  // the upper lanes
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
-  if (BACK) {  // PT = (P diag(bt)) (T0 diag(1 / bt))
-    if (tid == 0) {
-      tc_fence_after();
-      const uint32_t id_pt = idesc_bf16(64, 64, false, true);
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        umma_bf16(tb, desc_at(sw128_desc(sP, 16, 1024), kk * 32),
-                  desc_at(sw128_desc(sTt, TILE, 1024), kk * 2048), id_pt, kk > 0);
-      umma_commit(&sm.mma);
-    }
-    __syncwarp();
+  if (tid == 0) {  // Kw
+    tc_fence_after();
+    product(tb, sA, true, sK, 128, true);
+    product(tb, sA + TILE, true, sK, 128, false);
+    umma_commit(&sm.mma);
+  }
+  __syncwarp();
+  {
+    // The products above write the lower lanes of all columns; Q K^T is in the upper ones.
+    float v[32];
+    tc_fence_after();
+    scaled(v);
     mbar_wait(&sm.mma, phase, wc, W_PREP_MMA);
     phase ^= 1;
     __syncwarp();
+    if (isP) put_split(sA, v);
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0) {  // Pv
     tc_fence_after();
+    product(tU + 64, sA, false, sB, 64, true);
+    product(tU + 64, sA, false, sB + TILE, 64, false);
+    product(tU + 64, sA + TILE, false, sB, 64, false);
+    umma_commit(&sm.mma);
+  }
+  __syncwarp();
+  mbar_wait(&sm.mma, phase, wc, W_PREP_MMA);
+  phase ^= 1;
+  __syncwarp();
+  tc_fence_after();
+  {
     float v[32];
-    tmem_ld32(tb + lo + 32 * hh, v);
+    tmem_ld32(tb + lo + 64 + 32 * hh, v);
     tmem_ld_wait();
-    if (!isP) {
+    if (isP) {
+      put_split(sB, v);
 #pragma unroll
-      for (int cc = 0; cc < 4; ++cc) {
-        const float* x = v + 8 * cc;
-        st_shared_v4(sQ + sw128_off(i, 4 * hh + cc), pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                     pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+      for (int e = 0; e < 32; e += 4) {
+        const float4 g = at4(sm.G + 32 * hh + e);
+        v[e] *= -g.x;
+        v[e + 1] *= -g.y;
+        v[e + 2] *= -g.z;
+        v[e + 3] *= -g.w;
       }
-    }
-    fence_proxy_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    if (tid == kLoader) {
-      tma_store_3d(&tmPT, sm.Q, 0, t0, bh);
-      tma_store_commit();
+      put_split(sA, v);
     }
   }
-  if (tid == 0) {
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  if (tid == kLoader) {
+    tma_store_3d(&tmPv, sm.B[0], 0, t0, bh);
+    if (BACK) tma_store_3d(&tmPv, sm.B[1], 64, t0, bh);
+    tma_store_commit();
+  }
+  if (tid == 0) {  // - Pv diag(G) K
     tc_fence_after();
-    const uint32_t id_w = idesc_bf16(64, 128, false, true), id_wb = idesc_bf16(64, 128, true, true);
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      const uint64_t dk = desc_at(sw128_desc(sK, TILE, 1024), kk * 2048);  // K as [token][d_k]
-      umma_bf16(tb, desc_at(sw128_desc(sTg, 16, 1024), kk * 32), dk, id_w, kk > 0);
-      if (SPLIT) umma_bf16(tb, desc_at(sw128_desc(sTg + TILE, 16, 1024), kk * 32), dk, id_w, 1);
-      if (BACK)
-        umma_bf16(tb + LANE16, desc_at(sw128_desc(sTw, TILE, 1024), kk * 2048), dk, id_wb, kk > 0);
-    }
+    product(tU, sA, false, sK, 128, true);
+    product(tU, sA + TILE, false, sK, 128, false);
     umma_commit(&sm.mma);
   }
   __syncwarp();
   const bool done = mbar_wait(&sm.mma, phase, wc, W_PREP_MMA);
   phase ^= 1;
-  if (tid == kLoader && done && id + gridDim.x < total) {
-    tma_store_wait_read();  // PT
-    load_kq(id + gridDim.x);
-    ++loads;
+  const bool more = done && id + gridDim.x < total;
+  if (tid == kLoader) {
+    if (more) {
+      load_kq(id + gridDim.x, false);
+      ++loads;
+    }
+    if (SPLIT) tma_store_wait_read();  // Pv
   }
   __syncwarp();
+  if (SPLIT) __syncthreads();
   tc_fence_after();
-  // W (lanes < 16) and Wb (lanes >= 16) to bf16, columns [64 hh, 64 hh + 64)
+  // Kw (lanes < 16) and Wq (lanes >= 16) to bf16, columns [64 hh, 64 hh + 64)
+  const float sG = sm.sG[i];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     float v[32];
     tmem_ld32(tb + lo + 64 * hh + 32 * g, v);
     tmem_ld_wait();
-    if (BACK && isP) {
-      const float rb = sm.rb[i];
-#pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] *= rb;
-    }
-    const uint32_t dst = smem_u32(isP ? oWb : oW) + hh * TILE;
+    const uint32_t dst = (isP ? sQ : sA) + hh * TILE;
 #pragma unroll
     for (int cc = 0; cc < 4; ++cc) {
+      const uint32_t off = sw128_off(i, 4 * g + cc);
+      if (isP) {
+        const uint4 u = ld_shared_v4(dst + off);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[8 * cc + 2 * e] = fmaf(sG, bf16_lo(w[e]), v[8 * cc + 2 * e]);
+          v[8 * cc + 2 * e + 1] = fmaf(sG, bf16_hi(w[e]), v[8 * cc + 2 * e + 1]);
+        }
+      }
       uint32_t hi[4], low[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         hi[e] = pack_bf16(v[8 * cc + 2 * e], v[8 * cc + 2 * e + 1]);
         if (SPLIT) low[e] = pack_lo(v[8 * cc + 2 * e], v[8 * cc + 2 * e + 1], hi[e]);
       }
-      const uint32_t off = sw128_off(i, 4 * g + cc);
-      if (BACK || !isP) st_shared_v4(dst + off, hi[0], hi[1], hi[2], hi[3]);
-      if (SPLIT && !isP) st_shared_v4(smem_u32(oWlo) + hh * TILE + off, low[0], low[1], low[2], low[3]);
+      st_shared_v4(dst + off, hi[0], hi[1], hi[2], hi[3]);
+      if (SPLIT && !isP) st_shared_v4(sB + hh * TILE + off, low[0], low[1], low[2], low[3]);
     }
     __syncwarp();
   }
   fence_proxy_async_smem();
   tc_fence_before();
   const bool stop = __syncthreads_or(*reinterpret_cast<volatile int*>(&sm.abort));
-  if (tid == 0) {
+  if (tid == kLoader) {
     for (int kb = 0; kb < 2; ++kb) {
-      tma_store_3d(&tmW, oW + kb * TILE, 64 * kb, t0, bh);
-      if (SPLIT) tma_store_3d(&tmWlo, oWlo + kb * TILE, 64 * kb, t0, bh);
-      if (BACK) tma_store_3d(&tmWb, oWb + kb * TILE, 64 * kb, t0, bh);
+      tma_store_3d(&tmKw, sm.A[kb], 64 * kb, t0, bh);
+      if (SPLIT) tma_store_3d(&tmKwlo, sm.B[kb], 64 * kb, t0, bh);
+      tma_store_3d(&tmWq, sm.Q + kb * TILE, 64 * kb, t0, bh);
     }
     tma_store_commit();
+    tma_store_wait_read();  // the places are written again from the next chunk's gates on
+    if (more) load_kq(id + gridDim.x, true);
   }
+  __syncwarp();
   if (stop) break;
   }
   if (tid == kLoader) mbar_drain(&sm.full, loads & 1, wc, W_PREP_DRAIN);
-  if (tid == 0 || tid == kLoader) tma_store_wait_read();  // shared memory may go once it is read
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -488,21 +523,20 @@ __global__ void __launch_bounds__(kThreads, SPLIT && BACK ? 2 : 3) prep_kernel(c
 }
 
 template <bool SPLIT, bool BACK>
-static cudaError_t launch(const CUtensorMap (&m)[7], const PrepParams& p, unsigned grid, cudaStream_t st) {
+static cudaError_t launch(const CUtensorMap (&m)[6], const PrepParams& p, unsigned grid, cudaStream_t st) {
   static std::atomic<uint64_t> set{0};  // devices whose opt-in is done
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (!bit || !(set.load() & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(prep_kernel<SPLIT, BACK>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem_bytes<SPLIT && BACK>());
+    const cudaError_t e = cudaFuncSetAttribute(
+        prep_kernel<SPLIT, BACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     set.fetch_or(bit);
   }
-  const unsigned most = 148 * (SPLIT && BACK ? 2 : 3);
-  prep_kernel<SPLIT, BACK><<<grid < most ? grid : most, kThreads, smem_bytes<SPLIT && BACK>(), st>>>(m[0], m[1], m[2], m[3], m[4], m[5],
-                                                                              m[6], p);
+  const unsigned most = 148 * 3;
+  prep_kernel<SPLIT, BACK><<<grid < most ? grid : most, kThreads, kSmem, st>>>(m[0], m[1], m[2], m[3],
+                                                                               m[4], m[5], p);
   count_launch();
   return cudaGetLastError();
 }
@@ -510,15 +544,14 @@ static cudaError_t launch(const CUtensorMap (&m)[7], const PrepParams& p, unsign
 cudaError_t launch_prep(const Args& a, bool split, cudaStream_t st) {
   const Dims& d = a.d;
   const uint64_t N = chunks(d.T), kh = (uint64_t)d.B * d.Hk, bh = d.BH();
-  const bool back = a.m.Wb != nullptr;
-  CUtensorMap m[7];
+  const bool back = a.m.T0 != nullptr;
+  CUtensorMap m[6];
   using gradlev::tc::make_map_bf16_3d;
   if (!make_map_bf16_3d(&m[0], a.k, d.dk, d.T, kh, C) || !make_map_bf16_3d(&m[1], a.q, d.dk, d.T, kh, C) ||
-      !make_map_bf16_3d(&m[2], a.m.W, 128, N * C, bh, C) ||
-      !make_map_bf16_3d(&m[3], split ? a.m.Wlo : a.m.W, 128, N * C, bh, C) ||
-      !make_map_bf16_3d(&m[4], back ? a.m.Wb : a.m.W, 128, N * C, bh, C) ||
-      !make_map_bf16_3d(&m[5], a.m.Pb, C, N * C, bh, C) ||
-      !make_map_bf16_3d(&m[6], back ? a.m.PT : a.m.Pb, C, N * C, bh, C))
+      !make_map_bf16_3d(&m[2], a.m.Kw, 128, N * C, bh, C) ||
+      !make_map_bf16_3d(&m[3], a.m.Kwlo, 128, N * C, bh, C) ||
+      !make_map_bf16_3d(&m[4], a.m.Wq, 128, N * C, bh, C) ||
+      !make_map_bf16_3d(&m[5], a.m.Pv, 128, N * C, bh, C))
     return cudaErrorInvalidValue;
   const PrepParams p{d, a.beta, a.log_alpha, a.scale, a.status, a.timeout_ns, a.m};
   const unsigned grid = (unsigned)(N * bh);

@@ -202,16 +202,19 @@ static bf16* take(char*& at, size_t elems) {
 static size_t gate_bytes(const Dims& d) {
   return up256(d.BH() * chunks(d.T) * sizeof(GateBlock));
 }
-size_t token_rows_bytes(const Dims& d) { return up256(d.BH() * chunks(d.T) * dvp(d) * C * sizeof(bf16)); }
+size_t token_rows_bytes(const Dims& d) {
+  return up256(d.BH() * chunks(d.T) * 2 * dvp(d) * C * sizeof(bf16));
+}
+// one of Kw, Kwlo, Wq, Pv, T0
+static size_t mat_bytes(const Dims& d) { return up256(d.BH() * chunks(d.T) * C * 128 * sizeof(bf16)); }
 
 Saved saved_at(char* base, const Dims& d) {
   const size_t rows = d.BH() * chunks(d.T);
   char* at = base;
   Saved s;
   s.S = take(at, rows * dvp(d) * 128);
-  s.D = take(at, rows * dvp(d) * C);
-  s.Wb = take(at, rows * C * 128);
-  s.PT = take(at, rows * C * C);
+  s.D = take(at, rows * 2 * dvp(d) * C);
+  for (bf16** m : {&s.Kw, &s.Wq, &s.Pv}) *m = take(at, rows * C * 128);
   s.gates = reinterpret_cast<float*>(at);
   s.M = reinterpret_cast<float*>(at + gate_bytes(d));
   return s;
@@ -220,28 +223,27 @@ Saved saved_at(char* base, const Dims& d) {
 size_t saved_bytes(const Dims& d) {
   const size_t rows = d.BH() * chunks(d.T);
   const int nseg = seg_plan(d).nseg;
-  return up256(rows * dvp(d) * 256) + token_rows_bytes(d) + up256(rows * C * 256) +
-         up256(rows * C * C * 2) + gate_bytes(d) +
+  return up256(rows * dvp(d) * 256) + token_rows_bytes(d) + 3 * mat_bytes(d) + gate_bytes(d) +
          (nseg > 1 ? d.BH() * nseg * 128 * 128 * sizeof(float) : 0);
 }
 
-Mats mats_at(char* base, const Dims& d) {
-  const size_t rows = d.BH() * chunks(d.T);
+// With checkpoints Kw, Wq, Pv and the gates are among them, and T0 is needed for D.
+Mats mats_at(char* base, const Dims& d, bool saved) {
+  const size_t n = d.BH() * chunks(d.T) * C * 128;
   char* at = base;
   Mats m;
-  m.W = take(at, rows * C * 128);
-  m.Wlo = take(at, rows * C * 128);
-  m.T0 = take(at, rows * C * C);
-  m.T0lo = take(at, rows * C * C);
-  m.Pb = take(at, rows * C * C);
+  m.Kwlo = take(at, n);
+  if (saved) {
+    m.T0 = take(at, n);
+    return m;
+  }
+  for (bf16** x : {&m.Kw, &m.Wq, &m.Pv}) *x = take(at, n);
   m.gates = reinterpret_cast<float*>(at);
   return m;
 }
 
 size_t fwd_scratch_bytes(const Dims& d) {  // the segments' buffers come last
-  const size_t rows = d.BH() * chunks(d.T);
-  return 2 * up256(rows * C * 256) + 3 * up256(rows * C * C * 2) + gate_bytes(d) +
-         seg_bytes(d, true);
+  return 4 * mat_bytes(d) + gate_bytes(d) + seg_bytes(d, true);
 }
 
 size_t bwd_scratch_bytes(const Dims& d) {  // E, dS, the segments' buffers

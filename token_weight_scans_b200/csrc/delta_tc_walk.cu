@@ -4,26 +4,28 @@
 // so that the two operands made from the previous product stay in tensor memory:
 //
 //   forward                                backward (chunks in reverse, S is dS)
-//   D^T  = V^T T0^T + S W^T                E^T = dY^T PT + S Wb^T
-//   S    = G_C S + (beta w D)^T K          S   = G_C S + dY^T (scale G Q) + E^T (-beta G K)
-//   Y^T  = S (scale G Q)^T + D^T Pb^T      dV  = beta E
+//   R^T  = V^T - S (diag(G) K)^T           F^T  = S Kw^T
+//   S    = G_C S + R^T Kw                  S    = G_C S + dY^T Wq - (beta / bt G F)^T K
+//   Y^T  = V^T Pv^T + S Wq^T               bt E = F + Pv^T dY,  dV = beta E
+//   D^T  = R^T T0^T (for the backward)
 //
-// The chain through a chunk is: S to bf16 (TMEM -> registers -> TMEM), the product with W,
-// its result to bf16, the product with K. All else runs beside it: V^T T0^T of the next
-// chunk and the outputs' products are issued into the gaps of the chain, and their results
-// leave through an output warpgroup. Without SPLIT one product of N = 128 takes S through W
-// and Q together.
+// The chain through a chunk is: S to bf16 (TMEM -> registers -> TMEM), the product with K (Kw),
+// its result to bf16, the product with Kw (K). All else runs beside it: V^T of the next chunk
+// (a product with the identity, into the accumulator that S K^T is added to) and the outputs'
+// products are issued into the gaps of the chain, and their results leave through an output
+// warpgroup. One product of N = 128 takes S through K and Wq together.
 //
 // SPLIT (a forward whose last state is asked for): every operand of the state that is not
-// exact in bf16 comes as a sum of two bf16 (S, W, T0, beta w D), three products in place of
-// one, so that S carries 16 bits through the chunks and the float32 state it ends with is
-// good to 1e-5. Training needs no such state and takes single products.
+// exact in bf16 comes as a sum of two bf16 (S, R, Kw), so that S carries 16 bits through the
+// chunks and the float32 state it ends with is good to 1e-5. K is left as it is, and -G is applied
+// to the product. Training needs no such state and takes single products, with K diag(-G) in bf16.
 //
 // Warp roles (16): 0 and 3 TMA producers, 1 MMA issuer (owns TMEM), 2 copies the gates in,
-// 4-11 two chain warpgroups (each half of the columns), which also leave S and D^T (E^T) for
-// the kernels after, 12-15 scaling of Q by scale G, and Y (dV): 16-lane TMEM loads in the
+// 4-11 two chain warpgroups (each half of the columns), which also leave S and E^T for
+// the kernels after, 12-15 scaling of K by -G, D^T, and Y (dV): 16-lane TMEM loads in the
 // layout of 8 x 8 fragments, transposed on the way to shared memory (stmatrix) so that tokens
-// become rows, and TMA stores. D^T and E^T stay as they are, a chunk's tokens contiguous.
+// become rows, and TMA stores. D^T and E^T stay as they are, a chunk's tokens contiguous, in two
+// bf16 each.
 //
 // Measured (B8 H16 T4096 d 128, 128 CTAs of 64 chunks): forward 190 us, backward 180 us, of
 // 2304 and 2176 bytes per token: 6.3 TB/s, the measured copy bandwidth (6.47). Where HBM does
@@ -31,7 +33,8 @@
 // two passes of the state or D through registers.
 //
 // Each chunk's tiles come in three groups with a two-deep ring of their own, since they are
-// done with at different times: V (dY) with T0 (PT), W with Q, K with Pb.
+// done with at different times: V (dY) with Pv, K (Kw) with Wq, Kw (K). T0, needed last, has one
+// place.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -55,27 +58,26 @@ constexpr int kThreads = 512;
 // TMEM columns
 constexpr uint32_t COL_S = 0;      // float32 state, 128
 constexpr uint32_t COL_SH = 128;   // bf16 state, 64
-constexpr uint32_t COL_DB = 192;   // bf16 D (E), 32
-constexpr uint32_t COL_U = 224;    // bf16 beta w D, 32
-constexpr uint32_t COL_D = 256;    // D^T (E^T) accumulator, 64, and Y^T, 64; two such pairs
-// SPLIT has one set: D^T in two parts that the chain adds (the products with T0 and W, and with
-// their remainders), then Y^T: the three take one product of N = 192
-constexpr uint32_t COL_YS = 384;   // SPLIT: Y^T
-constexpr uint32_t COL_SL = 448;   // SPLIT: remainder of the state, 64; once the products with W
-constexpr uint32_t COL_UL = 448;   // have read it, that of beta w D, 32
+constexpr uint32_t COL_DB = 192;   // bf16 R, 32 (for D)
+constexpr uint32_t COL_U = 224;    // bf16 operand of the update, 32: R (with 0 where beta = 0), -G F
+// Accumulators, two pairs: R^T, 64, then D^T in its place, and Y^T, 64 (backward: Pv^T dY and F).
+// SPLIT has one set: V^T, then D^T in its place; S K^T, which the chain scales and adds; Y^T
+constexpr uint32_t COL_D = 256;
+constexpr uint32_t COL_SL = 448;   // SPLIT: remainder of the state, 64; once the products with K
+constexpr uint32_t COL_UL = 448;   // have read it, that of R, 32
 
 // A chunk's gates: the piece of GateBlock that the direction needs, as it lies there.
 template <bool BWD> struct GateSlot;
 template <> struct GateSlot<false> {
-  float u[C], GC, pad[3], q[C];         // bw .. q
-  static constexpr int offset = 0;
+  float nG[C], u[C], GC, pad[3];        // nG .. GC
+  static constexpr size_t offset = offsetof(GateBlock, nG);
 };
 template <> struct GateSlot<true> {
-  float GC, pad[3], q[C], u[C], be[C];  // GC .. be
-  static constexpr int offset = C * sizeof(float);
+  float GC, pad[3], u[C], rb[C], z[C];  // GCb .. zb
+  static constexpr size_t offset = offsetof(GateBlock, GCb);
 };
 static_assert(sizeof(GateSlot<false>) % 16 == 0 && sizeof(GateSlot<true>) % 16 == 0 &&
-              sizeof(GateBlock) % 16 == 0, "bulk copies");
+              offsetof(GateBlock, GCb) % 16 == 0 && sizeof(GateBlock) % 16 == 0, "bulk copies");
 
 template <bool BWD>
 struct Bars {
@@ -85,39 +87,41 @@ struct Bars {
   uint64_t gfull[GS], gempty[GS];
   uint64_t sready[2];                   // (SPLIT: in two halves of each warp's columns)
   uint64_t sscaled, dfull, uready, sfull, done;
+  uint64_t tfull, tempty;               // T0
   uint64_t yfull[2], yfree[2];          // per accumulator pair
   uint32_t tmem_base;
   int abort;
 };
-enum { VT = 0, WQ = 1, KP = 2 };
+enum { VP = 0, KQ = 1, UP = 2 };
 
-// The rings. VT: V (dY), T0 (PT), SPLIT also the remainder of T0. WQ: per 64 columns of d_k the
-// W (Wb) tile, SPLIT the remainder of W, and the Q tile next to each other (128 or 192 rows of
-// one operand). KP: K, forward also Pb.
+// The rings. VP: V (dY), Pv, backward also its remainder. KQ: per 64 columns of d_k the K (Kw)
+// tile and the Wq tile next to each other (128 rows of one operand). UP: Kw (K), SPLIT also the
+// remainder of Kw.
 template <bool BWD, bool SPLIT>
 struct Layout {
-  static constexpr int v = 0, t = 2 * TILE, tl = 3 * TILE;
-  static constexpr int w = 0, wl = TILE, q = SPLIT ? 2 * TILE : TILE;
-  static constexpr int wq = q + TILE;    // from one k-block to the next
-  static constexpr int k = 0, p = 2 * TILE;
-  static constexpr int vt_bytes = SPLIT ? 4 * TILE : 3 * TILE;
-  static constexpr int wq_bytes = SPLIT ? 6 * TILE : 4 * TILE;
-  static constexpr int kp_bytes = BWD ? 2 * TILE : 3 * TILE;
-  static constexpr int wq0 = NS * vt_bytes, kp0 = wq0 + NS * wq_bytes;
-  static constexpr bool staged = !SPLIT;   // S and D^T through shared memory and TMA
-  static constexpr int stage_s = kp0 + NS * kp_bytes, stage_o = stage_s + (staged ? 2 * BIG : 0);
-  static constexpr int stage_d = stage_o + 2 * TILE;
-  static constexpr int bars = stage_d + (staged ? 2 * TILE : 0);  // (SPLIT: Y alone is staged)
+  static constexpr int v = 0, p = 2 * TILE, pl = 3 * TILE;
+  static constexpr int w = 0, q = TILE;
+  static constexpr int wq = 2 * TILE;    // from one k-block to the next
+  static constexpr int k = 0, kl = 2 * TILE;
+  static constexpr int vp_bytes = BWD ? 4 * TILE : 3 * TILE;
+  static constexpr int kq_bytes = 4 * TILE;
+  static constexpr int up_bytes = SPLIT ? 4 * TILE : 2 * TILE;
+  static constexpr int kq0 = NS * vp_bytes, up0 = kq0 + NS * kq_bytes;
+  static constexpr int t0 = up0 + NS * up_bytes;          // forward: T0 and its remainder
+  static constexpr int id = t0 + (BWD ? 0 : 2 * TILE);    // forward: the identity
+  static constexpr bool staged = !SPLIT;   // S through shared memory and TMA
+  static constexpr int stage_s = id + (BWD ? 0 : TILE), stage_o = stage_s + (staged ? 2 * BIG : 0);
+  static constexpr int bars = stage_o + 2 * TILE;
   static constexpr size_t smem = bars + sizeof(Bars<BWD>) + 1024;
   static_assert(smem <= 227 * 1024, "over the shared memory of a CTA");
-  static constexpr int vt(int s) { return s * vt_bytes; }
-  static constexpr int wq_at(int s) { return wq0 + s * wq_bytes; }
-  static constexpr int kp(int s) { return kp0 + s * kp_bytes; }
+  static constexpr int vp(int s) { return s * vp_bytes; }
+  static constexpr int kq(int s) { return kq0 + s * kq_bytes; }
+  static constexpr int up(int s) { return up0 + s * up_bytes; }
 };
 
 enum : uint32_t {
   W_TMA = 0x901, W_TMA_DRAIN, W_FULL = 0x911, W_SCALED, W_SREADY, W_UREADY, W_YFREE, W_DONE,
-  W_GATE = 0x921, W_C_SFULL = 0x931, W_C_DFULL, W_C_GATE, W_O_FULL = 0x941, W_O_GATE, W_O_Y,
+  W_GATE = 0x921, W_T0, W_C_SFULL = 0x931, W_C_DFULL, W_C_GATE, W_O_FULL = 0x941, W_O_GATE, W_O_Y,
 };
 
 struct WalkParams {
@@ -131,7 +135,7 @@ struct WalkParams {
   float* ST;             // forward end
   bf16* dS0;             // backward end
   bf16* y;               // forward
-  bf16* D;               // forward: D^T, backward: E^T (null: not kept)
+  bf16* D;               // forward: D^T, backward: E^T, two parts (null: not kept)
   bf16* states;          // chunk-start (chunk-end) states, or null
   // Segments (delta_tc_seg.cu): CTA u < nsl B H segs walks segment seg0 + u / (nsl B H); the
   // slice past the last one carries the identity. CTAs past those carry it through the last
@@ -157,6 +161,29 @@ __device__ __forceinline__ void st_tmem16(uint32_t col, const uint32_t (&r)[16])
 }
 __device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
   return pack_bf16(a - bf16_lo(hi), b - bf16_hi(hi));
+}
+
+// The gates that only one direction has.
+__device__ __forceinline__ const float* gate_nG(const GateSlot<false>& g) { return g.nG; }
+__device__ __forceinline__ const float* gate_nG(const GateSlot<true>&) { return nullptr; }
+__device__ __forceinline__ const float* gate_rb(const GateSlot<true>& g) { return g.rb; }
+__device__ __forceinline__ const float* gate_rb(const GateSlot<false>&) { return nullptr; }
+__device__ __forceinline__ const float* gate_z(const GateSlot<true>& g) { return g.z; }
+
+// N values as two bf16, the remainders `apart` elements behind.
+template <int N>
+__device__ __forceinline__ void store_split(bf16* out, size_t apart, const float (&v)[N]) {
+#pragma unroll
+  for (int cc = 0; cc < N / 8; ++cc) {
+    uint32_t hi[4], rest[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      hi[e] = pack_bf16(v[8 * cc + 2 * e], v[8 * cc + 2 * e + 1]);
+      rest[e] = pack_rest(v[8 * cc + 2 * e], v[8 * cc + 2 * e + 1], hi[e]);
+    }
+    *reinterpret_cast<uint4*>(out + 8 * cc) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(out + apart + 8 * cc) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+  }
 }
 
 // Barrier `id` among `nthreads` threads; whether any of them brought `pred`.
@@ -233,12 +260,11 @@ __device__ __forceinline__ void put_frag64(uint32_t tile, int row, const float (
 
 template <bool BWD, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
-    walk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmW,
-                const __grid_constant__ CUtensorMap tmWl, const __grid_constant__ CUtensorMap tmT,
-                const __grid_constant__ CUtensorMap tmTl, const __grid_constant__ CUtensorMap tmP,
-                const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmY,
-                const __grid_constant__ CUtensorMap tmD, WalkParams p) {
+    walk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                const __grid_constant__ CUtensorMap tmKw, const __grid_constant__ CUtensorMap tmKwl,
+                const __grid_constant__ CUtensorMap tmWq, const __grid_constant__ CUtensorMap tmP,
+                const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmS,
+                const __grid_constant__ CUtensorMap tmY, WalkParams p) {
   using L = Layout<BWD, SPLIT>;
   constexpr int NY = SPLIT ? 1 : 2;   // accumulator pairs
   extern __shared__ uint8_t smem_raw[];
@@ -255,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n0 = ident ? 0 : slice * 128;
   const bool carry = p.sum || ident;                 // the end state is all that is wanted
   const bool outputs = !BWD && !carry;               // the forward's products for Y
+  const bool errors = outputs && p.D;                // and those for D
   const size_t sg = (size_t)bh * p.nseg + seg;
   const int b = bh / p.d.H, h = bh - b * p.d.H;
   const int kh = b * p.d.Hk + h / (p.d.H / p.d.Hk);
@@ -283,11 +310,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.uready, 8);
     mbar_init(&sm.sfull, 1);
     mbar_init(&sm.done, 1);
+    mbar_init(&sm.tfull, 1);
+    mbar_init(&sm.tempty, 1);
     for (int y = 0; y < 2; ++y) {
       mbar_init(&sm.yfull[y], 1);
       mbar_init(&sm.yfree[y], 4);
     }
     fence_mbar_init();
+  }
+  if (!BWD) {  // the identity, 16 bytes per thread
+    const int r = threadIdx.x >> 3, c = threadIdx.x & 7, e = r & 7;
+    const uint32_t one = (r >> 3) == c ? 0x3F80u << (16 * (e & 1)) : 0u;  // bf16
+    st_shared_v4(smem_u32(base + L::id) + sw128_off(r, c), e >> 1 == 0 ? one : 0u, e >> 1 == 1 ? one : 0u,
+                 e >> 1 == 2 ? one : 0u, e >> 1 == 3 ? one : 0u);
+    fence_proxy_async_smem();
   }
   if (warp == 1) {
     tmem_alloc(&sm.tmem_base, 512);
@@ -302,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0 || warp == 3) {
     // ------------------------------------------------------------ TMA producers
-    // warp 0: V with T0, and K with Pb; warp 3: W with Q
+    // warp 0: V with Pv, and Kw (K); warp 3: K (Kw) with Wq
     if (lane == 0) {
       int issued[3] = {0, 0, 0};
       auto open = [&](int r, int c, int bytes) -> bool {
@@ -311,31 +347,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         issued[r] = c + 1;
         return true;
       };
+      const bool pv = BWD ? !carry : outputs, wq = BWD || outputs;
       for (int c = 0; c < NC; ++c) {
         const int s = c % NS, t0 = cg(c) * C;
         if (warp == 0) {
-          uint8_t* a = base + L::vt(s);
-          uint64_t* f = &sm.full[VT][s];
-          if (!open(VT, c, L::vt_bytes)) break;
+          uint8_t* a = base + L::vp(s);
+          uint64_t* f = &sm.full[VP][s];
+          if (!open(VP, c, pv ? L::vp_bytes : 2 * TILE)) break;
           const int tv = ident ? N * C : t0;  // past the last token: zeros
           tma_load_3d(a + L::v, &tmV, f, n0, tv, bh);
           tma_load_3d(a + L::v + TILE, &tmV, f, n0 + 64, tv, bh);
-          tma_load_3d(a + L::t, &tmT, f, 0, t0, bh);
-          if (SPLIT) tma_load_3d(a + L::tl, &tmTl, f, 0, t0, bh);
-          a = base + L::kp(s);
-          f = &sm.full[KP][s];
-          if (!open(KP, c, L::kp_bytes - (!BWD && carry ? TILE : 0))) break;
-          tma_load_3d(a + L::k, &tmK, f, 0, t0, kh);
-          tma_load_3d(a + L::k + TILE, &tmK, f, 64, t0, kh);
-          if (outputs) tma_load_3d(a + L::p, &tmP, f, 0, t0, bh);
-        } else {
-          uint8_t* a = base + L::wq_at(s);
-          uint64_t* f = &sm.full[WQ][s];
-          if (!open(WQ, c, L::wq_bytes - (!BWD && carry ? 2 * TILE : 0))) break;
+          if (pv) tma_load_3d(a + L::p, &tmP, f, 0, t0, bh);
+          if (BWD && pv) tma_load_3d(a + L::pl, &tmP, f, 64, t0, bh);
+          a = base + L::up(s);
+          f = &sm.full[UP][s];
+          if (!open(UP, c, L::up_bytes)) break;
           for (int kb = 0; kb < 2; ++kb) {
-            if (BWD || outputs) tma_load_3d(a + L::q + kb * L::wq, &tmQ, f, 64 * kb, t0, kh);
-            tma_load_3d(a + L::w + kb * L::wq, &tmW, f, 64 * kb, t0, bh);
-            if (SPLIT) tma_load_3d(a + L::wl + kb * L::wq, &tmWl, f, 64 * kb, t0, bh);
+            tma_load_3d(a + L::k + kb * TILE, BWD ? &tmK : &tmKw, f, 64 * kb, t0, BWD ? kh : bh);
+            if (SPLIT) tma_load_3d(a + L::kl + kb * TILE, &tmKwl, f, 64 * kb, t0, bh);
+          }
+        } else {
+          uint8_t* a = base + L::kq(s);
+          uint64_t* f = &sm.full[KQ][s];
+          if (!open(KQ, c, wq ? L::kq_bytes : 2 * TILE)) break;
+          for (int kb = 0; kb < 2; ++kb) {
+            tma_load_3d(a + L::w + kb * L::wq, BWD ? &tmKw : &tmK, f, 64 * kb, t0, BWD ? bh : kh);
+            if (wq) tma_load_3d(a + L::q + kb * L::wq, &tmWq, f, 64 * kb, t0, bh);
           }
         }
       }
@@ -347,53 +384,64 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      const uint32_t id_v = idesc_bf16(128, SPLIT ? 128 : 64, true, BWD);  // V^T T0^T, dY^T PT
-      const uint32_t id_w = idesc_bf16(128, 64, false, false);    // S W^T, S Q^T, D^T Pb^T
-      const uint32_t id_wq = idesc_bf16(128, 128, false, false);  // S [W; Q]^T, S [W; Wlo]^T
-      const uint32_t id_wwq = idesc_bf16(128, 192, false, false); // S [W; Wlo; Q]^T
-      const uint32_t id_u = idesc_bf16(128, 128, false, true);    // U^T K, E^T K
-      const uint32_t id_o = idesc_bf16(128, 128, true, true);     // dY^T Q
-      // D^T of chunk c = V^T T0^T. Its pair of accumulators is free once the chain has read D
+      const uint32_t id_v = idesc_bf16(128, 64, true, BWD);       // V^T I, V^T Pv^T, dY^T Pv
+      const uint32_t id_w = idesc_bf16(128, 64, false, false);    // S K^T, D^T T0^T
+      const uint32_t id_wq = idesc_bf16(128, 128, false, false);  // S [K; Wq]^T
+      const uint32_t id_u = idesc_bf16(128, 128, false, true);    // R^T Kw, F^T K
+      const uint32_t id_o = idesc_bf16(128, 128, true, true);     // dY^T Wq
+      const uint32_t s_id = smem_u32(base + L::id);
+      // (V or dY)^T b into d, b [64 x 64]
+      auto from_v = [&](uint32_t d, int c, uint32_t b, bool on) {
+        const uint32_t sv = smem_u32(base + L::vp(c % NS)) + L::v;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_bf16(d, desc_at(sw128_desc(sv, TILE, 1024), kk * 2048),
+                    desc_at(sw128_desc(b, BWD ? TILE : 16, 1024), BWD ? kk * 2048 : kk * 32), id_v,
+                    on || kk > 0);
+      };
+      auto pv_at = [&](int c) { return smem_u32(base + L::vp(c % NS)) + L::p; };
+      // What of chunk c needs no state. Its accumulators are free once the chain has read R
       // (uready, waited by then) and the outputs have been taken.
       auto first = [&](int c) -> bool {
-        const int s = c % NS;
-        const uint32_t st = smem_u32(base + L::vt(s)), d = tb + COL_D + 128 * (c % NY);
-        if (!mbar_wait(&sm.full[VT][s], (c / NS) & 1, wc, W_FULL)) return false;
+        const uint32_t d = tb + COL_D + 128 * (c % NY);
+        if (!mbar_wait(&sm.full[VP][c % NS], (c / NS) & 1, wc, W_FULL)) return false;
         if (!SPLIT && !mbar_wait(&sm.yfree[c % NY], ((c / NY) & 1) ^ 1, wc, W_YFREE)) return false;
+        if (SPLIT && errors && !mbar_wait(&sm.yfree[0], (c & 1) ^ 1, wc, W_YFREE)) return false;
         tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t av = desc_at(sw128_desc(st + L::v, TILE, 1024), kk * 2048);
-          const uint32_t off = BWD ? kk * 2048 : kk * 32;
-          umma_bf16(d, av, desc_at(sw128_desc(st + L::t, BWD ? TILE : 16, 1024), off), id_v, kk > 0);
+        if (BWD) {
+          if (!carry) {
+            from_v(d, c, pv_at(c), false);
+            from_v(d, c, pv_at(c) + TILE, true);
+          }
+        } else {
+          from_v(d, c, s_id, false);
+          if (!SPLIT) {
+            if (outputs) from_v(d + 64, c, pv_at(c), false);
+            umma_commit(&sm.empty[VP][c % NS]);
+          }
         }
-        if (!BWD) umma_commit(&sm.empty[VT][s]);
         return true;
       };
       bool ok = first(0);
       for (int c = 0; c < NC && ok; ++c) {
         const int s = c % NS, yb = c % NY;
-        const uint32_t st = smem_u32(base + L::wq_at(s)), sv = smem_u32(base + L::vt(s));
-        const uint32_t sk = smem_u32(base + L::kp(s));
-        const uint32_t d = tb + COL_D + 128 * yb, y = SPLIT ? tb + COL_YS : d + 64;
-        if (!mbar_wait(carry && !BWD ? &sm.full[WQ][s] : &sm.scaled[s], (c / NS) & 1, wc, W_SCALED)) break;
+        const uint32_t st = smem_u32(base + L::kq(s)), sv = smem_u32(base + L::vp(s));
+        const uint32_t sk = smem_u32(base + L::up(s));
+        const uint32_t d = tb + COL_D + 128 * yb, y = d + 64;  // SPLIT: S K^T in y, Y^T behind it
+        if (!mbar_wait(!BWD && !SPLIT ? &sm.scaled[s] : &sm.full[KQ][s], (c / NS) & 1, wc, W_SCALED)) break;
         if (!mbar_wait(&sm.sready[0], c & 1, wc, W_SREADY)) break;
         tc_fence_after();
-        // D^T += S W^T, and without SPLIT Y^T = S Q^T in the same products
-        if (!SPLIT && outputs) {
-          umma_bf16_tmem_a(d, tb + COL_SH, sw128_desc(st + L::w, 16, 1024), id_w, 1);
-          umma_bf16_tmem_a(y, tb + COL_SH, sw128_desc(st + L::q, 16, 1024), id_w, 0);
-#pragma unroll
-          for (int kk = 1; kk < 8; ++kk)
-            umma_bf16_tmem_a(d, tb + COL_SH + 8 * kk,
-                             desc_at(sw128_desc(st + L::w, 16, 1024), (kk >> 2) * L::wq + (kk & 3) * 32),
-                             id_wq, 1);
-        } else if (!SPLIT) {
+        auto kq = [&](int kk) {
+          return desc_at(sw128_desc(st + L::w, 16, 1024), (kk >> 2) * L::wq + (kk & 3) * 32);
+        };
+        if (BWD) {  // F^T = S Kw^T
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            umma_bf16_tmem_a(d, tb + COL_SH + 8 * kk,
-                             desc_at(sw128_desc(st + L::w, 16, 1024), (kk >> 2) * L::wq + (kk & 3) * 32),
-                             id_w, 1);
+            umma_bf16_tmem_a(y, tb + COL_SH + 8 * kk, kq(kk), id_w, kk > 0);
+        } else if (!SPLIT) {  // R^T -= S (G K)^T, Y^T += S Wq^T
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_bf16_tmem_a(d, tb + COL_SH + 8 * kk, kq(kk), outputs ? id_wq : id_w, 1);
         } else {
           // the K steps in the order in which the two warpgroups convert S, so that the products
           // of the first half run while the second is converted
@@ -406,16 +454,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int kk = 4 * (j >> 1) + 2 * half + (j & 1);
-              const uint32_t off = (kk >> 2) * L::wq + (kk & 3) * 32;
-              const uint64_t bw = desc_at(sw128_desc(st + L::w, 16, 1024), off);
-              if (outputs && kk > 0) {
-                umma_bf16_tmem_a(d, tb + COL_SH + 8 * kk, bw, id_wwq, 1);
-              } else {
-                umma_bf16_tmem_a(d, tb + COL_SH + 8 * kk, bw, id_wq, 1);
-                if (outputs)
-                  umma_bf16_tmem_a(y, tb + COL_SH, desc_at(sw128_desc(st + L::q, 16, 1024), off), id_w, 0);
-              }
-              umma_bf16_tmem_a(d, tb + COL_SL + 8 * kk, bw, id_w, 1);
+              umma_bf16_tmem_a(y, tb + COL_SH + 8 * kk, kq(kk), outputs ? id_wq : id_w, half + j > 0);
+              umma_bf16_tmem_a(y, tb + COL_SL + 8 * kk, kq(kk), id_w, 1);
             }
           }
           if (!got) break;
@@ -426,35 +466,52 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!mbar_wait(&sm.sscaled, c & 1, wc, W_SREADY)) break;
           tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // S += dY^T (scale G Q)
+          for (int kk = 0; kk < 4; ++kk)  // S += dY^T Wq
             umma_bf16(tb + COL_S, desc_at(sw128_desc(sv + L::v, TILE, 1024), kk * 2048),
                       desc_at(sw128_desc(st + L::q, L::wq, 1024), kk * 2048), id_o, 1);
-          umma_commit(&sm.empty[VT][s]);
-          umma_commit(&sm.empty[WQ][s]);
+          umma_commit(&sm.empty[VP][s]);
+          umma_commit(&sm.empty[KQ][s]);
+        } else if (SPLIT) {
+          if (outputs) from_v(y + 64, c, pv_at(c), true);  // Y^T += V^T Pv^T
+          umma_commit(&sm.empty[VP][s]);
+          umma_commit(&sm.empty[KQ][s]);
+          if (!errors) umma_commit(&sm.yfull[yb]);
         } else {
-          umma_commit(&sm.empty[WQ][s]);
-          if (!SPLIT && c + 1 < NC && !first(c + 1)) break;
+          umma_commit(&sm.empty[KQ][s]);
+          if (!errors) umma_commit(&sm.yfull[yb]);
+          if (c + 1 < NC && !first(c + 1)) break;
         }
-        if (!mbar_wait(&sm.full[KP][s], (c / NS) & 1, wc, W_FULL)) break;
+        if (!mbar_wait(&sm.full[UP][s], (c / NS) & 1, wc, W_FULL)) break;
         if (!mbar_wait(&sm.uready, c & 1, wc, W_UREADY)) break;
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {  // S += U^T K
+        for (int kk = 0; kk < 4; ++kk) {  // S += U^T Kw
           const uint64_t bk = desc_at(sw128_desc(sk + L::k, TILE, 1024), kk * 2048);
           umma_bf16_tmem_a(tb + COL_S, tb + COL_U + 8 * kk, bk, id_u, 1);
-          if (SPLIT) umma_bf16_tmem_a(tb + COL_S, tb + COL_UL + 8 * kk, bk, id_u, 1);
+          if (SPLIT) {
+            umma_bf16_tmem_a(tb + COL_S, tb + COL_UL + 8 * kk, bk, id_u, 1);
+            umma_bf16_tmem_a(tb + COL_S, tb + COL_U + 8 * kk,
+                             desc_at(sw128_desc(sk + L::kl, TILE, 1024), kk * 2048), id_u, 1);
+          }
         }
-        umma_commit(&sm.sfull);
-        if (!BWD) {
-          if (outputs) {
+        if (!SPLIT || !errors) umma_commit(&sm.sfull);
+        umma_commit(&sm.empty[UP][s]);
+        if (!BWD && errors) {  // D^T = R^T T0^T
+          if (!mbar_wait(&sm.tfull, c & 1, wc, W_FULL)) break;
+          tc_fence_after();
+          const uint32_t t0 = smem_u32(base + L::t0);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)  // Y^T += D^T Pb^T
-              umma_bf16_tmem_a(y, tb + COL_DB + 8 * kk,
-                               desc_at(sw128_desc(sk + L::p, 16, 1024), kk * 32), id_w, 1);
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t hi = desc_at(sw128_desc(t0, 16, 1024), kk * 32);
+            umma_bf16_tmem_a(d, tb + COL_DB + 8 * kk, hi, id_w, kk > 0);
+            umma_bf16_tmem_a(d, tb + COL_DB + 8 * kk, desc_at(sw128_desc(t0 + TILE, 16, 1024), kk * 32),
+                             id_w, 1);
+            if (SPLIT) umma_bf16_tmem_a(d, tb + COL_UL + 8 * kk, hi, id_w, 1);
           }
           umma_commit(&sm.yfull[yb]);
+          umma_commit(&sm.tempty);
+          if (SPLIT) umma_commit(&sm.sfull);  // the remainder of R lies where that of S comes next
         }
-        umma_commit(&sm.empty[KP][s]);
         if ((BWD || SPLIT) && c + 1 < NC) ok = first(c + 1);
       }
       umma_commit(&sm.done);
@@ -464,17 +521,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ gates
     if (lane == 0) {
       const char* src = reinterpret_cast<const char*>(p.gates) + GateSlot<BWD>::offset;
-      int issued = 0;
-      for (int c = 0; c < NC; ++c) {
+      int issued = 0, loaded = 0;
+      auto gates = [&](int c) -> bool {
         const int g = c % GS;
-        if (!mbar_wait(&sm.gempty[g], ((c / GS) & 1) ^ 1, wc, W_GATE)) break;
+        if (!mbar_wait(&sm.gempty[g], ((c / GS) & 1) ^ 1, wc, W_GATE)) return false;
         mbar_arrive_expect_tx(&sm.gfull[g], sizeof(GateSlot<BWD>));
         bulk_load(&sm.gates[g], src + ((size_t)bh * N + cg(c)) * sizeof(GateBlock),
                   sizeof(GateSlot<BWD>), &sm.gfull[g]);
         issued = c + 1;
+        return true;
+      };
+      // two chunks ahead of T0, which waits for the chunk before
+      bool ok = gates(0) && (NC < 2 || gates(1));
+      for (int c = 0; c < NC && ok; ++c) {
+        if (!BWD && errors) {
+          if (!mbar_wait(&sm.tempty, (c & 1) ^ 1, wc, W_T0)) break;
+          mbar_arrive_expect_tx(&sm.tfull, 2 * TILE);
+          tma_load_3d(base + L::t0, &tmT, &sm.tfull, 0, cg(c) * C, bh);
+          tma_load_3d(base + L::t0 + TILE, &tmT, &sm.tfull, 64, cg(c) * C, bh);
+          loaded = c + 1;
+        }
+        if (c + 2 < NC) ok = gates(c + 2);
       }
       for (int c = issued > GS ? issued - GS : 0; c < issued; ++c)
         mbar_drain(&sm.gfull[c % GS], (c / GS) & 1, wc, W_TMA_DRAIN);
+      if (loaded) mbar_drain(&sm.tfull, (loaded - 1) & 1, wc, W_TMA_DRAIN);
     }
   } else if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------ the chain
@@ -620,69 +691,67 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // this warp's 32 factors, before the wait: shared memory is busy with operands after it
       float uf[32];
+      auto factors = [&](const float* f) {
 #pragma unroll
-      for (int e = 0; e < 32; e += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(gs.u + 32 * hh + e);
-        uf[e] = f.x;
-        uf[e + 1] = f.y;
-        uf[e + 2] = f.z;
-        uf[e + 3] = f.w;
-      }
+        for (int e = 0; e < 32; e += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(f + 32 * hh + e);
+          uf[e] = x.x;
+          uf[e + 1] = x.y;
+          uf[e + 2] = x.z;
+          uf[e + 3] = x.w;
+        }
+      };
+      factors(SPLIT ? gate_nG(gs) : gs.u);
       ok = mbar_wait_warp(&sm.dfull, c & 1, wc, W_C_DFULL);
       if (!ok) break;
       tc_fence_after();
-      float v[32];
-      tmem_ld32(tb + COL_D + 128 * (c % NY) + lo + 32 * hh, v);
+      float v[32];  // R, or F
+      const uint32_t acc = tb + COL_D + 128 * (c % NY) + lo + 32 * hh;
+      tmem_ld32(BWD ? acc + 64 : acc, v);
       if constexpr (SPLIT) {
         float w[32];
-        tmem_ld32(tb + COL_D + 64 + lo + 32 * hh, w);
+        tmem_ld32(acc + 64, w);
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] += w[e];
+        for (int e = 0; e < 32; ++e) v[e] = fmaf(uf[e], w[e], v[e]);
+        factors(gs.u);
       } else {
         tmem_ld_wait();
       }
-      uint32_t db[16];  // D (E) in bf16: 32 tokens of this row
       {
-        uint32_t ub[16], rest[16];
+        uint32_t ub[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float u0 = v[2 * e] * uf[2 * e], u1 = v[2 * e + 1] * uf[2 * e + 1];
-          ub[e] = pack_bf16(u0, u1);
-          db[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-          if (SPLIT) rest[e] = pack_rest(u0, u1, ub[e]);
-        }
+        for (int e = 0; e < 16; ++e) ub[e] = pack_bf16(v[2 * e] * uf[2 * e], v[2 * e + 1] * uf[2 * e + 1]);
         st_tmem16(tb + COL_U + lo + 16 * hh, ub);
-        if (!BWD) st_tmem16(tb + COL_DB + lo + 16 * hh, db);
-        if (SPLIT) st_tmem16(tb + COL_UL + lo + 16 * hh, rest);
+        if constexpr (SPLIT) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            ub[e] = pack_rest(v[2 * e] * uf[2 * e], v[2 * e + 1] * uf[2 * e + 1], ub[e]);
+          st_tmem16(tb + COL_UL + lo + 16 * hh, ub);
+        }
+        if (!BWD && errors) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) ub[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+          st_tmem16(tb + COL_DB + lo + 16 * hh, ub);
+        }
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.uready);
-      if (p.D && !carry) {
-        if (L::staged) {  // a warp stores its own 32 rows x 32 tokens (64-byte rows and swizzle)
-          if (lane == 0) tma_store_wait_read_n<1>();  // all but S of this chunk
-          __syncwarp();
-          uint8_t* const part = base + L::stage_d + (warp - 4) * 2048;
-          const uint32_t at = smem_u32(part) + lane * 64;
+      if (BWD && p.D && !carry) {  // E = (F + Pv^T dY) / bt, two bf16
+        bf16* const out = p.D + (((size_t)bh * N + n) * 2 * rows + n0 + r) * C + 32 * hh;
+        factors(gate_rb(gs));
 #pragma unroll
-          for (int cc = 0; cc < 4; ++cc)
-            st_shared_v4(at + ((cc ^ ((lane >> 1) & 3)) << 4), db[4 * cc], db[4 * cc + 1],
-                         db[4 * cc + 2], db[4 * cc + 3]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_3d(&tmD, part, 32 * hh, n0 + 32 * q, bh * N + n);
-            tma_store_commit();
-          }
-        } else {
-          uint4* out = reinterpret_cast<uint4*>(
-              p.D + (((size_t)bh * N + n) * rows + n0 + r) * C + 32 * hh);
+        for (int hf = 0; hf < 2; ++hf) {
+          float w[16];
+          tmem_ld16(acc + 16 * hf, w);
+          tmem_ld_wait();
 #pragma unroll
-          for (int cc = 0; cc < 4; ++cc)
-            out[cc] = make_uint4(db[4 * cc], db[4 * cc + 1], db[4 * cc + 2], db[4 * cc + 3]);
+          for (int e = 0; e < 16; ++e) w[e] = (w[e] + v[16 * hf + e]) * uf[16 * hf + e];
+          store_split<16>(out + 16 * hf, (size_t)rows * C, w);
         }
+        tc_fence_before();
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.gempty[g]);
@@ -718,22 +787,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp >= 12) {
-    // ------------------------------------------------------------ scaled Q; outputs
+    // ------------------------------------------------------------ scaled K; outputs
     const int q = warp & 3, t = threadIdx.x & 127;
     const uint32_t lo = (uint32_t)(32 * q) << 16;
     auto scale_chunk = [&](int c) -> bool {
       const int s = c % NS, g = c % GS;
-      if (!BWD && carry) return true;
-      if (!mbar_wait_warp(&sm.full[WQ][s], (c / NS) & 1, wc, W_O_FULL)) return false;
+      if (BWD || SPLIT) return true;
+      if (!mbar_wait_warp(&sm.full[KQ][s], (c / NS) & 1, wc, W_O_FULL)) return false;
       if (!mbar_wait_warp(&sm.gfull[g], (c / GS) & 1, wc, W_O_GATE)) return false;
-      scale_tile(smem_u32(base + L::wq_at(s)) + L::q, L::wq, sm.gates[g].q, t);
+      scale_tile(smem_u32(base + L::kq(s)) + L::w, L::wq, gate_nG(sm.gates[g]), t);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.scaled[s]);
       return true;
     };
-    // 128 rows x 64 tokens at TMEM column `col` to a [64 tokens x 128] tile of `map`, times
-    // factor[token] if given
+    // 128 rows x 64 tokens at TMEM column `col` (backward: the sum of those and the 64 behind them) to
+    // a [64 tokens x 128] tile of `map`, times factor[token] if given
     uint8_t* const stage = base + L::stage_o;
     const uint32_t tile = smem_u32(stage);
     auto emit = [&](uint32_t col, const CUtensorMap* map, const float* factor, int t0, uint64_t* after) {
@@ -743,7 +812,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int hf = 0; hf < 2; ++hf) {
         float v[32];
         tmem_ld_frag64(tb + col + lo + hf * LANE16, v);
-        tmem_ld_wait();
+        if constexpr (BWD) {
+          float w[32];
+          tmem_ld_frag64(tb + col + 64 + lo + hf * LANE16, w);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] += w[e];
+        } else {
+          tmem_ld_wait();
+        }
         if (after && hf == 1) {
           tc_fence_before();
           __syncwarp();
@@ -773,19 +850,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int c = 0; c < NC; ++c) {
       const int g = c % GS, yb = c % NY, t0 = cg(c) * C;
       if (ok && c + 1 < NC) ok = scale_chunk(c + 1);
+      if (BWD) ok = ok && mbar_wait_warp(&sm.gfull[g], (c / GS) & 1, wc, W_O_GATE);
       ok = ok && mbar_wait_warp(&sm.yfull[yb], (c / NY) & 1, wc, W_O_Y);
       // the warps of emit() meet at barriers: all of them go on, or none does
       ok = !named_bar_or(2, 128, !ok);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t d = COL_D + 128 * yb;  // D^T (E^T)
+      const uint32_t d = COL_D + 128 * yb;
+      if (!BWD && errors) {  // D, two bf16: a row of 64 tokens per thread
+        bf16* const out = p.D + (((size_t)bh * N + cg(c)) * 2 * dvp(p.d) + n0 + 32 * q + lane) * C;
+#pragma unroll
+        for (int hf = 0; hf < 4; ++hf) {
+          float v[16];
+          tmem_ld16(tb + d + lo + 16 * hf, v);
+          tmem_ld_wait();
+          store_split<16>(out + 16 * hf, (size_t)dvp(p.d) * C, v);
+        }
+      }
       if (carry || (!BWD && !p.y)) {
+        tc_fence_before();
+        __syncwarp();
         if (lane == 0) mbar_arrive(&sm.yfree[yb]);
       } else if constexpr (BWD) {
-        emit(d, &tmY, sm.gates[g].be, t0, &sm.yfree[yb]);  // dV = beta E
+        emit(d, &tmY, gate_z(sm.gates[g]), t0, &sm.yfree[yb]);  // dV = beta E
       } else {
-        emit(SPLIT ? COL_YS : d + 64, &tmY, nullptr, t0, &sm.yfree[yb]);
+        emit(SPLIT ? d + 128 : d + 64, &tmY, nullptr, t0, &sm.yfree[yb]);
       }
+      __syncwarp();
       if (lane == 0) mbar_arrive(&sm.gempty[g]);
     }
     if (t == 0) tma_store_wait_all();
@@ -806,22 +897,17 @@ static cudaError_t launch(const Args& a, bool sum, bool after, cudaStream_t st) 
   const uint64_t N = chunks(d.T), kh = (uint64_t)d.B * d.Hk, bh = d.BH();
   const void* v = BWD ? a.dy : a.v;
   bf16* states = BWD ? a.dS : a.sv.S;
-  const bf16* w = BWD ? a.sv.Wb : a.m.W;
-  const bf16* t = BWD ? a.sv.PT : a.m.T0;
+  const Mats& m = a.m;
   bf16* dd = BWD ? a.E : a.sv.D;           // D or E
   void* yy = BWD ? a.dv_ : a.y;
-  CUtensorMap mq, mk, mv, mw, mwl, mt, mtl, mp, ms, my, md;
-  if (!make_map_bf16_3d(&mq, a.q, d.dk, d.T, kh, C) || !make_map_bf16_3d(&mk, a.k, d.dk, d.T, kh, C) ||
-      !make_map_bf16_3d(&mv, v, d.dv, d.T, bh, C) || !make_map_bf16_3d(&mw, w, 128, N * C, bh, C) ||
-      !make_map_bf16_3d(&mwl, SPLIT ? a.m.Wlo : w, 128, N * C, bh, C) ||
-      !make_map_bf16_3d(&mt, t, C, N * C, bh, C) ||
-      !make_map_bf16_3d(&mtl, SPLIT ? a.m.T0lo : t, C, N * C, bh, C) ||
-      !make_map_bf16_3d(&mp, BWD ? t : a.m.Pb, C, N * C, bh, C) ||
-      !make_map_bf16_3d(&ms, states ? (const void*)states : w, 128, states ? dvp(d) : N * C,
+  CUtensorMap mk, mv, mw, mwl, mq, mp, mt, ms, my;
+  auto mat = [&](CUtensorMap* t, const bf16* x) { return make_map_bf16_3d(t, x, 128, N * C, bh, C); };
+  if (!make_map_bf16_3d(&mk, a.k, d.dk, d.T, kh, C) || !make_map_bf16_3d(&mv, v, d.dv, d.T, bh, C) ||
+      !mat(&mw, m.Kw) || !mat(&mwl, SPLIT ? m.Kwlo : m.Kw) || !mat(&mq, m.Wq) || !mat(&mp, m.Pv) ||
+      !mat(&mt, !BWD && dd ? m.T0 : m.Pv) ||
+      !make_map_bf16_3d(&ms, states ? states : m.Kw, 128, states ? dvp(d) : N * C,
                         states ? bh * N : bh, 32) ||
-      !make_map_bf16_3d(&my, yy ? yy : v, d.dv, d.T, bh, C) ||
-      !gradlev::tc::make_map_bf16_3d_box(&md, dd ? (const void*)dd : w, dd ? C : 128,
-                                         dd ? dvp(d) : N * C, dd ? bh * N : bh, 32, 32))
+      !make_map_bf16_3d(&my, yy ? yy : v, d.dv, d.T, bh, C))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> set{0};
   int dev = 0;
@@ -834,7 +920,7 @@ static cudaError_t launch(const Args& a, bool sum, bool after, cudaStream_t st) 
     set.fetch_or(bit);
   }
   const int ns = dvp(d) / 128, nseg = a.seg.nseg;
-  WalkParams p{d, BWD ? a.sv.gates : a.m.gates, a.status, a.timeout_ns, a.S0, a.log_alpha,
+  WalkParams p{d, m.gates, a.status, a.timeout_ns, a.S0, a.log_alpha,
                static_cast<const bf16*>(a.dST), a.ST, static_cast<bf16*>(a.dS0),
                static_cast<bf16*>(a.y), dd, states, nseg, a.seg.chunks, 0, nseg, ns, sum ? 0 : a.inject, sum,
                nseg > 1 ? a.init : nullptr, a.loc, a.M};
@@ -848,12 +934,11 @@ static cudaError_t launch(const Args& a, bool sum, bool after, cudaStream_t st) 
     grid += (unsigned)bh;  // the last segment's map, for the backward
   }
   if (after) {
-    const cudaError_t e = launch_after(d, walk_kernel<BWD, SPLIT>, grid, kThreads, L::smem, st, mq, mk, mv,
-                                       mw, mwl, mt, mtl, mp, ms, my, md, p);
+    const cudaError_t e = launch_after(d, walk_kernel<BWD, SPLIT>, grid, kThreads, L::smem, st, mk, mv, mw,
+                                       mwl, mq, mp, mt, ms, my, p);
     if (e != cudaSuccess) return e;
   } else {
-    walk_kernel<BWD, SPLIT><<<grid, kThreads, L::smem, st>>>(mq, mk, mv, mw, mwl, mt, mtl, mp, ms, my,
-                                                             md, p);
+    walk_kernel<BWD, SPLIT><<<grid, kThreads, L::smem, st>>>(mk, mv, mw, mwl, mq, mp, mt, ms, my, p);
   }
   count_launch();
   return cudaGetLastError();
