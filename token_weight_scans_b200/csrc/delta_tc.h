@@ -21,6 +21,8 @@ namespace gradlev {
 namespace tc {
 bool make_map_bf16_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                       uint32_t box1);
+bool make_map_bf16_3d_box(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                          uint32_t box0, uint32_t box1);
 }
 
 namespace delta {

@@ -234,7 +234,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int hv = 0; hv < grp; ++hv, ++nhead) {
     const int bh = bh0 + hv;
     const GradGates& g = sm.gates[nhead & 1];
-    int bh1 = bh, n1 = n, sl1 = 0;  // the next slice
+    // The slice after the last one of this head, of the next head or (behind what follows here) the
+    // next chunk; whether there is one
+    auto next = [&](int& bh1, int& n1) -> bool {
+      const unsigned id1 = id + (hv + 1 < grp ? 0u : gridDim.x);
+      bh1 = hv + 1 < grp ? bh + 1 : first_head(id1);
+      n1 = id1 % N;
+      return id1 < total;
+    };
     F2 ss = f2(0.f, 0.f);  // <dS, S>
     for (int sl = 0; sl < nsl; ++sl) {
       mbar_wait(&sm.full, nfull++ & 1, wc, W_G_FULL);
@@ -289,17 +296,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       // S and dS are read
       stop = __syncthreads_or(*reinterpret_cast<volatile int*>(&sm.abort));
       if (stop) break;
-      // the next slice, of this head or the next one or (behind what follows here) the next chunk;
-      // X and Yn come before its D and E
-      bh1 = bh, n1 = n, sl1 = sl + 1;
-      if (sl1 == nsl) {
-        const unsigned id1 = id + (hv + 1 < grp ? 0u : gridDim.x);
-        bh1 = hv + 1 < grp ? bh + 1 : first_head(id1);
-        n1 = id1 % N;
-        sl1 = id1 < total ? 0 : -1;
+      // the next slice; X and Yn come before the next head's D and E
+      if (sl + 1 < nsl) {
+        load_slice(bh, n, sl + 1, nullptr);
+        load_de(bh, n, sl + 1);
+      } else {
+        int bh1, n1;
+        if (next(bh1, n1)) load_slice(bh1, n1, 0, &sm.gates[(nhead + 1) & 1]);
       }
-      if (sl1 >= 0) load_slice(bh1, n1, sl1, &sm.gates[(nhead + 1) & 1]);
-      if (sl1 > 0) load_de(bh1, n1, sl1);
       __syncwarp();
     }
     if (stop) break;
@@ -314,26 +318,26 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float rx = p.scale * g.ra[i], ry = -g.be[i] * g.ra[i];
     float db = 0.f;
 #pragma unroll
-    for (int hf = 0; hf < 32 / XW; ++hf) {
-      float f[XW], y[XW];
-      const int j0 = 32 * hh + XW * hf;
-      tmem_ld(tb + COL_B + lo + j0, f);
-      tmem_ld(tb + COL_B + 64 + lo + j0, y);
+    for (int it = 0; it < 2 * 32 / XW; ++it) {
+      const bool second = it >= 32 / XW;  // Yn after X, as the registers allow
+      float f[XW];
+      const int hf = it % (32 / XW), j0 = 32 * hh + XW * hf;
+      tmem_ld(tb + COL_B + (second ? 64 : 0) + lo + j0, f);
       tmem_ld_wait();
       if (!up) {
-        const int keep = i - j0;  // columns left of the diagonal
+        const int keep = i - j0 + (second ? 0 : 1);  // the first columns: left of the diagonal (X: and on it)
+        const float r = second ? ry : rx;
+        if (second) {
 #pragma unroll
-        for (int e = 0; e < XW; ++e) db = e == keep ? y[e] : db;
+          for (int e = 0; e < XW; ++e) db = e == keep ? f[e] : db;
+        }
         if (g.fac != 0.f) {
 #pragma unroll
           for (int e = 0; e < XW; e += 4) {
             const float4 c = *reinterpret_cast<const float4*>(g.cb + j0 + e);
             const float cv[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              f[e + u] = e + u <= keep ? f[e + u] * (rx * cv[u]) : 0.f;
-              y[e + u] = e + u < keep ? y[e + u] * (ry * cv[u]) : 0.f;
-            }
+            for (int u = 0; u < 4; ++u) f[e + u] = e + u < keep ? f[e + u] * (r * cv[u]) : 0.f;
           }
         } else {  // a reset, or decays whose factors leave float32
           const float Lh = sm.Lh[i], Ll = sm.Ll[i];
@@ -342,17 +346,12 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int e = 0; e < XW; ++e) {
             const int j = j0 + e;
             const float m = g.cb[j] * expf(fminf((Lh - sm.Lh[j]) + (Ll - sm.Ll[j]), 0.f));
-            const bool on = sm.seg[j] == seg;
-            f[e] = on && e <= keep ? f[e] * (rx * m) : 0.f;
-            y[e] = on && e < keep ? y[e] * (ry * m) : 0.f;
+            f[e] = sm.seg[j] == seg && e < keep ? f[e] * (r * m) : 0.f;
           }
         }
 #pragma unroll
-        for (int cc = 0; cc < XW / 8; ++cc) {
-          const uint32_t off = sw128_off(i, 4 * hh + XW / 8 * hf + cc);
-          put_split8(sX + off, f + 8 * cc);
-          put_split8(sY + off, y + 8 * cc);
-        }
+        for (int cc = 0; cc < XW / 8; ++cc)
+          put_split8((second ? sY : sX) + sw128_off(i, 4 * hh + XW / 8 * hf + cc), f + 8 * cc);
       }
       __syncwarp();
     }
@@ -430,7 +429,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     mbar_wait(&sm.mma, nmma++ & 1, wc, W_G_MMA);
     __syncwarp();
     tc_fence_after();
-    if (sl1 >= 0) load_de(bh1, n1, 0);  // X and Yn are read
+    {
+      int bh1, n1;
+      if (next(bh1, n1)) load_de(bh1, n1, 0);  // X and Yn are read
+    }
     __syncwarp();
     // ---- xk (lower) and ka (upper); yk (upper)
     dv = dz = f2(0.f, 0.f);

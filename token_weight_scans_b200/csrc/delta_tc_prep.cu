@@ -45,15 +45,15 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int LD = 68;        // row stride (floats) of the 64 x 64 float32 matrices: 16-byte rows
-// TMEM, in the lower and the upper 16 lanes of each 32: K K^T | Q K^T in columns 0 to 63; Kw | Pv
-// (columns 64 to 127); Kw | Wq
+// TMEM, in the lower and the upper 16 lanes of each 32: K K^T | Q K^T (64 columns); Kw | Pv (64);
+// Kw | Wq
 constexpr uint32_t kCols = 128;
 constexpr float kTiny = 0x1p-60f;
 constexpr int kLoader = 128;  // the thread that loads K and Q, and stores P and PT
 
-// Tiles live where something dead was. Over N: diag(beta w) T0, then P diag(beta), then Pv diag(G)
-// (two bf16 each), at the end Kw. Over X: T0, then Pv, at the end the remainder of Kw. Wq goes over
-// Q, row by row as it is formed.
+// Tiles live where something dead was. Over N: diag(beta w) T0, then Pv diag(G), at the end Kw. Over
+// X: T0, then Pv, at the end the remainder of Kw. Over Q: P diag(beta) (all these two bf16 each);
+// then Q again, from L2, and Wq over it, row by row as it is formed.
 struct PrepSmem {
   uint8_t K[2 * TILE];         // k-blocks: 64 token rows x 128 B
   uint8_t Q[2 * TILE];
@@ -73,14 +73,14 @@ struct PrepSmem {
   float Lh[C], Ll[C], G[C], wb[C], sG[C];
   int seg[C];
   int fac;
-  uint64_t full, mma;
+  uint64_t full, qfull, mma;
   uint32_t tmem_base;
   int abort;
 };
 constexpr size_t kSmem = sizeof(PrepSmem) + 1024;
 static_assert(3 * (kSmem + 1024) <= 228 * 1024, "three CTAs per SM");
 
-enum : uint32_t { W_PREP_LOAD = 0x801, W_PREP_MMA, W_PREP_DRAIN };
+enum : uint32_t { W_PREP_LOAD = 0x801, W_PREP_Q, W_PREP_MMA, W_PREP_DRAIN };
 
 struct PrepParams {
   Dims d;
@@ -127,13 +127,12 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int N = chunks(p.d.T);
   const WaitCtx wc{&sm.abort, p.status, p.timeout_ns};
   const unsigned total = (unsigned)((size_t)p.d.B * p.d.H * N);
-  // one thread; K, which announces both, before Q
-  auto load_kq = [&](unsigned id, bool q) {
+  // one thread: K or Q of a chunk
+  auto load = [&](unsigned id, bool q, uint64_t* bar) {
     const int bh = id / N, t0 = (id - bh * N) * C, b = bh / p.d.H, h = bh - b * p.d.H;
     const int kh = b * p.d.Hk + h / (p.d.H / p.d.Hk);
-    if (!q) mbar_arrive_expect_tx(&sm.full, 4 * TILE);
-    tma_load_3d(q ? sm.Q : sm.K, q ? &tmQ : &tmK, &sm.full, 0, t0, kh);
-    tma_load_3d((q ? sm.Q : sm.K) + TILE, q ? &tmQ : &tmK, &sm.full, 64, t0, kh);
+    tma_load_3d(q ? sm.Q : sm.K, q ? &tmQ : &tmK, bar, 0, t0, kh);
+    tma_load_3d((q ? sm.Q : sm.K) + TILE, q ? &tmQ : &tmK, bar, 64, t0, kh);
   };
   grid_dep_launch();
   RawGates raw{};
@@ -145,10 +144,12 @@ __global__ void __launch_bounds__(kThreads, 3)
   if (tid == kLoader) {
     sm.abort = 0;
     mbar_init(&sm.full, 1);
+    mbar_init(&sm.qfull, 1);
     mbar_init(&sm.mma, 1);
     fence_mbar_init();
-    load_kq(blockIdx.x, false);
-    load_kq(blockIdx.x, true);
+    mbar_arrive_expect_tx(&sm.full, 4 * TILE);
+    load(blockIdx.x, false, &sm.full);
+    load(blockIdx.x, true, &sm.full);
   }
   if (warp == 1) {
     tmem_alloc(&sm.tmem_base, kCols);
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   tc_fence_after();
   const uint32_t tb = sm.tmem_base;
   const uint32_t sK = smem_u32(sm.K), sQ = smem_u32(sm.Q), sA = smem_u32(sm.A[0]), sB = smem_u32(sm.B[0]);
-  uint32_t phase = 0, full = 0, loads = 0;  // loads: after the first, of the loading thread
+  uint32_t phase = 0, full = 0, loads = 0, again = 0;  // loads after the first, and of Q again (loading thread)
   for (unsigned id = blockIdx.x; id < total; id += gridDim.x, full ^= 1) {
   const int bh = id / N, n = id - bh * N, t0 = n * C;
   if (tid == 0) {
@@ -276,6 +277,8 @@ __global__ void __launch_bounds__(kThreads, 3)
       for (int e = 0; e < 32; e += 4)
         *reinterpret_cast<float4*>(sm.N + i * LD + 32 * hh + e) =
             make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+    } else {
+      put_split(sQ, v);
     }
   }
   __syncthreads();
@@ -390,41 +393,30 @@ __global__ void __launch_bounds__(kThreads, 3)
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
-  if (tid == 0) {  // Kw
+  if (tid == 0) {  // Kw and Pv
     tc_fence_after();
     product(tb, sA, true, sK, 128, true);
     product(tb, sA + TILE, true, sK, 128, false);
+    product(tU, sQ, false, sB, 64, true);
+    product(tU, sQ, false, sB + TILE, 64, false);
+    product(tU, sQ + TILE, false, sB, 64, false);
     umma_commit(&sm.mma);
   }
   __syncwarp();
   {
-    // The products above write the lower lanes of all columns; Q K^T is in the upper ones.
-    float v[32];
-    tc_fence_after();
-    scaled(v);
-    mbar_wait(&sm.mma, phase, wc, W_PREP_MMA);
-    phase ^= 1;
-    __syncwarp();
-    if (isP) put_split(sA, v);
+    const bool got = mbar_wait(&sm.mma, phase, wc, W_PREP_MMA);
+    if (tid == kLoader && got) {
+      mbar_arrive_expect_tx(&sm.qfull, 2 * TILE);
+      load(id, true, &sm.qfull);
+      ++again;
+    }
   }
-  fence_proxy_async_smem();
-  tc_fence_before();
-  __syncthreads();
-  if (tid == 0) {  // Pv
-    tc_fence_after();
-    product(tU + 64, sA, false, sB, 64, true);
-    product(tU + 64, sA, false, sB + TILE, 64, false);
-    product(tU + 64, sA + TILE, false, sB, 64, false);
-    umma_commit(&sm.mma);
-  }
-  __syncwarp();
-  mbar_wait(&sm.mma, phase, wc, W_PREP_MMA);
   phase ^= 1;
   __syncwarp();
   tc_fence_after();
   {
     float v[32];
-    tmem_ld32(tb + lo + 64 + 32 * hh, v);
+    tmem_ld32(tb + lo + 32 * hh, v);
     tmem_ld_wait();
     if (isP) {
       put_split(sB, v);
@@ -459,11 +451,13 @@ __global__ void __launch_bounds__(kThreads, 3)
   const bool more = done && id + gridDim.x < total;
   if (tid == kLoader) {
     if (more) {
-      load_kq(id + gridDim.x, false);
+      mbar_arrive_expect_tx(&sm.full, 4 * TILE);
+      load(id + gridDim.x, false, &sm.full);
       ++loads;
     }
     if (SPLIT) tma_store_wait_read();  // Pv
   }
+  mbar_wait(&sm.qfull, full, wc, W_PREP_Q);
   __syncwarp();
   if (SPLIT) __syncthreads();
   tc_fence_after();
@@ -509,12 +503,15 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
     tma_store_commit();
     tma_store_wait_read();  // the places are written again from the next chunk's gates on
-    if (more) load_kq(id + gridDim.x, true);
+    if (more) load(id + gridDim.x, true, &sm.full);
   }
   __syncwarp();
   if (stop) break;
   }
-  if (tid == kLoader) mbar_drain(&sm.full, loads & 1, wc, W_PREP_DRAIN);
+  if (tid == kLoader) {
+    mbar_drain(&sm.full, loads & 1, wc, W_PREP_DRAIN);
+    if (again) mbar_drain(&sm.qfull, (again - 1) & 1, wc, W_PREP_DRAIN);
+  }
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();

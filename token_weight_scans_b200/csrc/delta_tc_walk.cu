@@ -109,7 +109,8 @@ struct Layout {
   static constexpr int kq0 = NS * vp_bytes, up0 = kq0 + NS * kq_bytes;
   static constexpr int t0 = up0 + NS * up_bytes;          // forward: T0 and its remainder
   static constexpr int id = t0 + (BWD ? 0 : 2 * TILE);    // forward: the identity
-  static constexpr bool staged = !SPLIT;   // S through shared memory and TMA
+  // S, and after it D^T (E^T), through shared memory and TMA: 4 KB for each warp of the chain
+  static constexpr bool staged = !SPLIT;
   static constexpr int stage_s = id + (BWD ? 0 : TILE), stage_o = stage_s + (staged ? 2 * BIG : 0);
   static constexpr int bars = stage_o + 2 * TILE;
   static constexpr size_t smem = bars + sizeof(Bars<BWD>) + 1024;
@@ -264,7 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __grid_constant__ CUtensorMap tmKw, const __grid_constant__ CUtensorMap tmKwl,
                 const __grid_constant__ CUtensorMap tmWq, const __grid_constant__ CUtensorMap tmP,
                 const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmS,
-                const __grid_constant__ CUtensorMap tmY, WalkParams p) {
+                const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmD,
+                WalkParams p) {
   using L = Layout<BWD, SPLIT>;
   constexpr int NY = SPLIT ? 1 : 2;   // accumulator pairs
   extern __shared__ uint8_t smem_raw[];
@@ -314,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.tempty, 1);
     for (int y = 0; y < 2; ++y) {
       mbar_init(&sm.yfull[y], 1);
-      mbar_init(&sm.yfree[y], 4);
+      mbar_init(&sm.yfree[y], !BWD && errors && !SPLIT ? 12 : 4);  // the chain takes D
     }
     fence_mbar_init();
   }
@@ -479,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           umma_commit(&sm.empty[KQ][s]);
           if (!errors) umma_commit(&sm.yfull[yb]);
-          if (c + 1 < NC && !first(c + 1)) break;
+          if (!errors && c + 1 < NC && !first(c + 1)) break;
         }
         if (!mbar_wait(&sm.full[UP][s], (c / NS) & 1, wc, W_FULL)) break;
         if (!mbar_wait(&sm.uready, c & 1, wc, W_UREADY)) break;
@@ -512,7 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit(&sm.tempty);
           if (SPLIT) umma_commit(&sm.sfull);  // the remainder of R lies where that of S comes next
         }
-        if ((BWD || SPLIT) && c + 1 < NC) ok = first(c + 1);
+        // (with D: not before this chunk's, whose predecessor the chain takes after uready)
+        if ((BWD || SPLIT || errors) && c + 1 < NC) ok = first(c + 1);
       }
       umma_commit(&sm.done);
       mbar_drain(&sm.done, 0, wc, W_DONE);
@@ -594,6 +597,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_st32(tb + COL_S + lo + col, v);
     }
     tmem_st_wait();
+    // 32 tokens of this row of D (E) as two bf16, the whole warp: through the warp's part of the
+    // buffer that S went through, 64-byte rows and swizzle
+    auto leave = [&](const float (&x)[32], int n) {
+      if (lane == 0) tma_store_wait_read_n<0>();
+      __syncwarp();
+      uint8_t* const part = base + L::stage_s + (warp - 4) * 4096;
+      const uint32_t at = smem_u32(part) + lane * 64;
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+        uint32_t hi[4], rest[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          hi[e] = pack_bf16(x[8 * cc + 2 * e], x[8 * cc + 2 * e + 1]);
+          rest[e] = pack_rest(x[8 * cc + 2 * e], x[8 * cc + 2 * e + 1], hi[e]);
+        }
+        const uint32_t off = (cc ^ ((lane >> 1) & 3)) << 4;
+        st_shared_v4(at + off, hi[0], hi[1], hi[2], hi[3]);
+        st_shared_v4(at + 2048 + off, rest[0], rest[1], rest[2], rest[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(&tmD, part, 32 * hh, n0 + 32 * q, bh * N + n);
+        tma_store_3d(&tmD, part + 2048, 32 * hh, rows + n0 + 32 * q, bh * N + n);
+        tma_store_commit();
+      }
+    };
+    // D of chunk c, once its product is done, and its place for the chunk after the next
+    auto leave_D = [&](int c) {
+      float x[32];
+      tmem_ld32(tb + COL_D + 128 * (c % NY) + lo + 32 * hh, x);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.yfree[c % NY]);
+      leave(x, cg(c));
+    };
+    constexpr bool chain_D = !BWD && !SPLIT;
     bool ok = true;
     for (int c = 0; c < NC && ok; ++c) {
       const int g = c % GS, n = cg(c);
@@ -739,22 +780,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.uready);
-      if (BWD && p.D && !carry) {  // E = (F + Pv^T dY) / bt, two bf16
-        bf16* const out = p.D + (((size_t)bh * N + n) * 2 * rows + n0 + r) * C + 32 * hh;
+      if (BWD && !carry) {  // E = (F + Pv^T dY) / bt
+        float w[32];
         factors(gate_rb(gs));
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float w[16];
-          tmem_ld16(acc + 16 * hf, w);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = (w[e] + v[16 * hf + e]) * uf[16 * hf + e];
-          store_split<16>(out + 16 * hf, (size_t)rows * C, w);
-        }
+        tmem_ld32(acc, w);
+        tmem_ld_wait();
         tc_fence_before();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) w[e] = (w[e] + v[e]) * uf[e];
+        leave(w, n);
       }
+      // D of the chunk before: its product was issued before the one that dfull stands for
+      if (chain_D && errors && c > 0) leave_D(c - 1);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.gempty[g]);
+    }
+    if (chain_D && errors && ok && mbar_wait_warp(&sm.yfull[(NC - 1) % NY], ((NC - 1) / NY) & 1, wc, W_C_DFULL)) {
+      tc_fence_after();
+      leave_D(NC - 1);
     }
     if (lane == 0 && L::staged) tma_store_wait_all();
     float* inner = ident ? p.M + (sg * 128 + r) * 128 : carry ? p.loc + (sg * rows + n0 + r) * 128 : nullptr;
@@ -857,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = COL_D + 128 * yb;
-      if (!BWD && errors) {  // D, two bf16: a row of 64 tokens per thread
+      if (SPLIT && errors) {  // D, two bf16: a row of 64 tokens per thread
         bf16* const out = p.D + (((size_t)bh * N + cg(c)) * 2 * dvp(p.d) + n0 + 32 * q + lane) * C;
 #pragma unroll
         for (int hf = 0; hf < 4; ++hf) {
@@ -900,14 +943,16 @@ static cudaError_t launch(const Args& a, bool sum, bool after, cudaStream_t st) 
   const Mats& m = a.m;
   bf16* dd = BWD ? a.E : a.sv.D;           // D or E
   void* yy = BWD ? a.dv_ : a.y;
-  CUtensorMap mk, mv, mw, mwl, mq, mp, mt, ms, my;
+  CUtensorMap mk, mv, mw, mwl, mq, mp, mt, ms, my, md;
   auto mat = [&](CUtensorMap* t, const bf16* x) { return make_map_bf16_3d(t, x, 128, N * C, bh, C); };
   if (!make_map_bf16_3d(&mk, a.k, d.dk, d.T, kh, C) || !make_map_bf16_3d(&mv, v, d.dv, d.T, bh, C) ||
       !mat(&mw, m.Kw) || !mat(&mwl, SPLIT ? m.Kwlo : m.Kw) || !mat(&mq, m.Wq) || !mat(&mp, m.Pv) ||
       !mat(&mt, !BWD && dd ? m.T0 : m.Pv) ||
       !make_map_bf16_3d(&ms, states ? states : m.Kw, 128, states ? dvp(d) : N * C,
                         states ? bh * N : bh, 32) ||
-      !make_map_bf16_3d(&my, yy ? yy : v, d.dv, d.T, bh, C))
+      !make_map_bf16_3d(&my, yy ? yy : v, d.dv, d.T, bh, C) ||
+      !gradlev::tc::make_map_bf16_3d_box(&md, dd ? dd : m.Kw, dd ? C : 128, dd ? 2 * dvp(d) : N * C,
+                                         dd ? bh * N : bh, 32, 32))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> set{0};
   int dev = 0;
@@ -935,10 +980,10 @@ static cudaError_t launch(const Args& a, bool sum, bool after, cudaStream_t st) 
   }
   if (after) {
     const cudaError_t e = launch_after(d, walk_kernel<BWD, SPLIT>, grid, kThreads, L::smem, st, mk, mv, mw,
-                                       mwl, mq, mp, mt, ms, my, p);
+                                       mwl, mq, mp, mt, ms, my, md, p);
     if (e != cudaSuccess) return e;
   } else {
-    walk_kernel<BWD, SPLIT><<<grid, kThreads, L::smem, st>>>(mk, mv, mw, mwl, mq, mp, mt, ms, my, p);
+    walk_kernel<BWD, SPLIT><<<grid, kThreads, L::smem, st>>>(mk, mv, mw, mwl, mq, mp, mt, ms, my, md, p);
   }
   count_launch();
   return cudaGetLastError();

@@ -794,19 +794,27 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 3-D bf16 map over [d2][d1][d0] (d0 innermost), box {64, box1, 1}, 128-byte swizzle.
-bool make_map_bf16_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
-                      uint32_t box1) {
+// 3-D bf16 map over [d2][d1][d0] (d0 innermost), box {box0, box1, 1}: box0 = 64 with the
+// 128-byte swizzle, box0 = 32 with the 64-byte one.
+bool make_map_bf16_3d_box(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                          uint32_t box0, uint32_t box1) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {d0, d1, d2};
   cuuint64_t strides[2] = {d0 * 2, d0 * d1 * 2};
-  cuuint32_t box[3] = {64, box1, 1};
+  cuuint32_t box[3] = {box0, box1, 1};
   cuuint32_t es[3] = {1, 1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
-                  box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  box0 == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+// Box {64, box1, 1}.
+bool make_map_bf16_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                      uint32_t box1) {
+  return make_map_bf16_3d_box(m, base, d0, d1, d2, 64, box1);
 }
 
 bool fwd_shape_ok(int din, int dout) { return din == 128 && dout % 128 == 0 && dout <= 256; }
