@@ -52,8 +52,8 @@ constexpr float kTiny = 0x1p-60f;
 constexpr int kLoader = 128;  // the thread that loads K and Q, and stores P and PT
 
 // Tiles live where something dead was. Over N: diag(beta w) T0, then Pv diag(G), at the end Kw. Over
-// X: T0, then Pv, at the end the remainder of Kw. Over Q: P diag(beta) (all these two bf16 each);
-// then Q again, from L2, and Wq over it, row by row as it is formed.
+// X: T0, then Pv, at the end Wq, or with SPLIT the remainder of Kw. Over Q: P diag(beta) (all these
+// two bf16 each); then Q again, from L2, and with SPLIT Wq over it, row by row as it is formed.
 struct PrepSmem {
   uint8_t K[2 * TILE];         // k-blocks: 64 token rows x 128 B
   uint8_t Q[2 * TILE];
@@ -217,7 +217,8 @@ __global__ void __launch_bounds__(kThreads, 3)
   }
   mbar_wait(&sm.mma, phase, wc, W_PREP_MMA);
   phase ^= 1;
-  __syncthreads();  // the gates are there
+  if (tid == kLoader) tma_store_wait_read();  // the last chunk's results, whose places come next
+  __syncthreads();                            // the gates are there
   tc_fence_after();
   // Lane l < 16 of quadrant q holds row i = 16 q + l of K K^T, lane l + 16 that of Q K^T;
   // warps q and q + 4 take half of the columns each.
@@ -455,11 +456,10 @@ __global__ void __launch_bounds__(kThreads, 3)
       load(id + gridDim.x, false, &sm.full);
       ++loads;
     }
-    if (SPLIT) tma_store_wait_read();  // Pv
+    tma_store_wait_read();  // Pv
   }
   mbar_wait(&sm.qfull, full, wc, W_PREP_Q);
-  __syncwarp();
-  if (SPLIT) __syncthreads();
+  __syncthreads();
   tc_fence_after();
   // Kw (lanes < 16) and Wq (lanes >= 16) to bf16, columns [64 hh, 64 hh + 64)
   const float sG = sm.sG[i];
@@ -468,12 +468,12 @@ __global__ void __launch_bounds__(kThreads, 3)
     float v[32];
     tmem_ld32(tb + lo + 64 * hh + 32 * g, v);
     tmem_ld_wait();
-    const uint32_t dst = (isP ? sQ : sA) + hh * TILE;
+    const uint32_t dst = (!isP ? sA : SPLIT ? sQ : sB) + hh * TILE;
 #pragma unroll
     for (int cc = 0; cc < 4; ++cc) {
       const uint32_t off = sw128_off(i, 4 * g + cc);
       if (isP) {
-        const uint4 u = ld_shared_v4(dst + off);
+        const uint4 u = ld_shared_v4(sQ + hh * TILE + off);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -499,10 +499,10 @@ __global__ void __launch_bounds__(kThreads, 3)
     for (int kb = 0; kb < 2; ++kb) {
       tma_store_3d(&tmKw, sm.A[kb], 64 * kb, t0, bh);
       if (SPLIT) tma_store_3d(&tmKwlo, sm.B[kb], 64 * kb, t0, bh);
-      tma_store_3d(&tmWq, sm.Q + kb * TILE, 64 * kb, t0, bh);
+      tma_store_3d(&tmWq, SPLIT ? sm.Q + kb * TILE : sm.B[kb], 64 * kb, t0, bh);
     }
     tma_store_commit();
-    tma_store_wait_read();  // the places are written again from the next chunk's gates on
+    if (SPLIT) tma_store_wait_read();  // Wq
     if (more) load(id + gridDim.x, true, &sm.full);
   }
   __syncwarp();
@@ -511,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   if (tid == kLoader) {
     mbar_drain(&sm.full, loads & 1, wc, W_PREP_DRAIN);
     if (again) mbar_drain(&sm.qfull, (again - 1) & 1, wc, W_PREP_DRAIN);
+    tma_store_wait_read();  // shared memory may go once it is read
   }
   __syncthreads();
   if (warp == 1) {

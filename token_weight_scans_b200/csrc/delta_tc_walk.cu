@@ -491,9 +491,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t bk = desc_at(sw128_desc(sk + L::k, TILE, 1024), kk * 2048);
           umma_bf16_tmem_a(tb + COL_S, tb + COL_U + 8 * kk, bk, id_u, 1);
           if (SPLIT) {
+            const uint64_t bl = desc_at(sw128_desc(sk + L::kl, TILE, 1024), kk * 2048);
             umma_bf16_tmem_a(tb + COL_S, tb + COL_UL + 8 * kk, bk, id_u, 1);
-            umma_bf16_tmem_a(tb + COL_S, tb + COL_U + 8 * kk,
-                             desc_at(sw128_desc(sk + L::kl, TILE, 1024), kk * 2048), id_u, 1);
+            umma_bf16_tmem_a(tb + COL_S, tb + COL_U + 8 * kk, bl, id_u, 1);
+            umma_bf16_tmem_a(tb + COL_S, tb + COL_UL + 8 * kk, bl, id_u, 1);  // ST 5.2e-6 -> 4.4e-6 off
           }
         }
         if (!SPLIT || !errors) umma_commit(&sm.sfull);
