@@ -329,7 +329,10 @@ GRADLEV_API gradlev_status gradlev_mlp2_recon(int B, int H, int T, int d_x, int 
  *     S0, ST (states)        [B, H, d_v, d_k]  float32 (all dtypes)
  *     dbeta, dlog_alpha      [B, H, T]         dtype
  *     dST, dS0               [B, H, d_v, d_k]  dtype
- * Every gradient has the I/O dtype: the bf16 path forms gradients from bf16 operands.
+ * Every gradient has the I/O dtype, those of the float32 gates and states too: the bf16
+ * path forms gradients from bf16 operands, and a last rounding (2^-9 in the mean) is no
+ * more than one of those. A state's gradient that crosses the parts of a split sequence
+ * rounds once per part.
  * H must be a multiple of Hk; dq and dk add up over the value heads of a key head.
  *
  * log_alpha <= 0. log_alpha = -inf starts a new sequence at that token (the state
@@ -341,7 +344,17 @@ GRADLEV_API gradlev_status gradlev_mlp2_recon(int B, int H, int T, int d_x, int 
  * A state that a call starts from is not used where the first token is a reset and may
  * hold anything there (a slot of an earlier request, fresh memory). Everything else must
  * be finite, padding and the tokens before a reset too: the chunks multiply what a gate
- * masks by zero. */
+ * masks by zero.
+ *
+ * Accuracy, in the 2-norm over a call's tensor: float32 outputs are 1e-6 off (operands are
+ * split into two tf32 each), dlog_alpha 1e-5 where keys are alike. bf16 outputs are 1.7e-3
+ * off by their own rounding; the tensor-core kernels (d_k 24 to 128 and d_v up to 256)
+ * round operands to bf16 as well and are 2.5 to 3.3e-3 off, up to 6e-3 where keys are alike
+ * (mean cosine 0.99) and beta is near 2; ST is 4e-6 off, up to 3e-5 there. Calls with
+ * gradients (ckpt, or gradlev_delta_bwd) take those kernels from B*H*T > 1024 gates on
+ * (8192 below d_k 64) and the float32 ones below, and a forward that is asked for ST carries
+ * its state in more bits: y may differ in its last bits between these. The same call on the
+ * same inputs gives the same bits. */
 
 /* Whether the shape is supported by gradlev_delta_fwd / _bwd: GRADLEV_OK, or
  * GRADLEV_ERR_INVALID_ARG / GRADLEV_ERR_UNSUPPORTED without touching the GPU.
@@ -399,6 +412,9 @@ GRADLEV_API gradlev_status gradlev_delta_bwd(int B, int H, int Hk, int T, int d_
  *       (-1: padding), or is also the slot of an earlier batch row, has no state: its
  *       y is zero and no state is written for it. Pool rows that no slot names keep
  *       their values.
+ *   The pool holds the states after all T tokens: a caller that may take some of them back
+ *   (drafted tokens being checked) copies the states first. gradlev_delta_fwd takes no
+ *   slots: a prompt's ST goes into the pool by a copy, or is a pool row itself (B = 1).
  *   Constraints: d_k a multiple of 4 up to 256, any d_v >= 1, H % Hk == 0,
  *   B*H*T < 2^31, B*H*d_v < 2^30 (GRADLEV_ERR_UNSUPPORTED). Alignment, else GRADLEV_ERR_INVALID_ARG: q and k to 4
  *   elements, v and y to one element, S to 16 bytes. One launch; no workspace. */
@@ -414,7 +430,11 @@ GRADLEV_API gradlev_status gradlev_delta_step(int B, int H, int Hk, int T, int d
  * (GRADLEV_NORM_L2) or its mean over d (GRADLEV_NORM_RMS), u = w r x, and for
  * i < rot / 2 with the angle th = pos[b][t] * inv_freq[i]:
  *   y_i = u_i cos th - u_{i + rot/2} sin th,  y_{i + rot/2} = u_{i + rot/2} cos th + u_i sin th,
- * and y_i = u_i for i >= rot. Angles are formed in double precision.
+ * and y_i = u_i for i >= rot. Angles keep their precision at far positions: the fraction of
+ * a turn is formed modulo 2^64 from inv_freq / 2 pi in 64 bits, and enters sine and cosine
+ * as a float32 fraction of a half turn (2^-24 of it off). ss is a float32 sum: rows whose
+ * squares leave float32's range (elements above 1e19, or below 1e-19 with eps = 0) are not
+ * normalised.
  *   q, k: [B, T, H*, d] by strides in elements {b, t, head}, the columns contiguous, so
  *     that a packed projection needs no copy. Strides are multiples of 16 bytes and not
  *     negative, bases 16-byte aligned, else GRADLEV_ERR_INVALID_ARG.

@@ -708,8 +708,8 @@ def gradlev_delta_step(q, k, v, beta, log_alpha, S, *, slots=None, scale=None, y
                        stream=None):
     """The T tokens of q, k, v in order on the states S [pool,H,d_v,d_k] float32, updated in
     place. slots [B] int32 picks each batch row's state (None: row b); a row without a state
-    of its own (slot outside the pool, or named by an earlier row) answers with zeros.
-    Returns y [B,H,T,d_v]."""
+    of its own (slot outside the pool, or named by an earlier row) answers with zeros. S ends
+    as the states after all T tokens. Returns y [B,H,T,d_v]."""
     if stream is not None:
         return _on_stream(gradlev_delta_step, stream, q, k, v, beta, log_alpha, S, slots=slots,
                           scale=scale, y=y)

@@ -50,7 +50,7 @@ struct Dims {
   size_t BH() const { return (size_t)B * H; }
 };
 
-// ---- CUDA-core kernels: float32 throughout, chunks of 32 tokens
+// ---- float32 kernels (products of split tf32 operands), chunks of 32 tokens
 namespace ffma {
 
 constexpr int C = 32;

@@ -30,14 +30,14 @@ Dims dims(int B, int H, int Hk, int T, int dk, int dv, gradlev_dtype dt) {
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // The tensor-core kernels round their operands to bf16, the float32 kernels nothing but the
-// outputs. A gate's gradient is one dot product of two rounded rows: 4 to 4.8e-3 off over many
-// gates (in the 2-norm; the float32 kernels 1.7e-3), but any single one that happens to be small
-// may be much further off, so that calls of few gates, or of heads so narrow that the chunk's
-// triangular systems amplify, passed 5e-3 (6e-3 at 300 gates; 7.6e-3 at d_k 8). Calls with
-// gradients take the tensor cores from there on: kernels of forward and gradients at 1024 gates
-// of d_k 128 31 against 62 us (H16 T64) and 83 against 213 us (H1 T1024); a call at 6888 gates
-// of d_k 48 83 against 93 us (H14 T492). Without gradients only the narrowest heads leave them
-// (tc::shape_ok).
+// outputs. A gate's gradient is one dot product of two such rows: 2.5 to 3.3e-3 off over many
+// gates (in the 2-norm; up to 5e-3 where keys are alike and beta is near 2; the float32 kernels
+// 1.7e-3), but any single one that happens to be small may be much further off (one token 3.3e-2,
+// two 9.5e-3, 600 gates of d_k 24 5.5e-3). Calls with gradients take the tensor cores where there
+// are gates enough, and where they are no slower: kernels of forward and gradients at 1024 gates of
+// d_k 128 37 against 62 us (H16 T64) and 138 against 215 us (H1 T1024); at 8190 gates of d_k 48 95
+// against 96 us (H14 T585), at 8000 of d_k 24 55 against 45 us. Without gradients only the
+// narrowest heads leave them (tc::shape_ok).
 bool use_tc(const Dims& d, bool gradients) {
   if (!tc::shape_ok(d)) return false;
   return !gradients || d.BH() * d.T > (d.dk >= 64 ? 1024 : 8192);

@@ -1,10 +1,12 @@
-// The gated delta rule on CUDA cores (float32 arithmetic): every shape and dtype the
-// tensor-core kernels do not take. The formulas are in delta.h.
+// The gated delta rule in float32: every shape and dtype that the tcgen05 kernels do not take.
+// The formulas are in delta.h.
 //
 // Four kernels. The chunk-local part (Z, P) and the gradients of q, k and the gates
 // need no order among the chunks and run one CTA per chunk; only the two state
-// recurrences walk the chunks in order. All products are warp tiles of split tf32 operands
-// (tf32.cuh), 1 to 2e-6 off: float32 FMAs waited for shared memory. The rows of S (and of dS) evolve
+// recurrences walk the chunks in order. All products are warp tiles (mma.sync) of operands split
+// into two tf32 each (tf32.cuh), 2^-21 off where a float32 FMA rounds by 2^-24: outputs are 1e-6
+// off, 3e-7 with FMAs, which waited for shared memory and took half as long again. Sums, states and
+// the chunk's triangular systems are float32. The rows of S (and of dS) evolve
 // independently given K, so a walk is cut into slices of kRows rows, one CTA each.
 //
 // Measured (B4 H8 T2048 d 64): Z and P 35 us, walks 145 and 143 us (239 and 219 us with FMAs),

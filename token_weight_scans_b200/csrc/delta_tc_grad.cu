@@ -17,12 +17,13 @@
 // D, E, X and Yn are two bf16 each: their terms cancel in all of these sums where keys are alike.
 // With one bf16 in their place dq and dk are 1 %, dlog_alpha 4 to 90 % off there.
 //
-// Measured: 295 us for B8 H16 T4096 d 128 (2816 bytes per token: 5.0 TB/s), 440 us for B1 H16
-// T32768 d_v 256 (4608 bytes: 5.5 TB/s), 293 us where four heads share a key head. 43 % of the
-// issue slots, 32 % of the tensor pipe (M = 64 products run at half its rate). Shared memory
-// holds two CTAs, which leaves next to no L1, so that a spilled register costs a trip to L2:
-// 260 bytes of spills per thread made 378 us of it. Hence the pieces of 8 columns, the sums that
-// begin late, and float32 pairs (half the FMAs).
+// Measured: 389 us for B8 H16 T4096 d 128 (3352 bytes per token: 4.5 TB/s), 587 us for B1 H16
+// T32768 d_v 256 (5632 bytes: 5.0 TB/s), 398 us where four heads share a key head. 42 % of the
+// tensor pipe (M = 64 products run at half its rate; the remainders doubled their number), 39 % of
+// the issue slots. Shared memory holds two CTAs, which leaves next to no L1, so that a spilled
+// register costs a trip to L2: 300 bytes of spills per thread cost 20 us. Hence X and Yn one
+// after the other in pieces, the sums that begin late, and float32 pairs (half the FMAs). The remainders of D and E
+// leave no room for X and Yn beside them, so the next D and E are loaded when those are done with.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -6,8 +6,8 @@
 // forward substitution (a lane per column, in registers), then twice
 //   [[X1, 0], [-X2 N21 X1, X2]]
 // which is as stable as substitution and needs only two products per level (warp-wide tf32
-// products of split operands: 247 -> 222 us for B8 H16 T4096 against float32 FMAs, whose
-// shared-memory reads held the kernel up; tiles this small leave tcgen05.mma idle).
+// products of split operands: float32 FMAs took 25 us more of a B8 H16 T4096, their shared-memory
+// reads held the kernel up; tiles this small leave tcgen05.mma idle).
 //
 // Kw = T0^T diag(beta w) K, Pv = P diag(beta) T0 and Wq = scale diag(G) Q - Pv diag(G) K then go
 // through the tensor core again. Their terms cancel where keys are alike, so T0, P and Pv diag(G)
@@ -17,12 +17,12 @@
 // beta = 0 would leave T0's column zero where E's row needs it: beta is taken at least 2^-60 in
 // size here (bt), which puts T0, Pv and Kw off by no more than that.
 //
-// Measured (B8 H16 T4096 d 128, 8192 chunks): 185 us with the backward's matrices, 1408 bytes per
-// token or 4.0 TB/s; 190 us with the remainders in their place (B1 H16 T32768). What bounds it is
-// the chain of short steps through a chunk at 24 warps per SM: 46 % of the issue slots, 44 % of
-// the shared-memory pipe, 26 % of the tensor pipe, 30 % of the DRAM. Without the triangular
-// inverse's products it would take 30 us less. Registers decide: products unrolled over their
-// terms spill and take 40 us more.
+// Measured (B8 H16 T4096 d 128, 8192 chunks): 278 us with the backward's matrices, 1590 bytes per
+// token or 3.0 TB/s; 300 us with the remainder of Kw in place of those (B1 H16 T32768). What bounds it
+// is the chain of short steps through a chunk at 24 warps per SM: 43 % of the issue slots, a third
+// of the shared-memory pipe, 23 % of the tensor pipe, 25 % of the DRAM. Registers decide: products
+// unrolled over their terms spill. (W = -T0 diag(G) K and P diag(beta) for an unfolded form, in one
+// bf16 each, took 185 us.)
 //
 // Waits: the in-flight TMA stores only read shared memory, so the CTA waits for that read
 // and not for their completion; the end of the kernel, which the walk waits for, orders them.

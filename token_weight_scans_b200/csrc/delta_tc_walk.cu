@@ -27,10 +27,12 @@
 // become rows, and TMA stores. D^T and E^T stay as they are, a chunk's tokens contiguous, in two
 // bf16 each.
 //
-// Measured (B8 H16 T4096 d 128, 128 CTAs of 64 chunks): forward 190 us, backward 180 us, of
-// 2304 and 2176 bytes per token: 6.3 TB/s, the measured copy bandwidth (6.47). Where HBM does
-// not bound it, a chunk takes 2.3 us (forward), 2.9 us with SPLIT: the chain, two products and
-// two passes of the state or D through registers.
+// Measured (B8 H16 T4096 d 128, 128 CTAs of 64 chunks): forward 234 us, backward 222 us, of
+// 2696 and 2572 bytes per token: 6.1 TB/s, near the measured copy bandwidth (6.47). Where HBM does
+// not bound it, a chunk takes 1.6 us (forward without outputs), 2.5 us with SPLIT: the chain, two
+// products and two passes of the state or R through registers. S, D and E go through shared memory:
+// stored from registers, 16 bytes per row and instruction, the walks of d_v 256 took 502 and 443 us
+// in place of 372 and 339 (B1 H16 T32768).
 //
 // Each chunk's tiles come in three groups with a two-deep ring of their own, since they are
 // done with at different times: V (dY) with Pv, K (Kw) with Wq, Kw (K). T0, needed last, has one
