@@ -82,6 +82,7 @@ cudaError_t fwd_run(const Dims& d, const void* q, const void* k, const void* v, 
       a.sv = tc::saved_at(saved, d);
       a.m.Kw = a.sv.Kw;
       a.m.Wq = a.sv.Wq;
+      a.m.Wq2 = a.sv.Wq2;
       a.m.Pv = a.sv.Pv;
       a.m.gates = a.sv.gates;
     }
@@ -186,6 +187,7 @@ gradlev_status gradlev_delta_bwd(int B, int H, int Hk, int T, int d_k, int d_v, 
     a.sv = delta::tc::saved_at(saved, d);
     a.m.Kw = a.sv.Kw;
     a.m.Wq = a.sv.Wq;
+    a.m.Wq2 = a.sv.Wq2;
     a.m.Pv = a.sv.Pv;
     a.m.gates = a.sv.gates;
     a.dy = dy;

@@ -67,11 +67,12 @@ using bf16 = __nv_bfloat16;
 // and E_j is that of beta E divided by bt.
 //
 // Chunk-local matrices that the walks read, all bf16 with N*64 rows per (b, h):
-//   Kw, Wq [64][128]; Kwlo, the remainder of Kw, for a forward whose last state is asked for;
-//   Pv [64][64 | 64], its remainder behind it (written for the backward alone);
-//   T0 [64][64 | 64] likewise, for the D that the backward needs.
+//   Kw, Wq [64][128]; the remainders Kw2 for the forward, Wq2 for the backward; Kw3, what Kw2
+//   leaves, for a forward whose last state is asked for;
+//   Pv [64][64 | 64], its remainder behind it; T0 likewise, for the D that the backward needs.
 struct Mats {
-  bf16 *Kw = nullptr, *Kwlo = nullptr, *Wq = nullptr, *Pv = nullptr, *T0 = nullptr;
+  bf16 *Kw = nullptr, *Kw2 = nullptr, *Kw3 = nullptr, *Wq = nullptr, *Wq2 = nullptr;
+  bf16 *Pv = nullptr, *T0 = nullptr;
   float* gates = nullptr;   // [B*H][N] GateBlock
 };
 
@@ -95,9 +96,9 @@ struct GateBlock {
 
 // What the forward keeps for the backward: chunk-start states S [B*H][N][dvp][128], D^T
 // [B*H][N][2][dvp][64] (bf16 and remainder, the tokens of a chunk contiguous, as the walk has
-// them), Kw, Wq, Pv and gates.
+// them), Kw, Wq, Wq2, Pv and gates.
 struct Saved {
-  bf16 *S = nullptr, *D = nullptr, *Kw = nullptr, *Wq = nullptr, *Pv = nullptr;
+  bf16 *S = nullptr, *D = nullptr, *Kw = nullptr, *Wq = nullptr, *Wq2 = nullptr, *Pv = nullptr;
   float *gates = nullptr, *M = nullptr;  // M: the segments' maps, with segments
 };
 
@@ -162,9 +163,10 @@ cudaError_t launch_after(const Dims& d, void (*kernel)(P...), unsigned grid, uns
   return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
 }
 
-cudaError_t launch_prep(const Args& a, bool split, cudaStream_t st);
+// last_state: one that is asked for, with a bf16 more for its operands (delta_tc_walk.cu)
+cudaError_t launch_prep(const Args& a, bool last_state, cudaStream_t st);
 // after: a kernel of the same call is before it
-cudaError_t launch_walk(const Args& a, bool backward, bool split, bool sum, bool after,
+cudaError_t launch_walk(const Args& a, bool backward, bool last_state, bool sum, bool after,
                         cudaStream_t st);
 cudaError_t launch_combine(const Args& a, bool backward, cudaStream_t st);
 cudaError_t launch_grad(const Args& a, cudaStream_t st);

@@ -1,5 +1,5 @@
 // Tensor-core gated delta rule: the chunk-local matrices (delta_tc.h, struct Mats) of one
-// (chunk, value head) after the other, three persistent CTAs per SM.
+// (chunk, value head) after the other, three persistent CTAs per SM (two with THREE).
 //
 // K K^T and Q K^T go through the tensor core; the unit lower triangular inverse
 // T0 = (I + A diag(beta))^-1 is formed in float32 by halves: 16 x 16 diagonal blocks by
@@ -52,8 +52,10 @@ constexpr float kTiny = 0x1p-60f;
 constexpr int kLoader = 128;  // the thread that loads K and Q, and stores P and PT
 
 // Tiles live where something dead was. Over N: diag(beta w) T0, then Pv diag(G), at the end Kw. Over
-// X: T0, then Pv, at the end Wq, or with SPLIT the remainder of Kw. Over Q: P diag(beta) (all these
-// two bf16 each); then Q again, from L2, and with SPLIT Wq over it, row by row as it is formed.
+// X: T0, then Pv, at the end the remainder of Kw. Over Q: P diag(beta) (all these two bf16 each);
+// then Q again, from L2, and Wq over it, row by row as it is formed, with BACK its remainder over K.
+// THREE has a place for the third part of diag(beta w) T0, and then of Kw.
+template <bool THREE>
 struct PrepSmem {
   uint8_t K[2 * TILE];         // k-blocks: 64 token rows x 128 B
   uint8_t Q[2 * TILE];
@@ -65,6 +67,7 @@ struct PrepSmem {
     float X[C * LD];           // T0
     uint8_t B[2][TILE];
   };
+  alignas(1024) uint8_t Z[THREE ? 2 * TILE : 16];
   // per token: M_ij = ra_i ca_j with both factors within e^40 (fac: all decays of the chunk within
   // e^80, and the factors taken from the middle of that range, so that ca kTiny stays a normal
   // number: a factor taken from a token, e^-80 kTiny, would underflow and take dbeta with it where
@@ -77,8 +80,9 @@ struct PrepSmem {
   uint32_t tmem_base;
   int abort;
 };
-constexpr size_t kSmem = sizeof(PrepSmem) + 1024;
-static_assert(3 * (kSmem + 1024) <= 228 * 1024, "three CTAs per SM");
+template <bool THREE> constexpr size_t smem_bytes() { return sizeof(PrepSmem<THREE>) + 1024; }
+static_assert(3 * (smem_bytes<false>() + 1024) <= 228 * 1024, "three CTAs per SM");
+static_assert(2 * (smem_bytes<true>() + 1024) <= 228 * 1024, "two CTAs per SM");
 
 enum : uint32_t { W_PREP_LOAD = 0x801, W_PREP_Q, W_PREP_MMA, W_PREP_DRAIN };
 
@@ -113,15 +117,17 @@ __device__ __forceinline__ void store16x8(float* at, const float (&v)[4], float 
 
 }  // namespace
 
-// SPLIT: the remainder of Kw; BACK: that of Pv, and T0, for the backward.
-template <bool SPLIT, bool BACK>
-__global__ void __launch_bounds__(kThreads, 3)
+// THREE: Kw in three parts; BACK: T0 and the remainder of Wq, for the backward.
+template <bool THREE, bool BACK>
+__global__ void __launch_bounds__(kThreads, THREE ? 2 : 3)
     prep_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ,
-                const __grid_constant__ CUtensorMap tmKw, const __grid_constant__ CUtensorMap tmKwlo,
-                const __grid_constant__ CUtensorMap tmWq, const __grid_constant__ CUtensorMap tmPv,
+                const __grid_constant__ CUtensorMap tmKw, const __grid_constant__ CUtensorMap tmKw2,
+                const __grid_constant__ CUtensorMap tmKw3, const __grid_constant__ CUtensorMap tmWq,
+                const __grid_constant__ CUtensorMap tmWq2, const __grid_constant__ CUtensorMap tmPv,
                 PrepParams p) {
   extern __shared__ uint8_t smem_raw[];
-  PrepSmem& sm = *reinterpret_cast<PrepSmem*>(
+  using Smem = PrepSmem<THREE>;
+  Smem& sm = *reinterpret_cast<Smem*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int N = chunks(p.d.T);
@@ -160,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   tc_fence_after();
   const uint32_t tb = sm.tmem_base;
   const uint32_t sK = smem_u32(sm.K), sQ = smem_u32(sm.Q), sA = smem_u32(sm.A[0]), sB = smem_u32(sm.B[0]);
+  const uint32_t sZ = smem_u32(sm.Z);
   uint32_t phase = 0, full = 0, loads = 0, again = 0;  // loads after the first, and of Q again (loading thread)
   for (unsigned id = blockIdx.x; id < total; id += gridDim.x, full ^= 1) {
   const int bh = id / N, n = id - bh * N, t0 = n * C;
@@ -217,8 +224,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   }
   mbar_wait(&sm.mma, phase, wc, W_PREP_MMA);
   phase ^= 1;
-  if (tid == kLoader) tma_store_wait_read();  // the last chunk's results, whose places come next
-  __syncthreads();                            // the gates are there
+  __syncthreads();  // the gates are there
   tc_fence_after();
   // Lane l < 16 of quadrant q holds row i = 16 q + l of K K^T, lane l + 16 that of Q K^T;
   // warps q and q + 4 take half of the columns each.
@@ -364,8 +370,18 @@ __global__ void __launch_bounds__(kThreads, 3)
       for (int e = 0; e < 8; ++e) x[e] *= wr;
       const uint32_t off = sw128_off(r, c >> 3);
       const uint4 h = pack8(x);
+      const uint4 l = rest8(x, h);
       put(sA + off, h);
-      put(sA + TILE + off, rest8(x, h));
+      put(sA + TILE + off, l);
+      if (THREE) {
+        const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[2 * e] -= bf16_lo(hw[e]);
+          x[2 * e + 1] -= bf16_hi(hw[e]);
+        }
+        put(sZ + off, rest8(x, l));
+      }
     }
     __syncthreads();  // X is read, and T0 goes over it
 #pragma unroll
@@ -398,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     tc_fence_after();
     product(tb, sA, true, sK, 128, true);
     product(tb, sA + TILE, true, sK, 128, false);
+    if (THREE) product(tb, sZ, true, sK, 128, false);
     product(tU, sQ, false, sB, 64, true);
     product(tU, sQ, false, sB + TILE, 64, false);
     product(tU, sQ + TILE, false, sB, 64, false);
@@ -437,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   __syncthreads();
   if (tid == kLoader) {
     tma_store_3d(&tmPv, sm.B[0], 0, t0, bh);
-    if (BACK) tma_store_3d(&tmPv, sm.B[1], 64, t0, bh);
+    tma_store_3d(&tmPv, sm.B[1], 64, t0, bh);
     tma_store_commit();
   }
   if (tid == 0) {  // - Pv diag(G) K
@@ -453,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   if (tid == kLoader) {
     if (more) {
       mbar_arrive_expect_tx(&sm.full, 4 * TILE);
-      load(id + gridDim.x, false, &sm.full);
+      if (!BACK) load(id + gridDim.x, false, &sm.full);
       ++loads;
     }
     tma_store_wait_read();  // Pv
@@ -468,12 +485,12 @@ __global__ void __launch_bounds__(kThreads, 3)
     float v[32];
     tmem_ld32(tb + lo + 64 * hh + 32 * g, v);
     tmem_ld_wait();
-    const uint32_t dst = (!isP ? sA : SPLIT ? sQ : sB) + hh * TILE;
+    const uint32_t dst = (isP ? sQ : sA) + hh * TILE;
 #pragma unroll
     for (int cc = 0; cc < 4; ++cc) {
       const uint32_t off = sw128_off(i, 4 * g + cc);
       if (isP) {
-        const uint4 u = ld_shared_v4(sQ + hh * TILE + off);
+        const uint4 u = ld_shared_v4(dst + off);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -481,14 +498,19 @@ __global__ void __launch_bounds__(kThreads, 3)
           v[8 * cc + 2 * e + 1] = fmaf(sG, bf16_hi(w[e]), v[8 * cc + 2 * e + 1]);
         }
       }
-      uint32_t hi[4], low[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        hi[e] = pack_bf16(v[8 * cc + 2 * e], v[8 * cc + 2 * e + 1]);
-        if (SPLIT) low[e] = pack_lo(v[8 * cc + 2 * e], v[8 * cc + 2 * e + 1], hi[e]);
+      for (int k = 0; k < (THREE ? 3 : 2); ++k) {  // the parts of Kw; of Wq one, or two
+        uint32_t part[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float &a = v[8 * cc + 2 * e], &b = v[8 * cc + 2 * e + 1];
+          part[e] = pack_bf16(a, b);
+          a -= bf16_lo(part[e]);
+          b -= bf16_hi(part[e]);
+        }
+        const uint32_t at = k == 0 ? dst : (k == 2 ? sZ : isP ? sK : sB) + hh * TILE;
+        if (k == 0 || !isP || (BACK && k == 1)) st_shared_v4(at + off, part[0], part[1], part[2], part[3]);
       }
-      st_shared_v4(dst + off, hi[0], hi[1], hi[2], hi[3]);
-      if (SPLIT && !isP) st_shared_v4(sB + hh * TILE + off, low[0], low[1], low[2], low[3]);
     }
     __syncwarp();
   }
@@ -497,12 +519,15 @@ __global__ void __launch_bounds__(kThreads, 3)
   const bool stop = __syncthreads_or(*reinterpret_cast<volatile int*>(&sm.abort));
   if (tid == kLoader) {
     for (int kb = 0; kb < 2; ++kb) {
+      tma_store_3d(&tmWq, sm.Q + kb * TILE, 64 * kb, t0, bh);
       tma_store_3d(&tmKw, sm.A[kb], 64 * kb, t0, bh);
-      if (SPLIT) tma_store_3d(&tmKwlo, sm.B[kb], 64 * kb, t0, bh);
-      tma_store_3d(&tmWq, SPLIT ? sm.Q + kb * TILE : sm.B[kb], 64 * kb, t0, bh);
+      tma_store_3d(&tmKw2, sm.B[kb], 64 * kb, t0, bh);
+      if (BACK) tma_store_3d(&tmWq2, sm.K + kb * TILE, 64 * kb, t0, bh);
+      if (THREE) tma_store_3d(&tmKw3, sm.Z + kb * TILE, 64 * kb, t0, bh);
     }
     tma_store_commit();
-    if (SPLIT) tma_store_wait_read();  // Wq
+    tma_store_wait_read();  // the places are written again from here on
+    if (more && BACK) load(id + gridDim.x, false, &sm.full);
     if (more) load(id + gridDim.x, true, &sm.full);
   }
   __syncwarp();
@@ -520,40 +545,40 @@ __global__ void __launch_bounds__(kThreads, 3)
   }
 }
 
-template <bool SPLIT, bool BACK>
-static cudaError_t launch(const CUtensorMap (&m)[6], const PrepParams& p, unsigned grid, cudaStream_t st) {
+template <bool THREE, bool BACK>
+static cudaError_t launch(const CUtensorMap (&m)[8], const PrepParams& p, unsigned grid, cudaStream_t st) {
   static std::atomic<uint64_t> set{0};  // devices whose opt-in is done
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (!bit || !(set.load() & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        prep_kernel<SPLIT, BACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    const cudaError_t e =
+        cudaFuncSetAttribute(prep_kernel<THREE, BACK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)smem_bytes<THREE>());
     if (e != cudaSuccess) return e;
     set.fetch_or(bit);
   }
-  const unsigned most = 148 * 3;
-  prep_kernel<SPLIT, BACK><<<grid < most ? grid : most, kThreads, kSmem, st>>>(m[0], m[1], m[2], m[3],
-                                                                               m[4], m[5], p);
+  const unsigned most = 148 * (THREE ? 2 : 3);
+  prep_kernel<THREE, BACK><<<grid < most ? grid : most, kThreads, smem_bytes<THREE>(), st>>>(
+      m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], p);
   count_launch();
   return cudaGetLastError();
 }
 
-cudaError_t launch_prep(const Args& a, bool split, cudaStream_t st) {
+cudaError_t launch_prep(const Args& a, bool last_state, cudaStream_t st) {
   const Dims& d = a.d;
   const uint64_t N = chunks(d.T), kh = (uint64_t)d.B * d.Hk, bh = d.BH();
   const bool back = a.m.T0 != nullptr;
-  CUtensorMap m[6];
+  CUtensorMap m[8];
   using gradlev::tc::make_map_bf16_3d;
+  auto mat = [&](CUtensorMap* t, const bf16* x) { return make_map_bf16_3d(t, x, 128, N * C, bh, C); };
   if (!make_map_bf16_3d(&m[0], a.k, d.dk, d.T, kh, C) || !make_map_bf16_3d(&m[1], a.q, d.dk, d.T, kh, C) ||
-      !make_map_bf16_3d(&m[2], a.m.Kw, 128, N * C, bh, C) ||
-      !make_map_bf16_3d(&m[3], a.m.Kwlo, 128, N * C, bh, C) ||
-      !make_map_bf16_3d(&m[4], a.m.Wq, 128, N * C, bh, C) ||
-      !make_map_bf16_3d(&m[5], a.m.Pv, 128, N * C, bh, C))
+      !mat(&m[2], a.m.Kw) || !mat(&m[3], a.m.Kw2) || !mat(&m[4], a.m.Kw3) || !mat(&m[5], a.m.Wq) ||
+      !mat(&m[6], back ? a.m.Wq2 : a.m.Wq) || !mat(&m[7], a.m.Pv))
     return cudaErrorInvalidValue;
   const PrepParams p{d, a.beta, a.log_alpha, a.scale, a.status, a.timeout_ns, a.m};
   const unsigned grid = (unsigned)(N * bh);
-  if (split) return back ? launch<true, true>(m, p, grid, st) : launch<true, false>(m, p, grid, st);
+  if (last_state) return back ? launch<true, true>(m, p, grid, st) : launch<true, false>(m, p, grid, st);
   return back ? launch<false, true>(m, p, grid, st) : launch<false, false>(m, p, grid, st);
 }
 

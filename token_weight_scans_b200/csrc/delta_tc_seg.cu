@@ -173,19 +173,19 @@ cudaError_t launch_combine(const Args& a, bool backward, cudaStream_t st) {
 }
 
 // ---------------------------------------------------------------- the kernels in order
-static cudaError_t walk(const Args& a, bool backward, bool split, cudaStream_t st) {
+static cudaError_t walk(const Args& a, bool backward, bool last_state, cudaStream_t st) {
   if (a.seg.nseg > 1) {
-    cudaError_t e = launch_walk(a, backward, split, true, !backward, st);
+    cudaError_t e = launch_walk(a, backward, last_state, true, !backward, st);
     if (e == cudaSuccess) e = launch_combine(a, backward, st);
     if (e != cudaSuccess) return e;
   }
-  return launch_walk(a, backward, split, false, !backward || a.seg.nseg > 1, st);
+  return launch_walk(a, backward, last_state, false, !backward || a.seg.nseg > 1, st);
 }
 
 cudaError_t run_fwd(const Args& a, cudaStream_t st) {
-  const bool split = a.ST != nullptr;
-  const cudaError_t e = launch_prep(a, split, st);
-  return e != cudaSuccess ? e : walk(a, false, split, st);
+  const bool last_state = a.ST != nullptr;
+  const cudaError_t e = launch_prep(a, last_state, st);
+  return e != cudaSuccess ? e : walk(a, false, last_state, st);
 }
 
 cudaError_t run_bwd(const Args& a, cudaStream_t st) {
@@ -205,7 +205,7 @@ static size_t gate_bytes(const Dims& d) {
 size_t token_rows_bytes(const Dims& d) {
   return up256(d.BH() * chunks(d.T) * 2 * dvp(d) * C * sizeof(bf16));
 }
-// one of Kw, Kwlo, Wq, Pv, T0
+// one of struct Mats
 static size_t mat_bytes(const Dims& d) { return up256(d.BH() * chunks(d.T) * C * 128 * sizeof(bf16)); }
 
 Saved saved_at(char* base, const Dims& d) {
@@ -214,7 +214,7 @@ Saved saved_at(char* base, const Dims& d) {
   Saved s;
   s.S = take(at, rows * dvp(d) * 128);
   s.D = take(at, rows * 2 * dvp(d) * C);
-  for (bf16** m : {&s.Kw, &s.Wq, &s.Pv}) *m = take(at, rows * C * 128);
+  for (bf16** m : {&s.Kw, &s.Wq, &s.Wq2, &s.Pv}) *m = take(at, rows * C * 128);
   s.gates = reinterpret_cast<float*>(at);
   s.M = reinterpret_cast<float*>(at + gate_bytes(d));
   return s;
@@ -223,7 +223,7 @@ Saved saved_at(char* base, const Dims& d) {
 size_t saved_bytes(const Dims& d) {
   const size_t rows = d.BH() * chunks(d.T);
   const int nseg = seg_plan(d).nseg;
-  return up256(rows * dvp(d) * 256) + token_rows_bytes(d) + 3 * mat_bytes(d) + gate_bytes(d) +
+  return up256(rows * dvp(d) * 256) + token_rows_bytes(d) + 4 * mat_bytes(d) + gate_bytes(d) +
          (nseg > 1 ? d.BH() * nseg * 128 * 128 * sizeof(float) : 0);
 }
 
@@ -232,7 +232,8 @@ Mats mats_at(char* base, const Dims& d, bool saved) {
   const size_t n = d.BH() * chunks(d.T) * C * 128;
   char* at = base;
   Mats m;
-  m.Kwlo = take(at, n);
+  m.Kw2 = take(at, n);
+  m.Kw3 = take(at, n);
   if (saved) {
     m.T0 = take(at, n);
     return m;
@@ -243,7 +244,7 @@ Mats mats_at(char* base, const Dims& d, bool saved) {
 }
 
 size_t fwd_scratch_bytes(const Dims& d) {  // the segments' buffers come last
-  return 4 * mat_bytes(d) + gate_bytes(d) + seg_bytes(d, true);
+  return 5 * mat_bytes(d) + gate_bytes(d) + seg_bytes(d, true);
 }
 
 size_t bwd_scratch_bytes(const Dims& d) {  // E, dS, the segments' buffers

@@ -11,18 +11,19 @@
 //
 // The chain through a chunk is: S to bf16 (TMEM -> registers -> TMEM), the product with K (Kw),
 // its result to bf16, the product with Kw (K). All else runs beside it: V^T of the next chunk
-// (a product with the identity, into the accumulator that S K^T is added to) and the outputs'
-// products are issued into the gaps of the chain, and their results leave through an output
-// warpgroup. One product of N = 128 takes S through K and Wq together.
+// (a product with the identity) and the outputs' products are issued into the gaps of the chain,
+// and their results leave through an output warpgroup. One product of N = 128 takes S through K
+// and Wq together; -G is applied to its result, so that K enters as it is.
 //
-// SPLIT (a forward whose last state is asked for): every operand of the state that is not
-// exact in bf16 comes as a sum of two bf16 (S, R, Kw), so that S carries 16 bits through the
-// chunks and the float32 state it ends with is good to 1e-5. K is left as it is, and -G is applied
-// to the product. Training needs no such state and takes single products, with K diag(-G) in bf16.
+// Every operand of the state that is not exact in bf16 comes as a sum of P bf16. Forward, P = 2:
+// S, R and Kw (and Pv in Y, T0 in D). The gradients and y are then off by their own rounding and by
+// that of what is multiplied once, Wq and the states that are kept: 2.0 to 2.4e-3, where one bf16
+// each makes 2.7 to 3.0e-3. P = 3 where the last state is asked for: it is float32, and 16 bits
+// would leave it 4e-6 off. Backward, P = 2 for S.
 //
 // Warp roles (16): 0 and 3 TMA producers, 1 MMA issuer (owns TMEM), 2 copies the gates in,
-// 4-11 two chain warpgroups (each half of the columns), which also leave S and E^T for
-// the kernels after, 12-15 scaling of K by -G, D^T, and Y (dV): 16-lane TMEM loads in the
+// 4-11 two chain warpgroups (each half of the columns), which also leave S, D^T and E^T for
+// the kernels after, 12-15 Y (dV): 16-lane TMEM loads in the
 // layout of 8 x 8 fragments, transposed on the way to shared memory (stmatrix) so that tokens
 // become rows, and TMA stores. D^T and E^T stay as they are, a chunk's tokens contiguous, in two
 // bf16 each.
@@ -34,9 +35,9 @@
 // stored from registers, 16 bytes per row and instruction, the walks of d_v 256 took 502 and 443 us
 // in place of 372 and 339 (B1 H16 T32768).
 //
-// Each chunk's tiles come in three groups with a two-deep ring of their own, since they are
-// done with at different times: V (dY) with Pv, K (Kw) with Wq, Kw (K). T0, needed last, has one
-// place.
+// Each chunk's tiles come in groups that are done with at different times: V (dY); K (Kw) with Wq;
+// Kw (K); Pv; T0. The first two have two places each; the others, for which a chunk's time is enough
+// to come, have one.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -59,14 +60,16 @@ constexpr int kThreads = 512;
 
 // TMEM columns
 constexpr uint32_t COL_S = 0;      // float32 state, 128
-constexpr uint32_t COL_SH = 128;   // bf16 state, 64
-constexpr uint32_t COL_DB = 192;   // bf16 R, 32 (for D)
-constexpr uint32_t COL_U = 224;    // bf16 operand of the update, 32: R (with 0 where beta = 0), -G F
-// Accumulators, two pairs: R^T, 64, then D^T in its place, and Y^T, 64 (backward: Pv^T dY and F).
-// SPLIT has one set: V^T, then D^T in its place; S K^T, which the chain scales and adds; Y^T
-constexpr uint32_t COL_D = 256;
-constexpr uint32_t COL_SL = 448;   // SPLIT: remainder of the state, 64; once the products with K
-constexpr uint32_t COL_UL = 448;   // have read it, that of R, 32
+constexpr uint32_t COL_SH = 128;   // bf16 state, 64 for each part
+// Over it, once the products with K have read it: the bf16 operand of the update, 32 for each part
+// (R with 0 where beta = 0, backward -G F), and behind it R in two parts, for D
+constexpr uint32_t COL_U = 128;
+// Accumulators. Forward: V^T, then D^T in its place (P = 2: two such), S K^T and Y^T. Backward: two
+// pairs of Pv^T dY and F.
+constexpr uint32_t COL_SK = 384, COL_Y = 448;
+constexpr uint32_t COL_P = 256;
+template <int P> constexpr uint32_t COL_DB = COL_U + 32 * P;
+template <int P> constexpr uint32_t COL_V = P == 2 ? 256 : 320;
 
 // A chunk's gates: the piece of GateBlock that the direction needs, as it lies there.
 template <bool BWD> struct GateSlot;
@@ -85,46 +88,43 @@ template <bool BWD>
 struct Bars {
   GateSlot<BWD> gates[GS];
   uint64_t full[3][NS], empty[3][NS];   // per group of tiles
-  uint64_t scaled[NS];
   uint64_t gfull[GS], gempty[GS];
-  uint64_t sready[2];                   // (SPLIT: in two halves of each warp's columns)
+  uint64_t sready[2];                   // in two halves of each warp's columns
   uint64_t sscaled, dfull, uready, sfull, done;
-  uint64_t tfull, tempty;               // T0
-  uint64_t yfull[2], yfree[2];          // per accumulator pair
+  uint64_t pfull, pempty, tfull, tempty;  // Pv; T0
+  uint64_t ddone, dfree[2];             // D^T
+  uint64_t yfull[2], yfree[2];          // per accumulator (pair)
   uint32_t tmem_base;
   int abort;
 };
-enum { VP = 0, KQ = 1, UP = 2 };
+enum { VD = 0, KQ = 1, UP = 2 };
 
-// The rings. VP: V (dY), Pv, backward also its remainder. KQ: per 64 columns of d_k the K (Kw)
-// tile and the Wq tile next to each other (128 rows of one operand). UP: Kw (K), SPLIT also the
-// remainder of Kw.
-template <bool BWD, bool SPLIT>
+// VD: V (dY). KQ: per 64 columns of d_k the K (Kw) tile and the Wq tile next to each other (128 rows
+// of one operand), backward also the remainder of Wq. UP: Kw in its parts (K).
+template <bool BWD, int P>
 struct Layout {
-  static constexpr int v = 0, p = 2 * TILE, pl = 3 * TILE;
   static constexpr int w = 0, q = TILE;
-  static constexpr int wq = 2 * TILE;    // from one k-block to the next
-  static constexpr int k = 0, kl = 2 * TILE;
-  static constexpr int vp_bytes = BWD ? 4 * TILE : 3 * TILE;
-  static constexpr int kq_bytes = 4 * TILE;
-  static constexpr int up_bytes = SPLIT ? 4 * TILE : 2 * TILE;
-  static constexpr int kq0 = NS * vp_bytes, up0 = kq0 + NS * kq_bytes;
-  static constexpr int t0 = up0 + NS * up_bytes;          // forward: T0 and its remainder
-  static constexpr int id = t0 + (BWD ? 0 : 2 * TILE);    // forward: the identity
+  static constexpr int wq = BWD ? 3 * TILE : 2 * TILE;  // from one k-block to the next
+  static constexpr int vd_bytes = 2 * TILE, kq_bytes = 2 * wq;
+  static constexpr int up_bytes = BWD ? 2 * TILE : 2 * P * TILE;
+  static constexpr int kq0 = NS * vd_bytes, up = kq0 + NS * kq_bytes;
+  // Pv, forward T0, with their remainders; forward the identity
+  static constexpr int pv = up + up_bytes, t0 = pv + 2 * TILE;
+  static constexpr int id = t0 + (BWD ? 0 : 2 * TILE);
   // S, and after it D^T (E^T), through shared memory and TMA: 4 KB for each warp of the chain
-  static constexpr bool staged = !SPLIT;
+  static constexpr bool staged = P == 2;
   static constexpr int stage_s = id + (BWD ? 0 : TILE), stage_o = stage_s + (staged ? 2 * BIG : 0);
   static constexpr int bars = stage_o + 2 * TILE;
   static constexpr size_t smem = bars + sizeof(Bars<BWD>) + 1024;
   static_assert(smem <= 227 * 1024, "over the shared memory of a CTA");
-  static constexpr int vp(int s) { return s * vp_bytes; }
+  static constexpr int vd(int s) { return s * vd_bytes; }
   static constexpr int kq(int s) { return kq0 + s * kq_bytes; }
-  static constexpr int up(int s) { return up0 + s * up_bytes; }
 };
 
 enum : uint32_t {
-  W_TMA = 0x901, W_TMA_DRAIN, W_FULL = 0x911, W_SCALED, W_SREADY, W_UREADY, W_YFREE, W_DONE,
-  W_GATE = 0x921, W_T0, W_C_SFULL = 0x931, W_C_DFULL, W_C_GATE, W_O_FULL = 0x941, W_O_GATE, W_O_Y,
+  W_TMA = 0x901, W_TMA_DRAIN, W_FULL = 0x911, W_SREADY, W_UREADY, W_YFREE, W_DFREE, W_DONE,
+  W_GATE = 0x921, W_PV, W_T0, W_C_SFULL = 0x931, W_C_DFULL, W_C_DDONE, W_C_GATE, W_O_GATE = 0x941, W_O_Y,
+  W_O_DDONE,
 };
 
 struct WalkParams {
@@ -150,12 +150,6 @@ struct WalkParams {
   float *loc, *M;        // [B*H][nseg][dvp][128], [B*H][nseg][128][128]
 };
 
-__device__ __forceinline__ void st_tmem32(uint32_t col, const uint32_t (&r)[32]) {
-  float v[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-  tmem_st32(col, v);
-}
 __device__ __forceinline__ void st_tmem16(uint32_t col, const uint32_t (&r)[16]) {
   float v[16];
 #pragma unroll
@@ -203,23 +197,6 @@ __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t nthreads, boo
   return r != 0;
 }
 
-// x *= factor[row] on a [64 tokens x 128] tile in place (its k-blocks `step` bytes apart), by
-// 128 threads; the loads go out together.
-__device__ __forceinline__ void scale_tile(uint32_t tile, uint32_t step, const float* factor, int t) {
-  uint4 v[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = ld_shared_v4(tile + (k >> 2) * step + (t + 128 * (k & 3)) * 16);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t in = (uint32_t)(t + 128 * (k & 3)) * 16;
-    const float f = factor[in >> 7];
-    st_shared_v4(tile + (k >> 2) * step + in, pack_bf16(f * bf16_lo(v[k].x), f * bf16_hi(v[k].x)),
-                 pack_bf16(f * bf16_lo(v[k].y), f * bf16_hi(v[k].y)),
-                 pack_bf16(f * bf16_lo(v[k].z), f * bf16_hi(v[k].z)),
-                 pack_bf16(f * bf16_lo(v[k].w), f * bf16_hi(v[k].w)));
-  }
-}
-
 // 64 float32 columns of 16 TMEM lanes as 8 x 8 fragments: registers 4 g .. 4 g + 3 hold, of
 // columns 8 g + 2 (lane % 4) and the one after, rows lane / 4 (first two) and lane / 4 + 8.
 __device__ __forceinline__ void tmem_ld_frag64(uint32_t taddr, float (&v)[32]) {
@@ -261,16 +238,17 @@ __device__ __forceinline__ void put_frag64(uint32_t tile, int row, const float (
 
 }  // namespace
 
-template <bool BWD, bool SPLIT>
+template <bool BWD, int P>
 __global__ void __launch_bounds__(kThreads, 1)
     walk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                const __grid_constant__ CUtensorMap tmKw, const __grid_constant__ CUtensorMap tmKwl,
-                const __grid_constant__ CUtensorMap tmWq, const __grid_constant__ CUtensorMap tmP,
-                const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmS,
-                const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmD,
-                WalkParams p) {
-  using L = Layout<BWD, SPLIT>;
-  constexpr int NY = SPLIT ? 1 : 2;   // accumulator pairs
+                const __grid_constant__ CUtensorMap tmKw, const __grid_constant__ CUtensorMap tmKw2,
+                const __grid_constant__ CUtensorMap tmKw3, const __grid_constant__ CUtensorMap tmWq,
+                const __grid_constant__ CUtensorMap tmWq2,
+                const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmT,
+                const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmY,
+                const __grid_constant__ CUtensorMap tmD, WalkParams p) {
+  using L = Layout<BWD, P>;
+  constexpr int NY = BWD ? 2 : 1, NV = P == 2 ? 2 : 1;  // places of Y (pairs); of V and D
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -284,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool ident = extra || slice == dvp(p.d) >> 7;  // carries the identity: the segment's map
   const int n0 = ident ? 0 : slice * 128;
   const bool carry = p.sum || ident;                 // the end state is all that is wanted
-  const bool outputs = !BWD && !carry;               // the forward's products for Y
-  const bool errors = outputs && p.D;                // and those for D
+  const bool outputs = !BWD && !carry && p.y;        // the forward's products for Y
+  const bool errors = !BWD && !carry && p.D;         // and those for D
   const size_t sg = (size_t)bh * p.nseg + seg;
   const int b = bh / p.d.H, h = bh - b * p.d.H;
   const int kh = b * p.d.Hk + h / (p.d.H / p.d.Hk);
@@ -301,11 +279,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sm.full[r][s], 1);
         mbar_init(&sm.empty[r][s], 1);
       }
-      mbar_init(&sm.scaled[s], 4);
     }
     for (int g = 0; g < GS; ++g) {
       mbar_init(&sm.gfull[g], 1);
-      mbar_init(&sm.gempty[g], 12);  // the chain's 8 warps, 4 that scale Q
+      mbar_init(&sm.gempty[g], BWD ? 12 : 8);  // the chain's 8 warps, backward the 4 of dV
     }
     mbar_init(&sm.sready[0], 8);
     mbar_init(&sm.sready[1], 8);
@@ -314,11 +291,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.uready, 8);
     mbar_init(&sm.sfull, 1);
     mbar_init(&sm.done, 1);
+    mbar_init(&sm.pfull, 1);
+    mbar_init(&sm.pempty, 1);
     mbar_init(&sm.tfull, 1);
     mbar_init(&sm.tempty, 1);
+    mbar_init(&sm.ddone, 1);
     for (int y = 0; y < 2; ++y) {
       mbar_init(&sm.yfull[y], 1);
-      mbar_init(&sm.yfree[y], !BWD && errors && !SPLIT ? 12 : 4);  // the chain takes D
+      mbar_init(&sm.yfree[y], 4);
+      mbar_init(&sm.dfree[y], 8);
     }
     fence_mbar_init();
   }
@@ -342,183 +323,174 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0 || warp == 3) {
     // ------------------------------------------------------------ TMA producers
-    // warp 0: V with Pv, and Kw (K); warp 3: K (Kw) with Wq
+    // warp 0: V (dY, with Pv), and Kw (K); warp 3: K (Kw) with Wq
     if (lane == 0) {
       int issued[3] = {0, 0, 0};
+      auto places = [](int r) { return r == UP ? 1 : NS; };
       auto open = [&](int r, int c, int bytes) -> bool {
-        if (!mbar_wait(&sm.empty[r][c % NS], ((c / NS) & 1) ^ 1, wc, W_TMA)) return false;
-        mbar_arrive_expect_tx(&sm.full[r][c % NS], bytes);
+        const int n = places(r);
+        if (!mbar_wait(&sm.empty[r][c % n], ((c / n) & 1) ^ 1, wc, W_TMA)) return false;
+        mbar_arrive_expect_tx(&sm.full[r][c % n], bytes);
         issued[r] = c + 1;
         return true;
       };
-      const bool pv = BWD ? !carry : outputs, wq = BWD || outputs;
+      const bool wq = BWD || outputs;
       for (int c = 0; c < NC; ++c) {
         const int s = c % NS, t0 = cg(c) * C;
         if (warp == 0) {
-          uint8_t* a = base + L::vp(s);
-          uint64_t* f = &sm.full[VP][s];
-          if (!open(VP, c, pv ? L::vp_bytes : 2 * TILE)) break;
+          uint8_t* a = base + L::vd(s);
+          uint64_t* f = &sm.full[VD][s];
+          if (!open(VD, c, L::vd_bytes)) break;
           const int tv = ident ? N * C : t0;  // past the last token: zeros
-          tma_load_3d(a + L::v, &tmV, f, n0, tv, bh);
-          tma_load_3d(a + L::v + TILE, &tmV, f, n0 + 64, tv, bh);
-          if (pv) tma_load_3d(a + L::p, &tmP, f, 0, t0, bh);
-          if (BWD && pv) tma_load_3d(a + L::pl, &tmP, f, 64, t0, bh);
-          a = base + L::up(s);
-          f = &sm.full[UP][s];
+          tma_load_3d(a, &tmV, f, n0, tv, bh);
+          tma_load_3d(a + TILE, &tmV, f, n0 + 64, tv, bh);
+          a = base + L::up;
+          f = &sm.full[UP][0];
           if (!open(UP, c, L::up_bytes)) break;
           for (int kb = 0; kb < 2; ++kb) {
-            tma_load_3d(a + L::k + kb * TILE, BWD ? &tmK : &tmKw, f, 64 * kb, t0, BWD ? kh : bh);
-            if (SPLIT) tma_load_3d(a + L::kl + kb * TILE, &tmKwl, f, 64 * kb, t0, bh);
+            tma_load_3d(a + kb * TILE, BWD ? &tmK : &tmKw, f, 64 * kb, t0, BWD ? kh : bh);
+            if (!BWD) tma_load_3d(a + (2 + kb) * TILE, &tmKw2, f, 64 * kb, t0, bh);
+            if (!BWD && P > 2) tma_load_3d(a + (4 + kb) * TILE, &tmKw3, f, 64 * kb, t0, bh);
           }
         } else {
           uint8_t* a = base + L::kq(s);
           uint64_t* f = &sm.full[KQ][s];
           if (!open(KQ, c, wq ? L::kq_bytes : 2 * TILE)) break;
-          for (int kb = 0; kb < 2; ++kb) {
-            tma_load_3d(a + L::w + kb * L::wq, BWD ? &tmKw : &tmK, f, 64 * kb, t0, BWD ? bh : kh);
-            if (wq) tma_load_3d(a + L::q + kb * L::wq, &tmWq, f, 64 * kb, t0, bh);
+          for (int kb = 0; kb < 2; ++kb, a += L::wq) {
+            tma_load_3d(a + L::w, BWD ? &tmKw : &tmK, f, 64 * kb, t0, BWD ? bh : kh);
+            if (wq) tma_load_3d(a + L::q, &tmWq, f, 64 * kb, t0, bh);
+            if (BWD) tma_load_3d(a + L::q + TILE, &tmWq2, f, 64 * kb, t0, bh);
           }
         }
       }
       // teardown: every load issued has landed
       for (int r = 0; r < 3; ++r)
-        for (int c = issued[r] > NS ? issued[r] - NS : 0; c < issued[r]; ++c)
-          mbar_drain(&sm.full[r][c % NS], (c / NS) & 1, wc, W_TMA_DRAIN);
+        for (int n = places(r), c = issued[r] > n ? issued[r] - n : 0; c < issued[r]; ++c)
+          mbar_drain(&sm.full[r][c % n], (c / n) & 1, wc, W_TMA_DRAIN);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       const uint32_t id_v = idesc_bf16(128, 64, true, BWD);       // V^T I, V^T Pv^T, dY^T Pv
-      const uint32_t id_w = idesc_bf16(128, 64, false, false);    // S K^T, D^T T0^T
+      const uint32_t id_w = idesc_bf16(128, 64, false, false);    // S K^T, S Kw^T, R^T T0^T
       const uint32_t id_wq = idesc_bf16(128, 128, false, false);  // S [K; Wq]^T
       const uint32_t id_u = idesc_bf16(128, 128, false, true);    // R^T Kw, F^T K
       const uint32_t id_o = idesc_bf16(128, 128, true, true);     // dY^T Wq
-      const uint32_t s_id = smem_u32(base + L::id);
-      // (V or dY)^T b into d, b [64 x 64]
+      // d (+)= (V or dY)^T b, b [64 x 64] at shared address b
       auto from_v = [&](uint32_t d, int c, uint32_t b, bool on) {
-        const uint32_t sv = smem_u32(base + L::vp(c % NS)) + L::v;
+        const uint32_t sv = smem_u32(base + L::vd(c % NS));
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           umma_bf16(d, desc_at(sw128_desc(sv, TILE, 1024), kk * 2048),
                     desc_at(sw128_desc(b, BWD ? TILE : 16, 1024), BWD ? kk * 2048 : kk * 32), id_v,
                     on || kk > 0);
       };
-      auto pv_at = [&](int c) { return smem_u32(base + L::vp(c % NS)) + L::p; };
+      const uint32_t s_id = smem_u32(base + L::id), s_pv = smem_u32(base + L::pv);
+      const uint32_t s_t0 = smem_u32(base + L::t0);
       // What of chunk c needs no state. Its accumulators are free once the chain has read R
-      // (uready, waited by then) and the outputs have been taken.
+      // (uready, waited by then) and D, and the outputs have been taken.
       auto first = [&](int c) -> bool {
-        const uint32_t d = tb + COL_D + 128 * (c % NY);
-        if (!mbar_wait(&sm.full[VP][c % NS], (c / NS) & 1, wc, W_FULL)) return false;
-        if (!SPLIT && !mbar_wait(&sm.yfree[c % NY], ((c / NY) & 1) ^ 1, wc, W_YFREE)) return false;
-        if (SPLIT && errors && !mbar_wait(&sm.yfree[0], (c & 1) ^ 1, wc, W_YFREE)) return false;
-        tc_fence_after();
+        if (!mbar_wait(&sm.full[VD][c % NS], (c / NS) & 1, wc, W_FULL)) return false;
         if (BWD) {
+          if (!mbar_wait(&sm.yfree[c & 1], ((c >> 1) & 1) ^ 1, wc, W_YFREE)) return false;
           if (!carry) {
-            from_v(d, c, pv_at(c), false);
-            from_v(d, c, pv_at(c) + TILE, true);
+            if (!mbar_wait(&sm.pfull, c & 1, wc, W_FULL)) return false;
+            tc_fence_after();
+            const uint32_t d = tb + COL_P + 128 * (c & 1);
+            from_v(d, c, s_pv, false);
+            from_v(d, c, s_pv + TILE, true);
+            umma_commit(&sm.pempty);
           }
-        } else {
-          from_v(d, c, s_id, false);
-          if (!SPLIT) {
-            if (outputs) from_v(d + 64, c, pv_at(c), false);
-            umma_commit(&sm.empty[VP][c % NS]);
-          }
+          return true;
         }
+        if (errors) {
+          if (P == 2 ? !mbar_wait(&sm.dfree[c % NV], ((c / NV) & 1) ^ 1, wc, W_DFREE)
+                     : !mbar_wait(&sm.yfree[0], (c & 1) ^ 1, wc, W_YFREE))
+            return false;
+        }
+        tc_fence_after();
+        from_v(tb + COL_V<P> + 64 * (c % NV), c, s_id, false);
         return true;
       };
       bool ok = first(0);
       for (int c = 0; c < NC && ok; ++c) {
-        const int s = c % NS, yb = c % NY;
-        const uint32_t st = smem_u32(base + L::kq(s)), sv = smem_u32(base + L::vp(s));
-        const uint32_t sk = smem_u32(base + L::up(s));
-        const uint32_t d = tb + COL_D + 128 * yb, y = d + 64;  // SPLIT: S K^T in y, Y^T behind it
-        if (!mbar_wait(!BWD && !SPLIT ? &sm.scaled[s] : &sm.full[KQ][s], (c / NS) & 1, wc, W_SCALED)) break;
-        if (!mbar_wait(&sm.sready[0], c & 1, wc, W_SREADY)) break;
-        tc_fence_after();
-        auto kq = [&](int kk) {
-          return desc_at(sw128_desc(st + L::w, 16, 1024), (kk >> 2) * L::wq + (kk & 3) * 32);
-        };
-        if (BWD) {  // F^T = S Kw^T
+        const int s = c % NS;
+        const uint32_t st = smem_u32(base + L::kq(s)), sk = smem_u32(base + L::up);
+        // S K^T and Y^T behind it; F^T
+        const uint32_t d = BWD ? tb + COL_P + 128 * (c & 1) + 64 : tb + COL_SK;
+        if (!mbar_wait(&sm.full[KQ][s], (c / NS) & 1, wc, W_FULL)) break;
+        bool got = !outputs || mbar_wait(&sm.yfree[0], (c & 1) ^ 1, wc, W_YFREE);
+        // the K steps in the order in which the two warpgroups convert S, so that the products
+        // of the first half run while the second is converted
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_bf16_tmem_a(y, tb + COL_SH + 8 * kk, kq(kk), id_w, kk > 0);
-        } else if (!SPLIT) {  // R^T -= S (G K)^T, Y^T += S Wq^T
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_bf16_tmem_a(d, tb + COL_SH + 8 * kk, kq(kk), outputs ? id_wq : id_w, 1);
-        } else {
-          // the K steps in the order in which the two warpgroups convert S, so that the products
-          // of the first half run while the second is converted
-          bool got = !outputs || mbar_wait(&sm.yfree[0], (c & 1) ^ 1, wc, W_YFREE);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (half == 1) got = got && mbar_wait(&sm.sready[1], c & 1, wc, W_SREADY);
-            if (!got) break;
-            tc_fence_after();
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int kk = 4 * (j >> 1) + 2 * half + (j & 1);
-              umma_bf16_tmem_a(y, tb + COL_SH + 8 * kk, kq(kk), outputs ? id_wq : id_w, half + j > 0);
-              umma_bf16_tmem_a(y, tb + COL_SL + 8 * kk, kq(kk), id_w, 1);
-            }
-          }
+        for (int half = 0; half < 2; ++half) {
+          got = got && mbar_wait(&sm.sready[half], c & 1, wc, W_SREADY);
           if (!got) break;
-        }
-        if (!(p.inject && c == 1)) umma_commit(&sm.dfull);
-        if (BWD) {
-          umma_commit(&sm.yfull[yb]);
-          if (!mbar_wait(&sm.sscaled, c & 1, wc, W_SREADY)) break;
           tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // S += dY^T Wq
-            umma_bf16(tb + COL_S, desc_at(sw128_desc(sv + L::v, TILE, 1024), kk * 2048),
-                      desc_at(sw128_desc(st + L::q, L::wq, 1024), kk * 2048), id_o, 1);
-          umma_commit(&sm.empty[VP][s]);
-          umma_commit(&sm.empty[KQ][s]);
-        } else if (SPLIT) {
-          if (outputs) from_v(y + 64, c, pv_at(c), true);  // Y^T += V^T Pv^T
-          umma_commit(&sm.empty[VP][s]);
-          umma_commit(&sm.empty[KQ][s]);
-          if (!errors) umma_commit(&sm.yfull[yb]);
-        } else {
-          umma_commit(&sm.empty[KQ][s]);
-          if (!errors) umma_commit(&sm.yfull[yb]);
-          if (!errors && c + 1 < NC && !first(c + 1)) break;
+          for (int j = 0; j < 4; ++j) {
+            const int kk = 4 * (j >> 1) + 2 * half + (j & 1);
+            const uint64_t kq = desc_at(sw128_desc(st + L::w, 16, 1024), (kk >> 2) * L::wq + (kk & 3) * 32);
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+              umma_bf16_tmem_a(d, tb + COL_SH + 64 * i + 8 * kk, kq, outputs && i < 2 ? id_wq : id_w,
+                               half + j + i > 0);
+          }
         }
-        if (!mbar_wait(&sm.full[UP][s], (c / NS) & 1, wc, W_FULL)) break;
+        if (!got) break;
+        if (!(p.inject && c == 1)) umma_commit(&sm.dfull);
+        if (BWD) {
+          umma_commit(&sm.yfull[c & 1]);
+          if (!mbar_wait(&sm.sscaled, c & 1, wc, W_SREADY)) break;
+          tc_fence_after();
+          const uint32_t sv = smem_u32(base + L::vd(s));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {  // S += dY^T Wq
+            const uint64_t av = desc_at(sw128_desc(sv, TILE, 1024), kk * 2048);
+            const uint64_t bq = desc_at(sw128_desc(st + L::q, L::wq, 1024), kk * 2048);
+            umma_bf16(tb + COL_S, av, bq, id_o, 1);
+            umma_bf16(tb + COL_S, av, desc_at(bq, TILE), id_o, 1);
+          }
+        } else if (outputs) {  // Y^T += V^T Pv^T
+          if (!mbar_wait(&sm.pfull, c & 1, wc, W_FULL)) break;
+          tc_fence_after();
+          from_v(tb + COL_Y, c, s_pv, true);
+          from_v(tb + COL_Y, c, s_pv + TILE, true);
+          umma_commit(&sm.pempty);
+          umma_commit(&sm.yfull[0]);
+        }
+        umma_commit(&sm.empty[VD][s]);
+        umma_commit(&sm.empty[KQ][s]);
+        if (!mbar_wait(&sm.full[UP][0], c & 1, wc, W_FULL)) break;
         if (!mbar_wait(&sm.uready, c & 1, wc, W_UREADY)) break;
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {  // S += U^T Kw
-          const uint64_t bk = desc_at(sw128_desc(sk + L::k, TILE, 1024), kk * 2048);
-          umma_bf16_tmem_a(tb + COL_S, tb + COL_U + 8 * kk, bk, id_u, 1);
-          if (SPLIT) {
-            const uint64_t bl = desc_at(sw128_desc(sk + L::kl, TILE, 1024), kk * 2048);
-            umma_bf16_tmem_a(tb + COL_S, tb + COL_UL + 8 * kk, bk, id_u, 1);
-            umma_bf16_tmem_a(tb + COL_S, tb + COL_U + 8 * kk, bl, id_u, 1);
-            umma_bf16_tmem_a(tb + COL_S, tb + COL_UL + 8 * kk, bl, id_u, 1);  // ST 5.2e-6 -> 4.4e-6 off
-          }
+        for (int kk = 0; kk < 4; ++kk) {  // S += U^T Kw, parts i and j down to 2^-8 of the last
+#pragma unroll
+          for (int i = 0; i < (BWD ? 1 : P); ++i)
+#pragma unroll
+            for (int j = 0; j < (BWD ? 1 : P); ++j)
+              if (i + j < P)
+                umma_bf16_tmem_a(tb + COL_S, tb + COL_U + 32 * i + 8 * kk,
+                                 desc_at(sw128_desc(sk + 2 * j * TILE, TILE, 1024), kk * 2048), id_u, 1);
         }
-        if (!SPLIT || !errors) umma_commit(&sm.sfull);
-        umma_commit(&sm.empty[UP][s]);
+        umma_commit(&sm.sfull);
+        umma_commit(&sm.empty[UP][0]);
         if (!BWD && errors) {  // D^T = R^T T0^T
           if (!mbar_wait(&sm.tfull, c & 1, wc, W_FULL)) break;
           tc_fence_after();
-          const uint32_t t0 = smem_u32(base + L::t0);
+          const uint32_t e = tb + COL_V<P> + 64 * (c % NV);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t hi = desc_at(sw128_desc(t0, 16, 1024), kk * 32);
-            umma_bf16_tmem_a(d, tb + COL_DB + 8 * kk, hi, id_w, kk > 0);
-            umma_bf16_tmem_a(d, tb + COL_DB + 8 * kk, desc_at(sw128_desc(t0 + TILE, 16, 1024), kk * 32),
-                             id_w, 1);
-            if (SPLIT) umma_bf16_tmem_a(d, tb + COL_UL + 8 * kk, hi, id_w, 1);
+            const uint64_t hi = desc_at(sw128_desc(s_t0, 16, 1024), kk * 32);
+            umma_bf16_tmem_a(e, tb + COL_DB<P> + 8 * kk, hi, id_w, kk > 0);
+            umma_bf16_tmem_a(e, tb + COL_DB<P> + 8 * kk, desc_at(hi, TILE), id_w, 1);
+            umma_bf16_tmem_a(e, tb + COL_DB<P> + 32 + 8 * kk, hi, id_w, 1);
           }
-          umma_commit(&sm.yfull[yb]);
+          umma_commit(&sm.ddone);
           umma_commit(&sm.tempty);
-          if (SPLIT) umma_commit(&sm.sfull);  // the remainder of R lies where that of S comes next
         }
-        // (with D: not before this chunk's, whose predecessor the chain takes after uready)
-        if ((BWD || SPLIT || errors) && c + 1 < NC) ok = first(c + 1);
+        if (c + 1 < NC) ok = first(c + 1);
       }
       umma_commit(&sm.done);
       mbar_drain(&sm.done, 0, wc, W_DONE);
@@ -537,20 +509,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         issued = c + 1;
         return true;
       };
-      // two chunks ahead of T0, which waits for the chunk before
+      // Pv and T0 wait for the chunk before, so the gates go two chunks ahead of them
+      auto pair = [&](int at, const CUtensorMap* map, uint64_t* full, uint64_t* empty, int c, uint32_t where) {
+        if (!mbar_wait(empty, (c & 1) ^ 1, wc, where)) return false;
+        mbar_arrive_expect_tx(full, 2 * TILE);
+        tma_load_3d(base + at, map, full, 0, cg(c) * C, bh);
+        tma_load_3d(base + at + TILE, map, full, 64, cg(c) * C, bh);
+        return true;
+      };
+      int pvs = 0;
       bool ok = gates(0) && (NC < 2 || gates(1));
       for (int c = 0; c < NC && ok; ++c) {
+        if (BWD ? !carry : outputs) {
+          if (!pair(L::pv, &tmP, &sm.pfull, &sm.pempty, c, W_PV)) break;
+          pvs = c + 1;
+        }
         if (!BWD && errors) {
-          if (!mbar_wait(&sm.tempty, (c & 1) ^ 1, wc, W_T0)) break;
-          mbar_arrive_expect_tx(&sm.tfull, 2 * TILE);
-          tma_load_3d(base + L::t0, &tmT, &sm.tfull, 0, cg(c) * C, bh);
-          tma_load_3d(base + L::t0 + TILE, &tmT, &sm.tfull, 64, cg(c) * C, bh);
+          if (!pair(L::t0, &tmT, &sm.tfull, &sm.tempty, c, W_T0)) break;
           loaded = c + 1;
         }
         if (c + 2 < NC) ok = gates(c + 2);
       }
       for (int c = issued > GS ? issued - GS : 0; c < issued; ++c)
         mbar_drain(&sm.gfull[c % GS], (c / GS) & 1, wc, W_TMA_DRAIN);
+      if (pvs) mbar_drain(&sm.pfull, (pvs - 1) & 1, wc, W_TMA_DRAIN);
       if (loaded) mbar_drain(&sm.tfull, (loaded - 1) & 1, wc, W_TMA_DRAIN);
     }
   } else if (warp >= 4 && warp < 12) {
@@ -630,14 +612,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // D of chunk c, once its product is done, and its place for the chunk after the next
     auto leave_D = [&](int c) {
       float x[32];
-      tmem_ld32(tb + COL_D + 128 * (c % NY) + lo + 32 * hh, x);
+      tmem_ld32(tb + COL_V<P> + 64 * (c % NV) + lo + 32 * hh, x);
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.yfree[c % NY]);
+      if (lane == 0) mbar_arrive(&sm.dfree[c % NV]);
       leave(x, cg(c));
     };
-    constexpr bool chain_D = !BWD && !SPLIT;
+    constexpr bool chain_D = !BWD && P == 2;
     bool ok = true;
     for (int c = 0; c < NC && ok; ++c) {
       const int g = c % GS, n = cg(c);
@@ -650,64 +632,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float GC = gs.GC;
       uint32_t pk[32];
       const uint32_t at = tb + COL_S + lo + 64 * hh;
-      if constexpr (SPLIT) {  // 32 columns at a time (registers), each half as it is ready
+      // 32 columns at a time (registers), each half as it is ready
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float v[32];
-          tmem_ld32(at + 32 * hf, v);
-          tmem_ld_wait();
-          uint32_t hi[16], rest[16];
+      for (int hf = 0; hf < 2; ++hf) {
+        float v[32];
+        tmem_ld32(at + 32 * hf, v);
+        tmem_ld_wait();
+        if (!BWD && errors && hf == 0 && c > 0)  // D's product has read what the parts go over
+          ok = mbar_wait_warp(&sm.ddone, (c - 1) & 1, wc, W_C_DDONE);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          uint32_t part[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            hi[e] = pk[16 * hf + e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-            rest[e] = pack_rest(v[2 * e], v[2 * e + 1], hi[e]);
+            part[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+            if (i == 0) pk[16 * hf + e] = part[e];
+            v[2 * e] -= bf16_lo(part[e]);
+            v[2 * e + 1] -= bf16_hi(part[e]);
           }
-          st_tmem16(tb + COL_SH + lo + 32 * hh + 16 * hf, hi);
-          st_tmem16(tb + COL_SL + lo + 32 * hh + 16 * hf, rest);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.sready[hf]);
+          st_tmem16(tb + COL_SH + 64 * i + lo + 32 * hh + 16 * hf, part);
         }
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {  // the decay, read again: not before the update
-          float v[32];
-          tmem_ld32(at + 32 * hf, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] *= GC;
-          tmem_st32(at + 32 * hf, v);
-        }
-      } else {
-        // the bf16 copy first; the decayed state is only needed by the update (backward: by
-        // dY^T Q)
-        float v0[32], v1[32];
-        tmem_ld32(at, v0);
-        tmem_ld32(at + 32, v1);
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          pk[e] = pack_bf16(v0[2 * e], v0[2 * e + 1]);
-          pk[16 + e] = pack_bf16(v1[2 * e], v1[2 * e + 1]);
-        }
-        st_tmem32(tb + COL_SH + lo + 32 * hh, pk);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.sready[0]);
+        if (lane == 0) mbar_arrive(&sm.sready[hf]);
+      }
+      if (!ok) break;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          v0[e] *= GC;
-          v1[e] *= GC;
-        }
-        tmem_st32(at, v0);
-        tmem_st32(at + 32, v1);
-        if (BWD) {
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.sscaled);
-        }
+      for (int hf = 0; hf < 2; ++hf) {  // the decay, read again: not before the update (dY^T Wq)
+        float v[32];
+        tmem_ld32(at + 32 * hf, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] *= GC;
+        tmem_st32(at + 32 * hf, v);
+      }
+      if (BWD) {
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.sscaled);
       }
       if (p.states && !carry) {
         if (L::staged) {
@@ -745,16 +711,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           uf[e + 3] = x.w;
         }
       };
-      factors(SPLIT ? gate_nG(gs) : gs.u);
+      factors(BWD ? gs.u : gate_nG(gs));
       ok = mbar_wait_warp(&sm.dfull, c & 1, wc, W_C_DFULL);
       if (!ok) break;
       tc_fence_after();
       float v[32];  // R, or F
-      const uint32_t acc = tb + COL_D + 128 * (c % NY) + lo + 32 * hh;
-      tmem_ld32(BWD ? acc + 64 : acc, v);
-      if constexpr (SPLIT) {
+      // backward: Pv^T dY, and F behind it
+      const uint32_t acc = tb + (BWD ? COL_P + 128 * (c & 1) : COL_SK) + lo + 32 * hh;
+      tmem_ld32(BWD ? acc + 64 : tb + COL_V<P> + 64 * (c % NV) + lo + 32 * hh, v);
+      if constexpr (!BWD) {
         float w[32];
-        tmem_ld32(acc + 64, w);
+        tmem_ld32(acc, w);
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = fmaf(uf[e], w[e], v[e]);
@@ -762,23 +729,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         tmem_ld_wait();
       }
-      {
-        uint32_t ub[16];
+      // v times the factors if given, in `parts` bf16 from column `col` on
+      auto put_parts = [&](uint32_t col, int parts, bool times) {
+        float x[32];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) ub[e] = pack_bf16(v[2 * e] * uf[2 * e], v[2 * e + 1] * uf[2 * e + 1]);
-        st_tmem16(tb + COL_U + lo + 16 * hh, ub);
-        if constexpr (SPLIT) {
+        for (int e = 0; e < 32; ++e) x[e] = times ? v[e] * uf[e] : v[e];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            ub[e] = pack_rest(v[2 * e] * uf[2 * e], v[2 * e + 1] * uf[2 * e + 1], ub[e]);
-          st_tmem16(tb + COL_UL + lo + 16 * hh, ub);
+        for (int i = 0; i < parts; ++i) {
+          uint32_t part[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            part[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+            x[2 * e] -= bf16_lo(part[e]);
+            x[2 * e + 1] -= bf16_hi(part[e]);
+          }
+          st_tmem16(tb + col + 32 * i + lo + 16 * hh, part);
         }
-        if (!BWD && errors) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) ub[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-          st_tmem16(tb + COL_DB + lo + 16 * hh, ub);
-        }
-      }
+      };
+      put_parts(COL_U, BWD ? 1 : P, true);
+      if (!BWD && errors) put_parts(COL_DB<P>, 2, false);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -798,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.gempty[g]);
     }
-    if (chain_D && errors && ok && mbar_wait_warp(&sm.yfull[(NC - 1) % NY], ((NC - 1) / NY) & 1, wc, W_C_DFULL)) {
+    if (chain_D && errors && ok && mbar_wait_warp(&sm.ddone, (NC - 1) & 1, wc, W_C_DDONE)) {
       tc_fence_after();
       leave_D(NC - 1);
     }
@@ -833,20 +802,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp >= 12) {
-    // ------------------------------------------------------------ scaled K; outputs
+    // ------------------------------------------------------------ outputs
     const int q = warp & 3, t = threadIdx.x & 127;
     const uint32_t lo = (uint32_t)(32 * q) << 16;
-    auto scale_chunk = [&](int c) -> bool {
-      const int s = c % NS, g = c % GS;
-      if (BWD || SPLIT) return true;
-      if (!mbar_wait_warp(&sm.full[KQ][s], (c / NS) & 1, wc, W_O_FULL)) return false;
-      if (!mbar_wait_warp(&sm.gfull[g], (c / GS) & 1, wc, W_O_GATE)) return false;
-      scale_tile(smem_u32(base + L::kq(s)) + L::w, L::wq, gate_nG(sm.gates[g]), t);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.scaled[s]);
-      return true;
-    };
     // 128 rows x 64 tokens at TMEM column `col` (backward: the sum of those and the 64 behind them) to
     // a [64 tokens x 128] tile of `map`, times factor[token] if given
     uint8_t* const stage = base + L::stage_o;
@@ -892,38 +850,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_store_commit();
       }
     };
-    bool ok = scale_chunk(0);
-    for (int c = 0; c < NC; ++c) {
+    const bool own_D = !BWD && P == 3 && errors;  // (P = 2: the chain)
+    bool ok = true;
+    for (int c = 0; c < NC && (BWD || outputs || own_D); ++c) {
       const int g = c % GS, yb = c % NY, t0 = cg(c) * C;
-      if (ok && c + 1 < NC) ok = scale_chunk(c + 1);
       if (BWD) ok = ok && mbar_wait_warp(&sm.gfull[g], (c / GS) & 1, wc, W_O_GATE);
-      ok = ok && mbar_wait_warp(&sm.yfull[yb], (c / NY) & 1, wc, W_O_Y);
+      if (BWD || outputs) ok = ok && mbar_wait_warp(&sm.yfull[yb], (c / NY) & 1, wc, W_O_Y);
+      if (own_D) ok = ok && mbar_wait_warp(&sm.ddone, c & 1, wc, W_O_DDONE);
       // the warps of emit() meet at barriers: all of them go on, or none does
       ok = !named_bar_or(2, 128, !ok);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t d = COL_D + 128 * yb;
-      if (SPLIT && errors) {  // D, two bf16: a row of 64 tokens per thread
+      if (own_D) {  // two bf16: a row of 64 tokens per thread
         bf16* const out = p.D + (((size_t)bh * N + cg(c)) * 2 * dvp(p.d) + n0 + 32 * q + lane) * C;
 #pragma unroll
         for (int hf = 0; hf < 4; ++hf) {
           float v[16];
-          tmem_ld16(tb + d + lo + 16 * hf, v);
+          tmem_ld16(tb + COL_V<P> + lo + 16 * hf, v);
           tmem_ld_wait();
           store_split<16>(out + 16 * hf, (size_t)dvp(p.d) * C, v);
         }
       }
-      if (carry || (!BWD && !p.y)) {
+      if (carry || (!BWD && !outputs)) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.yfree[yb]);
       } else if constexpr (BWD) {
-        emit(d, &tmY, gate_z(sm.gates[g]), t0, &sm.yfree[yb]);  // dV = beta E
+        emit(COL_P + 128 * yb, &tmY, gate_z(sm.gates[g]), t0, &sm.yfree[yb]);  // dV = beta E
       } else {
-        emit(SPLIT ? d + 128 : d + 64, &tmY, nullptr, t0, &sm.yfree[yb]);
+        emit(COL_Y, &tmY, nullptr, t0, &sm.yfree[yb]);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.gempty[g]);
+      if (BWD && lane == 0) mbar_arrive(&sm.gempty[g]);
     }
     if (t == 0) tma_store_wait_all();
   }
@@ -935,9 +893,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool BWD, bool SPLIT>
+template <bool BWD, int P>
 static cudaError_t launch(const Args& a, bool sum, bool after, cudaStream_t st) {
-  using L = Layout<BWD, SPLIT>;
+  using L = Layout<BWD, P>;
   using gradlev::tc::make_map_bf16_3d;
   const Dims& d = a.d;
   const uint64_t N = chunks(d.T), kh = (uint64_t)d.B * d.Hk, bh = d.BH();
@@ -946,10 +904,11 @@ static cudaError_t launch(const Args& a, bool sum, bool after, cudaStream_t st) 
   const Mats& m = a.m;
   bf16* dd = BWD ? a.E : a.sv.D;           // D or E
   void* yy = BWD ? a.dv_ : a.y;
-  CUtensorMap mk, mv, mw, mwl, mq, mp, mt, ms, my, md;
+  CUtensorMap mk, mv, mw, mw2, mw3, mq, mq2, mp, mt, ms, my, md;
   auto mat = [&](CUtensorMap* t, const bf16* x) { return make_map_bf16_3d(t, x, 128, N * C, bh, C); };
   if (!make_map_bf16_3d(&mk, a.k, d.dk, d.T, kh, C) || !make_map_bf16_3d(&mv, v, d.dv, d.T, bh, C) ||
-      !mat(&mw, m.Kw) || !mat(&mwl, SPLIT ? m.Kwlo : m.Kw) || !mat(&mq, m.Wq) || !mat(&mp, m.Pv) ||
+      !mat(&mw, m.Kw) || !mat(&mw2, BWD ? m.Kw : m.Kw2) || !mat(&mw3, P == 3 ? m.Kw3 : m.Kw) ||
+      !mat(&mq, m.Wq) || !mat(&mq2, BWD ? m.Wq2 : m.Wq) || !mat(&mp, m.Pv) ||
       !mat(&mt, !BWD && dd ? m.T0 : m.Pv) ||
       !make_map_bf16_3d(&ms, states ? states : m.Kw, 128, states ? dvp(d) : N * C,
                         states ? bh * N : bh, 32) ||
@@ -963,7 +922,7 @@ static cudaError_t launch(const Args& a, bool sum, bool after, cudaStream_t st) 
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (!bit || !(set.load() & bit)) {
     const cudaError_t e = cudaFuncSetAttribute(
-        walk_kernel<BWD, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::smem);
+        walk_kernel<BWD, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::smem);
     if (e != cudaSuccess) return e;
     set.fetch_or(bit);
   }
@@ -982,20 +941,20 @@ static cudaError_t launch(const Args& a, bool sum, bool after, cudaStream_t st) 
     grid += (unsigned)bh;  // the last segment's map, for the backward
   }
   if (after) {
-    const cudaError_t e = launch_after(d, walk_kernel<BWD, SPLIT>, grid, kThreads, L::smem, st, mk, mv, mw,
-                                       mwl, mq, mp, mt, ms, my, md, p);
+    const cudaError_t e = launch_after(d, walk_kernel<BWD, P>, grid, kThreads, L::smem, st, mk, mv, mw, mw2,
+                                       mw3, mq, mq2, mp, mt, ms, my, md, p);
     if (e != cudaSuccess) return e;
   } else {
-    walk_kernel<BWD, SPLIT><<<grid, kThreads, L::smem, st>>>(mk, mv, mw, mwl, mq, mp, mt, ms, my, md, p);
+    walk_kernel<BWD, P><<<grid, kThreads, L::smem, st>>>(mk, mv, mw, mw2, mw3, mq, mq2, mp, mt, ms, my, md, p);
   }
   count_launch();
   return cudaGetLastError();
 }
 
-cudaError_t launch_walk(const Args& a, bool backward, bool split, bool sum, bool after,
+cudaError_t launch_walk(const Args& a, bool backward, bool last_state, bool sum, bool after,
                         cudaStream_t st) {
-  if (backward) return launch<true, false>(a, sum, after, st);
-  return split ? launch<false, true>(a, sum, after, st) : launch<false, false>(a, sum, after, st);
+  if (backward) return launch<true, 2>(a, sum, after, st);
+  return last_state ? launch<false, 3>(a, sum, after, st) : launch<false, 2>(a, sum, after, st);
 }
 
 }  // namespace tc
