@@ -3,15 +3,15 @@ notice a rounding too many.
 
 A rounding to bf16 is uniform within half a step, 2^-8 of a value's leading power of two, so it is
 at most 2^-8 / sqrt(3) of the value in the mean square. Independent roundings add up as squares:
-sqrt(n) 2^-8 / sqrt(3) for the n that an output sees on the tensor cores, itself among them:
-  y: Pv, Wq, the state it is multiplied with, y;       dv: Kw, the state's gradient, dv;
-  dS0: Wq, Kw, the state's gradient, dS0;
-  dq: the state, R, Kw, dq;                            dk: those and the state's gradient;
-  dbeta, dlog_alpha: the state, R, Kw, the state's gradient, Wq, themselves.
-float32: products of operands that are split into two parts are 2^-21 off, four in a row, and
-their sums of at most 256 terms add sqrt(256) 2^-24 each. The float32 state of a bf16 forward is
-carried in pairs of bf16 (2^-17 apart): the state, R, diag(beta w) T0, Kw, and what of Kw's and
-T0's products is left out, five of them.
+sqrt(n) 2^-8 / sqrt(3) for the n that an output sees on the tensor cores, itself among them (what
+goes by two bf16 counts for none):
+  y: Wq, y;                 dq: the state, dq;          dk: the state, its gradient, dk;
+  dv, dbeta, dS0: Kw, F, themselves;
+  dlog_alpha: the state, its gradient, Kw, F, dlog_alpha.
+float32: products of operands that are split into two parts are 2^-21 off, and their sums of at
+most 256 terms add sqrt(256) 2^-24; four in a row, independent of each other. The float32 state of
+a bf16 forward goes by three bf16, as many bits as float32 has; what is left are the tensor core's
+24 additions to it per chunk, each cut to 2^-23.
 
 In float32 dlog_alpha gets the factor of `cancellation`. It is a sum over the pairs of tokens
 i >= t > j of a chunk of 32,
@@ -33,9 +33,9 @@ from tests.test_gpu_delta_alike import alike  # noqa: E402
 pytestmark = pytest.mark.gpu
 
 ROUNDING = 2.0 ** -8 / 3 ** 0.5
-SEEN = dict(y=4, dv=3, dS0=4, dq=4, dk=5, dbeta=6, dlog_alpha=6)
-F32 = 4 * (2.0 ** -21 + 256 ** 0.5 * 2.0 ** -24)
-PAIRS = 5 ** 0.5 * 2.0 ** -17
+SEEN = dict(y=2, dv=3, dS0=3, dq=2, dk=3, dbeta=3, dlog_alpha=5)
+F32 = 4 ** 0.5 * (2.0 ** -21 + 256 ** 0.5 * 2.0 ** -24)
+STATE = 24 * 2.0 ** -23
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -91,9 +91,9 @@ def errors(shape, cosine, beta, seed):
     return e, cancellation(x, want, scale) if dtype == "f32" else None
 
 
-# the fewest gates that take the tensor cores, and some more; then the float32 kernels
+# the smallest calls that take the tensor cores, and some more; then the float32 kernels
 @pytest.mark.parametrize("shape", [
-    (1, 5, 5, 205, 128, 128, "bf16"), (1, 5, 1, 205, 64, 64, "bf16"),
+    (1, 5, 5, 205, 128, 128, "bf16"), (1, 5, 1, 820, 64, 64, "bf16"), (9, 4, 4, 500, 24, 40, "bf16"),
     (1, 3, 3, 2731, 24, 40, "bf16"), (1, 3, 3, 2731, 56, 64, "bf16"), (2, 4, 4, 300, 128, 256, "bf16"),
     (1, 5, 5, 204, 128, 128, "bf16"), (1, 3, 3, 300, 64, 64, "f32"), (1, 2, 2, 300, 128, 128, "f32"),
 ], ids=lambda c: "-".join(map(str, c)))
@@ -105,7 +105,7 @@ def test_errors_are_those_of_the_roundings(shape, cosine, beta):
             if shape[-1] == "f32":
                 tol = F32 * (factor if n == "dlog_alpha" else 1.0)
             elif n == "ST":
-                tol = PAIRS
+                tol = STATE
             else:
                 tol = SEEN[n] ** 0.5 * ROUNDING
             assert err <= tol, (n, seed, err, tol)

@@ -31,7 +31,8 @@ def _lib():
 def gates(kind, B, H, T, seed):
     """log_alpha [B,H,T]. "wide": every token anywhere between -0.5 and -86, on a scale of
     factors. "half": mild but for one half of each chunk of 64, which takes a total of 55 to 95.
-    "early": tokens 12 to 31 of each chunk share 56 to 79 nats, the rest have 0.01 each."""
+    "early": tokens 12 to 31 of each chunk share 56 to 79 nats, the rest have 0.01 each. (And "docs", the mask
+    of the other tests: resets and padding.)"""
     g = torch.Generator().manual_seed(seed)
     u = torch.rand((B, H, T), generator=g)
     if kind == "wide":
@@ -56,18 +57,20 @@ def gates(kind, B, H, T, seed):
 
 CASES = [
     # (B, H, Hk, T, dk, dv, dtype): the tensor cores, in segments too; few gates; float32
-    (9, 4, 2, 150, 128, 128, "bf16"), (9, 4, 4, 130, 64, 40, "bf16"),
+    (9, 4, 2, 150, 128, 128, "bf16"), (16, 4, 4, 130, 64, 40, "bf16"),
+    (14, 4, 2, 150, 64, 64, "bf16"), (9, 8, 4, 130, 24, 136, "bf16"),
     (1, 2, 1, 1283, 128, 256, "bf16"), (1, 2, 2, 150, 128, 128, "bf16"),
     (2, 2, 1, 100, 136, 64, "bf16"), (2, 3, 3, 150, 64, 48, "f32"),
 ]
 
 
-@pytest.mark.parametrize("kind", ["wide", "half", "early"])
+@pytest.mark.parametrize("kind", ["wide", "half", "early", "docs"])
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
 def test_strong_decays(case, kind):
     B, H, Hk, T, dk, dv, dtype = case
-    d = ref.draw(B, H, Hk, T, dk, dv, dtype, True, seed=T + dk)
-    d["log_alpha"] = gates(kind, B, H, T, seed=dk + dv)
+    d = ref.draw(B, H, Hk, T, dk, dv, dtype, True, "docs" if kind == "docs" else "none", seed=T + dk)
+    if kind != "docs":
+        d["log_alpha"] = gates(kind, B, H, T, seed=dk + dv)
     still = (torch.arange(T) % 64 < 4) | (torch.arange(T) % 64 >= 60)
     d["beta"][:, :, still] = 0.0
     d["beta"][:, :, 40 % T::64] = 1e-7

@@ -29,33 +29,29 @@ Dims dims(int B, int H, int Hk, int T, int dk, int dv, gradlev_dtype dt) {
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// The tensor-core kernels round their operands to bf16, the float32 kernels nothing but the
-// outputs. A gate's gradient is one dot product of two such rows: 2.5 to 3.3e-3 off over many
-// gates (in the 2-norm; up to 5e-3 where keys are alike and beta is near 2; the float32 kernels
-// 1.7e-3), but any single one that happens to be small may be much further off (one token 3.3e-2,
-// two 9.5e-3, 600 gates of d_k 24 5.5e-3). Calls with gradients take the tensor cores where there
-// are gates enough, and where they are no slower: kernels of forward and gradients at 1024 gates of
-// d_k 128 37 against 62 us (H16 T64) and 138 against 215 us (H1 T1024); at 8190 gates of d_k 48 95
-// against 96 us (H14 T585), at 8000 of d_k 24 55 against 45 us. Without gradients only the
-// narrowest heads leave them (tc::shape_ok).
-bool use_tc(const Dims& d, bool gradients) {
-  if (!tc::shape_ok(d)) return false;
-  return !gradients || d.BH() * d.T > (d.dk >= 64 ? 1024 : 8192);
+// bf16 calls take the tensor cores from W = B H T d_k d_v > 2^24 on, and where few long scans are
+// walked in segments. Below, their latency and their padding to 128 columns cost more than the
+// float32 kernels, which are also the more exact ones (1.7e-3 off, the outputs' own rounding; the
+// tensor cores' 1.7 to 2.4e-3 over many gates, but single gates whose gradient happens to be small up
+// to 3e-2). Kernels of the forward with the last state: H16 T1 d128 13 against 28 us, T64 (2^24) 16
+// against 27, T256 31 against 40, T1000 97 against 85; of forward and gradients: d128 H16 T64 63
+// against 42 us, H1 T1024 214 against 171 (both 2^24), d64 B4 H8 T256 (2^25) 66 against 68, d48 B4 H8
+// T256 (2^24) 58 against 69. H2 T8192 d24, in segments, 347 against 244 and 768 against 438 us.
+bool use_tc(const Dims& d) {
+  return tc::shape_ok(d) &&
+         (d.BH() * d.T * d.dk * d.dv > (1u << 24) || tc::seg_plan(d).nseg > 1);
 }
 
 size_t ckpt_bytes(const Dims& d) {
-  return use_tc(d, true) ? tc::saved_bytes(d) : ffma::saved_bytes(d, true);
+  return use_tc(d) ? tc::saved_bytes(d) : ffma::saved_bytes(d, true);
 }
 
-size_t fwd_scratch(const Dims& d) {  // whichever family the call takes
-  const size_t f = ffma::saved_bytes(d, false);
-  if (!tc::shape_ok(d)) return f;
-  const size_t t = tc::fwd_scratch_bytes(d);
-  return use_tc(d, true) || t > f ? t : f;
+size_t fwd_scratch(const Dims& d) {
+  return use_tc(d) ? tc::fwd_scratch_bytes(d) : ffma::saved_bytes(d, false);
 }
 
 size_t bwd_scratch(const Dims& d) {  // E and the chunk-end gradients of the state
-  if (use_tc(d, true)) return tc::bwd_scratch_bytes(d);
+  if (use_tc(d)) return tc::bwd_scratch_bytes(d);
   return up256(d.BH() * d.T * d.dv * sizeof(float)) +
          up256(d.BH() * ffma::chunks(d.T) * d.dv * d.dk * sizeof(float));
 }
@@ -75,7 +71,7 @@ bool aligned(const void* p, size_t n) { return ((uintptr_t)p % n) == 0; }
 cudaError_t fwd_run(const Dims& d, const void* q, const void* k, const void* v, const float* beta,
                     const float* log_alpha, float scale, const float* S0, void* y, float* ST,
                     char* saved, char* ws, cudaStream_t st) {
-  if (use_tc(d, saved != nullptr)) {
+  if (use_tc(d)) {
     tc::Args a{d, q, k, v, beta, log_alpha, scale, reinterpret_cast<DeviceStatus*>(ws),
                kWaitTimeoutNs, tc::mats_at(ws + kStatusBytes, d, saved != nullptr)};
     if (saved) {
@@ -181,7 +177,7 @@ gradlev_status gradlev_delta_bwd(int B, int H, int Hk, int T, int d_k, int d_v, 
       return GRADLEV_ERR_CUDA;
   }
   char* scratch = ws + kStatusBytes;
-  if (use_tc(d, true)) {
+  if (use_tc(d)) {
     delta::tc::Args a{d, q, k, v, beta, log_alpha, scale, reinterpret_cast<DeviceStatus*>(ws),
                kWaitTimeoutNs};
     a.sv = delta::tc::saved_at(saved, d);

@@ -36,9 +36,8 @@ constexpr uint32_t LANE16 = 16u << 16;  // an M = 64 product in the upper 16 lan
 __host__ __device__ inline int chunks(int T) { return (T - 1) / C + 1; }
 
 // d_k of 8 and 16: seven eighths of a tile's columns and more would be padding. They stay on the
-// float32 kernels, 1.7e-3 off where these are up to 3.2e-3 (y), and faster in small calls (forward
-// of B1 H8 T1000 d 16 47 against 57 us, B2 H4 T512 d_k 8 26 against 37), though not in large ones
-// (B8 H16 T4096 d_k 16 d_v 64 574 against 431 us).
+// float32 kernels, which are the faster ones in small calls and in the forward (B8 H16 T4096 d_k 16
+// d_v 64 575 against 600 us), though not with the gradients of large ones (2027 against 1014 us).
 inline bool shape_ok(const Dims& d) { return d.bf16 && d.dk > 16 && d.dk <= 128 && d.dv <= 256; }
 
 // The kernels work on 128 columns of d_k and whole slices of 128 rows of d_v. Narrower heads
@@ -142,13 +141,16 @@ void set_segments(Args& a, char* at, float* M);
 size_t seg_bytes(const Dims& d, bool own_M);
 
 // A launch whose kernel waits by itself (grid_dep_wait, before it touches memory) for the one
-// before it, so that its launch and setup overlap that one's end: 65.7 -> 62.5 us for a forward of
-// B1 H16 T1000, 81.4 -> 77.8 us for training B2 H4 T257. Calls of more than one wave of chunks launch
-// in plain order: CTAs that move in early, one by one, cost them more than the gap between the
-// kernels (B8 H16 T4096 1114 -> 1128 us).
-inline bool launches_early(const Dims& d) { return d.BH() * chunks(d.T) <= 3 * 148; }
+// before it, so that its launch and setup overlap that one's end: 88.0 -> 82.9 us for training B2 H4
+// T257. Calls of more than one wave of chunks launch in plain order: CTAs that move in early, one by
+// one, cost them more than the gap between the kernels (B8 H16 T4096 1188 -> 1199 us).
+// Nor do calls for the last state, whose kernels leave no room for the next one's CTAs beside them (T1000
+// 80.7 -> 82.4 us).
+inline bool launches_early(const Dims& d, bool last_state) {
+  return !last_state && d.BH() * chunks(d.T) <= 3 * 148;
+}
 template <typename... P, typename... A>
-cudaError_t launch_after(const Dims& d, void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
+cudaError_t launch_after(bool early, void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
                          cudaStream_t st, A&&... args) {
   cudaLaunchConfig_t c{};
   c.gridDim = dim3(grid);
@@ -159,7 +161,7 @@ cudaError_t launch_after(const Dims& d, void (*kernel)(P...), unsigned grid, uns
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   c.attrs = &at;
-  c.numAttrs = launches_early(d) ? 1 : 0;
+  c.numAttrs = early ? 1 : 0;
   return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
 }
 

@@ -559,7 +559,7 @@ static cudaError_t launch(const CUtensorMap (&m)[9], const GradParams& p, unsign
   }
   const unsigned most = 2 * 148;
   const cudaError_t e =
-      launch_after(p.d, grad_kernel<GROUP>, work < most ? work : most, kThreads, kSmem, st, m[0], m[1], m[2],
+      launch_after(launches_early(p.d, false), grad_kernel<GROUP>, work < most ? work : most, kThreads, kSmem, st, m[0], m[1], m[2],
                    m[3], m[4], m[5], m[6], m[7], m[8], p);
   if (e != cudaSuccess) return e;
   count_launch();

@@ -126,7 +126,7 @@ cudaError_t combine(const Args& a, cudaStream_t st) {
     set.fetch_or(bit);
   }
   const cudaError_t e = launch_after(
-      a.d, combine_kernel<BWD, kRows>, (unsigned)(a.d.BH() * (dvp(a.d) / kRows)), kThreads,
+      launches_early(a.d, a.ST != nullptr), combine_kernel<BWD, kRows>, (unsigned)(a.d.BH() * (dvp(a.d) / kRows)), kThreads,
       combine_smem<kRows>(), st, a.d, a.seg.nseg, (const float*)a.loc, (const float*)a.M, a.S0,
       a.log_alpha, static_cast<const bf16*>(a.dST), a.init);
   if (e != cudaSuccess) return e;

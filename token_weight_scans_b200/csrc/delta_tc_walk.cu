@@ -941,7 +941,7 @@ static cudaError_t launch(const Args& a, bool sum, bool after, cudaStream_t st) 
     grid += (unsigned)bh;  // the last segment's map, for the backward
   }
   if (after) {
-    const cudaError_t e = launch_after(d, walk_kernel<BWD, P>, grid, kThreads, L::smem, st, mk, mv, mw, mw2,
+    const cudaError_t e = launch_after(launches_early(d, a.ST != nullptr), walk_kernel<BWD, P>, grid, kThreads, L::smem, st, mk, mv, mw, mw2,
                                        mw3, mq, mq2, mp, mt, ms, my, md, p);
     if (e != cudaSuccess) return e;
   } else {
