@@ -346,15 +346,14 @@ GRADLEV_API gradlev_status gradlev_mlp2_recon(int B, int H, int T, int d_x, int 
  * be finite, padding and the tokens before a reset too: the chunks multiply what a gate
  * masks by zero.
  *
- * Accuracy, in the 2-norm over a call's tensor: float32 outputs are 1e-6 off (operands are
- * split into two tf32 each), dlog_alpha 1e-5 where keys are alike. bf16 outputs are 1.7e-3
- * off by their own rounding; the tensor-core kernels (d_k 24 to 128 and d_v up to 256)
- * round operands to bf16 as well and are 2.5 to 3.3e-3 off, up to 6e-3 where keys are alike
- * (mean cosine 0.99) and beta is near 2; ST is 4e-6 off, up to 3e-5 there. Calls with
- * gradients (ckpt, or gradlev_delta_bwd) take those kernels from B*H*T > 1024 gates on
- * (8192 below d_k 64) and the float32 ones below, and a forward that is asked for ST carries
- * its state in more bits: y may differ in its last bits between these. The same call on the
- * same inputs gives the same bits. */
+ * Accuracy, in the 2-norm over a call's tensor: float32 outputs are 2 to 4e-7 off (dlog_alpha
+ * up to 1e-5 where keys are alike). bf16 outputs are 1.7e-3 off by their own rounding; the
+ * tensor-core kernels (d_k 24 to 128, d_v up to 256; from B*H*T*d_k*d_v > 2^24 on, and for few
+ * long scans) round some operands to bf16 as well: 1.7 to 2.4e-3, dlog_alpha up to 4e-3 where
+ * keys are alike (mean cosine 0.9 to 0.99). ST is 1e-6 off, up to 5e-6 where besides beta is
+ * near 2; a forward that is asked for it carries more bits, so that y may differ in its last
+ * bits between calls with and without ST. The same call on the same inputs gives the same
+ * bits. */
 
 /* Whether the shape is supported by gradlev_delta_fwd / _bwd: GRADLEV_OK, or
  * GRADLEV_ERR_INVALID_ARG / GRADLEV_ERR_UNSUPPORTED without touching the GPU.

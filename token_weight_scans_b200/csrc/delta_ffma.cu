@@ -4,13 +4,13 @@
 // Four kernels. The chunk-local part (Z, P) and the gradients of q, k and the gates
 // need no order among the chunks and run one CTA per chunk; only the two state
 // recurrences walk the chunks in order. All products are warp tiles (mma.sync) of operands split
-// into two tf32 each (tf32.cuh), 2^-21 off where a float32 FMA rounds by 2^-24: outputs are 1e-6
-// off, 3e-7 with FMAs, which waited for shared memory and took half as long again. Sums, states and
-// the chunk's triangular systems are float32. The rows of S (and of dS) evolve
+// into two tf32 each (tf32.cuh), whose sums are float32 additions: outputs are 2 to 4e-7 off, as
+// with FMAs, which waited for shared memory and took half as long again. Sums, states and the
+// chunk's triangular systems are float32. The rows of S (and of dS) evolve
 // independently given K, so a walk is cut into slices of kRows rows, one CTA each.
 //
-// Measured (B4 H8 T2048 d 64): Z and P 35 us, walks 145 and 143 us (239 and 219 us with FMAs),
-// gradients 166 us (235 us). A walk has 128 CTAs of one chain each, 2.2 us a chunk: four
+// Measured (B4 H8 T2048 d 64): Z and P 36 us, walks 147 and 143 us (239 and 219 us with FMAs),
+// gradients 169 us (235 us). A walk has 128 CTAs of one chain each, 2.2 us a chunk: four
 // products in a row at 8 warps per SM (44 % of the issue slots). The gradients' kernel has 16
 // warps per SM at 45 %: splitting operands is most of its instructions.
 #include <cuda_bf16.h>

@@ -17,9 +17,9 @@
 // D, E, X and Yn are two bf16 each: their terms cancel in all of these sums where keys are alike.
 // With one bf16 in their place dq and dk are 1 %, dlog_alpha 4 to 90 % off there.
 //
-// Measured: 389 us for B8 H16 T4096 d 128 (3352 bytes per token: 4.5 TB/s), 587 us for B1 H16
-// T32768 d_v 256 (5632 bytes: 5.0 TB/s), 398 us where four heads share a key head. 42 % of the
-// tensor pipe (M = 64 products run at half its rate; the remainders doubled their number), 39 % of
+// Measured: 389 us for B8 H16 T4096 d 128 (3352 bytes per token: 4.5 TB/s), 583 us for B1 H16
+// T32768 d_v 256 (5632 bytes: 5.1 TB/s), 393 us where four heads share a key head. 43 % of the
+// tensor pipe (M = 64 products run at half its rate; the remainders doubled their number), 36 % of
 // the issue slots. Shared memory holds two CTAs, which leaves next to no L1, so that a spilled
 // register costs a trip to L2: 300 bytes of spills per thread cost 20 us. Hence X and Yn one
 // after the other in pieces, the sums that begin late, and float32 pairs (half the FMAs). The remainders of D and E

@@ -17,12 +17,12 @@
 // beta = 0 would leave T0's column zero where E's row needs it: beta is taken at least 2^-60 in
 // size here (bt), which puts T0, Pv and Kw off by no more than that.
 //
-// Measured (B8 H16 T4096 d 128, 8192 chunks): 278 us with the backward's matrices, 1590 bytes per
-// token or 3.0 TB/s; 300 us with the remainder of Kw in place of those (B1 H16 T32768). What bounds it
-// is the chain of short steps through a chunk at 24 warps per SM: 43 % of the issue slots, a third
-// of the shared-memory pipe, 23 % of the tensor pipe, 25 % of the DRAM. Registers decide: products
-// unrolled over their terms spill. (W = -T0 diag(G) K and P diag(beta) for an unfolded form, in one
-// bf16 each, took 185 us.)
+// Measured (B8 H16 T4096 d 128, 8192 chunks): 313 us with the backward's matrices, 2110 bytes per
+// token or 3.5 TB/s; 395 us with Kw in three parts in place of those (B1 H16 T32768, two CTAs per
+// SM). What bounds it is the chain of short steps through a chunk at 24 warps per SM: 35 % of the issue
+// slots, 30 % of the shared-memory pipe, 19 % of the tensor pipe, 30 % of the DRAM. Registers decide:
+// products unrolled over their terms spill. (W = -T0 diag(G) K and P diag(beta) for an unfolded
+// form, in one bf16 each, took 185 us.)
 //
 // Waits: the in-flight TMA stores only read shared memory, so the CTA waits for that read
 // and not for their completion; the end of the kernel, which the walk waits for, orders them.

@@ -9,9 +9,9 @@
 //
 // The first walk costs about as much again, so segments pay where the scans leave the GPU
 // idle: B1 H16 T32768 d_v 256 has 32 CTAs of 512 chunks without them, and with four segments
-// 144 and then 144 of 128 chunks. Measured there: forward with the last state 336 us for the
-// first walk, 23 for the combination and 323 for the walk proper (the whole call 925 us, 1460 in one
-// walk); in training 206, 22 and 372, backward 183, 23 and 339 (2023 us, 3117 in one walk).
+// 144 and then 144 of 128 chunks. Measured there: forward with the last state 463 us for the
+// first walk, 23 for the combination and 466 for the walk proper (the whole call 1299 us, 2108 in one
+// walk); in training 319, 22 and 484, backward 241, 23 and 387 (2378 us, 3803 in one walk).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <atomic>

@@ -28,12 +28,12 @@
 // become rows, and TMA stores. D^T and E^T stay as they are, a chunk's tokens contiguous, in two
 // bf16 each.
 //
-// Measured (B8 H16 T4096 d 128, 128 CTAs of 64 chunks): forward 234 us, backward 222 us, of
-// 2696 and 2572 bytes per token: 6.1 TB/s, near the measured copy bandwidth (6.47). Where HBM does
-// not bound it, a chunk takes 1.6 us (forward without outputs), 2.5 us with SPLIT: the chain, two
-// products and two passes of the state or R through registers. S, D and E go through shared memory:
-// stored from registers, 16 bytes per row and instruction, the walks of d_v 256 took 502 and 443 us
-// in place of 372 and 339 (B1 H16 T32768).
+// Measured (B8 H16 T4096 d 128, 128 CTAs of 64 chunks): forward 270 us, backward 226 us, of
+// 3080 and 2830 bytes per token: 6.0 and 6.5 TB/s, near the measured copy bandwidth (6.47). Where HBM
+// does not bound it, a chunk takes 2.5 us (forward without outputs), 3.6 us with P = 3: the chain, two
+// products of P or P (P + 1) / 2 parts each and two passes of the state or R through registers. S, D
+// and E go through shared memory: stored from registers, 16 bytes per row and instruction, the walks
+// of d_v 256 took a third longer.
 //
 // Each chunk's tiles come in groups that are done with at different times: V (dY); K (Kw) with Wq;
 // Kw (K); Pv; T0. The first two have two places each; the others, for which a chunk's time is enough
