@@ -45,7 +45,7 @@ def alike(B, H, Hk, T, dk, dv, dtype, cosine, beta, seed):
 
 
 SHAPES = [
-    # (B, H, Hk, T, dk, dv, dtype): the tensor cores, narrower heads, segments, few gates, float32
+    # (B, H, Hk, T, dk, dv, dtype): the tensor cores, narrower heads, segments, a small call, float32
     (3, 4, 2, 200, 128, 128, "bf16"), (6, 3, 3, 260, 64, 72, "bf16"),
     (9, 4, 2, 257, 40, 72, "bf16"), (1, 2, 1, 1283, 128, 256, "bf16"),
     (1, 2, 2, 200, 128, 128, "bf16"), (1, 2, 1, 200, 64, 64, "f32"),

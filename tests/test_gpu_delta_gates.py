@@ -56,7 +56,7 @@ def gates(kind, B, H, T, seed):
 
 
 CASES = [
-    # (B, H, Hk, T, dk, dv, dtype): the tensor cores, in segments too; few gates; float32
+    # (B, H, Hk, T, dk, dv, dtype): the tensor cores, in segments too; a small call; float32
     (9, 4, 2, 150, 128, 128, "bf16"), (16, 4, 4, 130, 64, 40, "bf16"),
     (14, 4, 2, 150, 64, 64, "bf16"), (9, 8, 4, 130, 24, 136, "bf16"),
     (1, 2, 1, 1283, 128, 256, "bf16"), (1, 2, 2, 150, 128, 128, "bf16"),

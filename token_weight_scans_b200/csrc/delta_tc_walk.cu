@@ -17,16 +17,15 @@
 //
 // Every operand of the state that is not exact in bf16 comes as a sum of P bf16. Forward, P = 2:
 // S, R and Kw (and Pv in Y, T0 in D). The gradients and y are then off by their own rounding and by
-// that of what is multiplied once, Wq and the states that are kept: 2.0 to 2.4e-3, where one bf16
-// each makes 2.7 to 3.0e-3. P = 3 where the last state is asked for: it is float32, and 16 bits
-// would leave it 4e-6 off. Backward, P = 2 for S.
+// that of what is multiplied once, Wq and the states that are kept: 1.7 to 2.4e-3, where one bf16
+// each makes 2.4 to 3.3e-3. P = 3 where the last state is asked for: it is float32, and 16 bits
+// would leave it 4e-6 off, not 8e-7. Backward, P = 2 for S, Wq and Pv; Kw and F are one.
 //
 // Warp roles (16): 0 and 3 TMA producers, 1 MMA issuer (owns TMEM), 2 copies the gates in,
 // 4-11 two chain warpgroups (each half of the columns), which also leave S, D^T and E^T for
-// the kernels after, 12-15 Y (dV): 16-lane TMEM loads in the
-// layout of 8 x 8 fragments, transposed on the way to shared memory (stmatrix) so that tokens
-// become rows, and TMA stores. D^T and E^T stay as they are, a chunk's tokens contiguous, in two
-// bf16 each.
+// the kernels after, 12-15 Y (dV): 16-lane TMEM loads in the layout of 8 x 8 fragments, transposed on
+// the way to shared memory (stmatrix) so that tokens become rows, and TMA stores. D^T and E^T stay as
+// they are, a chunk's tokens contiguous, in two bf16 each.
 //
 // Measured (B8 H16 T4096 d 128, 128 CTAs of 64 chunks): forward 270 us, backward 226 us, of
 // 3080 and 2830 bytes per token: 6.0 and 6.5 TB/s, near the measured copy bandwidth (6.47). Where HBM
